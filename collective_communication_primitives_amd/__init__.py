@@ -615,9 +615,352 @@ def shard_views(fused: torch.Tensor, numels: Sequence[int], shard: int) -> List[
     return out
 
 
+# ----------------------------------------------- model-step operators ------
+# Layer norm, expert routing, the experts' token exchange and the loss over a
+# sharded vocabulary: the steps of a model whose mathematics crosses the ranks.
+DT_MAX_EXPERTS, DT_MAX_TOPK = 1024, 64
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _rank_list(name: str, tensors, p: int, dtype, dev: int, sizes) -> list:
+    """``tensors`` as a list of p contiguous tensors of ``dtype`` on the
+    current GPU with sizes[r] elements each (sizes: one number for all)."""
+    tensors = list(tensors)
+    if len(tensors) != p:
+        raise ValueError(f"{name} must list one tensor per rank ({p}), got {len(tensors)}")
+    for r, t in enumerate(tensors):
+        if t.dtype != dtype:
+            raise TypeError(f"{name}[{r}] must be {dtype}, got {t.dtype}")
+        if t.numel() != (sizes if isinstance(sizes, int) else sizes[r]):
+            want = sizes if isinstance(sizes, int) else sizes[r]
+            raise ValueError(f"{name}[{r}] must hold {want} elements, got {t.numel()}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}[{r}] must live on the current GPU (cuda:{dev}), got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{r}] must be contiguous")
+    return tensors
+
+
+def _float_dtype(t: torch.Tensor) -> int:
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def _workspace(given: Optional[torch.Tensor], nbytes: int, dev: int, stream, async_op: bool, comm_stream) -> torch.Tensor:
+    """The call's workspace: the caller's, or a block of torch's caching
+    allocator that is not reused before the stream that runs the call has
+    passed it."""
+    if given is not None:
+        _on_gpu([given], "workspace")
+        if given.numel() * given.element_size() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes, got {given.numel() * given.element_size()}")
+        return given
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=f"cuda:{dev}")
+    runs_on = (comm_stream if comm_stream is not None else side_stream(dev)) if async_op else stream
+    if runs_on is not None:
+        if isinstance(runs_on, int):
+            runs_on = torch.cuda.ExternalStream(runs_on, device=dev)
+        ws.record_stream(runs_on)
+    return ws
+
+
+def _sized(nbytes: int) -> int:
+    """The result of a *_workspace function: 0 with an error message means refused."""
+    if nbytes == 0:
+        detail = _L.dt_last_error().decode()
+        if detail:
+            raise DtError(DT_ERR_ARG, detail)
+    return nbytes
+
+
+def _width(t: torch.Tensor, name: str) -> int:
+    if t.dim() < 1 or t.shape[-1] < 1:
+        raise ValueError(f"{name} must have a last dimension of at least one element")
+    return t.shape[-1]
+
+
+def dt_layer_norm_workspace(rows: Sequence[int], cols: int) -> int:
+    """Bytes of workspace dt_layer_norm_backward takes for rows[r] rows of ``cols`` per rank."""
+    return _sized(_L.dt_layer_norm_workspace(len(rows), _size_array(rows), cols))
+
+
+def dt_layer_norm(x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], bias: Optional[Sequence[torch.Tensor]],
+                  y: Sequence[torch.Tensor], mean: Optional[Sequence[torch.Tensor]] = None,
+                  rstd: Optional[Sequence[torch.Tensor]] = None, eps: float = 1e-5, stream=None,
+                  async_op: bool = False, comm_stream=None):
+    """Layer norm of every rank's rows x[r] [..., cols] into y[r]; weight[r],
+    bias[r] (None: no bias) hold ``cols`` elements.  mean[r], rstd[r] (fp32,
+    one per row) keep the statistics for dt_layer_norm_backward."""
+    x = list(x)
+    p, dev, cols = len(x), torch.cuda.current_device(), _width(weight[0], "weight")
+    code, dtype = _float_dtype(x[0]), x[0].dtype
+    sizes = [t.numel() for t in x]
+    rows = [n // cols for n in sizes]
+    if any(n % cols for n in sizes):
+        raise ValueError(f"x must hold whole rows of {cols} elements")
+    if (mean is None) != (rstd is None):
+        raise ValueError("mean and rstd come together")
+    stash = _rank_list("x", x, p, dtype, dev, sizes) + _rank_list("weight", weight, p, dtype, dev, cols)
+    stash += _rank_list("y", y, p, dtype, dev, sizes)
+    if bias is not None:
+        stash += _rank_list("bias", bias, p, dtype, dev, cols)
+    if mean is not None:
+        stash += _rank_list("mean", mean, p, torch.float32, dev, rows) + _rank_list("rstd", rstd, p, torch.float32, dev, rows)
+    xs, ws, ys, n = _ptr_array(x), _ptr_array(weight), _ptr_array(y), _size_array(rows)
+    bs = _ptr_array(bias) if bias is not None else None
+    ms, rs = (_ptr_array(mean), _ptr_array(rstd)) if mean is not None else (None, None)
+    w = _launch(lambda st: _L.dt_layer_norm(xs, ws, bs, ys, ms, rs, p, n, cols, eps, code, st), stash, async_op, stream,
+                comm_stream)
+    return w if async_op else y
+
+
+def dt_layer_norm_backward(dy: Sequence[torch.Tensor], x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor],
+                           mean: Sequence[torch.Tensor], rstd: Sequence[torch.Tensor], dx: Sequence[torch.Tensor],
+                           dweight: Sequence[torch.Tensor], dbias: Optional[Sequence[torch.Tensor]] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False,
+                           comm_stream=None):
+    """Gradients of dt_layer_norm: dx[r], and dweight[q], dbias[q] (None: not
+    formed) summed over the rows of all ranks, for every rank q."""
+    x = list(x)
+    p, dev, cols = len(x), torch.cuda.current_device(), _width(weight[0], "weight")
+    code, dtype = _float_dtype(x[0]), x[0].dtype
+    sizes = [t.numel() for t in x]
+    rows = [n // cols for n in sizes]
+    if any(n % cols for n in sizes):
+        raise ValueError(f"x must hold whole rows of {cols} elements")
+    stash = _rank_list("x", x, p, dtype, dev, sizes) + _rank_list("dy", dy, p, dtype, dev, sizes)
+    stash += _rank_list("weight", weight, p, dtype, dev, cols) + _rank_list("dx", dx, p, dtype, dev, sizes)
+    stash += _rank_list("mean", mean, p, torch.float32, dev, rows) + _rank_list("rstd", rstd, p, torch.float32, dev, rows)
+    stash += _rank_list("dweight", dweight, p, dtype, dev, cols)
+    if dbias is not None:
+        stash += _rank_list("dbias", dbias, p, dtype, dev, cols)
+    n = _size_array(rows)
+    nbytes = _sized(_L.dt_layer_norm_workspace(p, n, cols))
+    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
+    gs, xs, ws, ds = _ptr_array(dy), _ptr_array(x), _ptr_array(weight), _ptr_array(dx)
+    ms, rs, dw = _ptr_array(mean), _ptr_array(rstd), _ptr_array(dweight)
+    db = _ptr_array(dbias) if dbias is not None else None
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_layer_norm_backward(gs, xs, ws, ms, rs, ds, dw, db, p, n, cols, code, at, have, st),
+                stash + [space], async_op, stream, comm_stream)
+    return w if async_op else dx
+
+
+def _score_code(score) -> int:
+    return _SCORES[score] if isinstance(score, str) else int(score)
+
+
+def dt_moe_route(logits: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], weights: Sequence[torch.Tensor],
+                 bias: Optional[torch.Tensor] = None, groups: int = 1, topk_groups: int = 1, score="softmax",
+                 renormalize: bool = True, scale: float = 1.0, stream=None, async_op: bool = False, comm_stream=None):
+    """Routing: experts[r] int32 and weights[r] fp32 [tokens, topk] from
+    logits[r] [tokens, nexperts]; see dt.h for the order and what -inf, NaN
+    and ties do.  ``bias`` (fp32 [nexperts]) moves the choice, not the weights."""
+    logits = list(logits)
+    p, dev = len(logits), torch.cuda.current_device()
+    e, k = _width(logits[0], "logits"), _width(experts[0], "experts")
+    code = _float_dtype(logits[0])
+    tokens = [t.numel() // e for t in logits]
+    slots = [t * k for t in tokens]
+    stash = _rank_list("logits", logits, p, logits[0].dtype, dev, [t * e for t in tokens])
+    stash += _rank_list("experts", experts, p, torch.int32, dev, slots)
+    stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
+    b = None
+    if bias is not None:
+        stash += _rank_list("bias", [bias], 1, torch.float32, dev, e)
+        b = bias.data_ptr()
+    ls, es, ws, n = _ptr_array(logits), _ptr_array(experts), _ptr_array(weights), _size_array(tokens)
+    sc, rn = _score_code(score), int(bool(renormalize))
+    w = _launch(lambda st: _L.dt_moe_route(ls, es, ws, p, n, e, k, b, groups, topk_groups, sc, rn, scale, code, st),
+                stash, async_op, stream, comm_stream)
+    return w if async_op else (experts, weights)
+
+
+def dt_moe_route_backward(logits: Sequence[torch.Tensor], experts: Sequence[torch.Tensor],
+                          dweights: Sequence[torch.Tensor], dlogits: Sequence[torch.Tensor], score="softmax",
+                          renormalize: bool = True, scale: float = 1.0, stream=None, async_op: bool = False,
+                          comm_stream=None):
+    """dlogits[r] from the gradient of dt_moe_route's weights, for its choice."""
+    logits = list(logits)
+    p, dev = len(logits), torch.cuda.current_device()
+    e, k = _width(logits[0], "logits"), _width(experts[0], "experts")
+    code, dtype = _float_dtype(logits[0]), logits[0].dtype
+    tokens = [t.numel() // e for t in logits]
+    sizes, slots = [t * e for t in tokens], [t * k for t in tokens]
+    stash = _rank_list("logits", logits, p, dtype, dev, sizes) + _rank_list("dlogits", dlogits, p, dtype, dev, sizes)
+    stash += _rank_list("experts", experts, p, torch.int32, dev, slots)
+    stash += _rank_list("dweights", dweights, p, torch.float32, dev, slots)
+    ls, es, gs, ds = _ptr_array(logits), _ptr_array(experts), _ptr_array(dweights), _ptr_array(dlogits)
+    n, sc, rn = _size_array(tokens), _score_code(score), int(bool(renormalize))
+    w = _launch(lambda st: _L.dt_moe_route_backward(ls, es, gs, ds, p, n, e, k, sc, rn, scale, code, st), stash, async_op,
+                stream, comm_stream)
+    return w if async_op else dlogits
+
+
+def dt_moe_dispatch_workspace(tokens: Sequence[int], nexperts: int, topk: int) -> int:
+    """Bytes of workspace dt_moe_dispatch takes."""
+    return _sized(_L.dt_moe_dispatch_workspace(len(tokens), _size_array(tokens), nexperts, topk))
+
+
+def _exchange(tok, rows, experts, nexperts: int, dev: int):
+    """(p, cols, topk, dtype, tokens, capacity, stash) of an exchange between
+    token tensors and the experts' row buffers."""
+    p = len(tok)
+    cols, k = _width(tok[0], "the rows"), _width(experts[0], "experts")
+    dtype = tok[0].dtype
+    if any(t.numel() % cols for t in tok) or any(t.numel() % cols for t in rows):
+        raise ValueError(f"token and expert rows must be whole rows of {cols} elements")
+    tokens, capacity = [t.numel() // cols for t in tok], [t.numel() // cols for t in rows]
+    stash = _rank_list("experts", experts, p, torch.int32, dev, [t * k for t in tokens])
+    if nexperts % p:
+        raise ValueError(f"{nexperts} experts do not divide by {p} ranks")
+    return p, cols, k, dtype, tokens, capacity, stash
+
+
+def dt_moe_dispatch(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], recv: Sequence[torch.Tensor],
+                    positions: Sequence[torch.Tensor], offsets: Sequence[torch.Tensor], nexperts: int,
+                    workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False, comm_stream=None):
+    """AllToAll of token rows x[r] [tokens, cols] to the ranks of their
+    experts[r] [tokens, topk]: recv[q] [capacity, cols] in expert order,
+    positions[r] int32 [tokens, topk] (-1: no row), offsets[q] int32
+    [nexperts / P + 1]."""
+    x, recv, dev = list(x), list(recv), torch.cuda.current_device()
+    p, cols, k, dtype, tokens, capacity, stash = _exchange(x, recv, experts, nexperts, dev)
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    code = _DTYPES[dtype]
+    stash += _rank_list("x", x, p, dtype, dev, [t * cols for t in tokens])
+    stash += _rank_list("recv", recv, p, dtype, dev, [c * cols for c in capacity])
+    stash += _rank_list("positions", positions, p, torch.int32, dev, [t * k for t in tokens])
+    stash += _rank_list("offsets", offsets, p, torch.int32, dev, nexperts // p + 1)
+    n, cap = _size_array(tokens), _size_array(capacity)
+    nbytes = _sized(_L.dt_moe_dispatch_workspace(p, n, nexperts, k))
+    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
+    xs, es, rs = _ptr_array(x), _ptr_array(experts), _ptr_array(recv)
+    ps, os_, at, have = _ptr_array(positions), _ptr_array(offsets), space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_moe_dispatch(xs, es, rs, ps, os_, p, n, cap, cols, nexperts, k, code, at, have, st),
+                stash + [space], async_op, stream, comm_stream)
+    return w if async_op else recv
+
+
+def dt_moe_combine(y: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], positions: Sequence[torch.Tensor],
+                   weights: Optional[Sequence[torch.Tensor]], out: Sequence[torch.Tensor], nexperts: int, stream=None,
+                   async_op: bool = False, comm_stream=None):
+    """out[r][t] = sum over its slots of weight * y[owner][position]
+    (weights None: all ones, dt_moe_dispatch's backward pass)."""
+    y, out, dev = list(y), list(out), torch.cuda.current_device()
+    p, cols, k, dtype, tokens, capacity, stash = _exchange(out, y, experts, nexperts, dev)
+    code, slots = _float_dtype(out[0]), [t * k for t in tokens]
+    stash += _rank_list("y", y, p, dtype, dev, [c * cols for c in capacity])
+    stash += _rank_list("out", out, p, dtype, dev, [t * cols for t in tokens])
+    stash += _rank_list("positions", positions, p, torch.int32, dev, slots)
+    if weights is not None:
+        stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
+    ys, es, ps, os_ = _ptr_array(y), _ptr_array(experts), _ptr_array(positions), _ptr_array(out)
+    ws = _ptr_array(weights) if weights is not None else None
+    n, cap = _size_array(tokens), _size_array(capacity)
+    w = _launch(lambda st: _L.dt_moe_combine(ys, es, ps, ws, os_, p, n, cap, cols, nexperts, k, code, st), stash, async_op,
+                stream, comm_stream)
+    return w if async_op else out
+
+
+def dt_moe_combine_backward(dout: Sequence[torch.Tensor], y: Sequence[torch.Tensor], experts: Sequence[torch.Tensor],
+                            positions: Sequence[torch.Tensor], weights: Sequence[torch.Tensor],
+                            dy: Sequence[torch.Tensor], dweights: Sequence[torch.Tensor], nexperts: int, stream=None,
+                            async_op: bool = False, comm_stream=None):
+    """Gradients of dt_moe_combine: dy[owner][position] = weight * dout[r][t]
+    (other rows of dy are left as they were), dweights[r] fp32."""
+    dout, y, dev = list(dout), list(y), torch.cuda.current_device()
+    p, cols, k, dtype, tokens, capacity, stash = _exchange(dout, y, experts, nexperts, dev)
+    code, slots, rows = _float_dtype(dout[0]), [t * k for t in tokens], [c * cols for c in capacity]
+    stash += _rank_list("dout", dout, p, dtype, dev, [t * cols for t in tokens])
+    stash += _rank_list("y", y, p, dtype, dev, rows) + _rank_list("dy", dy, p, dtype, dev, rows)
+    stash += _rank_list("positions", positions, p, torch.int32, dev, slots)
+    stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
+    stash += _rank_list("dweights", dweights, p, torch.float32, dev, slots)
+    gs, ys, es, ps = _ptr_array(dout), _ptr_array(y), _ptr_array(experts), _ptr_array(positions)
+    ws, ds, dw, n, cap = _ptr_array(weights), _ptr_array(dy), _ptr_array(dweights), _size_array(tokens), _size_array(capacity)
+    w = _launch(lambda st: _L.dt_moe_combine_backward(gs, ys, es, ps, ws, ds, dw, p, n, cap, cols, nexperts, k, code, st),
+                stash, async_op, stream, comm_stream)
+    return w if async_op else dy
+
+
+def dt_vocab_loss_workspace(vocab_rows: Sequence[int], tokens: int, cols: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace dt_vocab_loss takes."""
+    return _sized(_L.dt_vocab_loss_workspace(len(vocab_rows), _size_array(vocab_rows), tokens, cols, _DTYPES[dtype]))
+
+
+def dt_vocab_loss_backward_workspace(vocab_rows: Sequence[int], tokens: int, cols: int, dtype=torch.bfloat16,
+                                     piece_rows: int = 0) -> int:
+    """Bytes of workspace dt_vocab_loss_backward takes with pieces of ``piece_rows`` vocabulary rows (0: the library's choice)."""
+    return _sized(_L.dt_vocab_loss_backward_workspace(len(vocab_rows), _size_array(vocab_rows), tokens, cols, piece_rows,
+                                                      _DTYPES[dtype]))
+
+
+def _loss_inputs(hidden, weight, targets, dev: int):
+    hidden, weight = list(hidden), list(weight)
+    p, cols = len(hidden), _width(hidden[0], "hidden")
+    code, dtype, tokens = _float_dtype(hidden[0]), hidden[0].dtype, hidden[0].numel() // cols
+    if len(weight) != p or any(w.numel() % cols for w in weight):
+        raise ValueError(f"weight must list one shard of whole rows of {cols} elements per rank")
+    stash = _rank_list("hidden", hidden, p, dtype, dev, tokens * cols)
+    stash += _rank_list("weight", weight, p, dtype, dev, [w.numel() for w in weight])
+    stash += _rank_list("targets", targets, p, torch.int64, dev, tokens)
+    return p, cols, tokens, code, dtype, [w.numel() // cols for w in weight], stash
+
+
+def dt_vocab_loss(hidden: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], targets: Sequence[torch.Tensor],
+                  loss: Sequence[torch.Tensor], lse: Sequence[torch.Tensor], ignore_index: int = -100,
+                  workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False, comm_stream=None):
+    """Softmax cross entropy per token over a vocabulary sharded over the
+    ranks: hidden[r] [tokens, cols] (the same on every rank; one tensor may be
+    listed P times), weight[r] [rows of rank r, cols], targets[r] int64.
+    loss[q] and lse[q] fp32 [tokens] are written for every rank."""
+    dev = torch.cuda.current_device()
+    p, cols, tokens, code, dtype, rows, stash = _loss_inputs(hidden, weight, targets, dev)
+    stash += _rank_list("loss", loss, p, torch.float32, dev, tokens) + _rank_list("lse", lse, p, torch.float32, dev, tokens)
+    n = _size_array(rows)
+    nbytes = _sized(_L.dt_vocab_loss_workspace(p, n, tokens, cols, code))
+    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
+    hs, ws, ts, ls, es = (_ptr_array(v) for v in (hidden, weight, targets, loss, lse))
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_vocab_loss(hs, ws, ts, ls, es, p, n, tokens, cols, ignore_index, code, at, have, st),
+                stash + [space], async_op, stream, comm_stream)
+    return w if async_op else loss
+
+
+def dt_vocab_loss_backward(hidden: Sequence[torch.Tensor], weight: Sequence[torch.Tensor],
+                           targets: Sequence[torch.Tensor], lse: Sequence[torch.Tensor], dloss: Sequence[torch.Tensor],
+                           dhidden: Sequence[torch.Tensor], dweight: Sequence[torch.Tensor], ignore_index: int = -100,
+                           piece_rows: int = 0, workspace: Optional[torch.Tensor] = None, stream=None,
+                           async_op: bool = False, comm_stream=None):
+    """Gradients of dt_vocab_loss for dloss[r] fp32 [tokens]: dhidden[q] is
+    the sum over all ranks' shards for every rank q, dweight[r] rank r's own.
+    The logits are formed again, ``piece_rows`` vocabulary rows of a shard at
+    a time (0: the library's choice)."""
+    dev = torch.cuda.current_device()
+    p, cols, tokens, code, dtype, rows, stash = _loss_inputs(hidden, weight, targets, dev)
+    stash += _rank_list("lse", lse, p, torch.float32, dev, tokens) + _rank_list("dloss", dloss, p, torch.float32, dev, tokens)
+    stash += _rank_list("dhidden", dhidden, p, dtype, dev, tokens * cols)
+    stash += _rank_list("dweight", dweight, p, dtype, dev, [r * cols for r in rows])
+    n = _size_array(rows)
+    nbytes = _sized(_L.dt_vocab_loss_backward_workspace(p, n, tokens, cols, piece_rows, code))
+    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
+    hs, ws, ts, es, gs, dh, dw = (_ptr_array(v) for v in (hidden, weight, targets, lse, dloss, dhidden, dweight))
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_vocab_loss_backward(hs, ws, ts, es, gs, dh, dw, p, n, tokens, cols, ignore_index,
+                                                     piece_rows, code, at, have, st),
+                stash + [space], async_op, stream, comm_stream)
+    return w if async_op else dhidden
+
+
 __all__ = [
     "dt_allreduce", "dt_reduce_scatter", "dt_all_gather", "dt_all_to_all", "dt_bucket_allreduce", "dt_bucket_plan",
     "dt_all_gather_into_vec", "dt_broadcast", "dt_replicate_to_shard", "dt_all_to_all_dims",
     "dt_allreduce_coalesced", "dt_bucket_allreduce_noalloc", "dt_barrier", "dt_barrier_exchange", "HSDPPipeline", "Work", "DtError", "shard_views", "side_stream",
     "status_string", "version",
+    "dt_layer_norm", "dt_layer_norm_backward", "dt_layer_norm_workspace", "dt_moe_route", "dt_moe_route_backward",
+    "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
+    "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
 ]

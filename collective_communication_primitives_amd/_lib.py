@@ -19,6 +19,9 @@ EXPORTS = (
     "dt_barrier", "dt_barrier_exchange", "dt_bucket_plan", "dt_work_begin", "dt_work_end",
     "dt_work_wait", "dt_work_query", "dt_work_free", "dt_hsdp_create", "dt_hsdp_post_backward",
     "dt_hsdp_finish", "dt_hsdp_destroy", "dt_status_string", "dt_last_error", "dt_version",
+    "dt_layer_norm", "dt_layer_norm_backward", "dt_layer_norm_workspace", "dt_moe_route", "dt_moe_route_backward",
+    "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
+    "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
 )
 
 
@@ -33,6 +36,7 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
                           "(there is no non-HIP fallback)")
     lib = ctypes.CDLL(path)
     vp, sz, i32, u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint64
+    i64, f32 = ctypes.c_int64, ctypes.c_float
     sig = {
         "dt_allreduce": [vp, vp, i32, sz, i32, i32, vp],
         "dt_reduce_scatter": [vp, vp, i32, sz, i32, i32, vp],
@@ -57,6 +61,19 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
         "dt_hsdp_post_backward": [vp, vp, vp, i32, vp, vp],
         "dt_hsdp_finish": [vp, vp],
         "dt_hsdp_destroy": [vp],
+        "dt_layer_norm": [vp, vp, vp, vp, vp, vp, i32, vp, sz, f32, i32, vp],
+        "dt_layer_norm_backward": [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, i32, vp, sz, vp],
+        "dt_layer_norm_workspace": [i32, vp, sz],
+        "dt_moe_route": [vp, vp, vp, i32, vp, i32, i32, vp, i32, i32, i32, i32, f32, i32, vp],
+        "dt_moe_route_backward": [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, f32, i32, vp],
+        "dt_moe_dispatch": [vp, vp, vp, vp, vp, i32, vp, vp, sz, i32, i32, i32, vp, sz, vp],
+        "dt_moe_dispatch_workspace": [i32, vp, i32, i32],
+        "dt_moe_combine": [vp, vp, vp, vp, vp, i32, vp, vp, sz, i32, i32, i32, vp],
+        "dt_moe_combine_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, i32, i32, i32, vp],
+        "dt_vocab_loss": [vp, vp, vp, vp, vp, i32, vp, sz, sz, i64, i32, vp, sz, vp],
+        "dt_vocab_loss_workspace": [i32, vp, sz, sz, i32],
+        "dt_vocab_loss_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, sz, i64, sz, i32, vp, sz, vp],
+        "dt_vocab_loss_backward_workspace": [i32, vp, sz, sz, sz, i32],
         "dt_status_string": [i32],
         "dt_last_error": [],
         "dt_version": [],
@@ -64,5 +81,6 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
-        fn.restype = ctypes.c_char_p if name in ("dt_status_string", "dt_last_error", "dt_version") else ctypes.c_int
+        fn.restype = ctypes.c_char_p if name in ("dt_status_string", "dt_last_error", "dt_version") else \
+            sz if name.endswith("_workspace") else ctypes.c_int
     return lib

@@ -22,7 +22,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libdtcoll.so")
-SOURCES = ("api.cpp", "reduce.hip", "copy.hip", "barrier.hip", "scratch.hip")
+SOURCES = ("api.cpp", "reduce.hip", "copy.hip", "barrier.hip", "scratch.hip", "step_api.cpp", "norm.hip", "moe.hip",
+           "loss.hip")
 ARCH = os.environ.get("DT_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

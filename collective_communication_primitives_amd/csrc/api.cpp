@@ -14,6 +14,7 @@
 
 #include "dt.h"
 #include "dt_launch.h"
+#include "dt_step.h"
 
 static_assert(sizeof(dt::ReduceArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::PieceArgs) <= 4096, "kernel arguments must stay below 4 KiB");
@@ -1658,3 +1659,9 @@ dt_status dt_hsdp_destroy(dt_hsdp* h) {
 }
 
 }  // extern "C"
+
+// The last-error message of the entry points in step_api.cpp.
+dt_status dt::report_error(dt_status st, const char* message) {
+    g_last_error = message;
+    return st;
+}

@@ -1,0 +1,140 @@
+// dt_step.h -- kernel argument blocks and launchers of the model-step
+// operators whose mathematics crosses the ranks: layer norm (norm.hip),
+// expert routing and the experts' token exchange (moe.hip), the loss over a
+// sharded vocabulary (loss.hip).  step_api.cpp checks, plans and enqueues.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "dt.h"
+#include "dt_launch.h"
+
+namespace dt {
+
+// Records this thread's last error message (api.cpp) and hands `st` back.
+dt_status report_error(dt_status st, const char* message);
+
+// Rows of all ranks in rank order: rank r holds rows [start[r], start[r + 1]).
+// Entries past the last rank repeat the total, so a search needs no bound.
+struct RowTable {
+    uint32_t start[kMaxRanksHost + 1];
+};
+
+// ------------------------------------------------------------ layer norm --
+struct NormArgs {
+    const void* x[kMaxRanksHost];
+    const void* weight[kMaxRanksHost];
+    const void* bias[kMaxRanksHost];   // all NULL: no bias
+    void* y[kMaxRanksHost];
+    float* mean[kMaxRanksHost];        // all NULL: the statistics are not stored
+    float* rstd[kMaxRanksHost];
+    RowTable rows;
+    uint32_t cols;
+    float eps;
+    int nranks;
+};
+struct NormBackArgs {
+    const void* dy[kMaxRanksHost];
+    const void* x[kMaxRanksHost];
+    const void* weight[kMaxRanksHost];
+    const float* mean[kMaxRanksHost];
+    const float* rstd[kMaxRanksHost];
+    void* dx[kMaxRanksHost];
+    void* dweight[kMaxRanksHost];
+    void* dbias[kMaxRanksHost];        // all NULL: no bias
+    float* partial;                    // [strips][2][cols]
+    RowTable rows;
+    uint32_t cols;
+    uint32_t strips;
+    int nranks;
+};
+hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s);
+uint32_t norm_strips(uint32_t rows, uint32_t cols);
+hipError_t launch_norm_backward(const NormBackArgs& a, int dtype, hipStream_t s);
+
+// --------------------------------------------------------------- routing --
+struct RouteArgs {
+    const void* logits[kMaxRanksHost];
+    int32_t* experts[kMaxRanksHost];
+    float* weights[kMaxRanksHost];
+    const float* bias;
+    RowTable rows;
+    uint32_t nexperts, topk, groups, topk_groups;
+    int sigmoid, renormalize;
+    float scale;
+};
+struct RouteBackArgs {
+    const void* logits[kMaxRanksHost];
+    const int32_t* experts[kMaxRanksHost];
+    const float* dweights[kMaxRanksHost];
+    void* dlogits[kMaxRanksHost];
+    RowTable rows;
+    uint32_t nexperts, topk;
+    int sigmoid, renormalize;
+    float scale;
+};
+hipError_t launch_route(const RouteArgs& a, int nranks, int dtype, hipStream_t s);
+hipError_t launch_route_backward(const RouteBackArgs& a, int nranks, int dtype, hipStream_t s);
+
+// -------------------------------------------------------------- exchange --
+// A slot is one (rank, token, choice); slots are numbered in that order.
+constexpr uint32_t kPlanSlots = 2048;  // slots per workgroup of the plan
+struct PlanArgs {
+    const int32_t* experts[kMaxRanksHost];
+    int32_t* positions[kMaxRanksHost];
+    int32_t* offsets[kMaxRanksHost];
+    uint32_t capacity[kMaxRanksHost];
+    RowTable rows;
+    uint32_t* counts;                  // [plan workgroups][nexperts]
+    uint32_t nexperts, topk, per_rank;
+    int nranks;
+};
+// Row traffic between tokens (rank r's rows) and the experts' rows (rank q's
+// buffer): dispatch, combine and combine's backward pass.
+struct ExchangeRowsArgs {
+    const void* tokens_in[kMaxRanksHost];   // dispatch: x; combine's backward: dout
+    void* tokens_out[kMaxRanksHost];        // combine: out
+    const void* rows_in[kMaxRanksHost];     // combine and its backward: y
+    void* rows_out[kMaxRanksHost];          // dispatch: recv; combine's backward: dy
+    const int32_t* experts[kMaxRanksHost];
+    const int32_t* positions[kMaxRanksHost];
+    const float* weights[kMaxRanksHost];    // all NULL: ones
+    float* dweights[kMaxRanksHost];
+    uint32_t capacity[kMaxRanksHost];
+    RowTable rows;
+    uint32_t cols, nexperts, topk, per_rank;
+    int nranks;
+};
+inline uint32_t plan_blocks(uint64_t slots) { return uint32_t((slots + kPlanSlots - 1) / kPlanSlots); }
+hipError_t launch_plan(const PlanArgs& a, hipStream_t s);
+hipError_t launch_dispatch_rows(const ExchangeRowsArgs& a, int esize, hipStream_t s);
+hipError_t launch_combine(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
+hipError_t launch_combine_backward(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
+
+// ------------------------------------------------------- vocabulary loss --
+// Everything of one call; the launchers cut it into tiles and pieces.
+struct LossArgs {
+    const void* hidden[kMaxRanksHost];      // [tokens, cols] each
+    const void* weight[kMaxRanksHost];      // [vocab rows of rank r, cols]
+    const int64_t* targets[kMaxRanksHost];
+    float* loss[kMaxRanksHost];             // forward
+    float* lse[kMaxRanksHost];              // forward: written; backward: read
+    const float* dloss[kMaxRanksHost];
+    void* dhidden[kMaxRanksHost];
+    void* dweight[kMaxRanksHost];
+    RowTable vocab;                         // vocabulary rows of the ranks
+    uint32_t tokens, cols;
+    uint32_t piece;                         // backward: vocabulary rows per piece
+    int64_t ignore_index;
+    char* workspace;
+    int nranks;
+};
+uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype);
+uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype, uint64_t asked);
+uint64_t loss_backward_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, uint32_t piece,
+                                 int dtype);
+hipError_t launch_loss(const LossArgs& a, int dtype, hipStream_t s);
+hipError_t launch_loss_backward(const LossArgs& a, int dtype, hipStream_t s);
+
+}  // namespace dt

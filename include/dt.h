@@ -253,6 +253,140 @@ dt_status dt_barrier_exchange(const void* const* src, void* const* stage, void* 
                               int32_t* const* windows, int nranks, int32_t generation, int32_t* status_dev,
                               uint64_t timeout_ns, int layout, hipStream_t stream);
 
+/* ---- model-step operators across the ranks ---------------------------- */
+
+/* The steps of a model whose mathematics crosses the ranks, next to the
+ * collectives that the rest of the step uses.  Further conventions here:
+ *  - `rows`, `tokens`, `capacity`, `vocab_rows` are HOST arrays of nranks
+ *    counts; a rank may hold none (its pointers may then be NULL).  Fewer
+ *    than DT_MAX_STEP_ROWS rows in all.
+ *  - fp32 and bf16 tensors (DT_INT32: DT_ERR_UNSUPPORTED, but for the plain
+ *    copy of dt_moe_dispatch); arithmetic is fp32, one rounding at the end.
+ *    Results do not depend on timing: the same call gives the same bits.
+ *  - Inputs that every rank holds alike (weight, bias, hidden, targets, dloss)
+ *    may be one buffer listed nranks times; inputs may overlap each other.
+ *    A written buffer may overlap nothing (DT_ERR_ARG): no call is in place.
+ *  - Where a call takes a workspace, the matching _workspace function gives
+ *    its bytes (0 with dt_last_error set when the sizes are refused; a valid
+ *    call may need none).  It is 256-byte aligned device memory of the
+ *    caller, needs no initial value, holds nothing between calls, and may not
+ *    be shared by calls (or captured graphs) that may overlap in time.
+ *  - Every call may be captured into a HIP graph. */
+#define DT_MAX_STEP_ROWS (1 << 30)
+#define DT_MAX_STEP_COLS (1 << 18)
+#define DT_MAX_EXPERTS 1024
+#define DT_MAX_TOPK 64
+#define DT_MAX_GROUPS 64
+#define DT_MAX_LOSS_TOKENS (1 << 22)
+
+/* Layer norm of rows that are Shard(0) over the ranks: rank r holds x[r]
+ * [rows[r], cols], and weight[r], bias[r] [cols] (bias NULL: none).  Per row
+ * y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps), var the
+ * mean square of the centred row.  mean[r], rstd[r] [rows[r]] fp32 keep the
+ * statistics for the backward pass (both NULL: not kept). */
+dt_status dt_layer_norm(const void* const* x, const void* const* weight, const void* const* bias, void* const* y,
+                        float* const* mean, float* const* rstd, int nranks, const size_t* rows, size_t cols, float eps,
+                        dt_dtype dtype, hipStream_t stream);
+
+/* Its backward pass: dx[r] [rows[r], cols], and the gradients of weight and
+ * bias summed over the rows of ALL ranks, Partial -> Replicate: dweight[q],
+ * dbias[q] [cols] receive the sums for every rank q, as dt_allreduce of the
+ * ranks' own sums would leave them (dbias NULL: not formed).  No rows: zeros. */
+size_t dt_layer_norm_workspace(int nranks, const size_t* rows, size_t cols);
+dt_status dt_layer_norm_backward(const void* const* dy, const void* const* x, const void* const* weight,
+                                 const float* const* mean, const float* const* rstd, void* const* dx,
+                                 void* const* dweight, void* const* dbias, int nranks, const size_t* rows, size_t cols,
+                                 dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+typedef enum { DT_SCORE_SOFTMAX = 0, DT_SCORE_SIGMOID = 1 } dt_score;
+
+/* Routing of every rank's tokens to experts.  logits[r] [tokens[r], nexperts];
+ * scores s = softmax over the experts, or the sigmoid; candidates are ordered
+ * by s + bias (bias: one device array [nexperts] fp32 for all ranks, NULL:
+ * none; it balances the choice and does not enter the weights).  With groups
+ * > 1 the experts fall into `groups` equal runs, a run's score is the sum of
+ * its two largest candidates, and only the topk_groups best runs stay.
+ * experts[r] [tokens[r], topk] int32 gets the topk largest in descending
+ * order, the lowest index first among equals, and weights[r] [tokens[r],
+ * topk] fp32 their s, divided by the chosen s' sum when `renormalize`, times
+ * scale.  The order is that of the exact scores: the logits' own without a
+ * bias, 64-bit scores with one.  A logit or bias of -inf or NaN takes its
+ * expert out (a row of -inf is a padded token), +inf counts as the largest
+ * finite value; slots that no expert is left for get expert -1, weight 0. */
+dt_status dt_moe_route(const void* const* logits, int32_t* const* experts, float* const* weights, int nranks,
+                       const size_t* tokens, int nexperts, int topk, const float* bias, int groups, int topk_groups,
+                       dt_score score, int renormalize, float scale, dt_dtype dtype, hipStream_t stream);
+
+/* dlogits[r] [tokens[r], nexperts] from dweights[r] [tokens[r], topk], for the
+ * choice in experts[r] (an expert outside [0, nexperts) adds nothing).  The
+ * bias has no gradient. */
+dt_status dt_moe_route_backward(const void* const* logits, const int32_t* const* experts, const float* const* dweights,
+                                void* const* dlogits, int nranks, const size_t* tokens, int nexperts, int topk,
+                                dt_score score, int renormalize, float scale, dt_dtype dtype, hipStream_t stream);
+
+/* AllToAll of token rows to their experts' ranks, its splits decided on the
+ * device by the routing.  Rank q owns experts [q*E/P, (q+1)*E/P) (E =
+ * nexperts, divisible by P = nranks).  Row x[r][t] goes to the owner of
+ * every expert in experts[r][t*topk .. ], once per slot: recv[q]
+ * [capacity[q], cols] holds the rows ordered by expert, then by source rank,
+ * token and slot; offsets[q] [E/P + 1] int32 gives each owned expert's first
+ * row and the end.  positions[r] [tokens[r], topk] gets each slot's row in its
+ * owner's recv, or -1 where the expert is outside [0, E) or the owner's
+ * capacity is used up (offsets then end at the capacity).  Rows behind the
+ * last one are left as they were. */
+size_t dt_moe_dispatch_workspace(int nranks, const size_t* tokens, int nexperts, int topk);
+dt_status dt_moe_dispatch(const void* const* x, const int32_t* const* experts, void* const* recv,
+                          int32_t* const* positions, int32_t* const* offsets, int nranks, const size_t* tokens,
+                          const size_t* capacity, size_t cols, int nexperts, int topk, dt_dtype dtype, void* workspace,
+                          size_t workspace_bytes, hipStream_t stream);
+
+/* The way back: out[r][t] = sum over the slots j, in order, of weights[r][t,j]
+ * * y[owner][positions[r][t,j]] (weights NULL: all ones, which is also
+ * dt_moe_dispatch's backward pass).  A slot without a row (position outside
+ * the owner's capacity, or expert outside [0, E)) adds nothing. */
+dt_status dt_moe_combine(const void* const* y, const int32_t* const* experts, const int32_t* const* positions,
+                         const float* const* weights, void* const* out, int nranks, const size_t* tokens,
+                         const size_t* capacity, size_t cols, int nexperts, int topk, dt_dtype dtype,
+                         hipStream_t stream);
+
+/* Its backward pass: dy[owner][position] = weights * dout[r][t] for every slot
+ * with a row (positions as dt_moe_dispatch leaves them: no row twice; other
+ * rows of dy are left as they were), dweights = <dout[r][t], y row>, 0 for a
+ * slot without one. */
+dt_status dt_moe_combine_backward(const void* const* dout, const void* const* y, const int32_t* const* experts,
+                                  const int32_t* const* positions, const float* const* weights, void* const* dy,
+                                  float* const* dweights, int nranks, const size_t* tokens, const size_t* capacity,
+                                  size_t cols, int nexperts, int topk, dt_dtype dtype, hipStream_t stream);
+
+/* Softmax cross entropy over a vocabulary that is Shard(0) over the ranks,
+ * without keeping the logits.  hidden[r] [tokens, cols] is Replicate (rank
+ * r's shard is multiplied with hidden[r]); weight[r] [vocab_rows[r], cols]
+ * holds the next vocab_rows[r] rows of the vocabulary (V rows in all, at
+ * least one); targets[r] [tokens] int64.  lse[q] and loss[q] [tokens] fp32
+ * get log sum exp of the token's logits and lse - the target's logit for
+ * every rank q; a target equal to ignore_index or outside [0, V) leaves its
+ * token out (loss 0, no gradient). */
+size_t dt_vocab_loss_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols, dt_dtype dtype);
+dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, const int64_t* const* targets,
+                        float* const* loss, float* const* lse, int nranks, const size_t* vocab_rows, size_t tokens,
+                        size_t cols, int64_t ignore_index, dt_dtype dtype, void* workspace, size_t workspace_bytes,
+                        hipStream_t stream);
+
+/* Its gradients for dloss[r] [tokens] fp32 and the forward pass's lse.
+ * dhidden[q] [tokens, cols] gets the sum over all ranks' shards for every
+ * rank q (Partial -> Replicate, the AllReduce included); dweight[r]
+ * [vocab_rows[r], cols] is rank r's own.  The logits are formed again, one
+ * piece of at most piece_rows rows of a shard at a time (0: the library's
+ * choice); the workspace grows with the piece.  For bf16 tensors the logits'
+ * gradient is rounded to bf16 before it enters the two products. */
+size_t dt_vocab_loss_backward_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols,
+                                        size_t piece_rows, dt_dtype dtype);
+dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* weight, const int64_t* const* targets,
+                                 const float* const* lse, const float* const* dloss, void* const* dhidden,
+                                 void* const* dweight, int nranks, const size_t* vocab_rows, size_t tokens, size_t cols,
+                                 int64_t ignore_index, size_t piece_rows, dt_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
 /* ---- host planning (no GPU work) -------------------------------------- */
 
 /* One contiguous part of one tensor inside one bucket. */

@@ -1,0 +1,165 @@
+"""GPU: the loss over a sharded vocabulary and its gradients against the
+64-bit definition."""
+import pytest
+import torch
+
+import step_reference as ref
+from gpu_util import Guarded, note
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dt():
+    import collective_communication_primitives_amd as m
+    return m
+
+
+def _make(tokens, cols, shards, dtype, seed, offset=0, replicas=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    v = sum(shards)
+
+    def rows(n, std):
+        t = torch.empty(n * cols + offset, dtype=dtype, device="cuda")
+        t[offset:] = (torch.randn(n * cols, generator=g, device="cuda") * std).to(dtype)
+        return t[offset:].view(n, cols)
+
+    weight = [rows(n, 2.0 / cols ** 0.5) for n in shards]
+    hidden = rows(tokens, 1.0)
+    targets = torch.randint(0, v, (tokens,), generator=g, device="cuda")
+    if tokens > 3:
+        targets[1] = -100
+        targets[tokens - 1] = v - 1
+        targets[2] = 0
+    dloss = torch.randn(tokens, generator=g, device="cuda")
+    p = len(shards)
+    if replicas:
+        return [hidden.clone() if offset == 0 else hidden for _ in range(p)], weight, [targets.clone() for _ in range(p)], [
+            dloss.clone() for _ in range(p)]
+    return [hidden] * p, weight, [targets] * p, [dloss] * p
+
+
+def _run(dt, hidden, weight, targets, dloss, offset=0, **kw):
+    p, (tokens, cols), dtype = len(hidden), hidden[0].shape, hidden[0].dtype
+    loss = [Guarded(tokens, torch.float32).poison() for _ in range(p)]
+    lse = [Guarded(tokens, torch.float32).poison() for _ in range(p)]
+    dh = [Guarded(tokens * cols, dtype, offset_elems=offset).poison() for _ in range(p)]
+    dw = [Guarded(w.numel(), dtype, offset_elems=offset).poison() for w in weight]
+    ign = {k: v for k, v in kw.items() if k == "ignore_index"}
+    dt.dt_vocab_loss(hidden, weight, targets, [g.t for g in loss], [g.t for g in lse], **ign)
+    dt.dt_vocab_loss_backward(hidden, weight, targets, [g.t for g in lse], dloss, [g.t for g in dh], [g.t for g in dw], **kw)
+    torch.cuda.synchronize()
+    for g in loss + lse + dh + dw:
+        g.check()
+    return loss, lse, dh, dw
+
+
+def _check(dt, hidden, weight, targets, dloss, offset=0, **kw):
+    loss, lse, dh, dw = _run(dt, hidden, weight, targets, dloss, offset, **kw)
+    cols = hidden[0].shape[1]
+    want = ref.loss(hidden[0], weight, targets[0], dloss[0], kw.get("ignore_index", -100))
+    for q in range(len(hidden)):
+        ref.assert_close(lse[q].t, *want["lse"], f"lse[{q}]")
+        ref.assert_close(loss[q].t, *want["loss"], f"loss[{q}]")
+        ref.assert_close(dh[q].t.view(-1, cols), *want["dhidden"], f"dhidden[{q}]")
+        ref.assert_close(dw[q].t.view(-1, cols), want["dweight"][0][q], want["dweight"][1][q], f"dweight[{q}]")
+
+
+CASES = [
+    # tokens, cols, shards, piece
+    (1, 1, [1], 0), (1, 8, [2], 0), (3, 16, [5, 0, 4], 0), (5, 64, [130], 0), (2, 128, [100, 300], 0), (17, 100, [70, 33], 0),
+    (64, 256, [128, 128], 0), (65, 72, [257], 100), (130, 512, [200, 120, 77], 64), (129, 1000, [333, 1, 400], 0),
+    (300, 136, [260, 250], 96), (33, 1024, [1000], 0), (7, 33, [64] * 16, 0), (260, 40, [520, 10], 300), (16, 4096, [300, 500], 0),
+    (257, 320, [700, 513], 256), (1, 2048, [5000, 3001], 0), (4, 520, [1030], 0),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("tokens,cols,shards,piece", CASES, ids=lambda v: str(v).replace(" ", "")[:24])
+def test_loss_and_its_gradients(dt, tokens, cols, shards, piece, dtype):
+    note(f"loss tokens={tokens} cols={cols} shards={shards} piece={piece} {dtype}")
+    _check(dt, *_make(tokens, cols, shards, dtype, 5), piece_rows=piece)
+
+
+@pytest.mark.parametrize("off", [1, 2, 4])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_rows_off_alignment(dt, dtype, off):
+    note(f"loss off alignment {off} {dtype}")
+    _check(dt, *_make(70, 136, [190, 45], dtype, 6, offset=off), offset=off)
+
+
+def test_all_tokens_left_out(dt):
+    note("loss all ignored")
+    h, w, t, g = _make(9, 64, [40, 30], torch.bfloat16, 7)
+    for bad in (-100, 70, 2 ** 40, -1):
+        t = [torch.full_like(x, bad) for x in t]
+        loss, lse, dh, dw = _run(dt, h, w, t, g)
+        assert all(bool((v.t == 0).all()) for v in loss + dh + dw)
+        assert all(bool(v.t.isfinite().all()) for v in lse)
+
+
+def test_ignore_index_inside_the_vocabulary(dt):
+    note("loss ignore_index 3")
+    h, w, t, g = _make(40, 96, [50, 30], torch.float32, 8)
+    t = [x.clone() for x in t]
+    for x in t:
+        x[::3] = 3
+    _check(dt, h, w, t, g, ignore_index=3)
+
+
+def test_no_tokens_give_zero_weight_gradients(dt):
+    note("loss without tokens")
+    h, w, t, g = _make(0, 64, [40, 30], torch.float32, 9)
+    loss, lse, dh, dw = _run(dt, h, w, t, g)
+    assert all(bool((v.t == 0).all()) for v in dw)
+
+
+def test_large_logits_do_not_overflow(dt):
+    note("loss large logits")
+    h, w, t, g = _make(30, 64, [100, 28], torch.float32, 10)
+    h = [x * 300 for x in h]
+    _check(dt, h, w, t, g)
+
+
+def test_nan_stays_in_its_token(dt):
+    note("loss NaN row")
+    h, w, t, g = _make(20, 64, [100, 28], torch.bfloat16, 11, replicas=False)
+    h[0][4, 3] = float("nan")
+    loss, lse, dh, dw = _run(dt, h, w, t, g)
+    bad = lse[0].t.isnan()
+    assert bool(bad[4]) and int(bad.sum()) == 1
+    rows = dh[0].t.view(20, 64).isnan().any(1)
+    assert bool(rows[4]) and int(rows.sum()) == 1
+
+
+@pytest.mark.parametrize("piece", [1, 7, 64, 1000])
+def test_pieces_give_one_result(dt, piece):
+    """The piece changes only how dhidden's sum is cut."""
+    note(f"loss piece {piece}")
+    _check(dt, *_make(50, 96, [120, 60], torch.float32, 12), piece_rows=piece)
+
+
+def test_gradients_against_differences(dt):
+    note("loss gradients by differences")
+    h, w, t, g = _make(4, 24, [9, 6], torch.float32, 13)
+    _, _, dh, dw = _run(dt, h, w, t, g)
+    use = t[0] >= 0
+
+    def value(x, ws):
+        z = x @ torch.cat(ws).t()
+        at = t[0].clamp(min=0)
+        return float(((torch.logsumexp(z, 1) - z.gather(1, at[:, None])[:, 0]) * use * g[0].double()).sum())
+
+    e = 1e-5
+    x, ws = h[0].double(), [s.double() for s in w]
+    for i in range(4):
+        for c in range(0, 24, 5):
+            up, dn = x.clone(), x.clone()
+            up[i, c] += e
+            dn[i, c] -= e
+            assert abs((value(up, ws) - value(dn, ws)) / (2 * e) - float(dh[0].t.view(4, 24)[i, c])) < 2e-5
+    for v in range(9):
+        up, dn = [s.clone() for s in ws], [s.clone() for s in ws]
+        up[0][v, 3] += e
+        dn[0][v, 3] -= e
+        assert abs((value(x, up) - value(x, dn)) / (2 * e) - float(dw[0].t.view(9, 24)[v, 3])) < 2e-5

@@ -1,0 +1,207 @@
+"""CPU: the model-step entry points refuse what they cannot do, with a status
+and a message, before anything is queued (the pointers here are not memory)."""
+import ctypes
+
+import pytest
+
+ARG, UNSUPPORTED = 1, 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from collective_communication_primitives_amd import _lib
+    return _lib.load()
+
+
+def ptrs(*v):
+    return (ctypes.c_void_p * len(v))(*v)
+
+
+def sizes(*v):
+    return (ctypes.c_size_t * len(v))(*v)
+
+
+A, B, C, D, E, F, G, H, W = (0x100000 * i for i in range(1, 10))
+
+
+def norm(lib, **kw):
+    a = dict(x=ptrs(A, A + 4096), w=ptrs(B, B), b=ptrs(B + 4096, B + 4096), y=ptrs(C, C + 4096), m=ptrs(D, D + 64),
+             r=ptrs(E, E + 64), p=2, rows=sizes(2, 3), cols=8, eps=1e-5, dtype=0)
+    a.update(kw)
+    return lib.dt_layer_norm(a["x"], a["w"], a["b"], a["y"], a["m"], a["r"], a["p"], a["rows"], a["cols"], a["eps"], a["dtype"],
+                             None)
+
+
+def norm_back(lib, **kw):
+    a = dict(dy=ptrs(A, A + 4096), x=ptrs(A, A + 4096), w=ptrs(B, B), m=ptrs(D, D + 64), r=ptrs(E, E + 64),
+             dx=ptrs(C, C + 4096), dw=ptrs(F, F + 4096), db=ptrs(G, G + 4096), p=2, rows=sizes(2, 3), cols=8, dtype=0, ws=W,
+             n=1 << 20)
+    a.update(kw)
+    return lib.dt_layer_norm_backward(a["dy"], a["x"], a["w"], a["m"], a["r"], a["dx"], a["dw"], a["db"], a["p"], a["rows"],
+                                      a["cols"], a["dtype"], a["ws"], a["n"], None)
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(p=0), ARG, "nranks"), (dict(p=17), ARG, "nranks"), (dict(dtype=2), UNSUPPORTED, "int32"), (dict(dtype=7), ARG, "dtype"),
+    (dict(rows=None), ARG, "rows"), (dict(rows=sizes(1 << 30, 0)), ARG, "rows"), (dict(rows=sizes(1 << 63, 1 << 63)), ARG, "rows"),
+    (dict(cols=0), ARG, "cols"), (dict(cols=1 << 19), ARG, "cols"), (dict(eps=-1.0), ARG, "eps"), (dict(eps=float("nan")), ARG, "eps"),
+    (dict(x=None), ARG, "x is NULL"), (dict(x=ptrs(A, 0)), ARG, "x[1]"), (dict(x=ptrs(A, A + 4097)), ARG, "aligned"),
+    (dict(y=ptrs(A, C)), ARG, "overlap"), (dict(y=ptrs(C, C + 32)), ARG, "overlap"), (dict(m=None), ARG, "together"),
+    (dict(w=ptrs(B, C + 8)), ARG, "overlap"), (dict(b=ptrs(B, 0)), ARG, "bias[1]"), (dict(m=ptrs(D, E)), ARG, "overlap"),
+])
+def test_layer_norm(lib, kw, status, word):
+    assert norm(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(ws=0), ARG, "workspace"), (dict(n=16), ARG, "workspace"), (dict(ws=W + 16), ARG, "256"), (dict(ws=F), ARG, "overlap"),
+    (dict(dw=ptrs(F, F)), ARG, "overlap"), (dict(db=ptrs(F, G)), ARG, "overlap"), (dict(dx=ptrs(A, C)), ARG, "overlap"),
+    (dict(m=None), ARG, "mean"), (dict(r=ptrs(0, E)), ARG, "rstd[0]"), (dict(dtype=2), UNSUPPORTED, "int32"),
+])
+def test_layer_norm_backward(lib, kw, status, word):
+    assert norm_back(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def route(lib, **kw):
+    a = dict(x=ptrs(A), e=ptrs(B), w=ptrs(C), p=1, n=sizes(4), ne=16, k=2, b=None, g=1, tg=1, s=0, rn=1, dtype=0)
+    a.update(kw)
+    return lib.dt_moe_route(a["x"], a["e"], a["w"], a["p"], a["n"], a["ne"], a["k"], a["b"], a["g"], a["tg"], a["s"], a["rn"], 1.0,
+                            a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(p=17), ARG, "nranks"), (dict(ne=0), ARG, "nexperts"), (dict(ne=1025), ARG, "nexperts"), (dict(k=0), ARG, "topk"),
+    (dict(k=17), ARG, "topk"), (dict(ne=1024, k=65), ARG, "topk"), (dict(g=3), ARG, "groups"), (dict(g=0), ARG, "groups"),
+    (dict(ne=130, g=65, tg=1), ARG, "groups"), (dict(g=4, tg=0), ARG, "topk_groups"), (dict(g=4, tg=5), ARG, "topk_groups"),
+    (dict(g=8, tg=1, k=3), ARG, "topk"), (dict(s=2), ARG, "score"), (dict(dtype=2), UNSUPPORTED, "int32"), (dict(e=ptrs(C)), ARG, "overlap"),
+    (dict(b=C), ARG, "overlap"), (dict(b=A + 1), ARG, "aligned"), (dict(x=ptrs(0)), ARG, "logits[0]"), (dict(n=sizes(1 << 31)), ARG, "tokens"),
+])
+def test_route(lib, kw, status, word):
+    assert route(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def route_back(lib, **kw):
+    a = dict(x=ptrs(A), e=ptrs(B), w=ptrs(C), d=ptrs(D), p=1, n=sizes(4), ne=16, k=2, s=0, dtype=0)
+    a.update(kw)
+    return lib.dt_moe_route_backward(a["x"], a["e"], a["w"], a["d"], a["p"], a["n"], a["ne"], a["k"], a["s"], 1, 1.0, a["dtype"], None)
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(d=ptrs(A)), ARG, "overlap"), (dict(d=None), ARG, "dlogits"), (dict(k=17), ARG, "topk"), (dict(s=-1), ARG, "score"),
+    (dict(dtype=2), UNSUPPORTED, "int32"),
+])
+def test_route_backward(lib, kw, status, word):
+    assert route_back(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def dispatch(lib, **kw):
+    a = dict(x=ptrs(A, A + 4096), e=ptrs(B, B + 4096), r=ptrs(C, C + 4096), pos=ptrs(D, D + 4096), off=ptrs(E, E + 4096), p=2,
+             n=sizes(4, 4), cap=sizes(8, 8), cols=8, ne=4, k=2, dtype=0, ws=W, wn=1 << 20)
+    a.update(kw)
+    return lib.dt_moe_dispatch(a["x"], a["e"], a["r"], a["pos"], a["off"], a["p"], a["n"], a["cap"], a["cols"], a["ne"], a["k"],
+                               a["dtype"], a["ws"], a["wn"], None)
+
+
+@pytest.mark.parametrize("kw,status,word", [
+    (dict(p=0), ARG, "nranks"), (dict(ne=3), ARG, "divide"), (dict(cap=None), ARG, "capacity"), (dict(cap=sizes(8, 1 << 30)), ARG, "capacity"),
+    (dict(n=sizes(1 << 29, 1 << 29)), ARG, "tokens"), (dict(n=sizes(1 << 28, 1 << 28)), ARG, "slots"), (dict(dtype=5), ARG, "dtype"),
+    (dict(ws=0), ARG, "workspace"), (dict(wn=3), ARG, "workspace"), (dict(r=ptrs(C, C + 64)), ARG, "overlap"),
+    (dict(r=ptrs(A, C)), ARG, "overlap"), (dict(off=ptrs(E, E + 4)), ARG, "overlap"), (dict(off=ptrs(E, 0)), ARG, "offsets[1]"),
+    (dict(cols=0), ARG, "cols"), (dict(k=5), ARG, "topk"),
+])
+def test_dispatch(lib, kw, status, word):
+    assert dispatch(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def combine(lib, **kw):
+    a = dict(y=ptrs(C, C + 4096), e=ptrs(B, B + 4096), pos=ptrs(D, D + 4096), w=None, out=ptrs(A, A + 4096), p=2, n=sizes(4, 4),
+             cap=sizes(8, 8), cols=8, ne=4, k=2, dtype=0)
+    a.update(kw)
+    return lib.dt_moe_combine(a["y"], a["e"], a["pos"], a["w"], a["out"], a["p"], a["n"], a["cap"], a["cols"], a["ne"], a["k"],
+                              a["dtype"], None)
+
+
+def combine_back(lib, **kw):
+    a = dict(do=ptrs(A, A + 4096), y=ptrs(C, C + 4096), e=ptrs(B, B + 4096), pos=ptrs(D, D + 4096), w=ptrs(E, E + 4096),
+             dy=ptrs(F, F + 4096), dw=ptrs(G, G + 4096), p=2, n=sizes(4, 4), cap=sizes(8, 8), cols=8, ne=4, k=2, dtype=0)
+    a.update(kw)
+    return lib.dt_moe_combine_backward(a["do"], a["y"], a["e"], a["pos"], a["w"], a["dy"], a["dw"], a["p"], a["n"], a["cap"],
+                                       a["cols"], a["ne"], a["k"], a["dtype"], None)
+
+
+@pytest.mark.parametrize("fn,kw,status,word", [
+    (combine, dict(dtype=2), UNSUPPORTED, "int32"), (combine, dict(out=ptrs(C, A)), ARG, "overlap"),
+    (combine, dict(out=ptrs(A, A)), ARG, "overlap"), (combine, dict(pos=ptrs(D, 0)), ARG, "positions[1]"), (combine, dict(y=None), ARG, "y is NULL"),
+    (combine_back, dict(w=None), ARG, "weights"), (combine_back, dict(dy=ptrs(C, F)), ARG, "overlap"),
+    (combine_back, dict(dw=ptrs(E, G)), ARG, "overlap"), (combine_back, dict(dtype=2), UNSUPPORTED, "int32"),
+    (combine_back, dict(ne=5), ARG, "divide"),
+])
+def test_combine(lib, fn, kw, status, word):
+    assert fn(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def loss(lib, **kw):
+    a = dict(h=ptrs(A, A), w=ptrs(B, B + 4096), t=ptrs(C, C), l=ptrs(D, D + 64), s=ptrs(E, E + 64), p=2, v=sizes(5, 6), n=4, cols=8,
+             dtype=0, ws=W, wn=1 << 22)
+    a.update(kw)
+    return lib.dt_vocab_loss(a["h"], a["w"], a["t"], a["l"], a["s"], a["p"], a["v"], a["n"], a["cols"], -100, a["dtype"], a["ws"],
+                             a["wn"], None)
+
+
+def loss_back(lib, **kw):
+    a = dict(h=ptrs(A, A), w=ptrs(B, B + 4096), t=ptrs(C, C), s=ptrs(E, E), g=ptrs(D, D), dh=ptrs(F, F + 4096), dw=ptrs(G, G + 4096),
+             p=2, v=sizes(5, 6), n=4, cols=8, piece=0, dtype=0, ws=W, wn=1 << 22)
+    a.update(kw)
+    return lib.dt_vocab_loss_backward(a["h"], a["w"], a["t"], a["s"], a["g"], a["dh"], a["dw"], a["p"], a["v"], a["n"], a["cols"],
+                                      -100, a["piece"], a["dtype"], a["ws"], a["wn"], None)
+
+
+@pytest.mark.parametrize("fn,kw,status,word", [
+    (loss, dict(p=-1), ARG, "nranks"), (loss, dict(v=sizes(0, 0)), ARG, "vocabulary is empty"), (loss, dict(n=1 << 23), ARG, "tokens"),
+    (loss, dict(dtype=2), UNSUPPORTED, "int32"), (loss, dict(l=ptrs(D, D)), ARG, "overlap"), (loss, dict(l=ptrs(E, D)), ARG, "overlap"),
+    (loss, dict(wn=8), ARG, "workspace"), (loss, dict(ws=W + 128), ARG, "256"), (loss, dict(t=ptrs(C, C + 4)), ARG, "aligned"),
+    (loss, dict(w=ptrs(B, 0)), ARG, "weight[1]"), (loss, dict(v=None), ARG, "vocab_rows"), (loss, dict(cols=0), ARG, "cols"),
+    (loss_back, dict(dh=ptrs(F, F)), ARG, "overlap"), (loss_back, dict(dh=ptrs(A, F)), ARG, "overlap"),
+    (loss_back, dict(dw=ptrs(B, G)), ARG, "overlap"), (loss_back, dict(wn=64), ARG, "workspace"), (loss_back, dict(s=None), ARG, "lse"),
+    (loss_back, dict(g=ptrs(0, D)), ARG, "dloss[0]"), (loss_back, dict(ws=G), ARG, "overlap"),
+])
+def test_loss(lib, fn, kw, status, word):
+    assert fn(lib, **kw) == status
+    assert word in lib.dt_last_error().decode()
+
+
+def test_workspace_sizes_refuse_like_the_calls(lib):
+    assert lib.dt_layer_norm_workspace(0, sizes(1), 8) == 0 and lib.dt_last_error()
+    assert lib.dt_layer_norm_workspace(1, sizes(0), 8) == 0 and not lib.dt_last_error()
+    assert lib.dt_moe_dispatch_workspace(1, sizes(4), 16, 17) == 0 and lib.dt_last_error()
+    assert lib.dt_vocab_loss_workspace(1, sizes(0), 4, 8, 0) == 0 and lib.dt_last_error()
+    assert lib.dt_vocab_loss_backward_workspace(1, sizes(5), 4, 8, 0, 2) == 0 and lib.dt_last_error()
+    a = lib.dt_vocab_loss_backward_workspace(1, sizes(5000), 64, 64, 100, 1)
+    b = lib.dt_vocab_loss_backward_workspace(1, sizes(5000), 64, 64, 1000, 1)
+    assert 0 < a < b
+
+
+def test_calls_without_rows_do_nothing(lib):
+    assert norm(lib, rows=sizes(0, 0), x=ptrs(0, 0), y=ptrs(0, 0)) == 0
+    assert route(lib, n=sizes(0), x=ptrs(0)) == 0
+    assert combine(lib, n=sizes(0, 0), out=ptrs(0, 0)) == 0
+    assert combine_back(lib, n=sizes(0, 0)) == 0
+    assert loss(lib, n=0) == 0
+
+
+def test_workspace_functions_of_the_binding_raise():
+    import torch
+
+    import collective_communication_primitives_amd as dt
+    with pytest.raises(dt.DtError):
+        dt.dt_layer_norm_workspace([1], 0)
+    with pytest.raises(dt.DtError):
+        dt.dt_vocab_loss_workspace([0], 4, 8, torch.float32)
+    assert dt.dt_layer_norm_workspace([0], 8) == 0
+    assert dt.dt_moe_dispatch_workspace([100, 28], 8, 2) > 0

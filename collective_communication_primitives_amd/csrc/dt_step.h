@@ -113,14 +113,16 @@ hipError_t launch_combine(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_combine_backward(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
 
 // ------------------------------------------------------- vocabulary loss --
-// Everything of one call; the launchers cut it into tiles and pieces.
+// Everything of one call; the launchers cut it into tiles and pieces.  Of the
+// inputs that are Replicate, rank 0's copy is read.
 struct LossArgs {
-    const void* hidden[kMaxRanksHost];      // [tokens, cols] each
+    const void* hidden;                     // [tokens, cols]
     const void* weight[kMaxRanksHost];      // [vocab rows of rank r, cols]
-    const int64_t* targets[kMaxRanksHost];
+    const int64_t* targets;
+    const float* lse_in;                    // backward
+    const float* dloss;
     float* loss[kMaxRanksHost];             // forward
-    float* lse[kMaxRanksHost];              // forward: written; backward: read
-    const float* dloss[kMaxRanksHost];
+    float* lse[kMaxRanksHost];
     void* dhidden[kMaxRanksHost];
     void* dweight[kMaxRanksHost];
     RowTable vocab;                         // vocabulary rows of the ranks
@@ -130,10 +132,10 @@ struct LossArgs {
     char* workspace;
     int nranks;
 };
+constexpr uint32_t kLossPiece = 16384;      // vocabulary rows per piece, unless the caller says otherwise
+uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t asked);
 uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype);
-uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype, uint64_t asked);
-uint64_t loss_backward_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, uint32_t piece,
-                                 int dtype);
+uint64_t loss_backward_workspace(int nranks, uint64_t tokens, uint64_t cols, uint32_t piece, int dtype);
 hipError_t launch_loss(const LossArgs& a, int dtype, hipStream_t s);
 hipError_t launch_loss_backward(const LossArgs& a, int dtype, hipStream_t s);
 

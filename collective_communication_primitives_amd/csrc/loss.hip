@@ -11,11 +11,14 @@
 // tile's maximum and sum of exponentials per token; a second kernel joins
 // them over the tiles of all ranks (the AllReduces of the maximum and the sum
 // that a sharded vocabulary needs).  The backward pass forms the logits
-// again, one piece of a rank's vocabulary at a time, and multiplies the
-// piece's d into both gradients.
+// again, one piece of the vocabulary at a time (a piece may span ranks), and
+// multiplies the piece's d into both gradients.
 //
-// All products have both operands contiguous along the summed index, so one
-// matrix routine serves: out[n][m] = sum_k A[m][k] B[n][k].
+// All three products are the same routine: out[n][m] = sum_k A(m, k) B(n, k),
+// where an operand lies in memory either with k contiguous (kRows: hidden,
+// weight in the logits; d in dhidden) or with m or n contiguous (kCols:
+// weight in dhidden, hidden and d in dweight).  The second kind is turned on
+// the way from LDS to the registers, so nothing is stored transposed.
 #include "dt_step_device.h"
 
 namespace dt {
@@ -23,13 +26,17 @@ namespace {
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+#define DT_LDS __attribute__((address_space(3)))
 
-constexpr int kChunks = 8;        // 16-byte chunks of the summed index per step: 128 bytes of a row
-constexpr int kThreads = 256;     // workgroups of the kernels without a matrix tile
+constexpr int kChunks = 8;             // 16-byte chunks of the summed index per step
+constexpr int kStepBytes = kChunks * 16;
+constexpr int kThreads = 256;          // workgroups of the kernels without a matrix tile
+enum { kRows = 0, kCols = 1 };
 
 // A workgroup's tile of `out`: BM rows of A by BN rows of B, cut among GM x GN
-// waves.  Both operands are staged through LDS, two steps of 128 bytes of the
-// summed index at a time (one is multiplied while the next one loads).
+// waves.  Both operands are staged through LDS, two steps of the summed
+// index at a time (one is multiplied while the next one loads).
 template <int BM_, int BN_, int GM_, int GN_>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, GM = GM_, GN = GN_;
@@ -37,76 +44,147 @@ struct Shape {
     static constexpr int WM = BM / GM, WN = BN / GN;  // a wave's part
     static constexpr int MI = WM / 16, NI = WN / 16;  // in matrix instructions of 16 x 16
     static constexpr int lds = 2 * (BM + BN) * kChunks;  // u32x4
-    static constexpr int loads = (BM + BN) / 8 / waves;  // load instructions of 8 rows per wave and step
+    static constexpr int loads = (BM + BN) / 8 / waves;  // load instructions of 1 KiB per wave and step
 };
 
-template <int DT>
-struct Chunk {
-    static constexpr int elems = 16 / int(sizeof(typename Elem<DT>::type));
+// Where an operand's bytes of one step are: the buffer resource ends behind
+// the last valid row, so what lies past it loads zeros.
+struct StepSource {
+    const char* base;
+    uint64_t valid;   // bytes from base
 };
-
-// One operand: rows of `ld` elements, 16-byte aligned; the buffer resource
-// ends behind the last row, so rows past it load zeros.
-struct Operand {
-    rsrc_t r;
-    uint32_t pitch;   // bytes per row
-};
-__device__ __forceinline__ Operand operand(const void* p, uint32_t rows, int most, uint64_t pitch) {
-    const uint32_t n = rows < uint32_t(most) ? rows : uint32_t(most);
-    return Operand{make_rsrc(p, uint32_t(n * pitch)), uint32_t(pitch)};
+__device__ __forceinline__ rsrc_t step_rsrc(const StepSource& s) {
+    return make_rsrc(s.base, uint32_t(s.valid < 0x7FFFFFFFull ? s.valid : 0x7FFFFFFFull));
 }
 
-// acc[i][j][e]: row m = WM (wave % GM) + 16 i + 4 (lane / 16) + e of A's tile,
-// row n = WN (wave / GM) + 16 j + lane % 16 of B's.  `steps` is the number of
-// 128-byte steps, `bytes` the valid bytes of a row (a multiple of 16).
-template <int DT, typename S>
-__device__ __forceinline__ void matrix_tile(const Operand& A, const Operand& B, uint32_t first, uint32_t bytes,
-                                            u32x4* lds, f32x4 (&acc)[S::MI][S::NI]) {
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+// kRows: rows of `pitch` bytes, `bytes` of them valid (a multiple of 16).
+struct RowOperand {
+    const char* p;     // the tile's first row
+    uint32_t rows, pitch, bytes;
+    __device__ __forceinline__ StepSource at(uint32_t) const { return StepSource{p, uint64_t(rows) * pitch}; }
+};
+// kCols: row k of `pitch` bytes holds the operand's m (or n) side by side.
+template <int KR>
+struct ColOperand {
+    const char* p;     // row 0 at the tile's first column
+    uint64_t rows, pitch, skip;   // skip: bytes of a row before the tile
+    __device__ __forceinline__ StepSource at(uint32_t step) const {
+        const uint64_t k = uint64_t(step) * KR, left = k < rows ? rows - k : 0;
+        return StepSource{p + k * pitch, left > 0 ? (left < KR ? left : KR) * pitch - skip : 0};
+    }
+};
+
+// Rows of k per step and the turned layout of a kCols operand in LDS: a row
+// of k holds R elements in units of 16, unit u of row k in place u ^ f(k),
+// where f differs between the rows that one read instruction touches.
+template <int DT, int R>
+struct ColTile {
+    static constexpr int ES = DT == kBF16 ? 2 : 4;
+    static constexpr int KR = kStepBytes / ES;
+    static constexpr int row_bytes = R * ES, units = R / 16, unit_bytes = 16 * ES;
+    static constexpr int per_load = 1024 / row_bytes;  // rows per load instruction
+    static __device__ __forceinline__ uint32_t f(uint32_t k) {
+        if constexpr (DT == kBF16) return units >= 8 ? (k & 3) | ((k >> 3) & 1) << 2 : k & 3;
+        else return (k >> 2) & 3;
+    }
+};
+
+// One load instruction of the wave: 1 KiB of the operand's step into LDS.
+template <int DT, int MODE, int R, typename OP>
+__device__ __forceinline__ void load_group(const OP& op, rsrc_t r, uint32_t group, uint32_t step, DT_LDS void* to) {
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t off;
+    if constexpr (MODE == kRows) {
+        // 8 rows of 128 bytes: lane l brings row l / 8.  The chunk that lands in
+        // place l % 8 is turned by the row, so that the 16 rows that a read of
+        // one chunk touches spread over all banks.
+        const uint32_t row = lane >> 3, c = step * kStepBytes + ((lane & 7) ^ row) * 16;
+        off = c < op.bytes ? (group * 8 + row) * op.pitch + c : 0x80000000u;
+    } else {
+        typedef ColTile<DT, R> C;
+        constexpr uint32_t slots = C::row_bytes / 16, per_unit = C::unit_bytes / 16;
+        const uint32_t k = group * C::per_load + lane / slots, slot = lane % slots;
+        off = k * uint32_t(op.pitch) + ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, int(off), 0, 0, 0);
+}
+
+// The wave's registers of 16 rows (of A or B) from row `at` of the tile, part
+// kk of the step: lane l gets row l % 16 and 16 bytes of k.
+template <int DT, int MODE, int R>
+__device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t at, int kk) {
+    const uint32_t lane = threadIdx.x & 63;
+    if constexpr (MODE == kRows) {
+        const uint32_t row = at + (lane & 15), c = kk * 4 + (lane >> 4);
+        return tile[row * kChunks + (c ^ (row & 7))];
+    } else if constexpr (DT == kBF16) {
+        // k = 32 kk + 8 (lane / 16) + 0..7: two transposing reads of 4 rows of k x 16 each
+        typedef ColTile<DT, R> C;
+        u32x4 v;
+        const char* base = reinterpret_cast<const char*>(tile);
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const uint32_t k = kk * 32 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
+            const uint32_t off = k * C::row_bytes + ((at / 16) ^ C::f(k)) * C::unit_bytes + (lane & 3) * 8;
+            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DT_LDS s16x4*)(base + off));
+            uint32_t w[2];
+            __builtin_memcpy(w, &x, 8);
+            v[2 * h] = w[0];
+            v[2 * h + 1] = w[1];
+        }
+        return v;
+    } else {
+        // k = 16 kk + 4 (lane / 16) + 0..3
+        typedef ColTile<DT, R> C;
+        u32x4 v;
+        const char* base = reinterpret_cast<const char*>(tile);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const uint32_t k = kk * 16 + (lane >> 4) * 4 + e;
+            v[e] = *reinterpret_cast<const uint32_t*>(base + k * C::row_bytes + ((at / 16) ^ C::f(k)) * C::unit_bytes +
+                                                      (lane & 15) * 4);
+        }
+        return v;
+    }
+}
+
+// acc[i][j][e] over steps [lo, hi): row m = WM (wave % GM) + 16 i + 4 (lane /
+// 16) + e of A's tile, row n = WN (wave / GM) + 16 j + lane % 16 of B's.
+template <int DT, typename S, int MA, int MB, typename OA, typename OB>
+__device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t lo, uint32_t hi, u32x4* lds,
+                                            f32x4 (&acc)[S::MI][S::NI]) {
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
     for (int i = 0; i < S::MI; i++)
 #pragma unroll
         for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (first >= bytes) return;
-    // A load instruction fills 8 rows of 128 bytes: lane l brings row l / 8.
-    // The chunk that lands in place l % 8 is turned by the row, so that the 16
-    // rows that a read of one chunk touches spread over all banks.
-    const uint32_t row = lane >> 3, turn = ((lane & 7) ^ row) * 16;
-    auto stage = [&](uint32_t at, int buf) {
+    if (lo >= hi) return;
+    auto stage = [&](uint32_t step, int buf) {
         u32x4* to = lds + buf * (S::BM + S::BN) * kChunks;
-        const bool in = at + turn < bytes;  // zeros behind the row's end
+        const rsrc_t ra = step_rsrc(A.at(step)), rb = step_rsrc(B.at(step));
 #pragma unroll
         for (int i = 0; i < S::loads; i++) {
-            const uint32_t g = wave * S::loads + i;  // group of 8 rows: A's, then B's
-            const bool a = g < S::BM / 8;
-            const uint32_t r0 = (a ? g : g - S::BM / 8) * 8;
-            const uint32_t off = (r0 + row) * (a ? A.pitch : B.pitch) + at + turn;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? A.r : B.r, (__attribute__((address_space(3))) void*)(to + g * 64), 16,
-                                                     int(in ? off : 0x80000000u), 0, 0, 0);
+            // group of 1 KiB: A's, then B's
+            const uint32_t g = wave * S::loads + i;
+            if (g < S::BM / 8) load_group<DT, MA, S::BM>(A, ra, g, step, (DT_LDS void*)(to + g * 64));
+            else load_group<DT, MB, S::BN>(B, rb, g - S::BM / 8, step, (DT_LDS void*)(to + g * 64));
         }
     };
-    stage(first, 0);
+    stage(lo, 0);
     const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
     int buf = 0;
-    for (uint32_t at = first; at < bytes; at += kChunks * 16, buf ^= 1) {
+    for (uint32_t step = lo; step < hi; step++, buf ^= 1) {
         __syncthreads();  // this step's loads have landed, and the other half is no longer read
-        if (at + kChunks * 16 < bytes) stage(at + kChunks * 16, buf ^ 1);
+        if (step + 1 < hi) stage(step + 1, buf ^ 1);
         const u32x4* sa = lds + buf * (S::BM + S::BN) * kChunks;
         const u32x4* sb = sa + S::BM * kChunks;
 #pragma unroll
         for (int kk = 0; kk < kChunks / 4; kk++) {
             u32x4 fa[S::MI], fb[S::NI];
-            const uint32_t c = kk * 4 + (lane >> 4);
 #pragma unroll
-            for (int i = 0; i < S::MI; i++) {
-                const uint32_t r = wm + i * 16 + (lane & 15);
-                fa[i] = sa[r * kChunks + (c ^ (r & 7))];
-            }
+            for (int i = 0; i < S::MI; i++) fa[i] = fragment<DT, MA, S::BM>(sa, wm + i * 16, kk);
 #pragma unroll
-            for (int j = 0; j < S::NI; j++) {
-                const uint32_t r = wn + j * 16 + (lane & 15);
-                fb[j] = sb[r * kChunks + (c ^ (r & 7))];
-            }
+            for (int j = 0; j < S::NI; j++) fb[j] = fragment<DT, MB, S::BN>(sb, wn + j * 16, kk);
 #pragma unroll
             for (int i = 0; i < S::MI; i++)
 #pragma unroll
@@ -138,62 +216,96 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
     n = in / high;
 }
 
+// exp(x): the argument's product with log2 e is off by half a step of |x| log2 e,
+// which adds |x| half steps to the result's error.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
 
-// ---------------------------------------------------------------- forward --
-// Vocabulary rows [first, first + count) of rank `rank`, and the operands as
-// the matrix routine reads them: rows of `pitch` bytes (a multiple of 16) with
-// `bytes` valid ones.
-struct LossRows {
-    const char* weight;
-    const char* hidden;
-    uint64_t pitch;
-    uint32_t bytes;
-    uint32_t first, count;
-    int rank;
+// A piece of the vocabulary: the parts of it that single ranks hold.
+struct Segments {
+    const char* weight[kMaxRanksHost];   // the part's first row, rows of `pitch` bytes
+    char* dweight[kMaxRanksHost];        // its gradient, rows of the caller's width
+    uint32_t count[kMaxRanksHost];       // rows
+    uint32_t vocab[kMaxRanksHost];       // first row in the whole vocabulary
+    uint32_t tile[kMaxRanksHost + 1];    // first tile of vocabulary rows
+    uint32_t col[kMaxRanksHost + 1];     // first column in d; each part ends on a whole step
+    int n;
 };
+__device__ __forceinline__ int segment_of(const uint32_t* first, int n, uint32_t at) {
+    int s = 0;
+    while (s + 1 < n && at >= first[s + 1]) s++;
+    return s;
+}
+
+struct LossProblem {
+    const char* hidden;      // [tokens] rows of `pitch` bytes
+    const int64_t* targets;
+    const float* lse;
+    const float* dloss;
+    uint32_t pitch;          // of hidden and weight rows, a multiple of 16; all bytes valid
+    uint32_t tokens, cols, vocab;
+    int64_t ignore_index;
+};
+__device__ __forceinline__ bool counted(const LossProblem& a, int64_t t) {
+    return t != a.ignore_index && t >= 0 && t < int64_t(a.vocab);
+}
+
+// ---------------------------------------------------------------- forward --
 struct StatsArgs {
-    uint32_t tiles, token_tiles;  // of this launch
-    uint32_t first_tile, all;     // the launch's first tile among all, and how many all are
-    float2* part;                 // [all][tokens]: maximum, sum of exponentials
+    uint32_t token_tiles;
+    uint32_t entry, entries;      // the launch's first tile among all, and how many all are
+    float2* part;                 // [tokens][entries]: maximum, sum of exponentials
     float* target;                // [tokens]: the target's logit
 };
 
 // (top, s) joined with another maximum and sum.
-__device__ __forceinline__ void join(float& top, float& s, float2 v) {
-    const float t = fmaxf(top, v.x), base = t > -INFINITY ? t : 0.f;
-    s = s * exp_of(top - base) + v.y * exp_of(v.x - base);
+__device__ __forceinline__ void join(float& top, float& s, float top2, float s2) {
+    const float t = fmaxf(top, top2), base = t > -INFINITY ? t : 0.f;
+    s = s * exp_of(top - base) + s2 * exp_of(top2 - base);
     top = t;
 }
 
 template <int DT, typename S>
-__global__ __launch_bounds__(S::threads) void k_loss_stats(LossArgs a, LossRows p, StatsArgs q) {
+__global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segments g, StatsArgs q) {
     __shared__ u32x4 lds[S::lds];
     __shared__ float2 part[S::GM][S::BN];
     uint32_t mt, nt;
-    tile_of(blockIdx.x, q.tiles, q.token_tiles, mt, nt);
-    const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
-    const int r = p.rank;
+    tile_of(blockIdx.x, g.tile[g.n], q.token_tiles, mt, nt);
+    const int sg = segment_of(g.tile, g.n, mt);
+    const uint32_t m0 = (mt - g.tile[sg]) * S::BM, n0 = nt * S::BN, left = g.count[sg] - m0;
     f32x4 acc[S::MI][S::NI];
-    matrix_tile<DT, S>(operand(p.weight + uint64_t(m0) * p.pitch, p.count - m0, S::BM, p.pitch),
-                       operand(p.hidden + uint64_t(n0) * p.pitch, a.tokens - n0, S::BN, p.pitch), 0, p.bytes, lds, acc);
+    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
+    const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, lds, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t wm = wave % S::GM, wn = wave / S::GM;
-    const uint32_t mlane = m0 + wm * S::WM + (lane >> 4) * 4;
+    const uint32_t mlane = wm * S::WM + (lane >> 4) * 4;  // acc[i][j][e] is row mlane + 16 i + e of the tile
+    if (left < S::BM) {  // rows behind the shard's last one
+#pragma unroll
+        for (int i = 0; i < S::MI; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (mlane + i * 16 + e >= left) {
+#pragma unroll
+                    for (int j = 0; j < S::NI; j++) acc[i][j][e] = -INFINITY;
+                }
+    }
 #pragma unroll
     for (int j = 0; j < S::NI; j++) {
         const uint32_t nl = wn * S::WN + j * 16 + (lane & 15), n = n0 + nl;
-        const int64_t t = n < a.tokens ? a.targets[r][n] - int64_t(a.vocab.start[r]) - int64_t(p.first) : -1;
+        const int64_t t = n < a.tokens ? a.targets[n] - int64_t(g.vocab[sg]) - int64_t(m0) : -1;
+        const bool here = t >= 0 && t < int64_t(left < S::BM ? left : S::BM);
+        if (__any(here)) {  // few tiles hold a target of their tokens
+#pragma unroll
+            for (int i = 0; i < S::MI; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (here && uint32_t(t) == mlane + i * 16 + e) q.target[n] = acc[i][j][e];
+        }
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const uint32_t m = mlane + i * 16 + e;
-                if (m >= p.count) acc[i][j][e] = -INFINITY;
-                else if (t == int64_t(m)) q.target[n] = acc[i][j][e];
-                top = fmaxf(top, acc[i][j][e]);
-            }
+            for (int e = 0; e < 4; e++) top = fmaxf(top, acc[i][j][e]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         float s = 0.f;
@@ -210,118 +322,119 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossArgs a, LossRows 
     for (uint32_t nl = threadIdx.x; nl < S::BN && n0 + nl < a.tokens; nl += S::threads) {
         float top = part[0][nl].x, s = part[0][nl].y;
 #pragma unroll
-        for (int w = 1; w < S::GM; w++) join(top, s, part[w][nl]);
-        q.part[uint64_t(q.first_tile + mt) * a.tokens + n0 + nl] = make_float2(top, s);
+        for (int w = 1; w < S::GM; w++) join(top, s, part[w][nl].x, part[w][nl].y);
+        q.part[uint64_t(n0 + nl) * q.entries + q.entry + mt] = make_float2(top, s);
     }
 }
 
-__device__ __forceinline__ bool counted(const LossArgs& a, int64_t t) {
-    return t != a.ignore_index && t >= 0 && t < int64_t(a.vocab.start[a.nranks]);
-}
-
-__global__ __launch_bounds__(kThreads) void k_loss_join(LossArgs a, StatsArgs p) {
-    const uint32_t n = blockIdx.x * kThreads + threadIdx.x;
+// One wave per token: the tiles' maxima and sums joined, every rank's loss and lse written.
+struct LossOut {
+    float* loss[kMaxRanksHost];
+    float* lse[kMaxRanksHost];
+    int nranks;
+};
+__global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs q, LossOut o) {
+    const uint32_t n = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
     if (n >= a.tokens) return;
     float top = -INFINITY, s = 0.f;
-    for (uint32_t i = 0; i < p.all; i++) join(top, s, p.part[uint64_t(i) * a.tokens + n]);
+    for (uint32_t i = lane; i < q.entries; i += 64) {
+        const float2 v = q.part[uint64_t(n) * q.entries + i];
+        join(top, s, v.x, v.y);
+    }
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) join(top, s, __shfl_xor(top, m), __shfl_xor(s, m));
     const float lse = top + logf(s);
-    for (int r = 0; r < a.nranks; r++) {
-        a.lse[r][n] = lse;
-        a.loss[r][n] = counted(a, a.targets[r][n]) ? lse - p.target[n] : 0.f;
+    const float loss = counted(a, a.targets[n]) ? lse - q.target[n] : 0.f;
+    if (lane < uint32_t(o.nranks)) {
+        o.lse[lane][n] = lse;
+        o.loss[lane][n] = loss;
     }
 }
 
 // --------------------------------------------------------------- backward --
-// The piece's buffers in the workspace.
-struct PieceOfVocab {
-    char* d;          // [tokens][ldv]
-    char* dt;         // [count][ldt]
-    char* wt;         // [cols][ldv]
-    char* xt;         // [cols][ldt]
+struct DPiece {
+    char* d;          // [tokens] rows of ldv elements: the piece's d, each part's padding zero
     float* acc;       // [splits][tokens][ldx]
-    uint64_t ldv, ldt, ldx;
+    uint64_t ldv, ldx;
     uint32_t mt, nt;  // tiles of the launch
     uint32_t splits;  // workgroups that share one tile's sum over the piece
     int add;          // acc holds the earlier pieces' sum
 };
 
-// d of the piece, in both layouts; the rows' padding is zero.
 template <int DT, typename S>
-__global__ __launch_bounds__(S::threads) void k_loss_d(LossArgs a, LossRows w, PieceOfVocab p) {
+__global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
-    tile_of(blockIdx.x, p.mt, p.nt, mt, nt);
-    const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
-    const int r = w.rank;
+    tile_of(blockIdx.x, g.tile[g.n], p.nt, mt, nt);
+    const int sg = segment_of(g.tile, g.n, mt);
+    const uint32_t m0 = (mt - g.tile[sg]) * S::BM, n0 = nt * S::BN;
+    const uint32_t count = g.count[sg], padded = g.col[sg + 1] - g.col[sg];
+    const uint32_t left = count > m0 ? count - m0 : 0;  // the last tile may lie in the padding alone
     f32x4 acc[S::MI][S::NI];
-    // the last tiles may lie in the padding alone
-    const uint32_t rows_a = w.count > m0 ? w.count - m0 : 0, rows_b = a.tokens > n0 ? a.tokens - n0 : 0;
-    matrix_tile<DT, S>(operand(w.weight + uint64_t(m0) * w.pitch, rows_a, S::BM, w.pitch),
-                       operand(w.hidden + uint64_t(n0) * w.pitch, rows_b, S::BN, w.pitch), 0, w.bytes, lds, acc);
+    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
+    const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, lds, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T* d = reinterpret_cast<T*>(p.d);
-    T* dt = reinterpret_cast<T*>(p.dt);
+    const uint32_t mlane = (wave % S::GM) * S::WM + (lane >> 4) * 4;
+    T* d = reinterpret_cast<T*>(p.d) + g.col[sg] + m0;
 #pragma unroll
     for (int j = 0; j < S::NI; j++) {
         const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
-        const bool in = n < a.tokens;
-        const int64_t t = in ? a.targets[r][n] : -1;
-        const float lse = in ? a.lse[r][n] : 0.f;
-        const bool use = in && counted(a, t);
-        const float g = use ? a.dloss[r][n] : 0.f;
-        const int64_t at = t - int64_t(a.vocab.start[r]) - int64_t(w.first);  // the target's row in the piece
+        if (n >= a.tokens) continue;
+        const int64_t t = a.targets[n];
+        const float lse = a.lse[n];
+        const bool use = counted(a, t);
+        const float f = use ? a.dloss[n] : 0.f;
+        const int64_t at = t - int64_t(g.vocab[sg]) - int64_t(m0);
+        const uint32_t hit = use && at >= 0 && at < S::BM ? uint32_t(at) : UINT32_MAX;  // the target's row in the tile
 #pragma unroll
         for (int i = 0; i < S::MI; i++) {
-            const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
+            const uint32_t m = mlane + i * 16;
             T o[4];
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                float v = 0.f;
-                if (use && m + e < w.count) v = (exp_of(acc[i][j][e] - lse) - (at == int64_t(m + e) ? 1.f : 0.f)) * g;
-                o[e] = Elem<DT>::put(v);
+                const float v = (exp_of(acc[i][j][e] - lse) - (hit == m + e ? 1.f : 0.f)) * f;
+                o[e] = Elem<DT>::put(use && m + e < left ? v : 0.f);
             }
-            // ldv is a multiple of 4: the four are all inside a row or all behind it
-            if (in && m < p.ldv) __builtin_memcpy(__builtin_assume_aligned(d + uint64_t(n) * p.ldv + m, 4 * sizeof(T)), o, sizeof o);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (m + e < w.count && n < p.ldt) dt[uint64_t(m + e) * p.ldt + n] = o[e];
+            // a part's width is a multiple of 4: the four are all inside it or all behind it
+            if (m0 + m < padded)
+                __builtin_memcpy(__builtin_assume_aligned(d + uint64_t(n) * p.ldv + m, 4 * sizeof(T)), o, sizeof o);
         }
     }
 }
 
-// dst[c][r] = src[r][c], zeros for r in [rows, ld).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void k_transpose(const T* src, T* dst, uint32_t rows, uint32_t cols, uint64_t ld) {
-    __shared__ T tile[64][65];
-    const uint32_t r0 = blockIdx.x * 64, c0 = blockIdx.y * 64;
-    const uint32_t tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-    for (uint32_t i = ty; i < 64; i += 4) {
-        const uint32_t r = r0 + i, c = c0 + tx;
-        tile[i][tx] = r < rows && c < cols ? src[uint64_t(r) * cols + c] : T(0);
+// The weight rows of a piece as the summed index: step by step through the
+// parts, each of whole steps, zeros behind a part's last row.
+template <int KR>
+struct WeightOperand {
+    const Segments& g;
+    uint64_t pitch, skip;
+    mutable int sg;
+    __device__ __forceinline__ StepSource at(uint32_t step) const {
+        const uint32_t k = step * KR;
+        while (sg + 1 < g.n && k >= g.col[sg + 1]) sg++;
+        const uint32_t row = k - g.col[sg], left = row < g.count[sg] ? g.count[sg] - row : 0;
+        return StepSource{g.weight[sg] + uint64_t(row) * pitch + skip,
+                          left > 0 ? uint64_t(left < KR ? left : KR) * pitch - skip : 0};
     }
-    __syncthreads();
-    for (uint32_t i = ty; i < 64; i += 4) {
-        const uint32_t c = c0 + i, r = r0 + tx;
-        if (c < cols && r < ld) dst[uint64_t(c) * ld + r] = tile[tx][i];
-    }
-}
+};
 
 // acc[split][t][h] (+)= sum over the split's part of the piece of d[t][v] weight[v][h].
 template <int DT, typename S>
-__global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossArgs a, PieceOfVocab p) {
+__global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
+    constexpr int KR = kStepBytes / int(sizeof(T));
     __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
     tile_of(blockIdx.x, p.mt, p.nt, mt, nt);
     const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
-    f32x4 acc[S::MI][S::NI];
-    const uint64_t pitch = p.ldv * sizeof(T);
-    const uint32_t steps = uint32_t(pitch / (kChunks * 16));
+    const uint32_t pitch = uint32_t(p.ldv * sizeof(T)), steps = pitch / kStepBytes;
     const uint32_t lo = uint32_t(uint64_t(steps) * blockIdx.y / p.splits), hi = uint32_t(uint64_t(steps) * (blockIdx.y + 1) / p.splits);
-    matrix_tile<DT, S>(operand(p.wt + uint64_t(m0) * pitch, a.cols - m0, S::BM, pitch),
-                       operand(p.d + uint64_t(n0) * pitch, a.tokens - n0, S::BN, pitch), lo * kChunks * 16, hi * kChunks * 16,
-                       lds, acc);
+    f32x4 acc[S::MI][S::NI];
+    const WeightOperand<KR> A{g, a.pitch, m0 * sizeof(T), 0};
+    const RowOperand B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch};
+    matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, lds, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* to = p.acc + uint64_t(blockIdx.y) * a.tokens * p.ldx;
 #pragma unroll
@@ -338,18 +451,21 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossArgs a, PieceOf
 
 // dweight[v][h] = sum_t d[t][v] hidden[t][h].
 template <int DT, typename S>
-__global__ __launch_bounds__(S::threads) void k_loss_dweight(LossArgs a, LossRows w, PieceOfVocab p) {
+__global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
+    constexpr int KR = kStepBytes / int(sizeof(T));
     __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
-    tile_of(blockIdx.x, p.mt, p.nt, mt, nt);
-    const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
+    tile_of(blockIdx.x, p.mt, g.tile[g.n], mt, nt);
+    const int sg = segment_of(g.tile, g.n, nt);
+    const uint32_t m0 = mt * S::BM, n0 = (nt - g.tile[sg]) * S::BN;
     f32x4 acc[S::MI][S::NI];
-    const uint64_t pitch = p.ldt * sizeof(T);
-    matrix_tile<DT, S>(operand(p.xt + uint64_t(m0) * pitch, a.cols - m0, S::BM, pitch),
-                       operand(p.dt + uint64_t(n0) * pitch, w.count - n0, S::BN, pitch), 0, uint32_t(pitch), lds, acc);
+    const uint64_t es = sizeof(T), skip = uint64_t(g.col[sg] + n0) * es;
+    const ColOperand<KR> A{a.hidden + m0 * es, a.tokens, a.pitch, m0 * es};
+    const ColOperand<KR> B{p.d + skip, a.tokens, p.ldv * es, skip};
+    matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR, lds, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    T* out = static_cast<T*>(a.dweight[w.rank]) + uint64_t(w.first) * a.cols;
+    T* out = reinterpret_cast<T*>(g.dweight[sg]);
     const bool quads = a.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
 #pragma unroll
     for (int j = 0; j < S::NI; j++)
@@ -357,7 +473,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossArgs a, LossRow
         for (int i = 0; i < S::MI; i++) {
             const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
             const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
-            if (n >= w.count || m >= a.cols) continue;
+            if (n >= g.count[sg] || m >= a.cols) continue;
             T o[4];
 #pragma unroll
             for (int e = 0; e < 4; e++) o[e] = Elem<DT>::put(acc[i][j][e]);
@@ -373,15 +489,20 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossArgs a, LossRow
 }
 
 // Every rank's dhidden from the sums of the splits, in order, rounded once.
+struct DHiddenOut {
+    void* p[kMaxRanksHost];
+    int nranks;
+};
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_loss_out(LossArgs a, const float* acc, uint64_t ldx, uint32_t splits) {
+__global__ __launch_bounds__(kThreads) void k_loss_out(DHiddenOut o, const float* acc, uint32_t tokens, uint32_t cols,
+                                                      uint64_t ldx, uint32_t splits) {
     typedef typename Elem<DT>::type T;
     const uint32_t n = blockIdx.x;
-    for (uint32_t c = threadIdx.x; c < a.cols; c += kThreads) {
+    for (uint32_t c = threadIdx.x; c < cols; c += kThreads) {
         float s = 0.f;
-        for (uint32_t k = 0; k < splits; k++) s += acc[(uint64_t(k) * a.tokens + n) * ldx + c];
+        for (uint32_t k = 0; k < splits; k++) s += acc[(uint64_t(k) * tokens + n) * ldx + c];
         const T v = Elem<DT>::put(s);
-        for (int r = 0; r < a.nranks; r++) static_cast<T*>(a.dhidden[r])[uint64_t(n) * a.cols + c] = v;
+        for (int r = 0; r < o.nranks; r++) static_cast<T*>(o.p[r])[uint64_t(n) * cols + c] = v;
     }
 }
 
@@ -392,28 +513,38 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(const T* src, T* dst, uin
     for (uint32_t c = threadIdx.x; c < ld; c += kThreads) dst[row * ld + c] = c < cols ? src[row * cols + c] : T(0);
 }
 
+// -------------------------------------------------------------------- host --
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 uint32_t ceil_div(uint64_t n, uint64_t by) { return uint32_t((n + by - 1) / by); }
 uint64_t esize(int dtype) { return dtype == kBF16 ? 2 : 4; }
-uint64_t pad_of(int dtype) { return kChunks * 16 / esize(dtype); }  // elements per step of the summed index
+uint64_t step_elems(int dtype) { return kStepBytes / esize(dtype); }
 
 typedef Shape<256, 256, 2, 4> Wide;
 typedef Shape<128, 128, 2, 2> Square;
 typedef Shape<128, 64, 4, 1> Narrow;
-constexpr uint32_t kStatsRows = 128;  // vocabulary rows that one entry of the partial statistics covers, at least
+typedef Shape<64, 64, 2, 2> Small;
+enum Tile { kWide, kSquare, kNarrow, kSmall };
+constexpr uint32_t kTileM[] = {256, 128, 128, 64}, kTileN[] = {256, 128, 64, 64};
 
-// The tile for an m x n product: the largest that still gives every one of
-// the 256 CUs a workgroup.
-enum Tile { kWide, kSquare, kNarrow };
-Tile pick_tile(uint64_t m, uint64_t n, uint32_t splits = 1) {
-    if (n <= 64) return kNarrow;
+// The tile for an m x n product of `splits` sums: the largest that still
+// fills the 256 CUs.
+Tile pick_tile(int dtype, uint64_t m, uint64_t n, uint32_t splits = 1) {
+    const uint64_t square = uint64_t(ceil_div(m, 128)) * ceil_div(n, 128) * splits;
+    if (dtype == kF32) return square >= 1024 ? kSquare : kSmall;
+    if (n <= 64) return m >= 128 * 128 ? kNarrow : kSmall;
     if (uint64_t(ceil_div(m, 256)) * ceil_div(n, 256) * splits >= 224) return kWide;
-    return kSquare;
+    return square >= 192 ? kSquare : kSmall;
 }
-
-// Rows that start and end on 16-byte boundaries are read where they are;
-// others are copied to padded rows first, a piece at a time.
-constexpr uint32_t kPiece = 16384;
+// launch(Shape) with the shape of `t`.
+template <int DT, typename F>
+void with_tile(Tile t, F&& launch) {
+    if constexpr (DT == kBF16) {
+        if (t == kWide) return launch(Wide());
+        if (t == kNarrow) return launch(Narrow());
+    }
+    if (t == kSquare) launch(Square());
+    else launch(Small());
+}
 
 // The workspace's parts, each on a 256-byte boundary.
 struct Parts {
@@ -424,6 +555,9 @@ struct Parts {
         return here;
     }
 };
+
+// Rows that start and end on 16-byte boundaries are read where they are;
+// others are copied to padded rows in the workspace, a piece at a time.
 struct PadParts {
     uint64_t pitch, hidden, weight;
 };
@@ -434,204 +568,222 @@ PadParts pad_parts(Parts& w, uint64_t tokens, uint64_t cols, uint64_t piece, int
     b.weight = w.take(piece * b.pitch);
     return b;
 }
-uint32_t splits_of(uint64_t tokens, uint64_t cols) {
-    // few tiles of dhidden: the sum over the piece is cut among workgroups
-    const uint64_t tiles = uint64_t(ceil_div(cols, 128)) * ceil_div(tokens, tokens <= 64 ? 64 : 128);
-    if (tiles == 0 || tiles >= 256) return 1;
-    const uint64_t want = ceil_div(512, tiles);
-    return uint32_t(want < 16 ? want : 16);
+bool rows_aligned(const LossArgs& a, int dtype) {
+    if (a.cols * esize(dtype) % 16 != 0 || reinterpret_cast<uintptr_t>(a.hidden) % 16 != 0) return false;
+    for (int r = 0; r < a.nranks; r++)
+        if (reinterpret_cast<uintptr_t>(a.weight[r]) % 16 != 0) return false;
+    return true;
+}
+
+LossProblem problem_of(const LossArgs& a, uint64_t pitch) {
+    LossProblem p = {};
+    p.hidden = static_cast<const char*>(a.hidden);
+    p.targets = a.targets;
+    p.lse = a.lse_in;
+    p.dloss = a.dloss;
+    p.pitch = uint32_t(pitch);
+    p.tokens = a.tokens;
+    p.cols = a.cols;
+    p.vocab = a.vocab.start[a.nranks];
+    p.ignore_index = a.ignore_index;
+    return p;
+}
+
+// Vocabulary rows [first, first + count) as segments; pad != NULL: their rows are in
+// the workspace at *pad, one after the other.
+Segments segments_of(const LossArgs& a, int dtype, uint32_t first, uint32_t count, const char* pad, uint64_t pitch) {
+    Segments g = {};
+    const uint64_t es = esize(dtype), row = uint64_t(a.cols) * es;
+    for (int r = 0; r < a.nranks; r++) {
+        const uint32_t lo = first > a.vocab.start[r] ? first : a.vocab.start[r];
+        const uint32_t end = first + count, hi = end < a.vocab.start[r + 1] ? end : a.vocab.start[r + 1];
+        if (lo >= hi) continue;
+        const uint64_t local = lo - a.vocab.start[r];
+        g.weight[g.n] = pad != nullptr ? pad + uint64_t(lo - first) * pitch : static_cast<const char*>(a.weight[r]) + local * row;
+        g.dweight[g.n] = a.dweight[r] != nullptr ? static_cast<char*>(a.dweight[r]) + local * row : nullptr;
+        g.count[g.n] = hi - lo;
+        g.vocab[g.n] = lo;
+        g.col[g.n + 1] = g.col[g.n] + uint32_t(up(hi - lo, step_elems(dtype)));
+        g.n++;
+    }
+    return g;
+}
+void set_tiles(Segments& g, uint32_t rows_per_tile, bool padded) {
+    for (int s = 0; s < g.n; s++)
+        g.tile[s + 1] = g.tile[s] + ceil_div(padded ? g.col[s + 1] - g.col[s] : g.count[s], rows_per_tile);
+}
+
+template <typename T>
+void pad_rows(const void* src, char* dst, uint32_t rows, uint32_t cols, uint64_t pitch, hipStream_t s) {
+    if (rows > 0)
+        hipLaunchKernelGGL(k_pad_rows<T>, dim3(rows), dim3(kThreads), 0, s, static_cast<const T*>(src), reinterpret_cast<T*>(dst),
+                           cols, pitch / sizeof(T));
+}
+template <typename T>
+void pad_weight(const LossArgs& a, uint32_t first, uint32_t count, char* to, uint64_t pitch, hipStream_t s) {
+    const Segments g = segments_of(a, sizeof(T) == 2 ? kBF16 : kF32, first, count, nullptr, pitch);
+    for (int i = 0; i < g.n; i++) pad_rows<T>(g.weight[i], to + uint64_t(g.vocab[i] - first) * pitch, g.count[i], a.cols, pitch, s);
+}
+
+uint64_t stats_entries(const RowTable& vocab, int nranks) {
+    // at most one entry per 64 rows of a shard, and one per shard and piece end
+    uint64_t n = 0;
+    for (int r = 0; r < nranks; r++) n += ceil_div(vocab.start[r + 1] - vocab.start[r], 64);
+    return n + 2 * ceil_div(vocab.start[nranks], kLossPiece);
+}
+
+template <int DT>
+hipError_t forward(const LossArgs& a, hipStream_t s) {
+    typedef typename Elem<DT>::type T;
+    const uint32_t V = a.vocab.start[a.nranks];
+    const bool direct = rows_aligned(a, DT);
+    const uint32_t piece = direct ? V : loss_piece(a.vocab, a.nranks, 0);
+    Parts parts;
+    StatsArgs q = {};
+    q.part = reinterpret_cast<float2*>(a.workspace + parts.take(stats_entries(a.vocab, a.nranks) * a.tokens * sizeof(float2)));
+    q.target = reinterpret_cast<float*>(a.workspace + parts.take(uint64_t(a.tokens) * 4));
+    LossProblem p = problem_of(a, uint64_t(a.cols) * sizeof(T));
+    char* wpad = nullptr;
+    if (!direct) {
+        const PadParts pad = pad_parts(parts, a.tokens, a.cols, piece, DT);
+        p.pitch = uint32_t(pad.pitch);
+        pad_rows<T>(a.hidden, a.workspace + pad.hidden, a.tokens, a.cols, pad.pitch, s);
+        p.hidden = a.workspace + pad.hidden;
+        wpad = a.workspace + pad.weight;
+    }
+    const Tile t = pick_tile(DT, piece, a.tokens);
+    for (int pass = 0; pass < 2; pass++) {  // count the tiles, then launch
+        q.entry = 0;
+        for (uint32_t first = 0; first < V; first += piece) {
+            const uint32_t count = V - first < piece ? V - first : piece;
+            Segments g = segments_of(a, DT, first, count, wpad, p.pitch);
+            set_tiles(g, kTileM[t], false);
+            if (pass == 1) {
+                if (!direct) pad_weight<T>(a, first, count, wpad, p.pitch, s);
+                with_tile<DT>(t, [&](auto shape) {
+                    typedef decltype(shape) S;
+                    q.token_tiles = ceil_div(a.tokens, S::BN);
+                    hipLaunchKernelGGL((k_loss_stats<DT, S>), dim3(g.tile[g.n] * q.token_tiles), dim3(S::threads), 0, s, p, g, q);
+                });
+            }
+            q.entry += g.tile[g.n];
+        }
+        q.entries = q.entry;
+    }
+    LossOut o = {};
+    for (int r = 0; r < a.nranks; r++) {
+        o.loss[r] = a.loss[r];
+        o.lse[r] = a.lse[r];
+    }
+    o.nranks = a.nranks;
+    hipLaunchKernelGGL(k_loss_join, dim3(ceil_div(a.tokens, kThreads / 64)), dim3(kThreads), 0, s, p, q, o);
+    return hipGetLastError();
+}
+
+// Few tiles of dhidden: the sum over the piece is cut among workgroups, each
+// with at least 4 steps of it.
+uint32_t splits_of(uint64_t tokens, uint64_t cols, uint64_t ldv, int dtype) {
+    const uint64_t tiles = uint64_t(ceil_div(cols, 64)) * ceil_div(tokens, 64);
+    if (tiles == 0 || tiles >= 512) return 1;
+    uint64_t want = ceil_div(1024, tiles);
+    const uint64_t most = ldv / step_elems(dtype) / 4;
+    if (want > most) want = most;
+    return want < 1 ? 1 : want > 32 ? 32 : uint32_t(want);
 }
 struct BackwardParts {
-    uint64_t ldv, ldt, ldx, d, dt, wt, xt, acc;
+    uint64_t ldv, ldx, d, acc;
     uint32_t splits;
     PadParts pad;
     uint64_t bytes;
 };
-BackwardParts backward_parts(uint64_t tokens, uint64_t cols, uint64_t piece, int dtype) {
+BackwardParts backward_parts(int nranks, uint64_t tokens, uint64_t cols, uint64_t piece, int dtype) {
     BackwardParts b;
-    const uint64_t es = esize(dtype);
-    b.ldv = up(piece, pad_of(dtype));
-    b.ldt = up(tokens, pad_of(dtype));
+    // a piece may hold parts of all ranks, each padded to a whole step
+    b.ldv = up(piece, step_elems(dtype)) + (nranks - 1) * step_elems(dtype);
     b.ldx = up(cols, 4);
-    b.splits = splits_of(tokens, cols);
+    b.splits = splits_of(tokens, cols, b.ldv, dtype);
     Parts w;
-    b.d = w.take(tokens * b.ldv * es);
-    b.dt = w.take(piece * b.ldt * es);
-    b.wt = w.take(cols * b.ldv * es);
-    b.xt = w.take(cols * b.ldt * es);
+    b.d = w.take(tokens * b.ldv * esize(dtype));
     b.acc = w.take(b.splits * tokens * b.ldx * 4);
     b.pad = pad_parts(w, tokens, cols, piece, dtype);
     b.bytes = w.at;
     return b;
 }
 
-bool rows_aligned(const void* p, uint64_t cols, int dtype) {
-    return cols * esize(dtype) % 16 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-}
-
-// The operands of vocabulary rows [first, first + count) of rank r, copied to
-// padded rows in the workspace where they are not aligned.  `fresh`: the
-// rank's first piece.
-template <int DT>
-LossRows loss_rows(const LossArgs& a, const PadParts& pad, int r, uint32_t first, uint32_t count, bool fresh, hipStream_t s) {
-    typedef typename Elem<DT>::type T;
-    LossRows w = {};
-    const T* weight = static_cast<const T*>(a.weight[r]) + uint64_t(first) * a.cols;
-    w.rank = r;
-    w.first = first;
-    w.count = count;
-    if (rows_aligned(a.weight[r], a.cols, DT) && rows_aligned(a.hidden[r], a.cols, DT)) {
-        w.pitch = uint64_t(a.cols) * sizeof(T);
-        w.weight = reinterpret_cast<const char*>(weight);
-        w.hidden = static_cast<const char*>(a.hidden[r]);
-    } else {
-        w.pitch = pad.pitch;
-        char* to = a.workspace + pad.weight;
-        char* hidden = a.workspace + pad.hidden;
-        const uint64_t ld = pad.pitch / sizeof(T);
-        if (fresh)
-            hipLaunchKernelGGL(k_pad_rows<T>, dim3(a.tokens), dim3(kThreads), 0, s, static_cast<const T*>(a.hidden[r]),
-                               reinterpret_cast<T*>(hidden), a.cols, ld);
-        hipLaunchKernelGGL(k_pad_rows<T>, dim3(count), dim3(kThreads), 0, s, weight, reinterpret_cast<T*>(to), a.cols, ld);
-        w.weight = to;
-        w.hidden = hidden;
-    }
-    w.bytes = uint32_t(w.pitch);
-    return w;
-}
-
-template <int DT, typename S>
-void stats(const LossArgs& a, const LossRows& w, StatsArgs q, hipStream_t s) {
-    q.tiles = ceil_div(w.count, S::BM);
-    q.token_tiles = ceil_div(a.tokens, S::BN);
-    hipLaunchKernelGGL((k_loss_stats<DT, S>), dim3(q.tiles * q.token_tiles), dim3(S::threads), 0, s, a, w, q);
-}
-
-template <int DT>
-hipError_t forward(const LossArgs& a, hipStream_t s) {
-    Parts parts;
-    uint64_t entries = 0;
-    for (int r = 0; r < a.nranks; r++)
-        for (uint32_t V = a.vocab.start[r + 1] - a.vocab.start[r], f = 0; f < V; f += kPiece)
-            entries += ceil_div(V - f < kPiece ? V - f : kPiece, kStatsRows);
-    StatsArgs q = {};
-    q.part = reinterpret_cast<float2*>(a.workspace + parts.take(entries * a.tokens * sizeof(float2)));
-    q.target = reinterpret_cast<float*>(a.workspace + parts.take(uint64_t(a.tokens) * 4));
-    const PadParts pad = pad_parts(parts, a.tokens, a.cols, loss_piece(a.vocab, a.nranks, a.tokens, a.cols, DT, 0), DT);
-    for (int r = 0; r < a.nranks; r++) {
-        const uint32_t V = a.vocab.start[r + 1] - a.vocab.start[r];
-        for (uint32_t f = 0; f < V; f += kPiece) {
-            const LossRows w = loss_rows<DT>(a, pad, r, f, V - f < kPiece ? V - f : kPiece, f == 0, s);
-            const Tile t = pick_tile(w.count, a.tokens);
-            if (t == kWide) stats<DT, Wide>(a, w, q, s);
-            else if (t == kSquare) stats<DT, Square>(a, w, q, s);
-            else stats<DT, Narrow>(a, w, q, s);
-            q.first_tile += ceil_div(w.count, t == kWide ? 256 : 128);
-        }
-    }
-    q.all = q.first_tile;
-    hipLaunchKernelGGL(k_loss_join, dim3((a.tokens + kThreads - 1) / kThreads), dim3(kThreads), 0, s, a, q);
-    return hipGetLastError();
-}
-
-template <int DT, typename S>
-void piece_d(const LossArgs& a, const LossRows& w, PieceOfVocab p, hipStream_t s) {
-    p.mt = ceil_div(p.ldv, S::BM);
-    p.nt = ceil_div(p.ldt, S::BN);
-    hipLaunchKernelGGL((k_loss_d<DT, S>), dim3(p.mt * p.nt), dim3(S::threads), 0, s, a, w, p);
-}
-template <int DT, typename S>
-void piece_dhidden(const LossArgs& a, PieceOfVocab p, hipStream_t s) {
-    p.mt = ceil_div(a.cols, S::BM);
-    p.nt = ceil_div(a.tokens, S::BN);
-    hipLaunchKernelGGL((k_loss_dhidden<DT, S>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, a, p);
-}
-template <int DT, typename S>
-void piece_dweight(const LossArgs& a, const LossRows& w, PieceOfVocab p, hipStream_t s) {
-    p.mt = ceil_div(a.cols, S::BM);
-    p.nt = ceil_div(w.count, S::BN);
-    hipLaunchKernelGGL((k_loss_dweight<DT, S>), dim3(p.mt * p.nt), dim3(S::threads), 0, s, a, w, p);
-}
-
 template <int DT>
 hipError_t backward(const LossArgs& a, hipStream_t s) {
     typedef typename Elem<DT>::type T;
-    const BackwardParts b = backward_parts(a.tokens, a.cols, a.piece, DT);
-    PieceOfVocab p = {};
+    const uint32_t V = a.vocab.start[a.nranks];
+    const BackwardParts b = backward_parts(a.nranks, a.tokens, a.cols, a.piece, DT);
+    LossProblem q = problem_of(a, uint64_t(a.cols) * sizeof(T));
+    char* wpad = nullptr;
+    if (!rows_aligned(a, DT)) {
+        q.pitch = uint32_t(b.pad.pitch);
+        pad_rows<T>(a.hidden, a.workspace + b.pad.hidden, a.tokens, a.cols, b.pad.pitch, s);
+        q.hidden = a.workspace + b.pad.hidden;
+        wpad = a.workspace + b.pad.weight;
+    }
+    DPiece p = {};
     p.d = a.workspace + b.d;
-    p.dt = a.workspace + b.dt;
-    p.wt = a.workspace + b.wt;
-    p.xt = a.workspace + b.xt;
     p.acc = reinterpret_cast<float*>(a.workspace + b.acc);
-    p.ldt = b.ldt;
     p.ldx = b.ldx;
     p.splits = b.splits;
-    const dim3 block(kThreads);
-    for (int r = 0; r < a.nranks; r++) {
-        const uint32_t V = a.vocab.start[r + 1] - a.vocab.start[r];
-        if (V == 0) continue;
-        if (a.tokens > 0)
-            hipLaunchKernelGGL(k_transpose<T>, dim3(uint32_t((b.ldt + 63) / 64), (a.cols + 63) / 64), block, 0, s,
-                               static_cast<const T*>(a.hidden[r]), reinterpret_cast<T*>(p.xt), a.tokens, a.cols, b.ldt);
-        for (uint32_t first = 0; first < V; first += a.piece) {
-            const uint32_t count = V - first < a.piece ? V - first : a.piece;
-            LossRows w = {};
-            w.rank = r;
-            w.first = first;
-            w.count = count;
-            p.ldv = up(count, pad_of(DT));
-            if (a.tokens > 0) {
-                w = loss_rows<DT>(a, b.pad, r, first, count, first == 0, s);
-                const Tile t = pick_tile(count, a.tokens);
-                if (t == kWide) piece_d<DT, Wide>(a, w, p, s);
-                else if (t == kSquare) piece_d<DT, Square>(a, w, p, s);
-                else piece_d<DT, Narrow>(a, w, p, s);
-                hipLaunchKernelGGL(k_transpose<T>, dim3(uint32_t((p.ldv + 63) / 64), (a.cols + 63) / 64), block, 0, s,
-                                   static_cast<const T*>(a.weight[r]) + uint64_t(first) * a.cols,
-                                   reinterpret_cast<T*>(p.wt), count, a.cols, p.ldv);
-                const Tile h = pick_tile(a.cols, a.tokens, p.splits);
-                if (h == kWide) piece_dhidden<DT, Wide>(a, p, s);
-                else if (h == kSquare) piece_dhidden<DT, Square>(a, p, s);
-                else piece_dhidden<DT, Narrow>(a, p, s);
-                p.add = 1;
-            }
-            const Tile v = pick_tile(a.cols, count);
-            if (v == kWide) piece_dweight<DT, Wide>(a, w, p, s);
-            else if (v == kSquare) piece_dweight<DT, Square>(a, w, p, s);
-            else piece_dweight<DT, Narrow>(a, w, p, s);
+    for (uint32_t first = 0; first < V; first += a.piece) {
+        const uint32_t count = V - first < a.piece ? V - first : a.piece;
+        Segments g = segments_of(a, DT, first, count, wpad, q.pitch);
+        p.ldv = g.col[g.n];
+        if (a.tokens > 0) {
+            if (wpad != nullptr) pad_weight<T>(a, first, count, wpad, q.pitch, s);
+            const Tile t = pick_tile(DT, count, a.tokens);
+            set_tiles(g, kTileM[t], true);
+            with_tile<DT>(t, [&](auto shape) {
+                typedef decltype(shape) S;
+                p.nt = ceil_div(a.tokens, S::BN);
+                hipLaunchKernelGGL((k_loss_d<DT, S>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
+            });
+            with_tile<DT>(pick_tile(DT, a.cols, a.tokens, p.splits), [&](auto shape) {
+                typedef decltype(shape) S;
+                p.mt = ceil_div(a.cols, S::BM);
+                p.nt = ceil_div(a.tokens, S::BN);
+                hipLaunchKernelGGL((k_loss_dhidden<DT, S>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, q, g, p);
+            });
+            p.add = 1;
         }
+        const Tile t = pick_tile(DT, a.cols, count);
+        set_tiles(g, kTileN[t], false);
+        with_tile<DT>(t, [&](auto shape) {
+            typedef decltype(shape) S;
+            p.mt = ceil_div(a.cols, S::BM);
+            hipLaunchKernelGGL((k_loss_dweight<DT, S>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
+        });
     }
-    if (a.tokens > 0)
-        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens), block, 0, s, a, static_cast<const float*>(p.acc), p.ldx, p.splits);
+    if (a.tokens > 0) {
+        DHiddenOut o = {};
+        for (int r = 0; r < a.nranks; r++) o.p[r] = a.dhidden[r];
+        o.nranks = a.nranks;
+        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens), dim3(kThreads), 0, s, o, static_cast<const float*>(p.acc), a.tokens,
+                           a.cols, p.ldx, p.splits);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
 uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype) {
-    uint64_t entries = 0;
-    for (int r = 0; r < nranks; r++)
-        for (uint32_t V = vocab.start[r + 1] - vocab.start[r], f = 0; f < V; f += kPiece)
-            entries += ceil_div(V - f < kPiece ? V - f : kPiece, kStatsRows);
     Parts w;
-    w.take(entries * tokens * sizeof(float2));
+    w.take(stats_entries(vocab, nranks) * tokens * sizeof(float2));
     w.take(tokens * 4);
-    pad_parts(w, tokens, cols, loss_piece(vocab, nranks, tokens, cols, dtype, 0), dtype);
+    pad_parts(w, tokens, cols, loss_piece(vocab, nranks, 0), dtype);
     return w.at;
 }
 
-// Vocabulary rows per piece: the largest shard, at most what was asked for
-// (16384 by default).
-uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t, uint64_t, int, uint64_t asked) {
-    uint64_t most = 1;
-    for (int r = 0; r < nranks; r++)
-        if (vocab.start[r + 1] - vocab.start[r] > most) most = vocab.start[r + 1] - vocab.start[r];
-    const uint64_t want = asked > 0 ? asked : kPiece;
-    return uint32_t(want < most ? want : most);
+uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t asked) {
+    const uint64_t want = asked > 0 ? asked : kLossPiece, all = vocab.start[nranks];
+    return uint32_t(want < all ? want : all);
 }
 
-uint64_t loss_backward_workspace(const RowTable&, int, uint64_t tokens, uint64_t cols, uint32_t piece, int dtype) {
-    return backward_parts(tokens, cols, piece, dtype).bytes;
+uint64_t loss_backward_workspace(int nranks, uint64_t tokens, uint64_t cols, uint32_t piece, int dtype) {
+    return backward_parts(nranks, tokens, cols, piece, dtype).bytes;
 }
 
 hipError_t launch_loss(const LossArgs& a, int dtype, hipStream_t s) {

@@ -11,7 +11,6 @@
 
 static_assert(sizeof(dt::NormBackArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::ExchangeRowsArgs) <= 4096, "kernel arguments must stay below 4 KiB");
-static_assert(sizeof(dt::LossArgs) <= 3584, "kernel arguments must stay below 4 KiB");
 
 namespace {
 
@@ -520,9 +519,9 @@ dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, co
     g.add(&workspace, 0, need, 1, true, "workspace");
     TRY(g.check("vocab_loss"));
     if (tokens == 0) return DT_OK;
-    copy_list(a.hidden, hidden, nranks);
+    a.hidden = hidden[0];
     copy_list(a.weight, weight, nranks);
-    copy_list(a.targets, targets, nranks);
+    a.targets = targets[0];
     copy_list(a.loss, loss, nranks);
     copy_list(a.lse, lse, nranks);
     a.tokens = uint32_t(tokens);
@@ -538,8 +537,8 @@ size_t dt_vocab_loss_backward_workspace(int nranks, const size_t* vocab_rows, si
     RowTable t;
     dt::report_error(DT_OK, "");
     if (loss_shape(nranks, vocab_rows, tokens, cols, dtype, "vocab_loss_backward_workspace", t) != DT_OK) return 0;
-    const uint32_t piece = dt::loss_piece(t, nranks, tokens, cols, dtype, piece_rows);
-    return dt::loss_backward_workspace(t, nranks, tokens, cols, piece, dtype);
+    const uint32_t piece = dt::loss_piece(t, nranks, piece_rows);
+    return dt::loss_backward_workspace(nranks, tokens, cols, piece, dtype);
 }
 
 dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* weight, const int64_t* const* targets,
@@ -551,8 +550,8 @@ dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* w
     dt::LossArgs a = {};
     TRY(loss_shape(nranks, vocab_rows, tokens, cols, dtype, "vocab_loss_backward", a.vocab));
     const size_t es = esize_of(dtype);
-    a.piece = dt::loss_piece(a.vocab, nranks, tokens, cols, dtype, piece_rows);
-    const size_t need = dt::loss_backward_workspace(a.vocab, nranks, tokens, cols, a.piece, dtype);
+    a.piece = dt::loss_piece(a.vocab, nranks, piece_rows);
+    const size_t need = dt::loss_backward_workspace(nranks, tokens, cols, a.piece, dtype);
     TRY(check_workspace(workspace, workspace_bytes, need, "vocab_loss_backward"));
     Ranges g;
     for (int r = 0; r < nranks; r++) {
@@ -566,11 +565,11 @@ dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* w
     }
     g.add(&workspace, 0, need, 1, true, "workspace");
     TRY(g.check("vocab_loss_backward"));
-    copy_list(a.hidden, hidden, nranks);
+    a.hidden = hidden[0];
     copy_list(a.weight, weight, nranks);
-    copy_list(a.targets, targets, nranks);
-    for (int r = 0; r < nranks; r++) a.lse[r] = const_cast<float*>(lse[r]);
-    copy_list(a.dloss, dloss, nranks);
+    a.targets = targets[0];
+    a.lse_in = lse[0];
+    a.dloss = dloss[0];
     copy_list(a.dhidden, dhidden, nranks);
     copy_list(a.dweight, dweight, nranks);
     a.tokens = uint32_t(tokens);

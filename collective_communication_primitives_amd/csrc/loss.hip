@@ -29,49 +29,57 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 #define DT_LDS __attribute__((address_space(3)))
 
-constexpr int kChunks = 8;             // 16-byte chunks of the summed index per step
+constexpr int kChunks = 4;             // 16-byte chunks of the summed index per step
 constexpr int kStepBytes = kChunks * 16;
+constexpr int kStages = 4;             // steps in LDS
 constexpr int kThreads = 256;          // workgroups of the kernels without a matrix tile
 enum { kRows = 0, kCols = 1 };
 
 // A workgroup's tile of `out`: BM rows of A by BN rows of B, cut among GM x GN
-// waves.  Both operands are staged through LDS, two steps of the summed
-// index at a time (one is multiplied while the next one loads).
+// waves.  Both operands go through LDS, kStages steps of the summed index at a
+// time: one step is in registers and multiplied, the next one is read from
+// LDS, and the others are on their way from memory.
 template <int BM_, int BN_, int GM_, int GN_>
 struct Shape {
     static constexpr int BM = BM_, BN = BN_, GM = GM_, GN = GN_;
     static constexpr int waves = GM * GN, threads = waves * 64;
     static constexpr int WM = BM / GM, WN = BN / GN;  // a wave's part
     static constexpr int MI = WM / 16, NI = WN / 16;  // in matrix instructions of 16 x 16
-    static constexpr int lds = 2 * (BM + BN) * kChunks;  // u32x4
-    static constexpr int loads = (BM + BN) / 8 / waves;  // load instructions of 1 KiB per wave and step
+    static constexpr int stage = (BM + BN) * kChunks;     // u32x4 of a step in LDS
+    static constexpr int loads_a = BM / 16 / waves, loads_b = BN / 16 / waves;  // load instructions of 1 KiB per wave and step
+    static constexpr int loads = loads_a + loads_b;
 };
 
-// Where an operand's bytes of one step are: the buffer resource ends behind
-// the last valid row, so what lies past it loads zeros.
-struct StepSource {
-    const char* base;
-    uint64_t valid;   // bytes from base
-};
-__device__ __forceinline__ rsrc_t step_rsrc(const StepSource& s) {
-    return make_rsrc(s.base, uint32_t(s.valid < 0x7FFFFFFFull ? s.valid : 0x7FFFFFFFull));
+// A buffer resource from values that are the same in every lane, kept in scalar registers.
+__device__ __forceinline__ rsrc_t scalar_rsrc(const char* p, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(p);
+    const uint64_t lo = uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(at))), hi = uint32_t(__builtin_amdgcn_readfirstlane(uint32_t(at >> 32)));
+    return make_rsrc(reinterpret_cast<const char*>(hi << 32 | lo), __builtin_amdgcn_readfirstlane(bytes));
 }
 
+// An operand gives the bytes of each step as a buffer resource that ends
+// behind the last valid row (empty when not `any`), so what lies past it
+// loads zeros without touching memory.
+//
 // kRows: rows of `pitch` bytes, `bytes` of them valid (a multiple of 16).
 struct RowOperand {
     const char* p;     // the tile's first row
     uint32_t rows, pitch, bytes;
-    __device__ __forceinline__ StepSource at(uint32_t) const { return StepSource{p, uint64_t(rows) * pitch}; }
+    __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
+        return scalar_rsrc(p + step * kStepBytes, any && rows > 0 ? rows * pitch - step * kStepBytes : 0);
+    }
+    __device__ __forceinline__ uint32_t left(uint32_t step) const { return bytes - step * kStepBytes; }
 };
 // kCols: row k of `pitch` bytes holds the operand's m (or n) side by side.
 template <int KR>
 struct ColOperand {
     const char* p;     // row 0 at the tile's first column
-    uint64_t rows, pitch, skip;   // skip: bytes of a row before the tile
-    __device__ __forceinline__ StepSource at(uint32_t step) const {
-        const uint64_t k = uint64_t(step) * KR, left = k < rows ? rows - k : 0;
-        return StepSource{p + k * pitch, left > 0 ? (left < KR ? left : KR) * pitch - skip : 0};
+    uint32_t rows, pitch, skip;   // skip: bytes of a row before the tile
+    __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
+        const uint32_t k = step * KR, n = any && k < rows ? rows - k : 0;
+        return scalar_rsrc(p + uint64_t(k) * pitch, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
     }
+    __device__ __forceinline__ uint32_t left(uint32_t) const { return UINT32_MAX; }
 };
 
 // Rows of k per step and the turned layout of a kCols operand in LDS: a row
@@ -89,119 +97,164 @@ struct ColTile {
     }
 };
 
-// One load instruction of the wave: 1 KiB of the operand's step into LDS.
-template <int DT, int MODE, int R, typename OP>
-__device__ __forceinline__ void load_group(const OP& op, rsrc_t r, uint32_t group, uint32_t step, DT_LDS void* to) {
+// One load instruction of the wave brings 1 KiB of the operand's step into
+// LDS, 16 bytes per lane in lane order: the lane's place in the step.
+template <int DT, int MODE, int R>
+__device__ __forceinline__ uint32_t load_place(uint32_t group, uint32_t pitch) {
     const uint32_t lane = threadIdx.x & 63;
-    uint32_t off;
     if constexpr (MODE == kRows) {
-        // 8 rows of 128 bytes: lane l brings row l / 8.  The chunk that lands in
-        // place l % 8 is turned by the row, so that the 16 rows that a read of
+        // 16 rows of 64 bytes: lane l brings row l / 4.  The chunk that lands in
+        // place l % 4 is turned by the row, so that the 16 rows that a read of
         // one chunk touches spread over all banks.
-        const uint32_t row = lane >> 3, c = step * kStepBytes + ((lane & 7) ^ row) * 16;
-        off = c < op.bytes ? (group * 8 + row) * op.pitch + c : 0x80000000u;
+        const uint32_t row = lane >> 2;
+        return (group * 16 + row) * pitch + ((lane & 3) ^ (row >> 2 & 3)) * 16;
     } else {
         typedef ColTile<DT, R> C;
         constexpr uint32_t slots = C::row_bytes / 16, per_unit = C::unit_bytes / 16;
         const uint32_t k = group * C::per_load + lane / slots, slot = lane % slots;
-        off = k * uint32_t(op.pitch) + ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16;
+        return k * pitch + ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16;
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to, 16, int(off), 0, 0, 0);
+}
+// `groups` load instructions of the wave; kRows: zeros behind a row's last byte.
+template <int MODE, int N, typename OP>
+__device__ __forceinline__ void load_step(const OP& op, uint32_t step, bool any, const uint32_t (&place)[N], u32x4* to) {
+    const rsrc_t r = op.at(step, any);
+    const uint32_t lane = threadIdx.x & 63, c = ((lane & 3) ^ (lane >> 4)) * 16;
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const bool in = MODE == kCols || c < op.left(step);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (DT_LDS void*)(to + i * 64), 16, int(in ? place[i] : 0x80000000u), 0, 0, 0);
+    }
 }
 
-// The wave's registers of 16 rows (of A or B) from row `at` of the tile, part
-// kk of the step: lane l gets row l % 16 and 16 bytes of k.
+// The wave's registers of 16 rows (of A or B): lane l gets row l % 16 and
+// chunk l / 16 of the step.  `place` is the lane's byte in the operand's part
+// of a stage for the wave's first 16 rows; the others are a constant away.
 template <int DT, int MODE, int R>
-__device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t at, int kk) {
+__device__ __forceinline__ uint32_t fragment_place(uint32_t at) {
     const uint32_t lane = threadIdx.x & 63;
     if constexpr (MODE == kRows) {
-        const uint32_t row = at + (lane & 15), c = kk * 4 + (lane >> 4);
-        return tile[row * kChunks + (c ^ (row & 7))];
-    } else if constexpr (DT == kBF16) {
-        // k = 32 kk + 8 (lane / 16) + 0..7: two transposing reads of 4 rows of k x 16 each
-        typedef ColTile<DT, R> C;
-        u32x4 v;
-        const char* base = reinterpret_cast<const char*>(tile);
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const uint32_t k = kk * 32 + (lane >> 4) * 8 + h * 4 + ((lane & 15) >> 2);
-            const uint32_t off = k * C::row_bytes + ((at / 16) ^ C::f(k)) * C::unit_bytes + (lane & 3) * 8;
-            const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DT_LDS s16x4*)(base + off));
-            uint32_t w[2];
-            __builtin_memcpy(w, &x, 8);
-            v[2 * h] = w[0];
-            v[2 * h + 1] = w[1];
-        }
-        return v;
+        const uint32_t row = at + (lane & 15);
+        return row * kStepBytes + ((lane >> 4) ^ (row >> 2 & 3)) * 16;
     } else {
-        // k = 16 kk + 4 (lane / 16) + 0..3
         typedef ColTile<DT, R> C;
+        // bf16: row k = 8 (lane / 16) + lane % 16 / 4 of the first transposing read; fp32: k = 4 (lane / 16)
+        const uint32_t k = DT == kBF16 ? (lane >> 4) * 8 + ((lane & 15) >> 2) : (lane >> 4) * 4;
+        return k * C::row_bytes + ((at / 16) ^ C::f(k)) * C::unit_bytes + (DT == kBF16 ? (lane & 3) * 8 : (lane & 15) * 4);
+    }
+}
+template <int DT, int MODE, int R>
+__device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t place, int i) {
+    const char* base = reinterpret_cast<const char*>(tile);
+    if constexpr (MODE == kRows) {
+        return *reinterpret_cast<const u32x4*>(base + place + i * 16 * kStepBytes);
+    } else {
+        typedef ColTile<DT, R> C;
+        const char* from = base + (place ^ (i * C::unit_bytes));  // unit + i: the wave's first unit is a multiple of the others' number
         u32x4 v;
-        const char* base = reinterpret_cast<const char*>(tile);
+        if constexpr (DT == kBF16) {
+            // two transposing reads of 4 rows of k x 16 each
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const uint32_t k = kk * 16 + (lane >> 4) * 4 + e;
-            v[e] = *reinterpret_cast<const uint32_t*>(base + k * C::row_bytes + ((at / 16) ^ C::f(k)) * C::unit_bytes +
-                                                      (lane & 15) * 4);
+            for (int h = 0; h < 2; h++) {
+                const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((DT_LDS s16x4*)(from + h * 4 * C::row_bytes));
+                uint32_t w[2];
+                __builtin_memcpy(w, &x, 8);
+                v[2 * h] = w[0];
+                v[2 * h + 1] = w[1];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = *reinterpret_cast<const uint32_t*>(from + e * C::row_bytes);
         }
         return v;
     }
+}
+
+// Waits until at most `loads` of this wave's loads are outstanding and all its
+// LDS reads are done, then for the workgroup's other waves.
+template <int loads>
+__device__ __forceinline__ void arrive() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // acc[i][j][e] over steps [lo, hi): row m = WM (wave % GM) + 16 i + 4 (lane /
 // 16) + e of A's tile, row n = WN (wave / GM) + 16 j + lane % 16 of B's.
+//
+// The four LDS stages are arrays of their own, and the loop goes round them
+// with constant indices: only so does the compiler see that a read of one
+// stage need not wait for the loads into another.
 template <int DT, typename S, int MA, int MB, typename OA, typename OB>
-__device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t lo, uint32_t hi, u32x4* lds,
-                                            f32x4 (&acc)[S::MI][S::NI]) {
+__device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t lo, uint32_t hi, f32x4 (&acc)[S::MI][S::NI]) {
+    __shared__ u32x4 s0[S::stage], s1[S::stage], s2[S::stage], s3[S::stage];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
     for (int i = 0; i < S::MI; i++)
 #pragma unroll
         for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (lo >= hi) return;
-    auto stage = [&](uint32_t step, int buf) {
-        u32x4* to = lds + buf * (S::BM + S::BN) * kChunks;
-        const rsrc_t ra = step_rsrc(A.at(step)), rb = step_rsrc(B.at(step));
+    const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
+    // the wave's shares of A's and B's groups of 1 KiB
+    uint32_t pa[S::loads_a], pb[S::loads_b];
 #pragma unroll
-        for (int i = 0; i < S::loads; i++) {
-            // group of 1 KiB: A's, then B's
-            const uint32_t g = wave * S::loads + i;
-            if (g < S::BM / 8) load_group<DT, MA, S::BM>(A, ra, g, step, (DT_LDS void*)(to + g * 64));
-            else load_group<DT, MB, S::BN>(B, rb, g - S::BM / 8, step, (DT_LDS void*)(to + g * 64));
+    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(wave * S::loads_a + i, A.pitch);
+#pragma unroll
+    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(wave * S::loads_b + i, B.pitch);
+    // The loop runs in whole rounds of four steps: what is loaded for the steps
+    // behind the last one is zeros (from an empty buffer, no memory is read), so
+    // a wave's outstanding loads can be counted and the loop has one exit.
+    auto load = [&](uint32_t step, u32x4* to) {
+        load_step<MA>(A, step, step < hi, pa, to + wave * S::loads_a * 64);
+        load_step<MB>(B, step, step < hi, pb, to + S::BM * kChunks + wave * S::loads_b * 64);
+    };
+    load(lo, s0);
+    load(lo + 1, s1);
+    load(lo + 2, s2);
+    load(lo + 3, s3);
+    arrive<3 * S::loads>();
+    u32x4 fa[S::MI], fb[2][S::NI];
+    uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
+#pragma unroll
+    for (int i = 0; i < S::MI; i++) fa[i] = fragment<DT, MA, S::BM>(s0, ra, i);
+#pragma unroll
+    for (int j = 0; j < S::NI; j++) fb[0][j] = fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j);
+    // Step `step`: its registers are loaded, its stage of LDS is free once all
+    // waves are here, and the next step's has landed.  A row of A's registers
+    // takes the next step's as soon as it is multiplied; behind the last step
+    // these are bytes that nothing uses.
+    auto turn = [&](uint32_t step, u32x4* mine, const u32x4* following, const u32x4 (&now)[S::NI], u32x4 (&next)[S::NI]) {
+        arrive<2 * S::loads>();
+        load(step + 4, mine);
+        // keeps the compiler from holding every fragment's address of every stage in a register
+        asm volatile("" : "+v"(ra), "+v"(rb));
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) next[j] = fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j);
+#pragma unroll
+        for (int i = 0; i < S::MI; i++) {
+#pragma unroll
+            for (int j = 0; j < S::NI; j++) {
+                if constexpr (DT == kBF16) {
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
+                                                                        __builtin_bit_cast(bf16x8, now[j]), acc[i][j], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fa[i][e]), __uint_as_float(now[j][e]),
+                                                                         acc[i][j], 0, 0, 0);
+                }
+            }
+            fa[i] = fragment<DT, MA, S::BM>(following, ra, i);
         }
     };
-    stage(lo, 0);
-    const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
-    int buf = 0;
-    for (uint32_t step = lo; step < hi; step++, buf ^= 1) {
-        __syncthreads();  // this step's loads have landed, and the other half is no longer read
-        if (step + 1 < hi) stage(step + 1, buf ^ 1);
-        const u32x4* sa = lds + buf * (S::BM + S::BN) * kChunks;
-        const u32x4* sb = sa + S::BM * kChunks;
-#pragma unroll
-        for (int kk = 0; kk < kChunks / 4; kk++) {
-            u32x4 fa[S::MI], fb[S::NI];
-#pragma unroll
-            for (int i = 0; i < S::MI; i++) fa[i] = fragment<DT, MA, S::BM>(sa, wm + i * 16, kk);
-#pragma unroll
-            for (int j = 0; j < S::NI; j++) fb[j] = fragment<DT, MB, S::BN>(sb, wn + j * 16, kk);
-#pragma unroll
-            for (int i = 0; i < S::MI; i++)
-#pragma unroll
-                for (int j = 0; j < S::NI; j++) {
-                    if constexpr (DT == kBF16) {
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
-                                                                            __builtin_bit_cast(bf16x8, fb[j]), acc[i][j],
-                                                                            0, 0, 0);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fa[i][e]),
-                                                                             __uint_as_float(fb[j][e]), acc[i][j], 0, 0, 0);
-                    }
-                }
-        }
+    for (uint32_t step = lo; step < hi; step += 4) {
+        turn(step, s0, s1, fb[0], fb[1]);
+        turn(step + 1, s1, s2, fb[1], fb[0]);
+        turn(step + 2, s2, s3, fb[0], fb[1]);
+        turn(step + 3, s3, s0, fb[1], fb[0]);
     }
+    arrive<0>();  // nothing is on its way into LDS when the workgroup ends
 }
 
 // Tile `id` of mt x nt in an order that keeps an XCD's workgroups on
@@ -212,8 +265,9 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
     const uint32_t t = x * q + (x < rem ? x : rem) + id / 8;
     const uint32_t band = t / (8 * nt), first = band * 8, in = t - band * 8 * nt;
     const uint32_t high = mt - first < 8 ? mt - first : 8;
-    m = first + in % high;
-    n = in / high;
+    // divisions run on the vector unit: back into scalar registers, where the buffer resources are built
+    m = __builtin_amdgcn_readfirstlane(first + in % high);
+    n = __builtin_amdgcn_readfirstlane(in / high);
 }
 
 // exp(x): the argument's product with log2 e is off by half a step of |x| log2 e,
@@ -266,7 +320,6 @@ __device__ __forceinline__ void join(float& top, float& s, float top2, float s2)
 
 template <int DT, typename S>
 __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segments g, StatsArgs q) {
-    __shared__ u32x4 lds[S::lds];
     __shared__ float2 part[S::GM][S::BN];
     uint32_t mt, nt;
     tile_of(blockIdx.x, g.tile[g.n], q.token_tiles, mt, nt);
@@ -275,7 +328,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segmen
     f32x4 acc[S::MI][S::NI];
     const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
     const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
-    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, lds, acc);
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t wm = wave % S::GM, wn = wave / S::GM;
     const uint32_t mlane = wm * S::WM + (lane >> 4) * 4;  // acc[i][j][e] is row mlane + 16 i + e of the tile
@@ -364,7 +417,6 @@ struct DPiece {
 template <int DT, typename S>
 __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
-    __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
     tile_of(blockIdx.x, g.tile[g.n], p.nt, mt, nt);
     const int sg = segment_of(g.tile, g.n, mt);
@@ -374,7 +426,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
     f32x4 acc[S::MI][S::NI];
     const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
     const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
-    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, lds, acc);
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t mlane = (wave % S::GM) * S::WM + (lane >> 4) * 4;
     T* d = reinterpret_cast<T*>(p.d) + g.col[sg] + m0;
@@ -409,15 +461,15 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
 template <int KR>
 struct WeightOperand {
     const Segments& g;
-    uint64_t pitch, skip;
+    uint32_t pitch, skip;
     mutable int sg;
-    __device__ __forceinline__ StepSource at(uint32_t step) const {
+    __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
         const uint32_t k = step * KR;
         while (sg + 1 < g.n && k >= g.col[sg + 1]) sg++;
-        const uint32_t row = k - g.col[sg], left = row < g.count[sg] ? g.count[sg] - row : 0;
-        return StepSource{g.weight[sg] + uint64_t(row) * pitch + skip,
-                          left > 0 ? uint64_t(left < KR ? left : KR) * pitch - skip : 0};
+        const uint32_t row = k - g.col[sg], n = any && row < g.count[sg] ? g.count[sg] - row : 0;
+        return scalar_rsrc(g.weight[sg] + uint64_t(row) * pitch + skip, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
     }
+    __device__ __forceinline__ uint32_t left(uint32_t) const { return UINT32_MAX; }
 };
 
 // acc[split][t][h] (+)= sum over the split's part of the piece of d[t][v] weight[v][h].
@@ -425,16 +477,17 @@ template <int DT, typename S>
 __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     constexpr int KR = kStepBytes / int(sizeof(T));
-    __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
     tile_of(blockIdx.x, p.mt, p.nt, mt, nt);
     const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
     const uint32_t pitch = uint32_t(p.ldv * sizeof(T)), steps = pitch / kStepBytes;
-    const uint32_t lo = uint32_t(uint64_t(steps) * blockIdx.y / p.splits), hi = uint32_t(uint64_t(steps) * (blockIdx.y + 1) / p.splits);
+    // the first `more` splits take one step more than the others
+    const uint32_t each = __builtin_amdgcn_readfirstlane(steps / p.splits), more = steps - each * p.splits, y = blockIdx.y;
+    const uint32_t lo = y * each + (y < more ? y : more), hi = lo + each + (y < more ? 1 : 0);
     f32x4 acc[S::MI][S::NI];
-    const WeightOperand<KR> A{g, a.pitch, m0 * sizeof(T), 0};
+    const WeightOperand<KR> A{g, a.pitch, m0 * uint32_t(sizeof(T)), 0};
     const RowOperand B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch};
-    matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, lds, acc);
+    matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* to = p.acc + uint64_t(blockIdx.y) * a.tokens * p.ldx;
 #pragma unroll
@@ -454,16 +507,16 @@ template <int DT, typename S>
 __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     constexpr int KR = kStepBytes / int(sizeof(T));
-    __shared__ u32x4 lds[S::lds];
     uint32_t mt, nt;
     tile_of(blockIdx.x, p.mt, g.tile[g.n], mt, nt);
     const int sg = segment_of(g.tile, g.n, nt);
     const uint32_t m0 = mt * S::BM, n0 = (nt - g.tile[sg]) * S::BN;
     f32x4 acc[S::MI][S::NI];
-    const uint64_t es = sizeof(T), skip = uint64_t(g.col[sg] + n0) * es;
+    constexpr uint32_t es = sizeof(T);
+    const uint32_t skip = (g.col[sg] + n0) * es;
     const ColOperand<KR> A{a.hidden + m0 * es, a.tokens, a.pitch, m0 * es};
-    const ColOperand<KR> B{p.d + skip, a.tokens, p.ldv * es, skip};
-    matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR, lds, acc);
+    const ColOperand<KR> B{p.d + skip, a.tokens, uint32_t(p.ldv * es), skip};
+    matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     T* out = reinterpret_cast<T*>(g.dweight[sg]);
     const bool quads = a.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;

@@ -272,7 +272,23 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 
 // exp(x): the argument's product with log2 e is off by half a step of |x| log2 e,
 // which adds |x| half steps to the result's error.
-__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+
+// Four values rounded to the dtype and stored as one (`to` aligned for it); zeros unless `use`.
+template <int DT>
+__device__ __forceinline__ void store_quad(typename Elem<DT>::type* to, f32x4 v, bool use) {
+    if constexpr (DT == kBF16) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        uint2 o;
+        o.x = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[0]), __bf16(v[1])});
+        o.y = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[2]), __bf16(v[3])});
+        if (!use) o = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(to) = o;
+    } else {
+        *reinterpret_cast<f32x4*>(to) = use ? v : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+}
 
 // A piece of the vocabulary: the parts of it that single ranks hold.
 struct Segments {
@@ -362,11 +378,11 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segmen
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         float s = 0.f;
-        const float base = top > -INFINITY ? top : 0.f;
+        const float base2 = top > -INFINITY ? top * kLog2e : 0.f;
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) s += exp_of(acc[i][j][e] - base);
+            for (int e = 0; e < 4; e++) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -base2));
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16) part[wm][nl] = make_float2(top, s);
@@ -435,23 +451,31 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
         const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
         if (n >= a.tokens) continue;
         const int64_t t = a.targets[n];
-        const float lse = a.lse[n];
+        const float lse2 = a.lse[n] * kLog2e;
         const bool use = counted(a, t);
         const float f = use ? a.dloss[n] : 0.f;
+        // d = p f; the target's row and the rows behind the shard's last one are mended below
+#pragma unroll
+        for (int i = 0; i < S::MI; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -lse2)) * f;
         const int64_t at = t - int64_t(g.vocab[sg]) - int64_t(m0);
         const uint32_t hit = use && at >= 0 && at < S::BM ? uint32_t(at) : UINT32_MAX;  // the target's row in the tile
+        if (__any(hit != UINT32_MAX) || left < S::BM) {
+#pragma unroll
+            for (int i = 0; i < S::MI; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const uint32_t m = mlane + i * 16 + e;
+                    if (hit == m) acc[i][j][e] -= f;
+                    if (m >= left) acc[i][j][e] = 0.f;
+                }
+        }
 #pragma unroll
         for (int i = 0; i < S::MI; i++) {
             const uint32_t m = mlane + i * 16;
-            T o[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float v = (exp_of(acc[i][j][e] - lse) - (hit == m + e ? 1.f : 0.f)) * f;
-                o[e] = Elem<DT>::put(use && m + e < left ? v : 0.f);
-            }
             // a part's width is a multiple of 4: the four are all inside it or all behind it
-            if (m0 + m < padded)
-                __builtin_memcpy(__builtin_assume_aligned(d + uint64_t(n) * p.ldv + m, 4 * sizeof(T)), o, sizeof o);
+            if (m0 + m < padded) store_quad<DT>(d + uint64_t(n) * p.ldv + m, acc[i][j], use);
         }
     }
 }
@@ -527,16 +551,13 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
             const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
             const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
             if (n >= g.count[sg] || m >= a.cols) continue;
-            T o[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) o[e] = Elem<DT>::put(acc[i][j][e]);
             T* to = out + uint64_t(n) * a.cols + m;
             if (quads) {
-                __builtin_memcpy(__builtin_assume_aligned(to, 4 * sizeof(T)), o, sizeof o);
+                store_quad<DT>(to, acc[i][j], true);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (m + e < a.cols) to[e] = o[e];
+                    if (m + e < a.cols) to[e] = Elem<DT>::put(acc[i][j][e]);
             }
         }
 }

@@ -97,17 +97,26 @@ struct ColTile {
     }
 };
 
+// kRows: the chunk of row r that lies in place p of the row's 64 bytes is p ^
+// row_turn(r).  A read takes one chunk of 16 rows in lanes 0-15, the next chunk
+// in 16-31 and so on, and serves 16 lanes at a time: 0-3, 12-15, 20-23, 24-27,
+// then 4-11, 16-19, 28-31, and the same of the upper half.  Rows four apart lie
+// on the same banks; turned by 0, 2, 3, 1 in fours, each such 16 lanes take all
+// 64 banks once (turned by 0, 1, 2, 3 half the reads' cycles were conflicts).
+__device__ __forceinline__ uint32_t row_turn(uint32_t row) {
+    const uint32_t q = row >> 2 & 3;
+    return (q & 1) << 1 ^ (q >> 1) * 3;
+}
+
 // One load instruction of the wave brings 1 KiB of the operand's step into
 // LDS, 16 bytes per lane in lane order: the lane's place in the step.
 template <int DT, int MODE, int R>
 __device__ __forceinline__ uint32_t load_place(uint32_t group, uint32_t pitch) {
     const uint32_t lane = threadIdx.x & 63;
     if constexpr (MODE == kRows) {
-        // 16 rows of 64 bytes: lane l brings row l / 4.  The chunk that lands in
-        // place l % 4 is turned by the row, so that the 16 rows that a read of
-        // one chunk touches spread over all banks.
+        // 16 rows of 64 bytes: lane l brings row l / 4
         const uint32_t row = lane >> 2;
-        return (group * 16 + row) * pitch + ((lane & 3) ^ (row >> 2 & 3)) * 16;
+        return (group * 16 + row) * pitch + ((lane & 3) ^ row_turn(row)) * 16;
     } else {
         typedef ColTile<DT, R> C;
         constexpr uint32_t slots = C::row_bytes / 16, per_unit = C::unit_bytes / 16;
@@ -119,7 +128,7 @@ __device__ __forceinline__ uint32_t load_place(uint32_t group, uint32_t pitch) {
 template <int MODE, int N, typename OP>
 __device__ __forceinline__ void load_step(const OP& op, uint32_t step, bool any, const uint32_t (&place)[N], u32x4* to) {
     const rsrc_t r = op.at(step, any);
-    const uint32_t lane = threadIdx.x & 63, c = ((lane & 3) ^ (lane >> 4)) * 16;
+    const uint32_t lane = threadIdx.x & 63, c = ((lane & 3) ^ row_turn(lane >> 2)) * 16;
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const bool in = MODE == kCols || c < op.left(step);
@@ -135,7 +144,7 @@ __device__ __forceinline__ uint32_t fragment_place(uint32_t at) {
     const uint32_t lane = threadIdx.x & 63;
     if constexpr (MODE == kRows) {
         const uint32_t row = at + (lane & 15);
-        return row * kStepBytes + ((lane >> 4) ^ (row >> 2 & 3)) * 16;
+        return row * kStepBytes + ((lane >> 4) ^ row_turn(row)) * 16;
     } else {
         typedef ColTile<DT, R> C;
         // bf16: row k = 8 (lane / 16) + lane % 16 / 4 of the first transposing read; fp32: k = 4 (lane / 16)

@@ -10,17 +10,289 @@
 // rounded once.  The weight's gradient is the sum over the rows of every
 // rank, folded in a fixed order, and goes to every rank: the AllReduce of
 // the ranks' partial gradients in the same pass.
+//
+// Both passes read each row once: a row lives in the registers of WPR waves,
+// and a workgroup walks over rows with its share of the weight (and, in the
+// backward pass, of dw and db) in registers too.  The next row's loads go
+// out before the current row is reduced.
+#include <type_traits>
+
 #include "dt_step_device.h"
 
 namespace dt {
 namespace {
 
-constexpr int kNormWaves = kBlock / 64;
-
-template <int DT>
-__global__ __launch_bounds__(kBlock) void k_norm(NormArgs a) {
+// A lane's units of a row: 16-byte vectors, or single elements where rows are
+// off the 16-byte boundaries.
+template <int DT, bool VEC>
+struct Unit {
     typedef typename Elem<DT>::type T;
-    __shared__ float tmp[2][kNormWaves];
+    static constexpr int elems = VEC ? 16 / int(sizeof(T)) : 1;
+    T v[elems];
+    __device__ __forceinline__ float get(int e) const { return Elem<DT>::get(v[e]); }
+    __device__ __forceinline__ void put(int e, float f) { v[e] = Elem<DT>::put(f); }
+};
+template <int DT, bool VEC>
+__device__ __forceinline__ Unit<DT, VEC> load_unit(const void* row, uint32_t u) {
+    typedef Unit<DT, VEC> U;
+    U x;
+    if constexpr (VEC) {
+        const u32x4 v = load16(static_cast<const char*>(row) + uint64_t(u) * 16);
+        __builtin_memcpy(x.v, &v, 16);
+    } else {
+        x.v[0] = static_cast<const typename U::T*>(row)[u];
+    }
+    return x;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_unit(void* row, uint32_t u, const Unit<DT, VEC>& x) {
+    typedef Unit<DT, VEC> U;
+    if constexpr (VEC) {
+        u32x4 v;
+        __builtin_memcpy(&v, x.v, 16);
+        store16(static_cast<char*>(row) + uint64_t(u) * 16, v);
+    } else {
+        static_cast<typename U::T*>(row)[u] = x.v[0];
+    }
+}
+
+// Sum over the WPR waves that hold a row; `slot` is one of the workgroup's
+// exchange cells, not used again before the next-but-one barrier.
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* slot) {
+    v = wave_sum(v);
+    if constexpr (WPR == 1) return v;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WPR; w++) s += slot[w];
+    return s;
+}
+
+template <int WPR>
+struct Group {
+    static constexpr int waves = WPR > 4 ? WPR : 4;   // waves of a workgroup
+    static constexpr int threads = waves * 64;
+    static constexpr int rows = WPR == 1 ? waves : 1;  // rows in flight in a workgroup
+    static constexpr int lanes = 64 * WPR;             // lanes that share a row
+};
+
+template <int DT, bool VEC, int NV, int WPR>
+__global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
+    typedef Unit<DT, VEC> U;
+    typedef typename Elem<DT>::type T;
+    constexpr int E = U::elems, L = Group<WPR>::lanes;
+    __shared__ float cells[2][2][Group<WPR>::waves];
+    const uint32_t lane = threadIdx.x % L, units = a.cols / E, step = gridDim.x * Group<WPR>::rows;
+    const uint32_t total = a.rows.start[a.nranks];
+    uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+    if (row >= total) return;
+    int r = rank_of_row(a.rows, a.nranks, row);
+    U w[NV], b[NV], x[NV];
+    const bool biased = a.bias[r] != nullptr;
+    const uint64_t pitch = uint64_t(a.cols) * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < NV; i++) {
+        const uint32_t u = lane + i * L;
+        if (u < units) {
+            w[i] = load_unit<DT, VEC>(a.weight[r], u);
+            if (biased) b[i] = load_unit<DT, VEC>(a.bias[r], u);
+        }
+    }
+    const char* from = static_cast<const char*>(a.x[r]) + uint64_t(row - a.rows.start[r]) * pitch;
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+        if (lane + i * L < units) x[i] = load_unit<DT, VEC>(from, lane + i * L);
+    const float inv = 1.f / float(a.cols);
+    for (int parity = 0; row < total; parity ^= 1) {
+        float v[NV][E];
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool in = lane + i * L < units;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                v[i][e] = in ? x[i].get(e) : 0.f;
+                s += v[i][e];
+            }
+        }
+        const int now = r;
+        const uint64_t local = row - a.rows.start[now];
+        const uint32_t next = row + step;
+        if (next < total) {
+            while (next >= a.rows.start[r + 1]) r++;
+            from = static_cast<const char*>(a.x[r]) + uint64_t(next - a.rows.start[r]) * pitch;
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (lane + i * L < units) x[i] = load_unit<DT, VEC>(from, lane + i * L);
+        }
+        const float mean = row_sum<WPR>(s, cells[parity][0]) * inv;
+        float q = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const bool in = lane + i * L < units;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                v[i][e] -= mean;
+                q += in ? v[i][e] * v[i][e] : 0.f;
+            }
+        }
+        const float rstd = 1.f / sqrtf(row_sum<WPR>(q, cells[parity][1]) * inv + a.eps);
+        char* to = static_cast<char*>(a.y[now]) + local * pitch;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            if (lane + i * L >= units) continue;
+            U y;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const float n = v[i][e] * rstd * w[i].get(e);
+                y.put(e, biased ? n + b[i].get(e) : n);
+            }
+            store_unit<DT, VEC>(to, lane + i * L, y);
+        }
+        if (lane == 0 && a.mean[now] != nullptr) {
+            a.mean[now][local] = mean;
+            a.rstd[now][local] = rstd;
+        }
+        row = next;
+    }
+}
+
+template <int DT, bool VEC, int NV, int WPR>
+__global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackArgs a) {
+    typedef Unit<DT, VEC> U;
+    typedef typename Elem<DT>::type T;
+    constexpr int E = U::elems, L = Group<WPR>::lanes;
+    __shared__ float cells[2][2][Group<WPR>::waves];
+    const uint32_t lane = threadIdx.x % L, units = a.cols / E, step = gridDim.x * Group<WPR>::rows;
+    const uint32_t total = a.rows.start[a.nranks];
+    uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+    float dw[NV][E], db[NV][E];
+#pragma unroll
+    for (int i = 0; i < NV; i++)
+#pragma unroll
+        for (int e = 0; e < E; e++) dw[i][e] = db[i][e] = 0.f;
+    if (row < total) {
+        int r = rank_of_row(a.rows, a.nranks, row);
+        U w[NV], x[NV], d[NV];
+        const uint64_t pitch = uint64_t(a.cols) * sizeof(T);
+        uint64_t local = row - a.rows.start[r];
+        float mean = a.mean[r][local], rstd = a.rstd[r][local];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const uint32_t u = lane + i * L;
+            if (u < units) {
+                w[i] = load_unit<DT, VEC>(a.weight[r], u);
+                x[i] = load_unit<DT, VEC>(static_cast<const char*>(a.x[r]) + local * pitch, u);
+                d[i] = load_unit<DT, VEC>(static_cast<const char*>(a.dy[r]) + local * pitch, u);
+            }
+        }
+        const float inv = 1.f / float(a.cols);
+        for (int parity = 0; row < total; parity ^= 1) {
+            float n[NV][E], g[NV][E];
+            float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                const bool in = lane + i * L < units;
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    const float dy = in ? d[i].get(e) : 0.f;
+                    n[i][e] = in ? (x[i].get(e) - mean) * rstd : 0.f;
+                    g[i][e] = in ? dy * w[i].get(e) : 0.f;
+                    s1 += g[i][e];
+                    s2 += g[i][e] * n[i][e];
+                    dw[i][e] += dy * n[i][e];
+                    db[i][e] += dy;
+                }
+            }
+            const int now = r;
+            const float scale = rstd;
+            char* to = static_cast<char*>(a.dx[now]) + local * pitch;
+            const uint32_t next = row + step;
+            if (next < total) {
+                while (next >= a.rows.start[r + 1]) r++;
+                local = next - a.rows.start[r];
+                mean = a.mean[r][local];
+                rstd = a.rstd[r][local];
+#pragma unroll
+                for (int i = 0; i < NV; i++) {
+                    const uint32_t u = lane + i * L;
+                    if (u < units) {
+                        x[i] = load_unit<DT, VEC>(static_cast<const char*>(a.x[r]) + local * pitch, u);
+                        d[i] = load_unit<DT, VEC>(static_cast<const char*>(a.dy[r]) + local * pitch, u);
+                    }
+                }
+            }
+            s1 = wave_sum(s1);
+            s2 = wave_sum(s2);
+            if constexpr (WPR > 1) {
+                if ((threadIdx.x & 63) == 0) {
+                    cells[parity][0][threadIdx.x >> 6] = s1;
+                    cells[parity][1][threadIdx.x >> 6] = s2;
+                }
+                __syncthreads();
+                s1 = s2 = 0.f;
+#pragma unroll
+                for (int k = 0; k < WPR; k++) {
+                    s1 += cells[parity][0][k];
+                    s2 += cells[parity][1][k];
+                }
+            }
+            const float m1 = s1 * inv, m2 = s2 * inv;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                if (lane + i * L >= units) continue;
+                U o;
+#pragma unroll
+                for (int e = 0; e < E; e++) o.put(e, scale * (g[i][e] - m1 - n[i][e] * m2));
+                store_unit<DT, VEC>(to, lane + i * L, o);
+            }
+            row = next;
+        }
+    }
+    // the workgroup's strip of the partial sums
+    float* strip = a.partial + uint64_t(blockIdx.x) * 2 * a.cols;
+    if constexpr (WPR == 1) {
+        // its waves' sums one after the other, in a fixed order
+        __shared__ float sums[2][NV * E * 64];
+        for (int k = 0; k < Group<WPR>::waves; k++) {
+            if (int(threadIdx.x >> 6) == k) {
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const uint32_t c = (lane + i * L) * E + e;
+                        sums[0][c] = k == 0 ? dw[i][e] : sums[0][c] + dw[i][e];
+                        sums[1][c] = k == 0 ? db[i][e] : sums[1][c] + db[i][e];
+                    }
+            }
+            __syncthreads();
+        }
+        for (uint32_t c = threadIdx.x; c < a.cols; c += Group<WPR>::threads) {
+            strip[c] = sums[0][c];
+            strip[a.cols + c] = sums[1][c];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const uint32_t u = lane + i * L;
+            if (u >= units) continue;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                strip[u * E + e] = dw[i][e];
+                strip[a.cols + u * E + e] = db[i][e];
+            }
+        }
+    }
+}
+
+// Rows too wide for the registers: a workgroup per row that reads it again for
+// each sum, and the columns' sums strip by strip.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void k_norm_wide(NormArgs a) {
+    typedef typename Elem<DT>::type T;
+    __shared__ float tmp[2][kBlock / 64];
     const uint32_t row = blockIdx.x;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
@@ -31,13 +303,13 @@ __global__ __launch_bounds__(kBlock) void k_norm(NormArgs a) {
     T* y = static_cast<T*>(a.y[r]) + local * C;
     float s = 0.f;
     for (uint32_t c = threadIdx.x; c < C; c += kBlock) s += Elem<DT>::get(x[c]);
-    const float mean = block_sum<kNormWaves>(s, tmp[0]) / float(C);
+    const float mean = block_sum<kBlock / 64>(s, tmp[0]) / float(C);
     float q = 0.f;
     for (uint32_t c = threadIdx.x; c < C; c += kBlock) {
         const float d = Elem<DT>::get(x[c]) - mean;
         q += d * d;
     }
-    const float var = block_sum<kNormWaves>(q, tmp[1]) / float(C);
+    const float var = block_sum<kBlock / 64>(q, tmp[1]) / float(C);
     const float rstd = 1.f / sqrtf(var + a.eps);
     for (uint32_t c = threadIdx.x; c < C; c += kBlock) {
         float v = (Elem<DT>::get(x[c]) - mean) * rstd * Elem<DT>::get(w[c]);
@@ -51,9 +323,9 @@ __global__ __launch_bounds__(kBlock) void k_norm(NormArgs a) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(kBlock) void k_norm_dx(NormBackArgs a) {
+__global__ __launch_bounds__(kBlock) void k_norm_dx_wide(NormBackArgs a) {
     typedef typename Elem<DT>::type T;
-    __shared__ float tmp[2][kNormWaves];
+    __shared__ float tmp[2][kBlock / 64];
     const uint32_t row = blockIdx.x;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
@@ -69,8 +341,8 @@ __global__ __launch_bounds__(kBlock) void k_norm_dx(NormBackArgs a) {
         s1 += g;
         s2 += g * ((Elem<DT>::get(x[c]) - mean) * rstd);
     }
-    const float m1 = block_sum<kNormWaves>(s1, tmp[0]) / float(C);
-    const float m2 = block_sum<kNormWaves>(s2, tmp[1]) / float(C);
+    const float m1 = block_sum<kBlock / 64>(s1, tmp[0]) / float(C);
+    const float m2 = block_sum<kBlock / 64>(s2, tmp[1]) / float(C);
     for (uint32_t c = threadIdx.x; c < C; c += kBlock) {
         const float g = Elem<DT>::get(dy[c]) * Elem<DT>::get(w[c]);
         const float n = (Elem<DT>::get(x[c]) - mean) * rstd;
@@ -81,7 +353,7 @@ __global__ __launch_bounds__(kBlock) void k_norm_dx(NormBackArgs a) {
 // Strip blockIdx.y of the rows, one column per thread: the strip's share of
 // dw and db.
 template <int DT>
-__global__ __launch_bounds__(kBlock) void k_norm_dw(NormBackArgs a) {
+__global__ __launch_bounds__(kBlock) void k_norm_dw_wide(NormBackArgs a) {
     typedef typename Elem<DT>::type T;
     const uint32_t c = blockIdx.x * kBlock + threadIdx.x;
     if (c >= a.cols) return;
@@ -102,48 +374,146 @@ __global__ __launch_bounds__(kBlock) void k_norm_dw(NormBackArgs a) {
     a.partial[(uint64_t(blockIdx.y) * 2 + 1) * a.cols + c] = db;
 }
 
-// The strips folded in order; every rank gets the sum.
+// The strips folded in order: 64 columns per workgroup, each of its 16 waves
+// takes every 16th strip, then the waves in order; every rank gets the sums.
 template <int DT>
-__global__ __launch_bounds__(kBlock) void k_norm_fold(NormBackArgs a) {
+__global__ __launch_bounds__(1024) void k_norm_fold(NormBackArgs a) {
     typedef typename Elem<DT>::type T;
-    const uint32_t c = blockIdx.x * kBlock + threadIdx.x;
-    if (c >= a.cols) return;
+    __shared__ float sums[2][16][64];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
     float dw = 0.f, db = 0.f;
-    for (uint32_t s = 0; s < a.strips; s++) {
-        dw += a.partial[(uint64_t(s) * 2) * a.cols + c];
-        db += a.partial[(uint64_t(s) * 2 + 1) * a.cols + c];
-    }
-    for (int r = 0; r < a.nranks; r++) {
-        static_cast<T*>(a.dweight[r])[c] = Elem<DT>::put(dw);
-        if (a.dbias[r] != nullptr) static_cast<T*>(a.dbias[r])[c] = Elem<DT>::put(db);
-    }
+    if (c < a.cols)
+        for (uint32_t s = wave; s < a.strips; s += 16) {
+            dw += a.partial[(uint64_t(s) * 2) * a.cols + c];
+            db += a.partial[(uint64_t(s) * 2 + 1) * a.cols + c];
+        }
+    sums[0][wave][lane] = dw;
+    sums[1][wave][lane] = db;
+    __syncthreads();
+    if (wave >= 2 || c >= a.cols) return;
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k++) s += sums[wave][k][lane];
+    void* const* out = wave == 0 ? a.dweight : a.dbias;
+    for (int r = 0; r < a.nranks; r++)
+        if (out[r] != nullptr) static_cast<T*>(out[r])[c] = Elem<DT>::put(s);
 }
 
-template <int DT>
-hipError_t norm_backward(const NormBackArgs& a, hipStream_t s) {
-    const uint32_t rows = a.rows.start[a.nranks];
-    const uint32_t colblocks = (a.cols + kBlock - 1) / kBlock;
-    if (rows > 0) {
-        hipLaunchKernelGGL(k_norm_dx<DT>, dim3(rows), dim3(kBlock), 0, s, a);
-        hipLaunchKernelGGL(k_norm_dw<DT>, dim3(colblocks, a.strips), dim3(kBlock), 0, s, a);
+// How a row of `cols` elements is held: WPR waves with up to NV units per
+// lane.  NV stays small, so that several workgroups share a CU: a row of up to
+// 1024 (bf16) or 512 (fp32) elements fits one wave, which then needs no
+// exchange between waves at all.
+struct Hold {
+    int nv, wpr;   // wpr 0: too wide
+};
+Hold hold(uint32_t units, bool vec) {
+    if (vec) {
+        if (units <= 64) return {1, 1};
+        if (units <= 128) return {2, 1};
+        if (units <= 256) return {1, 4};
+        if (units <= 512) return {2, 4};
+        if (units <= 1024) return {4, 4};
+        if (units <= 2048) return {2, 16};
+        if (units <= 4096) return {4, 16};
+        return {0, 0};
     }
-    hipLaunchKernelGGL(k_norm_fold<DT>, dim3(colblocks), dim3(kBlock), 0, s, a);
+    if (units <= 256) return {4, 1};
+    if (units <= 512) return {8, 1};
+    if (units <= 1024) return {4, 4};
+    if (units <= 2048) return {8, 4};
+    if (units <= 4096) return {16, 4};
+    if (units <= 16384) return {16, 16};
+    return {0, 0};
+}
+// run(constant NV, constant WPR)
+template <bool VEC, typename F>
+void with_hold(Hold h, F&& run) {
+#define DT_HOLD(n, w) \
+    if (h.nv == n && h.wpr == w) return run(std::integral_constant<int, n>(), std::integral_constant<int, w>())
+    if constexpr (VEC) {
+        DT_HOLD(1, 1);
+        DT_HOLD(2, 1);
+        DT_HOLD(1, 4);
+        DT_HOLD(2, 4);
+        DT_HOLD(4, 4);
+        DT_HOLD(2, 16);
+        DT_HOLD(4, 16);
+    } else {
+        DT_HOLD(4, 1);
+        DT_HOLD(8, 1);
+        DT_HOLD(4, 4);
+        DT_HOLD(8, 4);
+        DT_HOLD(16, 4);
+        DT_HOLD(16, 16);
+    }
+#undef DT_HOLD
+}
+
+constexpr uint32_t kWorkgroups = 1024;  // that walk over the rows
+uint32_t workgroups(uint32_t rows, int wpr) {
+    const uint32_t need = wpr == 1 ? (rows + 3) / 4 : rows, most = wpr == 16 ? kWorkgroups / 2 : kWorkgroups;
+    return need < most ? need : most;
+}
+
+bool aligned(const void* const* list, int n) {
+    for (int r = 0; r < n; r++)
+        if (reinterpret_cast<uintptr_t>(list[r]) % 16 != 0) return false;
+    return true;
+}
+
+template <int DT, bool VEC>
+hipError_t norm(const NormArgs& a, hipStream_t s) {
+    const uint32_t rows = a.rows.start[a.nranks];
+    const Hold h = hold(a.cols / Unit<DT, VEC>::elems, VEC);
+    if (h.wpr == 0) {
+        hipLaunchKernelGGL(k_norm_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
+    } else {
+        with_hold<VEC>(h, [&](auto nv, auto wpr) {
+            constexpr int W = decltype(wpr)::value;
+            hipLaunchKernelGGL((k_norm<DT, VEC, decltype(nv)::value, W>), dim3(workgroups(rows, W)), dim3(Group<W>::threads), 0, s, a);
+        });
+    }
     return hipGetLastError();
 }
+
+template <int DT, bool VEC>
+hipError_t norm_backward(NormBackArgs a, hipStream_t s) {
+    const uint32_t rows = a.rows.start[a.nranks];
+    const Hold h = hold(a.cols / Unit<DT, VEC>::elems, VEC);
+    a.strips = 0;
+    if (rows > 0 && h.wpr == 0) {
+        a.strips = rows < 256 ? rows : 256;
+        hipLaunchKernelGGL(k_norm_dx_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
+        hipLaunchKernelGGL(k_norm_dw_wide<DT>, dim3((a.cols + kBlock - 1) / kBlock, a.strips), dim3(kBlock), 0, s, a);
+    } else if (rows > 0) {
+        with_hold<VEC>(h, [&](auto nv, auto wpr) {
+            constexpr int W = decltype(wpr)::value;
+            a.strips = workgroups(rows, W) < 512 ? workgroups(rows, W) : 512;
+            hipLaunchKernelGGL((k_norm_backward<DT, VEC, decltype(nv)::value, W>), dim3(a.strips), dim3(Group<W>::threads), 0, s, a);
+        });
+    }
+    hipLaunchKernelGGL(k_norm_fold<DT>, dim3((a.cols + 63) / 64), dim3(1024), 0, s, a);
+    return hipGetLastError();
+}
+
+bool rows_aligned(uint32_t cols, int dtype) { return cols * uint64_t(dtype == kBF16 ? 2 : 4) % 16 == 0; }
 
 }  // namespace
 
 hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
-    const uint32_t rows = a.rows.start[a.nranks];
-    if (dtype == kBF16) hipLaunchKernelGGL(k_norm<kBF16>, dim3(rows), dim3(kBlock), 0, s, a);
-    else hipLaunchKernelGGL(k_norm<kF32>, dim3(rows), dim3(kBlock), 0, s, a);
-    return hipGetLastError();
+    const bool vec = rows_aligned(a.cols, dtype) && aligned(a.x, a.nranks) && aligned(a.y, a.nranks) &&
+                     aligned(a.weight, a.nranks) && aligned(a.bias, a.nranks);
+    if (dtype == kBF16) return vec ? norm<kBF16, true>(a, s) : norm<kBF16, false>(a, s);
+    return vec ? norm<kF32, true>(a, s) : norm<kF32, false>(a, s);
 }
 
-uint32_t norm_strips(uint32_t rows, uint32_t) { return rows < 256 ? rows : 256; }
+uint32_t norm_strips(uint32_t rows, uint32_t) { return rows < 512 ? rows : 512; }
 
 hipError_t launch_norm_backward(const NormBackArgs& a, int dtype, hipStream_t s) {
-    return dtype == kBF16 ? norm_backward<kBF16>(a, s) : norm_backward<kF32>(a, s);
+    const bool vec = rows_aligned(a.cols, dtype) && aligned(a.x, a.nranks) && aligned(a.dy, a.nranks) &&
+                     aligned(a.dx, a.nranks) && aligned(a.weight, a.nranks);
+    if (dtype == kBF16) return vec ? norm_backward<kBF16, true>(a, s) : norm_backward<kBF16, false>(a, s);
+    return vec ? norm_backward<kF32, true>(a, s) : norm_backward<kF32, false>(a, s);
 }
 
 }  // namespace dt

@@ -32,27 +32,38 @@ struct Unit {
     __device__ __forceinline__ float get(int e) const { return Elem<DT>::get(v[e]); }
     __device__ __forceinline__ void put(int e, float f) { v[e] = Elem<DT>::put(f); }
 };
-template <int DT, bool VEC>
-__device__ __forceinline__ Unit<DT, VEC> load_unit(const void* row, uint32_t u) {
+// A row as a buffer resource: a vector past its end loads zeros and is not
+// stored, so the last vectors need no branch.  Row addresses are the same in
+// every lane of a wave.
+struct Row {
+    const char* p;
+    rsrc_t r;
+};
+__device__ __forceinline__ Row row_at(const void* base, uint64_t row, uint32_t pitch) {
+    const char* p = static_cast<const char*>(base) + row * pitch;
+    return Row{p, make_rsrc(p, pitch)};
+}
+template <int DT, bool VEC, int POL>
+__device__ __forceinline__ Unit<DT, VEC> load_unit(const Row& row, uint32_t u, uint32_t units) {
     typedef Unit<DT, VEC> U;
     U x;
     if constexpr (VEC) {
-        const u32x4 v = load16(static_cast<const char*>(row) + uint64_t(u) * 16);
+        const u32x4 v = bload16<POL>(row.r, u * 16);
         __builtin_memcpy(x.v, &v, 16);
     } else {
-        x.v[0] = static_cast<const typename U::T*>(row)[u];
+        x.v[0] = u < units ? reinterpret_cast<const typename U::T*>(row.p)[u] : typename U::T(0);
     }
     return x;
 }
 template <int DT, bool VEC>
-__device__ __forceinline__ void store_unit(void* row, uint32_t u, const Unit<DT, VEC>& x) {
+__device__ __forceinline__ void store_unit(const Row& row, uint32_t u, uint32_t units, const Unit<DT, VEC>& x) {
     typedef Unit<DT, VEC> U;
     if constexpr (VEC) {
         u32x4 v;
         __builtin_memcpy(&v, x.v, 16);
-        store16(static_cast<char*>(row) + uint64_t(u) * 16, v);
-    } else {
-        static_cast<typename U::T*>(row)[u] = x.v[0];
+        bstore16<kPolNT | kPolDevice>(row.r, u * 16, v);
+    } else if (u < units) {
+        const_cast<typename U::T*>(reinterpret_cast<const typename U::T*>(row.p))[u] = x.v[0];
     }
 }
 
@@ -91,29 +102,26 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
     int r = rank_of_row(a.rows, a.nranks, row);
     U w[NV], b[NV], x[NV];
     const bool biased = a.bias[r] != nullptr;
-    const uint64_t pitch = uint64_t(a.cols) * sizeof(T);
+    const uint32_t pitch = a.cols * sizeof(T);
+    {
+        const Row wr = row_at(a.weight[r], 0, pitch), br = row_at(biased ? a.bias[r] : a.weight[r], 0, pitch);
+        const Row xr = row_at(a.x[r], row - a.rows.start[r], pitch);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const uint32_t u = lane + i * L;
-        if (u < units) {
-            w[i] = load_unit<DT, VEC>(a.weight[r], u);
-            if (biased) b[i] = load_unit<DT, VEC>(a.bias[r], u);
+        for (int i = 0; i < NV; i++) {
+            w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L, units);
+            b[i] = load_unit<DT, VEC, 0>(br, lane + i * L, units);
+            x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
         }
     }
-    const char* from = static_cast<const char*>(a.x[r]) + uint64_t(row - a.rows.start[r]) * pitch;
-#pragma unroll
-    for (int i = 0; i < NV; i++)
-        if (lane + i * L < units) x[i] = load_unit<DT, VEC>(from, lane + i * L);
     const float inv = 1.f / float(a.cols);
     for (int parity = 0; row < total; parity ^= 1) {
         float v[NV][E];
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const bool in = lane + i * L < units;
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                v[i][e] = in ? x[i].get(e) : 0.f;
+                v[i][e] = x[i].get(e);
                 s += v[i][e];
             }
         }
@@ -122,10 +130,9 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
         const uint32_t next = row + step;
         if (next < total) {
             while (next >= a.rows.start[r + 1]) r++;
-            from = static_cast<const char*>(a.x[r]) + uint64_t(next - a.rows.start[r]) * pitch;
+            const Row xr = row_at(a.x[r], next - a.rows.start[r], pitch);
 #pragma unroll
-            for (int i = 0; i < NV; i++)
-                if (lane + i * L < units) x[i] = load_unit<DT, VEC>(from, lane + i * L);
+            for (int i = 0; i < NV; i++) x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
         }
         const float mean = row_sum<WPR>(s, cells[parity][0]) * inv;
         float q = 0.f;
@@ -139,17 +146,16 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
             }
         }
         const float rstd = 1.f / sqrtf(row_sum<WPR>(q, cells[parity][1]) * inv + a.eps);
-        char* to = static_cast<char*>(a.y[now]) + local * pitch;
+        const Row to = row_at(a.y[now], local, pitch);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            if (lane + i * L >= units) continue;
             U y;
 #pragma unroll
             for (int e = 0; e < E; e++) {
                 const float n = v[i][e] * rstd * w[i].get(e);
                 y.put(e, biased ? n + b[i].get(e) : n);
             }
-            store_unit<DT, VEC>(to, lane + i * L, y);
+            store_unit<DT, VEC>(to, lane + i * L, units, y);
         }
         if (lane == 0 && a.mean[now] != nullptr) {
             a.mean[now][local] = mean;
@@ -176,16 +182,16 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
     if (row < total) {
         int r = rank_of_row(a.rows, a.nranks, row);
         U w[NV], x[NV], d[NV];
-        const uint64_t pitch = uint64_t(a.cols) * sizeof(T);
+        const uint32_t pitch = a.cols * sizeof(T);
         uint64_t local = row - a.rows.start[r];
         float mean = a.mean[r][local], rstd = a.rstd[r][local];
+        {
+            const Row wr = row_at(a.weight[r], 0, pitch), xr = row_at(a.x[r], local, pitch), dr = row_at(a.dy[r], local, pitch);
 #pragma unroll
-        for (int i = 0; i < NV; i++) {
-            const uint32_t u = lane + i * L;
-            if (u < units) {
-                w[i] = load_unit<DT, VEC>(a.weight[r], u);
-                x[i] = load_unit<DT, VEC>(static_cast<const char*>(a.x[r]) + local * pitch, u);
-                d[i] = load_unit<DT, VEC>(static_cast<const char*>(a.dy[r]) + local * pitch, u);
+            for (int i = 0; i < NV; i++) {
+                w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L, units);
+                x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
+                d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L, units);
             }
         }
         const float inv = 1.f / float(a.cols);
@@ -194,12 +200,12 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
             float s1 = 0.f, s2 = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                const bool in = lane + i * L < units;
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    const float dy = in ? d[i].get(e) : 0.f;
-                    n[i][e] = in ? (x[i].get(e) - mean) * rstd : 0.f;
-                    g[i][e] = in ? dy * w[i].get(e) : 0.f;
+                    // past the row's end dy is 0, and nothing is added to any sum
+                    const float dy = d[i].get(e);
+                    n[i][e] = (x[i].get(e) - mean) * rstd;
+                    g[i][e] = dy * w[i].get(e);
                     s1 += g[i][e];
                     s2 += g[i][e] * n[i][e];
                     dw[i][e] += dy * n[i][e];
@@ -208,20 +214,18 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
             }
             const int now = r;
             const float scale = rstd;
-            char* to = static_cast<char*>(a.dx[now]) + local * pitch;
+            const Row to = row_at(a.dx[now], local, pitch);
             const uint32_t next = row + step;
             if (next < total) {
                 while (next >= a.rows.start[r + 1]) r++;
                 local = next - a.rows.start[r];
                 mean = a.mean[r][local];
                 rstd = a.rstd[r][local];
+                const Row xr = row_at(a.x[r], local, pitch), dr = row_at(a.dy[r], local, pitch);
 #pragma unroll
                 for (int i = 0; i < NV; i++) {
-                    const uint32_t u = lane + i * L;
-                    if (u < units) {
-                        x[i] = load_unit<DT, VEC>(static_cast<const char*>(a.x[r]) + local * pitch, u);
-                        d[i] = load_unit<DT, VEC>(static_cast<const char*>(a.dy[r]) + local * pitch, u);
-                    }
+                    x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
+                    d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L, units);
                 }
             }
             s1 = wave_sum(s1);
@@ -242,11 +246,10 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
             const float m1 = s1 * inv, m2 = s2 * inv;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                if (lane + i * L >= units) continue;
                 U o;
 #pragma unroll
                 for (int e = 0; e < E; e++) o.put(e, scale * (g[i][e] - m1 - n[i][e] * m2));
-                store_unit<DT, VEC>(to, lane + i * L, o);
+                store_unit<DT, VEC>(to, lane + i * L, units, o);
             }
             row = next;
         }
@@ -383,9 +386,19 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBackArgs a) {
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
     float dw = 0.f, db = 0.f;
     if (c < a.cols)
-        for (uint32_t s = wave; s < a.strips; s += 16) {
-            dw += a.partial[(uint64_t(s) * 2) * a.cols + c];
-            db += a.partial[(uint64_t(s) * 2 + 1) * a.cols + c];
+        for (uint32_t s0 = wave; s0 < a.strips; s0 += 16 * 8) {
+            float u[8], v[8];  // eight strips' loads go out before the first is added
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                const uint32_t s = s0 + 16 * k;
+                u[k] = s < a.strips ? a.partial[(uint64_t(s) * 2) * a.cols + c] : 0.f;
+                v[k] = s < a.strips ? a.partial[(uint64_t(s) * 2 + 1) * a.cols + c] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                dw += u[k];
+                db += v[k];
+            }
         }
     sums[0][wave][lane] = dw;
     sums[1][wave][lane] = db;

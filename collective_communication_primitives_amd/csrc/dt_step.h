@@ -80,13 +80,14 @@ hipError_t launch_route_backward(const RouteBackArgs& a, int nranks, int dtype, 
 // -------------------------------------------------------------- exchange --
 // A slot is one (rank, token, choice); slots are numbered in that order.
 constexpr uint32_t kPlanSlots = 2048;  // slots per workgroup of the plan
+constexpr uint32_t kFewSlots = 4096;   // up to here plan and copy are one launch
 struct PlanArgs {
     const int32_t* experts[kMaxRanksHost];
     int32_t* positions[kMaxRanksHost];
     int32_t* offsets[kMaxRanksHost];
     uint32_t capacity[kMaxRanksHost];
     RowTable rows;
-    uint32_t* counts;                  // [plan workgroups][nexperts]
+    uint32_t* counts;                  // [plan workgroups + 1][nexperts]
     uint32_t nexperts, topk, per_rank;
     int nranks;
 };
@@ -107,8 +108,7 @@ struct ExchangeRowsArgs {
     int nranks;
 };
 inline uint32_t plan_blocks(uint64_t slots) { return uint32_t((slots + kPlanSlots - 1) / kPlanSlots); }
-hipError_t launch_plan(const PlanArgs& a, hipStream_t s);
-hipError_t launch_dispatch_rows(const ExchangeRowsArgs& a, int esize, hipStream_t s);
+hipError_t launch_dispatch(const PlanArgs& p, const ExchangeRowsArgs& a, int esize, hipStream_t s);
 hipError_t launch_combine(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
 hipError_t launch_combine_backward(const ExchangeRowsArgs& a, int dtype, hipStream_t s);
 

@@ -13,7 +13,9 @@
 //
 // The choice has to be that of the exact scores: candidates are ordered by
 // the logits themselves where there is no bias (both scores are strictly
-// monotone), and by 64-bit scores where there is one.
+// monotone), and by 64-bit scores where there is one and 32 bits do not tell.
+#include <type_traits>
+
 #include "dt_step_device.h"
 
 namespace dt {
@@ -40,15 +42,13 @@ __device__ __forceinline__ void wave_argmax(double& key, uint32_t& idx) {
     }
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...
+// One token by the whole wave, scores in 64 bits: lane l holds experts l, l +
+// 64, ...  The way for every shape, and for the tokens whose candidates lie
+// too close together for 32 bits.
 template <int DT, int NV>
-__global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks) {
+__device__ __noinline__ void route_row(const RouteArgs& a, int r, uint64_t local) {
     typedef typename Elem<DT>::type T;
-    const uint32_t row = blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-    if (row >= a.rows.start[nranks]) return;
     const uint32_t lane = threadIdx.x & 63;
-    const int r = rank_of_row(a.rows, nranks, row);
-    const uint64_t local = row - a.rows.start[r];
     const T* x = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
     float v[NV];
     double c[NV];
@@ -180,45 +180,285 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks) {
     }
 }
 
+template <int DT, int NV>
+__global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
+    const uint32_t row = blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (row >= a.rows.start[nranks]) return;
+    const int r = rank_of_row(a.rows, nranks, row);
+    route_row<DT, NV>(a, r, row - a.rows.start[r]);
+}
+
+// Reductions over the 16 lanes that share a token, the same value in all of
+// them: neighbours, pairs, halves of eight, then the two eights.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140, kRotate = 0x120;
+template <typename F>
+__device__ __forceinline__ void over16(F&& step) {
+    step(std::integral_constant<int, kSwap1>());
+    step(std::integral_constant<int, kSwap2>());
+    step(std::integral_constant<int, kHalfMirror>());
+    step(std::integral_constant<int, kMirror>());
+}
+// The other 15 lanes' values, one rotation at a time.
+template <typename F>
+__device__ __forceinline__ void rotations(F&& step) {
+    step(std::integral_constant<int, kRotate + 1>());
+    step(std::integral_constant<int, kRotate + 2>());
+    step(std::integral_constant<int, kRotate + 3>());
+    step(std::integral_constant<int, kRotate + 4>());
+    step(std::integral_constant<int, kRotate + 5>());
+    step(std::integral_constant<int, kRotate + 6>());
+    step(std::integral_constant<int, kRotate + 7>());
+    step(std::integral_constant<int, kRotate + 8>());
+    step(std::integral_constant<int, kRotate + 9>());
+    step(std::integral_constant<int, kRotate + 10>());
+    step(std::integral_constant<int, kRotate + 11>());
+    step(std::integral_constant<int, kRotate + 12>());
+    step(std::integral_constant<int, kRotate + 13>());
+    step(std::integral_constant<int, kRotate + 14>());
+    step(std::integral_constant<int, kRotate + 15>());
+}
+__device__ __forceinline__ float max16(float v) {
+    over16([&](auto c) { v = fmaxf(v, dpp<decltype(c)::value>(v)); });
+    return v;
+}
+__device__ __forceinline__ float min16(float v) {
+    over16([&](auto c) { v = fminf(v, dpp<decltype(c)::value>(v)); });
+    return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+    over16([&](auto c) { v += dpp<decltype(c)::value>(v); });
+    return v;
+}
+__device__ __forceinline__ uint32_t min16(uint32_t v) {
+    over16([&](auto c) {
+        const uint32_t o = dpp<decltype(c)::value>(v);
+        v = o < v ? o : v;
+    });
+    return v;
+}
+
+constexpr float kBiggest = 3.402823466e38f;
+
+// The NL logits of a lane's experts [lane * NL, lane * NL + NL), -inf for
+// those that are not there or are NaN.
+template <int DT, int NL>
+__device__ __forceinline__ void load_logits(const void* base, uint64_t row, uint32_t nexperts, uint32_t first, bool vec, float (&x)[NL]) {
+    typedef typename Elem<DT>::type T;
+    const T* p = static_cast<const T*>(base) + row * nexperts + first;
+    constexpr int E = 16 / int(sizeof(T));
+    if (NL >= E && vec && first + NL <= nexperts) {
+#pragma unroll
+        for (int i = 0; i < NL / E; i++) {
+            const u32x4 v = *reinterpret_cast<const u32x4*>(p + i * E);
+            T t[E];
+            __builtin_memcpy(t, &v, 16);
+#pragma unroll
+            for (int e = 0; e < E; e++) x[i * E + e] = Elem<DT>::get(t[e]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? Elem<DT>::get(p[i]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < NL; i++) x[i] = x[i] > -INFINITY ? fminf(x[i], kBiggest) : -INFINITY;
+}
+
+// Four tokens per wave, 16 lanes each; lane l of the 16 holds experts [l * NL, l
+// * NL + NL).  Candidates are ordered by the logits (exact) or by 32-bit
+// scores with a bound `off` on how far such a score may be from the exact one:
+//   sigmoid  s (1 - s) * 2U of the exponential, 2 U of sum and quotient: under 4 U;
+//   softmax  |d| s <= 0.37 of the argument d = x - max, 2 U of the exponential,
+//            20 U of the sum over NL + 4 additions (NL <= 16; 36 for 32), s <= 1: under 42 U;
+//   the bias' addition  U |c|.
+// Where two neighbours in the order, or the last group that stays and the
+// first that goes, are closer than two such bounds, the token is done again in
+// 64 bits: about one in a thousand of normally distributed logits.
+template <int DT, int NL>
+__global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int vec) {
+    const uint32_t total = a.rows.start[nranks], lane = threadIdx.x & 15;
+    const uint32_t row0 = blockIdx.x * (kBlock / 16) + (threadIdx.x >> 4);
+    const bool there = row0 < total;
+    const uint32_t row = there ? row0 : total - 1;  // the last lanes repeat the last token and store nothing
+    int r = 0;
+    while (r + 1 < nranks && row >= a.rows.start[r + 1]) r++;
+    const uint64_t local = row - a.rows.start[r];
+    const uint32_t first = lane * NL;
+    constexpr float U = 5.9604645e-8f;
+    float x[NL], key[NL];
+    load_logits<DT, NL>(a.logits[r], local, a.nexperts, first, vec, x);
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NL; i++) top = fmaxf(top, x[i]);
+    top = max16(top);
+    const bool scored = a.bias != nullptr || a.groups > 1;
+    float sum = 0.f;
+    if (!a.sigmoid && (scored || !a.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            key[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
+            sum += key[i];
+        }
+        sum = sum16(sum);
+    }
+    float off = 0.f;
+    if (scored) {
+        const float inv = a.sigmoid ? 1.f : 1.f / sum;
+        float big = 0.f;
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            const float s = a.sigmoid ? 1.f / (1.f + expf(-x[i])) : key[i] * inv;
+            const float b = a.bias != nullptr && first + i < a.nexperts ? a.bias[first + i] : 0.f;
+            const bool live = x[i] > -INFINITY && b > -INFINITY;
+            key[i] = live ? s + b : -INFINITY;
+            big = fmaxf(big, live ? fabsf(b) : 0.f);
+        }
+        off = (a.sigmoid ? 4.f * U : 42.f * U) + U * (1.f + max16(big));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; i++) key[i] = x[i];
+    }
+    bool close = false;
+    if (a.groups > 1) {
+        // a group is `width` neighbouring lanes, a power of two
+        const uint32_t width = a.nexperts / a.groups / NL, group = lane / width;
+        float m1 = -INFINITY, m2 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            m2 = fmaxf(m2, fminf(m1, key[i]));
+            m1 = fmaxf(m1, key[i]);
+        }
+        uint32_t w = 1;
+        over16([&](auto c) {
+            if (w < width) {
+                const float o1 = dpp<decltype(c)::value>(m1), o2 = dpp<decltype(c)::value>(m2);
+                m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
+                m1 = fmaxf(m1, o1);
+            }
+            w *= 2;
+        });
+        // one expert left in a group: it alone; none: the group goes
+        const float score = m2 > -INFINITY ? m1 + m2 : m1;
+        uint32_t better = 0;
+        rotations([&](auto c) {
+            const float o = dpp<decltype(c)::value>(score);
+            const uint32_t og = dpp<decltype(c)::value>(group);
+            better += og != group && (o > score || (o == score && og < group)) ? 1 : 0;
+        });
+        const bool stays = better < a.topk_groups * width && score > -INFINITY;
+        const float last = min16(stays ? score : INFINITY), next = max16(stays ? -INFINITY : score);
+        close = last - next <= 4.f * off + 2.f * U * fabsf(last);
+#pragma unroll
+        for (int i = 0; i < NL; i++)
+            if (!stays) key[i] = -INFINITY;
+            else if (a.bias == nullptr) key[i] = x[i];  // the logits' own order within the groups that stay
+    }
+    const float gap = a.bias != nullptr ? 2.f * off : -1.f;  // the logits' order is exact
+    uint32_t mine = UINT32_MAX;
+    float before = INFINITY;
+    for (uint32_t k = 0; k <= a.topk; k++) {
+        float best = key[0];
+#pragma unroll
+        for (int i = 1; i < NL; i++) best = fmaxf(best, key[i]);
+        best = max16(best);
+        close = close || (best > -INFINITY && before - best <= gap);
+        if (k == a.topk) break;
+        before = best;
+        uint32_t at = UINT32_MAX;
+#pragma unroll
+        for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? first + i : at;
+        at = best > -INFINITY ? min16(at) : UINT32_MAX;
+#pragma unroll
+        for (int i = 0; i < NL; i++) key[i] = at == first + i ? -INFINITY : key[i];
+        if (lane == k) mine = at;
+    }
+    const bool has = mine != UINT32_MAX;
+    typedef typename Elem<DT>::type T;
+    float logit = -INFINITY;
+    if (has) logit = fminf(Elem<DT>::get(static_cast<const T*>(a.logits[r])[local * a.nexperts + mine]), kBiggest);
+    float s;
+    if (a.renormalize) {
+        const float ctop = max16(logit);
+        s = has ? expf(logit - ctop) : 0.f;
+        if (a.sigmoid && ctop > -60.f) s = has ? 1.f / (1.f + expf(-logit)) : 0.f;
+        const float all = sum16(s);
+        s = has ? s / all : 0.f;
+    } else {
+        s = !has ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / sum;
+    }
+    if (there && !close && lane < a.topk) {
+        a.experts[r][local * a.topk + lane] = has ? int32_t(mine) : -1;
+        a.weights[r][local * a.topk + lane] = s * a.scale;
+    }
+    // the wave's tokens that are too close, one after the other
+    uint64_t todo = __ballot(there && close && lane == 0);
+    while (todo != 0) {
+        const int from = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        const int rr = __builtin_amdgcn_readlane(r, from);
+        const uint32_t at = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(local)), from));
+        route_row<DT, (16 * NL + 63) / 64>(a, rr, at);
+    }
+}
+
 // dlogits of the weights' gradient g_j = dL/dw_j, with a_j the weight before
 // the scale and g'_j = scale g_j:
 //   renormalised: t_j = a_j (g'_j - sum_i g'_i a_i); softmax: dx_{e_j} += t_j
 //                 (the normaliser cancels), sigmoid: dx_{e_j} += t_j (1 - s_j)
 //   otherwise:    softmax: dx_e = s_e (sum_{j: e_j = e} g'_j - sum_i g'_i s_i),
 //                 sigmoid: dx_{e_j} += g'_j s_j (1 - s_j)
-template <int DT, int NV>
-__global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int nranks) {
+// L lanes per token (16 where topk and the experts fit, else the wave), NL
+// neighbouring experts each.
+template <int L>
+__device__ __forceinline__ float sum_lanes(float v) {
+    if constexpr (L == 16) return sum16(v);
+    else return wave_sum(v);
+}
+template <int L>
+__device__ __forceinline__ float max_lanes(float v) {
+    if constexpr (L == 16) return max16(v);
+    else return wave_max(v);
+}
+template <int DT, int NL, int L>
+__global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int nranks, int vec) {
     typedef typename Elem<DT>::type T;
-    const uint32_t row = blockIdx.x * (kBlock / 64) + (threadIdx.x >> 6);
-    if (row >= a.rows.start[nranks]) return;
-    const uint32_t lane = threadIdx.x & 63;
-    const int r = rank_of_row(a.rows, nranks, row);
+    const uint32_t total_rows = a.rows.start[nranks], lane = threadIdx.x % L;
+    const uint32_t row0 = blockIdx.x * (kBlock / L) + threadIdx.x / L;
+    const bool there = row0 < total_rows;
+    const uint32_t row = there ? row0 : total_rows - 1;
+    int r = 0;
+    while (r + 1 < nranks && row >= a.rows.start[r + 1]) r++;
     const uint64_t local = row - a.rows.start[r];
-    const T* x = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
-    T* dx = static_cast<T*>(a.dlogits[r]) + local * a.nexperts;
-    float v[NV];
-    float top = -INFINITY;
+    const uint32_t first = lane * NL;
+    const bool dense = !a.sigmoid && !a.renormalize;
+    float s[NL];
+    float top = -INFINITY, total = 0.f;
+    if (dense) {
+        load_logits<DT, NL>(a.logits[r], local, a.nexperts, first, vec, s);
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const uint32_t e = lane + 64 * i;
-        v[i] = e < a.nexperts ? Elem<DT>::get(x[e]) : -INFINITY;
-        v[i] = v[i] > -INFINITY ? fminf(v[i], 3.402823466e38f) : -INFINITY;
-        top = fmaxf(top, v[i]);
-    }
-    top = wave_max(top);
-    float total = 0.f;
-    if (!a.sigmoid && !a.renormalize) {
+        for (int i = 0; i < NL; i++) top = fmaxf(top, s[i]);
+        top = max_lanes<L>(top);
 #pragma unroll
-        for (int i = 0; i < NV; i++) total += v[i] > -INFINITY ? expf(v[i] - top) : 0.f;
-        total = wave_sum(total);
+        for (int i = 0; i < NL; i++) {
+            s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.f;
+            total += s[i];
+        }
+        total = sum_lanes<L>(total);
     }
     // lane j: choice j's logit and gradient
     int32_t e = lane < a.topk ? a.experts[r][local * a.topk + lane] : -1;
     float g = 0.f, logit = -INFINITY;
     if (e >= 0 && uint32_t(e) < a.nexperts) {
         g = a.dweights[r][local * a.topk + lane] * a.scale;
-        const float l = Elem<DT>::get(x[e]);
-        logit = l > -INFINITY ? fminf(l, 3.402823466e38f) : -INFINITY;
+        const float l = Elem<DT>::get(static_cast<const T*>(a.logits[r])[local * a.nexperts + e]);
+        logit = l > -INFINITY ? fminf(l, kBiggest) : -INFINITY;
     }
     const bool has = logit > -INFINITY;
     if (!has) {
@@ -228,233 +468,546 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
     float t;  // what choice j adds to its expert
     float all = 0.f;
     if (a.renormalize) {
-        const float ctop = wave_max(logit);
-        float s = has ? expf(logit - ctop) : 0.f;
-        if (a.sigmoid && ctop > -60.f) s = has ? 1.f / (1.f + expf(-logit)) : 0.f;
-        const float sum = wave_sum(s);
-        const float w = has ? s / sum : 0.f;
-        t = w * (g - wave_sum(g * w));
+        const float ctop = max_lanes<L>(logit);
+        float w = has ? expf(logit - ctop) : 0.f;
+        if (a.sigmoid && ctop > -60.f) w = has ? 1.f / (1.f + expf(-logit)) : 0.f;
+        const float sum = sum_lanes<L>(w);
+        w = has ? w / sum : 0.f;
+        t = w * (g - sum_lanes<L>(g * w));
         if (a.sigmoid && has) t *= 1.f / (1.f + expf(logit));
     } else if (a.sigmoid) {
         t = has ? g / (1.f + expf(-logit)) / (1.f + expf(logit)) : 0.f;
     } else {
-        const float s = has ? expf(logit - top) / total : 0.f;
-        all = wave_sum(g * s);
+        all = sum_lanes<L>(has ? g * (expf(logit - top) / total) : 0.f);
         t = g;
     }
-    float d[NV];
+    float d[NL];
 #pragma unroll
-    for (int i = 0; i < NV; i++) d[i] = 0.f;
+    for (int i = 0; i < NL; i++) d[i] = 0.f;
+    const int base = int(threadIdx.x & 63) - int(lane);
     for (uint32_t k = 0; k < a.topk; k++) {
-        const int32_t ek = __shfl(e, int(k));
-        const float tk = __shfl(t, int(k));
+        const uint32_t at = uint32_t(__shfl(e, base + int(k))) - first;  // huge when it is not this lane's
+        const float tk = __shfl(t, base + int(k));
 #pragma unroll
-        for (int i = 0; i < NV; i++)
-            if (ek == int32_t(lane + 64 * i)) d[i] += tk;
+        for (int i = 0; i < NL; i++) d[i] += at == uint32_t(i) ? tk : 0.f;
     }
+    if (dense) {
+        const float inv = total > 0.f ? 1.f / total : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; i++) {
-        const uint32_t c = lane + 64 * i;
-        if (c >= a.nexperts) continue;
-        if (!a.sigmoid && !a.renormalize) d[i] = v[i] > -INFINITY ? expf(v[i] - top) / total * (d[i] - all) : 0.f;
-        dx[c] = Elem<DT>::put(d[i]);
+        for (int i = 0; i < NL; i++) d[i] = s[i] * inv * (d[i] - all);
+    }
+    if (!there || first >= a.nexperts) return;
+    T* dx = static_cast<T*>(a.dlogits[r]) + local * a.nexperts + first;
+    constexpr int E = 16 / int(sizeof(T));
+    if (NL >= E && vec && first + NL <= a.nexperts) {
+#pragma unroll
+        for (int i = 0; i < NL / E; i++) {
+            T o[E];
+#pragma unroll
+            for (int k = 0; k < E; k++) o[k] = Elem<DT>::put(d[i * E + k]);
+            u32x4 v;
+            __builtin_memcpy(&v, o, 16);
+            *reinterpret_cast<u32x4*>(dx + i * E) = v;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NL; i++)
+            if (first + i < a.nexperts) dx[i] = Elem<DT>::put(d[i]);
     }
 }
 
 // --------------------------------------------------------------- exchange --
-// The plan is a stable counting sort of the slots by expert, over all ranks:
-// count per workgroup, scan, place.  Slot order (rank, token, choice) is kept
-// within an expert, so the rows' order does not depend on timing.
-__device__ __forceinline__ int32_t slot_expert(const PlanArgs& a, uint64_t slot, uint64_t slots) {
+// The plan is a stable counting sort of the slots by expert, over all ranks.
+// Slot order (rank, token, choice) is kept within an expert, so the rows' order
+// does not depend on timing.
+__device__ __forceinline__ int32_t slot_expert(const PlanArgs& a, uint32_t slot, uint32_t slots) {
     if (slot >= slots) return -1;
-    const uint32_t row = uint32_t(slot / a.topk);
-    const int r = rank_of_row(a.rows, a.nranks, row);
-    const int32_t e = a.experts[r][slot - uint64_t(a.rows.start[r]) * a.topk];
+    const uint32_t row = slot / a.topk;
+    int r = 0;
+    while (r + 1 < a.nranks && row >= a.rows.start[r + 1]) r++;
+    const int32_t e = a.experts[r][slot - a.rows.start[r] * a.topk];
     return e >= 0 && uint32_t(e) < a.nexperts ? e : -1;
 }
+__device__ __forceinline__ void store_position(const PlanArgs& a, uint32_t slot, int32_t e, uint32_t pos) {
+    const uint32_t row = slot / a.topk;
+    int r = 0;
+    while (r + 1 < a.nranks && row >= a.rows.start[r + 1]) r++;
+    const bool kept = e >= 0 && pos < a.capacity[uint32_t(e) / a.per_rank];
+    a.positions[r][slot - a.rows.start[r] * a.topk] = kept ? int32_t(pos) : -1;
+}
+// total[e]: slots of expert e over all ranks.  Each expert's first row, and the
+// end, to its rank's offsets.
+__device__ __forceinline__ void store_offsets(const PlanArgs& a, const uint32_t* total) {
+    for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBlock) {
+        const uint32_t q = e / a.per_rank, cap = a.capacity[q];
+        uint32_t base = 0;
+        for (uint32_t f = q * a.per_rank; f < e; f++) base += total[f];
+        a.offsets[q][e - q * a.per_rank] = int32_t(base < cap ? base : cap);
+        base += total[e];
+        if (e + 1 == (q + 1) * a.per_rank) a.offsets[q][a.per_rank] = int32_t(base < cap ? base : cap);
+    }
+}
 
+// counts[b][e]: slots of expert e in workgroup b's share.
 __global__ __launch_bounds__(kBlock) void k_plan_count(PlanArgs a) {
     __shared__ uint32_t hist[DT_MAX_EXPERTS];
-    const uint64_t slots = uint64_t(a.rows.start[a.nranks]) * a.topk;
+    const uint32_t slots = a.rows.start[a.nranks] * a.topk;
     for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBlock) hist[e] = 0;
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < kPlanSlots; i += kBlock) {
-        const int32_t e = slot_expert(a, uint64_t(blockIdx.x) * kPlanSlots + i, slots);
+        const int32_t e = slot_expert(a, blockIdx.x * kPlanSlots + i, slots);
         if (e >= 0) atomicAdd(&hist[e], 1u);
     }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBlock) a.counts[uint64_t(blockIdx.x) * a.nexperts + e] = hist[e];
 }
 
-// One workgroup: counts[b][e] becomes the row, in the expert's rank, of the
-// first slot of workgroup b for expert e; offsets get the experts' first rows.
-__global__ __launch_bounds__(1024) void k_plan_scan(PlanArgs a, uint32_t blocks) {
-    __shared__ uint32_t total[DT_MAX_EXPERTS];
-    const uint32_t e = threadIdx.x;
-    uint32_t sum = 0;
-    if (e < a.nexperts)
-        for (uint32_t b = 0; b < blocks; b++) sum += a.counts[uint64_t(b) * a.nexperts + e];
-    total[e] = sum;
-    __syncthreads();
+// Many workgroups: counts[b][e] becomes the number of expert e's slots in the
+// workgroups before b, and row `blocks` of counts their number in all.
+__global__ __launch_bounds__(64) void k_plan_scan(PlanArgs a, uint32_t blocks) {
+    const uint32_t e = blockIdx.x * 64 + threadIdx.x;
     if (e >= a.nexperts) return;
-    const uint32_t q = e / a.per_rank;
-    uint32_t base = 0;
-    for (uint32_t f = q * a.per_rank; f < e; f++) base += total[f];
-    const uint32_t cap = a.capacity[q];
-    a.offsets[q][e - q * a.per_rank] = int32_t(base < cap ? base : cap);
-    if (e + 1 == (q + 1) * a.per_rank) a.offsets[q][a.per_rank] = int32_t(base + sum < cap ? base + sum : cap);
-    for (uint32_t b = 0; b < blocks; b++) {
-        const uint64_t at = uint64_t(b) * a.nexperts + e;
-        const uint32_t n = a.counts[at];
-        a.counts[at] = base;
-        base += n;
+    uint32_t sum = 0;
+    for (uint32_t b0 = 0; b0 < blocks; b0 += 16) {
+        uint32_t n[16];
+#pragma unroll
+        for (int i = 0; i < 16; i++) n[i] = b0 + i < blocks ? a.counts[uint64_t(b0 + i) * a.nexperts + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+            if (b0 + i < blocks) a.counts[uint64_t(b0 + i) * a.nexperts + e] = sum;
+            sum += n[i];
+        }
     }
+    a.counts[uint64_t(blocks) * a.nexperts + e] = sum;
 }
 
-// Each wave takes a quarter of the workgroup's slots, 64 at a time in order;
-// a slot's row is its expert's next row plus the equal experts in lower lanes.
-__global__ __launch_bounds__(kBlock) void k_plan_place(PlanArgs a) {
+// Each wave takes a quarter of the workgroup's slots, 64 at a time in order; a
+// slot's row is its expert's next row plus the equal experts in lower lanes.
+// Without a scan each workgroup adds up the counts before its own by itself.
+__global__ __launch_bounds__(kBlock) void k_plan_place(PlanArgs a, uint32_t blocks, int scanned) {
     __shared__ uint32_t next[kBlock / 64][DT_MAX_EXPERTS];
-    const uint64_t slots = uint64_t(a.rows.start[a.nranks]) * a.topk;
+    __shared__ uint32_t total[DT_MAX_EXPERTS];
+    const uint32_t slots = a.rows.start[a.nranks] * a.topk;
     const uint32_t wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     constexpr uint32_t kPer = kPlanSlots / (kBlock / 64);
     for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBlock)
         for (int w = 0; w < kBlock / 64; w++) next[w][e] = 0;
     __syncthreads();
-    const uint64_t first = uint64_t(blockIdx.x) * kPlanSlots + wave * kPer;
-    for (uint32_t i = lane; i < kPer; i += 64) {
-        const int32_t e = slot_expert(a, first + i, slots);
-        if (e >= 0) atomicAdd(&next[wave][e], 1u);
+    const uint32_t first = blockIdx.x * kPlanSlots + wave * kPer;
+    int32_t ex[kPer / 64];
+#pragma unroll
+    for (uint32_t i = 0; i < kPer / 64; i++) ex[i] = slot_expert(a, first + i * 64 + lane, slots);
+#pragma unroll
+    for (uint32_t i = 0; i < kPer / 64; i++)
+        if (ex[i] >= 0) atomicAdd(&next[wave][ex[i]], 1u);
+    // slots of the experts in the workgroups before this one, and in all
+    uint32_t before[DT_MAX_EXPERTS / kBlock];
+#pragma unroll
+    for (uint32_t i = 0; i < DT_MAX_EXPERTS / kBlock; i++) {
+        const uint32_t e = threadIdx.x + i * kBlock;
+        before[i] = 0;
+        if (e >= a.nexperts) continue;
+        uint32_t all = 0;
+        if (scanned) {
+            before[i] = a.counts[uint64_t(blockIdx.x) * a.nexperts + e];
+            all = a.counts[uint64_t(blocks) * a.nexperts + e];
+        } else {
+            for (uint32_t b0 = 0; b0 < blocks; b0 += 16) {
+                uint32_t n[16];
+#pragma unroll
+                for (int k = 0; k < 16; k++) n[k] = b0 + k < blocks ? a.counts[uint64_t(b0 + k) * a.nexperts + e] : 0;
+#pragma unroll
+                for (int k = 0; k < 16; k++) {
+                    all += n[k];
+                    if (b0 + k < blockIdx.x) before[i] += n[k];
+                }
+            }
+        }
+        total[e] = all;
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.nexperts; e += kBlock) {
-        uint32_t at = a.counts[uint64_t(blockIdx.x) * a.nexperts + e];
+#pragma unroll
+    for (uint32_t i = 0; i < DT_MAX_EXPERTS / kBlock; i++) {
+        const uint32_t e = threadIdx.x + i * kBlock;
+        if (e >= a.nexperts) continue;
+        uint32_t at = before[i];
+        for (uint32_t f = e / a.per_rank * a.per_rank; f < e; f++) at += total[f];
         for (int w = 0; w < kBlock / 64; w++) {
             const uint32_t n = next[w][e];
             next[w][e] = at;
             at += n;
         }
     }
+    if (blockIdx.x == 0) store_offsets(a, total);
     __syncthreads();
-    for (uint32_t i = lane; i < kPer; i += 64) {
-        const uint64_t slot = first + i;
-        const int32_t e = slot_expert(a, slot, slots);
+    volatile uint32_t* mine = next[wave];
+#pragma unroll
+    for (uint32_t i = 0; i < kPer / 64; i++) {
+        const int32_t e = ex[i];
         uint64_t same = __ballot(e >= 0);
         for (uint32_t b = 1; b < a.nexperts; b <<= 1) {
             const uint64_t set = __ballot(e >= 0 && (uint32_t(e) & b));
             same &= (uint32_t(e) & b) ? set : ~set;
         }
-        const uint32_t before = uint32_t(__popcll(same & ((1ull << lane) - 1)));
+        const uint32_t before_me = uint32_t(__popcll(same & ((1ull << lane) - 1)));
         uint32_t pos = 0;
-        if (e >= 0) pos = next[wave][e] + before;
+        if (e >= 0) pos = mine[e] + before_me;
         __builtin_amdgcn_wave_barrier();
-        if (e >= 0 && before == 0) next[wave][e] += uint32_t(__popcll(same));
+        if (e >= 0 && before_me == 0) mine[e] = pos + uint32_t(__popcll(same));
         __builtin_amdgcn_wave_barrier();
-        if (slot < slots) {
-            const int r = rank_of_row(a.rows, a.nranks, uint32_t(slot / a.topk));
-            const bool kept = e >= 0 && pos < a.capacity[uint32_t(e) / a.per_rank];
-            a.positions[r][slot - uint64_t(a.rows.start[r]) * a.topk] = kept ? int32_t(pos) : -1;
-        }
+        const uint32_t slot = first + i * 64 + lane;
+        if (slot < slots) store_position(a, slot, e, pos);
     }
 }
 
 // Where slot j of a token lives: the owner rank and its row, or no row at all.
-__device__ __forceinline__ bool slot_row(const ExchangeRowsArgs& a, int r, uint64_t slot, uint32_t& q, uint32_t& pos) {
-    const int32_t e = a.experts[r][slot], p = a.positions[r][slot];
+__device__ __forceinline__ bool slot_row(const ExchangeRowsArgs& a, int32_t e, int32_t p, uint32_t& q, uint32_t& pos) {
     if (e < 0 || uint32_t(e) >= a.nexperts || p < 0) return false;
     q = uint32_t(e) / a.per_rank;
     pos = uint32_t(p);
     return pos < a.capacity[q];
 }
 
-template <typename T>
-__global__ __launch_bounds__(kBlock) void k_dispatch_rows(ExchangeRowsArgs a) {
-    const uint32_t row = blockIdx.x;
-    const int r = rank_of_row(a.rows, a.nranks, row);
-    const uint64_t local = row - a.rows.start[r];
-    const T* src = static_cast<const T*>(a.tokens_in[r]) + local * a.cols;
-    for (uint32_t j = 0; j < a.topk; j++) {
+// The choices of one token: lane j of the wave knows choice j's row.  `rows`
+// holds, for choice j with a row, its address; kept is the set of those.
+struct Choices {
+    uint64_t at;     // lane j: the row's address in the expert rank's buffer
+    uint64_t kept;   // bit j: choice j has a row (the same in all lanes)
+};
+__device__ __forceinline__ const char* choice_row(const Choices& c, int j) {
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(c.at)), j));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(c.at >> 32)), j));
+    return reinterpret_cast<const char*>(uint64_t(hi) << 32 | lo);
+}
+template <typename P>
+__device__ __forceinline__ Choices choices(const ExchangeRowsArgs& a, P* const (&buffers)[kMaxRanksHost], int r, uint64_t local,
+                                           uint32_t pitch) {
+    const uint32_t lane = threadIdx.x & 63;
+    Choices c = {0, 0};
+    bool kept = false;
+    if (lane < a.topk) {
+        const uint64_t slot = local * a.topk + lane;
         uint32_t q, pos;
-        if (!slot_row(a, r, local * a.topk + j, q, pos)) continue;
-        T* dst = static_cast<T*>(a.rows_out[q]) + uint64_t(pos) * a.cols;
-        for (uint32_t c = threadIdx.x; c < a.cols; c += kBlock) dst[c] = src[c];
+        kept = slot_row(a, a.experts[r][slot], a.positions[r][slot], q, pos);
+        if (kept) c.at = reinterpret_cast<uint64_t>(buffers[q]) + uint64_t(pos) * pitch;
+    }
+    c.kept = __ballot(kept);
+    return c;
+}
+
+// A token's row is worked on by WPT waves (1 for short rows, 4 for long ones),
+// NV units per lane at a time: 16-byte vectors, or single elements where rows
+// are off the 16-byte boundaries.
+template <int ES, bool VEC>
+struct RowUnit {
+    static constexpr int bytes = VEC ? 16 : ES;
+    typedef typename std::conditional<VEC, u32x4, typename std::conditional<ES == 2, uint16_t, uint32_t>::type>::type type;
+};
+template <typename X>
+__device__ __forceinline__ X load_at(const char* row, uint32_t u) {
+    return __builtin_nontemporal_load(reinterpret_cast<const X*>(row) + u);
+}
+template <typename X>
+__device__ __forceinline__ void store_at(const char* row, uint32_t u, X v) {
+    __builtin_nontemporal_store(v, reinterpret_cast<X*>(const_cast<char*>(row)) + u);
+}
+
+template <int ES, bool VEC, int WPT>
+__device__ __forceinline__ void dispatch_row(const char* src, uint32_t units, const Choices& c, uint32_t lane) {
+    typedef typename RowUnit<ES, VEC>::type X;
+    constexpr int NV = 4, L = 64 * WPT;
+    for (uint32_t u0 = lane; u0 < units; u0 += NV * L) {
+        X x[NV];
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (u0 + i * L < units) x[i] = load_at<X>(src, u0 + i * L);
+        for (uint64_t m = c.kept; m != 0; m &= m - 1) {
+            const char* to = choice_row(c, __builtin_ctzll(m));
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (u0 + i * L < units) store_at<X>(to, u0 + i * L, x[i]);
+        }
     }
 }
 
-// out[t] = sum_j w_tj y[owner][pos_tj], in slot order, fp32, one rounding.
-template <int DT>
-__global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
-    typedef typename Elem<DT>::type T;
-    const uint32_t row = blockIdx.x;
+// The token of this wave (WPT 1) or workgroup, or none.
+template <int WPT>
+__device__ __forceinline__ uint32_t token_of() {
+    return WPT == 1 ? blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : blockIdx.x;
+}
+
+template <int ES, bool VEC, int WPT>
+__global__ __launch_bounds__(kBlock) void k_dispatch_rows(ExchangeRowsArgs a) {
+    const uint32_t row = token_of<WPT>();
+    if (row >= a.rows.start[a.nranks]) return;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
-    T* out = static_cast<T*>(a.tokens_out[r]) + local * a.cols;
-    for (uint32_t c = threadIdx.x; c < a.cols; c += kBlock) {
-        float s = 0.f;
-        for (uint32_t j = 0; j < a.topk; j++) {
-            uint32_t q, pos;
-            if (!slot_row(a, r, local * a.topk + j, q, pos)) continue;
-            const float w = a.weights[r] != nullptr ? a.weights[r][local * a.topk + j] : 1.f;
-            s += w * Elem<DT>::get(static_cast<const T*>(a.rows_in[q])[uint64_t(pos) * a.cols + c]);
+    const uint32_t pitch = a.cols * ES;
+    const Choices c = choices(a, a.rows_out, r, local, pitch);
+    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch / RowUnit<ES, VEC>::bytes, c,
+                               threadIdx.x % (64 * WPT));
+}
+
+// Few slots: plan and copy in one launch.  Every workgroup finds the rows of
+// its own tokens' slots by itself, from all slots: slot s of expert e comes
+// behind the slots of its rank's lower experts and behind the earlier slots of
+// e.  The workgroup behind the last one writes the offsets.
+template <int ES, bool VEC, int WPT>
+__global__ __launch_bounds__(kBlock) void k_dispatch_few(ExchangeRowsArgs a, PlanArgs p) {
+    __shared__ uint32_t shared[DT_MAX_EXPERTS];
+    const uint32_t tokens = a.rows.start[a.nranks], slots = tokens * a.topk;
+    if (blockIdx.x + 1 == gridDim.x) {
+        for (uint32_t e = threadIdx.x; e < p.nexperts; e += kBlock) shared[e] = 0;
+        __syncthreads();
+        for (uint32_t s = threadIdx.x; s < slots; s += kBlock) {
+            const int32_t e = slot_expert(p, s, slots);
+            if (e >= 0) atomicAdd(&shared[e], 1u);
         }
-        out[c] = Elem<DT>::put(s);
+        __syncthreads();
+        store_offsets(p, shared);
+        return;
+    }
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const uint32_t row = token_of<WPT>();
+    const bool there = row < tokens;
+    const uint32_t own = there ? row * a.topk : 0;  // the token's first slot
+    const int32_t mine = there && lane < a.topk ? slot_expert(p, own + lane, slots) : -1;
+    uint32_t pos = 0;  // lane j: the row of choice j
+    // a wave takes all slots (WPT 1), or the workgroup's waves share them
+    for (uint32_t s0 = WPT == 1 ? 0 : wave * 64; there && s0 < slots; s0 += 64 * WPT) {
+        const uint32_t s = s0 + lane;
+        const int32_t e = slot_expert(p, s, slots);
+        for (uint32_t j = 0; j < a.topk; j++) {
+            const int32_t ej = __builtin_amdgcn_readlane(mine, int(j));
+            if (ej < 0) continue;
+            const int32_t lowest = ej - int32_t(uint32_t(ej) % a.per_rank);
+            const uint64_t m = __ballot((e >= lowest && e < ej) || (e == ej && s < own + j));
+            if (lane == j) pos += uint32_t(__popcll(m));
+        }
+    }
+    if constexpr (WPT > 1) {
+        shared[threadIdx.x] = pos;
+        __syncthreads();
+        pos = 0;
+#pragma unroll
+        for (int w = 0; w < WPT; w++) pos += shared[w * 64 + lane];
+    }
+    if (!there) return;
+    const int r = rank_of_row(a.rows, a.nranks, row);
+    const uint64_t local = row - a.rows.start[r];
+    const uint32_t pitch = a.cols * ES;
+    Choices c = {0, 0};
+    bool kept = false;
+    if (lane < a.topk) {
+        const uint32_t q = mine >= 0 ? uint32_t(mine) / a.per_rank : 0;
+        kept = mine >= 0 && pos < a.capacity[q];
+        if (kept) c.at = reinterpret_cast<uint64_t>(a.rows_out[q]) + uint64_t(pos) * pitch;
+        if (WPT == 1 || wave == 0) p.positions[r][local * a.topk + lane] = kept ? int32_t(pos) : -1;
+    }
+    c.kept = __ballot(kept);
+    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch / RowUnit<ES, VEC>::bytes, c,
+                               threadIdx.x % (64 * WPT));
+}
+
+// The elements of a unit as fp32.
+template <int DT, bool VEC>
+struct Values {
+    static constexpr int ES = DT == kBF16 ? 2 : 4, n = VEC ? 16 / ES : 1;
+    typedef typename RowUnit<ES, VEC>::type X;
+    typedef typename Elem<DT>::type T;
+    static __device__ __forceinline__ void get(X x, float (&f)[n]) {
+        T t[n];
+        __builtin_memcpy(t, &x, sizeof t);
+#pragma unroll
+        for (int i = 0; i < n; i++) f[i] = Elem<DT>::get(t[i]);
+    }
+    static __device__ __forceinline__ X put(const float (&f)[n]) {
+        T t[n];
+#pragma unroll
+        for (int i = 0; i < n; i++) t[i] = Elem<DT>::put(f[i]);
+        X x;
+        __builtin_memcpy(&x, t, sizeof t);
+        return x;
+    }
+};
+
+// out[t] = sum_j w_tj y[owner][pos_tj], in slot order, fp32, one rounding.  The
+// rows of up to four choices are on their way at a time.
+template <int DT, bool VEC, int WPT>
+__global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
+    typedef Values<DT, VEC> V;
+    typedef typename V::X X;
+    constexpr int NV = 2, L = 64 * WPT, AHEAD = 4;
+    const uint32_t row = token_of<WPT>();
+    if (row >= a.rows.start[a.nranks]) return;
+    const int r = rank_of_row(a.rows, a.nranks, row);
+    const uint64_t local = row - a.rows.start[r];
+    const uint32_t pitch = a.cols * V::ES, units = pitch / uint32_t(sizeof(X)), lane = threadIdx.x & 63;
+    const Choices c = choices(a, a.rows_in, r, local, pitch);
+    float w = 1.f;
+    if (a.weights[r] != nullptr && lane < a.topk) w = a.weights[r][local * a.topk + lane];
+    const char* out = static_cast<const char*>(a.tokens_out[r]) + local * pitch;
+    for (uint32_t u0 = threadIdx.x % L; u0 < units; u0 += NV * L) {
+        float s[NV][V::n];
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+#pragma unroll
+            for (int e = 0; e < V::n; e++) s[i][e] = 0.f;
+        for (uint64_t m = c.kept; m != 0;) {
+            X x[AHEAD][NV];
+            float wj[AHEAD];
+            bool got[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; k++) {
+                got[k] = m != 0;
+                if (!got[k]) continue;
+                const int j = __builtin_ctzll(m);
+                m &= m - 1;
+                wj[k] = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(w)), j)));
+                const char* y = choice_row(c, j);
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+                    if (u0 + i * L < units) x[k][i] = load_at<X>(y, u0 + i * L);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; k++) {
+                if (!got[k]) continue;
+#pragma unroll
+                for (int i = 0; i < NV; i++) {
+                    float f[V::n];
+                    V::get(x[k][i], f);
+#pragma unroll
+                    for (int e = 0; e < V::n; e++) s[i][e] += wj[k] * f[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; i++)
+            if (u0 + i * L < units) store_at<X>(out, u0 + i * L, V::put(s[i]));
     }
 }
 
 // dy[owner][pos] = w dout[t];  dw = <dout[t], y[owner][pos]>.
-template <int DT>
+template <int DT, bool VEC, int WPT>
 __global__ __launch_bounds__(kBlock) void k_combine_backward(ExchangeRowsArgs a) {
-    typedef typename Elem<DT>::type T;
-    __shared__ float tmp[kBlock / 64];
-    const uint32_t row = blockIdx.x;
+    typedef Values<DT, VEC> V;
+    typedef typename V::X X;
+    constexpr int NV = VEC ? 2 : 8, L = 64 * WPT;
+    __shared__ float dots[kBlock / 64][64];
+    const uint32_t row = token_of<WPT>(), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (row >= a.rows.start[a.nranks]) return;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
-    const T* g = static_cast<const T*>(a.tokens_in[r]) + local * a.cols;
-    for (uint32_t j = 0; j < a.topk; j++) {
-        uint32_t q, pos;
-        const uint64_t slot = local * a.topk + j;
-        if (!slot_row(a, r, slot, q, pos)) {
-            if (threadIdx.x == 0) a.dweights[r][slot] = 0.f;
-            continue;
+    const uint32_t pitch = a.cols * V::ES, units = pitch / uint32_t(sizeof(X));
+    const Choices from = choices(a, a.rows_in, r, local, pitch), to = choices(a, a.rows_out, r, local, pitch);
+    float w = 0.f;
+    if (lane < a.topk) w = a.weights[r][local * a.topk + lane];
+    const char* g = static_cast<const char*>(a.tokens_in[r]) + local * pitch;
+    float dot = 0.f;  // lane j: this wave's part of choice j's
+    for (uint32_t u0 = threadIdx.x % L; u0 - threadIdx.x % L < units; u0 += NV * L) {
+        float gf[NV][V::n];
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+#pragma unroll
+            for (int e = 0; e < V::n; e++) gf[i][e] = 0.f;
+            if (u0 + i * L < units) V::get(load_at<X>(g, u0 + i * L), gf[i]);
         }
-        const float w = a.weights[r][slot];
-        const T* y = static_cast<const T*>(a.rows_in[q]) + uint64_t(pos) * a.cols;
-        T* dy = static_cast<T*>(a.rows_out[q]) + uint64_t(pos) * a.cols;
-        float s = 0.f;
-        for (uint32_t c = threadIdx.x; c < a.cols; c += kBlock) {
-            const float gc = Elem<DT>::get(g[c]);
-            s += gc * Elem<DT>::get(y[c]);
-            dy[c] = Elem<DT>::put(w * gc);
+        for (uint64_t m = from.kept; m != 0; m &= m - 1) {
+            const int j = __builtin_ctzll(m);
+            const float wj = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(w)), j)));
+            const char* y = choice_row(from, j);
+            const char* dy = choice_row(to, j);
+            X x[NV];
+#pragma unroll
+            for (int i = 0; i < NV; i++)
+                if (u0 + i * L < units) x[i] = load_at<X>(y, u0 + i * L);
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < NV; i++) {
+                if (u0 + i * L >= units) continue;
+                float f[V::n], o[V::n];
+                V::get(x[i], f);
+#pragma unroll
+                for (int e = 0; e < V::n; e++) {
+                    s += gf[i][e] * f[e];
+                    o[e] = wj * gf[i][e];
+                }
+                store_at<X>(dy, u0 + i * L, V::put(o));
+            }
+            s = wave_sum(s);
+            if (lane == uint32_t(j)) dot += s;
         }
-        s = block_sum<kBlock / 64>(s, tmp);
-        if (threadIdx.x == 0) a.dweights[r][slot] = s;
-        __syncthreads();
     }
+    if constexpr (WPT > 1) {
+        dots[wave][lane] = dot;
+        __syncthreads();
+        if (wave > 0) return;
+        dot = 0.f;
+#pragma unroll
+        for (int k = 0; k < WPT; k++) dot += dots[k][lane];
+    }
+    if (lane < a.topk) a.dweights[r][local * a.topk + lane] = dot;
+}
+
+// Lanes per token and experts per lane: 16 lanes for up to 512 experts and 16
+// choices; with groups a group has to be whole lanes, a power of two of them.
+int lane_experts(uint32_t nexperts, uint32_t topk, uint32_t groups) {
+    if (topk > 16 || nexperts > 512) return 0;
+    const int nl = nexperts <= 64 ? 4 : nexperts <= 128 ? 8 : nexperts <= 256 ? 16 : 32;
+    if (groups > 1) {
+        const uint32_t per = nexperts / groups, width = per / nl;
+        if (per % nl != 0 || (width & (width - 1)) != 0 || nexperts != uint32_t(16 * nl) || width > 8) return 0;
+    }
+    return nl;
+}
+bool vector_rows(const void* const* list, int n, uint32_t elems, int dtype) {
+    if (elems * (dtype == kBF16 ? 2 : 4) % 16 != 0) return false;
+    for (int r = 0; r < n; r++)
+        if (reinterpret_cast<uintptr_t>(list[r]) % 16 != 0) return false;
+    return true;
 }
 
 template <int DT>
 hipError_t route(const RouteArgs& a, int nranks, hipStream_t s) {
-    const dim3 grid((a.rows.start[nranks] + kBlock / 64 - 1) / (kBlock / 64)), block(kBlock);
-    const uint32_t nv = (a.nexperts + 63) / 64;
-    if (nv <= 1) hipLaunchKernelGGL((k_route<DT, 1>), grid, block, 0, s, a, nranks);
-    else if (nv <= 2) hipLaunchKernelGGL((k_route<DT, 2>), grid, block, 0, s, a, nranks);
-    else if (nv <= 4) hipLaunchKernelGGL((k_route<DT, 4>), grid, block, 0, s, a, nranks);
-    else if (nv <= 8) hipLaunchKernelGGL((k_route<DT, 8>), grid, block, 0, s, a, nranks);
-    else hipLaunchKernelGGL((k_route<DT, 16>), grid, block, 0, s, a, nranks);
+    const uint32_t rows = a.rows.start[nranks];
+    const dim3 block(kBlock), few((rows + kBlock / 16 - 1) / (kBlock / 16)), any((rows + kBlock / 64 - 1) / (kBlock / 64));
+    const int vec = vector_rows(a.logits, nranks, a.nexperts, DT);
+    switch (lane_experts(a.nexperts, a.topk, a.groups)) {
+        case 4: hipLaunchKernelGGL((k_route<DT, 4>), few, block, 0, s, a, nranks, vec); break;
+        case 8: hipLaunchKernelGGL((k_route<DT, 8>), few, block, 0, s, a, nranks, vec); break;
+        case 16: hipLaunchKernelGGL((k_route<DT, 16>), few, block, 0, s, a, nranks, vec); break;
+        case 32: hipLaunchKernelGGL((k_route<DT, 32>), few, block, 0, s, a, nranks, vec); break;
+        default:
+            if (a.nexperts <= 128) hipLaunchKernelGGL((k_route_any<DT, 2>), any, block, 0, s, a, nranks);
+            else if (a.nexperts <= 512) hipLaunchKernelGGL((k_route_any<DT, 8>), any, block, 0, s, a, nranks);
+            else hipLaunchKernelGGL((k_route_any<DT, 16>), any, block, 0, s, a, nranks);
+    }
     return hipGetLastError();
 }
 template <int DT>
 hipError_t route_backward(const RouteBackArgs& a, int nranks, hipStream_t s) {
-    const dim3 grid((a.rows.start[nranks] + kBlock / 64 - 1) / (kBlock / 64)), block(kBlock);
-    const uint32_t nv = (a.nexperts + 63) / 64;
-    if (nv <= 1) hipLaunchKernelGGL((k_route_backward<DT, 1>), grid, block, 0, s, a, nranks);
-    else if (nv <= 2) hipLaunchKernelGGL((k_route_backward<DT, 2>), grid, block, 0, s, a, nranks);
-    else if (nv <= 4) hipLaunchKernelGGL((k_route_backward<DT, 4>), grid, block, 0, s, a, nranks);
-    else if (nv <= 8) hipLaunchKernelGGL((k_route_backward<DT, 8>), grid, block, 0, s, a, nranks);
-    else hipLaunchKernelGGL((k_route_backward<DT, 16>), grid, block, 0, s, a, nranks);
+    const uint32_t rows = a.rows.start[nranks];
+    const dim3 block(kBlock), few((rows + kBlock / 16 - 1) / (kBlock / 16)), any((rows + kBlock / 64 - 1) / (kBlock / 64));
+    const int vec = vector_rows(a.logits, nranks, a.nexperts, DT) && vector_rows(a.dlogits, nranks, a.nexperts, DT);
+    switch (lane_experts(a.nexperts, a.topk, 1)) {
+        case 4: hipLaunchKernelGGL((k_route_backward<DT, 4, 16>), few, block, 0, s, a, nranks, vec); break;
+        case 8: hipLaunchKernelGGL((k_route_backward<DT, 8, 16>), few, block, 0, s, a, nranks, vec); break;
+        case 16: hipLaunchKernelGGL((k_route_backward<DT, 16, 16>), few, block, 0, s, a, nranks, vec); break;
+        case 32: hipLaunchKernelGGL((k_route_backward<DT, 32, 16>), few, block, 0, s, a, nranks, vec); break;
+        default: hipLaunchKernelGGL((k_route_backward<DT, 16, 64>), any, block, 0, s, a, nranks, vec);
+    }
     return hipGetLastError();
 }
 
+// Short rows take a wave, long ones (over 4 KiB) the workgroup.
+uint32_t token_blocks(uint32_t tokens, bool shorter) { return shorter ? (tokens + kBlock / 64 - 1) / (kBlock / 64) : tokens; }
+template <typename F>
+void with_rows(bool vec, bool shorter, F&& run) {
+    if (vec && shorter) run(std::true_type(), std::integral_constant<int, 1>());
+    else if (vec) run(std::true_type(), std::integral_constant<int, 4>());
+    else if (shorter) run(std::false_type(), std::integral_constant<int, 1>());
+    else run(std::false_type(), std::integral_constant<int, 4>());
+}
 }  // namespace
 
 hipError_t launch_route(const RouteArgs& a, int nranks, int dtype, hipStream_t s) {
@@ -464,30 +1017,49 @@ hipError_t launch_route_backward(const RouteBackArgs& a, int nranks, int dtype, 
     return dtype == kBF16 ? route_backward<kBF16>(a, nranks, s) : route_backward<kF32>(a, nranks, s);
 }
 
-hipError_t launch_plan(const PlanArgs& a, hipStream_t s) {
-    const uint32_t blocks = plan_blocks(uint64_t(a.rows.start[a.nranks]) * a.topk);
-    if (blocks > 0) hipLaunchKernelGGL(k_plan_count, dim3(blocks), dim3(kBlock), 0, s, a);
-    hipLaunchKernelGGL(k_plan_scan, dim3(1), dim3(1024), 0, s, a, blocks);
-    if (blocks > 0) hipLaunchKernelGGL(k_plan_place, dim3(blocks), dim3(kBlock), 0, s, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_dispatch_rows(const ExchangeRowsArgs& a, int esize, hipStream_t s) {
-    const dim3 grid(a.rows.start[a.nranks]), block(kBlock);
-    if (esize == 2) hipLaunchKernelGGL(k_dispatch_rows<uint16_t>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_dispatch_rows<uint32_t>, grid, block, 0, s, a);
+hipError_t launch_dispatch(const PlanArgs& p, const ExchangeRowsArgs& a, int esize, hipStream_t s) {
+    const uint32_t tokens = a.rows.start[a.nranks], slots = tokens * a.topk, blocks = plan_blocks(slots);
+    const bool vec = vector_rows(a.tokens_in, a.nranks, a.cols, esize == 2 ? kBF16 : kF32) &&
+                     vector_rows(a.rows_out, a.nranks, a.cols, esize == 2 ? kBF16 : kF32);
+    const bool shorter = uint64_t(a.cols) * esize <= 4096;
+    const uint32_t grid = token_blocks(tokens, shorter);
+    if (slots <= kFewSlots) {
+        with_rows(vec, shorter, [&](auto v, auto w) {
+            if (esize == 2) hipLaunchKernelGGL((k_dispatch_few<2, decltype(v)::value, decltype(w)::value>), dim3(grid + 1), dim3(kBlock), 0, s, a, p);
+            else hipLaunchKernelGGL((k_dispatch_few<4, decltype(v)::value, decltype(w)::value>), dim3(grid + 1), dim3(kBlock), 0, s, a, p);
+        });
+        return hipGetLastError();
+    }
+    // up to 128 workgroups of the plan each add up the counts before their own
+    const int scanned = blocks > 128;
+    hipLaunchKernelGGL(k_plan_count, dim3(blocks), dim3(kBlock), 0, s, p);
+    if (scanned) hipLaunchKernelGGL(k_plan_scan, dim3((p.nexperts + 63) / 64), dim3(64), 0, s, p, blocks);
+    hipLaunchKernelGGL(k_plan_place, dim3(blocks), dim3(kBlock), 0, s, p, blocks, scanned);
+    with_rows(vec, shorter, [&](auto v, auto w) {
+        if (esize == 2) hipLaunchKernelGGL((k_dispatch_rows<2, decltype(v)::value, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
+        else hipLaunchKernelGGL((k_dispatch_rows<4, decltype(v)::value, decltype(w)::value>), dim3(grid), dim3(kBlock), 0, s, a);
+    });
     return hipGetLastError();
 }
 hipError_t launch_combine(const ExchangeRowsArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid(a.rows.start[a.nranks]), block(kBlock);
-    if (dtype == kBF16) hipLaunchKernelGGL(k_combine<kBF16>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_combine<kF32>, grid, block, 0, s, a);
+    const bool vec = vector_rows(a.tokens_out, a.nranks, a.cols, dtype) && vector_rows(a.rows_in, a.nranks, a.cols, dtype);
+    const bool shorter = uint64_t(a.cols) * (dtype == kBF16 ? 2 : 4) <= 4096;
+    const dim3 grid(token_blocks(a.rows.start[a.nranks], shorter)), block(kBlock);
+    with_rows(vec, shorter, [&](auto v, auto w) {
+        if (dtype == kBF16) hipLaunchKernelGGL((k_combine<kBF16, decltype(v)::value, decltype(w)::value>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_combine<kF32, decltype(v)::value, decltype(w)::value>), grid, block, 0, s, a);
+    });
     return hipGetLastError();
 }
 hipError_t launch_combine_backward(const ExchangeRowsArgs& a, int dtype, hipStream_t s) {
-    const dim3 grid(a.rows.start[a.nranks]), block(kBlock);
-    if (dtype == kBF16) hipLaunchKernelGGL(k_combine_backward<kBF16>, grid, block, 0, s, a);
-    else hipLaunchKernelGGL(k_combine_backward<kF32>, grid, block, 0, s, a);
+    const bool vec = vector_rows(a.tokens_in, a.nranks, a.cols, dtype) && vector_rows(a.rows_in, a.nranks, a.cols, dtype) &&
+                     vector_rows(a.rows_out, a.nranks, a.cols, dtype);
+    const bool shorter = uint64_t(a.cols) * (dtype == kBF16 ? 2 : 4) <= 4096;
+    const dim3 grid(token_blocks(a.rows.start[a.nranks], shorter)), block(kBlock);
+    with_rows(vec, shorter, [&](auto v, auto w) {
+        if (dtype == kBF16) hipLaunchKernelGGL((k_combine_backward<kBF16, decltype(v)::value, decltype(w)::value>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((k_combine_backward<kF32, decltype(v)::value, decltype(w)::value>), grid, block, 0, s, a);
+    });
     return hipGetLastError();
 }
 

@@ -348,7 +348,7 @@ void fill_exchange(dt::ExchangeRowsArgs& a, const ExchangeShape& s, int nranks, 
 }
 
 size_t plan_bytes(const RowTable& rows, int nranks, int nexperts, int topk) {
-    return size_t(dt::plan_blocks(uint64_t(rows.start[nranks]) * topk)) * nexperts * sizeof(uint32_t);
+    return size_t(dt::plan_blocks(uint64_t(rows.start[nranks]) * topk) + 1) * nexperts * sizeof(uint32_t);
 }
 
 }  // namespace
@@ -396,15 +396,13 @@ dt_status dt_moe_dispatch(const void* const* x, const int32_t* const* experts, v
     p.topk = uint32_t(topk);
     p.per_rank = s.per_rank;
     p.nranks = nranks;
-    TRY(done(dt::launch_plan(p, stream), "moe_dispatch"));
-    if (s.rows.start[nranks] == 0) return DT_OK;
     dt::ExchangeRowsArgs a = {};
     fill_exchange(a, s, nranks, cols, nexperts, topk);
     copy_list(a.tokens_in, x, nranks);
     copy_list(a.rows_out, recv, nranks);
     copy_list(a.experts, experts, nranks);
     copy_list(a.positions, positions, nranks);
-    return done(dt::launch_dispatch_rows(a, int(es), stream), "moe_dispatch");
+    return done(dt::launch_dispatch(p, a, int(es), stream), "moe_dispatch");
 }
 
 dt_status dt_moe_combine(const void* const* y, const int32_t* const* experts, const int32_t* const* positions,

@@ -22,6 +22,8 @@ struct Elem<kBF16> {
     static __device__ __forceinline__ uint16_t put(float v) { return uint16_t(to_bf16(v)); }
 };
 
+constexpr float kLog2e = 1.44269504088896340736f;
+
 // The rank that holds global row `row` (uniform across the lanes).
 __device__ __forceinline__ int rank_of_row(const RowTable& t, int nranks, uint32_t row) {
     int r = 0;

@@ -281,7 +281,6 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 
 // exp(x): the argument's product with log2 e is off by half a step of |x| log2 e,
 // which adds |x| half steps to the result's error.
-constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // Four values rounded to the dtype and stored as one (`to` aligned for it); zeros unless `use`.

@@ -45,11 +45,27 @@ __device__ __forceinline__ void wave_argmax(double& key, uint32_t& idx) {
 // One token by the whole wave, scores in 64 bits: lane l holds experts l, l +
 // 64, ...  The way for every shape, and for the tokens whose candidates lie
 // too close together for 32 bits.
+// (The arguments are passed by value: a reference to the kernel's would have
+// every wave copy them to scratch memory first.)
+struct RouteRow {
+    const void* logits;
+    int32_t* experts;
+    float* weights;
+    const float* bias;
+    uint32_t nexperts, topk, groups, topk_groups;
+    int sigmoid, renormalize;
+    float scale;
+};
+__device__ __forceinline__ RouteRow route_row_of(const RouteArgs& a, int r, uint64_t local, uint32_t es) {
+    return RouteRow{static_cast<const char*>(a.logits[r]) + local * a.nexperts * es, a.experts[r] + local * a.topk,
+                    a.weights[r] + local * a.topk, a.bias, a.nexperts, a.topk, a.groups, a.topk_groups, a.sigmoid,
+                    a.renormalize, a.scale};
+}
 template <int DT, int NV>
-__device__ __noinline__ void route_row(const RouteArgs& a, int r, uint64_t local) {
+__device__ __noinline__ void route_row(RouteRow a) {
     typedef typename Elem<DT>::type T;
     const uint32_t lane = threadIdx.x & 63;
-    const T* x = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
+    const T* x = static_cast<const T*>(a.logits);
     float v[NV];
     double c[NV];
     bool live[NV];
@@ -175,8 +191,8 @@ __device__ __noinline__ void route_row(const RouteArgs& a, int r, uint64_t local
         s = !has ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-mylogit)) : expf(mylogit - top) / total;
     }
     if (lane < a.topk) {
-        a.experts[r][local * a.topk + lane] = has ? int32_t(mine) : -1;
-        a.weights[r][local * a.topk + lane] = s * a.scale;
+        a.experts[lane] = has ? int32_t(mine) : -1;
+        a.weights[lane] = s * a.scale;
     }
 }
 
@@ -185,7 +201,7 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     const uint32_t row = blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (row >= a.rows.start[nranks]) return;
     const int r = rank_of_row(a.rows, nranks, row);
-    route_row<DT, NV>(a, r, row - a.rows.start[r]);
+    route_row<DT, NV>(route_row_of(a, r, row - a.rows.start[r], sizeof(typename Elem<DT>::type)));
 }
 
 // Reductions over the 16 lanes that share a token, the same value in all of
@@ -229,8 +245,11 @@ __device__ __forceinline__ float max16(float v) {
     over16([&](auto c) { v = fmaxf(v, dpp<decltype(c)::value>(v)); });
     return v;
 }
-__device__ __forceinline__ float min16(float v) {
-    over16([&](auto c) { v = fminf(v, dpp<decltype(c)::value>(v)); });
+__device__ __forceinline__ int32_t max16(int32_t v) {
+    over16([&](auto c) {
+        const int32_t o = int32_t(dpp<decltype(c)::value>(uint32_t(v)));
+        v = o > v ? o : v;
+    });
     return v;
 }
 __device__ __forceinline__ float sum16(float v) {
@@ -246,6 +265,15 @@ __device__ __forceinline__ uint32_t min16(uint32_t v) {
 }
 
 constexpr float kBiggest = 3.402823466e38f;
+
+// Floats as integers of the same order (no NaN, no -0), and back: integer
+// maxima are one instruction with the lane exchange in it.
+__device__ __forceinline__ int32_t ordered(float f) {
+    const int32_t i = int32_t(__float_as_uint(f));
+    return i ^ int32_t(uint32_t(i >> 31) >> 1);
+}
+__device__ __forceinline__ float unordered(int32_t i) { return __uint_as_float(uint32_t(i ^ int32_t(uint32_t(i >> 31) >> 1))); }
+constexpr int32_t kNone = int32_t(0x807FFFFF);  // ordered(-inf)
 
 // The NL logits of a lane's experts [lane * NL, lane * NL + NL), -inf for
 // those that are not there or are NaN.
@@ -268,15 +296,16 @@ __device__ __forceinline__ void load_logits(const void* base, uint64_t row, uint
         for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? Elem<DT>::get(p[i]) : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < NL; i++) x[i] = x[i] > -INFINITY ? fminf(x[i], kBiggest) : -INFINITY;
+    for (int i = 0; i < NL; i++) x[i] = x[i] > -INFINITY ? fminf(x[i], kBiggest) + 0.f : -INFINITY;  // + 0: no -0
 }
 
 // Four tokens per wave, 16 lanes each; lane l of the 16 holds experts [l * NL, l
 // * NL + NL).  Candidates are ordered by the logits (exact) or by 32-bit
 // scores with a bound `off` on how far such a score may be from the exact one:
-//   sigmoid  s (1 - s) * 2U of the exponential, 2 U of sum and quotient: under 4 U;
-//   softmax  |d| s <= 0.37 of the argument d = x - max, 2 U of the exponential,
-//            20 U of the sum over NL + 4 additions (NL <= 16; 36 for 32), s <= 1: under 42 U;
+//   sigmoid  s (1 - s) (|x| + 2) U <= 0.8 U of the exponential and its argument, U of the
+//            sum, 2 U of the reciprocal: under 5 U;
+//   softmax, s <= 1:  (2 |d| + 2) s U <= 3 U of the exponential and its argument d = x - max,
+//            (NL + 4) U <= 36 U of the sum and 4 U of the quotient: under 48 U;
 //   the bias' addition  U |c|.
 // Where two neighbours in the order, or the last group that stays and the
 // first that goes, are closer than two such bounds, the token is done again in
@@ -292,60 +321,76 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     const uint64_t local = row - a.rows.start[r];
     const uint32_t first = lane * NL;
     constexpr float U = 5.9604645e-8f;
-    float x[NL], key[NL];
+    float x[NL];
+    int32_t key[NL];
     load_logits<DT, NL>(a.logits[r], local, a.nexperts, first, vec, x);
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NL; i++) top = fmaxf(top, x[i]);
-    top = max16(top);
     const bool scored = a.bias != nullptr || a.groups > 1;
-    float sum = 0.f;
+    float top = 0.f, sum = 0.f, off = 0.f;
     if (!a.sigmoid && (scored || !a.renormalize)) {
+        int32_t most = kNone;
 #pragma unroll
         for (int i = 0; i < NL; i++) {
-            key[i] = x[i] > -INFINITY ? expf(x[i] - top) : 0.f;
-            sum += key[i];
+            const int32_t o = ordered(x[i]);
+            most = o > most ? o : most;
         }
-        sum = sum16(sum);
+        top = unordered(max16(most));
     }
-    float off = 0.f;
-    if (scored) {
-        const float inv = a.sigmoid ? 1.f : 1.f / sum;
-        float big = 0.f;
+    if (scored || (!a.sigmoid && !a.renormalize)) {
+        float s[NL];
+        if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < NL; i++) {
-            const float s = a.sigmoid ? 1.f / (1.f + expf(-x[i])) : key[i] * inv;
-            const float b = a.bias != nullptr && first + i < a.nexperts ? a.bias[first + i] : 0.f;
-            const bool live = x[i] > -INFINITY && b > -INFINITY;
-            key[i] = live ? s + b : -INFINITY;
-            big = fmaxf(big, live ? fabsf(b) : 0.f);
+            for (int i = 0; i < NL; i++) s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e));
+            off = 5.f * U;
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; i++) {
+                s[i] = x[i] > -INFINITY ? __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) : 0.f;
+                sum += s[i];
+            }
+            sum = sum16(sum);
+            const float inv = 1.f / sum;
+#pragma unroll
+            for (int i = 0; i < NL; i++) s[i] *= inv;
+            off = 48.f * U;
         }
-        off = (a.sigmoid ? 4.f * U : 42.f * U) + U * (1.f + max16(big));
-    } else {
+        if (a.bias != nullptr) {
+            float big = 0.f;
 #pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = x[i];
+            for (int i = 0; i < NL; i++) {
+                const float b = first + i < a.nexperts ? a.bias[first + i] : 0.f;
+                const bool live = x[i] > -INFINITY && b > -INFINITY;
+                key[i] = live ? ordered(s[i] + b + 0.f) : kNone;
+                big = fmaxf(big, live ? fabsf(b) : 0.f);
+            }
+            off += U * (1.f + max16(big));
+        } else {
+#pragma unroll
+            for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? ordered(s[i]) : kNone;
+        }
     }
     bool close = false;
     if (a.groups > 1) {
         // a group is `width` neighbouring lanes, a power of two
         const uint32_t width = a.nexperts / a.groups / NL, group = lane / width;
-        float m1 = -INFINITY, m2 = -INFINITY;
+        int32_t m1 = kNone, m2 = kNone;
 #pragma unroll
         for (int i = 0; i < NL; i++) {
-            m2 = fmaxf(m2, fminf(m1, key[i]));
-            m1 = fmaxf(m1, key[i]);
+            const int32_t low = m1 < key[i] ? m1 : key[i];
+            m2 = low > m2 ? low : m2;
+            m1 = key[i] > m1 ? key[i] : m1;
         }
         uint32_t w = 1;
         over16([&](auto c) {
+            const int32_t o1 = int32_t(dpp<decltype(c)::value>(uint32_t(m1))), o2 = int32_t(dpp<decltype(c)::value>(uint32_t(m2)));
             if (w < width) {
-                const float o1 = dpp<decltype(c)::value>(m1), o2 = dpp<decltype(c)::value>(m2);
-                m2 = fmaxf(fmaxf(m2, o2), fminf(m1, o1));
-                m1 = fmaxf(m1, o1);
+                const int32_t low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
+                m2 = low > second ? low : second;
+                m1 = o1 > m1 ? o1 : m1;
             }
             w *= 2;
         });
         // one expert left in a group: it alone; none: the group goes
-        const float score = m2 > -INFINITY ? m1 + m2 : m1;
+        const float score = m1 == kNone ? -INFINITY : m2 == kNone ? unordered(m1) : unordered(m1) + unordered(m2);
         uint32_t better = 0;
         rotations([&](auto c) {
             const float o = dpp<decltype(c)::value>(score);
@@ -353,30 +398,36 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
             better += og != group && (o > score || (o == score && og < group)) ? 1 : 0;
         });
         const bool stays = better < a.topk_groups * width && score > -INFINITY;
-        const float last = min16(stays ? score : INFINITY), next = max16(stays ? -INFINITY : score);
+        const float last = -max16(stays ? -score : -INFINITY), next = max16(stays ? -INFINITY : score);
         close = last - next <= 4.f * off + 2.f * U * fabsf(last);
 #pragma unroll
         for (int i = 0; i < NL; i++)
-            if (!stays) key[i] = -INFINITY;
-            else if (a.bias == nullptr) key[i] = x[i];  // the logits' own order within the groups that stay
+            if (!stays) key[i] = kNone;
+            else if (a.bias == nullptr) key[i] = ordered(x[i]);  // the logits' own order within the groups that stay
+    }
+    if (!scored) {
+#pragma unroll
+        for (int i = 0; i < NL; i++) key[i] = ordered(x[i]);
     }
     const float gap = a.bias != nullptr ? 2.f * off : -1.f;  // the logits' order is exact
     uint32_t mine = UINT32_MAX;
     float before = INFINITY;
     for (uint32_t k = 0; k <= a.topk; k++) {
-        float best = key[0];
+        int32_t best = key[0];
 #pragma unroll
-        for (int i = 1; i < NL; i++) best = fmaxf(best, key[i]);
+        for (int i = 1; i < NL; i++) best = key[i] > best ? key[i] : best;
         best = max16(best);
-        close = close || (best > -INFINITY && before - best <= gap);
+        const float now = unordered(best);
+        close = close || (best > kNone && before - now <= gap);
         if (k == a.topk) break;
-        before = best;
+        before = now;
         uint32_t at = UINT32_MAX;
 #pragma unroll
         for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? first + i : at;
-        at = best > -INFINITY ? min16(at) : UINT32_MAX;
+        at = best > kNone ? min16(at) : UINT32_MAX;
+        const uint32_t here = at - first;
 #pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = at == first + i ? -INFINITY : key[i];
+        for (int i = 0; i < NL; i++) key[i] = here == uint32_t(i) ? kNone : key[i];
         if (lane == k) mine = at;
     }
     const bool has = mine != UINT32_MAX;
@@ -404,7 +455,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
         todo &= todo - 1;
         const int rr = __builtin_amdgcn_readlane(r, from);
         const uint32_t at = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(local)), from));
-        route_row<DT, (16 * NL + 63) / 64>(a, rr, at);
+        route_row<DT, (16 * NL + 63) / 64>(route_row_of(a, rr, at, sizeof(T)));
     }
 }
 

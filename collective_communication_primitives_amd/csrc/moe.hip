@@ -42,30 +42,18 @@ __device__ __forceinline__ void wave_argmax(double& key, uint32_t& idx) {
     }
 }
 
-// One token by the whole wave, scores in 64 bits: lane l holds experts l, l +
-// 64, ...  The way for every shape, and for the tokens whose candidates lie
-// too close together for 32 bits.
-// (The arguments are passed by value: a reference to the kernel's would have
-// every wave copy them to scratch memory first.)
-struct RouteRow {
-    const void* logits;
-    int32_t* experts;
-    float* weights;
-    const float* bias;
-    uint32_t nexperts, topk, groups, topk_groups;
-    int sigmoid, renormalize;
-    float scale;
-};
-__device__ __forceinline__ RouteRow route_row_of(const RouteArgs& a, int r, uint64_t local, uint32_t es) {
-    return RouteRow{static_cast<const char*>(a.logits[r]) + local * a.nexperts * es, a.experts[r] + local * a.topk,
-                    a.weights[r] + local * a.topk, a.bias, a.nexperts, a.topk, a.groups, a.topk_groups, a.sigmoid,
-                    a.renormalize, a.scale};
-}
+// One token per wave, scores in 64 bits: lane l holds experts l, l + 64, ...
+// For the shapes that four tokens to a wave do not take: more than 512
+// experts, more than 16 choices, groups that are not whole lanes.
 template <int DT, int NV>
-__device__ __noinline__ void route_row(RouteRow a) {
+__global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     typedef typename Elem<DT>::type T;
+    const uint32_t row = blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (row >= a.rows.start[nranks]) return;
     const uint32_t lane = threadIdx.x & 63;
-    const T* x = static_cast<const T*>(a.logits);
+    const int r = rank_of_row(a.rows, nranks, row);
+    const uint64_t local = row - a.rows.start[r];
+    const T* x = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
     float v[NV];
     double c[NV];
     bool live[NV];
@@ -191,17 +179,9 @@ __device__ __noinline__ void route_row(RouteRow a) {
         s = !has ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-mylogit)) : expf(mylogit - top) / total;
     }
     if (lane < a.topk) {
-        a.experts[lane] = has ? int32_t(mine) : -1;
-        a.weights[lane] = s * a.scale;
+        a.experts[r][local * a.topk + lane] = has ? int32_t(mine) : -1;
+        a.weights[r][local * a.topk + lane] = s * a.scale;
     }
-}
-
-template <int DT, int NV>
-__global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
-    const uint32_t row = blockIdx.x * (kBlock / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (row >= a.rows.start[nranks]) return;
-    const int r = rank_of_row(a.rows, nranks, row);
-    route_row<DT, NV>(route_row_of(a, r, row - a.rows.start[r], sizeof(typename Elem<DT>::type)));
 }
 
 // Reductions over the 16 lanes that share a token, the same value in all of
@@ -292,26 +272,218 @@ __device__ __forceinline__ void load_logits(const void* base, uint64_t row, uint
             for (int e = 0; e < E; e++) x[i * E + e] = Elem<DT>::get(t[e]);
         }
     } else {
+        // the last expert again instead of a branch around each load
+        const T* all = static_cast<const T*>(base) + row * nexperts;
 #pragma unroll
-        for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? Elem<DT>::get(p[i]) : -INFINITY;
+        for (int i = 0; i < NL; i++) {
+            const uint32_t e = first + i < nexperts ? first + i : nexperts - 1;
+            x[i] = Elem<DT>::get(all[e]);
+        }
+#pragma unroll
+        for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? x[i] : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < NL; i++) x[i] = x[i] > -INFINITY ? fminf(x[i], kBiggest) + 0.f : -INFINITY;  // + 0: no -0
 }
 
+// The lane's experts' biases.
+template <int NL>
+__device__ __forceinline__ void load_bias(const float* bias, uint32_t nexperts, uint32_t first, float (&b)[NL]) {
+#pragma unroll
+    for (int i = 0; i < NL; i++) b[i] = bias[first + i < nexperts ? first + i : nexperts - 1];
+}
+
+// max over the 16 lanes of 64-bit keys.
+__device__ __forceinline__ int64_t max16(int64_t v) {
+    over16([&](auto c) {
+        const uint64_t u = uint64_t(v);
+        const uint64_t o = uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u));
+        v = int64_t(o) > v ? int64_t(o) : v;
+    });
+    return v;
+}
+__device__ __forceinline__ int64_t ordered(double f) {
+    const int64_t i = __double_as_longlong(f);
+    return i ^ int64_t(uint64_t(i >> 63) >> 1);
+}
+__device__ __forceinline__ double unordered(int64_t i) { return __longlong_as_double(i ^ int64_t(uint64_t(i >> 63) >> 1)); }
+
+// What the 16 lanes of a token know about it.
+struct RouteToken {
+    uint32_t nexperts, topk, groups, topk_groups, first;  // first: the lane's first expert
+    int sigmoid;
+    const float* bias;
+};
+
+// The groups that stay: true in the lanes of one of them.  m1, m2: the lane's
+// two largest candidates as ordered integers, `none` where there is none; a
+// group is `width` neighbouring lanes, a power of two.  `margin`: how far the
+// last score that stays is above the first that goes.
+template <typename K>
+__device__ __forceinline__ bool stays_in(const RouteToken& a, uint32_t width, K m1, K m2, K none, float& margin, float& size) {
+    typedef decltype(unordered(K())) F;
+    const uint32_t lane = threadIdx.x & 15, group = lane / width;
+    uint32_t w = 1;
+    over16([&](auto c) {
+        constexpr int C = decltype(c)::value;
+        K o1, o2;
+        if constexpr (sizeof(K) == 4) {
+            o1 = K(dpp<C>(uint32_t(m1)));
+            o2 = K(dpp<C>(uint32_t(m2)));
+        } else {
+            o1 = K(uint64_t(dpp<C>(uint32_t(uint64_t(m1) >> 32))) << 32 | dpp<C>(uint32_t(m1)));
+            o2 = K(uint64_t(dpp<C>(uint32_t(uint64_t(m2) >> 32))) << 32 | dpp<C>(uint32_t(m2)));
+        }
+        if (w < width) {
+            const K low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
+            m2 = low > second ? low : second;
+            m1 = o1 > m1 ? o1 : m1;
+        }
+        w *= 2;
+    });
+    // one expert left in a group: it alone; none: the group goes
+    const F score = m1 == none ? F(-INFINITY) : m2 == none ? unordered(m1) : unordered(m1) + unordered(m2);
+    const K key = score > F(-INFINITY) ? ordered(score + F(0)) : none;
+    uint32_t better = 0;
+    rotations([&](auto c) {
+        constexpr int C = decltype(c)::value;
+        K o;
+        if constexpr (sizeof(K) == 4) o = K(dpp<C>(uint32_t(key)));
+        else o = K(uint64_t(dpp<C>(uint32_t(uint64_t(key) >> 32))) << 32 | dpp<C>(uint32_t(key)));
+        const uint32_t og = dpp<C>(group);
+        better += og != group && (o > key || (o == key && og < group)) ? 1 : 0;
+    });
+    const bool stays = better < a.topk_groups * width && key != none;
+    if constexpr (sizeof(K) == 4) {
+        const float last = -max16(stays ? -score : -INFINITY), next = max16(stays ? -INFINITY : score);
+        margin = last - next;
+        size = fabsf(last);
+    }
+    return stays;
+}
+
+// The choice in 64 bits: lane j's `mine` becomes choice j's expert, UINT32_MAX
+// where none is left.  Logits and biases are read again one by one: held in
+// registers they would double what the kernel takes, and so halve the waves of
+// the tokens that never come here.
+template <int DT, int NL>
+__device__ __forceinline__ uint32_t choose_exactly(const RouteToken& a, const typename Elem<DT>::type* logits) {
+    const uint32_t lane = threadIdx.x & 15;
+    constexpr int64_t kLowest = INT64_MIN;
+    int64_t key[NL];
+    auto logit = [&](int i) {
+        asm volatile("" ::: "memory");  // no load is moved ahead
+        const uint32_t e = a.first + i < a.nexperts ? a.first + i : a.nexperts - 1;
+        const float x = Elem<DT>::get(logits[e]);
+        return a.first + i < a.nexperts && x > -INFINITY ? fminf(x, kBiggest) + 0.f : -INFINITY;
+    };
+    const bool scored = a.bias != nullptr || a.groups > 1;
+    double sum = 0., top = 0.;
+    if (scored && !a.sigmoid) {
+        float most = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NL; i++) most = fmaxf(most, logit(i));
+        top = double(max16(most));
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            const float x = logit(i);
+            sum += x > -INFINITY ? exp(double(x) - top) : 0.;
+        }
+        over16([&](auto c) {
+            const uint64_t u = __double_as_longlong(sum);
+            sum += __longlong_as_double(int64_t(uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u))));
+        });
+    }
+#pragma unroll
+    for (int i = 0; i < NL; i++) {
+        const float x = logit(i);
+        double v = double(x);
+        bool live = x > -INFINITY;
+        if (scored) v = a.sigmoid ? 1. / (1. + exp(-v)) : exp(v - top) / sum;
+        if (a.bias != nullptr) {
+            const float b = a.bias[a.first + i < a.nexperts ? a.first + i : a.nexperts - 1];
+            live = live && b > -INFINITY;
+            v += double(b);
+        }
+        key[i] = live ? ordered(v + 0.) : kLowest;
+    }
+    if (a.groups > 1) {
+        int64_t m1 = kLowest, m2 = kLowest;
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            const int64_t low = m1 < key[i] ? m1 : key[i];
+            m2 = low > m2 ? low : m2;
+            m1 = key[i] > m1 ? key[i] : m1;
+        }
+        float margin = 0.f, size = 0.f;
+        const bool stays = stays_in<int64_t>(a, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
+#pragma unroll
+        for (int i = 0; i < NL; i++) {
+            if (!stays) key[i] = kLowest;
+            else if (a.bias == nullptr && key[i] != kLowest) key[i] = ordered(double(logit(i)));
+        }
+    }
+    uint32_t mine = UINT32_MAX;
+    for (uint32_t k = 0; k < a.topk; k++) {
+        int64_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < NL; i++) best = key[i] > best ? key[i] : best;
+        best = max16(best);
+        uint32_t at = UINT32_MAX;
+#pragma unroll
+        for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? a.first + i : at;
+        at = best > kLowest ? min16(at) : UINT32_MAX;
+        const uint32_t here = at - a.first;
+#pragma unroll
+        for (int i = 0; i < NL; i++) key[i] = here == uint32_t(i) ? kLowest : key[i];
+        if (lane == k) mine = at;
+    }
+    return mine;
+}
+
+// Descending by odd-even merging: one maximum and one minimum per comparison.
+template <int NL>
+__device__ __forceinline__ void sort_down(int32_t (&key)[NL]) {
+#pragma unroll
+    for (int p = 1; p < NL; p <<= 1)
+#pragma unroll
+        for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+            for (int j = k % p; j + k < NL; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; i++)
+                    if (j + i + k < NL && (j + i) / (2 * p) == (j + i + k) / (2 * p)) {
+                        const int32_t u = key[j + i], v = key[j + i + k];
+                        key[j + i] = u > v ? u : v;
+                        key[j + i + k] = u > v ? v : u;
+                    }
+}
+
 // Four tokens per wave, 16 lanes each; lane l of the 16 holds experts [l * NL, l
-// * NL + NL).  Candidates are ordered by the logits (exact) or by 32-bit
-// scores with a bound `off` on how far such a score may be from the exact one:
+// * NL + NL), sorted once; then topk times the largest of the 16 lanes' heads
+// is taken off its list.
+//
+// The keys are 32-bit: the logit, or the score where there is a bias, as an
+// ordered integer whose last bits give way to the place in the lane.  The
+// chosen ones' uncut values are compared afterwards.  They tell two candidates
+// apart unless they are closer than twice `off`, the bound on a 32-bit score's
+// error:
 //   sigmoid  s (1 - s) (|x| + 2) U <= 0.8 U of the exponential and its argument, U of the
 //            sum, 2 U of the reciprocal: under 5 U;
 //   softmax, s <= 1:  (2 |d| + 2) s U <= 3 U of the exponential and its argument d = x - max,
 //            (NL + 4) U <= 36 U of the sum and 4 U of the quotient: under 48 U;
 //   the bias' addition  U |c|.
-// Where two neighbours in the order, or the last group that stays and the
-// first that goes, are closer than two such bounds, the token is done again in
-// 64 bits: about one in a thousand of normally distributed logits.
+// Where two neighbours in the order, the last choice and the one behind it, or
+// the last group that stays and the first that goes are that close, the wave
+// chooses again in 64 bits: about one token in a thousand of normally
+// distributed logits with a bias.
+//
+// 32768 tokens, 8 of 256 experts, sigmoid, bias, 8 groups: bound by the vector
+// unit (some 1100 instructions per wave).  A wave per token with 64-bit scores
+// throughout took 229 us; 16 lanes that scan for each choice 61 us.
 template <int DT, int NL>
 __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int vec) {
+    typedef typename Elem<DT>::type T;
     const uint32_t total = a.rows.start[nranks], lane = threadIdx.x & 15;
     const uint32_t row0 = blockIdx.x * (kBlock / 16) + (threadIdx.x >> 4);
     const bool there = row0 < total;
@@ -320,28 +492,29 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     while (r + 1 < nranks && row >= a.rows.start[r + 1]) r++;
     const uint64_t local = row - a.rows.start[r];
     const uint32_t first = lane * NL;
+    const RouteToken token{a.nexperts, a.topk, a.groups, a.topk_groups, first, a.sigmoid, a.bias};
     constexpr float U = 5.9604645e-8f;
+    constexpr int32_t kPlace = NL - 1, kLowest = INT32_MIN;
     float x[NL];
     int32_t key[NL];
     load_logits<DT, NL>(a.logits[r], local, a.nexperts, first, vec, x);
     const bool scored = a.bias != nullptr || a.groups > 1;
     float top = 0.f, sum = 0.f, off = 0.f;
-    if (!a.sigmoid && (scored || !a.renormalize)) {
-        int32_t most = kNone;
-#pragma unroll
-        for (int i = 0; i < NL; i++) {
-            const int32_t o = ordered(x[i]);
-            most = o > most ? o : most;
-        }
-        top = unordered(max16(most));
-    }
+    bool close = false, stays = true;
     if (scored || (!a.sigmoid && !a.renormalize)) {
-        float s[NL];
         if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < NL; i++) s[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e));
+            for (int i = 0; i < NL; i++) key[i] = ordered(__builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e)));
             off = 5.f * U;
         } else {
+            int32_t most = kNone;
+#pragma unroll
+            for (int i = 0; i < NL; i++) {
+                const int32_t o = ordered(x[i]);
+                most = o > most ? o : most;
+            }
+            top = unordered(max16(most));
+            float s[NL];
 #pragma unroll
             for (int i = 0; i < NL; i++) {
                 s[i] = x[i] > -INFINITY ? __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) : 0.f;
@@ -350,90 +523,78 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
             sum = sum16(sum);
             const float inv = 1.f / sum;
 #pragma unroll
-            for (int i = 0; i < NL; i++) s[i] *= inv;
+            for (int i = 0; i < NL; i++) key[i] = ordered(s[i] * inv);
             off = 48.f * U;
         }
         if (a.bias != nullptr) {
-            float big = 0.f;
+            float big = 0.f, b[NL];
+            load_bias<NL>(a.bias, a.nexperts, first, b);
 #pragma unroll
             for (int i = 0; i < NL; i++) {
-                const float b = first + i < a.nexperts ? a.bias[first + i] : 0.f;
-                const bool live = x[i] > -INFINITY && b > -INFINITY;
-                key[i] = live ? ordered(s[i] + b + 0.f) : kNone;
-                big = fmaxf(big, live ? fabsf(b) : 0.f);
+                const bool live = x[i] > -INFINITY && b[i] > -INFINITY;
+                key[i] = live ? ordered(unordered(key[i]) + b[i] + 0.f) : kLowest;
+                big = fmaxf(big, live ? fabsf(b[i]) : 0.f);
             }
             off += U * (1.f + max16(big));
         } else {
 #pragma unroll
-            for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? ordered(s[i]) : kNone;
+            for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? key[i] : kLowest;
         }
-    }
-    bool close = false;
-    if (a.groups > 1) {
-        // a group is `width` neighbouring lanes, a power of two
-        const uint32_t width = a.nexperts / a.groups / NL, group = lane / width;
-        int32_t m1 = kNone, m2 = kNone;
+        if (a.groups > 1) {
+            int32_t m1 = kLowest, m2 = kLowest;
 #pragma unroll
-        for (int i = 0; i < NL; i++) {
-            const int32_t low = m1 < key[i] ? m1 : key[i];
-            m2 = low > m2 ? low : m2;
-            m1 = key[i] > m1 ? key[i] : m1;
-        }
-        uint32_t w = 1;
-        over16([&](auto c) {
-            const int32_t o1 = int32_t(dpp<decltype(c)::value>(uint32_t(m1))), o2 = int32_t(dpp<decltype(c)::value>(uint32_t(m2)));
-            if (w < width) {
-                const int32_t low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
-                m2 = low > second ? low : second;
-                m1 = o1 > m1 ? o1 : m1;
+            for (int i = 0; i < NL; i++) {
+                const int32_t low = m1 < key[i] ? m1 : key[i];
+                m2 = low > m2 ? low : m2;
+                m1 = key[i] > m1 ? key[i] : m1;
             }
-            w *= 2;
-        });
-        // one expert left in a group: it alone; none: the group goes
-        const float score = m1 == kNone ? -INFINITY : m2 == kNone ? unordered(m1) : unordered(m1) + unordered(m2);
-        uint32_t better = 0;
-        rotations([&](auto c) {
-            const float o = dpp<decltype(c)::value>(score);
-            const uint32_t og = dpp<decltype(c)::value>(group);
-            better += og != group && (o > score || (o == score && og < group)) ? 1 : 0;
-        });
-        const bool stays = better < a.topk_groups * width && score > -INFINITY;
-        const float last = -max16(stays ? -score : -INFINITY), next = max16(stays ? -INFINITY : score);
-        close = last - next <= 4.f * off + 2.f * U * fabsf(last);
-#pragma unroll
-        for (int i = 0; i < NL; i++)
-            if (!stays) key[i] = kNone;
-            else if (a.bias == nullptr) key[i] = ordered(x[i]);  // the logits' own order within the groups that stay
+            float margin = 0.f, size = 0.f;
+            stays = stays_in<int32_t>(token, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
+            close = margin <= 4.f * off + 2.f * U * size;
+        }
     }
-    if (!scored) {
+    if (a.bias == nullptr) {  // the logits' own order
 #pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = ordered(x[i]);
+        for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? ordered(x[i]) : kLowest;
     }
-    const float gap = a.bias != nullptr ? 2.f * off : -1.f;  // the logits' order is exact
+#pragma unroll
+    for (int i = 0; i < NL; i++) key[i] = stays && key[i] != kLowest ? (key[i] & ~kPlace) | (kPlace - i) : kLowest;
+    sort_down(key);
     uint32_t mine = UINT32_MAX;
-    float before = INFINITY;
-    for (uint32_t k = 0; k <= a.topk; k++) {
-        int32_t best = key[0];
+    for (uint32_t k = 0; k < a.topk; k++) {
+        const int32_t best = max16(key[0]);
+        // the lowest of the lanes with that key, whatever the place in the lane
+        const uint32_t equal = uint32_t(__ballot(((key[0] ^ best) & ~kPlace) == 0) >> (threadIdx.x & 48)) & 0xFFFFu;
+        const uint32_t from = uint32_t(__builtin_ctz(equal | 0x10000u));
+        const uint32_t at = uint32_t(__shfl(int(first + kPlace - (key[0] & kPlace)), int((threadIdx.x & 48) + from)));
+        if (lane == k && best != kLowest) mine = at;
+        // bit selects: written as conditionals the compiler makes them indexed reads of the list
+        const int32_t taken = lane == from ? -1 : 0;
 #pragma unroll
-        for (int i = 1; i < NL; i++) best = key[i] > best ? key[i] : best;
-        best = max16(best);
-        const float now = unordered(best);
-        close = close || (best > kNone && before - now <= gap);
-        if (k == a.topk) break;
-        before = now;
-        uint32_t at = UINT32_MAX;
-#pragma unroll
-        for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? first + i : at;
-        at = best > kNone ? min16(at) : UINT32_MAX;
-        const uint32_t here = at - first;
-#pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = here == uint32_t(i) ? kNone : key[i];
-        if (lane == k) mine = at;
+        for (int i = 0; i + 1 < NL; i++) key[i] = (key[i + 1] & taken) | (key[i] & ~taken);
+        key[NL - 1] = (kLowest & taken) | (key[NL - 1] & ~taken);
+    }
+    const T* logits = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
+    float logit = mine != UINT32_MAX ? fminf(Elem<DT>::get(logits[mine]), kBiggest) : -INFINITY;
+    if (a.bias != nullptr || DT == kF32) {
+        // The choices' uncut values side by side, and the most that the best one left may be.  (bf16 logits keep all
+        // their bits: equal keys are equal logits.)
+        float v = logit;
+        if (a.bias != nullptr && mine != UINT32_MAX) {
+            v = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(logit * -kLog2e))
+                          : __builtin_amdgcn_exp2f((logit - top) * kLog2e) * (1.f / sum);
+            v += a.bias[mine];
+        }
+        const int32_t left = max16(key[0]);
+        const float after = dpp<0x101>(v), tail = left != kLowest ? unordered(left | kPlace) : -INFINITY;
+        const float next = lane + 1 < a.topk ? after : tail;
+        close = close || (lane < a.topk && next > -INFINITY && v - next <= 2.f * off + 2.f * U * fabsf(v));
+    }
+    if (__any(close)) {
+        mine = choose_exactly<DT, NL>(token, logits);
+        logit = mine != UINT32_MAX ? fminf(Elem<DT>::get(logits[mine]), kBiggest) : -INFINITY;
     }
     const bool has = mine != UINT32_MAX;
-    typedef typename Elem<DT>::type T;
-    float logit = -INFINITY;
-    if (has) logit = fminf(Elem<DT>::get(static_cast<const T*>(a.logits[r])[local * a.nexperts + mine]), kBiggest);
     float s;
     if (a.renormalize) {
         const float ctop = max16(logit);
@@ -444,18 +605,9 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     } else {
         s = !has ? 0.f : a.sigmoid ? 1.f / (1.f + expf(-logit)) : expf(logit - top) / sum;
     }
-    if (there && !close && lane < a.topk) {
+    if (there && lane < a.topk) {
         a.experts[r][local * a.topk + lane] = has ? int32_t(mine) : -1;
         a.weights[r][local * a.topk + lane] = s * a.scale;
-    }
-    // the wave's tokens that are too close, one after the other
-    uint64_t todo = __ballot(there && close && lane == 0);
-    while (todo != 0) {
-        const int from = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        const int rr = __builtin_amdgcn_readlane(r, from);
-        const uint32_t at = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(local)), from));
-        route_row<DT, (16 * NL + 63) / 64>(route_row_of(a, rr, at, sizeof(T)));
     }
 }
 

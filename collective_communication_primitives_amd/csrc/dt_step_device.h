@@ -2,6 +2,8 @@
 // element access by dtype, wave and workgroup sums, the row's rank.
 #pragma once
 
+#include <type_traits>
+
 #include "dt_device.h"
 #include "dt_step.h"
 
@@ -29,6 +31,52 @@ __device__ __forceinline__ int rank_of_row(const RowTable& t, int nranks, uint32
     int r = 0;
     while (r + 1 < nranks && row >= t.start[r + 1]) r++;
     return r;
+}
+
+// 16 bytes at an address that is aligned to elements of ES bytes only: one
+// access, which the memory unit splits where it crosses a line.
+template <int ES>
+struct Loose;
+template <>
+struct Loose<2> {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(2)));
+};
+template <>
+struct Loose<4> {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4)));
+};
+// Unit u (16 bytes) of a row of `bytes` bytes that starts and ends anywhere:
+// zeros behind the row's end, where nothing is read and nothing stored.
+template <int ES>
+__device__ __forceinline__ u32x4 load_loose(const char* row, uint32_t u, uint32_t bytes) {
+    const uint32_t at = u * 16;
+    u32x4 x = {0, 0, 0, 0};
+    if (at + 16 <= bytes) {
+        x = __builtin_nontemporal_load(reinterpret_cast<const typename Loose<ES>::type*>(row + at));
+    } else if (at < bytes) {
+        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
+        T t[16 / ES];
+#pragma unroll
+        for (int e = 0; e < 16 / ES; e++)
+            t[e] = at + e * ES < bytes ? *reinterpret_cast<const T*>(row + at + e * ES) : T(0);
+        __builtin_memcpy(&x, t, 16);
+    }
+    return x;
+}
+template <int ES>
+__device__ __forceinline__ void store_loose(char* row, uint32_t u, uint32_t bytes, u32x4 x) {
+    const uint32_t at = u * 16;
+    if (at + 16 <= bytes) {
+        const typename Loose<ES>::type v = x;
+        __builtin_nontemporal_store(v, reinterpret_cast<typename Loose<ES>::type*>(row + at));
+    } else if (at < bytes) {
+        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
+        T t[16 / ES];
+        __builtin_memcpy(t, &x, 16);
+#pragma unroll
+        for (int e = 0; e < 16 / ES; e++)
+            if (at + e * ES < bytes) *reinterpret_cast<T*>(row + at + e * ES) = t[e];
+    }
 }
 
 // Sums and maxima over the wave's 64 lanes, the same value in every lane.

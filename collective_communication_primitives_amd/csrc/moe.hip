@@ -899,36 +899,34 @@ __device__ __forceinline__ Choices choices(const ExchangeRowsArgs& a, P* const (
 }
 
 // A token's row is worked on by WPT waves (1 for short rows, 4 for long ones),
-// NV units per lane at a time: 16-byte vectors, or single elements where rows
-// are off the 16-byte boundaries.
+// NV units of 16 bytes per lane at a time.  VEC: rows start and end on 16-byte
+// boundaries; the others are read at their elements' alignment, with a last
+// unit that may be partly behind the row's end.
 template <int ES, bool VEC>
-struct RowUnit {
-    static constexpr int bytes = VEC ? 16 : ES;
-    typedef typename std::conditional<VEC, u32x4, typename std::conditional<ES == 2, uint16_t, uint32_t>::type>::type type;
-};
-template <typename X>
-__device__ __forceinline__ X load_at(const char* row, uint32_t u) {
-    return __builtin_nontemporal_load(reinterpret_cast<const X*>(row) + u);
+__device__ __forceinline__ u32x4 load_at(const char* row, uint32_t u, uint32_t bytes) {
+    if constexpr (VEC) return load16(row + u * 16);
+    else return load_loose<ES>(row, u, bytes);
 }
-template <typename X>
-__device__ __forceinline__ void store_at(const char* row, uint32_t u, X v) {
-    __builtin_nontemporal_store(v, reinterpret_cast<X*>(const_cast<char*>(row)) + u);
+template <int ES, bool VEC>
+__device__ __forceinline__ void store_at(const char* row, uint32_t u, uint32_t bytes, u32x4 v) {
+    if constexpr (VEC) store16(const_cast<char*>(row) + u * 16, v);
+    else store_loose<ES>(const_cast<char*>(row), u, bytes, v);
 }
 
 template <int ES, bool VEC, int WPT>
-__device__ __forceinline__ void dispatch_row(const char* src, uint32_t units, const Choices& c, uint32_t lane) {
-    typedef typename RowUnit<ES, VEC>::type X;
+__device__ __forceinline__ void dispatch_row(const char* src, uint32_t bytes, const Choices& c, uint32_t lane) {
     constexpr int NV = 4, L = 64 * WPT;
+    const uint32_t units = (bytes + 15) / 16;
     for (uint32_t u0 = lane; u0 < units; u0 += NV * L) {
-        X x[NV];
+        u32x4 x[NV];
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (u0 + i * L < units) x[i] = load_at<X>(src, u0 + i * L);
+            if (u0 + i * L < units) x[i] = load_at<ES, VEC>(src, u0 + i * L, bytes);
         for (uint64_t m = c.kept; m != 0; m &= m - 1) {
             const char* to = choice_row(c, __builtin_ctzll(m));
 #pragma unroll
             for (int i = 0; i < NV; i++)
-                if (u0 + i * L < units) store_at<X>(to, u0 + i * L, x[i]);
+                if (u0 + i * L < units) store_at<ES, VEC>(to, u0 + i * L, bytes, x[i]);
         }
     }
 }
@@ -947,7 +945,7 @@ __global__ __launch_bounds__(kBlock) void k_dispatch_rows(ExchangeRowsArgs a) {
     const uint64_t local = row - a.rows.start[r];
     const uint32_t pitch = a.cols * ES;
     const Choices c = choices(a, a.rows_out, r, local, pitch);
-    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch / RowUnit<ES, VEC>::bytes, c,
+    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch, c,
                                threadIdx.x % (64 * WPT));
 }
 
@@ -1008,28 +1006,27 @@ __global__ __launch_bounds__(kBlock) void k_dispatch_few(ExchangeRowsArgs a, Pla
         if (WPT == 1 || wave == 0) p.positions[r][local * a.topk + lane] = kept ? int32_t(pos) : -1;
     }
     c.kept = __ballot(kept);
-    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch / RowUnit<ES, VEC>::bytes, c,
+    dispatch_row<ES, VEC, WPT>(static_cast<const char*>(a.tokens_in[r]) + local * pitch, pitch, c,
                                threadIdx.x % (64 * WPT));
 }
 
 // The elements of a unit as fp32.
-template <int DT, bool VEC>
+template <int DT>
 struct Values {
-    static constexpr int ES = DT == kBF16 ? 2 : 4, n = VEC ? 16 / ES : 1;
-    typedef typename RowUnit<ES, VEC>::type X;
+    static constexpr int ES = DT == kBF16 ? 2 : 4, n = 16 / ES;
     typedef typename Elem<DT>::type T;
-    static __device__ __forceinline__ void get(X x, float (&f)[n]) {
+    static __device__ __forceinline__ void get(u32x4 x, float (&f)[n]) {
         T t[n];
-        __builtin_memcpy(t, &x, sizeof t);
+        __builtin_memcpy(t, &x, 16);
 #pragma unroll
         for (int i = 0; i < n; i++) f[i] = Elem<DT>::get(t[i]);
     }
-    static __device__ __forceinline__ X put(const float (&f)[n]) {
+    static __device__ __forceinline__ u32x4 put(const float (&f)[n]) {
         T t[n];
 #pragma unroll
         for (int i = 0; i < n; i++) t[i] = Elem<DT>::put(f[i]);
-        X x;
-        __builtin_memcpy(&x, t, sizeof t);
+        u32x4 x;
+        __builtin_memcpy(&x, t, 16);
         return x;
     }
 };
@@ -1038,14 +1035,13 @@ struct Values {
 // rows of up to four choices are on their way at a time.
 template <int DT, bool VEC, int WPT>
 __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
-    typedef Values<DT, VEC> V;
-    typedef typename V::X X;
+    typedef Values<DT> V;
     constexpr int NV = 2, L = 64 * WPT, AHEAD = 4;
     const uint32_t row = token_of<WPT>();
     if (row >= a.rows.start[a.nranks]) return;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
-    const uint32_t pitch = a.cols * V::ES, units = pitch / uint32_t(sizeof(X)), lane = threadIdx.x & 63;
+    const uint32_t pitch = a.cols * V::ES, units = (pitch + 15) / 16, lane = threadIdx.x & 63;
     const Choices c = choices(a, a.rows_in, r, local, pitch);
     float w = 1.f;
     if (a.weights[r] != nullptr && lane < a.topk) w = a.weights[r][local * a.topk + lane];
@@ -1057,7 +1053,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
 #pragma unroll
             for (int e = 0; e < V::n; e++) s[i][e] = 0.f;
         for (uint64_t m = c.kept; m != 0;) {
-            X x[AHEAD][NV];
+            u32x4 x[AHEAD][NV];
             float wj[AHEAD];
             bool got[AHEAD];
 #pragma unroll
@@ -1070,7 +1066,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
                 const char* y = choice_row(c, j);
 #pragma unroll
                 for (int i = 0; i < NV; i++)
-                    if (u0 + i * L < units) x[k][i] = load_at<X>(y, u0 + i * L);
+                    if (u0 + i * L < units) x[k][i] = load_at<V::ES, VEC>(y, u0 + i * L, pitch);
             }
 #pragma unroll
             for (int k = 0; k < AHEAD; k++) {
@@ -1086,22 +1082,21 @@ __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
         }
 #pragma unroll
         for (int i = 0; i < NV; i++)
-            if (u0 + i * L < units) store_at<X>(out, u0 + i * L, V::put(s[i]));
+            if (u0 + i * L < units) store_at<V::ES, VEC>(out, u0 + i * L, pitch, V::put(s[i]));
     }
 }
 
 // dy[owner][pos] = w dout[t];  dw = <dout[t], y[owner][pos]>.
 template <int DT, bool VEC, int WPT>
 __global__ __launch_bounds__(kBlock) void k_combine_backward(ExchangeRowsArgs a) {
-    typedef Values<DT, VEC> V;
-    typedef typename V::X X;
-    constexpr int NV = VEC ? 2 : 8, L = 64 * WPT;
+    typedef Values<DT> V;
+    constexpr int NV = 2, L = 64 * WPT;
     __shared__ float dots[kBlock / 64][64];
     const uint32_t row = token_of<WPT>(), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     if (row >= a.rows.start[a.nranks]) return;
     const int r = rank_of_row(a.rows, a.nranks, row);
     const uint64_t local = row - a.rows.start[r];
-    const uint32_t pitch = a.cols * V::ES, units = pitch / uint32_t(sizeof(X));
+    const uint32_t pitch = a.cols * V::ES, units = (pitch + 15) / 16;
     const Choices from = choices(a, a.rows_in, r, local, pitch), to = choices(a, a.rows_out, r, local, pitch);
     float w = 0.f;
     if (lane < a.topk) w = a.weights[r][local * a.topk + lane];
@@ -1113,17 +1108,17 @@ __global__ __launch_bounds__(kBlock) void k_combine_backward(ExchangeRowsArgs a)
         for (int i = 0; i < NV; i++) {
 #pragma unroll
             for (int e = 0; e < V::n; e++) gf[i][e] = 0.f;
-            if (u0 + i * L < units) V::get(load_at<X>(g, u0 + i * L), gf[i]);
+            if (u0 + i * L < units) V::get(load_at<V::ES, VEC>(g, u0 + i * L, pitch), gf[i]);
         }
         for (uint64_t m = from.kept; m != 0; m &= m - 1) {
             const int j = __builtin_ctzll(m);
             const float wj = __uint_as_float(uint32_t(__builtin_amdgcn_readlane(int(__float_as_uint(w)), j)));
             const char* y = choice_row(from, j);
             const char* dy = choice_row(to, j);
-            X x[NV];
+            u32x4 x[NV];
 #pragma unroll
             for (int i = 0; i < NV; i++)
-                if (u0 + i * L < units) x[i] = load_at<X>(y, u0 + i * L);
+                if (u0 + i * L < units) x[i] = load_at<V::ES, VEC>(y, u0 + i * L, pitch);
             float s = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++) {
@@ -1135,7 +1130,7 @@ __global__ __launch_bounds__(kBlock) void k_combine_backward(ExchangeRowsArgs a)
                     s += gf[i][e] * f[e];
                     o[e] = wj * gf[i][e];
                 }
-                store_at<X>(dy, u0 + i * L, V::put(o));
+                store_at<V::ES, VEC>(dy, u0 + i * L, pitch, V::put(o));
             }
             s = wave_sum(s);
             if (lane == uint32_t(j)) dot += s;

@@ -22,12 +22,13 @@
 namespace dt {
 namespace {
 
-// A lane's units of a row: 16-byte vectors, or single elements where rows are
-// off the 16-byte boundaries.
-template <int DT, bool VEC>
+// A lane's units of a row: 16 bytes.  VEC: rows start and end on 16-byte
+// boundaries; the others are read at their elements' alignment, with a last
+// unit that may be partly behind the row's end.
+template <int DT>
 struct Unit {
     typedef typename Elem<DT>::type T;
-    static constexpr int elems = VEC ? 16 / int(sizeof(T)) : 1;
+    static constexpr int elems = 16 / int(sizeof(T));
     T v[elems];
     __device__ __forceinline__ float get(int e) const { return Elem<DT>::get(v[e]); }
     __device__ __forceinline__ void put(int e, float f) { v[e] = Elem<DT>::put(f); }
@@ -38,33 +39,27 @@ struct Unit {
 struct Row {
     const char* p;
     rsrc_t r;
+    uint32_t bytes;
 };
 __device__ __forceinline__ Row row_at(const void* base, uint64_t row, uint32_t pitch) {
     const char* p = static_cast<const char*>(base) + row * pitch;
-    return Row{p, make_rsrc(p, pitch)};
+    return Row{p, make_rsrc(p, pitch), pitch};
 }
 template <int DT, bool VEC, int POL>
-__device__ __forceinline__ Unit<DT, VEC> load_unit(const Row& row, uint32_t u, uint32_t units) {
-    typedef Unit<DT, VEC> U;
-    U x;
-    if constexpr (VEC) {
-        const u32x4 v = bload16<POL>(row.r, u * 16);
-        __builtin_memcpy(x.v, &v, 16);
-    } else {
-        x.v[0] = u < units ? reinterpret_cast<const typename U::T*>(row.p)[u] : typename U::T(0);
-    }
+__device__ __forceinline__ Unit<DT> load_unit(const Row& row, uint32_t u) {
+    Unit<DT> x;
+    u32x4 v;
+    if constexpr (VEC) v = bload16<POL>(row.r, u * 16);
+    else v = load_loose<int(sizeof(typename Unit<DT>::T))>(row.p, u, row.bytes);
+    __builtin_memcpy(x.v, &v, 16);
     return x;
 }
 template <int DT, bool VEC>
-__device__ __forceinline__ void store_unit(const Row& row, uint32_t u, uint32_t units, const Unit<DT, VEC>& x) {
-    typedef Unit<DT, VEC> U;
-    if constexpr (VEC) {
-        u32x4 v;
-        __builtin_memcpy(&v, x.v, 16);
-        bstore16<kPolNT | kPolDevice>(row.r, u * 16, v);
-    } else if (u < units) {
-        const_cast<typename U::T*>(reinterpret_cast<const typename U::T*>(row.p))[u] = x.v[0];
-    }
+__device__ __forceinline__ void store_unit(const Row& row, uint32_t u, const Unit<DT>& x) {
+    u32x4 v;
+    __builtin_memcpy(&v, x.v, 16);
+    if constexpr (VEC) bstore16<kPolNT | kPolDevice>(row.r, u * 16, v);
+    else store_loose<int(sizeof(typename Unit<DT>::T))>(const_cast<char*>(row.p), u, row.bytes, v);
 }
 
 // Sum over the WPR waves that hold a row; `slot` is one of the workgroup's
@@ -91,11 +86,11 @@ struct Group {
 
 template <int DT, bool VEC, int NV, int WPR>
 __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
-    typedef Unit<DT, VEC> U;
+    typedef Unit<DT> U;
     typedef typename Elem<DT>::type T;
     constexpr int E = U::elems, L = Group<WPR>::lanes;
     __shared__ float cells[2][2][Group<WPR>::waves];
-    const uint32_t lane = threadIdx.x % L, units = a.cols / E, step = gridDim.x * Group<WPR>::rows;
+    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Group<WPR>::rows;
     const uint32_t total = a.rows.start[a.nranks];
     uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
     if (row >= total) return;
@@ -108,9 +103,9 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
         const Row xr = row_at(a.x[r], row - a.rows.start[r], pitch);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L, units);
-            b[i] = load_unit<DT, VEC, 0>(br, lane + i * L, units);
-            x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
+            w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L);
+            b[i] = load_unit<DT, VEC, 0>(br, lane + i * L);
+            x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L);
         }
     }
     const float inv = 1.f / float(a.cols);
@@ -132,17 +127,16 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
             while (next >= a.rows.start[r + 1]) r++;
             const Row xr = row_at(a.x[r], next - a.rows.start[r], pitch);
 #pragma unroll
-            for (int i = 0; i < NV; i++) x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
+            for (int i = 0; i < NV; i++) x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L);
         }
         const float mean = row_sum<WPR>(s, cells[parity][0]) * inv;
         float q = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const bool in = lane + i * L < units;
 #pragma unroll
             for (int e = 0; e < E; e++) {
                 v[i][e] -= mean;
-                q += in ? v[i][e] * v[i][e] : 0.f;
+                q += (lane + i * L) * E + e < a.cols ? v[i][e] * v[i][e] : 0.f;
             }
         }
         const float rstd = 1.f / sqrtf(row_sum<WPR>(q, cells[parity][1]) * inv + a.eps);
@@ -155,7 +149,7 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
                 const float n = v[i][e] * rstd * w[i].get(e);
                 y.put(e, biased ? n + b[i].get(e) : n);
             }
-            store_unit<DT, VEC>(to, lane + i * L, units, y);
+            store_unit<DT, VEC>(to, lane + i * L, y);
         }
         if (lane == 0 && a.mean[now] != nullptr) {
             a.mean[now][local] = mean;
@@ -167,11 +161,11 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm(NormArgs a) {
 
 template <int DT, bool VEC, int NV, int WPR>
 __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackArgs a) {
-    typedef Unit<DT, VEC> U;
+    typedef Unit<DT> U;
     typedef typename Elem<DT>::type T;
     constexpr int E = U::elems, L = Group<WPR>::lanes;
     __shared__ float cells[2][2][Group<WPR>::waves];
-    const uint32_t lane = threadIdx.x % L, units = a.cols / E, step = gridDim.x * Group<WPR>::rows;
+    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Group<WPR>::rows;
     const uint32_t total = a.rows.start[a.nranks];
     uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
     float dw[NV][E], db[NV][E];
@@ -189,9 +183,9 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
             const Row wr = row_at(a.weight[r], 0, pitch), xr = row_at(a.x[r], local, pitch), dr = row_at(a.dy[r], local, pitch);
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L, units);
-                x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
-                d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L, units);
+                w[i] = load_unit<DT, VEC, 0>(wr, lane + i * L);
+                x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L);
+                d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L);
             }
         }
         const float inv = 1.f / float(a.cols);
@@ -224,8 +218,8 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
                 const Row xr = row_at(a.x[r], local, pitch), dr = row_at(a.dy[r], local, pitch);
 #pragma unroll
                 for (int i = 0; i < NV; i++) {
-                    x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L, units);
-                    d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L, units);
+                    x[i] = load_unit<DT, VEC, kPolNT>(xr, lane + i * L);
+                    d[i] = load_unit<DT, VEC, kPolNT>(dr, lane + i * L);
                 }
             }
             s1 = wave_sum(s1);
@@ -249,7 +243,7 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
                 U o;
 #pragma unroll
                 for (int e = 0; e < E; e++) o.put(e, scale * (g[i][e] - m1 - n[i][e] * m2));
-                store_unit<DT, VEC>(to, lane + i * L, units, o);
+                store_unit<DT, VEC>(to, lane + i * L, o);
             }
             row = next;
         }
@@ -279,12 +273,12 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
     } else {
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            const uint32_t u = lane + i * L;
-            if (u >= units) continue;
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                strip[u * E + e] = dw[i][e];
-                strip[a.cols + u * E + e] = db[i][e];
+                const uint32_t c = (lane + i * L) * E + e;
+                if (c >= a.cols) continue;
+                strip[c] = dw[i][e];
+                strip[a.cols + c] = db[i][e];
             }
         }
     }
@@ -419,46 +413,28 @@ __global__ __launch_bounds__(1024) void k_norm_fold(NormBackArgs a) {
 struct Hold {
     int nv, wpr;   // wpr 0: too wide
 };
-Hold hold(uint32_t units, bool vec) {
-    if (vec) {
-        if (units <= 64) return {1, 1};
-        if (units <= 128) return {2, 1};
-        if (units <= 256) return {1, 4};
-        if (units <= 512) return {2, 4};
-        if (units <= 1024) return {4, 4};
-        if (units <= 2048) return {2, 16};
-        if (units <= 4096) return {4, 16};
-        return {0, 0};
-    }
-    if (units <= 256) return {4, 1};
-    if (units <= 512) return {8, 1};
+Hold hold(uint32_t units) {
+    if (units <= 64) return {1, 1};
+    if (units <= 128) return {2, 1};
+    if (units <= 256) return {1, 4};
+    if (units <= 512) return {2, 4};
     if (units <= 1024) return {4, 4};
-    if (units <= 2048) return {8, 4};
-    if (units <= 4096) return {16, 4};
-    if (units <= 16384) return {16, 16};
+    if (units <= 2048) return {2, 16};
+    if (units <= 4096) return {4, 16};
     return {0, 0};
 }
 // run(constant NV, constant WPR)
-template <bool VEC, typename F>
+template <typename F>
 void with_hold(Hold h, F&& run) {
 #define DT_HOLD(n, w) \
     if (h.nv == n && h.wpr == w) return run(std::integral_constant<int, n>(), std::integral_constant<int, w>())
-    if constexpr (VEC) {
-        DT_HOLD(1, 1);
-        DT_HOLD(2, 1);
-        DT_HOLD(1, 4);
-        DT_HOLD(2, 4);
-        DT_HOLD(4, 4);
-        DT_HOLD(2, 16);
-        DT_HOLD(4, 16);
-    } else {
-        DT_HOLD(4, 1);
-        DT_HOLD(8, 1);
-        DT_HOLD(4, 4);
-        DT_HOLD(8, 4);
-        DT_HOLD(16, 4);
-        DT_HOLD(16, 16);
-    }
+    DT_HOLD(1, 1);
+    DT_HOLD(2, 1);
+    DT_HOLD(1, 4);
+    DT_HOLD(2, 4);
+    DT_HOLD(4, 4);
+    DT_HOLD(2, 16);
+    DT_HOLD(4, 16);
 #undef DT_HOLD
 }
 
@@ -480,11 +456,11 @@ bool aligned(const void* const* list, int n) {
 template <int DT, bool VEC>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold(a.cols / Unit<DT, VEC>::elems, VEC);
+    const Hold h = hold((a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems);
     if (h.wpr == 0) {
         hipLaunchKernelGGL(k_norm_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
     } else {
-        with_hold<VEC>(h, [&](auto nv, auto wpr) {
+        with_hold(h, [&](auto nv, auto wpr) {
             constexpr int W = decltype(wpr)::value;
             hipLaunchKernelGGL((k_norm<DT, VEC, decltype(nv)::value, W>), dim3(workgroups(rows, W)), dim3(Group<W>::threads), 0, s, a);
         });
@@ -495,14 +471,14 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
 template <int DT, bool VEC>
 hipError_t norm_backward(NormBackArgs a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold(a.cols / Unit<DT, VEC>::elems, VEC);
+    const Hold h = hold((a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems);
     a.strips = 0;
     if (rows > 0 && h.wpr == 0) {
         a.strips = rows < 256 ? rows : 256;
         hipLaunchKernelGGL(k_norm_dx_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
         hipLaunchKernelGGL(k_norm_dw_wide<DT>, dim3((a.cols + kBlock - 1) / kBlock, a.strips), dim3(kBlock), 0, s, a);
     } else if (rows > 0) {
-        with_hold<VEC>(h, [&](auto nv, auto wpr) {
+        with_hold(h, [&](auto nv, auto wpr) {
             constexpr int W = decltype(wpr)::value;
             a.strips = workgroups(rows, W) < 512 ? workgroups(rows, W) : 512;
             hipLaunchKernelGGL((k_norm_backward<DT, VEC, decltype(nv)::value, W>), dim3(a.strips), dim3(Group<W>::threads), 0, s, a);

@@ -79,16 +79,75 @@ __device__ __forceinline__ void store_loose(char* row, uint32_t u, uint32_t byte
     }
 }
 
-// Sums and maxima over the wave's 64 lanes, the same value in every lane.
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
+// Reductions over 16 neighbouring lanes, the same value in all of them: neighbours, pairs, halves of eight, then the two eights.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
+}
+constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140, kRotate = 0x120;
+template <typename F>
+__device__ __forceinline__ void over16(F&& step) {
+    step(std::integral_constant<int, kSwap1>());
+    step(std::integral_constant<int, kSwap2>());
+    step(std::integral_constant<int, kHalfMirror>());
+    step(std::integral_constant<int, kMirror>());
+}
+// The other 15 lanes' values, one rotation at a time.
+template <typename F>
+__device__ __forceinline__ void rotations(F&& step) {
+    step(std::integral_constant<int, kRotate + 1>());
+    step(std::integral_constant<int, kRotate + 2>());
+    step(std::integral_constant<int, kRotate + 3>());
+    step(std::integral_constant<int, kRotate + 4>());
+    step(std::integral_constant<int, kRotate + 5>());
+    step(std::integral_constant<int, kRotate + 6>());
+    step(std::integral_constant<int, kRotate + 7>());
+    step(std::integral_constant<int, kRotate + 8>());
+    step(std::integral_constant<int, kRotate + 9>());
+    step(std::integral_constant<int, kRotate + 10>());
+    step(std::integral_constant<int, kRotate + 11>());
+    step(std::integral_constant<int, kRotate + 12>());
+    step(std::integral_constant<int, kRotate + 13>());
+    step(std::integral_constant<int, kRotate + 14>());
+    step(std::integral_constant<int, kRotate + 15>());
+}
+__device__ __forceinline__ float max16(float v) {
+    over16([&](auto c) { v = fmaxf(v, dpp<decltype(c)::value>(v)); });
     return v;
 }
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor(v, m));
+__device__ __forceinline__ int32_t max16(int32_t v) {
+    over16([&](auto c) {
+        const int32_t o = int32_t(dpp<decltype(c)::value>(uint32_t(v)));
+        v = o > v ? o : v;
+    });
     return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+    over16([&](auto c) { v += dpp<decltype(c)::value>(v); });
+    return v;
+}
+__device__ __forceinline__ uint32_t min16(uint32_t v) {
+    over16([&](auto c) {
+        const uint32_t o = dpp<decltype(c)::value>(v);
+        v = o < v ? o : v;
+    });
+    return v;
+}
+
+// Sums and maxima over the wave's 64 lanes, the same value in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = sum16(v);
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+__device__ __forceinline__ float wave_max(float v) {
+    v = max16(v);
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
 }
 
 // Sum over a workgroup of WAVES waves in a fixed order, the same value in

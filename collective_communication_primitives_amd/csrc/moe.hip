@@ -184,66 +184,6 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     }
 }
 
-// Reductions over the 16 lanes that share a token, the same value in all of
-// them: neighbours, pairs, halves of eight, then the two eights.
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
-}
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-    return __uint_as_float(dpp<CTRL>(__float_as_uint(v)));
-}
-constexpr int kSwap1 = 0xB1, kSwap2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140, kRotate = 0x120;
-template <typename F>
-__device__ __forceinline__ void over16(F&& step) {
-    step(std::integral_constant<int, kSwap1>());
-    step(std::integral_constant<int, kSwap2>());
-    step(std::integral_constant<int, kHalfMirror>());
-    step(std::integral_constant<int, kMirror>());
-}
-// The other 15 lanes' values, one rotation at a time.
-template <typename F>
-__device__ __forceinline__ void rotations(F&& step) {
-    step(std::integral_constant<int, kRotate + 1>());
-    step(std::integral_constant<int, kRotate + 2>());
-    step(std::integral_constant<int, kRotate + 3>());
-    step(std::integral_constant<int, kRotate + 4>());
-    step(std::integral_constant<int, kRotate + 5>());
-    step(std::integral_constant<int, kRotate + 6>());
-    step(std::integral_constant<int, kRotate + 7>());
-    step(std::integral_constant<int, kRotate + 8>());
-    step(std::integral_constant<int, kRotate + 9>());
-    step(std::integral_constant<int, kRotate + 10>());
-    step(std::integral_constant<int, kRotate + 11>());
-    step(std::integral_constant<int, kRotate + 12>());
-    step(std::integral_constant<int, kRotate + 13>());
-    step(std::integral_constant<int, kRotate + 14>());
-    step(std::integral_constant<int, kRotate + 15>());
-}
-__device__ __forceinline__ float max16(float v) {
-    over16([&](auto c) { v = fmaxf(v, dpp<decltype(c)::value>(v)); });
-    return v;
-}
-__device__ __forceinline__ int32_t max16(int32_t v) {
-    over16([&](auto c) {
-        const int32_t o = int32_t(dpp<decltype(c)::value>(uint32_t(v)));
-        v = o > v ? o : v;
-    });
-    return v;
-}
-__device__ __forceinline__ float sum16(float v) {
-    over16([&](auto c) { v += dpp<decltype(c)::value>(v); });
-    return v;
-}
-__device__ __forceinline__ uint32_t min16(uint32_t v) {
-    over16([&](auto c) {
-        const uint32_t o = dpp<decltype(c)::value>(v);
-        v = o < v ? o : v;
-    });
-    return v;
-}
-
 constexpr float kBiggest = 3.402823466e38f;
 
 // Floats as integers of the same order (no NaN, no -0), and back: integer
@@ -294,7 +234,7 @@ __device__ __forceinline__ void load_bias(const float* bias, uint32_t nexperts, 
 }
 
 // max over the 16 lanes of 64-bit keys.
-__device__ __forceinline__ int64_t max16(int64_t v) {
+__device__ __forceinline__ int64_t max16_wide(int64_t v) {
     over16([&](auto c) {
         const uint64_t u = uint64_t(v);
         const uint64_t o = uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u));
@@ -428,7 +368,7 @@ __device__ __forceinline__ uint32_t choose_exactly(const RouteToken& a, const ty
         int64_t best = key[0];
 #pragma unroll
         for (int i = 1; i < NL; i++) best = key[i] > best ? key[i] : best;
-        best = max16(best);
+        best = max16_wide(best);
         uint32_t at = UINT32_MAX;
 #pragma unroll
         for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? a.first + i : at;

@@ -284,6 +284,153 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_norm_backward(NormBackA
     }
 }
 
+// Rows of at most 16 units: 16 lanes per row, four rows to a wave.
+constexpr uint32_t kNarrowRows = kBlock / 16;  // rows in flight in a workgroup
+
+template <int DT, bool VEC>
+__device__ __forceinline__ Unit<DT> narrow_unit(const void* base, uint64_t row, uint32_t pitch, uint32_t u) {
+    Unit<DT> x;
+    u32x4 v = {0, 0, 0, 0};
+    const char* p = static_cast<const char*>(base) + row * pitch;
+    if constexpr (VEC) {
+        if (u * 16 < pitch) v = load16(p + u * 16);
+    } else {
+        v = load_loose<int(sizeof(typename Unit<DT>::T))>(p, u, pitch);
+    }
+    __builtin_memcpy(x.v, &v, 16);
+    return x;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void narrow_store(void* base, uint64_t row, uint32_t pitch, uint32_t u, const Unit<DT>& x) {
+    u32x4 v;
+    __builtin_memcpy(&v, x.v, 16);
+    char* p = static_cast<char*>(base) + row * pitch;
+    if constexpr (VEC) {
+        if (u * 16 < pitch) store16(p + u * 16, v);
+    } else {
+        store_loose<int(sizeof(typename Unit<DT>::T))>(p, u, pitch, v);
+    }
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kBlock) void k_norm_narrow(NormArgs a) {
+    typedef Unit<DT> U;
+    constexpr int E = U::elems;
+    const uint32_t u = threadIdx.x & 15, total = a.rows.start[a.nranks], step = gridDim.x * kNarrowRows;
+    const uint32_t pitch = a.cols * uint32_t(sizeof(typename U::T));
+    uint32_t row = blockIdx.x * kNarrowRows + (threadIdx.x >> 4);
+    int r = 0;
+    while (r + 1 < a.nranks && row >= a.rows.start[r + 1]) r++;
+    if (row >= total) return;  // whole rows of lanes leave together
+    const U w = narrow_unit<DT, VEC>(a.weight[r], 0, pitch, u);
+    const bool biased = a.bias[r] != nullptr;
+    const U b = narrow_unit<DT, VEC>(biased ? a.bias[r] : a.weight[r], 0, pitch, u);
+    U x = narrow_unit<DT, VEC>(a.x[r], row - a.rows.start[r], pitch, u);
+    const float inv = 1.f / float(a.cols);
+    while (row < total) {
+        float v[E], s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            v[e] = x.get(e);
+            s += v[e];
+        }
+        const int now = r;
+        const uint64_t local = row - a.rows.start[now];
+        row += step;
+        if (row < total) {
+            while (row >= a.rows.start[r + 1]) r++;
+            x = narrow_unit<DT, VEC>(a.x[r], row - a.rows.start[r], pitch, u);
+        }
+        const float mean = sum16(s) * inv;
+        float q = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            v[e] -= mean;
+            q += u * E + e < a.cols ? v[e] * v[e] : 0.f;
+        }
+        const float rstd = 1.f / sqrtf(sum16(q) * inv + a.eps);
+        U y;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            const float n = v[e] * rstd * w.get(e);
+            y.put(e, biased ? n + b.get(e) : n);
+        }
+        narrow_store<DT, VEC>(a.y[now], local, pitch, u, y);
+        if (u == 0 && a.mean[now] != nullptr) {
+            a.mean[now][local] = mean;
+            a.rstd[now][local] = rstd;
+        }
+    }
+}
+
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kBlock) void k_norm_backward_narrow(NormBackArgs a) {
+    typedef Unit<DT> U;
+    constexpr int E = U::elems;
+    __shared__ float sums[2][kNarrowRows][16 * E];
+    const uint32_t u = threadIdx.x & 15, total = a.rows.start[a.nranks], step = gridDim.x * kNarrowRows;
+    const uint32_t pitch = a.cols * uint32_t(sizeof(typename U::T));
+    uint32_t row = blockIdx.x * kNarrowRows + (threadIdx.x >> 4);
+    int r = 0;
+    while (r + 1 < a.nranks && row >= a.rows.start[r + 1]) r++;
+    float dw[E], db[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) dw[e] = db[e] = 0.f;
+    if (row < total) {
+        const U w = narrow_unit<DT, VEC>(a.weight[r], 0, pitch, u);
+        uint64_t local = row - a.rows.start[r];
+        U x = narrow_unit<DT, VEC>(a.x[r], local, pitch, u), d = narrow_unit<DT, VEC>(a.dy[r], local, pitch, u);
+        float mean = a.mean[r][local], rstd = a.rstd[r][local];
+        const float inv = 1.f / float(a.cols);
+        while (row < total) {
+            float n[E], g[E], s1 = 0.f, s2 = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                // past the row's end dy is 0, and nothing is added to any sum
+                const float dy = d.get(e);
+                n[e] = (x.get(e) - mean) * rstd;
+                g[e] = dy * w.get(e);
+                s1 += g[e];
+                s2 += g[e] * n[e];
+                dw[e] += dy * n[e];
+                db[e] += dy;
+            }
+            const int now = r;
+            const uint64_t at = local;
+            const float scale = rstd;
+            row += step;
+            if (row < total) {
+                while (row >= a.rows.start[r + 1]) r++;
+                local = row - a.rows.start[r];
+                x = narrow_unit<DT, VEC>(a.x[r], local, pitch, u);
+                d = narrow_unit<DT, VEC>(a.dy[r], local, pitch, u);
+                mean = a.mean[r][local];
+                rstd = a.rstd[r][local];
+            }
+            const float m1 = sum16(s1) * inv, m2 = sum16(s2) * inv;
+            U o;
+#pragma unroll
+            for (int e = 0; e < E; e++) o.put(e, scale * (g[e] - m1 - n[e] * m2));
+            narrow_store<DT, VEC>(a.dx[now], at, pitch, u, o);
+        }
+    }
+    // the workgroup's strip: its 16 groups' sums in order
+#pragma unroll
+    for (int e = 0; e < E; e++) {
+        sums[0][threadIdx.x >> 4][u * E + e] = dw[e];
+        sums[1][threadIdx.x >> 4][u * E + e] = db[e];
+    }
+    __syncthreads();
+    float* strip = a.partial + uint64_t(blockIdx.x) * 2 * a.cols;
+    for (uint32_t c = threadIdx.x; c < 2 * 16 * E; c += kBlock) {
+        const uint32_t which = c / (16 * E), col = c % (16 * E);
+        float s = 0.f;
+#pragma unroll
+        for (uint32_t k = 0; k < kNarrowRows; k++) s += sums[which][k][col];
+        if (col < a.cols) strip[which * a.cols + col] = s;
+    }
+}
+
 // Rows too wide for the registers: a workgroup per row that reads it again for
 // each sum, and the columns' sums strip by strip.
 template <int DT>
@@ -438,14 +585,27 @@ void with_hold(Hold h, F&& run) {
 #undef DT_HOLD
 }
 
-// Workgroups that walk over the rows: two per CU, all resident at once (four of
-// the small ones).  Forward, 8 x 4096 rows of 8192 bf16: 512 workgroups 191 us,
-// 768 (three per CU) 199, 1024 (a second, partial round) 222, 256 267, one per
-// row 201; backward, cols 4096: 512 145 us, 768 159, 256 191.
-uint32_t workgroups(uint32_t rows, int wpr) {
-    const uint32_t need = wpr == 1 ? (rows + 3) / 4 : rows, most = wpr == 1 ? 1024 : 512;
+// Workgroups that walk over the rows, from sweeps on 16 MiB .. 512 MiB of data.
+// Forward: rows held in up to two units per lane run best with many
+// workgroups (32768 x 4096 bf16: 512 workgroups 136 us, 2048 111, 4096 101);
+// larger holds with two per CU, all resident at once (8 x 4096 rows of 8192
+// bf16: 512 191 us, 768 199, 1024 222).
+uint32_t forward_workgroups(uint32_t rows, Hold h) {
+    const uint32_t need = h.wpr == 1 ? (rows + 3) / 4 : rows, most = h.nv <= 2 && h.wpr <= 4 ? 4096 : 512;
     return need < most ? need : most;
 }
+// Backward: every workgroup costs a strip of partial sums, written and read
+// again.  Two workgroups per CU (32768 x 4096 bf16: 512 146 us, 768 159, 256
+// 191), four where the strips are short and the rows many (262144 x 512: 1024
+// 139 us, 512 150), one where they are long.
+uint32_t backward_workgroups(uint32_t rows, Hold h) {
+    const uint32_t need = h.wpr == 1 ? (rows + 3) / 4 : rows;
+    uint32_t most = h.wpr == 16 ? 256 : 512;
+    if (h.wpr <= 4 && h.nv == 1 && need >= 16 * 1024) most = 1024;
+    if (need < 4 * most) most = (need + 3) / 4;  // at least four rows (2000 x 1001 fp32: 19 us; two 20, eight 22)
+    return need < most ? need : most;
+}
+constexpr uint32_t kMostStrips = 1024;
 
 bool aligned(const void* const* list, int n) {
     for (int r = 0; r < n; r++)
@@ -456,13 +616,17 @@ bool aligned(const void* const* list, int n) {
 template <int DT, bool VEC>
 hipError_t norm(const NormArgs& a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold((a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems);
-    if (h.wpr == 0) {
+    const uint32_t units = (a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems;
+    const Hold h = hold(units);
+    if (units <= 16) {
+        const uint32_t need = (rows + kNarrowRows - 1) / kNarrowRows;
+        hipLaunchKernelGGL((k_norm_narrow<DT, VEC>), dim3(need < 4096 ? need : 4096), dim3(kBlock), 0, s, a);
+    } else if (h.wpr == 0) {
         hipLaunchKernelGGL(k_norm_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
     } else {
         with_hold(h, [&](auto nv, auto wpr) {
             constexpr int W = decltype(wpr)::value;
-            hipLaunchKernelGGL((k_norm<DT, VEC, decltype(nv)::value, W>), dim3(workgroups(rows, W)), dim3(Group<W>::threads), 0, s, a);
+            hipLaunchKernelGGL((k_norm<DT, VEC, decltype(nv)::value, W>), dim3(forward_workgroups(rows, h)), dim3(Group<W>::threads), 0, s, a);
         });
     }
     return hipGetLastError();
@@ -471,16 +635,21 @@ hipError_t norm(const NormArgs& a, hipStream_t s) {
 template <int DT, bool VEC>
 hipError_t norm_backward(NormBackArgs a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold((a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems);
+    const uint32_t units = (a.cols + Unit<DT>::elems - 1) / Unit<DT>::elems;
+    const Hold h = hold(units);
     a.strips = 0;
-    if (rows > 0 && h.wpr == 0) {
+    if (rows > 0 && units <= 16) {
+        const uint32_t need = (rows + kNarrowRows - 1) / kNarrowRows;
+        a.strips = need < kMostStrips ? need : kMostStrips;
+        hipLaunchKernelGGL((k_norm_backward_narrow<DT, VEC>), dim3(a.strips), dim3(kBlock), 0, s, a);
+    } else if (rows > 0 && h.wpr == 0) {
         a.strips = rows < 256 ? rows : 256;
         hipLaunchKernelGGL(k_norm_dx_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
         hipLaunchKernelGGL(k_norm_dw_wide<DT>, dim3((a.cols + kBlock - 1) / kBlock, a.strips), dim3(kBlock), 0, s, a);
     } else if (rows > 0) {
         with_hold(h, [&](auto nv, auto wpr) {
             constexpr int W = decltype(wpr)::value;
-            a.strips = workgroups(rows, W) < 512 ? workgroups(rows, W) : 512;
+            a.strips = backward_workgroups(rows, h);
             hipLaunchKernelGGL((k_norm_backward<DT, VEC, decltype(nv)::value, W>), dim3(a.strips), dim3(Group<W>::threads), 0, s, a);
         });
     }
@@ -499,7 +668,7 @@ hipError_t launch_norm(const NormArgs& a, int dtype, hipStream_t s) {
     return vec ? norm<kF32, true>(a, s) : norm<kF32, false>(a, s);
 }
 
-uint32_t norm_strips(uint32_t rows, uint32_t) { return rows < 512 ? rows : 512; }
+uint32_t norm_strips(uint32_t rows, uint32_t) { return rows < kMostStrips ? rows : kMostStrips; }
 
 hipError_t launch_norm_backward(const NormBackArgs& a, int dtype, hipStream_t s) {
     const bool vec = rows_aligned(a.cols, dtype) && aligned(a.x, a.nranks) && aligned(a.dy, a.nranks) &&

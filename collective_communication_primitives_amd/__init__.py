@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import atexit
 import ctypes
+import operator
 import threading
 import weakref
 from typing import Dict, List, Optional, Sequence
@@ -622,23 +623,55 @@ DT_MAX_EXPERTS, DT_MAX_TOPK = 1024, 64
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _rank_list(name: str, tensors, p: int, dtype, dev: int, sizes) -> list:
-    """``tensors`` as a list of p contiguous tensors of ``dtype`` on the
-    current GPU with sizes[r] elements each (sizes: one number for all)."""
-    tensors = list(tensors)
+_POINTERS = [ctypes.c_void_p * max(1, n) for n in range(DT_MAX_RANKS + 1)]
+_SIZES = [ctypes.c_size_t * max(1, n) for n in range(DT_MAX_RANKS + 1)]
+
+
+def _refuse(name: str, r: int, t, dtype, dev: int, want: int) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name}[{r}] must be {dtype}, got {t.dtype}")
+    if t.numel() != want:
+        raise ValueError(f"{name}[{r}] must hold {want} elements, got {t.numel()}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}[{r}] must live on the current GPU (cuda:{dev}), got {t.device}")
+    raise ValueError(f"{name}[{r}] must be contiguous")
+
+
+_dtype_of = operator.attrgetter("dtype")
+_numel, _device_of, _contiguous, _data_ptr = (torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous,
+                                              torch.Tensor.data_ptr)
+
+
+def _buffers(name: str, tensors, sizes, dtype, dev: int, stash: list):
+    """The pointers of a list of contiguous tensors of ``dtype`` on the current
+    GPU, rank r's with sizes[r] elements; the tensors join ``stash``.  (Whole
+    lists go through map(): half the time of a loop over the tensors.)"""
+    p = len(sizes)
     if len(tensors) != p:
         raise ValueError(f"{name} must list one tensor per rank ({p}), got {len(tensors)}")
-    for r, t in enumerate(tensors):
-        if t.dtype != dtype:
-            raise TypeError(f"{name}[{r}] must be {dtype}, got {t.dtype}")
-        if t.numel() != (sizes if isinstance(sizes, int) else sizes[r]):
-            want = sizes if isinstance(sizes, int) else sizes[r]
-            raise ValueError(f"{name}[{r}] must hold {want} elements, got {t.numel()}")
-        if t.get_device() != dev:
-            raise ValueError(f"{name}[{r}] must live on the current GPU (cuda:{dev}), got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{r}] must be contiguous")
-    return tensors
+    if (list(map(_numel, tensors)) != sizes or list(map(_device_of, tensors)) != [dev] * p
+            or not all(map(_contiguous, tensors)) or list(map(_dtype_of, tensors)) != [dtype] * p):
+        for r, (t, n) in enumerate(zip(tensors, sizes)):
+            if t.dtype != dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+                _refuse(name, r, t, dtype, dev, n)
+    stash += tensors
+    return _POINTERS[p](*map(_data_ptr, tensors))
+
+
+def _ranks(tensors, name: str) -> int:
+    p = len(tensors)
+    if not 1 <= p <= DT_MAX_RANKS:
+        raise ValueError(f"{name} must list 1 to {DT_MAX_RANKS} ranks' tensors, got {p}")
+    return p
+
+
+def _row_counts(tensors, cols: int, name: str):
+    """(elements, rows) of each tensor, whole rows of ``cols``."""
+    sizes = list(map(_numel, tensors))
+    rows = [n // cols for n in sizes]
+    if sum(rows) * cols != sum(sizes):
+        raise ValueError(f"{name} must hold whole rows of {cols} elements")
+    return sizes, rows
 
 
 def _float_dtype(t: torch.Tensor) -> int:
@@ -647,7 +680,8 @@ def _float_dtype(t: torch.Tensor) -> int:
     return _DTYPES[t.dtype]
 
 
-def _workspace(given: Optional[torch.Tensor], nbytes: int, dev: int, stream, async_op: bool, comm_stream) -> torch.Tensor:
+def _workspace(given: Optional[torch.Tensor], nbytes: int, dev: int, stream, async_op: bool, comm_stream,
+               stash: list) -> torch.Tensor:
     """The call's workspace: the caller's, or a block of torch's caching
     allocator that is not reused before the stream that runs the call has
     passed it."""
@@ -655,13 +689,15 @@ def _workspace(given: Optional[torch.Tensor], nbytes: int, dev: int, stream, asy
         _on_gpu([given], "workspace")
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace must hold {nbytes} bytes, got {given.numel() * given.element_size()}")
+        stash.append(given)
         return given
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=f"cuda:{dev}")
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
     runs_on = (comm_stream if comm_stream is not None else side_stream(dev)) if async_op else stream
     if runs_on is not None:
         if isinstance(runs_on, int):
             runs_on = torch.cuda.ExternalStream(runs_on, device=dev)
         ws.record_stream(runs_on)
+    stash.append(ws)
     return ws
 
 
@@ -692,24 +728,18 @@ def dt_layer_norm(x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], bia
     """Layer norm of every rank's rows x[r] [..., cols] into y[r]; weight[r],
     bias[r] (None: no bias) hold ``cols`` elements.  mean[r], rstd[r] (fp32,
     one per row) keep the statistics for dt_layer_norm_backward."""
-    x = list(x)
-    p, dev, cols = len(x), torch.cuda.current_device(), _width(weight[0], "weight")
-    code, dtype = _float_dtype(x[0]), x[0].dtype
-    sizes = [t.numel() for t in x]
-    rows = [n // cols for n in sizes]
-    if any(n % cols for n in sizes):
-        raise ValueError(f"x must hold whole rows of {cols} elements")
+    p, dev, cols = _ranks(x, "x"), torch.cuda.current_device(), _width(weight[0], "weight")
+    code, dtype, stash = _float_dtype(x[0]), x[0].dtype, []
+    sizes, rows = _row_counts(x, cols, "x")
     if (mean is None) != (rstd is None):
         raise ValueError("mean and rstd come together")
-    stash = _rank_list("x", x, p, dtype, dev, sizes) + _rank_list("weight", weight, p, dtype, dev, cols)
-    stash += _rank_list("y", y, p, dtype, dev, sizes)
-    if bias is not None:
-        stash += _rank_list("bias", bias, p, dtype, dev, cols)
+    xs, ys = _buffers("x", x, sizes, dtype, dev, stash), _buffers("y", y, sizes, dtype, dev, stash)
+    ws = _buffers("weight", weight, [cols] * p, dtype, dev, stash)
+    bs = _buffers("bias", bias, [cols] * p, dtype, dev, stash) if bias is not None else None
+    ms = rs = None
     if mean is not None:
-        stash += _rank_list("mean", mean, p, torch.float32, dev, rows) + _rank_list("rstd", rstd, p, torch.float32, dev, rows)
-    xs, ws, ys, n = _ptr_array(x), _ptr_array(weight), _ptr_array(y), _size_array(rows)
-    bs = _ptr_array(bias) if bias is not None else None
-    ms, rs = (_ptr_array(mean), _ptr_array(rstd)) if mean is not None else (None, None)
+        ms, rs = _buffers("mean", mean, rows, torch.float32, dev, stash), _buffers("rstd", rstd, rows, torch.float32, dev, stash)
+    n = _SIZES[p](*rows)
     w = _launch(lambda st: _L.dt_layer_norm(xs, ws, bs, ys, ms, rs, p, n, cols, eps, code, st), stash, async_op, stream,
                 comm_stream)
     return w if async_op else y
@@ -722,28 +752,20 @@ def dt_layer_norm_backward(dy: Sequence[torch.Tensor], x: Sequence[torch.Tensor]
                            comm_stream=None):
     """Gradients of dt_layer_norm: dx[r], and dweight[q], dbias[q] (None: not
     formed) summed over the rows of all ranks, for every rank q."""
-    x = list(x)
-    p, dev, cols = len(x), torch.cuda.current_device(), _width(weight[0], "weight")
-    code, dtype = _float_dtype(x[0]), x[0].dtype
-    sizes = [t.numel() for t in x]
-    rows = [n // cols for n in sizes]
-    if any(n % cols for n in sizes):
-        raise ValueError(f"x must hold whole rows of {cols} elements")
-    stash = _rank_list("x", x, p, dtype, dev, sizes) + _rank_list("dy", dy, p, dtype, dev, sizes)
-    stash += _rank_list("weight", weight, p, dtype, dev, cols) + _rank_list("dx", dx, p, dtype, dev, sizes)
-    stash += _rank_list("mean", mean, p, torch.float32, dev, rows) + _rank_list("rstd", rstd, p, torch.float32, dev, rows)
-    stash += _rank_list("dweight", dweight, p, dtype, dev, cols)
-    if dbias is not None:
-        stash += _rank_list("dbias", dbias, p, dtype, dev, cols)
-    n = _size_array(rows)
-    nbytes = _sized(_L.dt_layer_norm_workspace(p, n, cols))
-    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
-    gs, xs, ws, ds = _ptr_array(dy), _ptr_array(x), _ptr_array(weight), _ptr_array(dx)
-    ms, rs, dw = _ptr_array(mean), _ptr_array(rstd), _ptr_array(dweight)
-    db = _ptr_array(dbias) if dbias is not None else None
+    p, dev, cols = _ranks(x, "x"), torch.cuda.current_device(), _width(weight[0], "weight")
+    code, dtype, stash = _float_dtype(x[0]), x[0].dtype, []
+    sizes, rows = _row_counts(x, cols, "x")
+    wide = [cols] * p
+    xs, gs = _buffers("x", x, sizes, dtype, dev, stash), _buffers("dy", dy, sizes, dtype, dev, stash)
+    ds, ws = _buffers("dx", dx, sizes, dtype, dev, stash), _buffers("weight", weight, wide, dtype, dev, stash)
+    ms, rs = _buffers("mean", mean, rows, torch.float32, dev, stash), _buffers("rstd", rstd, rows, torch.float32, dev, stash)
+    dw = _buffers("dweight", dweight, wide, dtype, dev, stash)
+    db = _buffers("dbias", dbias, wide, dtype, dev, stash) if dbias is not None else None
+    n = _SIZES[p](*rows)
+    space = _workspace(workspace, _sized(_L.dt_layer_norm_workspace(p, n, cols)), dev, stream, async_op, comm_stream, stash)
     at, have = space.data_ptr(), space.numel() * space.element_size()
-    w = _launch(lambda st: _L.dt_layer_norm_backward(gs, xs, ws, ms, rs, ds, dw, db, p, n, cols, code, at, have, st),
-                stash + [space], async_op, stream, comm_stream)
+    w = _launch(lambda st: _L.dt_layer_norm_backward(gs, xs, ws, ms, rs, ds, dw, db, p, n, cols, code, at, have, st), stash,
+                async_op, stream, comm_stream)
     return w if async_op else dx
 
 
@@ -757,20 +779,17 @@ def dt_moe_route(logits: Sequence[torch.Tensor], experts: Sequence[torch.Tensor]
     """Routing: experts[r] int32 and weights[r] fp32 [tokens, topk] from
     logits[r] [tokens, nexperts]; see dt.h for the order and what -inf, NaN
     and ties do.  ``bias`` (fp32 [nexperts]) moves the choice, not the weights."""
-    logits = list(logits)
-    p, dev = len(logits), torch.cuda.current_device()
-    e, k = _width(logits[0], "logits"), _width(experts[0], "experts")
-    code = _float_dtype(logits[0])
-    tokens = [t.numel() // e for t in logits]
+    p, dev = _ranks(logits, "logits"), torch.cuda.current_device()
+    e, k, stash = _width(logits[0], "logits"), _width(experts[0], "experts"), []
+    code, dtype = _float_dtype(logits[0]), logits[0].dtype
+    sizes, tokens = _row_counts(logits, e, "logits")
     slots = [t * k for t in tokens]
-    stash = _rank_list("logits", logits, p, logits[0].dtype, dev, [t * e for t in tokens])
-    stash += _rank_list("experts", experts, p, torch.int32, dev, slots)
-    stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
+    ls, es = _buffers("logits", logits, sizes, dtype, dev, stash), _buffers("experts", experts, slots, torch.int32, dev, stash)
+    ws, n = _buffers("weights", weights, slots, torch.float32, dev, stash), _SIZES[p](*tokens)
     b = None
     if bias is not None:
-        stash += _rank_list("bias", [bias], 1, torch.float32, dev, e)
+        _buffers("bias", [bias], [e], torch.float32, dev, stash)
         b = bias.data_ptr()
-    ls, es, ws, n = _ptr_array(logits), _ptr_array(experts), _ptr_array(weights), _size_array(tokens)
     sc, rn = _score_code(score), int(bool(renormalize))
     w = _launch(lambda st: _L.dt_moe_route(ls, es, ws, p, n, e, k, b, groups, topk_groups, sc, rn, scale, code, st),
                 stash, async_op, stream, comm_stream)
@@ -782,17 +801,14 @@ def dt_moe_route_backward(logits: Sequence[torch.Tensor], experts: Sequence[torc
                           renormalize: bool = True, scale: float = 1.0, stream=None, async_op: bool = False,
                           comm_stream=None):
     """dlogits[r] from the gradient of dt_moe_route's weights, for its choice."""
-    logits = list(logits)
-    p, dev = len(logits), torch.cuda.current_device()
-    e, k = _width(logits[0], "logits"), _width(experts[0], "experts")
+    p, dev = _ranks(logits, "logits"), torch.cuda.current_device()
+    e, k, stash = _width(logits[0], "logits"), _width(experts[0], "experts"), []
     code, dtype = _float_dtype(logits[0]), logits[0].dtype
-    tokens = [t.numel() // e for t in logits]
-    sizes, slots = [t * e for t in tokens], [t * k for t in tokens]
-    stash = _rank_list("logits", logits, p, dtype, dev, sizes) + _rank_list("dlogits", dlogits, p, dtype, dev, sizes)
-    stash += _rank_list("experts", experts, p, torch.int32, dev, slots)
-    stash += _rank_list("dweights", dweights, p, torch.float32, dev, slots)
-    ls, es, gs, ds = _ptr_array(logits), _ptr_array(experts), _ptr_array(dweights), _ptr_array(dlogits)
-    n, sc, rn = _size_array(tokens), _score_code(score), int(bool(renormalize))
+    sizes, tokens = _row_counts(logits, e, "logits")
+    slots = [t * k for t in tokens]
+    ls, ds = _buffers("logits", logits, sizes, dtype, dev, stash), _buffers("dlogits", dlogits, sizes, dtype, dev, stash)
+    es, gs = _buffers("experts", experts, slots, torch.int32, dev, stash), _buffers("dweights", dweights, slots, torch.float32, dev, stash)
+    n, sc, rn = _SIZES[p](*tokens), _score_code(score), int(bool(renormalize))
     w = _launch(lambda st: _L.dt_moe_route_backward(ls, es, gs, ds, p, n, e, k, sc, rn, scale, code, st), stash, async_op,
                 stream, comm_stream)
     return w if async_op else dlogits
@@ -803,19 +819,16 @@ def dt_moe_dispatch_workspace(tokens: Sequence[int], nexperts: int, topk: int) -
     return _sized(_L.dt_moe_dispatch_workspace(len(tokens), _size_array(tokens), nexperts, topk))
 
 
-def _exchange(tok, rows, experts, nexperts: int, dev: int):
-    """(p, cols, topk, dtype, tokens, capacity, stash) of an exchange between
-    token tensors and the experts' row buffers."""
-    p = len(tok)
+def _exchange(tok, rows, experts, nexperts: int):
+    """(p, cols, topk, token elements, tokens, expert row elements, capacity, slots)
+    of an exchange between token tensors and the experts' row buffers."""
+    p = _ranks(tok, "tokens")
     cols, k = _width(tok[0], "the rows"), _width(experts[0], "experts")
-    dtype = tok[0].dtype
-    if any(t.numel() % cols for t in tok) or any(t.numel() % cols for t in rows):
-        raise ValueError(f"token and expert rows must be whole rows of {cols} elements")
-    tokens, capacity = [t.numel() // cols for t in tok], [t.numel() // cols for t in rows]
-    stash = _rank_list("experts", experts, p, torch.int32, dev, [t * k for t in tokens])
     if nexperts % p:
         raise ValueError(f"{nexperts} experts do not divide by {p} ranks")
-    return p, cols, k, dtype, tokens, capacity, stash
+    sizes, tokens = _row_counts(tok, cols, "the token tensors")
+    held, capacity = _row_counts(rows, cols, "the experts' buffers")
+    return p, cols, k, sizes, tokens, held, capacity, [t * k for t in tokens]
 
 
 def dt_moe_dispatch(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], recv: Sequence[torch.Tensor],
@@ -825,22 +838,18 @@ def dt_moe_dispatch(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], 
     experts[r] [tokens, topk]: recv[q] [capacity, cols] in expert order,
     positions[r] int32 [tokens, topk] (-1: no row), offsets[q] int32
     [nexperts / P + 1]."""
-    x, recv, dev = list(x), list(recv), torch.cuda.current_device()
-    p, cols, k, dtype, tokens, capacity, stash = _exchange(x, recv, experts, nexperts, dev)
+    dev, dtype, stash, i32 = torch.cuda.current_device(), x[0].dtype, [], torch.int32
+    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(x, recv, experts, nexperts)
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
-    code = _DTYPES[dtype]
-    stash += _rank_list("x", x, p, dtype, dev, [t * cols for t in tokens])
-    stash += _rank_list("recv", recv, p, dtype, dev, [c * cols for c in capacity])
-    stash += _rank_list("positions", positions, p, torch.int32, dev, [t * k for t in tokens])
-    stash += _rank_list("offsets", offsets, p, torch.int32, dev, nexperts // p + 1)
-    n, cap = _size_array(tokens), _size_array(capacity)
-    nbytes = _sized(_L.dt_moe_dispatch_workspace(p, n, nexperts, k))
-    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
-    xs, es, rs = _ptr_array(x), _ptr_array(experts), _ptr_array(recv)
-    ps, os_, at, have = _ptr_array(positions), _ptr_array(offsets), space.data_ptr(), space.numel() * space.element_size()
-    w = _launch(lambda st: _L.dt_moe_dispatch(xs, es, rs, ps, os_, p, n, cap, cols, nexperts, k, code, at, have, st),
-                stash + [space], async_op, stream, comm_stream)
+    code, n, cap = _DTYPES[dtype], _SIZES[p](*tokens), _SIZES[p](*capacity)
+    xs, rs = _buffers("x", x, sizes, dtype, dev, stash), _buffers("recv", recv, held, dtype, dev, stash)
+    es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
+    fs = _buffers("offsets", offsets, [nexperts // p + 1] * p, i32, dev, stash)
+    space = _workspace(workspace, _sized(_L.dt_moe_dispatch_workspace(p, n, nexperts, k)), dev, stream, async_op, comm_stream, stash)
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_moe_dispatch(xs, es, rs, ps, fs, p, n, cap, cols, nexperts, k, code, at, have, st), stash,
+                async_op, stream, comm_stream)
     return w if async_op else recv
 
 
@@ -849,18 +858,13 @@ def dt_moe_combine(y: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], p
                    async_op: bool = False, comm_stream=None):
     """out[r][t] = sum over its slots of weight * y[owner][position]
     (weights None: all ones, dt_moe_dispatch's backward pass)."""
-    y, out, dev = list(y), list(out), torch.cuda.current_device()
-    p, cols, k, dtype, tokens, capacity, stash = _exchange(out, y, experts, nexperts, dev)
-    code, slots = _float_dtype(out[0]), [t * k for t in tokens]
-    stash += _rank_list("y", y, p, dtype, dev, [c * cols for c in capacity])
-    stash += _rank_list("out", out, p, dtype, dev, [t * cols for t in tokens])
-    stash += _rank_list("positions", positions, p, torch.int32, dev, slots)
-    if weights is not None:
-        stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
-    ys, es, ps, os_ = _ptr_array(y), _ptr_array(experts), _ptr_array(positions), _ptr_array(out)
-    ws = _ptr_array(weights) if weights is not None else None
-    n, cap = _size_array(tokens), _size_array(capacity)
-    w = _launch(lambda st: _L.dt_moe_combine(ys, es, ps, ws, os_, p, n, cap, cols, nexperts, k, code, st), stash, async_op,
+    dev, dtype, stash, i32 = torch.cuda.current_device(), out[0].dtype, [], torch.int32
+    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(out, y, experts, nexperts)
+    code, n, cap = _float_dtype(out[0]), _SIZES[p](*tokens), _SIZES[p](*capacity)
+    ys, outs = _buffers("y", y, held, dtype, dev, stash), _buffers("out", out, sizes, dtype, dev, stash)
+    es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
+    ws = _buffers("weights", weights, slots, torch.float32, dev, stash) if weights is not None else None
+    w = _launch(lambda st: _L.dt_moe_combine(ys, es, ps, ws, outs, p, n, cap, cols, nexperts, k, code, st), stash, async_op,
                 stream, comm_stream)
     return w if async_op else out
 
@@ -871,16 +875,13 @@ def dt_moe_combine_backward(dout: Sequence[torch.Tensor], y: Sequence[torch.Tens
                             async_op: bool = False, comm_stream=None):
     """Gradients of dt_moe_combine: dy[owner][position] = weight * dout[r][t]
     (other rows of dy are left as they were), dweights[r] fp32."""
-    dout, y, dev = list(dout), list(y), torch.cuda.current_device()
-    p, cols, k, dtype, tokens, capacity, stash = _exchange(dout, y, experts, nexperts, dev)
-    code, slots, rows = _float_dtype(dout[0]), [t * k for t in tokens], [c * cols for c in capacity]
-    stash += _rank_list("dout", dout, p, dtype, dev, [t * cols for t in tokens])
-    stash += _rank_list("y", y, p, dtype, dev, rows) + _rank_list("dy", dy, p, dtype, dev, rows)
-    stash += _rank_list("positions", positions, p, torch.int32, dev, slots)
-    stash += _rank_list("weights", weights, p, torch.float32, dev, slots)
-    stash += _rank_list("dweights", dweights, p, torch.float32, dev, slots)
-    gs, ys, es, ps = _ptr_array(dout), _ptr_array(y), _ptr_array(experts), _ptr_array(positions)
-    ws, ds, dw, n, cap = _ptr_array(weights), _ptr_array(dy), _ptr_array(dweights), _size_array(tokens), _size_array(capacity)
+    dev, dtype, stash, i32, f32 = torch.cuda.current_device(), dout[0].dtype, [], torch.int32, torch.float32
+    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(dout, y, experts, nexperts)
+    code, n, cap = _float_dtype(dout[0]), _SIZES[p](*tokens), _SIZES[p](*capacity)
+    gs, ys = _buffers("dout", dout, sizes, dtype, dev, stash), _buffers("y", y, held, dtype, dev, stash)
+    es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
+    ws, ds = _buffers("weights", weights, slots, f32, dev, stash), _buffers("dy", dy, held, dtype, dev, stash)
+    dw = _buffers("dweights", dweights, slots, f32, dev, stash)
     w = _launch(lambda st: _L.dt_moe_combine_backward(gs, ys, es, ps, ws, ds, dw, p, n, cap, cols, nexperts, k, code, st),
                 stash, async_op, stream, comm_stream)
     return w if async_op else dy
@@ -898,16 +899,16 @@ def dt_vocab_loss_backward_workspace(vocab_rows: Sequence[int], tokens: int, col
                                                       _DTYPES[dtype]))
 
 
-def _loss_inputs(hidden, weight, targets, dev: int):
-    hidden, weight = list(hidden), list(weight)
-    p, cols = len(hidden), _width(hidden[0], "hidden")
+def _loss_inputs(hidden, weight, targets, dev: int, stash: list):
+    p, cols = _ranks(hidden, "hidden"), _width(hidden[0], "hidden")
     code, dtype, tokens = _float_dtype(hidden[0]), hidden[0].dtype, hidden[0].numel() // cols
-    if len(weight) != p or any(w.numel() % cols for w in weight):
-        raise ValueError(f"weight must list one shard of whole rows of {cols} elements per rank")
-    stash = _rank_list("hidden", hidden, p, dtype, dev, tokens * cols)
-    stash += _rank_list("weight", weight, p, dtype, dev, [w.numel() for w in weight])
-    stash += _rank_list("targets", targets, p, torch.int64, dev, tokens)
-    return p, cols, tokens, code, dtype, [w.numel() // cols for w in weight], stash
+    held, rows = _row_counts(weight, cols, "weight")
+    hs = _buffers("hidden", hidden, [tokens * cols] * p, dtype, dev, stash)
+    if len(weight) != p:
+        raise ValueError(f"weight must list one tensor per rank ({p}), got {len(weight)}")
+    ws = _buffers("weight", weight, held, dtype, dev, stash)
+    ts = _buffers("targets", targets, [tokens] * p, torch.int64, dev, stash)
+    return p, cols, tokens, code, dtype, held, _SIZES[p](*rows), hs, ws, ts
 
 
 def dt_vocab_loss(hidden: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], targets: Sequence[torch.Tensor],
@@ -917,16 +918,15 @@ def dt_vocab_loss(hidden: Sequence[torch.Tensor], weight: Sequence[torch.Tensor]
     ranks: hidden[r] [tokens, cols] (the same on every rank; one tensor may be
     listed P times), weight[r] [rows of rank r, cols], targets[r] int64.
     loss[q] and lse[q] fp32 [tokens] are written for every rank."""
-    dev = torch.cuda.current_device()
-    p, cols, tokens, code, dtype, rows, stash = _loss_inputs(hidden, weight, targets, dev)
-    stash += _rank_list("loss", loss, p, torch.float32, dev, tokens) + _rank_list("lse", lse, p, torch.float32, dev, tokens)
-    n = _size_array(rows)
-    nbytes = _sized(_L.dt_vocab_loss_workspace(p, n, tokens, cols, code))
-    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
-    hs, ws, ts, ls, es = (_ptr_array(v) for v in (hidden, weight, targets, loss, lse))
+    dev, stash = torch.cuda.current_device(), []
+    p, cols, tokens, code, dtype, _, n, hs, ws, ts = _loss_inputs(hidden, weight, targets, dev, stash)
+    each = [tokens] * p
+    ls, es = _buffers("loss", loss, each, torch.float32, dev, stash), _buffers("lse", lse, each, torch.float32, dev, stash)
+    space = _workspace(workspace, _sized(_L.dt_vocab_loss_workspace(p, n, tokens, cols, code)), dev, stream, async_op, comm_stream,
+                       stash)
     at, have = space.data_ptr(), space.numel() * space.element_size()
-    w = _launch(lambda st: _L.dt_vocab_loss(hs, ws, ts, ls, es, p, n, tokens, cols, ignore_index, code, at, have, st),
-                stash + [space], async_op, stream, comm_stream)
+    w = _launch(lambda st: _L.dt_vocab_loss(hs, ws, ts, ls, es, p, n, tokens, cols, ignore_index, code, at, have, st), stash,
+                async_op, stream, comm_stream)
     return w if async_op else loss
 
 
@@ -937,21 +937,19 @@ def dt_vocab_loss_backward(hidden: Sequence[torch.Tensor], weight: Sequence[torc
                            async_op: bool = False, comm_stream=None):
     """Gradients of dt_vocab_loss for dloss[r] fp32 [tokens]: dhidden[q] is
     the sum over all ranks' shards for every rank q, dweight[r] rank r's own.
-    The logits are formed again, ``piece_rows`` vocabulary rows of a shard at
-    a time (0: the library's choice)."""
-    dev = torch.cuda.current_device()
-    p, cols, tokens, code, dtype, rows, stash = _loss_inputs(hidden, weight, targets, dev)
-    stash += _rank_list("lse", lse, p, torch.float32, dev, tokens) + _rank_list("dloss", dloss, p, torch.float32, dev, tokens)
-    stash += _rank_list("dhidden", dhidden, p, dtype, dev, tokens * cols)
-    stash += _rank_list("dweight", dweight, p, dtype, dev, [r * cols for r in rows])
-    n = _size_array(rows)
-    nbytes = _sized(_L.dt_vocab_loss_backward_workspace(p, n, tokens, cols, piece_rows, code))
-    space = _workspace(workspace, nbytes, dev, stream, async_op, comm_stream)
-    hs, ws, ts, es, gs, dh, dw = (_ptr_array(v) for v in (hidden, weight, targets, lse, dloss, dhidden, dweight))
+    The logits are formed again, ``piece_rows`` vocabulary rows at a time (0:
+    the library's choice); the workspace grows with the piece."""
+    dev, stash = torch.cuda.current_device(), []
+    p, cols, tokens, code, dtype, held, n, hs, ws, ts = _loss_inputs(hidden, weight, targets, dev, stash)
+    each = [tokens] * p
+    es, gs = _buffers("lse", lse, each, torch.float32, dev, stash), _buffers("dloss", dloss, each, torch.float32, dev, stash)
+    dh = _buffers("dhidden", dhidden, [tokens * cols] * p, dtype, dev, stash)
+    dw = _buffers("dweight", dweight, held, dtype, dev, stash)
+    space = _workspace(workspace, _sized(_L.dt_vocab_loss_backward_workspace(p, n, tokens, cols, piece_rows, code)), dev, stream,
+                       async_op, comm_stream, stash)
     at, have = space.data_ptr(), space.numel() * space.element_size()
-    w = _launch(lambda st: _L.dt_vocab_loss_backward(hs, ws, ts, es, gs, dh, dw, p, n, tokens, cols, ignore_index,
-                                                     piece_rows, code, at, have, st),
-                stash + [space], async_op, stream, comm_stream)
+    w = _launch(lambda st: _L.dt_vocab_loss_backward(hs, ws, ts, es, gs, dh, dw, p, n, tokens, cols, ignore_index, piece_rows,
+                                                     code, at, have, st), stash, async_op, stream, comm_stream)
     return w if async_op else dhidden
 
 

@@ -179,12 +179,12 @@ __device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t place, int
     }
 }
 
-// Waits until at most `loads` of this wave's loads are outstanding and all its
-// LDS reads are done, then for the workgroup's other waves.
+// Waits until at most `loads` of this wave's loads are outstanding, then for
+// the workgroup's other waves.
 template <int loads>
 __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4);
+    __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4 | 15 << 8);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -221,21 +221,22 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     load(lo, s0);
     load(lo + 1, s1);
     load(lo + 2, s2);
-    load(lo + 3, s3);
-    arrive<3 * S::loads>();
+    arrive<2 * S::loads>();
     u32x4 fa[S::MI], fb[2][S::NI];
     uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
 #pragma unroll
     for (int i = 0; i < S::MI; i++) fa[i] = fragment<DT, MA, S::BM>(s0, ra, i);
 #pragma unroll
     for (int j = 0; j < S::NI; j++) fb[0][j] = fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j);
-    // Step `step`: its registers are loaded, its stage of LDS is free once all
-    // waves are here, and the next step's has landed.  A row of A's registers
-    // takes the next step's as soon as it is multiplied; behind the last step
-    // these are bytes that nothing uses.
-    auto turn = [&](uint32_t step, u32x4* mine, const u32x4* following, const u32x4 (&now)[S::NI], u32x4 (&next)[S::NI]) {
-        arrive<2 * S::loads>();
-        load(step + 4, mine);
+    // Step `step`: its registers are loaded, and the next step's bytes are in
+    // LDS once all waves are here.  The stage that is loaded into, the one
+    // before this step's, was read two turns ago and multiplied in the last
+    // one, so no wave has to wait for its LDS reads at the barrier.  A row of
+    // A's registers takes the next step's as soon as it is multiplied; behind
+    // the last step these are bytes that nothing uses.
+    auto turn = [&](uint32_t step, u32x4* free, const u32x4* following, const u32x4 (&now)[S::NI], u32x4 (&next)[S::NI]) {
+        arrive<S::loads>();
+        load(step + 3, free);
         // keeps the compiler from holding every fragment's address of every stage in a register
         asm volatile("" : "+v"(ra), "+v"(rb));
 #pragma unroll
@@ -258,10 +259,10 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
         }
     };
     for (uint32_t step = lo; step < hi; step += 4) {
-        turn(step, s0, s1, fb[0], fb[1]);
-        turn(step + 1, s1, s2, fb[1], fb[0]);
-        turn(step + 2, s2, s3, fb[0], fb[1]);
-        turn(step + 3, s3, s0, fb[1], fb[0]);
+        turn(step, s3, s1, fb[0], fb[1]);
+        turn(step + 1, s0, s2, fb[1], fb[0]);
+        turn(step + 2, s1, s3, fb[0], fb[1]);
+        turn(step + 3, s2, s0, fb[1], fb[0]);
     }
     arrive<0>();  // nothing is on its way into LDS when the workgroup ends
 }

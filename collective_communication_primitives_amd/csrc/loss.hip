@@ -281,7 +281,10 @@ __device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, u
 }
 
 // exp(x): the argument's product with log2 e is off by half a step of |x| log2 e,
-// which adds |x| half steps to the result's error.
+// which adds |x| half steps to the result's error.  So the difference is taken
+// before the product: where a token's probability is near 1 its gradient is
+// what is left of 1 - p, and a product of logit and lse apart would leave |lse|
+// half steps in it.
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
 // Four values rounded to the dtype and stored as one (`to` aligned for it); zeros unless `use`.
@@ -387,11 +390,11 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segmen
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         float s = 0.f;
-        const float base2 = top > -INFINITY ? top * kLog2e : 0.f;
+        const float base = top > -INFINITY ? top : 0.f;
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) s += __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -base2));
+            for (int e = 0; e < 4; e++) s += exp_of(acc[i][j][e] - base);
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (lane < 16) part[wm][nl] = make_float2(top, s);
@@ -460,14 +463,14 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
         const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
         if (n >= a.tokens) continue;
         const int64_t t = a.targets[n];
-        const float lse2 = a.lse[n] * kLog2e;
+        const float lse = a.lse[n];
         const bool use = counted(a, t);
         const float f = use ? a.dloss[n] : 0.f;
         // d = p f; the target's row and the rows behind the shard's last one are mended below
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][j][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -lse2)) * f;
+            for (int e = 0; e < 4; e++) acc[i][j][e] = exp_of(acc[i][j][e] - lse) * f;
         const int64_t at = t - int64_t(g.vocab[sg]) - int64_t(m0);
         const uint32_t hit = use && at >= 0 && at < S::BM ? uint32_t(at) : UINT32_MAX;  // the target's row in the tile
         if (__any(hit != UINT32_MAX) || left < S::BM) {

@@ -61,7 +61,8 @@ __device__ __forceinline__ rsrc_t scalar_rsrc(const char* p, uint32_t bytes) {
 // behind the last valid row (empty when not `any`), so what lies past it
 // loads zeros without touching memory.
 //
-// kRows: rows of `pitch` bytes, `bytes` of them valid (a multiple of 16).
+// kRows: rows of `pitch` bytes, read up to `bytes` (a multiple of 16; where that
+// is past a row's end, the other operand has zeros there).
 struct RowOperand {
     const char* p;     // the tile's first row
     uint32_t rows, pitch, bytes;
@@ -323,7 +324,8 @@ struct LossProblem {
     const int64_t* targets;
     const float* lse;
     const float* dloss;
-    uint32_t pitch;          // of hidden and weight rows, a multiple of 16; all bytes valid
+    uint32_t hpitch;         // bytes between hidden's rows, a multiple of 16; all of them valid
+    uint32_t wpitch;         // bytes between weight's rows; what lies behind a row's end meets zeros of hidden
     uint32_t tokens, cols, vocab;
     int64_t ignore_index;
 };
@@ -354,9 +356,9 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segmen
     const int sg = segment_of(g.tile, g.n, mt);
     const uint32_t m0 = (mt - g.tile[sg]) * S::BM, n0 = nt * S::BN, left = g.count[sg] - m0;
     f32x4 acc[S::MI][S::NI];
-    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
-    const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
-    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, acc);
+    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch};
+    const RowOperand B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch};
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.hpitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t wm = wave % S::GM, wn = wave / S::GM;
     const uint32_t mlane = wm * S::WM + (lane >> 4) * 4;  // acc[i][j][e] is row mlane + 16 i + e of the tile
@@ -452,9 +454,9 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
     const uint32_t count = g.count[sg], padded = g.col[sg + 1] - g.col[sg];
     const uint32_t left = count > m0 ? count - m0 : 0;  // the last tile may lie in the padding alone
     f32x4 acc[S::MI][S::NI];
-    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.pitch, left < S::BM ? left : S::BM, a.pitch, a.pitch};
-    const RowOperand B{a.hidden + uint64_t(n0) * a.pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.pitch, a.pitch};
-    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.pitch + kStepBytes - 1) / kStepBytes, acc);
+    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch};
+    const RowOperand B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch};
+    matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.hpitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t mlane = (wave % S::GM) * S::WM + (lane >> 4) * 4;
     T* d = reinterpret_cast<T*>(p.d) + g.col[sg] + m0;
@@ -521,7 +523,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
     const uint32_t each = __builtin_amdgcn_readfirstlane(steps / p.splits), more = steps - each * p.splits, y = blockIdx.y;
     const uint32_t lo = y * each + (y < more ? y : more), hi = lo + each + (y < more ? 1 : 0);
     f32x4 acc[S::MI][S::NI];
-    const WeightOperand<KR> A{g, a.pitch, m0 * uint32_t(sizeof(T)), 0};
+    const WeightOperand<KR> A{g, a.wpitch, m0 * uint32_t(sizeof(T)), 0};
     const RowOperand B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch};
     matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
     f32x4 acc[S::MI][S::NI];
     constexpr uint32_t es = sizeof(T);
     const uint32_t skip = (g.col[sg] + n0) * es;
-    const ColOperand<KR> A{a.hidden + m0 * es, a.tokens, a.pitch, m0 * es};
+    const ColOperand<KR> A{a.hidden + m0 * es, a.tokens, a.hpitch, m0 * es};
     const ColOperand<KR> B{p.d + skip, a.tokens, uint32_t(p.ldv * es), skip};
     matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -642,8 +644,10 @@ struct Parts {
     }
 };
 
-// Rows that start and end on 16-byte boundaries are read where they are;
-// others are copied to padded rows in the workspace, a piece at a time.
+// hidden is read where it is if its rows start and end on 16-byte boundaries;
+// otherwise it is copied to such rows with zeros behind them (a small part of
+// the call's bytes unless the vocabulary is small too).  weight may lie on any
+// 4-byte boundaries; only bf16 rows of odd width are copied, a piece at a time.
 struct PadParts {
     uint64_t pitch, hidden, weight;
 };
@@ -654,20 +658,22 @@ PadParts pad_parts(Parts& w, uint64_t tokens, uint64_t cols, uint64_t piece, int
     b.weight = w.take(piece * b.pitch);
     return b;
 }
-bool rows_aligned(const LossArgs& a, int dtype) {
-    if (a.cols * esize(dtype) % 16 != 0 || reinterpret_cast<uintptr_t>(a.hidden) % 16 != 0) return false;
+bool hidden_direct(const LossArgs& a, int dtype) {
+    return a.cols * esize(dtype) % 16 == 0 && reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0;
+}
+bool weight_direct(const LossArgs& a, int dtype) {
+    if (a.cols * esize(dtype) % 4 != 0) return false;
     for (int r = 0; r < a.nranks; r++)
-        if (reinterpret_cast<uintptr_t>(a.weight[r]) % 16 != 0) return false;
+        if (reinterpret_cast<uintptr_t>(a.weight[r]) % 4 != 0) return false;
     return true;
 }
 
-LossProblem problem_of(const LossArgs& a, uint64_t pitch) {
+LossProblem problem_of(const LossArgs& a) {
     LossProblem p = {};
     p.hidden = static_cast<const char*>(a.hidden);
     p.targets = a.targets;
     p.lse = a.lse_in;
     p.dloss = a.dloss;
-    p.pitch = uint32_t(pitch);
     p.tokens = a.tokens;
     p.cols = a.cols;
     p.vocab = a.vocab.start[a.nranks];
@@ -711,6 +717,20 @@ void pad_weight(const LossArgs& a, uint32_t first, uint32_t count, char* to, uin
     for (int i = 0; i < g.n; i++) pad_rows<T>(g.weight[i], to + uint64_t(g.vocab[i] - first) * pitch, g.count[i], a.cols, pitch, s);
 }
 
+// hidden's place and pitch, and weight's pitch; where weight has to be copied
+// piece by piece, the place for it.
+template <typename T>
+char* place_rows(const LossArgs& a, int dtype, const PadParts& pad, LossProblem& p, hipStream_t s) {
+    p.hpitch = uint32_t(pad.pitch);
+    if (!hidden_direct(a, dtype)) {
+        pad_rows<T>(a.hidden, a.workspace + pad.hidden, a.tokens, a.cols, pad.pitch, s);
+        p.hidden = a.workspace + pad.hidden;
+    }
+    const bool direct = weight_direct(a, dtype);
+    p.wpitch = direct ? a.cols * uint32_t(sizeof(T)) : uint32_t(pad.pitch);
+    return direct ? nullptr : a.workspace + pad.weight;
+}
+
 uint64_t stats_entries(const RowTable& vocab, int nranks) {
     // at most one entry per 64 rows of a shard, and one per shard and piece end
     uint64_t n = 0;
@@ -722,30 +742,24 @@ template <int DT>
 hipError_t forward(const LossArgs& a, hipStream_t s) {
     typedef typename Elem<DT>::type T;
     const uint32_t V = a.vocab.start[a.nranks];
-    const bool direct = rows_aligned(a, DT);
+    const bool direct = weight_direct(a, DT);
     const uint32_t piece = direct ? V : loss_piece(a.vocab, a.nranks, 0);
     Parts parts;
     StatsArgs q = {};
     q.part = reinterpret_cast<float2*>(a.workspace + parts.take(stats_entries(a.vocab, a.nranks) * a.tokens * sizeof(float2)));
     q.target = reinterpret_cast<float*>(a.workspace + parts.take(uint64_t(a.tokens) * 4));
-    LossProblem p = problem_of(a, uint64_t(a.cols) * sizeof(T));
-    char* wpad = nullptr;
-    if (!direct) {
-        const PadParts pad = pad_parts(parts, a.tokens, a.cols, piece, DT);
-        p.pitch = uint32_t(pad.pitch);
-        pad_rows<T>(a.hidden, a.workspace + pad.hidden, a.tokens, a.cols, pad.pitch, s);
-        p.hidden = a.workspace + pad.hidden;
-        wpad = a.workspace + pad.weight;
-    }
+    LossProblem p = problem_of(a);
+    const PadParts pad = pad_parts(parts, a.tokens, a.cols, loss_piece(a.vocab, a.nranks, 0), DT);
+    char* wpad = place_rows<T>(a, DT, pad, p, s);
     const Tile t = pick_tile(DT, piece, a.tokens);
     for (int pass = 0; pass < 2; pass++) {  // count the tiles, then launch
         q.entry = 0;
         for (uint32_t first = 0; first < V; first += piece) {
             const uint32_t count = V - first < piece ? V - first : piece;
-            Segments g = segments_of(a, DT, first, count, wpad, p.pitch);
+            Segments g = segments_of(a, DT, first, count, wpad, p.wpitch);
             set_tiles(g, kTileM[t], false);
             if (pass == 1) {
-                if (!direct) pad_weight<T>(a, first, count, wpad, p.pitch, s);
+                if (!direct) pad_weight<T>(a, first, count, wpad, p.wpitch, s);
                 with_tile<DT>(t, [&](auto shape) {
                     typedef decltype(shape) S;
                     q.token_tiles = ceil_div(a.tokens, S::BN);
@@ -801,14 +815,8 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     typedef typename Elem<DT>::type T;
     const uint32_t V = a.vocab.start[a.nranks];
     const BackwardParts b = backward_parts(a.nranks, a.tokens, a.cols, a.piece, DT);
-    LossProblem q = problem_of(a, uint64_t(a.cols) * sizeof(T));
-    char* wpad = nullptr;
-    if (!rows_aligned(a, DT)) {
-        q.pitch = uint32_t(b.pad.pitch);
-        pad_rows<T>(a.hidden, a.workspace + b.pad.hidden, a.tokens, a.cols, b.pad.pitch, s);
-        q.hidden = a.workspace + b.pad.hidden;
-        wpad = a.workspace + b.pad.weight;
-    }
+    LossProblem q = problem_of(a);
+    char* wpad = place_rows<T>(a, DT, b.pad, q, s);
     DPiece p = {};
     p.d = a.workspace + b.d;
     p.acc = reinterpret_cast<float*>(a.workspace + b.acc);
@@ -816,10 +824,10 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     p.splits = b.splits;
     for (uint32_t first = 0; first < V; first += a.piece) {
         const uint32_t count = V - first < a.piece ? V - first : a.piece;
-        Segments g = segments_of(a, DT, first, count, wpad, q.pitch);
+        Segments g = segments_of(a, DT, first, count, wpad, q.wpitch);
         p.ldv = g.col[g.n];
         if (a.tokens > 0) {
-            if (wpad != nullptr) pad_weight<T>(a, first, count, wpad, q.pitch, s);
+            if (wpad != nullptr) pad_weight<T>(a, first, count, wpad, q.wpitch, s);
             const Tile t = pick_tile(DT, count, a.tokens);
             set_tiles(g, kTileM[t], true);
             with_tile<DT>(t, [&](auto shape) {

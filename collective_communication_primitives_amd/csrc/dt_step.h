@@ -79,7 +79,7 @@ hipError_t launch_route_backward(const RouteBackArgs& a, int nranks, int dtype, 
 
 // -------------------------------------------------------------- exchange --
 // A slot is one (rank, token, choice); slots are numbered in that order.
-constexpr uint32_t kPlanSlots = 2048;  // slots per workgroup of the plan
+constexpr uint32_t kPlanSlots = 1024;  // slots per workgroup of the plan (2048 took 10 us longer for 131072 slots)
 constexpr uint32_t kFewSlots = 4096;   // up to here plan and copy are one launch
 struct PlanArgs {
     const int32_t* experts[kMaxRanksHost];

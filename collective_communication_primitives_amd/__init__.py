@@ -19,14 +19,13 @@ from __future__ import annotations
 
 import atexit
 import ctypes
-import operator
 import threading
 import weakref
 from typing import Dict, List, Optional, Sequence
 
 import torch
 
-from . import _lib
+from . import _lib, _marshal
 
 _L = _lib.load()
 
@@ -623,39 +622,31 @@ DT_MAX_EXPERTS, DT_MAX_TOPK = 1024, 64
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-_POINTERS = [ctypes.c_void_p * max(1, n) for n in range(DT_MAX_RANKS + 1)]
-_SIZES = [ctypes.c_size_t * max(1, n) for n in range(DT_MAX_RANKS + 1)]
-
-
-def _refuse(name: str, r: int, t, dtype, dev: int, want: int) -> None:
-    if t.dtype != dtype:
-        raise TypeError(f"{name}[{r}] must be {dtype}, got {t.dtype}")
-    if t.numel() != want:
-        raise ValueError(f"{name}[{r}] must hold {want} elements, got {t.numel()}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}[{r}] must live on the current GPU (cuda:{dev}), got {t.device}")
-    raise ValueError(f"{name}[{r}] must be contiguous")
-
-
-_dtype_of = operator.attrgetter("dtype")
-_numel, _device_of, _contiguous, _data_ptr = (torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous,
-                                              torch.Tensor.data_ptr)
+def _refuse(name: str, tensors, sizes, dtype, dev: int) -> None:
+    """Say which tensor of a list the call cannot take, and why."""
+    if not isinstance(tensors, (list, tuple)):
+        raise TypeError(f"{name} must be a list of tensors, got {type(tensors).__name__}")
+    if len(tensors) != len(sizes):
+        raise ValueError(f"{name} must list one tensor per rank ({len(sizes)}), got {len(tensors)}")
+    for r, (t, want) in enumerate(zip(tensors, sizes)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{r}] must be a tensor, got {type(t).__name__}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name}[{r}] must be {dtype}, got {t.dtype}")
+        if t.numel() != want:
+            raise ValueError(f"{name}[{r}] must hold {want} elements, got {t.numel()}")
+        if t.get_device() != dev:
+            raise ValueError(f"{name}[{r}] must live on the current GPU (cuda:{dev}), got {t.device}")
+    raise ValueError(f"{name} must list contiguous tensors")
 
 
 def _buffers(name: str, tensors, sizes, dtype, dev: int, stash: list):
     """The pointers of a list of contiguous tensors of ``dtype`` on the current
-    GPU, rank r's with sizes[r] elements; the tensors join ``stash``.  (Whole
-    lists go through map(): half the time of a loop over the tensors.)"""
-    p = len(sizes)
-    if len(tensors) != p:
-        raise ValueError(f"{name} must list one tensor per rank ({p}), got {len(tensors)}")
-    if (list(map(_numel, tensors)) != sizes or list(map(_device_of, tensors)) != [dev] * p
-            or not all(map(_contiguous, tensors)) or list(map(_dtype_of, tensors)) != [dtype] * p):
-        for r, (t, n) in enumerate(zip(tensors, sizes)):
-            if t.dtype != dtype or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
-                _refuse(name, r, t, dtype, dev, n)
-    stash += tensors
-    return _POINTERS[p](*map(_data_ptr, tensors))
+    GPU, rank r's with sizes[r] elements; the tensors join ``stash``."""
+    ptrs = _marshal.buffers(tensors, sizes, dtype, dev, stash)
+    if ptrs is None:
+        _refuse(name, tensors, sizes, dtype, dev)
+    return ptrs
 
 
 def _ranks(tensors, name: str) -> int:
@@ -665,13 +656,13 @@ def _ranks(tensors, name: str) -> int:
     return p
 
 
-def _row_counts(tensors, cols: int, name: str):
-    """(elements, rows) of each tensor, whole rows of ``cols``."""
-    sizes = list(map(_numel, tensors))
-    rows = [n // cols for n in sizes]
-    if sum(rows) * cols != sum(sizes):
-        raise ValueError(f"{name} must hold whole rows of {cols} elements")
-    return sizes, rows
+def _row_counts(tensors, cols: int, name: str, times: int = 1):
+    """(elements, rows, rows * times, rows as the C ABI takes them) of each
+    tensor, whole rows of ``cols``."""
+    counts = _marshal.counts(tensors, cols, times)
+    if counts is None:
+        raise ValueError(f"{name} must be a list of tensors of whole rows of {cols} elements")
+    return counts
 
 
 def _float_dtype(t: torch.Tensor) -> int:
@@ -730,7 +721,7 @@ def dt_layer_norm(x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], bia
     one per row) keep the statistics for dt_layer_norm_backward."""
     p, dev, cols = _ranks(x, "x"), torch.cuda.current_device(), _width(weight[0], "weight")
     code, dtype, stash = _float_dtype(x[0]), x[0].dtype, []
-    sizes, rows = _row_counts(x, cols, "x")
+    sizes, rows, _, n = _row_counts(x, cols, "x")
     if (mean is None) != (rstd is None):
         raise ValueError("mean and rstd come together")
     xs, ys = _buffers("x", x, sizes, dtype, dev, stash), _buffers("y", y, sizes, dtype, dev, stash)
@@ -739,7 +730,6 @@ def dt_layer_norm(x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], bia
     ms = rs = None
     if mean is not None:
         ms, rs = _buffers("mean", mean, rows, torch.float32, dev, stash), _buffers("rstd", rstd, rows, torch.float32, dev, stash)
-    n = _SIZES[p](*rows)
     w = _launch(lambda st: _L.dt_layer_norm(xs, ws, bs, ys, ms, rs, p, n, cols, eps, code, st), stash, async_op, stream,
                 comm_stream)
     return w if async_op else y
@@ -754,14 +744,13 @@ def dt_layer_norm_backward(dy: Sequence[torch.Tensor], x: Sequence[torch.Tensor]
     formed) summed over the rows of all ranks, for every rank q."""
     p, dev, cols = _ranks(x, "x"), torch.cuda.current_device(), _width(weight[0], "weight")
     code, dtype, stash = _float_dtype(x[0]), x[0].dtype, []
-    sizes, rows = _row_counts(x, cols, "x")
+    sizes, rows, _, n = _row_counts(x, cols, "x")
     wide = [cols] * p
     xs, gs = _buffers("x", x, sizes, dtype, dev, stash), _buffers("dy", dy, sizes, dtype, dev, stash)
     ds, ws = _buffers("dx", dx, sizes, dtype, dev, stash), _buffers("weight", weight, wide, dtype, dev, stash)
     ms, rs = _buffers("mean", mean, rows, torch.float32, dev, stash), _buffers("rstd", rstd, rows, torch.float32, dev, stash)
     dw = _buffers("dweight", dweight, wide, dtype, dev, stash)
     db = _buffers("dbias", dbias, wide, dtype, dev, stash) if dbias is not None else None
-    n = _SIZES[p](*rows)
     space = _workspace(workspace, _sized(_L.dt_layer_norm_workspace(p, n, cols)), dev, stream, async_op, comm_stream, stash)
     at, have = space.data_ptr(), space.numel() * space.element_size()
     w = _launch(lambda st: _L.dt_layer_norm_backward(gs, xs, ws, ms, rs, ds, dw, db, p, n, cols, code, at, have, st), stash,
@@ -782,10 +771,9 @@ def dt_moe_route(logits: Sequence[torch.Tensor], experts: Sequence[torch.Tensor]
     p, dev = _ranks(logits, "logits"), torch.cuda.current_device()
     e, k, stash = _width(logits[0], "logits"), _width(experts[0], "experts"), []
     code, dtype = _float_dtype(logits[0]), logits[0].dtype
-    sizes, tokens = _row_counts(logits, e, "logits")
-    slots = [t * k for t in tokens]
+    sizes, _, slots, n = _row_counts(logits, e, "logits", k)
     ls, es = _buffers("logits", logits, sizes, dtype, dev, stash), _buffers("experts", experts, slots, torch.int32, dev, stash)
-    ws, n = _buffers("weights", weights, slots, torch.float32, dev, stash), _SIZES[p](*tokens)
+    ws = _buffers("weights", weights, slots, torch.float32, dev, stash)
     b = None
     if bias is not None:
         _buffers("bias", [bias], [e], torch.float32, dev, stash)
@@ -804,11 +792,10 @@ def dt_moe_route_backward(logits: Sequence[torch.Tensor], experts: Sequence[torc
     p, dev = _ranks(logits, "logits"), torch.cuda.current_device()
     e, k, stash = _width(logits[0], "logits"), _width(experts[0], "experts"), []
     code, dtype = _float_dtype(logits[0]), logits[0].dtype
-    sizes, tokens = _row_counts(logits, e, "logits")
-    slots = [t * k for t in tokens]
+    sizes, _, slots, n = _row_counts(logits, e, "logits", k)
     ls, ds = _buffers("logits", logits, sizes, dtype, dev, stash), _buffers("dlogits", dlogits, sizes, dtype, dev, stash)
     es, gs = _buffers("experts", experts, slots, torch.int32, dev, stash), _buffers("dweights", dweights, slots, torch.float32, dev, stash)
-    n, sc, rn = _SIZES[p](*tokens), _score_code(score), int(bool(renormalize))
+    sc, rn = _score_code(score), int(bool(renormalize))
     w = _launch(lambda st: _L.dt_moe_route_backward(ls, es, gs, ds, p, n, e, k, sc, rn, scale, code, st), stash, async_op,
                 stream, comm_stream)
     return w if async_op else dlogits
@@ -820,15 +807,15 @@ def dt_moe_dispatch_workspace(tokens: Sequence[int], nexperts: int, topk: int) -
 
 
 def _exchange(tok, rows, experts, nexperts: int):
-    """(p, cols, topk, token elements, tokens, expert row elements, capacity, slots)
+    """(p, cols, topk, token elements, slots, tokens, expert row elements, capacity)
     of an exchange between token tensors and the experts' row buffers."""
     p = _ranks(tok, "tokens")
     cols, k = _width(tok[0], "the rows"), _width(experts[0], "experts")
     if nexperts % p:
         raise ValueError(f"{nexperts} experts do not divide by {p} ranks")
-    sizes, tokens = _row_counts(tok, cols, "the token tensors")
-    held, capacity = _row_counts(rows, cols, "the experts' buffers")
-    return p, cols, k, sizes, tokens, held, capacity, [t * k for t in tokens]
+    sizes, _, slots, n = _row_counts(tok, cols, "the token tensors", k)
+    held, _, _, cap = _row_counts(rows, cols, "the experts' buffers")
+    return p, cols, k, sizes, slots, n, held, cap
 
 
 def dt_moe_dispatch(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], recv: Sequence[torch.Tensor],
@@ -839,10 +826,10 @@ def dt_moe_dispatch(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], 
     positions[r] int32 [tokens, topk] (-1: no row), offsets[q] int32
     [nexperts / P + 1]."""
     dev, dtype, stash, i32 = torch.cuda.current_device(), x[0].dtype, [], torch.int32
-    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(x, recv, experts, nexperts)
+    p, cols, k, sizes, slots, n, held, cap = _exchange(x, recv, experts, nexperts)
     if dtype not in _DTYPES:
         raise TypeError(f"unsupported dtype {dtype}")
-    code, n, cap = _DTYPES[dtype], _SIZES[p](*tokens), _SIZES[p](*capacity)
+    code = _DTYPES[dtype]
     xs, rs = _buffers("x", x, sizes, dtype, dev, stash), _buffers("recv", recv, held, dtype, dev, stash)
     es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
     fs = _buffers("offsets", offsets, [nexperts // p + 1] * p, i32, dev, stash)
@@ -859,8 +846,8 @@ def dt_moe_combine(y: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], p
     """out[r][t] = sum over its slots of weight * y[owner][position]
     (weights None: all ones, dt_moe_dispatch's backward pass)."""
     dev, dtype, stash, i32 = torch.cuda.current_device(), out[0].dtype, [], torch.int32
-    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(out, y, experts, nexperts)
-    code, n, cap = _float_dtype(out[0]), _SIZES[p](*tokens), _SIZES[p](*capacity)
+    p, cols, k, sizes, slots, n, held, cap = _exchange(out, y, experts, nexperts)
+    code = _float_dtype(out[0])
     ys, outs = _buffers("y", y, held, dtype, dev, stash), _buffers("out", out, sizes, dtype, dev, stash)
     es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
     ws = _buffers("weights", weights, slots, torch.float32, dev, stash) if weights is not None else None
@@ -876,8 +863,8 @@ def dt_moe_combine_backward(dout: Sequence[torch.Tensor], y: Sequence[torch.Tens
     """Gradients of dt_moe_combine: dy[owner][position] = weight * dout[r][t]
     (other rows of dy are left as they were), dweights[r] fp32."""
     dev, dtype, stash, i32, f32 = torch.cuda.current_device(), dout[0].dtype, [], torch.int32, torch.float32
-    p, cols, k, sizes, tokens, held, capacity, slots = _exchange(dout, y, experts, nexperts)
-    code, n, cap = _float_dtype(dout[0]), _SIZES[p](*tokens), _SIZES[p](*capacity)
+    p, cols, k, sizes, slots, n, held, cap = _exchange(dout, y, experts, nexperts)
+    code = _float_dtype(dout[0])
     gs, ys = _buffers("dout", dout, sizes, dtype, dev, stash), _buffers("y", y, held, dtype, dev, stash)
     es, ps = _buffers("experts", experts, slots, i32, dev, stash), _buffers("positions", positions, slots, i32, dev, stash)
     ws, ds = _buffers("weights", weights, slots, f32, dev, stash), _buffers("dy", dy, held, dtype, dev, stash)
@@ -902,13 +889,13 @@ def dt_vocab_loss_backward_workspace(vocab_rows: Sequence[int], tokens: int, col
 def _loss_inputs(hidden, weight, targets, dev: int, stash: list):
     p, cols = _ranks(hidden, "hidden"), _width(hidden[0], "hidden")
     code, dtype, tokens = _float_dtype(hidden[0]), hidden[0].dtype, hidden[0].numel() // cols
-    held, rows = _row_counts(weight, cols, "weight")
+    held, _, _, n = _row_counts(weight, cols, "weight")
     hs = _buffers("hidden", hidden, [tokens * cols] * p, dtype, dev, stash)
     if len(weight) != p:
         raise ValueError(f"weight must list one tensor per rank ({p}), got {len(weight)}")
     ws = _buffers("weight", weight, held, dtype, dev, stash)
     ts = _buffers("targets", targets, [tokens] * p, torch.int64, dev, stash)
-    return p, cols, tokens, code, dtype, held, _SIZES[p](*rows), hs, ws, ts
+    return p, cols, tokens, code, dtype, held, n, hs, ws, ts
 
 
 def dt_vocab_loss(hidden: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], targets: Sequence[torch.Tensor],

@@ -6,7 +6,8 @@
 stale build this script replaces.)
 
 Each source is compiled on its own (in parallel) into ``_build/`` at the
-repository root, then linked into ``libdtcoll.so`` next to this file.
+repository root, then linked into ``libdtcoll.so`` next to this file.  Beside
+it ``_marshal.so``, the host helper of the Python binding (g++, no GPU code).
 """
 from __future__ import annotations
 
@@ -14,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libdtcoll.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 SOURCES = ("api.cpp", "reduce.hip", "copy.hip", "barrier.hip", "scratch.hip", "step_api.cpp", "norm.hip", "moe.hip",
            "loss.hip")
 ARCH = os.environ.get("DT_OFFLOAD_ARCH", "gfx950")
@@ -48,10 +51,26 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_marshal() -> str:
+    import torch
+    from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
+    paths = [flag for path in include_paths() for flag in ("-isystem", path)]
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_path("include"), *paths,
+           os.path.join(CSRC, "marshal.cpp"), "-L", TORCH_LIB_PATH, "-ltorch_python", "-o", MARSHAL + ".tmp"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for marshal.cpp:\n{res.stdout}\n{res.stderr}")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+    return MARSHAL
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        marshal = pool.submit(_compile_marshal)
         objs = list(pool.map(_compile, SOURCES))
+        marshal.result()
     tmp = LIBRARY + ".tmp"
     cmd = [_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -59,7 +78,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIBRARY)
     if verbose:
-        print(f"built {LIBRARY}")
+        print(f"built {LIBRARY} and {MARSHAL}")
     return LIBRARY
 
 

@@ -731,6 +731,16 @@ char* place_rows(const LossArgs& a, int dtype, const PadParts& pad, LossProblem&
     return direct ? nullptr : a.workspace + pad.weight;
 }
 
+// Vocabulary rows of one launch of the forward pass: HIP counts a launch's
+// threads in 32 bits, so it stays within 2^22 tiles of at most 512 threads.
+// Never fewer than kLossPiece rows, for no more tokens than the call takes.
+uint32_t stats_piece(uint32_t vocab, uint32_t tokens) {
+    constexpr uint32_t most = 1 << 22;
+    static_assert(most / (DT_MAX_LOSS_TOKENS / 128) * 128 >= kLossPiece, "stats_entries counts pieces of kLossPiece rows");
+    const uint64_t rows = uint64_t(most / ceil_div(tokens, 128)) * 128;
+    return uint32_t(rows < vocab ? rows : vocab);
+}
+
 uint64_t stats_entries(const RowTable& vocab, int nranks) {
     // at most one entry per 64 rows of a shard, and one per shard and piece end
     uint64_t n = 0;
@@ -743,7 +753,7 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
     typedef typename Elem<DT>::type T;
     const uint32_t V = a.vocab.start[a.nranks];
     const bool direct = weight_direct(a, DT);
-    const uint32_t piece = direct ? V : loss_piece(a.vocab, a.nranks, 0);
+    const uint32_t piece = direct ? stats_piece(V, a.tokens) : loss_piece(a.vocab, a.nranks, 0);
     Parts parts;
     StatsArgs q = {};
     q.part = reinterpret_cast<float2*>(a.workspace + parts.take(stats_entries(a.vocab, a.nranks) * a.tokens * sizeof(float2)));
@@ -872,7 +882,9 @@ uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint
 }
 
 uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t asked) {
-    const uint64_t want = asked > 0 ? asked : kLossPiece, all = vocab.start[nranks];
+    uint64_t want = asked > 0 ? asked : kLossPiece;
+    const uint64_t all = vocab.start[nranks];
+    if (want > kMaxLossPiece) want = kMaxLossPiece;
     return uint32_t(want < all ? want : all);
 }
 

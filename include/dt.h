@@ -264,9 +264,8 @@ dt_status dt_barrier_exchange(const void* const* src, void* const* stage, void* 
  *    copy of dt_moe_dispatch); arithmetic is fp32, one rounding at the end.
  *    Results do not depend on timing: the same call gives the same bits.
  *  - Inputs that every rank holds alike (norm weight, bias, hidden, targets,
- *    lse, dloss)
- *    may be one buffer listed nranks times; which rank's copy is read is not
- *    said.  Inputs may overlap each other.
+ *    lse, dloss) may be one buffer listed nranks times; which rank's copy is
+ *    read is not said.  Inputs may overlap each other.
  *    A written buffer may overlap nothing (DT_ERR_ARG): no call is in place.
  *  - Where a call takes a workspace, the matching _workspace function gives
  *    its bytes (0 with dt_last_error set when the sizes are refused; a valid
@@ -363,10 +362,11 @@ dt_status dt_moe_combine_backward(const void* const* dout, const void* const* y,
 /* Softmax cross entropy over a vocabulary that is Shard(0) over the ranks,
  * without keeping the logits.  hidden[r] [tokens, cols] is Replicate;
  * weight[r] [vocab_rows[r], cols] holds the next vocab_rows[r] rows of the
- * vocabulary (V rows in all, at least one); targets[r] [tokens] int64.  lse[q] and loss[q] [tokens] fp32
- * get log sum exp of the token's logits and lse - the target's logit for
- * every rank q; a target equal to ignore_index or outside [0, V) leaves its
- * token out (loss 0, no gradient). */
+ * vocabulary (V rows in all, at least one); targets[r] [tokens] int64.  lse[q]
+ * and loss[q] [tokens] fp32 get log sum exp of the token's logits and lse - the
+ * target's logit for every rank q; a target equal to ignore_index or outside
+ * [0, V) leaves its token out (loss 0, no gradient).  At most
+ * DT_MAX_LOSS_TOKENS tokens. */
 size_t dt_vocab_loss_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols, dt_dtype dtype);
 dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, const int64_t* const* targets,
                         float* const* loss, float* const* lse, int nranks, const size_t* vocab_rows, size_t tokens,
@@ -378,8 +378,9 @@ dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, co
  * rank q (Partial -> Replicate, the AllReduce included); dweight[r]
  * [vocab_rows[r], cols] is rank r's own.  The logits are formed again, one
  * piece of at most piece_rows vocabulary rows at a time (0: the library's
- * choice); the workspace grows with the piece.  For bf16 tensors the logits'
- * gradient is rounded to bf16 before it enters the two products. */
+ * choice; never more than 2^20); the workspace grows with the piece.  For bf16
+ * tensors the logits' gradient is rounded to bf16 before it enters the two
+ * products. */
 size_t dt_vocab_loss_backward_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols,
                                         size_t piece_rows, dt_dtype dtype);
 dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* weight, const int64_t* const* targets,

@@ -205,3 +205,13 @@ def test_workspace_functions_of_the_binding_raise():
         dt.dt_vocab_loss_workspace([0], 4, 8, torch.float32)
     assert dt.dt_layer_norm_workspace([0], 8) == 0
     assert dt.dt_moe_dispatch_workspace([100, 28], 8, 2) > 0
+
+
+def test_a_piece_of_the_vocabulary_is_bounded(lib):
+    """A piece's d rows are addressed with 32 bits: no more than 2^20 vocabulary rows at once, whatever is asked for."""
+    rows = sizes(1 << 24, 1 << 24)
+    want = lib.dt_vocab_loss_backward_workspace(2, rows, 64, 8, 1 << 20, 0)
+    assert want > 0
+    for asked in ((1 << 20) + 1, 1 << 25, 1 << 60):
+        assert lib.dt_vocab_loss_backward_workspace(2, rows, 64, 8, asked, 0) == want
+    assert lib.dt_vocab_loss_backward_workspace(2, rows, 64, 8, 1 << 19, 0) < want

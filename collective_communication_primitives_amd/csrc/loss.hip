@@ -61,15 +61,28 @@ __device__ __forceinline__ rsrc_t scalar_rsrc(const char* p, uint32_t bytes) {
 // behind the last valid row (empty when not `any`), so what lies past it
 // loads zeros without touching memory.
 //
-// kRows: rows of `pitch` bytes, read up to `bytes` (a multiple of 16; where that
-// is past a row's end, the other operand has zeros there).
+// kRows: rows of `pitch` bytes, read up to `bytes`, a multiple of 16.  TAIL: the
+// row ends before that, after `valid` bytes (a multiple of 4), and what is read
+// behind its end, the next row's first values, is masked in the registers: the
+// other operand has zeros there, but an infinity times zero is NaN.
+template <bool TAIL>
 struct RowOperand {
+    static constexpr bool tail = TAIL;
     const char* p;     // the tile's first row
-    uint32_t rows, pitch, bytes;
+    uint32_t rows, pitch, bytes, valid;
     __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
         return scalar_rsrc(p + step * kStepBytes, any && rows > 0 ? rows * pitch - step * kStepBytes : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t step) const { return bytes - step * kStepBytes; }
+    // the lane's chunk of a step, without what lies behind the row
+    __device__ __forceinline__ u32x4 cut(u32x4 v, uint32_t step) const {
+        if constexpr (TAIL) {
+            const uint32_t at = step * kStepBytes + (threadIdx.x >> 4 & 3) * 16;
+#pragma unroll
+            for (int e = 0; e < 4; e++) v[e] = at + 4 * e < valid ? v[e] : 0;
+        }
+        return v;
+    }
 };
 // kCols: row k of `pitch` bytes holds the operand's m (or n) side by side.
 template <int KR>
@@ -81,6 +94,7 @@ struct ColOperand {
         return scalar_rsrc(p + uint64_t(k) * pitch, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t) const { return UINT32_MAX; }
+    __device__ __forceinline__ u32x4 cut(u32x4 v, uint32_t) const { return v; }
 };
 
 // Rows of k per step and the turned layout of a kCols operand in LDS: a row
@@ -226,7 +240,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     u32x4 fa[S::MI], fb[2][S::NI];
     uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
 #pragma unroll
-    for (int i = 0; i < S::MI; i++) fa[i] = fragment<DT, MA, S::BM>(s0, ra, i);
+    for (int i = 0; i < S::MI; i++) fa[i] = A.cut(fragment<DT, MA, S::BM>(s0, ra, i), lo);
 #pragma unroll
     for (int j = 0; j < S::NI; j++) fb[0][j] = fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j);
     // Step `step`: its registers are loaded, and the next step's bytes are in
@@ -256,7 +270,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
                                                                          acc[i][j], 0, 0, 0);
                 }
             }
-            fa[i] = fragment<DT, MA, S::BM>(following, ra, i);
+            fa[i] = A.cut(fragment<DT, MA, S::BM>(following, ra, i), step + 1);
         }
     };
     for (uint32_t step = lo; step < hi; step += 4) {
@@ -325,7 +339,7 @@ struct LossProblem {
     const float* lse;
     const float* dloss;
     uint32_t hpitch;         // bytes between hidden's rows, a multiple of 16; all of them valid
-    uint32_t wpitch;         // bytes between weight's rows; what lies behind a row's end meets zeros of hidden
+    uint32_t wpitch;         // bytes between weight's rows; not a multiple of 16: the kernels' TAIL form
     uint32_t tokens, cols, vocab;
     int64_t ignore_index;
 };
@@ -348,7 +362,7 @@ __device__ __forceinline__ void join(float& top, float& s, float top2, float s2)
     top = t;
 }
 
-template <int DT, typename S>
+template <int DT, typename S, bool TAIL>
 __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segments g, StatsArgs q) {
     __shared__ float2 part[S::GM][S::BN];
     uint32_t mt, nt;
@@ -356,8 +370,9 @@ __global__ __launch_bounds__(S::threads) void k_loss_stats(LossProblem a, Segmen
     const int sg = segment_of(g.tile, g.n, mt);
     const uint32_t m0 = (mt - g.tile[sg]) * S::BM, n0 = nt * S::BN, left = g.count[sg] - m0;
     f32x4 acc[S::MI][S::NI];
-    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch};
-    const RowOperand B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch};
+    const RowOperand<TAIL> A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch,
+                             a.cols * uint32_t(sizeof(typename Elem<DT>::type))};
+    const RowOperand<false> B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch, a.hpitch};
     matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.hpitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t wm = wave % S::GM, wn = wave / S::GM;
@@ -444,7 +459,7 @@ struct DPiece {
     int add;          // acc holds the earlier pieces' sum
 };
 
-template <int DT, typename S>
+template <int DT, typename S, bool TAIL>
 __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     uint32_t mt, nt;
@@ -454,8 +469,9 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
     const uint32_t count = g.count[sg], padded = g.col[sg + 1] - g.col[sg];
     const uint32_t left = count > m0 ? count - m0 : 0;  // the last tile may lie in the padding alone
     f32x4 acc[S::MI][S::NI];
-    const RowOperand A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch};
-    const RowOperand B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch};
+    const RowOperand<TAIL> A{g.weight[sg] + uint64_t(m0) * a.wpitch, left < S::BM ? left : S::BM, a.wpitch, a.hpitch,
+                             a.cols * uint32_t(sizeof(typename Elem<DT>::type))};
+    const RowOperand<false> B{a.hidden + uint64_t(n0) * a.hpitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, a.hpitch, a.hpitch, a.hpitch};
     matrix_tile<DT, S, kRows, kRows>(A, B, 0, (a.hpitch + kStepBytes - 1) / kStepBytes, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t mlane = (wave % S::GM) * S::WM + (lane >> 4) * 4;
@@ -508,6 +524,7 @@ struct WeightOperand {
         return scalar_rsrc(g.weight[sg] + uint64_t(row) * pitch + skip, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t) const { return UINT32_MAX; }
+    __device__ __forceinline__ u32x4 cut(u32x4 v, uint32_t) const { return v; }
 };
 
 // acc[split][t][h] (+)= sum over the split's part of the piece of d[t][v] weight[v][h].
@@ -524,7 +541,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
     const uint32_t lo = y * each + (y < more ? y : more), hi = lo + each + (y < more ? 1 : 0);
     f32x4 acc[S::MI][S::NI];
     const WeightOperand<KR> A{g, a.wpitch, m0 * uint32_t(sizeof(T)), 0};
-    const RowOperand B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch};
+    const RowOperand<false> B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch, pitch};
     matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* to = p.acc + uint64_t(blockIdx.y) * a.tokens * p.ldx;
@@ -632,6 +649,15 @@ void with_tile(Tile t, F&& launch) {
     }
     if (t == kSquare) launch(Square());
     else launch(Small());
+}
+// launch(Shape, TAIL): where weight's rows end inside a 16-byte chunk, the form
+// that masks what follows them.
+template <int DT, typename F>
+void with_rows_of(Tile t, uint32_t wpitch, F&& launch) {
+    with_tile<DT>(t, [&](auto shape) {
+        if (wpitch % 16 != 0) launch(shape, std::true_type());
+        else launch(shape, std::false_type());
+    });
 }
 
 // The workspace's parts, each on a 256-byte boundary.
@@ -770,10 +796,11 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
             set_tiles(g, kTileM[t], false);
             if (pass == 1) {
                 if (!direct) pad_weight<T>(a, first, count, wpad, p.wpitch, s);
-                with_tile<DT>(t, [&](auto shape) {
+                with_rows_of<DT>(t, p.wpitch, [&](auto shape, auto tail) {
                     typedef decltype(shape) S;
+                    constexpr bool TAIL = decltype(tail)::value;
                     q.token_tiles = ceil_div(a.tokens, S::BN);
-                    hipLaunchKernelGGL((k_loss_stats<DT, S>), dim3(g.tile[g.n] * q.token_tiles), dim3(S::threads), 0, s, p, g, q);
+                    hipLaunchKernelGGL((k_loss_stats<DT, S, TAIL>), dim3(g.tile[g.n] * q.token_tiles), dim3(S::threads), 0, s, p, g, q);
                 });
             }
             q.entry += g.tile[g.n];
@@ -840,10 +867,11 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
             if (wpad != nullptr) pad_weight<T>(a, first, count, wpad, q.wpitch, s);
             const Tile t = pick_tile(DT, count, a.tokens);
             set_tiles(g, kTileM[t], true);
-            with_tile<DT>(t, [&](auto shape) {
+            with_rows_of<DT>(t, q.wpitch, [&](auto shape, auto tail) {
                 typedef decltype(shape) S;
+                constexpr bool TAIL = decltype(tail)::value;
                 p.nt = ceil_div(a.tokens, S::BN);
-                hipLaunchKernelGGL((k_loss_d<DT, S>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
+                hipLaunchKernelGGL((k_loss_d<DT, S, TAIL>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
             });
             with_tile<DT>(pick_tile(DT, a.cols, a.tokens, p.splits), [&](auto shape) {
                 typedef decltype(shape) S;

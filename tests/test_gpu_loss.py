@@ -163,3 +163,29 @@ def test_gradients_against_differences(dt):
         up[0][v, 3] += e
         dn[0][v, 3] -= e
         assert abs((value(x, up) - value(x, dn)) / (2 * e) - float(dw[0].t.view(9, 24)[v, 3])) < 2e-5
+
+
+@pytest.mark.parametrize("dtype,cols", [(torch.bfloat16, 34), (torch.bfloat16, 1002), (torch.bfloat16, 35), (torch.float32, 33),
+                                        (torch.float32, 131), (torch.float32, 64)], ids=str)
+def test_an_infinite_weight_stays_in_its_row(dt, dtype, cols):
+    """A vocabulary row that -inf takes out (all hidden values of that column
+    positive) leaves the rows beside it alone, wherever a row ends."""
+    note(f"loss row of -inf, {cols} columns {dtype}")
+    h, w, t, g = _make(70, cols, [200, 90], dtype, 14, replicas=False)
+    h[0][:, 0] = h[0][:, 0].abs() + 0.5
+    t[0].clamp_(min=10)
+    gone = [3, 4, 199]
+    for v in gone:
+        w[0][v] = 0
+        w[0][v, 0] = -float("inf")
+    t[0][torch.isin(t[0], torch.tensor(gone, device="cuda"))] = 11
+    loss, lse, dh, dw = _run(dt, h, w, t, g)
+    keep = [v for v in range(200) if v not in gone]
+    want = ref.loss(h[0], [w[0][keep], w[1]], t[0] - (t[0] > 3).long() - (t[0] > 4).long() - (t[0] > 199).long(), g[0])
+    for q in range(2):
+        ref.assert_close(lse[q].t, *want["lse"], f"lse[{q}]")
+        ref.assert_close(loss[q].t, *want["loss"], f"loss[{q}]")
+    mine = dw[0].t.view(200, cols)
+    ref.assert_close(mine[keep], want["dweight"][0][0], want["dweight"][1][0], "dweight[0]")
+    ref.assert_close(dw[1].t.view(90, cols), want["dweight"][0][1], want["dweight"][1][1], "dweight[1]")
+    assert bool((mine[gone] == 0).all())

@@ -125,6 +125,14 @@ dt_status check_cols(size_t cols, const char* what) {
     return DT_OK;
 }
 
+// A launch of the expert calls takes up to 256 threads a token, and HIP counts
+// a launch's threads in 32 bits.
+dt_status check_tokens(const RowTable& t, int nranks) {
+    if (t.start[nranks] > DT_MAX_MOE_TOKENS)
+        return fail(DT_ERR_ARG, "tokens: %u in all, above %d", t.start[nranks], DT_MAX_MOE_TOKENS);
+    return DT_OK;
+}
+
 dt_status check_experts(int nexperts, int topk) {
     if (nexperts < 1 || nexperts > DT_MAX_EXPERTS)
         return fail(DT_ERR_ARG, "nexperts=%d outside [1, %d]", nexperts, DT_MAX_EXPERTS);
@@ -244,6 +252,7 @@ dt_status dt_moe_route(const void* const* logits, int32_t* const* experts, float
     TRY(check_ranks(nranks));
     TRY(check_float(dtype, "moe_route"));
     TRY(row_table(tokens, nranks, "tokens", a.rows));
+    TRY(check_tokens(a.rows, nranks));
     TRY(check_experts(nexperts, topk));
     if (score != DT_SCORE_SOFTMAX && score != DT_SCORE_SIGMOID) return fail(DT_ERR_ARG, "bad score %d", int(score));
     if (groups < 1 || groups > DT_MAX_GROUPS || nexperts % groups != 0)
@@ -284,6 +293,7 @@ dt_status dt_moe_route_backward(const void* const* logits, const int32_t* const*
     TRY(check_ranks(nranks));
     TRY(check_float(dtype, "moe_route_backward"));
     TRY(row_table(tokens, nranks, "tokens", a.rows));
+    TRY(check_tokens(a.rows, nranks));
     TRY(check_experts(nexperts, topk));
     if (score != DT_SCORE_SOFTMAX && score != DT_SCORE_SIGMOID) return fail(DT_ERR_ARG, "bad score %d", int(score));
     const size_t es = esize_of(dtype);
@@ -328,6 +338,7 @@ dt_status exchange_shape(int nranks, const size_t* tokens, const size_t* capacit
     if (nexperts % nranks != 0) return fail(DT_ERR_ARG, "%s: %d experts do not divide by %d ranks", what, nexperts, nranks);
     if (uint64_t(s.rows.start[nranks]) * topk >= DT_MAX_STEP_ROWS)
         return fail(DT_ERR_ARG, "%s: %d or more slots in all", what, DT_MAX_STEP_ROWS);
+    TRY(check_tokens(s.rows, nranks));
     if (capacity == nullptr) return fail(DT_ERR_ARG, "capacity is NULL");
     for (int q = 0; q < nranks; q++) {
         if (capacity[q] >= DT_MAX_STEP_ROWS) return fail(DT_ERR_ARG, "capacity[%d] is too large", q);
@@ -359,7 +370,7 @@ size_t dt_moe_dispatch_workspace(int nranks, const size_t* tokens, int nexperts,
     RowTable t;
     dt::report_error(DT_OK, "");
     if (check_ranks(nranks) != DT_OK || row_table(tokens, nranks, "tokens", t) != DT_OK ||
-        check_experts(nexperts, topk) != DT_OK)
+        check_tokens(t, nranks) != DT_OK || check_experts(nexperts, topk) != DT_OK)
         return 0;
     return plan_bytes(t, nranks, nexperts, topk);
 }

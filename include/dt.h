@@ -275,6 +275,7 @@ dt_status dt_barrier_exchange(const void* const* src, void* const* stage, void* 
  *  - Every call may be captured into a HIP graph. */
 #define DT_MAX_STEP_ROWS (1 << 30)
 #define DT_MAX_STEP_COLS (1 << 18)
+#define DT_MAX_MOE_TOKENS (1 << 23) /* of all ranks together, in the expert calls */
 #define DT_MAX_EXPERTS 1024
 #define DT_MAX_TOPK 64
 #define DT_MAX_GROUPS 64

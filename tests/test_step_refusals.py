@@ -215,3 +215,20 @@ def test_a_piece_of_the_vocabulary_is_bounded(lib):
     for asked in ((1 << 20) + 1, 1 << 25, 1 << 60):
         assert lib.dt_vocab_loss_backward_workspace(2, rows, 64, 8, asked, 0) == want
     assert lib.dt_vocab_loss_backward_workspace(2, rows, 64, 8, 1 << 19, 0) < want
+
+
+def test_the_expert_calls_bound_their_tokens(lib):
+    """More tokens than a launch's 32-bit thread count carries are refused, not left to the launch."""
+    n, far = (1 << 23) + 1, 1 << 40
+    lists = [ptrs(far * i) for i in range(1, 8)]
+    calls = (lambda: route(lib, n=sizes(n), x=lists[0], e=lists[1], w=lists[2], ne=1, k=1),
+             lambda: route_back(lib, n=sizes(n), x=lists[0], e=lists[1], w=lists[2], d=lists[3], ne=1, k=1),
+             lambda: dispatch(lib, p=1, n=sizes(n), x=lists[0], e=lists[1], r=lists[2], pos=lists[3], off=lists[4], cap=sizes(8), ne=1, k=1),
+             lambda: combine(lib, p=1, n=sizes(n), y=lists[0], e=lists[1], pos=lists[2], out=lists[3], cap=sizes(8), ne=1, k=1),
+             lambda: combine_back(lib, p=1, n=sizes(n), do=lists[0], y=lists[1], e=lists[2], pos=lists[3], w=lists[4], dy=lists[5],
+                                  dw=lists[6], cap=sizes(8), ne=1, k=1))
+    for call in calls:
+        assert call() == ARG
+        assert "tokens" in lib.dt_last_error().decode()
+    assert lib.dt_moe_dispatch_workspace(1, sizes(n), 8, 1) == 0 and lib.dt_last_error()
+    assert lib.dt_moe_dispatch_workspace(1, sizes(n - 1), 8, 1) > 0

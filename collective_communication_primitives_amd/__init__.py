@@ -127,6 +127,10 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream
 
 
+def _as_stream(handle: int, dev: int) -> torch.cuda.Stream:
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
 _side_streams: Dict[int, torch.cuda.Stream] = {}
 
 
@@ -248,14 +252,40 @@ class Prepared:
     ``prepare``).  Each call enqueues it again on ``stream`` (default: the
     current stream) at the host cost of the C call alone: the pointer arrays
     and checks were done once.  The buffers stay referenced while this object
-    lives; their contents may change between calls."""
+    lives; their contents may change between calls.  A graph that captured a
+    call needs this object for as long as it is replayed, and calls on several
+    streams at once need a prepared call each: they share its buffers."""
 
-    def __init__(self, fn, stash: List[torch.Tensor]):
+    def __init__(self, fn, stash: List[torch.Tensor], space: Optional["_Space"] = None):
         self._fn = fn
         self._stash = stash
+        self._space = space
 
     def __call__(self, stream=None) -> None:
-        _check(self._fn(_stream_handle(stream)))
+        handle = _stream_handle(stream)
+        if self._space is not None:
+            self._space.used_on(handle)
+        _check(self._fn(handle))
+
+
+class _Space:
+    """The workspace that prepare() made for a call: torch's allocator hands it
+    out in the order of one stream, so another stream that runs the call first
+    waits for that order and is recorded as a user of the memory."""
+
+    def __init__(self, tensor: torch.Tensor, home: int):
+        self._tensor = tensor
+        self._seen = {home}
+        self._ready = torch.cuda.Event()
+        self._ready.record(_as_stream(home, tensor.device.index))
+
+    def used_on(self, handle: int) -> None:
+        if handle in self._seen or torch.cuda.is_current_stream_capturing():
+            return  # a capture begins behind all work of the device
+        stream = _as_stream(handle, self._tensor.device.index)
+        stream.wait_event(self._ready)
+        self._tensor.record_stream(stream)
+        self._seen.add(handle)
 
 
 def prepare(collective, *args, **kwargs) -> Prepared:
@@ -266,15 +296,18 @@ def prepare(collective, *args, **kwargs) -> Prepared:
         raise ValueError("prepare() binds a synchronous call; order it with streams and events")
     _preparing.active = True
     _preparing.result = None
+    _preparing.space = None
     try:
         collective(*args, **kwargs)
         if _preparing.result is None:
             raise TypeError(f"{collective!r} does not enqueue a collective")
         fn, stash = _preparing.result
+        space = _preparing.space
     finally:
         _preparing.active = False
         _preparing.result = None
-    return Prepared(fn, stash)
+        _preparing.space = None
+    return Prepared(fn, stash, space)
 
 
 def _launch(fn, stash, async_op: bool, stream, comm_stream):
@@ -674,20 +707,24 @@ def _float_dtype(t: torch.Tensor) -> int:
 def _workspace(given: Optional[torch.Tensor], nbytes: int, dev: int, stream, async_op: bool, comm_stream,
                stash: list) -> torch.Tensor:
     """The call's workspace: the caller's, or a block of torch's caching
-    allocator that is not reused before the stream that runs the call has
-    passed it."""
+    allocator, taken in the order of the stream that runs the call.  (An async
+    call's stream waits for the producer, whose order serves as well.)"""
     if given is not None:
         _on_gpu([given], "workspace")
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace must hold {nbytes} bytes, got {given.numel() * given.element_size()}")
         stash.append(given)
         return given
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    runs_on = (comm_stream if comm_stream is not None else side_stream(dev)) if async_op else stream
-    if runs_on is not None:
-        if isinstance(runs_on, int):
-            runs_on = torch.cuda.ExternalStream(runs_on, device=dev)
-        ws.record_stream(runs_on)
+    home = _stream_handle(stream)
+    if home == _current_stream_handle():
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(_as_stream(home, dev)):
+            ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    if getattr(_preparing, "active", False):
+        _preparing.space = _Space(ws, home)
+    if async_op:
+        ws.record_stream(_as_stream(_stream_handle(comm_stream if comm_stream is not None else side_stream(dev)), dev))
     stash.append(ws)
     return ws
 

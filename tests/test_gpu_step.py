@@ -228,3 +228,46 @@ def test_the_binding_refuses(dt):
         dt.dt_moe_route(x, ex, we)  # one buffer for two ranks' experts
     with pytest.raises(ValueError):
         dt.dt_moe_combine(x, ex, ex, we, y, 3)  # 3 experts on 2 ranks
+
+
+def test_a_workspace_of_the_library_on_other_streams(dt):
+    """The library's own workspace, taken while the current stream still writes a block that was just given back:
+    the call on another stream, plain or prepared, neither sees nor disturbs that."""
+    note("step operators: workspace of the library on another stream")
+    p, rows, cols = 2, 600, 256
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x, dy = ([torch.randn(rows, cols, generator=g, device="cuda") for _ in range(p)] for _ in range(2))
+    w = [torch.ones(cols, device="cuda")] * p
+    y, dx = ([torch.empty_like(v) for v in x] for _ in range(2))
+    m, r = ([torch.empty(rows, device="cuda") for _ in range(p)] for _ in range(2))
+    want, dw = ([torch.empty(cols, device="cuda") for _ in range(p)] for _ in range(2))
+    dt.dt_layer_norm(x, w, None, y, m, r)
+    dt.dt_layer_norm_backward(dy, x, w, m, r, dx, want)
+    nbytes = dt.dt_layer_norm_workspace([rows] * p, cols)
+    other, third = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for v in dw:
+            v.zero_()
+        torch.cuda.synchronize()
+        block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(5_000_000)
+        block.fill_(255)
+        del block
+        dt.dt_layer_norm_backward(dy, x, w, m, r, dx, dw, stream=other)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(dw, want))
+        for v in dw:
+            v.zero_()
+        torch.cuda.synchronize()
+        block = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(5_000_000)
+        block.fill_(255)
+        del block
+        step = dt.prepare(dt.dt_layer_norm_backward, dy, x, w, m, r, dx, dw)
+        step(third)
+        del step
+        block = torch.empty(nbytes, dtype=torch.uint8, device="cuda").fill_(255)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(dw, want))
+        del block

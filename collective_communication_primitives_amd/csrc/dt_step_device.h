@@ -115,6 +115,12 @@ __device__ __forceinline__ void rotations(F&& step) {
     step(std::integral_constant<int, kRotate + 14>());
     step(std::integral_constant<int, kRotate + 15>());
 }
+// step(k, control that gives every lane of the 16 lane k's value), k = 0 .. 15.
+template <int K = 0, typename F>
+__device__ __forceinline__ void broadcasts16(F&& step) {
+    step(std::integral_constant<int, K>(), std::integral_constant<int, 0x150 + K>());
+    if constexpr (K < 15) broadcasts16<K + 1>(step);
+}
 __device__ __forceinline__ float max16(float v) {
     over16([&](auto c) { v = fmaxf(v, dpp<decltype(c)::value>(v)); });
     return v;

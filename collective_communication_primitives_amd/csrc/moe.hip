@@ -233,149 +233,139 @@ __device__ __forceinline__ void load_bias(const float* bias, uint32_t nexperts, 
     for (int i = 0; i < NL; i++) b[i] = bias[first + i < nexperts ? first + i : nexperts - 1];
 }
 
-// max over the 16 lanes of 64-bit keys.
-__device__ __forceinline__ int64_t max16_wide(int64_t v) {
-    over16([&](auto c) {
-        const uint64_t u = uint64_t(v);
-        const uint64_t o = uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u));
-        v = int64_t(o) > v ? int64_t(o) : v;
-    });
-    return v;
-}
 __device__ __forceinline__ int64_t ordered(double f) {
     const int64_t i = __double_as_longlong(f);
     return i ^ int64_t(uint64_t(i >> 63) >> 1);
 }
 __device__ __forceinline__ double unordered(int64_t i) { return __longlong_as_double(i ^ int64_t(uint64_t(i >> 63) >> 1)); }
 
-// What the 16 lanes of a token know about it.
-struct RouteToken {
-    uint32_t nexperts, topk, groups, topk_groups, first;  // first: the lane's first expert
-    int sigmoid;
-    const float* bias;
-};
-
 // The groups that stay: true in the lanes of one of them.  m1, m2: the lane's
 // two largest candidates as ordered integers, `none` where there is none; a
 // group is `width` neighbouring lanes, a power of two.  `margin`: how far the
-// last score that stays is above the first that goes.
-template <typename K>
-__device__ __forceinline__ bool stays_in(const RouteToken& a, uint32_t width, K m1, K m2, K none, float& margin, float& size) {
-    typedef decltype(unordered(K())) F;
+// last score that stays, of size `size`, is above the first that goes.
+__device__ __forceinline__ bool stays_in(uint32_t topk_groups, uint32_t width, int32_t m1, int32_t m2, int32_t none, float& margin,
+                                         float& size) {
     const uint32_t lane = threadIdx.x & 15, group = lane / width;
     uint32_t w = 1;
     over16([&](auto c) {
-        constexpr int C = decltype(c)::value;
-        K o1, o2;
-        if constexpr (sizeof(K) == 4) {
-            o1 = K(dpp<C>(uint32_t(m1)));
-            o2 = K(dpp<C>(uint32_t(m2)));
-        } else {
-            o1 = K(uint64_t(dpp<C>(uint32_t(uint64_t(m1) >> 32))) << 32 | dpp<C>(uint32_t(m1)));
-            o2 = K(uint64_t(dpp<C>(uint32_t(uint64_t(m2) >> 32))) << 32 | dpp<C>(uint32_t(m2)));
-        }
+        const int32_t o1 = int32_t(dpp<decltype(c)::value>(uint32_t(m1))), o2 = int32_t(dpp<decltype(c)::value>(uint32_t(m2)));
         if (w < width) {
-            const K low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
+            const int32_t low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
             m2 = low > second ? low : second;
             m1 = o1 > m1 ? o1 : m1;
         }
         w *= 2;
     });
     // one expert left in a group: it alone; none: the group goes
-    const F score = m1 == none ? F(-INFINITY) : m2 == none ? unordered(m1) : unordered(m1) + unordered(m2);
-    const K key = score > F(-INFINITY) ? ordered(score + F(0)) : none;
+    const float score = m1 == none ? -INFINITY : m2 == none ? unordered(m1) : unordered(m1) + unordered(m2);
+    const int32_t key = score > -INFINITY ? ordered(score + 0.f) : none;
     uint32_t better = 0;
     rotations([&](auto c) {
-        constexpr int C = decltype(c)::value;
-        K o;
-        if constexpr (sizeof(K) == 4) o = K(dpp<C>(uint32_t(key)));
-        else o = K(uint64_t(dpp<C>(uint32_t(uint64_t(key) >> 32))) << 32 | dpp<C>(uint32_t(key)));
-        const uint32_t og = dpp<C>(group);
+        const int32_t o = int32_t(dpp<decltype(c)::value>(uint32_t(key)));
+        const uint32_t og = dpp<decltype(c)::value>(group);
         better += og != group && (o > key || (o == key && og < group)) ? 1 : 0;
     });
-    const bool stays = better < a.topk_groups * width && key != none;
-    if constexpr (sizeof(K) == 4) {
-        const float last = -max16(stays ? -score : -INFINITY), next = max16(stays ? -INFINITY : score);
-        margin = last - next;
-        size = fabsf(last);
-    }
+    const bool stays = better < topk_groups * width && key != none;
+    const float last = -max16(stays ? -score : -INFINITY), next = max16(stays ? -INFINITY : score);
+    margin = last - next;
+    size = fabsf(last);
     return stays;
 }
 
-// The choice in 64 bits: lane j's `mine` becomes choice j's expert, UINT32_MAX
-// where none is left.  Logits and biases are read again one by one: held in
-// registers they would double what the kernel takes, and so halve the waves of
-// the tokens that never come here.
-template <int DT, int NL>
-__device__ __forceinline__ uint32_t choose_exactly(const RouteToken& a, const typename Elem<DT>::type* logits) {
-    const uint32_t lane = threadIdx.x & 15;
+// The choice for one token by the whole wave, in 64 bits: lane l has experts [l *
+// NK, l * NK + NK), lane j gets choice j's expert, UINT32_MAX where none is left.
+// The kernel's last waves wait for it, so it is short in time and in code: the 16
+// lanes of the token alone, 4 NK experts each, took 10 us.
+template <int DT, int NK>
+__device__ __forceinline__ uint32_t choose_exactly(const RouteArgs& a, const typename Elem<DT>::type* logits) {
+    const uint32_t lane = threadIdx.x & 63, first = lane * NK;
     constexpr int64_t kLowest = INT64_MIN;
-    int64_t key[NL];
-    auto logit = [&](int i) {
-        asm volatile("" ::: "memory");  // no load is moved ahead
-        const uint32_t e = a.first + i < a.nexperts ? a.first + i : a.nexperts - 1;
-        const float x = Elem<DT>::get(logits[e]);
-        return a.first + i < a.nexperts && x > -INFINITY ? fminf(x, kBiggest) + 0.f : -INFINITY;
-    };
+    float x[NK], b[NK];
+#pragma unroll
+    for (int i = 0; i < NK; i++) {
+        const uint32_t e = first + i < a.nexperts ? first + i : a.nexperts - 1;
+        x[i] = Elem<DT>::get(logits[e]);
+        b[i] = a.bias != nullptr ? a.bias[e] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NK; i++) x[i] = first + i < a.nexperts && x[i] > -INFINITY ? fminf(x[i], kBiggest) + 0.f : -INFINITY;
     const bool scored = a.bias != nullptr || a.groups > 1;
     double sum = 0., top = 0.;
     if (scored && !a.sigmoid) {
         float most = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < NL; i++) most = fmaxf(most, logit(i));
-        top = double(max16(most));
+        for (int i = 0; i < NK; i++) most = fmaxf(most, x[i]);
+        top = double(wave_max(most));
 #pragma unroll
-        for (int i = 0; i < NL; i++) {
-            const float x = logit(i);
-            sum += x > -INFINITY ? exp(double(x) - top) : 0.;
-        }
-        over16([&](auto c) {
-            const uint64_t u = __double_as_longlong(sum);
-            sum += __longlong_as_double(int64_t(uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u))));
-        });
+        for (int i = 0; i < NK; i++) sum += x[i] > -INFINITY ? exp(double(x[i]) - top) : 0.;
+#pragma unroll 1
+        for (int m = 1; m < 64; m <<= 1) sum += shfl_xor_d(sum, m);
     }
+    int64_t key[NK];
 #pragma unroll
-    for (int i = 0; i < NL; i++) {
-        const float x = logit(i);
-        double v = double(x);
-        bool live = x > -INFINITY;
+    for (int i = 0; i < NK; i++) {
+        double v = double(x[i]);
         if (scored) v = a.sigmoid ? 1. / (1. + exp(-v)) : exp(v - top) / sum;
-        if (a.bias != nullptr) {
-            const float b = a.bias[a.first + i < a.nexperts ? a.first + i : a.nexperts - 1];
-            live = live && b > -INFINITY;
-            v += double(b);
-        }
-        key[i] = live ? ordered(v + 0.) : kLowest;
+        if (a.bias != nullptr) v += double(b[i]);
+        key[i] = x[i] > -INFINITY && b[i] > -INFINITY ? ordered(v + 0.) : kLowest;
     }
     if (a.groups > 1) {
+        const uint32_t width = a.nexperts / a.groups / NK, group = lane / width;  // lanes of a group, a power of two
         int64_t m1 = kLowest, m2 = kLowest;
 #pragma unroll
-        for (int i = 0; i < NL; i++) {
+        for (int i = 0; i < NK; i++) {
             const int64_t low = m1 < key[i] ? m1 : key[i];
             m2 = low > m2 ? low : m2;
             m1 = key[i] > m1 ? key[i] : m1;
         }
-        float margin = 0.f, size = 0.f;
-        const bool stays = stays_in<int64_t>(a, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
+#pragma unroll 1
+        for (uint32_t w = 1; w < width; w <<= 1) {
+            const int64_t o1 = __shfl_xor(m1, int(w)), o2 = __shfl_xor(m2, int(w));
+            const int64_t low = m1 < o1 ? m1 : o1, second = m2 > o2 ? m2 : o2;
+            m2 = low > second ? low : second;
+            m1 = o1 > m1 ? o1 : m1;
+        }
+        const double score = m1 == kLowest ? -INFINITY : m2 == kLowest ? unordered(m1) : unordered(m1) + unordered(m2);
+        const int64_t mine = m1 != kLowest ? ordered(score + 0.) : kLowest;
+        uint32_t better = 0;
+#pragma unroll 1
+        for (uint32_t g = 0; g < a.groups; g++) {
+            const int64_t o = __shfl(mine, int(g * width));
+            better += g != group && (o > mine || (o == mine && g < group)) ? 1 : 0;
+        }
+        const bool stays = better < a.topk_groups && mine != kLowest;
 #pragma unroll
-        for (int i = 0; i < NL; i++) {
+        for (int i = 0; i < NK; i++) {
             if (!stays) key[i] = kLowest;
-            else if (a.bias == nullptr && key[i] != kLowest) key[i] = ordered(double(logit(i)));
+            else if (a.bias == nullptr && key[i] != kLowest) key[i] = ordered(double(x[i]));
         }
     }
     uint32_t mine = UINT32_MAX;
+#pragma unroll 1
     for (uint32_t k = 0; k < a.topk; k++) {
-        int64_t best = key[0];
+        int64_t own = key[0];
+        uint32_t at = first;
 #pragma unroll
-        for (int i = 1; i < NL; i++) best = key[i] > best ? key[i] : best;
-        best = max16_wide(best);
-        uint32_t at = UINT32_MAX;
+        for (int i = 1; i < NK; i++) {
+            at = key[i] > own ? first + i : at;
+            own = key[i] > own ? key[i] : own;
+        }
+        int64_t best = own;
+        over16([&](auto c) {
+            const uint64_t u = uint64_t(best);
+            const int64_t o = int64_t(uint64_t(dpp<decltype(c)::value>(uint32_t(u >> 32))) << 32 | dpp<decltype(c)::value>(uint32_t(u)));
+            best = o > best ? o : best;
+        });
 #pragma unroll
-        for (int i = NL - 1; i >= 0; i--) at = key[i] == best ? a.first + i : at;
-        at = best > kLowest ? min16(at) : UINT32_MAX;
-        const uint32_t here = at - a.first;
+        for (int m = 16; m < 64; m <<= 1) {
+            const int64_t o = __shfl_xor(best, m);
+            best = o > best ? o : best;
+        }
+        if (best == kLowest) break;
+        const uint32_t from = uint32_t(__builtin_ctzll(__ballot(own == best)));  // experts rise with the lanes
+        at = uint32_t(__builtin_amdgcn_readlane(int(at), int(from)));
 #pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = here == uint32_t(i) ? kLowest : key[i];
+        for (int i = 0; i < NK; i++) key[i] = at == first + i ? kLowest : key[i];
         if (lane == k) mine = at;
     }
     return mine;
@@ -415,7 +405,7 @@ __device__ __forceinline__ void sort_down(int32_t (&key)[NL]) {
 //   the bias' addition  U |c|.
 // Where two neighbours in the order, the last choice and the one behind it, or
 // the last group that stays and the first that goes are that close, the wave
-// chooses again in 64 bits: about one token in a thousand of normally
+// chooses for that token again in 64 bits: about one token in a thousand of normally
 // distributed logits with a bias.
 //
 // 32768 tokens, 8 of 256 experts, sigmoid, bias, 8 groups: bound by the vector
@@ -432,7 +422,6 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     while (r + 1 < nranks && row >= a.rows.start[r + 1]) r++;
     const uint64_t local = row - a.rows.start[r];
     const uint32_t first = lane * NL;
-    const RouteToken token{a.nexperts, a.topk, a.groups, a.topk_groups, first, a.sigmoid, a.bias};
     constexpr float U = 5.9604645e-8f;
     constexpr int32_t kPlace = NL - 1, kLowest = INT32_MIN;
     float x[NL];
@@ -489,7 +478,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
                 m1 = key[i] > m1 ? key[i] : m1;
             }
             float margin = 0.f, size = 0.f;
-            stays = stays_in<int32_t>(token, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
+            stays = stays_in(a.topk_groups, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
             close = margin <= 4.f * off + 2.f * U * size;
         }
     }
@@ -530,8 +519,17 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
         const float next = lane + 1 < a.topk ? after : tail;
         close = close || (lane < a.topk && next > -INFINITY && v - next <= 2.f * off + 2.f * U * fabsf(v));
     }
+    for (uint64_t todo = __ballot(close); todo != 0;) {  // one of the wave's tokens at a time
+        const uint32_t at = uint32_t(__builtin_ctzll(todo)) & 48;
+        todo &= ~(0xFFFFull << at);
+        const uint64_t p = reinterpret_cast<uint64_t>(logits);
+        const uint64_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(p)), int(at)));
+        const uint64_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(p >> 32)), int(at)));
+        const uint32_t exact = choose_exactly<DT, NL / 4>(a, reinterpret_cast<const T*>(hi << 32 | lo));
+        const uint32_t choice = uint32_t(__shfl(int(exact), int(lane)));
+        if ((threadIdx.x & 48) == at) mine = choice;
+    }
     if (__any(close)) {
-        mine = choose_exactly<DT, NL>(token, logits);
         logit = mine != UINT32_MAX ? fminf(Elem<DT>::get(logits[mine]), kBiggest) : -INFINITY;
     }
     const bool has = mine != UINT32_MAX;
@@ -590,7 +588,7 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
         top = max_lanes<L>(top);
 #pragma unroll
         for (int i = 0; i < NL; i++) {
-            s[i] = s[i] > -INFINITY ? expf(s[i] - top) : 0.f;
+            s[i] = s[i] > -INFINITY ? __builtin_amdgcn_exp2f((s[i] - top) * kLog2e) : 0.f;
             total += s[i];
         }
         total = sum_lanes<L>(total);
@@ -598,18 +596,18 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
     // lane j: choice j's logit and gradient
     int32_t e = lane < a.topk ? a.experts[r][local * a.topk + lane] : -1;
     float g = 0.f, logit = -INFINITY;
-    if (e >= 0 && uint32_t(e) < a.nexperts) {
-        g = a.dweights[r][local * a.topk + lane] * a.scale;
+    if (lane < a.topk) g = a.dweights[r][local * a.topk + lane] * a.scale;
+    // dense: the choice's score is in the registers of the lane that holds its expert
+    if (!dense && e >= 0 && uint32_t(e) < a.nexperts) {
         const float l = Elem<DT>::get(static_cast<const T*>(a.logits[r])[local * a.nexperts + e]);
         logit = l > -INFINITY ? fminf(l, kBiggest) : -INFINITY;
     }
     const bool has = logit > -INFINITY;
-    if (!has) {
+    if (!dense && !has) {
         g = 0.f;
         e = -1;
     }
     float t;  // what choice j adds to its expert
-    float all = 0.f;
     if (a.renormalize) {
         const float ctop = max_lanes<L>(logit);
         float w = has ? expf(logit - ctop) : 0.f;
@@ -621,23 +619,35 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
     } else if (a.sigmoid) {
         t = has ? g / (1.f + expf(-logit)) / (1.f + expf(logit)) : 0.f;
     } else {
-        all = sum_lanes<L>(has ? g * (expf(logit - top) / total) : 0.f);
         t = g;
     }
     float d[NL];
 #pragma unroll
     for (int i = 0; i < NL; i++) d[i] = 0.f;
-    const int base = int(threadIdx.x & 63) - int(lane);
-    for (uint32_t k = 0; k < a.topk; k++) {
-        const uint32_t at = uint32_t(__shfl(e, base + int(k))) - first;  // huge when it is not this lane's
-        const float tk = __shfl(t, base + int(k));
+    auto add = [&](uint32_t ek, float tk) {
+        const uint32_t at = ek - first;  // huge when it is not this lane's
 #pragma unroll
         for (int i = 0; i < NL; i++) d[i] += at == uint32_t(i) ? tk : 0.f;
+    };
+    if constexpr (L == 16) {
+        broadcasts16([&](auto k, auto c) {
+            if (uint32_t(decltype(k)::value) < a.topk) add(dpp<decltype(c)::value>(uint32_t(e)), dpp<decltype(c)::value>(t));
+        });
+    } else {
+        for (uint32_t k = 0; k < a.topk; k++) add(uint32_t(__shfl(e, int(k))), __shfl(t, int(k)));
     }
     if (dense) {
         const float inv = total > 0.f ? 1.f / total : 0.f;
+        float all = 0.f;
 #pragma unroll
-        for (int i = 0; i < NL; i++) d[i] = s[i] * inv * (d[i] - all);
+        for (int i = 0; i < NL; i++) {
+            s[i] *= inv;
+            d[i] = s[i] > 0.f ? d[i] : 0.f;  // an expert that was out has no gradient
+            all += s[i] * d[i];
+        }
+        all = sum_lanes<L>(all);
+#pragma unroll
+        for (int i = 0; i < NL; i++) d[i] = s[i] * (d[i] - all);
     }
     if (!there || first >= a.nexperts) return;
     T* dx = static_cast<T*>(a.dlogits[r]) + local * a.nexperts + first;

@@ -223,7 +223,7 @@ __device__ __forceinline__ void load_logits(const void* base, uint64_t row, uint
         for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? x[i] : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < NL; i++) x[i] = x[i] > -INFINITY ? fminf(x[i], kBiggest) + 0.f : -INFINITY;  // + 0: no -0
+    for (int i = 0; i < NL; i++) x[i] = fminf(fmaxf(x[i], -INFINITY), kBiggest) + 0.f;  // NaN to -inf; + 0: no -0
 }
 
 // The lane's experts' biases.
@@ -402,7 +402,7 @@ __device__ __forceinline__ void sort_down(int32_t (&key)[NL]) {
 //            sum, 2 U of the reciprocal: under 5 U;
 //   softmax, s <= 1:  (2 |d| + 2) s U <= 3 U of the exponential and its argument d = x - max,
 //            (NL + 4) U <= 36 U of the sum and 4 U of the quotient: under 48 U;
-//   the bias' addition  U |c|.
+//   the bias' addition  U |c|, for each of the two that are compared.
 // Where two neighbours in the order, the last choice and the one behind it, or
 // the last group that stays and the first that goes are that close, the wave
 // chooses for that token again in 64 bits: about one token in a thousand of normally
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     const uint64_t local = row - a.rows.start[r];
     const uint32_t first = lane * NL;
     constexpr float U = 5.9604645e-8f;
-    constexpr int32_t kPlace = NL - 1, kLowest = INT32_MIN;
+    constexpr int32_t kPlace = NL - 1;
     float x[NL];
     int32_t key[NL];
     load_logits<DT, NL>(a.logits[r], local, a.nexperts, first, vec, x);
@@ -431,63 +431,67 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     float top = 0.f, sum = 0.f, off = 0.f;
     bool close = false, stays = true;
     if (scored || (!a.sigmoid && !a.renormalize)) {
+        float c[NL];
         if (a.sigmoid) {
 #pragma unroll
-            for (int i = 0; i < NL; i++) key[i] = ordered(__builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e)));
+            for (int i = 0; i < NL; i++) c[i] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[i] * -kLog2e));
             off = 5.f * U;
         } else {
-            int32_t most = kNone;
+            float most = x[0];
+#pragma unroll
+            for (int i = 1; i < NL; i++) most = fmaxf(most, x[i]);
+            most = max16(most);
+            top = most > -INFINITY ? most : 0.f;
 #pragma unroll
             for (int i = 0; i < NL; i++) {
-                const int32_t o = ordered(x[i]);
-                most = o > most ? o : most;
-            }
-            top = unordered(max16(most));
-            float s[NL];
-#pragma unroll
-            for (int i = 0; i < NL; i++) {
-                s[i] = x[i] > -INFINITY ? __builtin_amdgcn_exp2f((x[i] - top) * kLog2e) : 0.f;
-                sum += s[i];
+                c[i] = __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+                sum += c[i];
             }
             sum = sum16(sum);
             const float inv = 1.f / sum;
 #pragma unroll
-            for (int i = 0; i < NL; i++) key[i] = ordered(s[i] * inv);
+            for (int i = 0; i < NL; i++) c[i] *= inv;
             off = 48.f * U;
         }
-        if (a.bias != nullptr) {
-            float big = 0.f, b[NL];
-            load_bias<NL>(a.bias, a.nexperts, first, b);
+        if (scored) {
+            // a candidate that is out is -inf, also where the bias is NaN
+            float big = 0.f;
+            if (a.bias != nullptr) {
+                float b[NL];
+                load_bias<NL>(a.bias, a.nexperts, first, b);
 #pragma unroll
-            for (int i = 0; i < NL; i++) {
-                const bool live = x[i] > -INFINITY && b[i] > -INFINITY;
-                key[i] = live ? ordered(unordered(key[i]) + b[i] + 0.f) : kLowest;
-                big = fmaxf(big, live ? fabsf(b[i]) : 0.f);
+                for (int i = 0; i < NL; i++) c[i] = fmaxf(x[i] > -INFINITY ? c[i] + b[i] : -INFINITY, -INFINITY);
+                if (a.groups > 1) {
+#pragma unroll
+                    for (int i = 0; i < NL; i++) big = fmaxf(big, c[i] > -INFINITY ? fabsf(b[i]) : 0.f);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NL; i++) c[i] = x[i] > -INFINITY ? c[i] : -INFINITY;
             }
-            off += U * (1.f + max16(big));
-        } else {
 #pragma unroll
-            for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? key[i] : kLowest;
-        }
-        if (a.groups > 1) {
-            int32_t m1 = kLowest, m2 = kLowest;
+            for (int i = 0; i < NL; i++) key[i] = ordered(c[i]);
+            if (a.groups > 1) {
+                int32_t m1 = kNone, m2 = kNone;
 #pragma unroll
-            for (int i = 0; i < NL; i++) {
-                const int32_t low = m1 < key[i] ? m1 : key[i];
-                m2 = low > m2 ? low : m2;
-                m1 = key[i] > m1 ? key[i] : m1;
+                for (int i = 0; i < NL; i++) {
+                    const int32_t low = m1 < key[i] ? m1 : key[i];
+                    m2 = low > m2 ? low : m2;
+                    m1 = key[i] > m1 ? key[i] : m1;
+                }
+                float margin = 0.f, size = 0.f;
+                stays = stays_in(a.topk_groups, a.nexperts / a.groups / NL, m1, m2, kNone, margin, size);
+                close = margin <= 4.f * (off + U * (1.f + max16(big))) + 2.f * U * size;
             }
-            float margin = 0.f, size = 0.f;
-            stays = stays_in(a.topk_groups, a.nexperts / a.groups / NL, m1, m2, kLowest, margin, size);
-            close = margin <= 4.f * off + 2.f * U * size;
         }
     }
     if (a.bias == nullptr) {  // the logits' own order
 #pragma unroll
-        for (int i = 0; i < NL; i++) key[i] = x[i] > -INFINITY ? ordered(x[i]) : kLowest;
+        for (int i = 0; i < NL; i++) key[i] = ordered(x[i]);
     }
+    // kNone, also without its last bits, is below every finite value's key
 #pragma unroll
-    for (int i = 0; i < NL; i++) key[i] = stays && key[i] != kLowest ? (key[i] & ~kPlace) | (kPlace - i) : kLowest;
+    for (int i = 0; i < NL; i++) key[i] = stays ? (key[i] & ~kPlace) | (kPlace - i) : kNone;
     sort_down(key);
     uint32_t mine = UINT32_MAX;
     for (uint32_t k = 0; k < a.topk; k++) {
@@ -496,12 +500,12 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
         const uint32_t equal = uint32_t(__ballot(((key[0] ^ best) & ~kPlace) == 0) >> (threadIdx.x & 48)) & 0xFFFFu;
         const uint32_t from = uint32_t(__builtin_ctz(equal | 0x10000u));
         const uint32_t at = uint32_t(__shfl(int(first + kPlace - (key[0] & kPlace)), int((threadIdx.x & 48) + from)));
-        if (lane == k && best != kLowest) mine = at;
+        if (lane == k && best > kNone) mine = at;
         // bit selects: written as conditionals the compiler makes them indexed reads of the list
         const int32_t taken = lane == from ? -1 : 0;
 #pragma unroll
         for (int i = 0; i + 1 < NL; i++) key[i] = (key[i + 1] & taken) | (key[i] & ~taken);
-        key[NL - 1] = (kLowest & taken) | (key[NL - 1] & ~taken);
+        key[NL - 1] = (kNone & taken) | (key[NL - 1] & ~taken);
     }
     const T* logits = static_cast<const T*>(a.logits[r]) + local * a.nexperts;
     float logit = mine != UINT32_MAX ? fminf(Elem<DT>::get(logits[mine]), kBiggest) : -INFINITY;
@@ -515,9 +519,9 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
             v += a.bias[mine];
         }
         const int32_t left = max16(key[0]);
-        const float after = dpp<0x101>(v), tail = left != kLowest ? unordered(left | kPlace) : -INFINITY;
+        const float after = dpp<0x101>(v), tail = left > kNone ? unordered(left | kPlace) : -INFINITY;
         const float next = lane + 1 < a.topk ? after : tail;
-        close = close || (lane < a.topk && next > -INFINITY && v - next <= 2.f * off + 2.f * U * fabsf(v));
+        close = close || (lane < a.topk && next > -INFINITY && v - next <= 2.f * off + 2.5f * U * fabsf(v));
     }
     for (uint64_t todo = __ballot(close); todo != 0;) {  // one of the wave's tokens at a time
         const uint32_t at = uint32_t(__builtin_ctzll(todo)) & 48;

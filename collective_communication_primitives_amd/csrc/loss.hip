@@ -84,14 +84,31 @@ struct RowOperand {
         return v;
     }
 };
+// The rows of d in two parts, the second one `part` bytes behind the first: its
+// steps follow after the first one's `steps`.
+struct PartsOperand : RowOperand<false> {
+    uint32_t steps;
+    uint64_t part;
+    __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
+        const bool second = step >= steps;
+        const uint32_t s = second ? step - steps : step;
+        return scalar_rsrc(p + (second ? part : 0) + s * kStepBytes, any && rows > 0 ? rows * pitch - s * kStepBytes : 0);
+    }
+    __device__ __forceinline__ uint32_t left(uint32_t step) const { return bytes - (step >= steps ? step - steps : step) * kStepBytes; }
+};
 // kCols: row k of `pitch` bytes holds the operand's m (or n) side by side.
-template <int KR>
+// PARTS 2: after the steps of all rows come those of a second part, `part` bytes
+// behind the first (0: the same rows again).
+template <int KR, int PARTS>
 struct ColOperand {
     const char* p;     // row 0 at the tile's first column
     uint32_t rows, pitch, skip;   // skip: bytes of a row before the tile
+    uint64_t part;
     __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
-        const uint32_t k = step * KR, n = any && k < rows ? rows - k : 0;
-        return scalar_rsrc(p + uint64_t(k) * pitch, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
+        const uint32_t steps = (rows + KR - 1) / KR;
+        const bool second = PARTS > 1 && step >= steps;
+        const uint32_t k = (second ? step - steps : step) * KR, n = any && k < rows ? rows - k : 0;
+        return scalar_rsrc(p + (second ? part : 0) + uint64_t(k) * pitch, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t) const { return UINT32_MAX; }
     __device__ __forceinline__ u32x4 cut(u32x4 v, uint32_t) const { return v; }
@@ -450,8 +467,18 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
 }
 
 // --------------------------------------------------------------- backward --
+// d in bf16 is rounded once more than the gradients themselves.  In a sum over
+// many tokens that is little beside the gradients' own rounding; where few tokens
+// make it, one of them may carry a whole row of a gradient, and half a step of d
+// shows in all of it.  So up to this many tokens d is kept in two parts, its
+// rounding and the rest's, and both enter the products, which are bound by the
+// weight's bytes there (error of 12 tokens' gradients against 64 bits: 3.1e-3
+// with one part, 1.7e-3, that of the result's rounding, with two).
+constexpr uint32_t kTwoPartTokens = 256;
+int d_parts(uint64_t tokens, int dtype) { return dtype == kBF16 && tokens <= kTwoPartTokens ? 2 : 1; }
+
 struct DPiece {
-    char* d;          // [tokens] rows of ldv elements: the piece's d, each part's padding zero
+    char* d;          // [parts][tokens] rows of ldv elements: the piece's d, each segment's padding zero
     float* acc;       // [splits][tokens][ldx]
     uint64_t ldv, ldx;
     uint32_t mt, nt;  // tiles of the launch
@@ -459,7 +486,7 @@ struct DPiece {
     int add;          // acc holds the earlier pieces' sum
 };
 
-template <int DT, typename S, bool TAIL>
+template <int DT, typename S, bool TAIL, int PARTS>
 __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     uint32_t mt, nt;
@@ -505,20 +532,30 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
         for (int i = 0; i < S::MI; i++) {
             const uint32_t m = mlane + i * 16;
             // a part's width is a multiple of 4: the four are all inside it or all behind it
-            if (m0 + m < padded) store_quad<DT>(d + uint64_t(n) * p.ldv + m, acc[i][j], use);
+            if (m0 + m >= padded) continue;
+            store_quad<DT>(d + uint64_t(n) * p.ldv + m, acc[i][j], use);
+            if constexpr (PARTS > 1) {
+                f32x4 rest;
+#pragma unroll
+                for (int e = 0; e < 4; e++) rest[e] = acc[i][j][e] - float(__bf16(acc[i][j][e]));
+                store_quad<DT>(d + (uint64_t(a.tokens) + n) * p.ldv + m, rest, use);
+            }
         }
     }
 }
 
 // The weight rows of a piece as the summed index: step by step through the
-// parts, each of whole steps, zeros behind a part's last row.
-template <int KR>
+// segments, each of whole steps, zeros behind a segment's last row.  PARTS 2: all
+// of them a second time.
+template <int KR, int PARTS>
 struct WeightOperand {
     const Segments& g;
-    uint32_t pitch, skip;
+    uint32_t pitch, skip, steps;
     mutable int sg;
     __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
-        const uint32_t k = step * KR;
+        const bool second = PARTS > 1 && step >= steps;
+        const uint32_t k = (second ? step - steps : step) * KR;
+        if (PARTS > 1 && k < g.col[sg]) sg = 0;
         while (sg + 1 < g.n && k >= g.col[sg + 1]) sg++;
         const uint32_t row = k - g.col[sg], n = any && row < g.count[sg] ? g.count[sg] - row : 0;
         return scalar_rsrc(g.weight[sg] + uint64_t(row) * pitch + skip, n > 0 ? (n < KR ? n : KR) * pitch - skip : 0);
@@ -528,7 +565,7 @@ struct WeightOperand {
 };
 
 // acc[split][t][h] (+)= sum over the split's part of the piece of d[t][v] weight[v][h].
-template <int DT, typename S>
+template <int DT, typename S, int PARTS>
 __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     constexpr int KR = kStepBytes / int(sizeof(T));
@@ -537,12 +574,14 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
     const uint32_t m0 = mt * S::BM, n0 = nt * S::BN;
     const uint32_t pitch = uint32_t(p.ldv * sizeof(T)), steps = pitch / kStepBytes;
     // the first `more` splits take one step more than the others
-    const uint32_t each = __builtin_amdgcn_readfirstlane(steps / p.splits), more = steps - each * p.splits, y = blockIdx.y;
+    const uint32_t all = steps * PARTS, y = blockIdx.y;
+    const uint32_t each = __builtin_amdgcn_readfirstlane(all / p.splits), more = all - each * p.splits;
     const uint32_t lo = y * each + (y < more ? y : more), hi = lo + each + (y < more ? 1 : 0);
     f32x4 acc[S::MI][S::NI];
-    const WeightOperand<KR> A{g, a.wpitch, m0 * uint32_t(sizeof(T)), 0};
+    const WeightOperand<KR, PARTS> A{g, a.wpitch, m0 * uint32_t(sizeof(T)), steps, 0};
     const RowOperand<false> B{p.d + uint64_t(n0) * pitch, a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN, pitch, pitch, pitch};
-    matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
+    if constexpr (PARTS > 1) matrix_tile<DT, S, kCols, kRows>(A, PartsOperand{B, steps, uint64_t(a.tokens) * pitch}, lo, hi, acc);
+    else matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* to = p.acc + uint64_t(blockIdx.y) * a.tokens * p.ldx;
 #pragma unroll
@@ -558,7 +597,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
 }
 
 // dweight[v][h] = sum_t d[t][v] hidden[t][h].
-template <int DT, typename S>
+template <int DT, typename S, int PARTS>
 __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segments g, DPiece p) {
     typedef typename Elem<DT>::type T;
     constexpr int KR = kStepBytes / int(sizeof(T));
@@ -569,9 +608,9 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
     f32x4 acc[S::MI][S::NI];
     constexpr uint32_t es = sizeof(T);
     const uint32_t skip = (g.col[sg] + n0) * es;
-    const ColOperand<KR> A{a.hidden + m0 * es, a.tokens, a.hpitch, m0 * es};
-    const ColOperand<KR> B{p.d + skip, a.tokens, uint32_t(p.ldv * es), skip};
-    matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR, acc);
+    const ColOperand<KR, PARTS> A{a.hidden + m0 * es, a.tokens, a.hpitch, m0 * es, 0};
+    const ColOperand<KR, PARTS> B{p.d + skip, a.tokens, uint32_t(p.ldv * es), skip, a.tokens * p.ldv * es};
+    matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR * PARTS, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     T* out = reinterpret_cast<T*>(g.dweight[sg]);
     const bool quads = a.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
@@ -817,6 +856,17 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// launch(Shape, parts of d)
+template <int DT, typename F>
+void with_parts(Tile t, uint64_t tokens, F&& launch) {
+    with_tile<DT>(t, [&](auto shape) {
+        if constexpr (DT == kBF16) {
+            if (d_parts(tokens, DT) == 2) return launch(shape, std::integral_constant<int, 2>());
+        }
+        launch(shape, std::integral_constant<int, 1>());
+    });
+}
+
 // Few tiles of dhidden: the sum over the piece is cut among workgroups, each
 // with at least 4 steps of it.
 uint32_t splits_of(uint64_t tokens, uint64_t cols, uint64_t ldv, int dtype) {
@@ -840,7 +890,7 @@ BackwardParts backward_parts(int nranks, uint64_t tokens, uint64_t cols, uint64_
     b.ldx = up(cols, 4);
     b.splits = splits_of(tokens, cols, b.ldv, dtype);
     Parts w;
-    b.d = w.take(tokens * b.ldv * esize(dtype));
+    b.d = w.take(d_parts(tokens, dtype) * tokens * b.ldv * esize(dtype));
     b.acc = w.take(b.splits * tokens * b.ldx * 4);
     b.pad = pad_parts(w, tokens, cols, piece, dtype);
     b.bytes = w.at;
@@ -868,25 +918,27 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
             const Tile t = pick_tile(DT, count, a.tokens);
             set_tiles(g, kTileM[t], true);
             with_rows_of<DT>(t, q.wpitch, [&](auto shape, auto tail) {
-                typedef decltype(shape) S;
-                constexpr bool TAIL = decltype(tail)::value;
-                p.nt = ceil_div(a.tokens, S::BN);
-                hipLaunchKernelGGL((k_loss_d<DT, S, TAIL>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
+                with_parts<DT>(t, a.tokens, [&](auto, auto parts) {
+                    typedef decltype(shape) S;
+                    constexpr bool TAIL = decltype(tail)::value;
+                    p.nt = ceil_div(a.tokens, S::BN);
+                    hipLaunchKernelGGL((k_loss_d<DT, S, TAIL, decltype(parts)::value>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
+                });
             });
-            with_tile<DT>(pick_tile(DT, a.cols, a.tokens, p.splits), [&](auto shape) {
+            with_parts<DT>(pick_tile(DT, a.cols, a.tokens, p.splits), a.tokens, [&](auto shape, auto parts) {
                 typedef decltype(shape) S;
                 p.mt = ceil_div(a.cols, S::BM);
                 p.nt = ceil_div(a.tokens, S::BN);
-                hipLaunchKernelGGL((k_loss_dhidden<DT, S>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, q, g, p);
+                hipLaunchKernelGGL((k_loss_dhidden<DT, S, decltype(parts)::value>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, q, g, p);
             });
             p.add = 1;
         }
         const Tile t = pick_tile(DT, a.cols, count);
         set_tiles(g, kTileN[t], false);
-        with_tile<DT>(t, [&](auto shape) {
+        with_parts<DT>(t, a.tokens, [&](auto shape, auto parts) {
             typedef decltype(shape) S;
             p.mt = ceil_div(a.cols, S::BM);
-            hipLaunchKernelGGL((k_loss_dweight<DT, S>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
+            hipLaunchKernelGGL((k_loss_dweight<DT, S, decltype(parts)::value>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
         });
     }
     if (a.tokens > 0) {

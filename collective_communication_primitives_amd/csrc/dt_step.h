@@ -132,9 +132,9 @@ struct LossArgs {
     char* workspace;
     int nranks;
 };
-constexpr uint32_t kLossPiece = 16384;      // vocabulary rows per piece, unless the caller says otherwise
+constexpr uint32_t kLossPiece = 16384;      // vocabulary rows per piece at least, unless the caller says otherwise
 constexpr uint32_t kMaxLossPiece = 1 << 20; // 256 rows of d stay within the 31 bits of a buffer resource's offsets
-uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t asked);
+uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype, uint64_t asked);
 uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype);
 uint64_t loss_backward_workspace(int nranks, uint64_t tokens, uint64_t cols, uint32_t piece, int dtype);
 hipError_t launch_loss(const LossArgs& a, int dtype, hipStream_t s);

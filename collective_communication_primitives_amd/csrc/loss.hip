@@ -474,7 +474,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
 // rounding and the rest's, and both enter the products, which are bound by the
 // weight's bytes there (error of 12 tokens' gradients against 64 bits: 3.1e-3
 // with one part, 1.7e-3, that of the result's rounding, with two).
-constexpr uint32_t kTwoPartTokens = 256;
+constexpr uint32_t kTwoPartTokens = 512;
 int d_parts(uint64_t tokens, int dtype) { return dtype == kBF16 && tokens <= kTwoPartTokens ? 2 : 1; }
 
 struct DPiece {
@@ -641,13 +641,20 @@ template <int DT>
 __global__ __launch_bounds__(kThreads) void k_loss_out(DHiddenOut o, const float* acc, uint32_t tokens, uint32_t cols,
                                                       uint64_t ldx, uint32_t splits) {
     typedef typename Elem<DT>::type T;
-    const uint32_t n = blockIdx.x;
-    for (uint32_t c = threadIdx.x; c < cols; c += kThreads) {
-        float s = 0.f;
-        for (uint32_t k = 0; k < splits; k++) s += acc[(uint64_t(k) * tokens + n) * ldx + c];
-        const T v = Elem<DT>::put(s);
-        for (int r = 0; r < o.nranks; r++) static_cast<T*>(o.p[r])[uint64_t(n) * cols + c] = v;
+    const uint32_t n = blockIdx.x, c = blockIdx.y * kThreads + threadIdx.x;
+    if (c >= cols) return;
+    const float* from = acc + uint64_t(n) * ldx + c;
+    const uint64_t next = uint64_t(tokens) * ldx;
+    float s = 0.f;
+    for (uint32_t k0 = 0; k0 < splits; k0 += 8) {
+        float v[8];  // eight splits' loads go out before the first is added
+#pragma unroll
+        for (int k = 0; k < 8; k++) v[k] = k0 + k < splits ? from[(k0 + k) * next] : 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; k++) s += v[k];
     }
+    const T v = Elem<DT>::put(s);
+    for (int r = 0; r < o.nranks; r++) static_cast<T*>(o.p[r])[uint64_t(n) * cols + c] = v;
 }
 
 // Rows of `cols` elements copied to rows of ld elements (a multiple of 16 bytes).
@@ -818,13 +825,13 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
     typedef typename Elem<DT>::type T;
     const uint32_t V = a.vocab.start[a.nranks];
     const bool direct = weight_direct(a, DT);
-    const uint32_t piece = direct ? stats_piece(V, a.tokens) : loss_piece(a.vocab, a.nranks, 0);
+    const uint32_t piece = direct ? stats_piece(V, a.tokens) : loss_piece(a.vocab, a.nranks, a.tokens, a.cols, DT, 0);
     Parts parts;
     StatsArgs q = {};
     q.part = reinterpret_cast<float2*>(a.workspace + parts.take(stats_entries(a.vocab, a.nranks) * a.tokens * sizeof(float2)));
     q.target = reinterpret_cast<float*>(a.workspace + parts.take(uint64_t(a.tokens) * 4));
     LossProblem p = problem_of(a);
-    const PadParts pad = pad_parts(parts, a.tokens, a.cols, loss_piece(a.vocab, a.nranks, 0), DT);
+    const PadParts pad = pad_parts(parts, a.tokens, a.cols, loss_piece(a.vocab, a.nranks, a.tokens, a.cols, DT, 0), DT);
     char* wpad = place_rows<T>(a, DT, pad, p, s);
     const Tile t = pick_tile(DT, piece, a.tokens);
     for (int pass = 0; pass < 2; pass++) {  // count the tiles, then launch
@@ -945,7 +952,7 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
         DHiddenOut o = {};
         for (int r = 0; r < a.nranks; r++) o.p[r] = a.dhidden[r];
         o.nranks = a.nranks;
-        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens), dim3(kThreads), 0, s, o, static_cast<const float*>(p.acc), a.tokens,
+        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens, ceil_div(a.cols, kThreads)), dim3(kThreads), 0, s, o, static_cast<const float*>(p.acc), a.tokens,
                            a.cols, p.ldx, p.splits);
     }
     return hipGetLastError();
@@ -957,12 +964,21 @@ uint64_t loss_workspace(const RowTable& vocab, int nranks, uint64_t tokens, uint
     Parts w;
     w.take(stats_entries(vocab, nranks) * tokens * sizeof(float2));
     w.take(tokens * 4);
-    pad_parts(w, tokens, cols, loss_piece(vocab, nranks, 0), dtype);
+    pad_parts(w, tokens, cols, loss_piece(vocab, nranks, tokens, cols, dtype, 0), dtype);
     return w.at;
 }
 
-uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t asked) {
-    uint64_t want = asked > 0 ? asked : kLossPiece;
+// A piece's weight rows are read three times and its d four times.  kLossPiece
+// rows, or more where those rows and their d stay below 64 MiB, and so in the
+// 256 MiB of cache in front of the memory: fewer launches (2 tokens x 129 fp32,
+// 60174 rows: 191 us with four pieces, 131 with one).
+uint32_t loss_piece(const RowTable& vocab, int nranks, uint64_t tokens, uint64_t cols, int dtype, uint64_t asked) {
+    constexpr uint64_t cached = 64 << 20;
+    uint64_t want = asked;
+    if (want == 0) {
+        want = cached / ((cols + d_parts(tokens, dtype) * tokens) * esize(dtype)) / 64 * 64;
+        if (want < kLossPiece) want = kLossPiece;
+    }
     const uint64_t all = vocab.start[nranks];
     if (want > kMaxLossPiece) want = kMaxLossPiece;
     return uint32_t(want < all ? want : all);

@@ -546,7 +546,7 @@ size_t dt_vocab_loss_backward_workspace(int nranks, const size_t* vocab_rows, si
     RowTable t;
     dt::report_error(DT_OK, "");
     if (loss_shape(nranks, vocab_rows, tokens, cols, dtype, "vocab_loss_backward_workspace", t) != DT_OK) return 0;
-    const uint32_t piece = dt::loss_piece(t, nranks, piece_rows);
+    const uint32_t piece = dt::loss_piece(t, nranks, tokens, cols, dtype, piece_rows);
     return dt::loss_backward_workspace(nranks, tokens, cols, piece, dtype);
 }
 
@@ -559,7 +559,7 @@ dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* w
     dt::LossArgs a = {};
     TRY(loss_shape(nranks, vocab_rows, tokens, cols, dtype, "vocab_loss_backward", a.vocab));
     const size_t es = esize_of(dtype);
-    a.piece = dt::loss_piece(a.vocab, nranks, piece_rows);
+    a.piece = dt::loss_piece(a.vocab, nranks, tokens, cols, dtype, piece_rows);
     const size_t need = dt::loss_backward_workspace(nranks, tokens, cols, a.piece, dtype);
     TRY(check_workspace(workspace, workspace_bytes, need, "vocab_loss_backward"));
     Ranges g;

@@ -19,6 +19,14 @@
 // weight in the logits; d in dhidden) or with m or n contiguous (kCols:
 // weight in dhidden, hidden and d in dweight).  The second kind is turned on
 // the way from LDS to the registers, so nothing is stored transposed.
+//
+// 4096 tokens x 4096, 131072 rows in bf16: the forward pass takes 3.4 ms, 1.29
+// PFLOP/s, with gradients 14.2 ms: 1.24 PFLOP/s over its four products (the logits
+// twice), where a plain matrix product of that size reaches 1.46.  The matrix
+// units are busy for 68% of the time, at a clock of 1.8 GHz: bound by them and by
+// power.  In fp32 (154 TFLOP/s in a large product) 509 tokens x 1000, 10007 rows
+// take 368 us with gradients, 110 TFLOP/s, the matrix units of a running workgroup
+// 83% busy.
 #include "dt_step_device.h"
 
 namespace dt {

@@ -189,3 +189,22 @@ def test_an_infinite_weight_stays_in_its_row(dt, dtype, cols):
     ref.assert_close(mine[keep], want["dweight"][0][0], want["dweight"][1][0], "dweight[0]")
     ref.assert_close(dw[1].t.view(90, cols), want["dweight"][0][1], want["dweight"][1][1], "dweight[1]")
     assert bool((mine[gone] == 0).all())
+
+
+@pytest.mark.parametrize("tokens", [1, 12, 65, 300, 512])
+def test_few_tokens_lose_nothing_to_the_rounded_gradient(dt, tokens):
+    """bf16, few tokens: the gradients are off by their own rounding and, relative to the terms' magnitudes, by 2^-16 (the
+    logits' gradient in two bf16 parts), 350 * 2^-24 (logits of 256 terms of up to 16 in all, in fp32) and the sums' 40 *
+    2^-24: under 2^-14 together.  One bf16 part would add 2^-8."""
+    note(f"loss in two parts, {tokens} tokens")
+    h, w, t, g = _make(tokens, 256, [300, 213], torch.bfloat16, 15, replicas=False)
+    _, _, dh, dw = _run(dt, h, w, t, g)
+    x, v = h[0].double(), torch.cat(w).double()
+    use = (t[0] >= 0).double()[:, None] * g[0].double()[:, None]
+    p = (x @ v.t()).softmax(1)
+    hot = torch.zeros_like(p).scatter_(1, t[0].clamp(min=0)[:, None], 1.0)
+    d, size = (p - hot) * use, (p + hot) * use.abs()
+    for q in range(2):
+        ref.assert_close(dh[q].t.view(-1, 256), d @ v, 2.0 ** -14 * (size @ v.abs()), f"dhidden[{q}]")
+    got = torch.cat([s.t.view(-1, 256) for s in dw])
+    ref.assert_close(got, d.t() @ x, 2.0 ** -14 * (size.t() @ x.abs()), "dweight")

@@ -644,25 +644,36 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
 struct DHiddenOut {
     void* p[kMaxRanksHost];
     int nranks;
+    int quads;   // rows are whole fours, aligned to them
 };
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_loss_out(DHiddenOut o, const float* acc, uint32_t tokens, uint32_t cols,
                                                       uint64_t ldx, uint32_t splits) {
     typedef typename Elem<DT>::type T;
-    const uint32_t n = blockIdx.x, c = blockIdx.y * kThreads + threadIdx.x;
+    const uint32_t n = blockIdx.x, c = (blockIdx.y * kThreads + threadIdx.x) * 4;
     if (c >= cols) return;
-    const float* from = acc + uint64_t(n) * ldx + c;
+    const float* from = acc + uint64_t(n) * ldx + c;  // ldx is a multiple of 4
     const uint64_t next = uint64_t(tokens) * ldx;
-    float s = 0.f;
-    for (uint32_t k0 = 0; k0 < splits; k0 += 8) {
-        float v[8];  // eight splits' loads go out before the first is added
+    f32x4 s = *reinterpret_cast<const f32x4*>(from);
+    for (uint32_t k0 = 1; k0 < splits; k0 += 8) {
+        f32x4 v[8];  // eight splits' loads go out before the first is added
 #pragma unroll
-        for (int k = 0; k < 8; k++) v[k] = k0 + k < splits ? from[(k0 + k) * next] : 0.f;
+        for (int k = 0; k < 8; k++)
+            if (k0 + k < splits) v[k] = *reinterpret_cast<const f32x4*>(from + (k0 + k) * next);
 #pragma unroll
-        for (int k = 0; k < 8; k++) s += v[k];
+        for (int k = 0; k < 8; k++)
+            if (k0 + k < splits) s += v[k];
     }
-    const T v = Elem<DT>::put(s);
-    for (int r = 0; r < o.nranks; r++) static_cast<T*>(o.p[r])[uint64_t(n) * cols + c] = v;
+    for (int r = 0; r < o.nranks; r++) {
+        T* to = static_cast<T*>(o.p[r]) + uint64_t(n) * cols + c;
+        if (o.quads) {
+            store_quad<DT>(to, s, true);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (c + e < cols) to[e] = Elem<DT>::put(s[e]);
+        }
+    }
 }
 
 // Rows of `cols` elements copied to rows of ld elements (a multiple of 16 bytes).
@@ -967,9 +978,13 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     }
     if (a.tokens > 0) {
         DHiddenOut o = {};
-        for (int r = 0; r < a.nranks; r++) o.p[r] = a.dhidden[r];
+        o.quads = a.cols % 4 == 0;
+        for (int r = 0; r < a.nranks; r++) {
+            o.p[r] = a.dhidden[r];
+            if (reinterpret_cast<uintptr_t>(o.p[r]) % (4 * sizeof(T)) != 0) o.quads = 0;
+        }
         o.nranks = a.nranks;
-        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens, ceil_div(a.cols, kThreads)), dim3(kThreads), 0, s, o, static_cast<const float*>(p.acc), a.tokens,
+        hipLaunchKernelGGL(k_loss_out<DT>, dim3(a.tokens, ceil_div(a.cols, kThreads * 4)), dim3(kThreads), 0, s, o, static_cast<const float*>(p.acc), a.tokens,
                            a.cols, p.ldx, p.splits);
     }
     return hipGetLastError();

@@ -466,7 +466,8 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
     }
 #pragma unroll
     for (int m = 1; m < 64; m <<= 1) join(top, s, __shfl_xor(top, m), __shfl_xor(s, m));
-    const float lse = top + logf(s);
+    // the first lane's for every rank: a join rounds differently with its sides swapped
+    const float lse = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top + logf(s))));
     const float loss = counted(a, a.targets[n]) ? lse - q.target[n] : 0.f;
     if (lane < uint32_t(o.nranks)) {
         o.lse[lane][n] = lse;

@@ -208,3 +208,38 @@ def test_few_tokens_lose_nothing_to_the_rounded_gradient(dt, tokens):
         ref.assert_close(dh[q].t.view(-1, 256), d @ v, 2.0 ** -14 * (size @ v.abs()), f"dhidden[{q}]")
     got = torch.cat([s.t.view(-1, 256) for s in dw])
     ref.assert_close(got, d.t() @ x, 2.0 ** -14 * (size.t() @ x.abs()), "dweight")
+
+
+def test_odd_rows_copied_in_several_pieces(dt):
+    """bf16 rows of odd width are copied piece by piece; these need three pieces, which cut the shards."""
+    note("loss, odd bf16 rows in three pieces")
+    _check(dt, *_make(2000, 33, [25000, 0, 15001], torch.bfloat16, 16, replicas=False))
+
+
+def test_as_many_tokens_as_the_call_takes(dt):
+    """2^22 tokens: the forward pass needs more than one launch for 20000 rows.  Sampled tokens against the definition; a
+    logit of 8 terms and the sum of 20000 exponentials in fp32."""
+    note("loss of 2^22 tokens")
+    tokens, cols, shards = 1 << 22, 8, [9000, 11000]
+    g = torch.Generator(device="cuda").manual_seed(17)
+    h = torch.randn(tokens, cols, generator=g, device="cuda").bfloat16()
+    w = [(torch.randn(n, cols, generator=g, device="cuda") / 2).bfloat16() for n in shards]
+    t = torch.randint(0, sum(shards), (tokens,), generator=g, device="cuda")
+    loss, lse = [[torch.empty(tokens, device="cuda") for _ in range(2)] for _ in range(2)]
+    dt.dt_vocab_loss([h] * 2, w, [t] * 2, loss, lse)
+    at = torch.cat([torch.arange(300, device="cuda"), torch.randint(0, tokens, (2000,), generator=g, device="cuda"),
+                    torch.arange(tokens - 300, tokens, device="cuda")])
+    want = ref.loss(h[at], w, t[at], None)
+    for q in range(2):
+        ref.assert_close(lse[q][at], *want["lse"], f"lse[{q}]")
+        ref.assert_close(loss[q][at], *want["loss"], f"loss[{q}]")
+    assert torch.equal(lse[0], lse[1]) and bool(lse[0].isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_every_rank_gets_the_same_bits(dt, dtype):
+    note(f"loss, sixteen ranks' bits {dtype}")
+    h, w, t, g = _make(600, 64, [300] * 16, dtype, 18, replicas=False)
+    loss, lse, dh, _ = _run(dt, h, w, t, g)
+    for outs in (loss, lse, dh):
+        assert all(torch.equal(o.t, outs[0].t) for o in outs)

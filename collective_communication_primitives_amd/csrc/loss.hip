@@ -476,24 +476,54 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
 }
 
 // --------------------------------------------------------------- backward --
-// d in bf16 is rounded once more than the gradients themselves.  In a sum over
-// many tokens that is little beside the gradients' own rounding; where few tokens
-// make it, one of them may carry a whole row of a gradient, and half a step of d
-// shows in all of it.  So up to this many tokens d is kept in two parts, its
-// rounding and the rest's, and both enter the products, which are bound by the
-// weight's bytes there (error of 12 tokens' gradients against 64 bits: 3.1e-3
-// with one part, 1.7e-3, that of the result's rounding, with two).
+// d in bf16 is rounded once more than the gradients themselves.  Two things keep
+// that small beside their own rounding:
+//  - Where few tokens make a sum, one of them may carry a whole row of a gradient,
+//    and half a step of d shows in all of it.  So up to kTwoPartTokens d is kept in
+//    two parts, its rounding and the rest's, and both enter the products, which are
+//    bound by the weight's bytes there (error of 12 tokens' gradients against 64
+//    bits: 3.1e-3 with one part, 1.7e-3, that of the result's rounding, with two).
+//  - Above it d is kept relative to the largest |dloss|, which the products are
+//    multiplied with in fp32.  A mean's gradient is the same for every token, and
+//    so was its rounding, all in one direction (3481 tokens: 2.8e-3); relative to
+//    the largest it is 1.
 constexpr uint32_t kTwoPartTokens = 512;
 int d_parts(uint64_t tokens, int dtype) { return dtype == kBF16 && tokens <= kTwoPartTokens ? 2 : 1; }
+
+// The largest finite |dloss| of the tokens that count, in kScaleParts shares.
+constexpr int kScaleParts = 64;
+__global__ __launch_bounds__(kThreads) void k_loss_scale(LossProblem a, float* scale) {
+    __shared__ float tmp[kThreads / 64];
+    float top = 0.f;
+    for (uint32_t n = blockIdx.x * kThreads + threadIdx.x; n < a.tokens; n += kScaleParts * kThreads) {
+        const float f = fabsf(a.dloss[n]);
+        if (counted(a, a.targets[n]) && f < INFINITY) top = fmaxf(top, f);
+    }
+    top = wave_max(top);
+    if ((threadIdx.x & 63) == 0) tmp[threadIdx.x >> 6] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kThreads / 64; w++) top = fmaxf(top, tmp[w]);
+        scale[blockIdx.x] = top;
+    }
+}
 
 struct DPiece {
     char* d;          // [parts][tokens] rows of ldv elements: the piece's d, each segment's padding zero
     float* acc;       // [splits][tokens][ldx]
+    const float* scale;  // [kScaleParts], NULL: 1
     uint64_t ldv, ldx;
     uint32_t mt, nt;  // tiles of the launch
     uint32_t splits;  // workgroups that share one tile's sum over the piece
     int add;          // acc holds the earlier pieces' sum
 };
+
+// What d is relative to (the whole wave asks; the same value in every lane).
+__device__ __forceinline__ float scale_of(const DPiece& p) {
+    if (p.scale == nullptr) return 1.f;
+    const float top = wave_max(p.scale[threadIdx.x & 63]);
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top > 0.f ? top : 1.f)));
+}
 
 template <int DT, typename S, bool TAIL, int PARTS>
 __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g, DPiece p) {
@@ -512,6 +542,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const uint32_t mlane = (wave % S::GM) * S::WM + (lane >> 4) * 4;
     T* d = reinterpret_cast<T*>(p.d) + g.col[sg] + m0;
+    const float scale = scale_of(p);
 #pragma unroll
     for (int j = 0; j < S::NI; j++) {
         const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
@@ -519,7 +550,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
         const int64_t t = a.targets[n];
         const float lse = a.lse[n];
         const bool use = counted(a, t);
-        const float f = use ? a.dloss[n] : 0.f;
+        const float f = use ? a.dloss[n] / scale : 0.f;
         // d = p f; the target's row and the rows behind the shard's last one are mended below
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
@@ -593,6 +624,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
     else matrix_tile<DT, S, kCols, kRows>(A, B, lo, hi, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float* to = p.acc + uint64_t(blockIdx.y) * a.tokens * p.ldx;
+    const float scale = scale_of(p);
 #pragma unroll
     for (int j = 0; j < S::NI; j++)
 #pragma unroll
@@ -601,7 +633,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dhidden(LossProblem a, Segm
             const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
             if (n >= a.tokens || m >= p.ldx) continue;
             f32x4* o = reinterpret_cast<f32x4*>(to + uint64_t(n) * p.ldx + m);
-            *o = p.add ? *o + acc[i][j] : acc[i][j];
+            *o = p.add ? *o + acc[i][j] * scale : acc[i][j] * scale;
         }
 }
 
@@ -622,6 +654,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
     matrix_tile<DT, S, kCols, kCols>(A, B, 0, (a.tokens + KR - 1) / KR * PARTS, acc);
     const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     T* out = reinterpret_cast<T*>(g.dweight[sg]);
+    const float scale = scale_of(p);
     const bool quads = a.cols % 4 == 0 && reinterpret_cast<uintptr_t>(out) % (4 * sizeof(T)) == 0;
 #pragma unroll
     for (int j = 0; j < S::NI; j++)
@@ -632,11 +665,11 @@ __global__ __launch_bounds__(S::threads) void k_loss_dweight(LossProblem a, Segm
             if (n >= g.count[sg] || m >= a.cols) continue;
             T* to = out + uint64_t(n) * a.cols + m;
             if (quads) {
-                store_quad<DT>(to, acc[i][j], true);
+                store_quad<DT>(to, acc[i][j] * scale, true);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; e++)
-                    if (m + e < a.cols) to[e] = Elem<DT>::put(acc[i][j][e]);
+                    if (m + e < a.cols) to[e] = Elem<DT>::put(acc[i][j][e] * scale);
             }
         }
 }
@@ -914,7 +947,7 @@ uint32_t splits_of(uint64_t tokens, uint64_t cols, uint64_t ldv, int dtype) {
     return want < 1 ? 1 : want > 32 ? 32 : uint32_t(want);
 }
 struct BackwardParts {
-    uint64_t ldv, ldx, d, acc;
+    uint64_t ldv, ldx, d, acc, scale;
     uint32_t splits;
     PadParts pad;
     uint64_t bytes;
@@ -928,6 +961,7 @@ BackwardParts backward_parts(int nranks, uint64_t tokens, uint64_t cols, uint64_
     Parts w;
     b.d = w.take(d_parts(tokens, dtype) * tokens * b.ldv * esize(dtype));
     b.acc = w.take(b.splits * tokens * b.ldx * 4);
+    b.scale = w.take(kScaleParts * sizeof(float));
     b.pad = pad_parts(w, tokens, cols, piece, dtype);
     b.bytes = w.at;
     return b;
@@ -945,6 +979,11 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     p.acc = reinterpret_cast<float*>(a.workspace + b.acc);
     p.ldx = b.ldx;
     p.splits = b.splits;
+    if (DT == kBF16 && a.tokens > kTwoPartTokens) {
+        float* scale = reinterpret_cast<float*>(a.workspace + b.scale);
+        hipLaunchKernelGGL(k_loss_scale, dim3(kScaleParts), dim3(kThreads), 0, s, q, scale);
+        p.scale = scale;
+    }
     for (uint32_t first = 0; first < V; first += a.piece) {
         const uint32_t count = V - first < a.piece ? V - first : a.piece;
         Segments g = segments_of(a, DT, first, count, wpad, q.wpitch);

@@ -243,3 +243,39 @@ def test_every_rank_gets_the_same_bits(dt, dtype):
     loss, lse, dh, _ = _run(dt, h, w, t, g)
     for outs in (loss, lse, dh):
         assert all(torch.equal(o.t, outs[0].t) for o in outs)
+
+
+@pytest.mark.parametrize("dloss", ["mean", "one large", "infinite", "zero", "masked NaN"])
+def test_gradients_of_the_loss_scaled(dt, dloss):
+    """More tokens than are kept in two parts: the logits' gradient is relative to the largest finite dloss."""
+    note(f"loss, dloss {dloss}")
+    tokens = 700
+    h, w, t, g = _make(tokens, 96, [180, 130], torch.bfloat16, 19, replicas=False)
+    if dloss == "mean":
+        g[0].fill_(1.0 / tokens)
+    elif dloss == "one large":
+        g[0][5] = 3e30
+    elif dloss == "zero":
+        g[0].zero_()
+    if dloss in ("mean", "one large", "zero"):
+        _check(dt, h, w, t, g)
+    if dloss == "mean":
+        # the rounding of 1 / tokens itself must not be in the result: its half step would shift the whole norm by up to
+        # 2^-9, the results' and the other terms' roundings are independent of it and leave its average near 0
+        _, _, dh, _ = _run(dt, h, w, t, g)
+        want = ref.loss(h[0], w, t[0], g[0])["dhidden"][0].cuda()
+        got = dh[0].t.view(tokens, 96).double()
+        assert abs(float((got * want).sum() / want.square().sum()) - 1) < 2.0 ** -12
+    if dloss == "infinite":
+        g[0][5] = float("inf")
+        _, _, dh, _ = _run(dt, h, w, t, g)
+        ok = dh[0].t.view(tokens, 96).isfinite().all(1)
+        assert int((~ok).sum()) == 1 and not bool(ok[5])
+    if dloss == "masked NaN":
+        t[0][7] = -100
+        g[0][7] = float("nan")
+        clean = g[0].clone()
+        clean[7] = 0
+        a, b = _run(dt, h, w, t, g), _run(dt, h, w, t, [clean] * 2)
+        for x, y in zip(a[2] + a[3], b[2] + b[3]):
+            assert torch.equal(x.t, y.t)

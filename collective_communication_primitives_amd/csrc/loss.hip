@@ -219,12 +219,14 @@ __device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t place, int
     }
 }
 
-// Waits until at most `loads` of this wave's loads are outstanding, then for
-// the workgroup's other waves.
-template <int loads>
+// Waits until at most `loads` of this wave's loads and `reads` of its LDS reads
+// (15: as many as the counter holds) are outstanding, then for the workgroup's
+// other waves.
+template <int loads, int reads>
 __device__ __forceinline__ void arrive() {
+    static_assert(loads < 64 && reads < 16, "the counters hold 6 and 4 bits");
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4 | 15 << 8);
+    __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4 | reads << 8);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -261,7 +263,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     load(lo, s0);
     load(lo + 1, s1);
     load(lo + 2, s2);
-    arrive<2 * S::loads>();
+    arrive<2 * S::loads, 15>();
     u32x4 fa[S::MI], fb[2][S::NI];
     uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
 #pragma unroll
@@ -270,12 +272,17 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     for (int j = 0; j < S::NI; j++) fb[0][j] = fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j);
     // Step `step`: its registers are loaded, and the next step's bytes are in
     // LDS once all waves are here.  The stage that is loaded into, the one
-    // before this step's, was read two turns ago and multiplied in the last
-    // one, so no wave has to wait for its LDS reads at the barrier.  A row of
-    // A's registers takes the next step's as soon as it is multiplied; behind
-    // the last step these are bytes that nothing uses.
+    // before this step's, was read two turns ago, so the last turn's reads may
+    // still be on their way at the barrier, but none before them: LDS answers in
+    // order, and a turn reads each fragment with one instruction at least (kCols:
+    // two, as none reads from more than two places).  Their use in the last turn
+    // does not see to that, since the compiler may move a matrix instruction, and
+    // its wait, behind the barrier.  A row of A's registers takes the next step's
+    // as soon as it is multiplied; behind the last step these are bytes that
+    // nothing uses.
+    constexpr int turn_reads = S::MI * (MA == kRows ? 1 : 2) + S::NI * (MB == kRows ? 1 : 2);
     auto turn = [&](uint32_t step, u32x4* free, const u32x4* following, const u32x4 (&now)[S::NI], u32x4 (&next)[S::NI]) {
-        arrive<S::loads>();
+        arrive<S::loads, turn_reads < 15 ? turn_reads : 15>();
         load(step + 3, free);
         // keeps the compiler from holding every fragment's address of every stage in a register
         asm volatile("" : "+v"(ra), "+v"(rb));
@@ -304,7 +311,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
         turn(step + 2, s1, s3, fb[0], fb[1]);
         turn(step + 3, s2, s0, fb[1], fb[0]);
     }
-    arrive<0>();  // nothing is on its way into LDS when the workgroup ends
+    arrive<0, 0>();  // nothing is on its way into LDS when the workgroup ends
 }
 
 // Tile `id` of mt x nt in an order that keeps an XCD's workgroups on

@@ -852,6 +852,8 @@ def _exchange(tok, rows, experts, nexperts: int):
         raise ValueError(f"{nexperts} experts do not divide by {p} ranks")
     sizes, _, slots, n = _row_counts(tok, cols, "the token tensors", k)
     held, _, _, cap = _row_counts(rows, cols, "the experts' buffers")
+    if len(rows) != p:
+        raise ValueError(f"the experts' buffers must list one tensor per rank ({p}), got {len(rows)}")
     return p, cols, k, sizes, slots, n, held, cap
 
 

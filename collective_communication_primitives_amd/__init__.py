@@ -20,14 +20,35 @@ from __future__ import annotations
 import atexit
 import ctypes
 import threading
+import types
 import weakref
 from typing import Dict, List, Optional, Sequence
 
 import torch
 
-from . import _lib, _marshal
+from . import _lib
 
 _L = _lib.load()
+
+
+def _load_marshal():
+    """The host helper of the model-step operators' binding, or a stand-in that
+    says why they cannot be called: the collectives do without it."""
+    try:
+        from . import _marshal as helper
+        if helper.torch_version == str(torch.__version__):
+            return helper
+        why = f"it was built for torch {helper.torch_version}, this is {torch.__version__}"
+    except ImportError as e:
+        why = str(e)
+
+    def missing(*_):
+        raise ImportError(f"the binding's helper _marshal is missing ({why}); run `python collective_communication_primitives_amd/build.py`")
+
+    return types.SimpleNamespace(buffers=missing, counts=missing)
+
+
+_marshal = _load_marshal()
 
 DT_FLOAT32, DT_BFLOAT16, DT_INT32 = 0, 1, 2
 DT_SUM, DT_MAX, DT_MIN, DT_AVG = 0, 1, 2, 3

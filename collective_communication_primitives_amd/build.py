@@ -7,7 +7,8 @@ stale build this script replaces.)
 
 Each source is compiled on its own (in parallel) into ``_build/`` at the
 repository root, then linked into ``libdtcoll.so`` next to this file.  Beside
-it ``_marshal.so``, the host helper of the Python binding (g++, no GPU code).
+it ``_marshal`` with the suffix of this Python's extensions, the host helper of
+the model-step operators' binding (g++, no GPU code).
 """
 from __future__ import annotations
 
@@ -24,7 +25,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libdtcoll.so")
-MARSHAL = os.path.join(PKG, "_marshal.so")
+MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ("api.cpp", "reduce.hip", "copy.hip", "barrier.hip", "scratch.hip", "step_api.cpp", "norm.hip", "moe.hip",
            "loss.hip")
 ARCH = os.environ.get("DT_OFFLOAD_ARCH", "gfx950")
@@ -56,7 +57,8 @@ def _compile_marshal() -> str:
     from torch.utils.cpp_extension import TORCH_LIB_PATH, include_paths
     paths = [flag for path in include_paths() for flag in ("-isystem", path)]
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", sysconfig.get_path("include"), *paths,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DDT_TORCH_VERSION="{torch.__version__}"',
+           "-I", sysconfig.get_path("include"), *paths,
            os.path.join(CSRC, "marshal.cpp"), "-L", TORCH_LIB_PATH, "-ltorch_python", "-o", MARSHAL + ".tmp"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
@@ -70,13 +72,13 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
         marshal = pool.submit(_compile_marshal)
         objs = list(pool.map(_compile, SOURCES))
-        marshal.result()
     tmp = LIBRARY + ".tmp"
     cmd = [_hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIBRARY)
+    marshal.result()  # the library is in place where the helper cannot be built
     if verbose:
         print(f"built {LIBRARY} and {MARSHAL}")
     return LIBRARY

@@ -42,6 +42,10 @@ __device__ __forceinline__ void wave_argmax(double& key, uint32_t& idx) {
     }
 }
 
+constexpr float kBiggest = 3.402823466e38f;
+// A logit or bias as it counts: NaN is -inf, +inf the largest finite value.
+__device__ __forceinline__ float in_range(float f) { return fminf(fmaxf(f, -INFINITY), kBiggest); }
+
 // One token per wave, scores in 64 bits: lane l holds experts l, l + 64, ...
 // For the shapes that four tokens to a wave do not take: more than 512
 // experts, more than 16 choices, groups that are not whole lanes.
@@ -63,7 +67,7 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
         const uint32_t e = lane + 64 * i;
         v[i] = e < a.nexperts ? Elem<DT>::get(x[e]) : -INFINITY;
         live[i] = v[i] > -INFINITY;  // false for NaN
-        v[i] = live[i] ? fminf(v[i], 3.402823466e38f) : -INFINITY;
+        v[i] = in_range(v[i]);
         if (live[i] && a.bias != nullptr) live[i] = a.bias[e] > -INFINITY;
         top = fmaxf(top, v[i]);
     }
@@ -88,7 +92,7 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
         c[i] = double(v[i]);
         if (scored && live[i]) {
             c[i] = a.sigmoid ? 1. / (1. + exp(-double(v[i]))) : exp(double(v[i]) - double(top)) / totald;
-            if (a.bias != nullptr) c[i] += double(a.bias[e]);
+            if (a.bias != nullptr) c[i] += double(in_range(a.bias[e]));
         }
     }
     if (a.groups > 1) {
@@ -184,8 +188,6 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     }
 }
 
-constexpr float kBiggest = 3.402823466e38f;
-
 // Floats as integers of the same order (no NaN, no -0), and back: integer
 // maxima are one instruction with the lane exchange in it.
 __device__ __forceinline__ int32_t ordered(float f) {
@@ -223,14 +225,14 @@ __device__ __forceinline__ void load_logits(const void* base, uint64_t row, uint
         for (int i = 0; i < NL; i++) x[i] = first + i < nexperts ? x[i] : -INFINITY;
     }
 #pragma unroll
-    for (int i = 0; i < NL; i++) x[i] = fminf(fmaxf(x[i], -INFINITY), kBiggest) + 0.f;  // NaN to -inf; + 0: no -0
+    for (int i = 0; i < NL; i++) x[i] = in_range(x[i]) + 0.f;  // + 0: no -0
 }
 
 // The lane's experts' biases.
 template <int NL>
 __device__ __forceinline__ void load_bias(const float* bias, uint32_t nexperts, uint32_t first, float (&b)[NL]) {
 #pragma unroll
-    for (int i = 0; i < NL; i++) b[i] = bias[first + i < nexperts ? first + i : nexperts - 1];
+    for (int i = 0; i < NL; i++) b[i] = in_range(bias[first + i < nexperts ? first + i : nexperts - 1]);
 }
 
 __device__ __forceinline__ int64_t ordered(double f) {
@@ -241,8 +243,9 @@ __device__ __forceinline__ double unordered(int64_t i) { return __longlong_as_do
 
 // The groups that stay: true in the lanes of one of them.  m1, m2: the lane's
 // two largest candidates as ordered integers, `none` where there is none; a
-// group is `width` neighbouring lanes, a power of two.  `margin`: how far the
-// last score that stays, of size `size`, is above the first that goes.
+// group is `width` neighbouring lanes, a power of two.  Scores are halved, so
+// that the sum of two stays in range.  `margin`: how far the last half score
+// that stays, of size `size`, is above the first that goes.
 __device__ __forceinline__ bool stays_in(uint32_t topk_groups, uint32_t width, int32_t m1, int32_t m2, int32_t none, float& margin,
                                          float& size) {
     const uint32_t lane = threadIdx.x & 15, group = lane / width;
@@ -257,7 +260,7 @@ __device__ __forceinline__ bool stays_in(uint32_t topk_groups, uint32_t width, i
         w *= 2;
     });
     // one expert left in a group: it alone; none: the group goes
-    const float score = m1 == none ? -INFINITY : m2 == none ? unordered(m1) : unordered(m1) + unordered(m2);
+    const float score = m1 == none ? -INFINITY : .5f * unordered(m1) + (m2 == none ? 0.f : .5f * unordered(m2));
     const int32_t key = score > -INFINITY ? ordered(score + 0.f) : none;
     uint32_t better = 0;
     rotations([&](auto c) {
@@ -285,7 +288,7 @@ __device__ __forceinline__ uint32_t choose_exactly(const RouteArgs& a, const typ
     for (int i = 0; i < NK; i++) {
         const uint32_t e = first + i < a.nexperts ? first + i : a.nexperts - 1;
         x[i] = Elem<DT>::get(logits[e]);
-        b[i] = a.bias != nullptr ? a.bias[e] : 0.f;
+        b[i] = a.bias != nullptr ? in_range(a.bias[e]) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < NK; i++) x[i] = first + i < a.nexperts && x[i] > -INFINITY ? fminf(x[i], kBiggest) + 0.f : -INFINITY;
@@ -482,7 +485,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
                 }
                 float margin = 0.f, size = 0.f;
                 stays = stays_in(a.topk_groups, a.nexperts / a.groups / NL, m1, m2, kNone, margin, size);
-                close = margin <= 4.f * (off + U * (1.f + max16(big))) + 2.f * U * size;
+                close = margin <= 2.f * (off + U * (1.f + max16(big))) + 2.f * U * size;
             }
         }
     }
@@ -517,7 +520,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
         if (a.bias != nullptr && mine != UINT32_MAX) {
             v = a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(logit * -kLog2e))
                           : __builtin_amdgcn_exp2f((logit - top) * kLog2e) * (1.f / sum);
-            v += a.bias[mine];
+            v += in_range(a.bias[mine]);
         }
         const int32_t left = max16(key[0]);
         const float after = dpp<0x101>(v), tail = left > kNone ? unordered(left | kPlace) : -INFINITY;

@@ -490,10 +490,11 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
 //    two parts, its rounding and the rest's, and both enter the products, which are
 //    bound by the weight's bytes there (error of 12 tokens' gradients against 64
 //    bits: 3.1e-3 with one part, 1.7e-3, that of the result's rounding, with two).
-//  - Above it d is kept relative to the largest |dloss|, which the products are
-//    multiplied with in fp32.  A mean's gradient is the same for every token, and
-//    so was its rounding, all in one direction (3481 tokens: 2.8e-3); relative to
-//    the largest it is 1.
+//  - Above it d is kept relative to the mantissa of the largest |dloss|, which the
+//    products are multiplied with in fp32.  A mean's gradient is the same for every
+//    token, and so was its rounding, all in one direction (3481 tokens: 2.8e-3);
+//    relative to that mantissa it is a power of two.  The exponent stays in d:
+//    divided by a dloss of 1e38, the other tokens' d would vanish.
 constexpr uint32_t kTwoPartTokens = 512;
 int d_parts(uint64_t tokens, int dtype) { return dtype == kBF16 && tokens <= kTwoPartTokens ? 2 : 1; }
 
@@ -525,11 +526,12 @@ struct DPiece {
     int add;          // acc holds the earlier pieces' sum
 };
 
-// What d is relative to (the whole wave asks; the same value in every lane).
+// What d is relative to, 1 or more and less than 2 (the whole wave asks; the same
+// value in every lane).
 __device__ __forceinline__ float scale_of(const DPiece& p) {
     if (p.scale == nullptr) return 1.f;
     const float top = wave_max(p.scale[threadIdx.x & 63]);
-    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top > 0.f ? top : 1.f)));
+    return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(top) & 0x7FFFFFu) | 0x3F800000u);
 }
 
 template <int DT, typename S, bool TAIL, int PARTS>

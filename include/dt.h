@@ -380,8 +380,9 @@ dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, co
  * [vocab_rows[r], cols] is rank r's own.  The logits are formed again, one
  * piece of at most piece_rows vocabulary rows at a time (0: the library's
  * choice; never more than 2^20); the workspace grows with the piece.  For bf16
- * tensors the logits' gradient, relative to the largest dloss, is rounded to
- * bf16 before it enters the two products (in two parts for few tokens). */
+ * tensors the logits' gradient, relative to the largest dloss' mantissa, is
+ * rounded to bf16 before it enters the two products (in two parts for few
+ * tokens). */
 size_t dt_vocab_loss_backward_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols,
                                         size_t piece_rows, dt_dtype dtype);
 dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* weight, const int64_t* const* targets,

@@ -726,6 +726,25 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(const T* src, T* dst, uin
     for (uint32_t c = threadIdx.x; c < ld; c += kThreads) dst[row * ld + c] = c < cols ? src[row * cols + c] : T(0);
 }
 
+// The backward pass' copy of hidden: rows at hpitch with zeros behind them, and
+// rows of zeros for the tokens that are left out.  Their d is zero, but zero times
+// what a padded row holds may be NaN.  VEC: the rows start and end on 16-byte
+// boundaries.  509 tokens of 1000 fp32: 4 us of 369.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_loss_hidden(LossProblem a, const T* src, char* dst) {
+    const uint64_t n = blockIdx.x;
+    const bool use = counted(a, a.targets[n]);
+    char* to = dst + n * a.hpitch;
+    if constexpr (VEC) {
+        const char* from = reinterpret_cast<const char*>(src) + n * a.hpitch;
+        for (uint32_t at = threadIdx.x * 16; at < a.hpitch; at += kThreads * 16)
+            *reinterpret_cast<u32x4*>(to + at) = use ? load16(from + at) : u32x4{0, 0, 0, 0};  // read again soon
+    } else {
+        for (uint32_t c = threadIdx.x; c < a.hpitch / sizeof(T); c += kThreads)
+            reinterpret_cast<T*>(to)[c] = use && c < a.cols ? src[n * a.cols + c] : T(0);
+    }
+}
+
 // -------------------------------------------------------------------- host --
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 uint32_t ceil_div(uint64_t n, uint64_t by) { return uint32_t((n + by - 1) / by); }
@@ -787,8 +806,8 @@ struct Parts {
     }
 };
 
-// hidden is read where it is if its rows start and end on 16-byte boundaries;
-// otherwise it is copied to such rows with zeros behind them (a small part of
+// The forward pass reads hidden where it is if its rows start and end on 16-byte
+// boundaries; otherwise, and in the backward pass, it is copied to such rows with zeros behind them (a small part of
 // the call's bytes unless the vocabulary is small too).  weight may lie on any
 // 4-byte boundaries; only bf16 rows of odd width are copied, a piece at a time.
 struct PadParts {
@@ -861,11 +880,19 @@ void pad_weight(const LossArgs& a, uint32_t first, uint32_t count, char* to, uin
 }
 
 // hidden's place and pitch, and weight's pitch; where weight has to be copied
-// piece by piece, the place for it.
+// piece by piece, the place for it.  leave_out: hidden is copied in any case,
+// without the rows of the tokens that are left out.
 template <typename T>
-char* place_rows(const LossArgs& a, int dtype, const PadParts& pad, LossProblem& p, hipStream_t s) {
+char* place_rows(const LossArgs& a, int dtype, const PadParts& pad, LossProblem& p, bool leave_out, hipStream_t s) {
     p.hpitch = uint32_t(pad.pitch);
-    if (!hidden_direct(a, dtype)) {
+    const bool vec = hidden_direct(a, dtype);
+    if (leave_out && a.tokens > 0) {
+        char* to = a.workspace + pad.hidden;
+        const T* from = static_cast<const T*>(a.hidden);
+        if (vec) hipLaunchKernelGGL((k_loss_hidden<T, true>), dim3(a.tokens), dim3(kThreads), 0, s, p, from, to);
+        else hipLaunchKernelGGL((k_loss_hidden<T, false>), dim3(a.tokens), dim3(kThreads), 0, s, p, from, to);
+        p.hidden = to;
+    } else if (!vec) {
         pad_rows<T>(a.hidden, a.workspace + pad.hidden, a.tokens, a.cols, pad.pitch, s);
         p.hidden = a.workspace + pad.hidden;
     }
@@ -903,7 +930,7 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
     q.target = reinterpret_cast<float*>(a.workspace + parts.take(uint64_t(a.tokens) * 4));
     LossProblem p = problem_of(a);
     const PadParts pad = pad_parts(parts, a.tokens, a.cols, loss_piece(a.vocab, a.nranks, a.tokens, a.cols, DT, 0), DT);
-    char* wpad = place_rows<T>(a, DT, pad, p, s);
+    char* wpad = place_rows<T>(a, DT, pad, p, false, s);
     const Tile t = pick_tile(DT, piece, a.tokens, DT == kF32);
     for (int pass = 0; pass < 2; pass++) {  // count the tiles, then launch
         q.entry = 0;
@@ -982,7 +1009,7 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     const uint32_t V = a.vocab.start[a.nranks];
     const BackwardParts b = backward_parts(a.nranks, a.tokens, a.cols, a.piece, DT);
     LossProblem q = problem_of(a);
-    char* wpad = place_rows<T>(a, DT, b.pad, q, s);
+    char* wpad = place_rows<T>(a, DT, b.pad, q, true, s);
     DPiece p = {};
     p.d = a.workspace + b.d;
     p.acc = reinterpret_cast<float*>(a.workspace + b.acc);

@@ -807,9 +807,10 @@ struct Parts {
 };
 
 // The forward pass reads hidden where it is if its rows start and end on 16-byte
-// boundaries; otherwise, and in the backward pass, it is copied to such rows with zeros behind them (a small part of
-// the call's bytes unless the vocabulary is small too).  weight may lie on any
-// 4-byte boundaries; only bf16 rows of odd width are copied, a piece at a time.
+// boundaries; otherwise, and in the backward pass, it is copied to such rows with
+// zeros behind them (a small part of the call's bytes unless the vocabulary is
+// small too).  weight may lie on any 4-byte boundaries; only bf16 rows of odd
+// width, or at odd addresses, are copied, a piece at a time.
 struct PadParts {
     uint64_t pitch, hidden, weight;
 };
@@ -817,14 +818,15 @@ PadParts pad_parts(Parts& w, uint64_t tokens, uint64_t cols, uint64_t piece, int
     PadParts b;
     b.pitch = up(cols * esize(dtype), 16);
     b.hidden = w.take(tokens * b.pitch);
-    b.weight = w.take(piece * b.pitch);
+    b.weight = dtype == kBF16 ? w.take(piece * b.pitch) : 0;
     return b;
 }
 bool hidden_direct(const LossArgs& a, int dtype) {
     return a.cols * esize(dtype) % 16 == 0 && reinterpret_cast<uintptr_t>(a.hidden) % 16 == 0;
 }
 bool weight_direct(const LossArgs& a, int dtype) {
-    if (a.cols * esize(dtype) % 4 != 0) return false;
+    if (dtype == kF32) return true;
+    if (a.cols % 2 != 0) return false;
     for (int r = 0; r < a.nranks; r++)
         if (reinterpret_cast<uintptr_t>(a.weight[r]) % 4 != 0) return false;
     return true;
@@ -873,10 +875,9 @@ void pad_rows(const void* src, char* dst, uint32_t rows, uint32_t cols, uint64_t
         hipLaunchKernelGGL(k_pad_rows<T>, dim3(rows), dim3(kThreads), 0, s, static_cast<const T*>(src), reinterpret_cast<T*>(dst),
                            cols, pitch / sizeof(T));
 }
-template <typename T>
 void pad_weight(const LossArgs& a, uint32_t first, uint32_t count, char* to, uint64_t pitch, hipStream_t s) {
-    const Segments g = segments_of(a, sizeof(T) == 2 ? kBF16 : kF32, first, count, nullptr, pitch);
-    for (int i = 0; i < g.n; i++) pad_rows<T>(g.weight[i], to + uint64_t(g.vocab[i] - first) * pitch, g.count[i], a.cols, pitch, s);
+    const Segments g = segments_of(a, kBF16, first, count, nullptr, pitch);
+    for (int i = 0; i < g.n; i++) pad_rows<uint16_t>(g.weight[i], to + uint64_t(g.vocab[i] - first) * pitch, g.count[i], a.cols, pitch, s);
 }
 
 // hidden's place and pitch, and weight's pitch; where weight has to be copied
@@ -939,7 +940,7 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
             Segments g = segments_of(a, DT, first, count, wpad, p.wpitch);
             set_tiles(g, kTileM[t], false);
             if (pass == 1) {
-                if (!direct) pad_weight<T>(a, first, count, wpad, p.wpitch, s);
+                if (!direct) pad_weight(a, first, count, wpad, p.wpitch, s);
                 with_rows_of<DT>(t, p.wpitch, [&](auto shape, auto tail) {
                     typedef decltype(shape) S;
                     constexpr bool TAIL = decltype(tail)::value;
@@ -1025,7 +1026,7 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
         Segments g = segments_of(a, DT, first, count, wpad, q.wpitch);
         p.ldv = g.col[g.n];
         if (a.tokens > 0) {
-            if (wpad != nullptr) pad_weight<T>(a, first, count, wpad, q.wpitch, s);
+            if (wpad != nullptr) pad_weight(a, first, count, wpad, q.wpitch, s);
             const Tile t = pick_tile(DT, count, a.tokens, true);
             set_tiles(g, kTileM[t], true);
             with_rows_of<DT>(t, q.wpitch, [&](auto shape, auto tail) {

@@ -367,7 +367,9 @@ dt_status dt_moe_combine_backward(const void* const* dout, const void* const* y,
  * and loss[q] [tokens] fp32 get log sum exp of the token's logits and lse - the
  * target's logit for every rank q; a target equal to ignore_index or outside
  * [0, V) leaves its token out (loss 0, no gradient, whatever its row of hidden
- * holds).  At most DT_MAX_LOSS_TOKENS tokens. */
+ * holds).  At most DT_MAX_LOSS_TOKENS tokens.  For bf16 the workspace has room
+ * for a copy of one piece of weight (16384 rows or more), which rows of odd
+ * width or at odd addresses need. */
 size_t dt_vocab_loss_workspace(int nranks, const size_t* vocab_rows, size_t tokens, size_t cols, dt_dtype dtype);
 dt_status dt_vocab_loss(const void* const* hidden, const void* const* weight, const int64_t* const* targets,
                         float* const* loss, float* const* lse, int nranks, const size_t* vocab_rows, size_t tokens,

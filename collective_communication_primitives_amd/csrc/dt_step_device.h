@@ -136,14 +136,6 @@ __device__ __forceinline__ float sum16(float v) {
     over16([&](auto c) { v += dpp<decltype(c)::value>(v); });
     return v;
 }
-__device__ __forceinline__ uint32_t min16(uint32_t v) {
-    over16([&](auto c) {
-        const uint32_t o = dpp<decltype(c)::value>(v);
-        v = o < v ? o : v;
-    });
-    return v;
-}
-
 // Sums and maxima over the wave's 64 lanes, the same value in every lane.
 __device__ __forceinline__ float wave_sum(float v) {
     v = sum16(v);

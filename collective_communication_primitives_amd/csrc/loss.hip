@@ -39,12 +39,11 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kChunks = 4;             // 16-byte chunks of the summed index per step
 constexpr int kStepBytes = kChunks * 16;
-constexpr int kStages = 4;             // steps in LDS
 constexpr int kThreads = 256;          // workgroups of the kernels without a matrix tile
 enum { kRows = 0, kCols = 1 };
 
 // A workgroup's tile of `out`: BM rows of A by BN rows of B, cut among GM x GN
-// waves.  Both operands go through LDS, kStages steps of the summed index at a
+// waves.  Both operands go through LDS, four steps of the summed index at a
 // time: one step is in registers and multiplied, the next one is read from
 // LDS, and the others are on their way from memory.
 template <int BM_, int BN_, int GM_, int GN_>
@@ -773,10 +772,10 @@ Tile pick_tile(int dtype, uint64_t m, uint64_t n, bool tiny, uint32_t splits = 1
     if (uint64_t(ceil_div(m, 256)) * ceil_div(n, 256) * splits >= 224) return kWide;
     return square >= 192 ? kSquare : kSmall;
 }
-// launch(Shape) with the shape of `t`.
-template <int DT, bool TOKENS, typename F>
+// launch(Shape) with the shape of `t`; TINY: where pick_tile may say so.
+template <int DT, bool TINY, typename F>
 void with_tile(Tile t, F&& launch) {
-    if constexpr (TOKENS) {
+    if constexpr (TINY) {
         if (t == kTiny) return launch(Tiny());
     }
     if constexpr (DT == kBF16) {
@@ -788,9 +787,9 @@ void with_tile(Tile t, F&& launch) {
 }
 // launch(Shape, TAIL): where weight's rows end inside a 16-byte chunk, the form
 // that masks what follows them.
-template <int DT, typename F>
+template <int DT, bool TINY, typename F>
 void with_rows_of(Tile t, uint32_t wpitch, F&& launch) {
-    with_tile<DT, true>(t, [&](auto shape) {
+    with_tile<DT, TINY>(t, [&](auto shape) {
         if (wpitch % 16 != 0) launch(shape, std::true_type());
         else launch(shape, std::false_type());
     });
@@ -941,7 +940,7 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
             set_tiles(g, kTileM[t], false);
             if (pass == 1) {
                 if (!direct) pad_weight(a, first, count, wpad, p.wpitch, s);
-                with_rows_of<DT>(t, p.wpitch, [&](auto shape, auto tail) {
+                with_rows_of<DT, DT == kF32>(t, p.wpitch, [&](auto shape, auto tail) {
                     typedef decltype(shape) S;
                     constexpr bool TAIL = decltype(tail)::value;
                     q.token_tiles = ceil_div(a.tokens, S::BN);
@@ -962,15 +961,15 @@ hipError_t forward(const LossArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// launch(Shape, parts of d)
-template <int DT, bool TOKENS, typename F>
-void with_parts(Tile t, uint64_t tokens, F&& launch) {
-    with_tile<DT, TOKENS>(t, [&](auto shape) {
-        if constexpr (DT == kBF16) {
-            if (d_parts(tokens, DT) == 2) return launch(shape, std::integral_constant<int, 2>());
-        }
-        launch(shape, std::integral_constant<int, 1>());
-    });
+// launch(parts of d).  TOKENS: the tile's n counts tokens, so the tiles of up to
+// 64 of them only meet d in two parts.
+template <int DT, typename S, bool TOKENS, typename F>
+void with_parts(uint64_t tokens, F&& launch) {
+    constexpr bool few = std::is_same<S, Tiny>::value || std::is_same<S, Narrow>::value;
+    if constexpr (DT == kBF16) {
+        if (d_parts(tokens, DT) == 2) return launch(std::integral_constant<int, 2>());
+    }
+    if constexpr (DT != kBF16 || !TOKENS || !few) launch(std::integral_constant<int, 1>());
 }
 
 // Few tiles of dhidden: the sum over the piece is cut among workgroups, each
@@ -1029,28 +1028,32 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
             if (wpad != nullptr) pad_weight(a, first, count, wpad, q.wpitch, s);
             const Tile t = pick_tile(DT, count, a.tokens, true);
             set_tiles(g, kTileM[t], true);
-            with_rows_of<DT>(t, q.wpitch, [&](auto shape, auto tail) {
-                with_parts<DT, true>(t, a.tokens, [&](auto, auto parts) {
-                    typedef decltype(shape) S;
-                    constexpr bool TAIL = decltype(tail)::value;
-                    p.nt = ceil_div(a.tokens, S::BN);
+            with_rows_of<DT, true>(t, q.wpitch, [&](auto shape, auto tail) {
+                typedef decltype(shape) S;
+                constexpr bool TAIL = decltype(tail)::value;
+                p.nt = ceil_div(a.tokens, S::BN);
+                with_parts<DT, S, true>(a.tokens, [&](auto parts) {
                     hipLaunchKernelGGL((k_loss_d<DT, S, TAIL, decltype(parts)::value>), dim3(g.tile[g.n] * p.nt), dim3(S::threads), 0, s, q, g, p);
                 });
             });
-            with_parts<DT, true>(pick_tile(DT, a.cols, a.tokens, true, p.splits), a.tokens, [&](auto shape, auto parts) {
+            with_tile<DT, true>(pick_tile(DT, a.cols, a.tokens, true, p.splits), [&](auto shape) {
                 typedef decltype(shape) S;
                 p.mt = ceil_div(a.cols, S::BM);
                 p.nt = ceil_div(a.tokens, S::BN);
-                hipLaunchKernelGGL((k_loss_dhidden<DT, S, decltype(parts)::value>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, q, g, p);
+                with_parts<DT, S, true>(a.tokens, [&](auto parts) {
+                    hipLaunchKernelGGL((k_loss_dhidden<DT, S, decltype(parts)::value>), dim3(p.mt * p.nt, p.splits), dim3(S::threads), 0, s, q, g, p);
+                });
             });
             p.add = 1;
         }
         const Tile t = pick_tile(DT, a.cols, count, false);
         set_tiles(g, kTileN[t], false);
-        with_parts<DT, false>(t, a.tokens, [&](auto shape, auto parts) {
+        with_tile<DT, false>(t, [&](auto shape) {
             typedef decltype(shape) S;
             p.mt = ceil_div(a.cols, S::BM);
-            hipLaunchKernelGGL((k_loss_dweight<DT, S, decltype(parts)::value>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
+            with_parts<DT, S, false>(a.tokens, [&](auto parts) {
+                hipLaunchKernelGGL((k_loss_dweight<DT, S, decltype(parts)::value>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
+            });
         });
     }
     if (a.tokens > 0) {

@@ -48,7 +48,11 @@ __device__ __forceinline__ float in_range(float f) { return fminf(fmaxf(f, -INFI
 
 // One token per wave, scores in 64 bits: lane l holds experts l, l + 64, ...
 // For the shapes that four tokens to a wave do not take: more than 512
-// experts, more than 16 choices, groups that are not whole lanes.
+// experts, more than 16 choices, and groups unless there are 64, 128, 256 or 512
+// experts in groups of a power of two of whole lanes.  An exponential in 64 bits for
+// each expert and a 64-bit reduction over the wave for each choice, and two for each
+// group: 32768 fp32 tokens with a bias, 6 of 160 experts in 8 groups 243 us, 8 of 96
+// in 4 137, 6 of 72 in 8 181, 8 of 1024 310, 17 of 128 136.
 template <int DT, int NV>
 __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     typedef typename Elem<DT>::type T;
@@ -411,10 +415,14 @@ __device__ __forceinline__ void sort_down(int32_t (&key)[NL]) {
 // chooses for that token again in 64 bits: about one token in a thousand of normally
 // distributed logits with a bias.
 //
-// 32768 tokens, 8 of 256 experts, fp32, sigmoid, bias, 8 groups: 30 us, bound by
-// the vector unit (some 900 instructions per wave; the logits' bytes alone are 7
-// us), 3 us of it the waves that choose again.  A wave per token with 64-bit
-// scores throughout took 229 us; 16 lanes that scan for each choice 61 us.
+// 32768 tokens, 8 of 256 experts, fp32, sigmoid, bias, 8 groups: 30 us (the logits'
+// bytes alone are 7), 3 us of it the waves that choose again.  The vector units are
+// busy for 67% of it, with 1230 instructions a wave; the rest is latency that too
+// few waves hide: 96 registers, most of them choose_exactly's, let 5 of the 8 waves
+// that each SIMD gets run at a time.  A wave per token with 64-bit scores
+// throughout took 229 us; 16 lanes that scan for each choice 61 us.  Equal logits
+// are close calls as well: 8 of 256 experts without groups and bias take 13 us, 49
+// where all logits are the same.
 template <int DT, int NL>
 __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int vec) {
     typedef typename Elem<DT>::type T;
@@ -565,7 +573,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
 //                 sigmoid: dx_{e_j} += g'_j s_j (1 - s_j)
 // L lanes per token (16 where topk and the experts fit, else the wave), NL
 // neighbouring experts each.  87000 tokens, 6 of 128 experts, bf16, dense: 18 us,
-// 2.7 TB/s, bound by the vector unit: some 400 instructions per wave, half of
+// 2.7 TB/s, bound by the vector unit: 450 instructions per wave, half of
 // them the comparisons that bring a choice's gradient to its expert.
 template <int L>
 __device__ __forceinline__ float sum_lanes(float v) {
@@ -683,7 +691,7 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
 // The plan is a stable counting sort of the slots by expert, over all ranks.
 // Slot order (rank, token, choice) is kept within an expert, so the rows' order
 // does not depend on timing.  Two launches, latency-bound: 131072 slots of 64
-// experts 6 us of counting and 15 us of placing, of 270 us with the rows.
+// experts 7 us of counting and 14 us of placing, of 270 us with the rows.
 __device__ __forceinline__ int32_t slot_expert(const PlanArgs& a, uint32_t slot, uint32_t slots) {
     if (slot >= slots) return -1;
     const uint32_t row = slot / a.topk;
@@ -859,7 +867,7 @@ __device__ __forceinline__ Choices choices(const ExchangeRowsArgs& a, P* const (
 }
 
 // The rows' traffic is bound by memory: 32768 rows of 8 KiB to 4 experts each
-// (1.34 GB) take 209 us, 6.4 TB/s.  Each row is read
+// (1.34 GB) take 247 us, 5.4 TB/s.  Each row is read
 // once and stored to all its places from registers.
 //
 // A token's row is worked on by WPT waves (1 for rows of up to 4 KiB, where four
@@ -1004,7 +1012,7 @@ struct Values {
 
 // out[t] = sum_j w_tj y[owner][pos_tj], in slot order, fp32, one rounding.  The
 // rows of up to four choices are on their way at a time.  12519 rows of 1001
-// fp32, 3 choices: 39 us, 5.1 TB/s on rows that start at any 4-byte boundary.
+// fp32, 3 choices: 41 us, 4.9 TB/s on rows that start at any 4-byte boundary.
 template <int DT, bool VEC, int WPT>
 __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
     typedef Values<DT> V;
@@ -1059,7 +1067,7 @@ __global__ __launch_bounds__(kBlock) void k_combine(ExchangeRowsArgs a) {
 }
 
 // dy[owner][pos] = w dout[t];  dw = <dout[t], y[owner][pos]>.  One pass over dout
-// and y; the same rows as above: 74 us, 4.7 TB/s.
+// and y; the same rows as above: 79 us, 4.4 TB/s.
 template <int DT, bool VEC, int WPT>
 __global__ __launch_bounds__(kBlock) void k_combine_backward(ExchangeRowsArgs a) {
     typedef Values<DT> V;

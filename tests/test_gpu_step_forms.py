@@ -155,7 +155,9 @@ def test_a_plan_of_many_workgroups(dt, rows, e, k, room):
     ([9000, 0, 12001], 256, 0), ([18000, 500], 251, 0),   # a wave to a row, above 16384 rows
     ([4000, 2, 3000], 1024, 0), ([6001], 1023, 1),        # four waves, above 4096 rows
     ([300, 0, 0, 900], 4104, 0), ([1100], 4111, 0),       # four units a lane (bf16), above 512 rows
+    ([4200, 300], 1504, 0), ([2100, 2300], 3001, 0),      # four waves with one and two units a lane (bf16), above 4096 rows
     ([700, 500], 16384, 0), ([1, 800], 16377, 0),         # sixteen waves, above 512 rows
+    ([300, 301], 20000, 0), ([530], 20001, 1),            # four units a lane (bf16); too wide for the registers (fp32)
 ], ids=str)
 def test_more_rows_than_workgroups(dt, rows, cols, offset, dtype):
     note(f"norm loops rows={rows} cols={cols} offset={offset} {dtype}")

@@ -520,6 +520,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_scale(LossProblem a, float* s
 }
 
 struct DPiece {
+    char* hidden;     // the first piece: where the tokens' rows go for dweight; NULL: nowhere
     char* d;          // [parts][tokens] rows of ldv elements: the piece's d, each segment's padding zero
     float* acc;       // [splits][tokens][ldx]
     const float* scale;  // [kScaleParts], NULL: 1
@@ -528,6 +529,20 @@ struct DPiece {
     uint32_t splits;  // workgroups that share one tile's sum over the piece
     int add;          // acc holds the earlier pieces' sum
 };
+
+// dweight reads a copy of hidden with rows of zeros for the tokens that are left
+// out: their d is zero, but zero times what a padded row holds may be NaN.  The
+// workgroups that form the first piece's d make it, each its share of the token
+// tile's rows, without a launch of its own (4.8 us of 369 for 509 x 1000 fp32).
+template <typename S>
+__device__ __forceinline__ void copy_tokens(const LossProblem& a, uint32_t n0, uint32_t part, uint32_t parts, char* to) {
+    const uint32_t units = a.hpitch / 16, rows = a.tokens - n0 < S::BN ? a.tokens - n0 : S::BN;
+    for (uint32_t i = part * S::threads + threadIdx.x; i < rows * units; i += parts * S::threads) {
+        const uint64_t n = n0 + i / units, at = n * a.hpitch + i % units * 16;
+        const bool use = counted(a, a.targets[n]);
+        *reinterpret_cast<u32x4*>(to + at) = use ? *reinterpret_cast<const u32x4*>(a.hidden + at) : u32x4{0, 0, 0, 0};
+    }
+}
 
 // What d is relative to, 1 or more and less than 2 (the whole wave asks; the same
 // value in every lane).
@@ -594,6 +609,7 @@ __global__ __launch_bounds__(S::threads) void k_loss_d(LossProblem a, Segments g
             }
         }
     }
+    if (p.hidden != nullptr) copy_tokens<S>(a, n0, mt, g.tile[g.n], p.hidden);
 }
 
 // The weight rows of a piece as the summed index: step by step through the
@@ -729,23 +745,13 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(const T* src, T* dst, uin
     for (uint32_t c = threadIdx.x; c < ld; c += kThreads) dst[row * ld + c] = c < cols ? src[row * cols + c] : T(0);
 }
 
-// The backward pass' copy of hidden: rows at hpitch with zeros behind them, and
-// rows of zeros for the tokens that are left out.  Their d is zero, but zero times
-// what a padded row holds may be NaN.  VEC: the rows start and end on 16-byte
-// boundaries.  4096 tokens of 4096 bf16: 11 us of 14.3 ms; 509 of 1000 fp32: 5 of 369.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_loss_hidden(LossProblem a, const T* src, char* dst) {
-    const uint64_t n = blockIdx.x;
+// hidden's rows of `cols` elements copied to rows of hpitch with zeros behind them,
+// and rows of zeros for the tokens that are left out.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void k_loss_hidden(LossProblem a, const T* src, T* dst) {
+    const uint64_t n = blockIdx.x, ld = a.hpitch / sizeof(T);
     const bool use = counted(a, a.targets[n]);
-    char* to = dst + n * a.hpitch;
-    if constexpr (VEC) {
-        const char* from = reinterpret_cast<const char*>(src) + n * a.hpitch;
-        for (uint32_t at = threadIdx.x * 16; at < a.hpitch; at += kThreads * 16)
-            *reinterpret_cast<u32x4*>(to + at) = use ? load16(from + at) : u32x4{0, 0, 0, 0};  // read again soon
-    } else {
-        for (uint32_t c = threadIdx.x; c < a.hpitch / sizeof(T); c += kThreads)
-            reinterpret_cast<T*>(to)[c] = use && c < a.cols ? src[n * a.cols + c] : T(0);
-    }
+    for (uint32_t c = threadIdx.x; c < ld; c += kThreads) dst[n * ld + c] = use && c < a.cols ? src[n * a.cols + c] : T(0);
 }
 
 // -------------------------------------------------------------------- host --
@@ -810,10 +816,9 @@ struct Parts {
     }
 };
 
-// The forward pass reads hidden where it is if its rows start and end on 16-byte
-// boundaries; otherwise, and in the backward pass, it is copied to such rows with
-// zeros behind them (a small part of the call's bytes unless the vocabulary is
-// small too).  weight may lie on any 4-byte boundaries; only bf16 rows of odd
+// hidden is read where it is if its rows start and end on 16-byte boundaries;
+// otherwise it is copied to such rows with zeros behind them (a small part of the
+// call's bytes unless the vocabulary is small too).  weight may lie on any 4-byte boundaries; only bf16 rows of odd
 // width, or at odd addresses, are copied, a piece at a time.
 struct PadParts {
     uint64_t pitch, hidden, weight;
@@ -885,21 +890,17 @@ void pad_weight(const LossArgs& a, uint32_t first, uint32_t count, char* to, uin
 }
 
 // hidden's place and pitch, and weight's pitch; where weight has to be copied
-// piece by piece, the place for it.  leave_out: hidden is copied in any case,
-// without the rows of the tokens that are left out.
+// piece by piece, the place for it.  leave_out: where hidden is copied, without the
+// rows of the tokens that are left out (the forward pass gives their lse too).
 template <typename T>
 char* place_rows(const LossArgs& a, int dtype, const PadParts& pad, LossProblem& p, bool leave_out, hipStream_t s) {
     p.hpitch = uint32_t(pad.pitch);
-    const bool vec = hidden_direct(a, dtype);
-    if (leave_out && a.tokens > 0) {
+    if (!hidden_direct(a, dtype)) {
         char* to = a.workspace + pad.hidden;
-        const T* from = static_cast<const T*>(a.hidden);
-        if (vec) hipLaunchKernelGGL((k_loss_hidden<T, true>), dim3(a.tokens), dim3(kThreads), 0, s, p, from, to);
-        else hipLaunchKernelGGL((k_loss_hidden<T, false>), dim3(a.tokens), dim3(kThreads), 0, s, p, from, to);
+        if (!leave_out) pad_rows<T>(a.hidden, to, a.tokens, a.cols, pad.pitch, s);
+        else if (a.tokens > 0)
+            hipLaunchKernelGGL(k_loss_hidden<T>, dim3(a.tokens), dim3(kThreads), 0, s, p, static_cast<const T*>(a.hidden), reinterpret_cast<T*>(to));
         p.hidden = to;
-    } else if (!vec) {
-        pad_rows<T>(a.hidden, a.workspace + pad.hidden, a.tokens, a.cols, pad.pitch, s);
-        p.hidden = a.workspace + pad.hidden;
     }
     const bool direct = weight_direct(a, dtype);
     p.wpitch = direct ? a.cols * uint32_t(sizeof(T)) : uint32_t(pad.pitch);
@@ -1015,7 +1016,10 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
     const BackwardParts b = backward_parts(a.nranks, a.tokens, a.cols, a.piece, DT);
     LossProblem q = problem_of(a);
     char* wpad = place_rows<T>(a, DT, b.pad, q, true, s);
+    LossProblem left = q;  // hidden without the tokens that are left out
+    left.hidden = a.workspace + b.pad.hidden;
     DPiece p = {};
+    if (hidden_direct(a, DT)) p.hidden = a.workspace + b.pad.hidden;
     p.d = a.workspace + b.d;
     p.acc = reinterpret_cast<float*>(a.workspace + b.acc);
     p.ldx = b.ldx;
@@ -1050,6 +1054,7 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
                 });
             });
             p.add = 1;
+            p.hidden = nullptr;
         }
         const Tile t = pick_tile(DT, a.cols, count, false);
         set_tiles(g, kTileN[t], false);
@@ -1057,7 +1062,7 @@ hipError_t backward(const LossArgs& a, hipStream_t s) {
             typedef decltype(shape) S;
             p.mt = ceil_div(a.cols, S::BM);
             with_parts<DT, S, false>(a.tokens, [&](auto parts) {
-                hipLaunchKernelGGL((k_loss_dweight<DT, S, decltype(parts)::value>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, q, g, p);
+                hipLaunchKernelGGL((k_loss_dweight<DT, S, decltype(parts)::value>), dim3(p.mt * g.tile[g.n]), dim3(S::threads), 0, s, left, g, p);
             });
         });
     }

@@ -20,12 +20,12 @@
 // weight in dhidden, hidden and d in dweight).  The second kind is turned on
 // the way from LDS to the registers, so nothing is stored transposed.
 //
-// 4096 tokens x 4096, 131072 rows in bf16: the forward pass takes 3.43 ms, 1.28
-// PFLOP/s, with gradients 14.3 ms: 1.23 PFLOP/s over its four products (the logits
+// 4096 tokens x 4096, 131072 rows in bf16: the forward pass takes 3.4 ms, 1.29
+// PFLOP/s, with gradients 14.2 ms: 1.24 PFLOP/s over its four products (the logits
 // twice), where a plain matrix product of that size reaches 1.46.  The matrix
 // units are busy for 68% of the time, at a clock of 1.8 GHz: bound by them and by
 // power.  In fp32 (154 TFLOP/s in a large product) 509 tokens x 1000, 10007 rows
-// take 369 us with gradients, 110 TFLOP/s, the matrix units of a running workgroup
+// take 365 us with gradients, 111 TFLOP/s, the matrix units of a running workgroup
 // 83% busy.
 #include "dt_step_device.h"
 
@@ -495,7 +495,7 @@ __global__ __launch_bounds__(kThreads) void k_loss_join(LossProblem a, StatsArgs
 //    relative to that mantissa it is a power of two.  The exponent stays in d:
 //    divided by a dloss of 1e38, the other tokens' d would vanish.
 // The cost of two parts for many tokens, where the matrix units are the bound: 4096
-// tokens x 4096, 131072 rows take 21.4 ms instead of 14.3, and the gradients are
+// tokens x 4096, 131072 rows take 21.4 ms instead of 14.2, and the gradients are
 // off by 1.7e-3 (the rounding of the results alone, as with d in fp32) instead of
 // 1.9e-3.
 constexpr uint32_t kTwoPartTokens = 512;
@@ -771,9 +771,8 @@ constexpr uint32_t kTileM[] = {256, 128, 128, 64, 64}, kTileN[] = {256, 128, 64,
 // The tile for an m x n product of `splits` sums: the largest that still
 // fills the 256 CUs.
 // tiny: for up to 16 tokens tiles of 16 of them, not to multiply mostly zeros
-// (12 x 1088 fp32, 30000 rows: forward 45 -> 32 us, backward 182 -> 146 without
-// hidden's copy of 5; 1 x 4096 bf16, 131072 rows: backward 1250 -> 1100).  The
-// forward pass in bf16 keeps tiles of 64 or 128 rows, whose maxima and sums are fewer
+// (12 x 1088 fp32, 30000 rows: forward 45 -> 32 us, backward 182 -> 146; 1 x
+// 4096 bf16, 131072 rows: backward 1250 -> 1090).  The forward pass in bf16 keeps tiles of 64 or 128 rows, whose maxima and sums are fewer
 // (187 us, tiny ones 227).
 Tile pick_tile(int dtype, uint64_t m, uint64_t n, bool tiny, uint32_t splits = 1) {
     if (tiny && n <= 16) return kTiny;

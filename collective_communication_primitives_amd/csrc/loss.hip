@@ -772,8 +772,8 @@ constexpr uint32_t kTileM[] = {256, 128, 128, 64, 64}, kTileN[] = {256, 128, 64,
 // fills the 256 CUs.
 // tiny: for up to 16 tokens tiles of 16 of them, not to multiply mostly zeros
 // (12 x 1088 fp32, 30000 rows: forward 45 -> 32 us, backward 182 -> 146; 1 x
-// 4096 bf16, 131072 rows: backward 1250 -> 1090).  The forward pass in bf16 keeps tiles of 64 or 128 rows, whose maxima and sums are fewer
-// (187 us, tiny ones 227).
+// 4096 bf16, 131072 rows: backward 1250 -> 1090).  The forward pass in bf16 keeps
+// tiles of 64 or 128 rows, whose maxima and sums are fewer (187 us, tiny ones 227).
 Tile pick_tile(int dtype, uint64_t m, uint64_t n, bool tiny, uint32_t splits = 1) {
     if (tiny && n <= 16) return kTiny;
     const uint64_t square = uint64_t(ceil_div(m, 128)) * ceil_div(n, 128) * splits;

@@ -46,6 +46,15 @@ constexpr float kBiggest = 3.402823466e38f;
 // A logit or bias as it counts: NaN is -inf, +inf the largest finite value.
 __device__ __forceinline__ float in_range(float f) { return fminf(fmaxf(f, -INFINITY), kBiggest); }
 
+// What a choice of logit x is in the sum over the chosen, whose largest logit is
+// `top`: its score but for a factor that is the same for all of them, exp(-top) for
+// softmax and exp(-min(top, 0)) for the sigmoid, so that the largest is not below a
+// half and a share keeps its digits where the score itself underflows.
+__device__ __forceinline__ float share_of(float x, float top, bool sigmoid) {
+    if (!sigmoid) return expf(x - top);
+    return x > 0.f ? 1.f / (1.f + expf(-x)) : expf(x - fminf(top, 0.f)) / (1.f + expf(x));
+}
+
 // One token per wave, scores in 64 bits: lane l holds experts l, l + 64, ...
 // For the shapes that four tokens to a wave do not take: more than 512
 // experts, more than 16 choices, and groups unless there are 64, 128, 256 or 512
@@ -176,11 +185,8 @@ __global__ __launch_bounds__(kBlock) void k_route_any(RouteArgs a, int nranks) {
     const bool has = mine != UINT32_MAX;
     float s;
     if (a.renormalize) {
-        // softmax: exp(x - max) over the chosen, the normaliser cancels; sigmoid: s over
-        // their sum, and exp(x - max) too where the scores underflow
         const float ctop = wave_max(has ? mylogit : -INFINITY);
-        s = has ? expf(mylogit - ctop) : 0.f;
-        if (a.sigmoid && ctop > -60.f) s = has ? 1.f / (1.f + expf(-mylogit)) : 0.f;
+        s = has ? share_of(mylogit, ctop, a.sigmoid) : 0.f;
         const float sum = wave_sum(s);
         s = has ? s / sum : 0.f;
     } else {
@@ -552,8 +558,7 @@ __global__ __launch_bounds__(kBlock) void k_route(RouteArgs a, int nranks, int v
     float s;
     if (a.renormalize) {
         const float ctop = max16(logit);
-        s = has ? expf(logit - ctop) : 0.f;
-        if (a.sigmoid && ctop > -60.f) s = has ? 1.f / (1.f + expf(-logit)) : 0.f;
+        s = has ? share_of(logit, ctop, a.sigmoid) : 0.f;
         const float all = sum16(s);
         s = has ? s / all : 0.f;
     } else {
@@ -628,8 +633,7 @@ __global__ __launch_bounds__(kBlock) void k_route_backward(RouteBackArgs a, int 
     float t;  // what choice j adds to its expert
     if (a.renormalize) {
         const float ctop = max_lanes<L>(logit);
-        float w = has ? expf(logit - ctop) : 0.f;
-        if (a.sigmoid && ctop > -60.f) w = has ? 1.f / (1.f + expf(-logit)) : 0.f;
+        float w = has ? share_of(logit, ctop, a.sigmoid) : 0.f;
         const float sum = sum_lanes<L>(w);
         w = has ? w / sum : 0.f;
         t = w * (g - sum_lanes<L>(g * w));

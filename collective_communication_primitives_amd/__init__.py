@@ -1000,6 +1000,86 @@ def dt_vocab_loss_backward(hidden: Sequence[torch.Tensor], weight: Sequence[torc
     return w if async_op else dhidden
 
 
+_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _act_code(act) -> int:
+    return _ACTS[act] if isinstance(act, str) else int(act)
+
+
+def dt_linear_backward_workspace(rows: Sequence[int], runs: int, outs: int, act="none", gated: bool = False, with_dbias: bool = False,
+                                 dtype=torch.bfloat16) -> int:
+    """Bytes of workspace dt_linear_backward takes."""
+    return _sized(_L.dt_linear_backward_workspace(len(rows), _size_array(rows), runs, outs, _act_code(act), int(bool(gated)),
+                                                  int(bool(with_dbias)), _DTYPES[dtype]))
+
+
+def _linear_shape(x, weight, offsets, gated):
+    """(ranks, cols, outs, runs, features, row counts) of products of x's rows with weight[r] [outs, cols], or [runs, outs, cols]
+    with offsets; gated: twice as many features as outs."""
+    p, cols = _ranks(x, "x"), _width(x[0], "x")
+    shape = weight[0].shape
+    if len(shape) != (2 if offsets is None else 3) and not (offsets is None and len(shape) == 3 and shape[0] == 1):
+        raise ValueError("weight[r] must be [outs, cols], or [runs, outs, cols] with offsets")
+    if shape[-1] != cols:
+        raise ValueError(f"weight[r] must have rows of {cols} elements, got {shape[-1]}")
+    features, runs = shape[-2], shape[0] if len(shape) == 3 else 1
+    if features < 1 or runs < 1 or (gated and features % 2):
+        raise ValueError("weight[r] must have at least one row for each run, and gated an even number")
+    return p, cols, features // (2 if gated else 1), runs, features, _row_counts(x, cols, "x")
+
+
+def dt_linear(x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor], y: Sequence[torch.Tensor],
+              bias: Optional[Sequence[torch.Tensor]] = None, residual: Optional[Sequence[torch.Tensor]] = None,
+              pre: Optional[Sequence[torch.Tensor]] = None, offsets: Optional[Sequence[torch.Tensor]] = None, act="none",
+              gated: bool = False, stream=None, async_op: bool = False, comm_stream=None):
+    """y[r] = residual[r] + act(x[r] weight[r]^T + bias[r]) for every rank's rows x[r] [rows, cols], weight[r] [outs, cols].
+    With offsets[r] (int32 [runs + 1], as dt_moe_dispatch leaves them) each run of rows meets its own weight[r][e]; rows
+    outside the runs are left as they were.  gated: weight[r] has 2 * outs rows, and act of the first half's products is
+    multiplied with the second half's.  act: "none", "relu", "gelu", "silu".  pre[r] keeps the products, before act, for
+    dt_linear_backward."""
+    dev, stash = torch.cuda.current_device(), []
+    code, dtype = _float_dtype(x[0]), x[0].dtype
+    p, cols, outs, runs, features, (sizes, rows, _, n) = _linear_shape(x, weight, offsets, gated)
+    narrow, wide = [k * outs for k in rows], [k * features for k in rows]
+    xs, ws = _buffers("x", x, sizes, dtype, dev, stash), _buffers("weight", weight, [runs * features * cols] * p, dtype, dev, stash)
+    bs = _buffers("bias", bias, [runs * features] * p, dtype, dev, stash) if bias is not None else None
+    rs = _buffers("residual", residual, narrow, dtype, dev, stash) if residual is not None else None
+    os = _buffers("offsets", offsets, [runs + 1] * p, torch.int32, dev, stash) if offsets is not None else None
+    ys = _buffers("y", y, narrow, dtype, dev, stash)
+    ps = _buffers("pre", pre, wide, dtype, dev, stash) if pre is not None else None
+    ac, gt = _act_code(act), int(bool(gated))
+    w = _launch(lambda st: _L.dt_linear(xs, ws, bs, rs, os, ys, ps, p, n, runs, cols, outs, ac, gt, code, st), stash, async_op, stream,
+                comm_stream)
+    return w if async_op else y
+
+
+def dt_linear_backward(dy: Sequence[torch.Tensor], x: Sequence[torch.Tensor], weight: Sequence[torch.Tensor],
+                       dx: Sequence[torch.Tensor], dweight: Sequence[torch.Tensor], pre: Optional[Sequence[torch.Tensor]] = None,
+                       dbias: Optional[Sequence[torch.Tensor]] = None, offsets: Optional[Sequence[torch.Tensor]] = None, act="none",
+                       gated: bool = False, workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False,
+                       comm_stream=None):
+    """Gradients of dt_linear: dx[r], dweight[r] and dbias[r] (None: not formed) from dy[r] and what the forward pass left in
+    pre[r] (None where act is "none" and the product is not gated).  residual's gradient is dy."""
+    dev, stash = torch.cuda.current_device(), []
+    code, dtype = _float_dtype(x[0]), x[0].dtype
+    p, cols, outs, runs, features, (sizes, rows, _, n) = _linear_shape(x, weight, offsets, gated)
+    weights = [runs * features * cols] * p
+    gs = _buffers("dy", dy, [k * outs for k in rows], dtype, dev, stash)
+    xs, ws = _buffers("x", x, sizes, dtype, dev, stash), _buffers("weight", weight, weights, dtype, dev, stash)
+    ps = _buffers("pre", pre, [k * features for k in rows], dtype, dev, stash) if pre is not None else None
+    os = _buffers("offsets", offsets, [runs + 1] * p, torch.int32, dev, stash) if offsets is not None else None
+    dxs, dws = _buffers("dx", dx, sizes, dtype, dev, stash), _buffers("dweight", dweight, weights, dtype, dev, stash)
+    dbs = _buffers("dbias", dbias, [runs * features] * p, dtype, dev, stash) if dbias is not None else None
+    ac, gt = _act_code(act), int(bool(gated))
+    need = _sized(_L.dt_linear_backward_workspace(p, n, runs, outs, ac, gt, int(dbias is not None), code))
+    space = _workspace(workspace, need, dev, stream, async_op, comm_stream, stash)
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_linear_backward(gs, xs, ws, ps, os, dxs, dws, dbs, p, n, runs, cols, outs, ac, gt, code, at, have, st),
+                stash, async_op, stream, comm_stream)
+    return w if async_op else dx
+
+
 __all__ = [
     "dt_allreduce", "dt_reduce_scatter", "dt_all_gather", "dt_all_to_all", "dt_bucket_allreduce", "dt_bucket_plan",
     "dt_all_gather_into_vec", "dt_broadcast", "dt_replicate_to_shard", "dt_all_to_all_dims",
@@ -1008,4 +1088,5 @@ __all__ = [
     "dt_layer_norm", "dt_layer_norm_backward", "dt_layer_norm_workspace", "dt_moe_route", "dt_moe_route_backward",
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
+    "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
 ]

@@ -22,6 +22,7 @@ EXPORTS = (
     "dt_layer_norm", "dt_layer_norm_backward", "dt_layer_norm_workspace", "dt_moe_route", "dt_moe_route_backward",
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
+    "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
 )
 
 
@@ -74,6 +75,9 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
         "dt_vocab_loss_workspace": [i32, vp, sz, sz, i32],
         "dt_vocab_loss_backward": [vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, sz, i64, sz, i32, vp, sz, vp],
         "dt_vocab_loss_backward_workspace": [i32, vp, sz, sz, sz, i32],
+        "dt_linear": [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, sz, sz, i32, i32, i32, vp],
+        "dt_linear_backward": [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, sz, sz, i32, i32, i32, vp, sz, vp],
+        "dt_linear_backward_workspace": [i32, vp, i32, sz, i32, i32, i32, i32],
         "dt_status_string": [i32],
         "dt_last_error": [],
         "dt_version": [],

@@ -47,8 +47,8 @@ __device__ __forceinline__ rsrc_t scalar_rsrc(const char* p, uint32_t bytes) {
 //
 // kRows: rows of `pitch` bytes, read up to `bytes`, a multiple of 16.  TAIL: the
 // row ends before that, after `valid` bytes (a multiple of 4), and what is read
-// behind its end, the next row's first values, is masked in the registers: the
-// other operand has zeros there, but an infinity times zero is NaN.
+// behind its end, the next row's first values, is masked in the registers: where
+// the other operand has zeros there, an infinity times zero would still be NaN.
 template <bool TAIL>
 struct RowOperand {
     static constexpr bool tail = TAIL;
@@ -58,6 +58,7 @@ struct RowOperand {
         return scalar_rsrc(p + step * kStepBytes, any && rows > 0 ? rows * pitch - step * kStepBytes : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t step) const { return bytes - step * kStepBytes; }
+    __device__ __forceinline__ uint32_t group_at(uint32_t group) const { return group * 16 * pitch; }  // 16 rows of the tile
     // the lane's chunk of a step, without what lies behind the row
     __device__ __forceinline__ u32x4 cut(u32x4 v, uint32_t step) const {
         if constexpr (TAIL) {
@@ -114,18 +115,18 @@ __device__ __forceinline__ uint32_t row_turn(uint32_t row) {
 
 // One load instruction of the wave brings 1 KiB of the operand's step into
 // LDS, 16 bytes per lane in lane order: the lane's place in the step.
-template <int DT, int MODE, int R>
-__device__ __forceinline__ uint32_t load_place(uint32_t group, uint32_t pitch) {
+template <int DT, int MODE, int R, typename OP>
+__device__ __forceinline__ uint32_t load_place(const OP& op, uint32_t group) {
     const uint32_t lane = threadIdx.x & 63;
     if constexpr (MODE == kRows) {
         // 16 rows of 64 bytes: lane l brings row l / 4
         const uint32_t row = lane >> 2;
-        return (group * 16 + row) * pitch + ((lane & 3) ^ row_turn(row)) * 16;
+        return op.group_at(group) + row * op.pitch + ((lane & 3) ^ row_turn(row)) * 16;
     } else {
         typedef ColTile<DT, R> C;
         constexpr uint32_t slots = C::row_bytes / 16, per_unit = C::unit_bytes / 16;
         const uint32_t k = group * C::per_load + lane / slots, slot = lane % slots;
-        return k * pitch + ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16;
+        return k * op.pitch + ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16;
     }
 }
 // `groups` load instructions of the wave; kRows: zeros behind a row's last byte.
@@ -195,6 +196,18 @@ __device__ __forceinline__ void arrive() {
     asm volatile("" ::: "memory");
 }
 
+// A wave's 16 x 16 part of the product of two fragments.
+template <int DT>
+__device__ __forceinline__ f32x4 multiply(const u32x4& a, const u32x4& b, f32x4 acc) {
+    if constexpr (DT == kBF16) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), acc, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[e]), __uint_as_float(b[e]), acc, 0, 0, 0);
+        return acc;
+    }
+}
+
 // acc[i][j][e] over steps [lo, hi): row m = WM (wave % GM) + 16 i + 4 (lane /
 // 16) + e of A's tile, row n = WN (wave / GM) + 16 j + lane % 16 of B's.
 //
@@ -214,9 +227,9 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     // the wave's shares of A's and B's groups of 1 KiB
     uint32_t pa[S::loads_a], pb[S::loads_b];
 #pragma unroll
-    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(wave * S::loads_a + i, A.pitch);
+    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(A, wave * S::loads_a + i);
 #pragma unroll
-    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(wave * S::loads_b + i, B.pitch);
+    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(B, wave * S::loads_b + i);
     // The loop runs in whole rounds of four steps: what is loaded for the steps
     // behind the last one is zeros (from an empty buffer, no memory is read), so
     // a wave's outstanding loads can be counted and the loop has one exit.
@@ -233,7 +246,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
 #pragma unroll
     for (int i = 0; i < S::MI; i++) fa[i] = A.cut(fragment<DT, MA, S::BM>(s0, ra, i), lo);
 #pragma unroll
-    for (int j = 0; j < S::NI; j++) fb[0][j] = fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j);
+    for (int j = 0; j < S::NI; j++) fb[0][j] = B.cut(fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j), lo);
     // Step `step`: its registers are loaded, and the next step's bytes are in
     // LDS once all waves are here.  The stage that is loaded into, the one
     // before this step's, was read two turns ago, so the last turn's reads may
@@ -251,21 +264,11 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
         // keeps the compiler from holding every fragment's address of every stage in a register
         asm volatile("" : "+v"(ra), "+v"(rb));
 #pragma unroll
-        for (int j = 0; j < S::NI; j++) next[j] = fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j);
+        for (int j = 0; j < S::NI; j++) next[j] = B.cut(fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j), step + 1);
 #pragma unroll
         for (int i = 0; i < S::MI; i++) {
 #pragma unroll
-            for (int j = 0; j < S::NI; j++) {
-                if constexpr (DT == kBF16) {
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, fa[i]),
-                                                                        __builtin_bit_cast(bf16x8, now[j]), acc[i][j], 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(fa[i][e]), __uint_as_float(now[j][e]),
-                                                                         acc[i][j], 0, 0, 0);
-                }
-            }
+            for (int j = 0; j < S::NI; j++) acc[i][j] = multiply<DT>(fa[i], now[j], acc[i][j]);
             fa[i] = A.cut(fragment<DT, MA, S::BM>(following, ra, i), step + 1);
         }
     };

@@ -140,4 +140,31 @@ uint64_t loss_backward_workspace(int nranks, uint64_t tokens, uint64_t cols, uin
 hipError_t launch_loss(const LossArgs& a, int dtype, hipStream_t s);
 hipError_t launch_loss_backward(const LossArgs& a, int dtype, hipStream_t s);
 
+// ------------------------------------------------------- matrix products --
+// Of every rank's rows, which fall into `runs` runs by the rank's offsets (NULL:
+// one run of all rows), each with a weight of its own.
+struct LinearArgs {
+    const void* x[kMaxRanksHost];           // [rows, cols]
+    const void* weight[kMaxRanksHost];      // [runs, outs (gated: twice), cols]
+    const int32_t* offsets[kMaxRanksHost];  // [runs + 1]
+    const void* bias[kMaxRanksHost];        // forward; all NULL: none
+    const void* residual[kMaxRanksHost];
+    void* y[kMaxRanksHost];
+    void* pre[kMaxRanksHost];
+    const void* dy[kMaxRanksHost];          // backward
+    const void* saved[kMaxRanksHost];       // what the forward pass left in pre
+    void* dx[kMaxRanksHost];
+    void* dweight[kMaxRanksHost];
+    void* dbias[kMaxRanksHost];
+    char* dz;                               // [all ranks' rows] rows of zpitch bytes; unused where dz is dy
+    float* partial;                         // [tiles of rows][outs (gated: twice)]
+    RowTable rows;
+    uint32_t runs, cols, outs, zpitch;
+    int act, gated, need_dz, nranks;
+    int quads, col_quads;                   // rows of outs, of cols, are whole fours, aligned to them
+};
+uint64_t linear_backward_workspace(const RowTable& rows, int nranks, uint32_t runs, uint64_t outs, int act, int gated, bool dbias, int dtype);
+hipError_t launch_linear(const LinearArgs& a, int dtype, hipStream_t s);
+hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, int dtype, hipStream_t s);
+
 }  // namespace dt

@@ -1,0 +1,589 @@
+// linear.hip -- matrix products of every rank's rows with bias, activation and
+// residual in the epilogue, one weight matrix per run of rows: the experts'
+// products between dispatch and combine, or a dense layer (one run).
+//
+//   z = W_e x + b_e        y = residual + act(z)
+//   gated: z = [g; u],     y = residual + act(g) u
+//   dz = dy act'(z); gated: dg = dy u act'(g), du = dy act(g)
+//   dx = W_e^T dz          dW_e = sum over the run's rows of dz x^T,  db_e = sum of dz
+//   relu: max(z, 0)   gelu: z Phi(z), Phi the normal distribution function   silu: z / (1 + exp(-z))
+//
+// The runs' ends are known on the device only (dt_moe_dispatch leaves them
+// there), so a workgroup counts the tiles of all runs itself and walks over its
+// share of them; nothing depends on the capacity of the rows' buffers.
+//
+// All sums are fp32.  z, y, dx, dW and db are rounded once; dz is rounded to the
+// tensors' type before it enters its two products, as the matrix units take it.
+#include "dt_act.h"
+#include "dt_matrix.h"
+
+namespace dt {
+namespace {
+
+constexpr int kThreads = 256;     // workgroups of the kernels without a matrix tile
+constexpr uint32_t kMaxRuns = DT_MAX_EXPERTS;
+
+// Run g = rank * runs + run: its rank and its rows of the rank's, cut to the rows that are there.
+struct Run {
+    uint32_t rank, run, lo, count;
+};
+__device__ __forceinline__ Run run_at(const LinearArgs& a, uint32_t g) {
+    const uint32_t q = g / a.runs, e = g % a.runs, rows = a.rows.start[q + 1] - a.rows.start[q];
+    if (rows == 0 || a.offsets[q] == nullptr) return Run{q, e, 0, rows};
+    const int32_t lo = a.offsets[q][e], hi = a.offsets[q][e + 1];
+    const uint32_t from = lo < 0 ? 0 : uint32_t(lo) < rows ? uint32_t(lo) : rows;
+    const uint32_t to = hi < 0 ? 0 : uint32_t(hi) < rows ? uint32_t(hi) : rows;
+    return Run{q, e, from, to > from ? to - from : 0};
+}
+// The same run in every lane of the wave.
+__device__ __forceinline__ Run same(const Run& r) {
+    return Run{uint32_t(__builtin_amdgcn_readfirstlane(r.rank)), uint32_t(__builtin_amdgcn_readfirstlane(r.run)),
+               uint32_t(__builtin_amdgcn_readfirstlane(r.lo)), uint32_t(__builtin_amdgcn_readfirstlane(r.count))};
+}
+
+// first[g]: tiles of `per` rows of the runs before g; first[all runs]: their number in all.
+__device__ __forceinline__ void count_tiles(const LinearArgs& a, uint32_t per, uint32_t* first) {
+    const uint32_t groups = a.runs * a.nranks;
+    for (uint32_t g = threadIdx.x; g < groups; g += blockDim.x) first[g] = (run_at(a, g).count + per - 1) / per;
+    __syncthreads();
+    if (threadIdx.x < 64) {
+        const uint32_t each = (groups + 63) / 64, lo = threadIdx.x * each, hi = lo + each < groups ? lo + each : groups;
+        uint32_t sum = 0;
+        for (uint32_t g = lo; g < hi; g++) sum += first[g];
+        uint32_t before = sum;
+#pragma unroll
+        for (int m = 1; m < 64; m <<= 1) {
+            const uint32_t o = uint32_t(__shfl_up(int(before), m));
+            if (int(threadIdx.x) >= m) before += o;
+        }
+        before -= sum;
+        for (uint32_t g = lo; g < hi; g++) {
+            const uint32_t n = first[g];
+            first[g] = before;
+            before += n;
+        }
+        if (threadIdx.x == 63) first[groups] = before;
+    }
+    __syncthreads();
+}
+// The run that tile t belongs to.
+__device__ __forceinline__ uint32_t run_of_tile(const uint32_t* first, uint32_t groups, uint32_t t) {
+    uint32_t lo = 0, hi = groups;  // first[lo] <= t < first[hi]
+    while (lo + 1 < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (first[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return uint32_t(__builtin_amdgcn_readfirstlane(lo));
+}
+
+// --------------------------------------------------------------- operands --
+// A gated product's tile of weight rows: 16 rows of the gate and the 16 of the
+// linear part that they meet, in turn, so that a lane has both of a feature.
+template <bool TAIL>
+struct GatedOperand : RowOperand<TAIL> {
+    uint32_t half;   // bytes between a gate row and its linear row
+    __device__ __forceinline__ uint32_t group_at(uint32_t group) const { return (group >> 1) * 16 * this->pitch + (group & 1) * half; }
+};
+
+// Operands whose rows start at any element: read at that alignment into
+// registers and put into LDS in the order that the direct loads leave there.
+template <int ES>
+__device__ __forceinline__ u32x4 read_loose(const char* row, uint32_t at, uint32_t bytes) {
+    u32x4 x = {0, 0, 0, 0};
+    if (at + 16 <= bytes) {
+        x = *reinterpret_cast<const typename Loose<ES>::type*>(row + at);
+    } else if (at < bytes) {
+        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
+        T t[16 / ES];
+#pragma unroll
+        for (int e = 0; e < 16 / ES; e++) t[e] = at + e * ES < bytes ? *reinterpret_cast<const T*>(row + at + e * ES) : T(0);
+        __builtin_memcpy(&x, t, 16);
+    }
+    return x;
+}
+struct LooseRows {
+    const char* p;      // the tile's first row
+    uint32_t rows, pitch;
+    uint32_t half;      // gated: rows between a gate row and its linear row, otherwise 0
+    template <int ES, int R>
+    __device__ __forceinline__ u32x4 chunk(uint32_t group, uint32_t step) const {
+        const uint32_t lane = threadIdx.x & 63, sub = lane >> 2;
+        const uint32_t row = half != 0 ? (group >> 1) * 16 + sub : group * 16 + sub;
+        if (row >= rows) return u32x4{0, 0, 0, 0};
+        return read_loose<ES>(p + uint64_t(row + (group & 1) * half) * pitch, step * kStepBytes + ((lane & 3) ^ row_turn(sub)) * 16, pitch);
+    }
+};
+struct LooseCols {
+    const char* p;      // row 0 at the tile's first column
+    uint32_t rows, pitch, bytes;   // bytes: of a row from the tile's first column on
+    template <int ES, int R>
+    __device__ __forceinline__ u32x4 chunk(uint32_t group, uint32_t step) const {
+        typedef ColTile<ES == 2 ? kBF16 : kF32, R> C;
+        constexpr uint32_t slots = C::row_bytes / 16, per_unit = C::unit_bytes / 16;
+        const uint32_t lane = threadIdx.x & 63, k = group * C::per_load + lane / slots, slot = lane % slots, row = step * C::KR + k;
+        if (row >= rows) return u32x4{0, 0, 0, 0};
+        return read_loose<ES>(p + uint64_t(row) * pitch, ((slot / per_unit) ^ C::f(k)) * C::unit_bytes + slot % per_unit * 16, bytes);
+    }
+};
+
+// matrix_tile for such operands: two stages of LDS, the next step's bytes on
+// their way to registers while one is multiplied.
+template <int DT, typename S, int MA, int MB, typename OA, typename OB>
+__device__ __forceinline__ void loose_tile(const OA& A, const OB& B, uint32_t steps, f32x4 (&acc)[S::MI][S::NI]) {
+    constexpr int ES = DT == kBF16 ? 2 : 4;
+    __shared__ u32x4 stage[2][S::stage];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < S::MI; i++)
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    u32x4 ca[S::loads_a], cb[S::loads_b];
+    auto read = [&](uint32_t step) {
+#pragma unroll
+        for (int i = 0; i < S::loads_a; i++) ca[i] = A.template chunk<ES, S::BM>(wave * S::loads_a + i, step);
+#pragma unroll
+        for (int i = 0; i < S::loads_b; i++) cb[i] = B.template chunk<ES, S::BN>(wave * S::loads_b + i, step);
+    };
+    const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
+    const uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
+    if (steps > 0) read(0);
+    for (uint32_t step = 0; step < steps; step++) {
+        u32x4* to = stage[step & 1];
+#pragma unroll
+        for (int i = 0; i < S::loads_a; i++) to[(wave * S::loads_a + i) * 64 + lane] = ca[i];
+#pragma unroll
+        for (int i = 0; i < S::loads_b; i++) to[S::BM * kChunks + (wave * S::loads_b + i) * 64 + lane] = cb[i];
+        // The other stage was read before this barrier's predecessor by every wave, or is read behind it: it is
+        // written again behind the next one only.
+        __syncthreads();
+        if (step + 1 < steps) read(step + 1);
+        u32x4 fa, fb[S::NI];
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) fb[j] = fragment<DT, MB, S::BN>(to + S::BM * kChunks, rb, j);
+#pragma unroll
+        for (int i = 0; i < S::MI; i++) {
+            fa = fragment<DT, MA, S::BM>(to, ra, i);
+#pragma unroll
+            for (int j = 0; j < S::NI; j++) acc[i][j] = multiply<DT>(fa, fb[j], acc[i][j]);
+        }
+    }
+    __syncthreads();  // the next tile writes the first stage
+}
+
+// Four neighbouring values; quads: stored and read as one.
+template <int DT>
+__device__ __forceinline__ f32x4 load_four(const typename Elem<DT>::type* p, bool quads, uint32_t left) {
+    typedef typename Elem<DT>::type T;
+    T t[4];
+    if (quads) {
+        if constexpr (DT == kBF16) *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(p);
+        else *reinterpret_cast<u32x4*>(t) = *reinterpret_cast<const u32x4*>(p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) t[e] = uint32_t(e) < left ? p[e] : T(0);
+    }
+    return f32x4{Elem<DT>::get(t[0]), Elem<DT>::get(t[1]), Elem<DT>::get(t[2]), Elem<DT>::get(t[3])};
+}
+template <int DT>
+__device__ __forceinline__ void store_four(typename Elem<DT>::type* p, f32x4 v, bool quads, uint32_t left) {
+    if (quads) {
+        store_quad<DT>(p, v, true);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            if (uint32_t(e) < left) p[e] = Elem<DT>::put(v[e]);
+    }
+}
+
+// ---------------------------------------------------------------- forward --
+// What becomes of four neighbouring features' sums of one row (gated: u their linear parts).
+template <int DT, bool GATED>
+__device__ __forceinline__ void finish(const LinearArgs& a, const Run& r, uint64_t row, uint32_t m, f32x4 z, f32x4 u) {
+    typedef typename Elem<DT>::type T;
+    const uint32_t left = a.outs - m, wide = GATED ? 2 * a.outs : a.outs;
+    const bool quads = a.quads;
+    if (a.bias[r.rank] != nullptr) {
+        const T* b = static_cast<const T*>(a.bias[r.rank]) + uint64_t(r.run) * wide + m;
+        z += load_four<DT>(b, quads, left);
+        if (GATED) u += load_four<DT>(b + a.outs, quads, left);
+    }
+    if (a.pre[r.rank] != nullptr) {
+        T* p = static_cast<T*>(a.pre[r.rank]) + row * wide + m;
+        store_four<DT>(p, z, quads, left);
+        if (GATED) store_four<DT>(p + a.outs, u, quads, left);
+    }
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; e++) y[e] = act<DT>(z[e], a.act) * (GATED ? u[e] : 1.f);
+    if (a.residual[r.rank] != nullptr) y += load_four<DT>(static_cast<const T*>(a.residual[r.rank]) + row * a.outs + m, quads, left);
+    store_four<DT>(static_cast<T*>(a.y[r.rank]) + row * a.outs + m, y, quads, left);
+}
+
+// PATH: rows on 16-byte boundaries, on 4-byte boundaries, or on any.
+enum { kWhole = 0, kTail = 1, kLoose = 2 };
+
+template <int DT, typename S, int PATH, bool GATED>
+__global__ __launch_bounds__(S::threads) void k_linear(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    constexpr uint32_t BM = GATED ? S::BM / 2 : S::BM;   // features of a tile
+    __shared__ uint32_t first[kMaxRuns + 1];
+    count_tiles(a, S::BN, first);
+    const uint32_t groups = a.runs * a.nranks, nts = __builtin_amdgcn_readfirstlane(first[groups]), mts = (a.outs + BM - 1) / BM;
+    const uint32_t pitch = a.cols * uint32_t(sizeof(T)), steps = (pitch + kStepBytes - 1) / kStepBytes;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint32_t id = blockIdx.x; id < mts * nts; id += gridDim.x) {
+        uint32_t mt, nt;
+        tile_of(id, mts, nts, mt, nt);
+        const uint32_t g = run_of_tile(first, groups, nt);
+        const Run r = same(run_at(a, g));
+        const uint32_t m0 = mt * BM, n0 = (nt - __builtin_amdgcn_readfirstlane(first[g])) * S::BN;
+        const uint32_t mleft = a.outs - m0, nleft = r.count - n0, nrows = nleft < S::BN ? nleft : S::BN;
+        const char* w = static_cast<const char*>(a.weight[r.rank]) + (uint64_t(r.run) * (GATED ? 2 : 1) * a.outs + m0) * pitch;
+        const char* x = static_cast<const char*>(a.x[r.rank]) + uint64_t(r.lo + n0) * pitch;
+        f32x4 acc[S::MI][S::NI];
+        if constexpr (PATH == kLoose) {
+            loose_tile<DT, S, kRows, kRows>(LooseRows{w, mleft < BM ? mleft : BM, pitch, GATED ? a.outs : 0}, LooseRows{x, nrows, pitch, 0}, steps, acc);
+        } else {
+            constexpr bool TAIL = PATH == kTail;
+            const uint32_t whole = (pitch + 15) / 16 * 16, mrows = mleft < BM ? mleft : BM;
+            const RowOperand<TAIL> B{x, nrows, pitch, whole, pitch};
+            if constexpr (GATED) {
+                GatedOperand<TAIL> A;
+                A.p = w;
+                A.rows = a.outs + mrows;
+                A.pitch = pitch;
+                A.bytes = whole;
+                A.valid = pitch;
+                A.half = a.outs * pitch;
+                matrix_tile<DT, S, kRows, kRows>(A, B, 0, steps, acc);
+            } else {
+                matrix_tile<DT, S, kRows, kRows>(RowOperand<TAIL>{w, mrows, pitch, whole, pitch}, B, 0, steps, acc);
+            }
+        }
+        // acc[i][j][e]: feature row WM (wave % GM) + 16 i + 4 (lane / 16) + e of the tile, token WN (wave / GM) + 16 j + lane % 16
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) {
+            const uint32_t n = (wave / S::GM) * S::WN + j * 16 + (lane & 15);
+            if (n >= nleft) continue;
+#pragma unroll
+            for (int i = 0; i < S::MI; i += GATED ? 2 : 1) {
+                const uint32_t ml = ((wave % S::GM) * S::WM + i * 16) / (GATED ? 2 : 1) + (lane >> 4) * 4;
+                if (ml >= mleft) continue;
+                finish<DT, GATED>(a, r, r.lo + n0 + n, m0 + ml, acc[i][j], acc[GATED ? i + 1 : i][j]);
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------- backward --
+// dz of the runs' rows, kDzRows rows and 1024 columns to a workgroup, and its
+// columns' sums over those rows.  A thread has four neighbouring columns.
+constexpr uint32_t kDzRows = 64;
+
+template <int DT, bool GATED>
+__global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    __shared__ uint32_t first[kMaxRuns + 1];
+    count_tiles(a, kDzRows, first);
+    const uint32_t groups = a.runs * a.nranks, tiles = first[groups], m = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    const uint32_t wide = GATED ? 2 * a.outs : a.outs;
+    const uint64_t ldz = a.zpitch / sizeof(T);
+    const bool quads = a.quads;
+    if (m >= a.outs) return;
+    const uint32_t left = a.outs - m;
+    for (uint32_t t = blockIdx.y; t < tiles; t += gridDim.y) {
+        const uint32_t g = run_of_tile(first, groups, t);
+        const Run r = same(run_at(a, g));
+        const uint32_t n0 = (t - first[g]) * kDzRows, rows = r.count - n0 < kDzRows ? r.count - n0 : kDzRows;
+        const uint64_t row0 = r.lo + n0;
+        const T* dy = static_cast<const T*>(a.dy[r.rank]) + row0 * a.outs + m;
+        const T* pre = a.need_dz ? static_cast<const T*>(a.saved[r.rank]) + row0 * wide + m : nullptr;
+        T* dz = a.need_dz ? reinterpret_cast<T*>(a.dz) + (a.rows.start[r.rank] + row0) * ldz : nullptr;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f}, sumu = sum;
+        for (uint32_t n = 0; n < rows; n++) {
+            f32x4 d = load_four<DT>(dy + uint64_t(n) * a.outs, quads, left), du = {0.f, 0.f, 0.f, 0.f};
+            if (a.need_dz) {
+                const f32x4 z = load_four<DT>(pre + uint64_t(n) * wide, quads, left);
+                if (GATED) {
+                    const f32x4 u = load_four<DT>(pre + uint64_t(n) * wide + a.outs, quads, left);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        float value, slope;
+                        act_and_slope<DT>(z[e], a.act, value, slope);
+                        du[e] = d[e] * value;
+                        d[e] = d[e] * u[e] * slope;
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        float value, slope;
+                        act_and_slope<DT>(z[e], a.act, value, slope);
+                        d[e] *= slope;
+                    }
+                }
+                T* to = dz + n * ldz;
+                store_four<DT>(to + m, d, quads, left);
+                if (GATED) store_four<DT>(to + a.outs + m, du, quads, left);
+                if (left <= 4)  // what lies between the row's end and its pitch
+                    for (uint64_t c = wide; c < ldz; c++) to[c] = T(0);
+            }
+            sum += d;
+            if (GATED) sumu += du;
+        }
+        if (a.partial != nullptr) {
+            float* to = a.partial + uint64_t(t) * wide + m;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (uint32_t(e) < left) {
+                    to[e] = sum[e];
+                    if (GATED) to[a.outs + e] = sumu[e];
+                }
+        }
+    }
+}
+
+// db of run blockIdx.y: its tiles' sums in order.
+template <int DT>
+__global__ __launch_bounds__(kThreads) void k_linear_dbias(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    __shared__ uint32_t first[kMaxRuns + 1];
+    count_tiles(a, kDzRows, first);
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, c = blockIdx.x * kThreads + threadIdx.x, g = blockIdx.y;
+    if (c >= wide) return;
+    float s = 0.f;
+    for (uint32_t t = first[g]; t < first[g + 1]; t++) s += a.partial[uint64_t(t) * wide + c];
+    static_cast<T*>(a.dbias[g / a.runs])[uint64_t(g % a.runs) * wide + c] = Elem<DT>::put(s);
+}
+
+// Rows of dz: in the workspace, or dy itself where dz is dy.
+template <typename T>
+__device__ __forceinline__ const char* dz_row(const LinearArgs& a, const Run& r, uint32_t row) {
+    return a.need_dz ? a.dz + (uint64_t(a.rows.start[r.rank]) + r.lo + row) * a.zpitch
+                     : static_cast<const char*>(a.dy[r.rank]) + uint64_t(r.lo + row) * a.zpitch;
+}
+
+// dx[t][k] = sum over the features of dz[t][m] W[m][k].
+template <int DT, typename S, int PATH>
+__global__ __launch_bounds__(S::threads) void k_linear_dx(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    constexpr uint32_t es = sizeof(T);
+    __shared__ uint32_t first[kMaxRuns + 1];
+    count_tiles(a, S::BN, first);
+    const uint32_t groups = a.runs * a.nranks, nts = __builtin_amdgcn_readfirstlane(first[groups]), mts = (a.cols + S::BM - 1) / S::BM;
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es, steps = (wide * es + kStepBytes - 1) / kStepBytes;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint32_t id = blockIdx.x; id < mts * nts; id += gridDim.x) {
+        uint32_t mt, nt;
+        tile_of(id, mts, nts, mt, nt);
+        const uint32_t g = run_of_tile(first, groups, nt);
+        const Run r = same(run_at(a, g));
+        const uint32_t m0 = mt * S::BM, n0 = (nt - __builtin_amdgcn_readfirstlane(first[g])) * S::BN;
+        const uint32_t nleft = r.count - n0, nrows = nleft < S::BN ? nleft : S::BN;
+        const char* w = static_cast<const char*>(a.weight[r.rank]) + uint64_t(r.run) * wide * pitch + m0 * es;
+        const char* d = dz_row<T>(a, r, n0);
+        f32x4 acc[S::MI][S::NI];
+        if constexpr (PATH == kLoose) {
+            loose_tile<DT, S, kCols, kRows>(LooseCols{w, wide, pitch, pitch - m0 * es}, LooseRows{d, nrows, a.zpitch, 0}, steps, acc);
+        } else {
+            const ColOperand<kStepBytes / int(es), 1> A{w, wide, pitch, m0 * es, 0};
+            const RowOperand<PATH == kTail> B{d, nrows, a.zpitch, (a.zpitch + 15) / 16 * 16, wide * es};
+            matrix_tile<DT, S, kCols, kRows>(A, B, 0, steps, acc);
+        }
+        T* out = static_cast<T*>(a.dx[r.rank]);
+        const bool quads = a.col_quads;
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) {
+            const uint32_t n = (wave / S::GM) * S::WN + j * 16 + (lane & 15);
+            if (n >= nleft) continue;
+#pragma unroll
+            for (int i = 0; i < S::MI; i++) {
+                const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
+                if (m >= a.cols) continue;
+                store_four<DT>(out + uint64_t(r.lo + n0 + n) * a.cols + m, acc[i][j], quads, a.cols - m);
+            }
+        }
+    }
+}
+
+// dW[m][k] = sum over the run's rows of dz[t][m] x[t][k]; zeros for a run without rows.
+template <int DT, typename S, int PATH>
+__global__ __launch_bounds__(S::threads) void k_linear_dweight(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    constexpr uint32_t es = sizeof(T), KR = kStepBytes / es;
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es;
+    const uint32_t mts = (a.cols + S::BM - 1) / S::BM, each = (wide + S::BN - 1) / S::BN, nts = each * a.runs * a.nranks;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (uint64_t at = blockIdx.x; at < uint64_t(mts) * nts; at += gridDim.x) {
+        uint32_t mt, nt;
+        tile_of(uint32_t(at), mts, nts, mt, nt);
+        const Run r = same(run_at(a, nt / each));
+        const uint32_t m0 = mt * S::BM, n0 = nt % each * S::BN, steps = (r.count + KR - 1) / KR;
+        const char* x = static_cast<const char*>(a.x[r.rank]) + uint64_t(r.lo) * pitch + m0 * es;
+        const char* d = dz_row<T>(a, r, 0) + n0 * es;
+        f32x4 acc[S::MI][S::NI];
+        if constexpr (PATH == kLoose) {
+            loose_tile<DT, S, kCols, kCols>(LooseCols{x, r.count, pitch, pitch - m0 * es}, LooseCols{d, r.count, a.zpitch, (wide - n0) * es}, steps, acc);
+        } else {
+            matrix_tile<DT, S, kCols, kCols>(ColOperand<KR, 1>{x, r.count, pitch, m0 * es, 0}, ColOperand<KR, 1>{d, r.count, a.zpitch, n0 * es, 0}, 0, steps, acc);
+        }
+        T* out = static_cast<T*>(a.dweight[r.rank]) + uint64_t(r.run) * wide * a.cols;
+        const bool quads = a.col_quads;
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) {
+            const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
+            if (n >= wide) continue;
+#pragma unroll
+            for (int i = 0; i < S::MI; i++) {
+                const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
+                if (m >= a.cols) continue;
+                store_four<DT>(out + uint64_t(n) * a.cols + m, acc[i][j], quads, a.cols - m);
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------------------- host --
+uint64_t ceil_div(uint64_t n, uint64_t by) { return (n + by - 1) / by; }
+
+typedef Shape<256, 256, 2, 4> Wide;
+typedef Shape<128, 128, 2, 2> Square;
+typedef Shape<64, 64, 2, 2> Small;
+typedef Shape<64, 16, 1, 1> Tiny;
+enum Tile { kWide, kSquare, kSmall, kTiny };
+constexpr uint32_t kTileM[] = {256, 128, 64, 64}, kTileN[] = {256, 128, 64, 16};
+constexpr uint32_t kTilesPerCu[] = {1, 2, 4, 7};   // workgroups of a tile's LDS that share a CU
+
+// The tile for products of m features with runs of `mean` rows each.
+Tile pick_tile(int dtype, uint64_t m, uint64_t mean, uint64_t groups, int path) {
+    if (mean <= 16) return kTiny;
+    auto tiles = [&](uint64_t by) { return ceil_div(m, by) * ceil_div(mean, by) * groups; };
+    if (path == kLoose || dtype == kF32) return tiles(128) >= 1024 ? kSquare : kSmall;
+    if (mean > 128 && tiles(256) >= 224) return kWide;
+    return mean > 64 && tiles(128) >= 192 ? kSquare : kSmall;
+}
+template <int DT, int PATH, typename F>
+void with_tile(Tile t, F&& launch) {
+    if constexpr (DT == kBF16 && PATH != kLoose) {
+        if (t == kWide) return launch(Wide());
+    }
+    if (t == kSquare) launch(Square());
+    else if (t == kTiny) launch(Tiny());
+    else launch(Small());
+}
+template <typename F>
+void with_path(int path, F&& launch) {
+    if (path == kWhole) launch(std::integral_constant<int, kWhole>());
+    else if (path == kTail) launch(std::integral_constant<int, kTail>());
+    else launch(std::integral_constant<int, kLoose>());
+}
+// Workgroups that walk over at most `tiles` tiles: as many as run at a time.
+uint32_t walkers(uint64_t tiles, Tile t) {
+    const uint64_t most = 256 * kTilesPerCu[t];
+    return uint32_t(tiles < 1 ? 1 : tiles < most ? tiles : most);
+}
+
+bool on(const void* const* list, int n, uintptr_t boundary) {
+    for (int r = 0; r < n; r++)
+        if (reinterpret_cast<uintptr_t>(list[r]) % boundary != 0) return false;
+    return true;
+}
+int path_of(uint64_t pitch, bool on4) { return !on4 || pitch % 4 != 0 ? kLoose : pitch % 16 != 0 ? kTail : kWhole; }
+
+template <int DT>
+hipError_t forward(LinearArgs a, hipStream_t s) {
+    constexpr uint64_t es = sizeof(typename Elem<DT>::type);
+    const uint64_t rows = a.rows.start[a.nranks], groups = uint64_t(a.runs) * a.nranks;
+    a.quads = a.outs % 4 == 0 && on(a.bias, a.nranks, 4 * es) && on(a.residual, a.nranks, 4 * es) && on(a.y, a.nranks, 4 * es) && on(a.pre, a.nranks, 4 * es);
+    const uint64_t features = uint64_t(a.outs) * (a.gated ? 2 : 1);
+    with_path(path_of(a.cols * es, on(a.x, a.nranks, 4) && on(a.weight, a.nranks, 4)), [&](auto path) {
+        constexpr int P = decltype(path)::value;
+        const Tile t = pick_tile(DT, features, ceil_div(rows, groups), groups, P);
+        // a run ends inside a tile, so there are up to one tile more than its rows fill
+        const uint64_t tiles = ceil_div(features, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
+        with_tile<DT, P>(t, [&](auto shape) {
+            typedef decltype(shape) S;
+            if (a.gated) hipLaunchKernelGGL((k_linear<DT, S, P, true>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
+            else hipLaunchKernelGGL((k_linear<DT, S, P, false>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
+        });
+    });
+    return hipGetLastError();
+}
+
+uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
+uint64_t dz_tiles(const RowTable& rows, int nranks, uint32_t runs) {
+    const uint64_t n = rows.start[nranks], groups = uint64_t(runs) * nranks;
+    return n / kDzRows + (groups < n ? groups : n);
+}
+struct BackwardParts {
+    uint64_t dz, partial, bytes;
+};
+BackwardParts backward_parts(const RowTable& rows, int nranks, uint32_t runs, uint64_t wide, bool need_dz, bool dbias, int dtype) {
+    const uint64_t es = dtype == kBF16 ? 2 : 4;
+    BackwardParts b;
+    b.dz = 0;
+    b.partial = need_dz ? up(rows.start[nranks] * up(wide * es, 16), 256) : 0;
+    b.bytes = b.partial + (dbias ? up(dz_tiles(rows, nranks, runs) * wide * 4, 256) : 0);
+    return b;
+}
+
+template <int DT>
+hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
+    constexpr uint64_t es = sizeof(typename Elem<DT>::type);
+    const uint64_t rows = a.rows.start[a.nranks], groups = uint64_t(a.runs) * a.nranks, wide = uint64_t(a.outs) * (a.gated ? 2 : 1);
+    const bool dbias = a.dbias[0] != nullptr;
+    const BackwardParts b = backward_parts(a.rows, a.nranks, a.runs, wide, a.need_dz, dbias, DT);
+    a.dz = workspace + b.dz;
+    a.zpitch = uint32_t(a.need_dz ? up(wide * es, 16) : wide * es);
+    a.partial = dbias ? reinterpret_cast<float*>(workspace + b.partial) : nullptr;
+    a.quads = a.outs % 4 == 0 && on(a.dy, a.nranks, 4 * es) && (!a.need_dz || on(a.saved, a.nranks, 4 * es));
+    a.col_quads = a.cols % 4 == 0 && on(a.dx, a.nranks, 4 * es) && on(a.dweight, a.nranks, 4 * es);
+    if (rows > 0 && (a.need_dz || dbias)) {
+        const uint64_t tiles = dz_tiles(a.rows, a.nranks, a.runs), across = ceil_div(a.outs, 4 * kThreads), most = ceil_div(4096, across);
+        const dim3 grid(uint32_t(across), uint32_t(tiles < most ? tiles : most));
+        if (a.gated) hipLaunchKernelGGL((k_linear_dz<DT, true>), grid, dim3(kThreads), 0, s, a);
+        else hipLaunchKernelGGL((k_linear_dz<DT, false>), grid, dim3(kThreads), 0, s, a);
+    }
+    if (dbias) hipLaunchKernelGGL(k_linear_dbias<DT>, dim3(uint32_t(ceil_div(wide, kThreads)), uint32_t(groups)), dim3(kThreads), 0, s, a);
+    const bool dz4 = a.need_dz || on(a.dy, a.nranks, 4), x4 = on(a.x, a.nranks, 4), w4 = on(a.weight, a.nranks, 4);
+    if (rows > 0) {
+        // dx: only dz' rows can end inside 16 bytes that count
+        const int zp = path_of(a.zpitch, dz4), wp = path_of(a.cols * es, w4);
+        with_path(zp == kLoose || wp == kLoose ? kLoose : zp, [&](auto path) {
+            constexpr int P = decltype(path)::value;
+            const Tile t = pick_tile(DT, a.cols, ceil_div(rows, groups), groups, P);
+            const uint64_t tiles = ceil_div(a.cols, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
+            with_tile<DT, P>(t, [&](auto shape) {
+                typedef decltype(shape) S;
+                hipLaunchKernelGGL((k_linear_dx<DT, S, P>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
+            });
+        });
+    }
+    const bool loose = path_of(a.zpitch, dz4) == kLoose || path_of(a.cols * es, x4) == kLoose;
+    auto dweight = [&](auto path) {
+        constexpr int P = decltype(path)::value;
+        const Tile t = pick_tile(DT, a.cols, wide < 17 ? 17 : wide, groups, P);
+        with_tile<DT, P>(t, [&](auto shape) {
+            typedef decltype(shape) S;
+            if constexpr (!std::is_same<S, Tiny>::value)
+                hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, kTileM[t]) * ceil_div(wide, kTileN[t]) * groups, t)),
+                                   dim3(S::threads), 0, s, a);
+        });
+    };
+    if (loose) dweight(std::integral_constant<int, kLoose>());
+    else dweight(std::integral_constant<int, kWhole>());
+    return hipGetLastError();
+}
+
+}  // namespace
+
+uint64_t linear_backward_workspace(const RowTable& rows, int nranks, uint32_t runs, uint64_t outs, int act, int gated, bool dbias, int dtype) {
+    return backward_parts(rows, nranks, runs, outs * (gated ? 2 : 1), gated || act != DT_ACT_NONE, dbias, dtype).bytes;
+}
+hipError_t launch_linear(const LinearArgs& a, int dtype, hipStream_t s) { return dtype == kBF16 ? forward<kBF16>(a, s) : forward<kF32>(a, s); }
+hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, int dtype, hipStream_t s) {
+    char* ws = static_cast<char*>(workspace);
+    return dtype == kBF16 ? backward<kBF16>(a, ws, s) : backward<kF32>(a, ws, s);
+}
+
+}  // namespace dt

@@ -1,6 +1,6 @@
 // step_api.cpp -- the C ABI of the model-step operators of include/dt.h:
 // argument checks, row tables and workspace sizes.  The arithmetic is in
-// norm.hip, moe.hip and loss.hip; nothing here allocates or throws.
+// norm.hip, moe.hip, loss.hip and linear.hip; nothing here allocates or throws.
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -11,6 +11,7 @@
 
 static_assert(sizeof(dt::NormBackArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::ExchangeRowsArgs) <= 4096, "kernel arguments must stay below 4 KiB");
+static_assert(sizeof(dt::LinearArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 
 namespace {
 
@@ -587,6 +588,118 @@ dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* w
     a.workspace = static_cast<char*>(workspace);
     a.nranks = nranks;
     return done(dt::launch_loss_backward(a, dtype, stream), "vocab_loss_backward");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------- matrix products --
+namespace {
+
+dt_status check_act(dt_act act) {
+    if (act < DT_ACT_NONE || act > DT_ACT_SILU) return fail(DT_ERR_ARG, "bad act %d", int(act));
+    return DT_OK;
+}
+
+dt_status linear_shape(int nranks, const size_t* rows, int runs, size_t cols, size_t outs, dt_act act, int gated, dt_dtype dtype,
+                       const char* what, dt::LinearArgs& a) {
+    TRY(check_ranks(nranks));
+    TRY(check_float(dtype, what));
+    TRY(row_table(rows, nranks, "rows", a.rows));
+    TRY(check_cols(cols, what));
+    if (outs < 1 || outs > DT_MAX_STEP_COLS) return fail(DT_ERR_ARG, "%s: outs=%zu outside [1, %d]", what, outs, DT_MAX_STEP_COLS);
+    TRY(check_act(act));
+    if (runs < 1 || runs > DT_MAX_EXPERTS / nranks)
+        return fail(DT_ERR_ARG, "%s: runs=%d outside [1, %d / nranks]", what, runs, DT_MAX_EXPERTS);
+    if (uint64_t(outs) * (gated ? 2 : 1) * cols * esize_of(dtype) >= uint64_t(1) << 31)
+        return fail(DT_ERR_ARG, "%s: a weight of 2 GiB or more", what);
+    a.runs = uint32_t(runs);
+    a.cols = uint32_t(cols);
+    a.outs = uint32_t(outs);
+    a.act = act;
+    a.gated = gated != 0;
+    a.need_dz = a.gated || act != DT_ACT_NONE;
+    a.nranks = nranks;
+    return DT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dt_status dt_linear(const void* const* x, const void* const* weight, const void* const* bias, const void* const* residual,
+                    const int32_t* const* offsets, void* const* y, void* const* pre, int nranks, const size_t* rows,
+                    int runs, size_t cols, size_t outs, dt_act act, int gated, dt_dtype dtype, hipStream_t stream) {
+    dt::report_error(DT_OK, "");
+    dt::LinearArgs a = {};
+    TRY(linear_shape(nranks, rows, runs, cols, outs, act, gated, dtype, "linear", a));
+    if (offsets == nullptr && runs != 1) return fail(DT_ERR_ARG, "linear: %d runs need offsets", runs);
+    const size_t es = esize_of(dtype), wide = outs * (a.gated ? 2 : 1);
+    Ranges g;
+    for (int r = 0; r < nranks; r++) {
+        if (rows[r] == 0) continue;
+        g.add(x, r, rows[r] * cols * es, es, false, "x");
+        g.add(weight, r, runs * wide * cols * es, es, false, "weight");
+        if (bias != nullptr) g.add(bias, r, runs * wide * es, es, false, "bias");
+        if (residual != nullptr) g.add(residual, r, rows[r] * outs * es, es, false, "residual");
+        if (offsets != nullptr) g.add(offsets, r, (runs + 1) * sizeof(int32_t), sizeof(int32_t), false, "offsets");
+        g.add(y, r, rows[r] * outs * es, es, true, "y");
+        if (pre != nullptr) g.add(pre, r, rows[r] * wide * es, es, true, "pre");
+    }
+    TRY(g.check("linear"));
+    if (a.rows.start[nranks] == 0) return DT_OK;
+    copy_list(a.x, x, nranks);
+    copy_list(a.weight, weight, nranks);
+    copy_list(a.bias, bias, nranks);
+    copy_list(a.residual, residual, nranks);
+    copy_list(a.offsets, offsets, nranks);
+    copy_list(a.y, y, nranks);
+    copy_list(a.pre, pre, nranks);
+    return done(dt::launch_linear(a, dtype, stream), "linear");
+}
+
+size_t dt_linear_backward_workspace(int nranks, const size_t* rows, int runs, size_t outs, dt_act act, int gated, int with_dbias,
+                                    dt_dtype dtype) {
+    dt::LinearArgs a = {};
+    dt::report_error(DT_OK, "");
+    if (linear_shape(nranks, rows, runs, 1, outs, act, gated, dtype, "linear_backward_workspace", a) != DT_OK) return 0;
+    return dt::linear_backward_workspace(a.rows, nranks, a.runs, outs, act, a.gated, with_dbias != 0, dtype);
+}
+
+dt_status dt_linear_backward(const void* const* dy, const void* const* x, const void* const* weight, const void* const* pre,
+                             const int32_t* const* offsets, void* const* dx, void* const* dweight, void* const* dbias,
+                             int nranks, const size_t* rows, int runs, size_t cols, size_t outs, dt_act act, int gated,
+                             dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    dt::report_error(DT_OK, "");
+    dt::LinearArgs a = {};
+    TRY(linear_shape(nranks, rows, runs, cols, outs, act, gated, dtype, "linear_backward", a));
+    if (offsets == nullptr && runs != 1) return fail(DT_ERR_ARG, "linear_backward: %d runs need offsets", runs);
+    const size_t es = esize_of(dtype), wide = outs * (a.gated ? 2 : 1);
+    const size_t need = dt::linear_backward_workspace(a.rows, nranks, a.runs, outs, act, a.gated, dbias != nullptr, dtype);
+    TRY(check_workspace(workspace, workspace_bytes, need, "linear_backward"));
+    Ranges g;
+    for (int r = 0; r < nranks; r++) {
+        if (rows[r] > 0) {
+            g.add(dy, r, rows[r] * outs * es, es, false, "dy");
+            g.add(x, r, rows[r] * cols * es, es, false, "x");
+            g.add(weight, r, runs * wide * cols * es, es, false, "weight");
+            if (a.need_dz) g.add(pre, r, rows[r] * wide * es, es, false, "pre");
+            if (offsets != nullptr) g.add(offsets, r, (runs + 1) * sizeof(int32_t), sizeof(int32_t), false, "offsets");
+            g.add(dx, r, rows[r] * cols * es, es, true, "dx");
+        }
+        g.add(dweight, r, runs * wide * cols * es, es, true, "dweight");
+        if (dbias != nullptr) g.add(dbias, r, runs * wide * es, es, true, "dbias");
+    }
+    g.add(&workspace, 0, need, 1, true, "workspace");
+    TRY(g.check("linear_backward"));
+    copy_list(a.dy, dy, nranks);
+    copy_list(a.x, x, nranks);
+    copy_list(a.weight, weight, nranks);
+    if (a.need_dz) copy_list(a.saved, pre, nranks);
+    copy_list(a.offsets, offsets, nranks);
+    copy_list(a.dx, dx, nranks);
+    copy_list(a.dweight, dweight, nranks);
+    copy_list(a.dbias, dbias, nranks);
+    return done(dt::launch_linear_backward(a, workspace, dtype, stream), "linear_backward");
 }
 
 }  // extern "C"

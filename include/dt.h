@@ -393,6 +393,37 @@ dt_status dt_vocab_loss_backward(const void* const* hidden, const void* const* w
                                  int64_t ignore_index, size_t piece_rows, dt_dtype dtype, void* workspace,
                                  size_t workspace_bytes, hipStream_t stream);
 
+/* Matrix products of every rank's rows, with bias, activation and residual: the
+ * experts' products between dt_moe_dispatch and dt_moe_combine, or a dense layer.
+ * Rank q's x[q] [rows[q], cols] falls into `runs` runs of rows: offsets[q]
+ * [runs + 1] int32, on the device and not decreasing, gives each run's first row
+ * and the end, as dt_moe_dispatch leaves them (values outside [0, rows[q]] are
+ * cut to it).  offsets NULL: runs is 1 and the run is all rows.  Run e meets
+ * weight[q][e] [outs, cols] and bias[q][e] [outs] (bias NULL: none):
+ *   z = weight x + bias,   y = residual + act(z)      (residual NULL: none)
+ * or, gated, weight[q][e] [2 outs, cols] and bias[q][e] [2 outs]:
+ *   z = [g; u],            y = residual + act(g) * u
+ * y[q], residual[q] [rows[q], outs]; pre[q] [rows[q], outs, gated 2 outs] keeps z
+ * for the backward pass (NULL: not kept).  Rows outside the runs are left as they
+ * were.  At most DT_MAX_EXPERTS runs over all ranks; a run's weight is below 2 GiB. */
+typedef enum { DT_ACT_NONE = 0, DT_ACT_RELU = 1, DT_ACT_GELU = 2 /* z Phi(z) */, DT_ACT_SILU = 3 /* z / (1 + exp(-z)) */ } dt_act;
+dt_status dt_linear(const void* const* x, const void* const* weight, const void* const* bias, const void* const* residual,
+                    const int32_t* const* offsets, void* const* y, void* const* pre, int nranks, const size_t* rows,
+                    int runs, size_t cols, size_t outs, dt_act act, int gated, dt_dtype dtype, hipStream_t stream);
+
+/* Its gradients for dy[q] [rows[q], outs]: dx[q] [rows[q], cols] (rows outside the
+ * runs are left as they were), dweight[q] like weight[q] and dbias[q] like bias[q]
+ * (NULL: not formed), zeros for a run without rows.  residual's is dy itself.  pre:
+ * the forward pass's z, read unless act is DT_ACT_NONE and the product is not
+ * gated (may be NULL then).  For bf16 tensors z's gradient is rounded to bf16 before
+ * it enters the two products. */
+size_t dt_linear_backward_workspace(int nranks, const size_t* rows, int runs, size_t outs, dt_act act, int gated, int with_dbias,
+                                    dt_dtype dtype);
+dt_status dt_linear_backward(const void* const* dy, const void* const* x, const void* const* weight, const void* const* pre,
+                             const int32_t* const* offsets, void* const* dx, void* const* dweight, void* const* dbias,
+                             int nranks, const size_t* rows, int runs, size_t cols, size_t outs, dt_act act, int gated,
+                             dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ---- host planning (no GPU work) -------------------------------------- */
 
 /* One contiguous part of one tensor inside one bucket. */

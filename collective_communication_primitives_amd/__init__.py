@@ -1080,6 +1080,45 @@ def dt_linear_backward(dy: Sequence[torch.Tensor], x: Sequence[torch.Tensor], we
     return w if async_op else dx
 
 
+def dt_moe_layer_workspace(tokens: Sequence[int], cols: int, inner: int, nexperts: int, topk: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace dt_moe_layer takes."""
+    return _sized(_L.dt_moe_layer_workspace(len(tokens), _size_array(tokens), cols, inner, nexperts, topk, _DTYPES[dtype]))
+
+
+def dt_moe_layer(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], weights: Sequence[torch.Tensor],
+                 w_in: Sequence[torch.Tensor], w_out: Sequence[torch.Tensor], out: Sequence[torch.Tensor],
+                 b_in: Optional[Sequence[torch.Tensor]] = None, b_out: Optional[Sequence[torch.Tensor]] = None,
+                 residual: Optional[Sequence[torch.Tensor]] = None, act="silu", gated: bool = True,
+                 workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False, comm_stream=None):
+    """The experts' layer for up to 256 tokens over all ranks, in two launches: out[r] = residual[r] + the sum over a token's
+    slots of weights * (w_out act(w_in x + b_in) + b_out) of its experts.  x[r], out[r] [tokens, cols]; experts[r], weights[r]
+    [tokens, topk] from dt_moe_route; w_in[q] [E / P, inner (gated: 2 * inner), cols], w_out[q] [E / P, cols, inner] of the
+    experts that rank q owns."""
+    dev, stash = torch.cuda.current_device(), []
+    p, cols, k = _ranks(x, "x"), _width(x[0], "x"), _width(experts[0], "experts")
+    code, dtype = _float_dtype(x[0]), x[0].dtype
+    if w_out[0].dim() != 3 or w_out[0].shape[1] != cols:
+        raise ValueError(f"w_out[q] must be [experts of a rank, {cols}, inner]")
+    per, _, inner = w_out[0].shape
+    wide = inner * (2 if gated else 1)
+    if tuple(w_in[0].shape) != (per, wide, cols):
+        raise ValueError(f"w_in[q] must be [{per}, {wide}, {cols}]")
+    e = per * p
+    sizes, rows, slots, n = _row_counts(x, cols, "x", k)
+    xs, outs = _buffers("x", x, sizes, dtype, dev, stash), _buffers("out", out, sizes, dtype, dev, stash)
+    es, gs = _buffers("experts", experts, slots, torch.int32, dev, stash), _buffers("weights", weights, slots, torch.float32, dev, stash)
+    wi, wo = _buffers("w_in", w_in, [per * wide * cols] * p, dtype, dev, stash), _buffers("w_out", w_out, [per * cols * inner] * p, dtype, dev, stash)
+    bi = _buffers("b_in", b_in, [per * wide] * p, dtype, dev, stash) if b_in is not None else None
+    bo = _buffers("b_out", b_out, [per * cols] * p, dtype, dev, stash) if b_out is not None else None
+    rs = _buffers("residual", residual, sizes, dtype, dev, stash) if residual is not None else None
+    ac, gt = _act_code(act), int(bool(gated))
+    space = _workspace(workspace, _sized(_L.dt_moe_layer_workspace(p, n, cols, inner, e, k, code)), dev, stream, async_op, comm_stream, stash)
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_moe_layer(xs, es, gs, wi, bi, wo, bo, rs, outs, p, n, cols, inner, e, k, ac, gt, code, at, have, st), stash,
+                async_op, stream, comm_stream)
+    return w if async_op else out
+
+
 __all__ = [
     "dt_allreduce", "dt_reduce_scatter", "dt_all_gather", "dt_all_to_all", "dt_bucket_allreduce", "dt_bucket_plan",
     "dt_all_gather_into_vec", "dt_broadcast", "dt_replicate_to_shard", "dt_all_to_all_dims",
@@ -1089,4 +1128,5 @@ __all__ = [
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
     "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
+    "dt_moe_layer", "dt_moe_layer_workspace",
 ]

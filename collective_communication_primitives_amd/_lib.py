@@ -23,6 +23,7 @@ EXPORTS = (
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
     "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
+    "dt_moe_layer", "dt_moe_layer_workspace",
 )
 
 
@@ -78,6 +79,8 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
         "dt_linear": [vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, sz, sz, i32, i32, i32, vp],
         "dt_linear_backward": [vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, sz, sz, i32, i32, i32, vp, sz, vp],
         "dt_linear_backward_workspace": [i32, vp, i32, sz, i32, i32, i32, i32],
+        "dt_moe_layer": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, sz, i32, i32, i32, i32, i32, vp, sz, vp],
+        "dt_moe_layer_workspace": [i32, vp, sz, sz, i32, i32, i32],
         "dt_status_string": [i32],
         "dt_last_error": [],
         "dt_version": [],

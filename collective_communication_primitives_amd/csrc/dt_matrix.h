@@ -281,6 +281,23 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     arrive<0, 0>();  // nothing is on its way into LDS when the workgroup ends
 }
 
+// 16 bytes at byte `at` of a row of `bytes` bytes that starts and ends at any
+// element: zeros behind the row's end, where nothing is read.
+template <int ES>
+__device__ __forceinline__ u32x4 read_loose(const char* row, uint32_t at, uint32_t bytes) {
+    u32x4 x = {0, 0, 0, 0};
+    if (at + 16 <= bytes) {
+        x = *reinterpret_cast<const typename Loose<ES>::type*>(row + at);
+    } else if (at < bytes) {
+        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
+        T t[16 / ES];
+#pragma unroll
+        for (int e = 0; e < 16 / ES; e++) t[e] = at + e * ES < bytes ? *reinterpret_cast<const T*>(row + at + e * ES) : T(0);
+        __builtin_memcpy(&x, t, 16);
+    }
+    return x;
+}
+
 // Tile `id` of mt x nt in an order that keeps an XCD's workgroups on
 // neighbouring tiles: ids go round the 8 XCDs, so each XCD gets a run of the
 // tiles, walked in bands of 8 rows of tiles.

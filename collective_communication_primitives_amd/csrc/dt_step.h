@@ -167,4 +167,29 @@ uint64_t linear_backward_workspace(const RowTable& rows, int nranks, uint32_t ru
 hipError_t launch_linear(const LinearArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, int dtype, hipStream_t s);
 
+// ------------------------------------------------------ the experts' layer --
+// For few tokens: two launches.  Tokens are numbered over all ranks; a slot is
+// one (token, choice).
+constexpr uint32_t kLayerHeader = 64;       // ints of the table before its rows: [0] experts in use, then nothing
+struct LayerArgs {
+    const void* x[kMaxRanksHost];           // [tokens, cols]
+    const int32_t* experts[kMaxRanksHost];  // [tokens, topk]
+    const float* weights[kMaxRanksHost];
+    const void* w_in[kMaxRanksHost];        // [per_rank, inner (gated: twice), cols]
+    const void* b_in[kMaxRanksHost];        // all NULL: none
+    const void* w_out[kMaxRanksHost];       // [per_rank, cols, inner]
+    const void* b_out[kMaxRanksHost];
+    const void* residual[kMaxRanksHost];
+    void* out[kMaxRanksHost];
+    char* hidden;                           // [slots] rows of hpitch bytes; bf16: a second part hpart bytes behind
+    int32_t* table;                         // header, experts in use [used], their tokens' slots [used][tpad]
+    RowTable rows;
+    uint32_t cols, inner, nexperts, per_rank, topk, tokens;
+    uint32_t hpitch, used, tpad;            // used: the most experts that can be in use
+    uint64_t hpart;
+    int act, gated, nranks;
+};
+uint64_t layer_workspace(uint64_t tokens, uint64_t cols, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype);
+hipError_t launch_layer(LayerArgs a, void* workspace, int dtype, hipStream_t s);
+
 }  // namespace dt

@@ -88,20 +88,6 @@ struct GatedOperand : RowOperand<TAIL> {
 
 // Operands whose rows start at any element: read at that alignment into
 // registers and put into LDS in the order that the direct loads leave there.
-template <int ES>
-__device__ __forceinline__ u32x4 read_loose(const char* row, uint32_t at, uint32_t bytes) {
-    u32x4 x = {0, 0, 0, 0};
-    if (at + 16 <= bytes) {
-        x = *reinterpret_cast<const typename Loose<ES>::type*>(row + at);
-    } else if (at < bytes) {
-        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
-        T t[16 / ES];
-#pragma unroll
-        for (int e = 0; e < 16 / ES; e++) t[e] = at + e * ES < bytes ? *reinterpret_cast<const T*>(row + at + e * ES) : T(0);
-        __builtin_memcpy(&x, t, 16);
-    }
-    return x;
-}
 struct LooseRows {
     const char* p;      // the tile's first row
     uint32_t rows, pitch;

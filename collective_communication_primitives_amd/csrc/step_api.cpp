@@ -1,6 +1,6 @@
 // step_api.cpp -- the C ABI of the model-step operators of include/dt.h:
 // argument checks, row tables and workspace sizes.  The arithmetic is in
-// norm.hip, moe.hip, loss.hip and linear.hip; nothing here allocates or throws.
+// norm.hip, moe.hip, loss.hip, linear.hip and layer.hip; nothing here allocates or throws.
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -12,6 +12,7 @@
 static_assert(sizeof(dt::NormBackArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::ExchangeRowsArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::LinearArgs) <= 4096, "kernel arguments must stay below 4 KiB");
+static_assert(sizeof(dt::LayerArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 
 namespace {
 
@@ -700,6 +701,88 @@ dt_status dt_linear_backward(const void* const* dy, const void* const* x, const 
     copy_list(a.dweight, dweight, nranks);
     copy_list(a.dbias, dbias, nranks);
     return done(dt::launch_linear_backward(a, workspace, dtype, stream), "linear_backward");
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------- the experts' layer --
+namespace {
+
+dt_status layer_shape(int nranks, const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk, dt_dtype dtype,
+                      const char* what, RowTable& t) {
+    TRY(check_ranks(nranks));
+    TRY(check_float(dtype, what));
+    TRY(row_table(tokens, nranks, "tokens", t));
+    if (t.start[nranks] > DT_MAX_LAYER_TOKENS)
+        return fail(DT_ERR_ARG, "%s: tokens: %u in all, above %d", what, t.start[nranks], DT_MAX_LAYER_TOKENS);
+    TRY(check_cols(cols, what));
+    if (inner < 1 || inner > DT_MAX_STEP_COLS) return fail(DT_ERR_ARG, "%s: inner=%zu outside [1, %d]", what, inner, DT_MAX_STEP_COLS);
+    TRY(check_experts(nexperts, topk));
+    if (nexperts % nranks != 0) return fail(DT_ERR_ARG, "%s: %d experts do not divide by %d ranks", what, nexperts, nranks);
+    if (2 * uint64_t(inner) * cols * esize_of(dtype) >= uint64_t(1) << 32) return fail(DT_ERR_ARG, "%s: an expert's weight of 2 GiB or more", what);
+    return DT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dt_moe_layer_workspace(int nranks, const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk,
+                              dt_dtype dtype) {
+    RowTable t;
+    dt::report_error(DT_OK, "");
+    if (layer_shape(nranks, tokens, cols, inner, nexperts, topk, dtype, "moe_layer_workspace", t) != DT_OK) return 0;
+    return dt::layer_workspace(t.start[nranks], cols, inner, uint32_t(nexperts), uint32_t(topk), dtype);
+}
+
+dt_status dt_moe_layer(const void* const* x, const int32_t* const* experts, const float* const* weights,
+                       const void* const* w_in, const void* const* b_in, const void* const* w_out,
+                       const void* const* b_out, const void* const* residual, void* const* out, int nranks,
+                       const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk, dt_act act, int gated,
+                       dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    dt::report_error(DT_OK, "");
+    dt::LayerArgs a = {};
+    TRY(layer_shape(nranks, tokens, cols, inner, nexperts, topk, dtype, "moe_layer", a.rows));
+    TRY(check_act(act));
+    const size_t es = esize_of(dtype), wide = inner * (gated ? 2 : 1), per = size_t(nexperts / nranks);
+    const uint32_t total = a.rows.start[nranks];
+    if (total == 0) return DT_OK;
+    const size_t need = dt::layer_workspace(total, cols, inner, uint32_t(nexperts), uint32_t(topk), dtype);
+    TRY(check_workspace(workspace, workspace_bytes, need, "moe_layer"));
+    Ranges g;
+    for (int r = 0; r < nranks; r++) {
+        const size_t n = tokens[r] * cols * es;
+        g.add(x, r, n, es, false, "x");
+        g.add(experts, r, tokens[r] * topk * sizeof(int32_t), sizeof(int32_t), false, "experts");
+        g.add(weights, r, tokens[r] * topk * sizeof(float), sizeof(float), false, "weights");
+        g.add(w_in, r, per * wide * cols * es, es, false, "w_in");
+        if (b_in != nullptr) g.add(b_in, r, per * wide * es, es, false, "b_in");
+        g.add(w_out, r, per * inner * cols * es, es, false, "w_out");
+        if (b_out != nullptr) g.add(b_out, r, per * cols * es, es, false, "b_out");
+        if (residual != nullptr) g.add(residual, r, n, es, false, "residual");
+        g.add(out, r, n, es, true, "out");
+    }
+    g.add(&workspace, 0, need, 1, true, "workspace");
+    TRY(g.check("moe_layer"));
+    copy_list(a.x, x, nranks);
+    copy_list(a.experts, experts, nranks);
+    copy_list(a.weights, weights, nranks);
+    copy_list(a.w_in, w_in, nranks);
+    copy_list(a.b_in, b_in, nranks);
+    copy_list(a.w_out, w_out, nranks);
+    copy_list(a.b_out, b_out, nranks);
+    copy_list(a.residual, residual, nranks);
+    copy_list(a.out, out, nranks);
+    a.cols = uint32_t(cols);
+    a.inner = uint32_t(inner);
+    a.nexperts = uint32_t(nexperts);
+    a.per_rank = uint32_t(per);
+    a.topk = uint32_t(topk);
+    a.tokens = total;
+    a.act = act;
+    a.gated = gated != 0;
+    a.nranks = nranks;
+    return done(dt::launch_layer(a, workspace, dtype, stream), "moe_layer");
 }
 
 }  // extern "C"

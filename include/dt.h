@@ -280,6 +280,7 @@ dt_status dt_barrier_exchange(const void* const* src, void* const* stage, void* 
 #define DT_MAX_TOPK 64
 #define DT_MAX_GROUPS 64
 #define DT_MAX_LOSS_TOKENS (1 << 22)
+#define DT_MAX_LAYER_TOKENS 256 /* of all ranks together, in dt_moe_layer */
 
 /* Layer norm of rows that are Shard(0) over the ranks: rank r holds x[r]
  * [rows[r], cols], and weight[r], bias[r] [cols] (bias NULL: none).  Per row
@@ -423,6 +424,27 @@ dt_status dt_linear_backward(const void* const* dy, const void* const* x, const 
                              const int32_t* const* offsets, void* const* dx, void* const* dweight, void* const* dbias,
                              int nranks, const size_t* rows, int runs, size_t cols, size_t outs, dt_act act, int gated,
                              dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The experts' layer for few tokens (at most DT_MAX_LAYER_TOKENS over all ranks),
+ * what dt_moe_dispatch, two dt_linear and dt_moe_combine do, in two launches that
+ * read each chosen expert's weights once:
+ *   out[r][t] = residual[r][t] + sum over the slots j of weights[r][t,j] *
+ *               (w_out_e act(w_in_e x[r][t] + b_in_e) + b_out_e),   e = experts[r][t,j]
+ * with experts and weights as dt_moe_route leaves them (an expert outside [0, E)
+ * adds nothing; the same one twice counts twice).  Rank q owns experts [q*E/P,
+ * (q+1)*E/P): w_in[q] [E/P, inner, cols] (gated: [E/P, 2 inner, cols], act of the
+ * first half's products times the second half's), b_in[q] [E/P, inner or 2 inner],
+ * w_out[q] [E/P, cols, inner], b_out[q] [E/P, cols] (biases and residual NULL:
+ * none).  out[r], residual[r], x[r] [tokens[r], cols].  What lies between the two
+ * products is kept in fp32, or for bf16 tensors in two bf16 parts.  An expert's
+ * w_in and w_out are below 2 GiB each. */
+size_t dt_moe_layer_workspace(int nranks, const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk,
+                              dt_dtype dtype);
+dt_status dt_moe_layer(const void* const* x, const int32_t* const* experts, const float* const* weights,
+                       const void* const* w_in, const void* const* b_in, const void* const* w_out,
+                       const void* const* b_out, const void* const* residual, void* const* out, int nranks,
+                       const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk, dt_act act, int gated,
+                       dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---- host planning (no GPU work) -------------------------------------- */
 

@@ -111,3 +111,37 @@ def linear_backward(dy, x, w, z, kind, gated):
     edw = rounded.t() @ x.abs() + (rows + 8) * U * (dz.abs().t() @ x.abs())
     edb = ed.sum(0) + (rows + 16) * U * dz.abs().sum(0)
     return (dx, dw, db), (edx, edw, edb)
+
+
+# -------------------------------------------------------- the experts' layer --
+def layer(x, experts, weights, w_in, w_out, b_in, b_out, residual, kind, gated):
+    """All tokens [T, cols] with experts, weights [T, topk] and all experts' weights [E, ...]: (out, error bound).
+
+    Between the products a value is kept in fp32, or for bf16 in two parts: off by half a step of half a step."""
+    dtype = x.dtype
+    t, k = experts.shape
+    out = residual.double().clone() if residual is not None else torch.zeros(x.shape, dtype=torch.float64, device=x.device)
+    err, size = torch.zeros_like(out), out.abs()
+    kept = half_step(dtype) ** 2 if dtype == torch.bfloat16 else U
+    for e in range(w_in.shape[0]):
+        hit = experts == e
+        tok = hit.any(1).nonzero()[:, 0]
+        if tok.numel() == 0:
+            continue
+        w = torch.where(hit, weights.double(), 0.0).sum(1)[tok][:, None]
+        aw = torch.where(hit, weights.double().abs(), 0.0).sum(1)[tok][:, None] * (1 + k * U)
+        (h, _), (eh, _) = linear(x[tok], w_in[e], b_in[e] if b_in is not None else None, None, kind, gated)
+        eh = aw * eh + (k + 2) * U * aw * h.abs()
+        h = h * w
+        eh = eh + kept * (h.abs() + eh)
+        w2 = w_out[e].double()
+        y = h @ w2.t()
+        out[tok] += y
+        err[tok] += eh @ w2.abs().t()
+        mag = h.abs() @ w2.abs().t()
+        if b_out is not None:
+            out[tok] += w * b_out[e].double()
+            mag = mag + aw * b_out[e].double().abs()
+        size[tok] += mag
+    n = k * (w_out.shape[2] + 2) + 8 + 16
+    return out, err + n * U * size

@@ -1119,6 +1119,79 @@ def dt_moe_layer(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], wei
     return w if async_op else out
 
 
+def dt_block_norm_workspace(rows: Sequence[int], cols: int, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace dt_block_norm_backward takes for rows[r] rows of ``cols`` per rank."""
+    return _sized(_L.dt_block_norm_workspace(len(rows), _size_array(rows), cols, _DTYPES[dtype]))
+
+
+def _block_cols(post_weight, pre_weight) -> int:
+    if post_weight is None and pre_weight is None:
+        raise ValueError("one of post_weight and pre_weight must be given")
+    return _width((pre_weight if post_weight is None else post_weight)[0], "the norms' weights")
+
+
+def _block_gate(gate, sizes, cols: int) -> tuple:
+    """(a row of its own for every row?, elements of each rank's gate)"""
+    per_row = gate is not None and gate[0].dim() > 1
+    return int(per_row), sizes if per_row else [cols] * len(sizes)
+
+
+def dt_block_norm(z: Sequence[torch.Tensor], x: Sequence[torch.Tensor], h: Sequence[torch.Tensor],
+                  y: Optional[Sequence[torch.Tensor]], gate: Optional[Sequence[torch.Tensor]] = None, scale: float = 1.0,
+                  post_weight: Optional[Sequence[torch.Tensor]] = None, post_bias: Optional[Sequence[torch.Tensor]] = None,
+                  pre_weight: Optional[Sequence[torch.Tensor]] = None, pre_bias: Optional[Sequence[torch.Tensor]] = None,
+                  stats: Optional[Sequence[torch.Tensor]] = None, rms: bool = False, eps: float = 1e-5, stream=None,
+                  async_op: bool = False, comm_stream=None):
+    """h[r] = x[r] + scale * gate[r] * N(z[r]; post_weight, post_bias) and y[r] = N(h[r]; pre_weight, pre_bias) for every
+    rank's rows [rows, cols]: what a block's result z goes through on its way into the residual and the next block.  N is the
+    layer norm, or the RMS norm with ``rms``; without post_weight z enters as it is, without pre_weight y is None.  gate[r]
+    is [cols], the same for all rows and ranks, or [rows, cols].  stats[r] (fp32 [rows, 4]) keeps the statistics for
+    dt_block_norm_backward."""
+    dev, stash, cols = torch.cuda.current_device(), [], _block_cols(post_weight, pre_weight)
+    p, code, dtype = _ranks(z, "z"), _float_dtype(z[0]), z[0].dtype
+    sizes, rows, quads, n = _row_counts(z, cols, "z", 4)
+    per_row, gates = _block_gate(gate, sizes, cols)
+    take = lambda name, t, counts: _buffers(name, t, counts, dtype, dev, stash) if t is not None else None
+    wide = [cols] * p
+    args = [take("z", z, sizes), take("x", x, sizes), take("gate", gate, gates), take("post_weight", post_weight, wide),
+            take("post_bias", post_bias, wide), take("pre_weight", pre_weight, wide), take("pre_bias", pre_bias, wide),
+            take("h", h, sizes), take("y", y, sizes),
+            _buffers("stats", stats, quads, torch.float32, dev, stash) if stats is not None else None]
+    w = _launch(lambda st: _L.dt_block_norm(*args, p, n, cols, per_row, scale, int(bool(rms)), eps, code, st), stash, async_op, stream,
+                comm_stream)
+    return w if async_op else h
+
+
+def dt_block_norm_backward(dy: Optional[Sequence[torch.Tensor]], dh: Optional[Sequence[torch.Tensor]], z: Optional[Sequence[torch.Tensor]],
+                           h: Optional[Sequence[torch.Tensor]], stats: Sequence[torch.Tensor], dz: Sequence[torch.Tensor],
+                           dx: Sequence[torch.Tensor], gate: Optional[Sequence[torch.Tensor]] = None, scale: float = 1.0,
+                           post_weight: Optional[Sequence[torch.Tensor]] = None, post_bias: Optional[Sequence[torch.Tensor]] = None,
+                           pre_weight: Optional[Sequence[torch.Tensor]] = None, dgate: Optional[Sequence[torch.Tensor]] = None,
+                           dpost_weight: Optional[Sequence[torch.Tensor]] = None, dpost_bias: Optional[Sequence[torch.Tensor]] = None,
+                           dpre_weight: Optional[Sequence[torch.Tensor]] = None, dpre_bias: Optional[Sequence[torch.Tensor]] = None,
+                           rms: bool = False, workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False,
+                           comm_stream=None):
+    """Gradients of dt_block_norm from dy[r] and dh[r] (what reaches h past y; None: nothing): dz[r], dx[r], and of those that
+    are asked for dgate, dpost_weight, dpost_bias, dpre_weight, dpre_bias, summed over the rows of all ranks for every rank
+    (dgate[r] [rows, cols] for a gate per row)."""
+    dev, stash, cols = torch.cuda.current_device(), [], _block_cols(post_weight, pre_weight)
+    p, code, dtype = _ranks(dx, "dx"), _float_dtype(dx[0]), dx[0].dtype
+    sizes, rows, quads, n = _row_counts(dx, cols, "dx", 4)
+    per_row, gates = _block_gate(gate, sizes, cols)
+    take = lambda name, t, counts: _buffers(name, t, counts, dtype, dev, stash) if t is not None else None
+    wide = [cols] * p
+    args = [take("dy", dy, sizes), take("dh", dh, sizes), take("z", z, sizes), take("h", h, sizes), take("gate", gate, gates),
+            take("post_weight", post_weight, wide), take("post_bias", post_bias, wide), take("pre_weight", pre_weight, wide),
+            _buffers("stats", stats, quads, torch.float32, dev, stash), take("dz", dz, sizes), take("dx", dx, sizes),
+            take("dgate", dgate, gates), take("dpost_weight", dpost_weight, wide), take("dpost_bias", dpost_bias, wide),
+            take("dpre_weight", dpre_weight, wide), take("dpre_bias", dpre_bias, wide)]
+    space = _workspace(workspace, _sized(_L.dt_block_norm_workspace(p, n, cols, code)), dev, stream, async_op, comm_stream, stash)
+    at, have = space.data_ptr(), space.numel() * space.element_size()
+    w = _launch(lambda st: _L.dt_block_norm_backward(*args, p, n, cols, per_row, scale, int(bool(rms)), code, at, have, st), stash,
+                async_op, stream, comm_stream)
+    return w if async_op else dx
+
+
 __all__ = [
     "dt_allreduce", "dt_reduce_scatter", "dt_all_gather", "dt_all_to_all", "dt_bucket_allreduce", "dt_bucket_plan",
     "dt_all_gather_into_vec", "dt_broadcast", "dt_replicate_to_shard", "dt_all_to_all_dims",
@@ -1128,5 +1201,5 @@ __all__ = [
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
     "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
-    "dt_moe_layer", "dt_moe_layer_workspace",
+    "dt_moe_layer", "dt_moe_layer_workspace", "dt_block_norm", "dt_block_norm_backward", "dt_block_norm_workspace",
 ]

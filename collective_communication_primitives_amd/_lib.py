@@ -23,7 +23,7 @@ EXPORTS = (
     "dt_moe_dispatch", "dt_moe_dispatch_workspace", "dt_moe_combine", "dt_moe_combine_backward", "dt_vocab_loss",
     "dt_vocab_loss_backward", "dt_vocab_loss_workspace", "dt_vocab_loss_backward_workspace",
     "dt_linear", "dt_linear_backward", "dt_linear_backward_workspace",
-    "dt_moe_layer", "dt_moe_layer_workspace",
+    "dt_moe_layer", "dt_moe_layer_workspace", "dt_block_norm", "dt_block_norm_backward", "dt_block_norm_workspace",
 )
 
 
@@ -81,6 +81,9 @@ def load(path: str = LIBRARY) -> ctypes.CDLL:
         "dt_linear_backward_workspace": [i32, vp, i32, sz, i32, i32, i32, i32],
         "dt_moe_layer": [vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, vp, sz, sz, i32, i32, i32, i32, i32, vp, sz, vp],
         "dt_moe_layer_workspace": [i32, vp, sz, sz, i32, i32, i32],
+        "dt_block_norm": [vp] * 10 + [i32, vp, sz, i32, f32, i32, f32, i32, vp],
+        "dt_block_norm_backward": [vp] * 16 + [i32, vp, sz, i32, f32, i32, i32, vp, sz, vp],
+        "dt_block_norm_workspace": [i32, vp, sz, i32],
         "dt_status_string": [i32],
         "dt_last_error": [],
         "dt_version": [],

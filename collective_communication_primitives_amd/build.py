@@ -27,7 +27,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIBRARY = os.path.join(PKG, "libdtcoll.so")
 MARSHAL = os.path.join(PKG, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))
 SOURCES = ("api.cpp", "reduce.hip", "copy.hip", "barrier.hip", "scratch.hip", "step_api.cpp", "norm.hip", "moe.hip",
-           "loss.hip", "linear.hip", "layer.hip")
+           "loss.hip", "linear.hip", "layer.hip", "block.hip")
 ARCH = os.environ.get("DT_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [

@@ -192,4 +192,49 @@ struct LayerArgs {
 uint64_t layer_workspace(uint64_t tokens, uint64_t cols, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype);
 hipError_t launch_layer(LayerArgs a, void* workspace, int dtype, hipStream_t s);
 
+// --------------------------------------------------- norms around a block --
+struct BlockArgs {
+    const void* z[kMaxRanksHost];
+    const void* x[kMaxRanksHost];
+    const void* gate[kMaxRanksHost];
+    const void* post_weight[kMaxRanksHost];  // all NULL: no norm after the block
+    const void* post_bias[kMaxRanksHost];
+    const void* pre_weight[kMaxRanksHost];   // all NULL: none before the next one
+    const void* pre_bias[kMaxRanksHost];
+    void* h[kMaxRanksHost];
+    void* y[kMaxRanksHost];
+    float* stats[kMaxRanksHost];             // [rows][4]: mean and 1 / deviation of z, then of h
+    RowTable rows;
+    uint32_t cols;
+    int gate_kind, rms, nranks;              // gate_kind: 0 none, 1 one row for all, 2 one per row
+    float scale, eps;
+};
+struct BlockBackArgs {
+    const void* dy[kMaxRanksHost];
+    const void* dh[kMaxRanksHost];           // all NULL: zeros
+    const void* z[kMaxRanksHost];            // all NULL: not needed
+    const void* h[kMaxRanksHost];
+    const void* gate[kMaxRanksHost];
+    const void* post_weight[kMaxRanksHost];
+    const void* post_bias[kMaxRanksHost];
+    const void* pre_weight[kMaxRanksHost];
+    const float* stats[kMaxRanksHost];
+    void* dz[kMaxRanksHost];
+    void* dx[kMaxRanksHost];
+    void* dgate[kMaxRanksHost];
+    void* dpost_weight[kMaxRanksHost];
+    void* dpost_bias[kMaxRanksHost];
+    void* dpre_weight[kMaxRanksHost];
+    void* dpre_bias[kMaxRanksHost];
+    float* partial;                          // [strips][wanted sums][cols]
+    float* row_sums;                         // wide rows: [rows][2]
+    RowTable rows;
+    uint32_t cols, strips, sums, wanted;     // sums: bits of the column sums that are wanted
+    int gate_kind, rms, nranks;
+    float scale;
+};
+hipError_t launch_block(const BlockArgs& a, int dtype, hipStream_t s);
+uint64_t block_workspace(uint32_t rows, uint32_t cols, int dtype);
+hipError_t launch_block_backward(BlockBackArgs a, void* workspace, int dtype, hipStream_t s);
+
 }  // namespace dt

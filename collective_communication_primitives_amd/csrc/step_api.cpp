@@ -1,6 +1,6 @@
 // step_api.cpp -- the C ABI of the model-step operators of include/dt.h:
 // argument checks, row tables and workspace sizes.  The arithmetic is in
-// norm.hip, moe.hip, loss.hip, linear.hip and layer.hip; nothing here allocates or throws.
+// norm.hip, moe.hip, loss.hip, linear.hip, layer.hip and block.hip; nothing here allocates or throws.
 #include <stdarg.h>
 #include <stdio.h>
 
@@ -13,6 +13,7 @@ static_assert(sizeof(dt::NormBackArgs) <= 4096, "kernel arguments must stay belo
 static_assert(sizeof(dt::ExchangeRowsArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::LinearArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 static_assert(sizeof(dt::LayerArgs) <= 4096, "kernel arguments must stay below 4 KiB");
+static_assert(sizeof(dt::BlockBackArgs) <= 4096, "kernel arguments must stay below 4 KiB");
 
 namespace {
 
@@ -102,7 +103,7 @@ class Ranges {
         int index;
         bool write;
     };
-    Range r_[12 * DT_MAX_RANKS];
+    Range r_[17 * DT_MAX_RANKS];
     int n_ = 0;
     dt_status st_ = DT_OK;
 };
@@ -783,6 +784,152 @@ dt_status dt_moe_layer(const void* const* x, const int32_t* const* experts, cons
     a.gated = gated != 0;
     a.nranks = nranks;
     return done(dt::launch_layer(a, workspace, dtype, stream), "moe_layer");
+}
+
+}  // extern "C"
+
+// --------------------------------------------------- norms around a block --
+namespace {
+
+dt_status block_shape(int nranks, const size_t* rows, size_t cols, const void* const* gate, int gate_per_row,
+                      const void* const* post_weight, const void* const* post_bias, const void* const* pre_weight, float scale,
+                      dt_dtype dtype, const char* what, RowTable& t) {
+    TRY(check_ranks(nranks));
+    TRY(check_float(dtype, what));
+    TRY(row_table(rows, nranks, "rows", t));
+    TRY(check_cols(cols, what));
+    if (post_weight == nullptr && pre_weight == nullptr) return fail(DT_ERR_ARG, "%s: neither post_weight nor pre_weight", what);
+    if (post_weight == nullptr && post_bias != nullptr) return fail(DT_ERR_ARG, "%s: post_bias without post_weight", what);
+    if (gate == nullptr && gate_per_row) return fail(DT_ERR_ARG, "%s: gate_per_row without gate", what);
+    if (!(scale >= -1e30f && scale <= 1e30f)) return fail(DT_ERR_ARG, "%s: scale must be finite", what);
+    return DT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dt_status dt_block_norm(const void* const* z, const void* const* x, const void* const* gate, const void* const* post_weight,
+                        const void* const* post_bias, const void* const* pre_weight, const void* const* pre_bias,
+                        void* const* h, void* const* y, float* const* stats, int nranks, const size_t* rows, size_t cols,
+                        int gate_per_row, float scale, int rms, float eps, dt_dtype dtype, hipStream_t stream) {
+    dt::report_error(DT_OK, "");
+    dt::BlockArgs a = {};
+    TRY(block_shape(nranks, rows, cols, gate, gate_per_row, post_weight, post_bias, pre_weight, scale, dtype, "block_norm", a.rows));
+    if (pre_weight == nullptr && pre_bias != nullptr) return fail(DT_ERR_ARG, "block_norm: pre_bias without pre_weight");
+    if ((pre_weight == nullptr) != (y == nullptr)) return fail(DT_ERR_ARG, "block_norm: y and pre_weight come together");
+    if (!(eps >= 0.f) || eps > 1e30f) return fail(DT_ERR_ARG, "block_norm: eps must be finite and not negative");
+    const size_t es = esize_of(dtype);
+    Ranges g;
+    for (int r = 0; r < nranks; r++) {
+        if (rows[r] == 0) continue;
+        const size_t n = rows[r] * cols * es;
+        g.add(z, r, n, es, false, "z");
+        g.add(x, r, n, es, false, "x");
+        if (gate != nullptr) g.add(gate, r, gate_per_row ? n : cols * es, es, false, "gate");
+        if (post_weight != nullptr) g.add(post_weight, r, cols * es, es, false, "post_weight");
+        if (post_bias != nullptr) g.add(post_bias, r, cols * es, es, false, "post_bias");
+        if (pre_weight != nullptr) g.add(pre_weight, r, cols * es, es, false, "pre_weight");
+        if (pre_bias != nullptr) g.add(pre_bias, r, cols * es, es, false, "pre_bias");
+        g.add(h, r, n, es, true, "h");
+        if (y != nullptr) g.add(y, r, n, es, true, "y");
+        if (stats != nullptr) g.add(stats, r, rows[r] * 4 * sizeof(float), sizeof(float), true, "stats");
+    }
+    TRY(g.check("block_norm"));
+    if (a.rows.start[nranks] == 0) return DT_OK;
+    copy_list(a.z, z, nranks);
+    copy_list(a.x, x, nranks);
+    copy_list(a.gate, gate, nranks);
+    copy_list(a.post_weight, post_weight, nranks);
+    copy_list(a.post_bias, post_bias, nranks);
+    copy_list(a.pre_weight, pre_weight, nranks);
+    copy_list(a.pre_bias, pre_bias, nranks);
+    copy_list(a.h, h, nranks);
+    copy_list(a.y, y, nranks);
+    copy_list(a.stats, stats, nranks);
+    a.cols = uint32_t(cols);
+    a.gate_kind = gate == nullptr ? 0 : gate_per_row ? 2 : 1;
+    a.rms = rms != 0;
+    a.nranks = nranks;
+    a.scale = scale;
+    a.eps = eps;
+    return done(dt::launch_block(a, dtype, stream), "block_norm");
+}
+
+size_t dt_block_norm_workspace(int nranks, const size_t* rows, size_t cols, dt_dtype dtype) {
+    RowTable t;
+    dt::report_error(DT_OK, "");
+    if (check_ranks(nranks) != DT_OK || check_float(dtype, "block_norm_workspace") != DT_OK ||
+        row_table(rows, nranks, "rows", t) != DT_OK || check_cols(cols, "block_norm_workspace") != DT_OK)
+        return 0;
+    return dt::block_workspace(t.start[nranks], uint32_t(cols), dtype);
+}
+
+dt_status dt_block_norm_backward(const void* const* dy, const void* const* dh, const void* const* z, const void* const* h,
+                                 const void* const* gate, const void* const* post_weight, const void* const* post_bias,
+                                 const void* const* pre_weight, const float* const* stats, void* const* dz, void* const* dx,
+                                 void* const* dgate, void* const* dpost_weight, void* const* dpost_bias,
+                                 void* const* dpre_weight, void* const* dpre_bias, int nranks, const size_t* rows,
+                                 size_t cols, int gate_per_row, float scale, int rms, dt_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    dt::report_error(DT_OK, "");
+    dt::BlockBackArgs a = {};
+    TRY(block_shape(nranks, rows, cols, gate, gate_per_row, post_weight, post_bias, pre_weight, scale, dtype, "block_norm_backward", a.rows));
+    if ((pre_weight == nullptr) != (dy == nullptr)) return fail(DT_ERR_ARG, "block_norm_backward: dy and pre_weight come together");
+    if (pre_weight == nullptr && (dpre_weight != nullptr || dpre_bias != nullptr))
+        return fail(DT_ERR_ARG, "block_norm_backward: gradients of a norm that is not there (pre_weight is NULL)");
+    if (post_weight == nullptr && (dpost_weight != nullptr || dpost_bias != nullptr))
+        return fail(DT_ERR_ARG, "block_norm_backward: gradients of a norm that is not there (post_weight is NULL)");
+    if (gate == nullptr && dgate != nullptr) return fail(DT_ERR_ARG, "block_norm_backward: dgate without gate");
+    const size_t es = esize_of(dtype), need = dt::block_workspace(a.rows.start[nranks], uint32_t(cols), dtype);
+    const bool need_z = post_weight != nullptr || dgate != nullptr;
+    TRY(check_workspace(workspace, workspace_bytes, need, "block_norm_backward"));
+    Ranges g;
+    for (int r = 0; r < nranks; r++) {
+        const size_t n = rows[r] * cols * es, row = cols * es;
+        if (rows[r] > 0) {
+            if (dy != nullptr) g.add(dy, r, n, es, false, "dy");
+            if (dh != nullptr) g.add(dh, r, n, es, false, "dh");
+            if (need_z) g.add(z, r, n, es, false, "z");
+            if (pre_weight != nullptr) g.add(h, r, n, es, false, "h");
+            if (gate != nullptr) g.add(gate, r, gate_per_row ? n : row, es, false, "gate");
+            if (post_weight != nullptr) g.add(post_weight, r, row, es, false, "post_weight");
+            if (post_bias != nullptr) g.add(post_bias, r, row, es, false, "post_bias");
+            if (pre_weight != nullptr) g.add(pre_weight, r, row, es, false, "pre_weight");
+            g.add(stats, r, rows[r] * 4 * sizeof(float), sizeof(float), false, "stats");
+            g.add(dz, r, n, es, true, "dz");
+            g.add(dx, r, n, es, true, "dx");
+        }
+        if (dgate != nullptr) g.add(dgate, r, gate_per_row ? n : row, es, true, "dgate");
+        if (dpost_weight != nullptr) g.add(dpost_weight, r, row, es, true, "dpost_weight");
+        if (dpost_bias != nullptr) g.add(dpost_bias, r, row, es, true, "dpost_bias");
+        if (dpre_weight != nullptr) g.add(dpre_weight, r, row, es, true, "dpre_weight");
+        if (dpre_bias != nullptr) g.add(dpre_bias, r, row, es, true, "dpre_bias");
+    }
+    g.add(&workspace, 0, need, 1, true, "workspace");
+    TRY(g.check("block_norm_backward"));
+    copy_list(a.dy, dy, nranks);
+    copy_list(a.dh, dh, nranks);
+    if (need_z) copy_list(a.z, z, nranks);
+    if (pre_weight != nullptr) copy_list(a.h, h, nranks);
+    copy_list(a.gate, gate, nranks);
+    copy_list(a.post_weight, post_weight, nranks);
+    copy_list(a.post_bias, post_bias, nranks);
+    copy_list(a.pre_weight, pre_weight, nranks);
+    copy_list(a.stats, stats, nranks);
+    copy_list(a.dz, dz, nranks);
+    copy_list(a.dx, dx, nranks);
+    copy_list(a.dgate, dgate, nranks);
+    copy_list(a.dpost_weight, dpost_weight, nranks);
+    copy_list(a.dpost_bias, dpost_bias, nranks);
+    copy_list(a.dpre_weight, dpre_weight, nranks);
+    copy_list(a.dpre_bias, dpre_bias, nranks);
+    a.cols = uint32_t(cols);
+    a.gate_kind = gate == nullptr ? 0 : gate_per_row ? 2 : 1;
+    a.rms = rms != 0;
+    a.nranks = nranks;
+    a.scale = scale;
+    return done(dt::launch_block_backward(a, workspace, dtype, stream), "block_norm_backward");
 }
 
 }  // extern "C"

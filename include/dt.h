@@ -446,6 +446,38 @@ dt_status dt_moe_layer(const void* const* x, const int32_t* const* experts, cons
                        const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk, dt_act act, int gated,
                        dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* The norms after and before a block with its gate and residual, over rows that are
+ * Shard(0) over the ranks, in one pass:
+ *   p = N(z; post_weight, post_bias)     (post_weight NULL: p = z)
+ *   h = x + scale * gate * p             (gate NULL: 1)
+ *   y = N(h; pre_weight, pre_bias)       (pre_weight and y NULL: no y)
+ * N is the layer norm of dt_layer_norm or, with rms, the same without the mean: v *
+ * weight / sqrt(mean(v^2) + eps).  One of the two norms at least is there; a bias
+ * (NULL: none) comes with its weight.  gate[r] is [cols], the same for all rows and
+ * ranks, or with gate_per_row [rows[r], cols].  z is what the block made of the
+ * rows, x the residual that went past it.  y is taken from h before it is rounded.
+ * stats[r] [rows[r], 4] fp32 keeps mean and 1 / sqrt(..) of z's row, then of h's,
+ * zeros for a norm that is not there (NULL: not kept). */
+dt_status dt_block_norm(const void* const* z, const void* const* x, const void* const* gate, const void* const* post_weight,
+                        const void* const* post_bias, const void* const* pre_weight, const void* const* pre_bias,
+                        void* const* h, void* const* y, float* const* stats, int nranks, const size_t* rows, size_t cols,
+                        int gate_per_row, float scale, int rms, float eps, dt_dtype dtype, hipStream_t stream);
+
+/* Its backward pass from dy (NULL with pre_weight) and dh, the gradient of h that
+ * does not come through y (NULL: zeros): dx[r], dz[r], and the gradients of the
+ * weights, biases and a gate of all rows summed over the rows of ALL ranks, for every
+ * rank (Partial -> Replicate); dgate[r] [rows[r], cols] for a gate per row.  Each of
+ * those may be NULL: not formed.  h is read with pre_weight, z with post_weight or for
+ * dgate (else they may be NULL), post_bias for dgate.  No rows: zeros. */
+size_t dt_block_norm_workspace(int nranks, const size_t* rows, size_t cols, dt_dtype dtype);
+dt_status dt_block_norm_backward(const void* const* dy, const void* const* dh, const void* const* z, const void* const* h,
+                                 const void* const* gate, const void* const* post_weight, const void* const* post_bias,
+                                 const void* const* pre_weight, const float* const* stats, void* const* dz, void* const* dx,
+                                 void* const* dgate, void* const* dpost_weight, void* const* dpost_bias,
+                                 void* const* dpre_weight, void* const* dpre_bias, int nranks, const size_t* rows,
+                                 size_t cols, int gate_per_row, float scale, int rms, dt_dtype dtype, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+
 /* ---- host planning (no GPU work) -------------------------------------- */
 
 /* One contiguous part of one tensor inside one bucket. */

@@ -145,3 +145,105 @@ def layer(x, experts, weights, w_in, w_out, b_in, b_out, residual, kind, gated):
         size[tok] += mag
     n = k * (w_out.shape[2] + 2) + 8 + 16
     return out, err + n * U * size
+
+
+# ------------------------------------------------------ norms around a block --
+def _chain(n: int) -> float:
+    # a thread adds at most n / 64 terms of a row, the trees over lanes and waves some more
+    return n / 64.0 + 24.0
+
+
+def _norm(v, ev, w, b, eps, rms):
+    """(output, mean, rstd) of rows v that are off by ev, and their bounds."""
+    c = v.shape[1]
+    mean = torch.zeros_like(v[:, :1]) if rms else v.mean(1, keepdim=True)
+    em = torch.zeros_like(mean) if rms else (_chain(c) + 2) * U * v.abs().mean(1, keepdim=True) + ev.mean(1, keepdim=True)
+    d = v - mean
+    ed = em + ev + (0 if rms else U) * d.abs()
+    var = d.square().mean(1, keepdim=True)
+    evar = (_chain(c) + 4) * U * var + 2 * (ed * d.abs()).mean(1, keepdim=True) + ed.square().mean(1, keepdim=True)
+    rstd = 1 / torch.sqrt(var + eps)
+    er = rstd * (0.5 * evar / (var + eps) * 1.01 + 4 * U) + 1e-30
+    n = d * rstd
+    en = rstd * ed + d.abs() * er + 2 * U * n.abs()
+    out, size = n * w, (n * w).abs()
+    if b is not None:
+        out, size = out + b, size + b.abs()
+    return (out, mean, rstd), (w.abs() * en + 3 * U * size, em, er)
+
+
+def _d(t):
+    return None if t is None else t.double()
+
+
+def block(z, x, gate, w1, b1, w2, b2, scale, rms, eps):
+    """All ranks' rows: dict of h, y, stats -> (value, bound)."""
+    z, x, gate, w1, b1, w2, b2 = (_d(t) for t in (z, x, gate, w1, b1, w2, b2))
+    none = torch.zeros_like(z[:, :1])
+    p, ep, first, efirst = z, torch.zeros_like(z), (none, none), (none, none)
+    if w1 is not None:
+        (p, *first), (ep, *efirst) = _norm(z, ep, w1, b1, eps, rms)
+    f = torch.full_like(z[:1], scale) if gate is None else scale * gate
+    h = x + f * p
+    eh = f.abs() * ep + 3 * U * (f * p).abs() + U * (x.abs() + (f * p).abs())
+    out, second, esecond = dict(h=(h, eh)), (none, none), (none, none)
+    if w2 is not None:
+        (y, *second), (ey, *esecond) = _norm(h, eh, w2, b2, eps, rms)
+        out["y"] = (y, ey)
+    out["stats"] = (torch.cat([*first, *second], 1), torch.cat([*efirst, *esecond], 1))
+    return out
+
+
+def _norm_back(g, eg, n, rstd, rms):
+    """rstd (g - mean(g) - n mean(g n)) for a gradient that is off by eg, and its bound."""
+    c = g.shape[1]
+    m1 = torch.zeros_like(g[:, :1]) if rms else g.mean(1, keepdim=True)
+    e1 = torch.zeros_like(m1) if rms else eg.mean(1, keepdim=True) + (_chain(c) + 3) * U * g.abs().mean(1, keepdim=True)
+    m2 = (g * n).mean(1, keepdim=True)
+    e2 = (eg * n.abs()).mean(1, keepdim=True) + (_chain(c) + 8) * U * (g * n).abs().mean(1, keepdim=True)
+    out = rstd * (g - m1 - n * m2)
+    return out, rstd.abs() * (eg + 4 * U * g.abs() + e1 + 3 * U * m1.abs() + n.abs() * e2 + 8 * U * (n * m2).abs())
+
+
+def block_backward(dy, dh, z, h, gate, w1, b1, w2, stats, scale, rms):
+    """All ranks' rows: dict of dx, dz, dgate (of every row), dpost_weight ... -> (value, bound); shared sums are over all rows."""
+    dy, dh, z, h, gate, w1, b1, w2, stats = (_d(t) for t in (dy, dh, z, h, gate, w1, b1, w2, stats))
+    m1, r1, m2, r2 = stats.split(1, 1)
+    rows, out = stats.shape[0], {}
+
+    def total(name, v, ev):
+        out[name] = (v.sum(0), ev.sum(0) + (rows + 24) * U * v.abs().sum(0))
+
+    like = dy if dy is not None else dh
+    dx = dh if dh is not None else torch.zeros_like(like)
+    ex = torch.zeros_like(dx)
+    if w2 is not None:
+        n = (h - m2) * r2
+        g = dy * w2
+        part, epart = _norm_back(g, U * g.abs(), n, r2, rms)
+        total("dpre_weight", dy * n, 5 * U * (dy * n).abs())
+        total("dpre_bias", dy, torch.zeros_like(dy))
+        ex = epart + 2 * U * (dx.abs() + part.abs())
+        dx = dx + part
+    out["dx"] = (dx, ex)
+    f = scale if gate is None else scale * gate
+    du = dx * f
+    eu = ex * (abs(f) if gate is None else f.abs()) + 3 * U * du.abs()
+    if z is None:
+        z = torch.zeros_like(dx)
+    if w1 is not None:
+        n = (z - m1) * r1
+        p = n * w1 if b1 is None else n * w1 + b1
+        ep = 6 * U * ((n * w1).abs() + (0 if b1 is None else b1.abs()))
+        g = du * w1
+        out["dz"] = _norm_back(g, eu * w1.abs() + U * g.abs(), n, r1, rms)
+        total("dpost_weight", du * n, eu * n.abs() + 5 * U * (du * n).abs())
+        total("dpost_bias", du, eu)
+    else:
+        p, ep = z, torch.zeros_like(z)
+        out["dz"] = (du, eu)
+    dg = dx * p * scale
+    eg = (ex * p.abs() + dx.abs() * ep) * abs(scale) + 5 * U * dg.abs()
+    out["dgate"] = (dg, eg)
+    total("dgate_sum", dg, eg)
+    return out

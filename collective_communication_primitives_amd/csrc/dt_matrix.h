@@ -116,8 +116,7 @@ __device__ __forceinline__ uint32_t row_turn(uint32_t row) {
 // One load instruction of the wave brings 1 KiB of the operand's step into
 // LDS, 16 bytes per lane in lane order: the lane's place in the step.
 template <int DT, int MODE, int R, typename OP>
-__device__ __forceinline__ uint32_t load_place(const OP& op, uint32_t group) {
-    const uint32_t lane = threadIdx.x & 63;
+__device__ __forceinline__ uint32_t load_place(const OP& op, uint32_t group, uint32_t lane) {
     if constexpr (MODE == kRows) {
         // 16 rows of 64 bytes: lane l brings row l / 4
         const uint32_t row = lane >> 2;
@@ -145,8 +144,7 @@ __device__ __forceinline__ void load_step(const OP& op, uint32_t step, bool any,
 // chunk l / 16 of the step.  `place` is the lane's byte in the operand's part
 // of a stage for the wave's first 16 rows; the others are a constant away.
 template <int DT, int MODE, int R>
-__device__ __forceinline__ uint32_t fragment_place(uint32_t at) {
-    const uint32_t lane = threadIdx.x & 63;
+__device__ __forceinline__ uint32_t fragment_place(uint32_t at, uint32_t lane) {
     if constexpr (MODE == kRows) {
         const uint32_t row = at + (lane & 15);
         return row * kStepBytes + ((lane >> 4) ^ row_turn(row)) * 16;
@@ -224,12 +222,13 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
         for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (lo >= hi) return;
     const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
+    const uint32_t lane = threadIdx.x & 63;
     // the wave's shares of A's and B's groups of 1 KiB
     uint32_t pa[S::loads_a], pb[S::loads_b];
 #pragma unroll
-    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(A, wave * S::loads_a + i);
+    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(A, wave * S::loads_a + i, lane);
 #pragma unroll
-    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(B, wave * S::loads_b + i);
+    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(B, wave * S::loads_b + i, lane);
     // The loop runs in whole rounds of four steps: what is loaded for the steps
     // behind the last one is zeros (from an empty buffer, no memory is read), so
     // a wave's outstanding loads can be counted and the loop has one exit.
@@ -242,7 +241,7 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     load(lo + 2, s2);
     arrive<2 * S::loads, 15>();
     u32x4 fa[S::MI], fb[2][S::NI];
-    uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
+    uint32_t ra = fragment_place<DT, MA, S::BM>(wm, lane), rb = fragment_place<DT, MB, S::BN>(wn, lane);
 #pragma unroll
     for (int i = 0; i < S::MI; i++) fa[i] = A.cut(fragment<DT, MA, S::BM>(s0, ra, i), lo);
 #pragma unroll
@@ -281,6 +280,151 @@ __device__ __forceinline__ void matrix_tile(const OA& A, const OB& B, uint32_t l
     arrive<0, 0>();  // nothing is on its way into LDS when the workgroup ends
 }
 
+// Four values rounded to the dtype and stored as one (`to` aligned for it); zeros unless `use`.
+template <int DT>
+__device__ __forceinline__ void store_quad(typename Elem<DT>::type* to, f32x4 v, bool use) {
+    if constexpr (DT == kBF16) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        uint2 o;
+        o.x = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[0]), __bf16(v[1])});
+        o.y = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[2]), __bf16(v[3])});
+        if (!use) o = make_uint2(0, 0);
+        *reinterpret_cast<uint2*>(to) = o;
+    } else {
+        *reinterpret_cast<f32x4*>(to) = use ? v : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+}
+
+// The lane, without what the compiler knows of it: a loop over tiles would
+// otherwise hold each address that it gives in a register through the products.
+__device__ __forceinline__ uint32_t fresh_lane() {
+    uint32_t lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
+// The tiles of a workgroup one after the other, as matrix_tile multiplies them, with
+// the loads running on from tile to tile: the next tile's first three steps are on
+// their way while the last ones of a tile are multiplied and while its sums leave
+// the registers.
+//   next(t)               the workgroup's next tile; false: there is none
+//   operands(t, A, B)     sets its operands and returns its steps of the summed
+//                         index; a row's end and pitch are the same in all tiles
+//   rows(t)               its rows of B that are there: waves with none of them leave
+//                         the matrix units to the others
+//   done(t, acc, room)    what becomes of its sums, acc as matrix_tile leaves it; room:
+//                         LDS of the wave's own
+// A tile takes whole rounds of four steps, one at least, so the loads are never
+// more than one tile ahead.
+template <int DT, typename S, int MA, int MB, typename OA, typename OB, typename Tile, typename Next, typename Operands, typename Rows, typename Done>
+__device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Rows&& rows, Done&& done) {
+    __shared__ u32x4 s0[S::stage], s1[S::stage], s2[S::stage], s3[S::stage];
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Tile now, ahead;     // multiplied, loaded
+    if (!next(ahead)) return;
+    OA A;
+    OB B;
+    auto rounds = [](uint32_t n) { return n == 0 ? 4 : (n + 3) / 4 * 4; };
+    uint32_t steps = operands(ahead, A, B), end = rounds(steps), step = 0;   // of the loads
+    bool more = true;
+    const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN, lane = fresh_lane();
+    uint32_t pa[S::loads_a], pb[S::loads_b];
+#pragma unroll
+    for (int i = 0; i < S::loads_a; i++) pa[i] = load_place<DT, MA, S::BM>(A, wave * S::loads_a + i, lane);
+#pragma unroll
+    for (int i = 0; i < S::loads_b; i++) pb[i] = load_place<DT, MB, S::BN>(B, wave * S::loads_b + i, lane);
+    auto load = [&](u32x4* to) {
+        load_step<MA>(A, step, step < steps, pa, to + wave * S::loads_a * 64);
+        load_step<MB>(B, step, step < steps, pb, to + S::BM * kChunks + wave * S::loads_b * 64);
+        step++;
+    };
+    load(s0);
+    load(s1);
+    load(s2);
+    arrive<2 * S::loads, 15>();
+    u32x4 fa[S::MI], fb[2][S::NI];
+    uint32_t ra = fragment_place<DT, MA, S::BM>(wm, lane), rb = fragment_place<DT, MB, S::BN>(wn, lane);
+#pragma unroll
+    for (int i = 0; i < S::MI; i++) fa[i] = A.cut(fragment<DT, MA, S::BM>(s0, ra, i), 0);
+#pragma unroll
+    for (int j = 0; j < S::NI; j++) fb[0][j] = B.cut(fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j), 0);
+    f32x4 acc[S::MI][S::NI];
+    // One step, as in matrix_tile.  settled: the bytes of the following step have
+    // been waited for already, behind the tile before, and its stores need not be.
+    constexpr int turn_reads = S::MI * (MA == kRows ? 1 : 2) + S::NI * (MB == kRows ? 1 : 2);
+    bool active = wn < rows(ahead);   // the wave has rows in the tile that is multiplied
+    auto turn = [&](uint32_t following_step, bool settled, u32x4* free, const u32x4* following, const u32x4 (&fn)[S::NI], u32x4 (&fnext)[S::NI]) {
+        if (settled) arrive<63, turn_reads < 15 ? turn_reads : 15>();
+        else arrive<S::loads, turn_reads < 15 ? turn_reads : 15>();
+        load(free);
+        // keeps the compiler from holding every fragment's address of every stage in a register
+        asm volatile("" : "+v"(ra), "+v"(rb));
+        if (!active && following_step != 0) return;
+#pragma unroll
+        for (int j = 0; j < S::NI; j++) fnext[j] = B.cut(fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j), following_step);
+#pragma unroll
+        for (int i = 0; i < S::MI; i++) {
+#pragma unroll
+            for (int j = 0; j < S::NI; j++) acc[i][j] = multiply<DT>(fa[i], fn[j], acc[i][j]);
+            fa[i] = A.cut(fragment<DT, MA, S::BM>(following, ra, i), following_step);
+        }
+    };
+    bool settled = false;
+    while (true) {
+        now = ahead;
+        const uint32_t last = end;
+#pragma unroll
+        for (int i = 0; i < S::MI; i++)
+#pragma unroll
+            for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (uint32_t k = 0; k < last; k += 4) {
+            turn(k + 1, settled, s3, s1, fb[0], fb[1]);
+            if (step == end) {   // three steps of this tile are left to be multiplied
+                more = next(ahead);
+                steps = more ? operands(ahead, A, B) : 0;
+                end = rounds(steps);
+                step = 0;
+            }
+            turn(k + 2, settled, s0, s2, fb[1], fb[0]);
+            settled = false;
+            turn(k + 3, false, s1, s3, fb[0], fb[1]);
+            turn(k + 4 == last ? 0 : k + 4, false, s2, s0, fb[1], fb[0]);
+        }
+        // The loads that are on their way arrive before the stores go out, so that nothing waits for those; and s3,
+        // loaded again behind the next barrier, is read no more.
+        arrive<0, 0>();
+        constexpr uint32_t room = S::stage / S::waves;
+        static_assert(room * 16 >= 16 * S::WM * (DT == kBF16 ? 2 : 4) && room * 16 >= 16 * (S::WM < 64 ? S::WM : 64) * 4,
+                      "the wave's room holds 16 rows of its features in the type, or of up to 64 of them in fp32");
+        if (active) done(now, acc, s3 + wave * room);
+        if (!more) break;
+        settled = true;
+        active = wn < rows(ahead);
+    }
+    arrive<0, 0>();  // nothing is on its way into LDS when the workgroup ends
+}
+
+// 16 rows of W features, row lane % 16 in the lane's quads v[q] (features 16 q + 4
+// (lane / 16) on), rounded to the type and turned through the wave's room in LDS:
+// emit(row, feature, 16 bytes of them), so that stores are of whole lines where
+// quads would touch 16 rows each.
+template <int DT, int W, typename Emit>
+__device__ __forceinline__ void turn_rows(u32x4* room, const f32x4 (&v)[W / 16], Emit&& emit) {
+    constexpr uint32_t es = DT == kBF16 ? 2 : 4, per_row = W * es / 16, all = 16 * per_row;
+    const uint32_t lane = fresh_lane(), n = lane & 15;
+#pragma unroll
+    for (int q = 0; q < W / 16; q++) {
+        const uint32_t byte = (16 * q + (lane >> 4) * 4) * es, at = (n * per_row + ((byte / 16) ^ (n % per_row))) * 16 + byte % 16;
+        store_quad<DT>(reinterpret_cast<typename Elem<DT>::type*>(reinterpret_cast<char*>(room) + at), v[q], true);
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < (all + 63) / 64; k++) {
+        const uint32_t i = k * 64 + lane, row = i / per_row, vec = i % per_row;
+        if (all % 64 != 0 && i >= all) continue;
+        emit(row, vec * (16 / es), room[row * per_row + (vec ^ (row % per_row))]);
+    }
+}
+
 // 16 bytes at byte `at` of a row of `bytes` bytes that starts and ends at any
 // element: zeros behind the row's end, where nothing is read.
 template <int ES>
@@ -298,32 +442,23 @@ __device__ __forceinline__ u32x4 read_loose(const char* row, uint32_t at, uint32
     return x;
 }
 
-// Tile `id` of mt x nt in an order that keeps an XCD's workgroups on
-// neighbouring tiles: ids go round the 8 XCDs, so each XCD gets a run of the
-// tiles, walked in bands of 8 rows of tiles.
-__device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
-    const uint32_t total = mt * nt, q = total / 8, rem = total % 8, x = id % 8;
-    const uint32_t t = x * q + (x < rem ? x : rem) + id / 8;
+// Which of `total` tiles workgroup `id` takes: ids go round the 8 XCDs, and each XCD
+// gets a run of neighbouring tiles.
+__device__ __forceinline__ uint32_t share_of(uint32_t id, uint32_t total) {
+    const uint32_t q = total / 8, rem = total % 8, x = id % 8;
+    return x * q + (x < rem ? x : rem) + id / 8;
+}
+// Tile t of mt x nt, walked in bands of 8 rows of tiles.
+__device__ __forceinline__ void band_tile(uint32_t t, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
     const uint32_t band = t / (8 * nt), first = band * 8, in = t - band * 8 * nt;
     const uint32_t high = mt - first < 8 ? mt - first : 8;
     // divisions run on the vector unit: back into scalar registers, where the buffer resources are built
     m = __builtin_amdgcn_readfirstlane(first + in % high);
     n = __builtin_amdgcn_readfirstlane(in / high);
 }
-
-// Four values rounded to the dtype and stored as one (`to` aligned for it); zeros unless `use`.
-template <int DT>
-__device__ __forceinline__ void store_quad(typename Elem<DT>::type* to, f32x4 v, bool use) {
-    if constexpr (DT == kBF16) {
-        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-        uint2 o;
-        o.x = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[0]), __bf16(v[1])});
-        o.y = __builtin_bit_cast(uint32_t, bf16x2{__bf16(v[2]), __bf16(v[3])});
-        if (!use) o = make_uint2(0, 0);
-        *reinterpret_cast<uint2*>(to) = o;
-    } else {
-        *reinterpret_cast<f32x4*>(to) = use ? v : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
+// Tile `id` of mt x nt in an order that keeps an XCD's workgroups on neighbouring tiles.
+__device__ __forceinline__ void tile_of(uint32_t id, uint32_t mt, uint32_t nt, uint32_t& m, uint32_t& n) {
+    band_tile(share_of(id, mt * nt), mt, nt, m, n);
 }
 
 }  // namespace

@@ -162,6 +162,7 @@ struct LinearArgs {
     uint32_t runs, cols, outs, zpitch;
     int act, gated, need_dz, nranks;
     int quads, col_quads;                   // rows of outs, of cols, are whole fours, aligned to them
+    int vecs, col_vecs;                     // the same of 16 bytes, where they are written
 };
 uint64_t linear_backward_workspace(const RowTable& rows, int nranks, uint32_t runs, uint64_t outs, int act, int gated, bool dbias, int dtype);
 hipError_t launch_linear(const LinearArgs& a, int dtype, hipStream_t s);

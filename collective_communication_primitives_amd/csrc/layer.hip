@@ -205,7 +205,7 @@ __device__ __forceinline__ void in_tile(const LayerArgs& a, const Plan& p, uint3
                 z[i] += Elem<DT>::get(b[i]);
                 if (GATED) u[i] += Elem<DT>::get(b[a.inner + i]);
             }
-            const float v = act<DT>(z[i], a.act) * (GATED ? u[i] : 1.f) * p.weight[c];
+            const float v = act(z[i], a.act) * (GATED ? u[i] : 1.f) * p.weight[c];
             h[i] = in ? v : 0.f;   // zeros up to the row's pitch
             const float near = Elem<DT>::get(Elem<DT>::put(h[i]));
             rest[i] = fabsf(near) < INFINITY ? h[i] - near : 0.f;

@@ -41,15 +41,27 @@ __device__ __forceinline__ Run same(const Run& r) {
                uint32_t(__builtin_amdgcn_readfirstlane(r.lo)), uint32_t(__builtin_amdgcn_readfirstlane(r.count))};
 }
 
-// first[g]: tiles of `per` rows of the runs before g; first[all runs]: their number in all.
-__device__ __forceinline__ void count_tiles(const LinearArgs& a, uint32_t per, uint32_t* first) {
+// The runs' tiles of `per` rows, counted by the workgroup itself.
+constexpr uint32_t kCachedRuns = 256;
+struct Runs {
+    uint32_t first[kMaxRuns + 1];                    // tiles of the runs before g; of all runs
+    uint32_t lo[kCachedRuns], count[kCachedRuns];    // rows of the first runs
+};
+__device__ __forceinline__ void count_tiles(const LinearArgs& a, uint32_t per, Runs& t) {
     const uint32_t groups = a.runs * a.nranks;
-    for (uint32_t g = threadIdx.x; g < groups; g += blockDim.x) first[g] = (run_at(a, g).count + per - 1) / per;
+    for (uint32_t g = threadIdx.x; g < groups; g += blockDim.x) {
+        const Run r = run_at(a, g);
+        t.first[g] = (r.count + per - 1) / per;
+        if (g < kCachedRuns) {
+            t.lo[g] = r.lo;
+            t.count[g] = r.count;
+        }
+    }
     __syncthreads();
     if (threadIdx.x < 64) {
         const uint32_t each = (groups + 63) / 64, lo = threadIdx.x * each, hi = lo + each < groups ? lo + each : groups;
         uint32_t sum = 0;
-        for (uint32_t g = lo; g < hi; g++) sum += first[g];
+        for (uint32_t g = lo; g < hi; g++) sum += t.first[g];
         uint32_t before = sum;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
@@ -58,24 +70,80 @@ __device__ __forceinline__ void count_tiles(const LinearArgs& a, uint32_t per, u
         }
         before -= sum;
         for (uint32_t g = lo; g < hi; g++) {
-            const uint32_t n = first[g];
-            first[g] = before;
+            const uint32_t n = t.first[g];
+            t.first[g] = before;
             before += n;
         }
-        if (threadIdx.x == 63) first[groups] = before;
+        if (threadIdx.x == 63) t.first[groups] = before;
     }
     __syncthreads();
+}
+// Run g in scalar registers.
+__device__ __forceinline__ Run run_of(const LinearArgs& a, const Runs& t, uint32_t g) {
+    if (g >= kCachedRuns) return same(run_at(a, g));
+    return Run{g / a.runs, g % a.runs, uint32_t(__builtin_amdgcn_readfirstlane(t.lo[g])), uint32_t(__builtin_amdgcn_readfirstlane(t.count[g]))};
 }
 // The run that tile t belongs to.
 __device__ __forceinline__ uint32_t run_of_tile(const uint32_t* first, uint32_t groups, uint32_t t) {
     uint32_t lo = 0, hi = groups;  // first[lo] <= t < first[hi]
     while (lo + 1 < hi) {
         const uint32_t mid = (lo + hi) / 2;
-        if (first[mid] <= t) lo = mid;
+        if (uint32_t(__builtin_amdgcn_readfirstlane(first[mid])) <= t) lo = mid;
         else hi = mid;
     }
-    return uint32_t(__builtin_amdgcn_readfirstlane(lo));
+    return lo;
 }
+
+// A tile of a product: its run, its first feature (or column) m0 and row (or feature) n0.
+struct LinearTile {
+    Run r;
+    uint32_t m0, n0;
+};
+// The workgroup's tiles of products whose rows are the runs': every gridDim.x-th, run
+// by run, so that neighbouring tiles meet the same weights.
+template <uint32_t BM, uint32_t BN>
+struct RowTiles {
+    const LinearArgs& a;
+    const Runs& runs;
+    uint32_t mts, all, id;
+    __device__ __forceinline__ RowTiles(const LinearArgs& args, Runs& t, uint32_t features)
+        : a(args), runs(t), mts((features + BM - 1) / BM), id(blockIdx.x) {
+        count_tiles(a, BN, t);
+        all = mts * __builtin_amdgcn_readfirstlane(t.first[a.runs * a.nranks]);
+    }
+    __device__ __forceinline__ bool operator()(LinearTile& t) {
+        if (id >= all) return false;
+        const uint32_t at = share_of(id, all), g = run_of_tile(runs.first, a.runs * a.nranks, __builtin_amdgcn_readfirstlane(at / mts));
+        const uint32_t from = __builtin_amdgcn_readfirstlane(runs.first[g]), to = __builtin_amdgcn_readfirstlane(runs.first[g + 1]);
+        uint32_t mt, nt;
+        band_tile(at - from * mts, mts, to - from, mt, nt);
+        id += gridDim.x;
+        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN};
+        return true;
+    }
+};
+// The same for the runs' weights: run by run, so that a run's rows are read while they are near.
+template <uint32_t BM, uint32_t BN>
+struct WeightTiles {
+    const LinearArgs& a;
+    const Runs& runs;
+    uint32_t mts, nts;
+    uint64_t id;
+    __device__ __forceinline__ WeightTiles(const LinearArgs& args, Runs& t, uint32_t cols, uint32_t features)
+        : a(args), runs(t), mts((cols + BM - 1) / BM), nts((features + BN - 1) / BN), id(blockIdx.x) {
+        count_tiles(a, BN, t);
+    }
+    __device__ __forceinline__ bool operator()(LinearTile& t) {
+        const uint32_t each = mts * nts;
+        if (id >= uint64_t(each) * (a.runs * a.nranks)) return false;
+        const uint32_t g = __builtin_amdgcn_readfirstlane(uint32_t(id / each));
+        uint32_t mt, nt;
+        tile_of(__builtin_amdgcn_readfirstlane(uint32_t(id % each)), mts, nts, mt, nt);
+        id += gridDim.x;
+        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN};
+        return true;
+    }
+};
 
 // --------------------------------------------------------------- operands --
 // A gated product's tile of weight rows: 16 rows of the gate and the 16 of the
@@ -115,8 +183,9 @@ struct LooseCols {
 
 // matrix_tile for such operands: two stages of LDS, the next step's bytes on
 // their way to registers while one is multiplied.
+// Returns LDS of the wave's own, which the next tile may use again.
 template <int DT, typename S, int MA, int MB, typename OA, typename OB>
-__device__ __forceinline__ void loose_tile(const OA& A, const OB& B, uint32_t steps, f32x4 (&acc)[S::MI][S::NI]) {
+__device__ __forceinline__ u32x4* loose_tile(const OA& A, const OB& B, uint32_t steps, f32x4 (&acc)[S::MI][S::NI]) {
     constexpr int ES = DT == kBF16 ? 2 : 4;
     __shared__ u32x4 stage[2][S::stage];
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -132,8 +201,9 @@ __device__ __forceinline__ void loose_tile(const OA& A, const OB& B, uint32_t st
         for (int i = 0; i < S::loads_b; i++) cb[i] = B.template chunk<ES, S::BN>(wave * S::loads_b + i, step);
     };
     const uint32_t wm = (wave % S::GM) * S::WM, wn = (wave / S::GM) * S::WN;
-    const uint32_t ra = fragment_place<DT, MA, S::BM>(wm), rb = fragment_place<DT, MB, S::BN>(wn);
+    const uint32_t ra = fragment_place<DT, MA, S::BM>(wm, lane), rb = fragment_place<DT, MB, S::BN>(wn, lane);
     if (steps > 0) read(0);
+    __syncthreads();  // the waves have left the room of the tile before
     for (uint32_t step = 0; step < steps; step++) {
         u32x4* to = stage[step & 1];
 #pragma unroll
@@ -154,7 +224,8 @@ __device__ __forceinline__ void loose_tile(const OA& A, const OB& B, uint32_t st
             for (int j = 0; j < S::NI; j++) acc[i][j] = multiply<DT>(fa, fb[j], acc[i][j]);
         }
     }
-    __syncthreads();  // the next tile writes the first stage
+    __syncthreads();
+    return &stage[0][0] + wave * (S::stage / S::waves);
 }
 
 // Four neighbouring values; quads: stored and read as one.
@@ -183,27 +254,116 @@ __device__ __forceinline__ void store_four(typename Elem<DT>::type* p, f32x4 v, 
 }
 
 // ---------------------------------------------------------------- forward --
-// What becomes of four neighbouring features' sums of one row (gated: u their linear parts).
-template <int DT, bool GATED>
-__device__ __forceinline__ void finish(const LinearArgs& a, const Run& r, uint64_t row, uint32_t m, f32x4 z, f32x4 u) {
+// 16 bytes of a row at element m, `left` elements before the row's end, as floats.
+template <int DT, int E>
+__device__ __forceinline__ void add_some(float (&v)[E], const typename Elem<DT>::type* p, bool vec, uint32_t left) {
     typedef typename Elem<DT>::type T;
-    const uint32_t left = a.outs - m, wide = GATED ? 2 * a.outs : a.outs;
-    const bool quads = a.quads;
-    if (a.bias[r.rank] != nullptr) {
-        const T* b = static_cast<const T*>(a.bias[r.rank]) + uint64_t(r.run) * wide + m;
-        z += load_four<DT>(b, quads, left);
-        if (GATED) u += load_four<DT>(b + a.outs, quads, left);
-    }
-    if (a.pre[r.rank] != nullptr) {
-        T* p = static_cast<T*>(a.pre[r.rank]) + row * wide + m;
-        store_four<DT>(p, z, quads, left);
-        if (GATED) store_four<DT>(p + a.outs, u, quads, left);
-    }
-    f32x4 y;
+    T t[E];
+    if (vec) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(p);
+        __builtin_memcpy(t, &x, 16);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; e++) y[e] = act<DT>(z[e], a.act) * (GATED ? u[e] : 1.f);
-    if (a.residual[r.rank] != nullptr) y += load_four<DT>(static_cast<const T*>(a.residual[r.rank]) + row * a.outs + m, quads, left);
-    store_four<DT>(static_cast<T*>(a.y[r.rank]) + row * a.outs + m, y, quads, left);
+        for (int e = 0; e < E; e++) t[e] = uint32_t(e) < left ? p[e] : T(0);
+    }
+#pragma unroll
+    for (int e = 0; e < E; e++) v[e] += Elem<DT>::get(t[e]);
+}
+template <int DT, int E>
+__device__ __forceinline__ void store_some(typename Elem<DT>::type* p, const float (&v)[E], bool vec, uint32_t left) {
+    typedef typename Elem<DT>::type T;
+    T t[E];
+#pragma unroll
+    for (int e = 0; e < E; e++) t[e] = Elem<DT>::put(v[e]);
+    if (vec) {
+        u32x4 x;
+        __builtin_memcpy(&x, t, 16);
+        *reinterpret_cast<u32x4*>(p) = x;
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            if (uint32_t(e) < left) p[e] = t[e];
+    }
+}
+
+// Bias, activation and residual of a tile.  The sums go through the wave's room in
+// LDS, 16 rows of up to 64 features at a time, so that a lane has 16 bytes of
+// neighbouring features of y, and whole lines are read and written.  One copy of
+// the arithmetic for all of them: unrolled over the tile it did not fit the
+// registers.
+template <int DT, typename S, bool GATED>
+__device__ __forceinline__ void epilogue(const LinearArgs& a, const LinearTile& t, const f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
+    typedef typename Elem<DT>::type T;
+    constexpr int E = 16 / int(sizeof(T)), step = GATED ? 2 : 1;
+    constexpr int F = S::WM < 64 ? S::WM : 64, passes = S::WM / F, chunks = F / 4;   // features of acc in a pass
+    constexpr uint32_t per_row = F / step / E, all = 16 * per_row;
+    const uint32_t lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t nleft = t.r.count - t.n0, wide = step * a.outs;
+    const uint64_t row0 = t.r.lo + t.n0;
+    const bool vec = a.vecs;
+    const T* bias = a.bias[t.r.rank] != nullptr ? static_cast<const T*>(a.bias[t.r.rank]) + uint64_t(t.r.run) * wide : nullptr;
+    const T* residual = static_cast<const T*>(a.residual[t.r.rank]);
+    T* pre = static_cast<T*>(a.pre[t.r.rank]);
+    T* out = static_cast<T*>(a.y[t.r.rank]);
+    // 16 bytes (four sums) c of row n of the room
+    auto place = [&](uint32_t n, uint32_t c) { return n * chunks + (c ^ (n & (chunks - 1))); };
+#pragma unroll 1
+    for (int pass = 0; pass < S::NI * passes; pass++) {
+        const int j = pass / passes, h = pass % passes;
+#pragma unroll
+        for (int jj = 0; jj < S::NI; jj++)
+#pragma unroll
+            for (int hh = 0; hh < passes; hh++)
+                if (j == jj && h == hh) {
+#pragma unroll
+                    for (int q = 0; q < F / 16; q++) room[place(lane & 15, 4 * q + (lane >> 4))] = __builtin_bit_cast(u32x4, acc[hh * (F / 16) + q][jj]);
+                }
+#pragma unroll 1
+        for (uint32_t i = lane; i < all; i += 64) {
+            const uint32_t row = i / per_row, f = i % per_row * E;
+            const uint32_t n = (wave / S::GM) * S::WN + j * 16 + row, m = t.m0 + ((wave % S::GM) * S::WM + h * F) / step + f;
+            float z[E], u[E];
+            // gated: 16 features' gates and their 16 linear parts lie in turn
+            const uint32_t c = GATED ? (f / 16) * 8 + f % 16 / 4 : f / 4;
+#pragma unroll
+            for (int k = 0; k < E / 4; k++) {
+                const f32x4 v = __builtin_bit_cast(f32x4, room[place(row, c + k)]);
+                const f32x4 w = GATED ? __builtin_bit_cast(f32x4, room[place(row, c + 4 + k)]) : v;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    z[4 * k + e] = v[e];
+                    u[4 * k + e] = w[e];
+                }
+            }
+            if (n >= nleft || m >= a.outs) continue;
+            const uint32_t left = a.outs - m;
+            if (bias != nullptr) {
+                add_some<DT, E>(z, bias + m, vec, left);
+                if (GATED) add_some<DT, E>(u, bias + a.outs + m, vec, left);
+            }
+            const uint64_t at = row0 + n;
+            if (pre != nullptr) {
+                store_some<DT, E>(pre + at * wide + m, z, vec, left);
+                if (GATED) store_some<DT, E>(pre + at * wide + a.outs + m, u, vec, left);
+            }
+            if (a.act == DT_ACT_GELU) {
+#pragma unroll
+                for (int e = 0; e < E; e++) z[e] = act(z[e], DT_ACT_GELU);
+            } else if (a.act == DT_ACT_SILU) {
+#pragma unroll
+                for (int e = 0; e < E; e++) z[e] = act(z[e], DT_ACT_SILU);
+            } else if (a.act == DT_ACT_RELU) {
+#pragma unroll
+                for (int e = 0; e < E; e++) z[e] = act(z[e], DT_ACT_RELU);
+            }
+            if (GATED) {
+#pragma unroll
+                for (int e = 0; e < E; e++) z[e] *= u[e];
+            }
+            if (residual != nullptr) add_some<DT, E>(z, residual + at * a.outs + m, vec, left);
+            store_some<DT, E>(out + at * a.outs + m, z, vec, left);
+        }
+    }
 }
 
 // PATH: rows on 16-byte boundaries, on 4-byte boundaries, or on any.
@@ -213,52 +373,34 @@ template <int DT, typename S, int PATH, bool GATED>
 __global__ __launch_bounds__(S::threads) void k_linear(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t BM = GATED ? S::BM / 2 : S::BM;   // features of a tile
-    __shared__ uint32_t first[kMaxRuns + 1];
-    count_tiles(a, S::BN, first);
-    const uint32_t groups = a.runs * a.nranks, nts = __builtin_amdgcn_readfirstlane(first[groups]), mts = (a.outs + BM - 1) / BM;
+    __shared__ Runs runs;
+    RowTiles<BM, S::BN> tiles(a, runs, a.outs);
     const uint32_t pitch = a.cols * uint32_t(sizeof(T)), steps = (pitch + kStepBytes - 1) / kStepBytes;
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint32_t id = blockIdx.x; id < mts * nts; id += gridDim.x) {
-        uint32_t mt, nt;
-        tile_of(id, mts, nts, mt, nt);
-        const uint32_t g = run_of_tile(first, groups, nt);
-        const Run r = same(run_at(a, g));
-        const uint32_t m0 = mt * BM, n0 = (nt - __builtin_amdgcn_readfirstlane(first[g])) * S::BN;
-        const uint32_t mleft = a.outs - m0, nleft = r.count - n0, nrows = nleft < S::BN ? nleft : S::BN;
-        const char* w = static_cast<const char*>(a.weight[r.rank]) + (uint64_t(r.run) * (GATED ? 2 : 1) * a.outs + m0) * pitch;
-        const char* x = static_cast<const char*>(a.x[r.rank]) + uint64_t(r.lo + n0) * pitch;
-        f32x4 acc[S::MI][S::NI];
-        if constexpr (PATH == kLoose) {
-            loose_tile<DT, S, kRows, kRows>(LooseRows{w, mleft < BM ? mleft : BM, pitch, GATED ? a.outs : 0}, LooseRows{x, nrows, pitch, 0}, steps, acc);
-        } else {
-            constexpr bool TAIL = PATH == kTail;
-            const uint32_t whole = (pitch + 15) / 16 * 16, mrows = mleft < BM ? mleft : BM;
-            const RowOperand<TAIL> B{x, nrows, pitch, whole, pitch};
-            if constexpr (GATED) {
-                GatedOperand<TAIL> A;
-                A.p = w;
-                A.rows = a.outs + mrows;
-                A.pitch = pitch;
-                A.bytes = whole;
-                A.valid = pitch;
-                A.half = a.outs * pitch;
-                matrix_tile<DT, S, kRows, kRows>(A, B, 0, steps, acc);
-            } else {
-                matrix_tile<DT, S, kRows, kRows>(RowOperand<TAIL>{w, mrows, pitch, whole, pitch}, B, 0, steps, acc);
-            }
+    auto weight_of = [&](const LinearTile& t) {
+        return static_cast<const char*>(a.weight[t.r.rank]) + (uint64_t(t.r.run) * (GATED ? 2 : 1) * a.outs + t.m0) * pitch;
+    };
+    auto x_of = [&](const LinearTile& t) { return static_cast<const char*>(a.x[t.r.rank]) + uint64_t(t.r.lo + t.n0) * pitch; };
+    auto features_of = [&](const LinearTile& t) { return a.outs - t.m0 < BM ? a.outs - t.m0 : BM; };
+    auto rows_of = [&](const LinearTile& t) { return t.r.count - t.n0 < uint32_t(S::BN) ? t.r.count - t.n0 : uint32_t(S::BN); };
+    auto done = [&](const LinearTile& t, f32x4 (&acc)[S::MI][S::NI], u32x4* room) { epilogue<DT, S, GATED>(a, t, acc, room); };
+    if constexpr (PATH == kLoose) {
+        for (LinearTile t; tiles(t);) {
+            f32x4 acc[S::MI][S::NI];
+            u32x4* room = loose_tile<DT, S, kRows, kRows>(LooseRows{weight_of(t), features_of(t), pitch, GATED ? a.outs : 0},
+                                                          LooseRows{x_of(t), rows_of(t), pitch, 0}, steps, acc);
+            done(t, acc, room);
         }
-        // acc[i][j][e]: feature row WM (wave % GM) + 16 i + 4 (lane / 16) + e of the tile, token WN (wave / GM) + 16 j + lane % 16
-#pragma unroll
-        for (int j = 0; j < S::NI; j++) {
-            const uint32_t n = (wave / S::GM) * S::WN + j * 16 + (lane & 15);
-            if (n >= nleft) continue;
-#pragma unroll
-            for (int i = 0; i < S::MI; i += GATED ? 2 : 1) {
-                const uint32_t ml = ((wave % S::GM) * S::WM + i * 16) / (GATED ? 2 : 1) + (lane >> 4) * 4;
-                if (ml >= mleft) continue;
-                finish<DT, GATED>(a, r, r.lo + n0 + n, m0 + ml, acc[i][j], acc[GATED ? i + 1 : i][j]);
-            }
-        }
+    } else {
+        constexpr bool TAIL = PATH == kTail;
+        typedef typename std::conditional<GATED, GatedOperand<TAIL>, RowOperand<TAIL>>::type OA;
+        typedef RowOperand<TAIL> OB;
+        const uint32_t whole = (pitch + 15) / 16 * 16;
+        matrix_walk<DT, S, kRows, kRows, OA, OB, LinearTile>(tiles, [&](const LinearTile& t, OA& A, OB& B) {
+            static_cast<RowOperand<TAIL>&>(A) = RowOperand<TAIL>{weight_of(t), (GATED ? a.outs : 0) + features_of(t), pitch, whole, pitch};
+            if constexpr (GATED) A.half = a.outs * pitch;
+            B = OB{x_of(t), rows_of(t), pitch, whole, pitch};
+            return steps;
+        }, rows_of, done);
     }
 }
 
@@ -270,18 +412,18 @@ constexpr uint32_t kDzRows = 64;
 template <int DT, bool GATED>
 __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
     typedef typename Elem<DT>::type T;
-    __shared__ uint32_t first[kMaxRuns + 1];
-    count_tiles(a, kDzRows, first);
-    const uint32_t groups = a.runs * a.nranks, tiles = first[groups], m = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    __shared__ Runs runs;
+    count_tiles(a, kDzRows, runs);
+    const uint32_t groups = a.runs * a.nranks, tiles = runs.first[groups], m = (blockIdx.x * kThreads + threadIdx.x) * 4;
     const uint32_t wide = GATED ? 2 * a.outs : a.outs;
     const uint64_t ldz = a.zpitch / sizeof(T);
     const bool quads = a.quads;
     if (m >= a.outs) return;
     const uint32_t left = a.outs - m;
     for (uint32_t t = blockIdx.y; t < tiles; t += gridDim.y) {
-        const uint32_t g = run_of_tile(first, groups, t);
-        const Run r = same(run_at(a, g));
-        const uint32_t n0 = (t - first[g]) * kDzRows, rows = r.count - n0 < kDzRows ? r.count - n0 : kDzRows;
+        const uint32_t g = run_of_tile(runs.first, groups, t);
+        const Run r = run_of(a, runs, g);
+        const uint32_t n0 = (t - runs.first[g]) * kDzRows, rows = r.count - n0 < kDzRows ? r.count - n0 : kDzRows;
         const uint64_t row0 = r.lo + n0;
         const T* dy = static_cast<const T*>(a.dy[r.rank]) + row0 * a.outs + m;
         const T* pre = a.need_dz ? static_cast<const T*>(a.saved[r.rank]) + row0 * wide + m : nullptr;
@@ -296,7 +438,7 @@ __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         float value, slope;
-                        act_and_slope<DT>(z[e], a.act, value, slope);
+                        act_and_slope(z[e], a.act, value, slope);
                         du[e] = d[e] * value;
                         d[e] = d[e] * u[e] * slope;
                     }
@@ -304,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         float value, slope;
-                        act_and_slope<DT>(z[e], a.act, value, slope);
+                        act_and_slope(z[e], a.act, value, slope);
                         d[e] *= slope;
                     }
                 }
@@ -333,12 +475,12 @@ __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
 template <int DT>
 __global__ __launch_bounds__(kThreads) void k_linear_dbias(LinearArgs a) {
     typedef typename Elem<DT>::type T;
-    __shared__ uint32_t first[kMaxRuns + 1];
-    count_tiles(a, kDzRows, first);
+    __shared__ Runs runs;
+    count_tiles(a, kDzRows, runs);
     const uint32_t wide = (a.gated ? 2 : 1) * a.outs, c = blockIdx.x * kThreads + threadIdx.x, g = blockIdx.y;
     if (c >= wide) return;
     float s = 0.f;
-    for (uint32_t t = first[g]; t < first[g + 1]; t++) s += a.partial[uint64_t(t) * wide + c];
+    for (uint32_t t = runs.first[g]; t < runs.first[g + 1]; t++) s += a.partial[uint64_t(t) * wide + c];
     static_cast<T*>(a.dbias[g / a.runs])[uint64_t(g % a.runs) * wide + c] = Elem<DT>::put(s);
 }
 
@@ -349,46 +491,64 @@ __device__ __forceinline__ const char* dz_row(const LinearArgs& a, const Run& r,
                      : static_cast<const char*>(a.dy[r.rank]) + uint64_t(r.lo + row) * a.zpitch;
 }
 
+// A tile's sums to rows of `cols` elements from `out` on, row n0, column m0.
+template <int DT, typename S, bool ROOM>
+__device__ __forceinline__ void store_tile(const LinearArgs& a, typename Elem<DT>::type* out, uint32_t m0, uint32_t n0, uint32_t nleft,
+                                           const f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
+    const uint32_t lane = fresh_lane(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t mw = m0 + (wave % S::GM) * S::WM, nw = (wave / S::GM) * S::WN, cols = a.cols;
+#pragma unroll
+    for (int j = 0; j < S::NI; j++) {
+        if (ROOM && a.col_vecs) {
+            f32x4 v[S::MI];
+#pragma unroll
+            for (int i = 0; i < S::MI; i++) v[i] = acc[i][j];
+            turn_rows<DT, S::WM>(room, v, [&](uint32_t row, uint32_t m, u32x4 x) {
+                const uint32_t n = nw + j * 16 + row;
+                if (n < nleft && mw + m < cols) *reinterpret_cast<u32x4*>(out + uint64_t(n0 + n) * cols + mw + m) = x;
+            });
+            continue;
+        }
+        const uint32_t n = nw + j * 16 + (lane & 15);
+        if (n >= nleft) continue;
+#pragma unroll
+        for (int i = 0; i < S::MI; i++) {
+            const uint32_t m = mw + i * 16 + (lane >> 4) * 4;
+            if (m >= cols) continue;
+            store_four<DT>(out + uint64_t(n0 + n) * cols + m, acc[i][j], a.col_quads, cols - m);
+        }
+    }
+}
+
 // dx[t][k] = sum over the features of dz[t][m] W[m][k].
 template <int DT, typename S, int PATH>
 __global__ __launch_bounds__(S::threads) void k_linear_dx(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t es = sizeof(T);
-    __shared__ uint32_t first[kMaxRuns + 1];
-    count_tiles(a, S::BN, first);
-    const uint32_t groups = a.runs * a.nranks, nts = __builtin_amdgcn_readfirstlane(first[groups]), mts = (a.cols + S::BM - 1) / S::BM;
+    __shared__ Runs runs;
+    RowTiles<S::BM, S::BN> tiles(a, runs, a.cols);
     const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es, steps = (wide * es + kStepBytes - 1) / kStepBytes;
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint32_t id = blockIdx.x; id < mts * nts; id += gridDim.x) {
-        uint32_t mt, nt;
-        tile_of(id, mts, nts, mt, nt);
-        const uint32_t g = run_of_tile(first, groups, nt);
-        const Run r = same(run_at(a, g));
-        const uint32_t m0 = mt * S::BM, n0 = (nt - __builtin_amdgcn_readfirstlane(first[g])) * S::BN;
-        const uint32_t nleft = r.count - n0, nrows = nleft < S::BN ? nleft : S::BN;
-        const char* w = static_cast<const char*>(a.weight[r.rank]) + uint64_t(r.run) * wide * pitch + m0 * es;
-        const char* d = dz_row<T>(a, r, n0);
-        f32x4 acc[S::MI][S::NI];
-        if constexpr (PATH == kLoose) {
-            loose_tile<DT, S, kCols, kRows>(LooseCols{w, wide, pitch, pitch - m0 * es}, LooseRows{d, nrows, a.zpitch, 0}, steps, acc);
-        } else {
-            const ColOperand<kStepBytes / int(es), 1> A{w, wide, pitch, m0 * es, 0};
-            const RowOperand<PATH == kTail> B{d, nrows, a.zpitch, (a.zpitch + 15) / 16 * 16, wide * es};
-            matrix_tile<DT, S, kCols, kRows>(A, B, 0, steps, acc);
+    auto weight_of = [&](const LinearTile& t) {
+        return static_cast<const char*>(a.weight[t.r.rank]) + uint64_t(t.r.run) * wide * pitch + t.m0 * es;
+    };
+    auto rows_of = [&](const LinearTile& t) { return t.r.count - t.n0 < uint32_t(S::BN) ? t.r.count - t.n0 : uint32_t(S::BN); };
+    auto done = [&](const LinearTile& t, f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
+        store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dx[t.r.rank]) + uint64_t(t.r.lo) * a.cols, t.m0, t.n0, t.r.count - t.n0, acc, room);
+    };
+    if constexpr (PATH == kLoose) {
+        for (LinearTile t; tiles(t);) {
+            f32x4 acc[S::MI][S::NI];
+            loose_tile<DT, S, kCols, kRows>(LooseCols{weight_of(t), wide, pitch, pitch - t.m0 * es}, LooseRows{dz_row<T>(a, t.r, t.n0), rows_of(t), a.zpitch, 0}, steps, acc);
+            done(t, acc, nullptr);
         }
-        T* out = static_cast<T*>(a.dx[r.rank]);
-        const bool quads = a.col_quads;
-#pragma unroll
-        for (int j = 0; j < S::NI; j++) {
-            const uint32_t n = (wave / S::GM) * S::WN + j * 16 + (lane & 15);
-            if (n >= nleft) continue;
-#pragma unroll
-            for (int i = 0; i < S::MI; i++) {
-                const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
-                if (m >= a.cols) continue;
-                store_four<DT>(out + uint64_t(r.lo + n0 + n) * a.cols + m, acc[i][j], quads, a.cols - m);
-            }
-        }
+    } else {
+        typedef ColOperand<kStepBytes / int(es), 1> OA;
+        typedef RowOperand<PATH == kTail> OB;
+        matrix_walk<DT, S, kCols, kRows, OA, OB, LinearTile>(tiles, [&](const LinearTile& t, OA& A, OB& B) {
+            A = OA{weight_of(t), wide, pitch, t.m0 * es, 0};
+            B = OB{dz_row<T>(a, t.r, t.n0), rows_of(t), a.zpitch, (a.zpitch + 15) / 16 * 16, wide * es};
+            return steps;
+        }, rows_of, done);
     }
 }
 
@@ -397,35 +557,28 @@ template <int DT, typename S, int PATH>
 __global__ __launch_bounds__(S::threads) void k_linear_dweight(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t es = sizeof(T), KR = kStepBytes / es;
+    __shared__ Runs runs;
     const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es;
-    const uint32_t mts = (a.cols + S::BM - 1) / S::BM, each = (wide + S::BN - 1) / S::BN, nts = each * a.runs * a.nranks;
-    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    for (uint64_t at = blockIdx.x; at < uint64_t(mts) * nts; at += gridDim.x) {
-        uint32_t mt, nt;
-        tile_of(uint32_t(at), mts, nts, mt, nt);
-        const Run r = same(run_at(a, nt / each));
-        const uint32_t m0 = mt * S::BM, n0 = nt % each * S::BN, steps = (r.count + KR - 1) / KR;
-        const char* x = static_cast<const char*>(a.x[r.rank]) + uint64_t(r.lo) * pitch + m0 * es;
-        const char* d = dz_row<T>(a, r, 0) + n0 * es;
-        f32x4 acc[S::MI][S::NI];
-        if constexpr (PATH == kLoose) {
-            loose_tile<DT, S, kCols, kCols>(LooseCols{x, r.count, pitch, pitch - m0 * es}, LooseCols{d, r.count, a.zpitch, (wide - n0) * es}, steps, acc);
-        } else {
-            matrix_tile<DT, S, kCols, kCols>(ColOperand<KR, 1>{x, r.count, pitch, m0 * es, 0}, ColOperand<KR, 1>{d, r.count, a.zpitch, n0 * es, 0}, 0, steps, acc);
+    WeightTiles<S::BM, S::BN> tiles(a, runs, a.cols, wide);
+    auto x_of = [&](const LinearTile& t) { return static_cast<const char*>(a.x[t.r.rank]) + uint64_t(t.r.lo) * pitch + t.m0 * es; };
+    auto dz_of = [&](const LinearTile& t) { return dz_row<T>(a, t.r, 0) + t.n0 * es; };
+    auto done = [&](const LinearTile& t, f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
+        store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dweight[t.r.rank]) + uint64_t(t.r.run) * wide * a.cols, t.m0, t.n0, wide - t.n0, acc, room);
+    };
+    if constexpr (PATH == kLoose) {
+        for (LinearTile t; tiles(t);) {
+            f32x4 acc[S::MI][S::NI];
+            loose_tile<DT, S, kCols, kCols>(LooseCols{x_of(t), t.r.count, pitch, pitch - t.m0 * es}, LooseCols{dz_of(t), t.r.count, a.zpitch, (wide - t.n0) * es},
+                                            (t.r.count + KR - 1) / KR, acc);
+            done(t, acc, nullptr);
         }
-        T* out = static_cast<T*>(a.dweight[r.rank]) + uint64_t(r.run) * wide * a.cols;
-        const bool quads = a.col_quads;
-#pragma unroll
-        for (int j = 0; j < S::NI; j++) {
-            const uint32_t n = n0 + (wave / S::GM) * S::WN + j * 16 + (lane & 15);
-            if (n >= wide) continue;
-#pragma unroll
-            for (int i = 0; i < S::MI; i++) {
-                const uint32_t m = m0 + (wave % S::GM) * S::WM + i * 16 + (lane >> 4) * 4;
-                if (m >= a.cols) continue;
-                store_four<DT>(out + uint64_t(n) * a.cols + m, acc[i][j], quads, a.cols - m);
-            }
-        }
+    } else {
+        typedef ColOperand<KR, 1> OP;
+        matrix_walk<DT, S, kCols, kCols, OP, OP, LinearTile>(tiles, [&](const LinearTile& t, OP& A, OP& B) {
+            A = OP{x_of(t), t.r.count, pitch, t.m0 * es, 0};
+            B = OP{dz_of(t), t.r.count, a.zpitch, t.n0 * es, 0};
+            return (t.r.count + KR - 1) / KR;
+        }, [&](const LinearTile& t) { return wide - t.n0; }, done);
     }
 }
 
@@ -438,7 +591,7 @@ typedef Shape<64, 64, 2, 2> Small;
 typedef Shape<64, 16, 1, 1> Tiny;
 enum Tile { kWide, kSquare, kSmall, kTiny };
 constexpr uint32_t kTileM[] = {256, 128, 64, 64}, kTileN[] = {256, 128, 64, 16};
-constexpr uint32_t kTilesPerCu[] = {1, 2, 4, 7};   // workgroups of a tile's LDS that share a CU
+constexpr uint32_t kTilesPerCu[] = {1, 2, 4, 6};   // workgroups of a tile's LDS that share a CU
 
 // The tile for products of m features with runs of `mean` rows each.
 Tile pick_tile(int dtype, uint64_t m, uint64_t mean, uint64_t groups, int path) {
@@ -480,7 +633,7 @@ template <int DT>
 hipError_t forward(LinearArgs a, hipStream_t s) {
     constexpr uint64_t es = sizeof(typename Elem<DT>::type);
     const uint64_t rows = a.rows.start[a.nranks], groups = uint64_t(a.runs) * a.nranks;
-    a.quads = a.outs % 4 == 0 && on(a.bias, a.nranks, 4 * es) && on(a.residual, a.nranks, 4 * es) && on(a.y, a.nranks, 4 * es) && on(a.pre, a.nranks, 4 * es);
+    a.vecs = a.outs * es % 16 == 0 && on(a.y, a.nranks, 16) && on(a.pre, a.nranks, 16) && on(a.bias, a.nranks, 16) && on(a.residual, a.nranks, 16);
     const uint64_t features = uint64_t(a.outs) * (a.gated ? 2 : 1);
     with_path(path_of(a.cols * es, on(a.x, a.nranks, 4) && on(a.weight, a.nranks, 4)), [&](auto path) {
         constexpr int P = decltype(path)::value;
@@ -523,6 +676,7 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
     a.zpitch = uint32_t(a.need_dz ? up(wide * es, 16) : wide * es);
     a.partial = dbias ? reinterpret_cast<float*>(workspace + b.partial) : nullptr;
     a.quads = a.outs % 4 == 0 && on(a.dy, a.nranks, 4 * es) && (!a.need_dz || on(a.saved, a.nranks, 4 * es));
+    a.col_vecs = a.cols * es % 16 == 0 && on(a.dx, a.nranks, 16) && on(a.dweight, a.nranks, 16);
     a.col_quads = a.cols % 4 == 0 && on(a.dx, a.nranks, 4 * es) && on(a.dweight, a.nranks, 4 * es);
     if (rows > 0 && (a.need_dz || dbias)) {
         const uint64_t tiles = dz_tiles(a.rows, a.nranks, a.runs), across = ceil_div(a.outs, 4 * kThreads), most = ceil_div(4096, across);
@@ -552,7 +706,7 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
         with_tile<DT, P>(t, [&](auto shape) {
             typedef decltype(shape) S;
             if constexpr (!std::is_same<S, Tiny>::value)
-                hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, kTileM[t]) * ceil_div(wide, kTileN[t]) * groups, t)),
+                hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)),
                                    dim3(S::threads), 0, s, a);
         });
     };

@@ -26,12 +26,83 @@ namespace {
 
 enum { kNoGate = 0, kChannelGate = 1, kRowGate = 2 };
 
-// Sums of two values over the WPR waves that hold a row.
-template <int WPR>
-__device__ __forceinline__ void row_sums(float& u, float& v, float (*cells)[Group<WPR>::waves]) {
-    u = wave_sum(u);
-    v = wave_sum(v);
-    if constexpr (WPR > 1) {
+// A row is shared by L lanes: 8 or 16 (several rows to a wave), a wave, or several
+// waves, then the workgroup's all.
+template <int L>
+struct Share {
+    static constexpr int waves = L <= 64 ? 4 : L / 64, threads = waves * 64, rows = threads / L;
+};
+
+// Rows of a wave or more are buffer resources; narrower ones are plain addresses.
+struct NarrowRow {
+    char* p;
+    uint32_t bytes;
+};
+template <int DT, bool VEC, int POL>
+__device__ __forceinline__ Unit<DT> load_unit(const NarrowRow& row, uint32_t u) {
+    Unit<DT> x;
+    u32x4 v = {0, 0, 0, 0};
+    if constexpr (VEC) {
+        if (u * 16 < row.bytes) v = load16_h<POL != 0>(row.p + u * 16);
+    } else {
+        v = load_loose<int(sizeof(typename Unit<DT>::T))>(row.p, u, row.bytes);
+    }
+    __builtin_memcpy(x.v, &v, 16);
+    return x;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_unit(const NarrowRow& row, uint32_t u, const Unit<DT>& x) {
+    u32x4 v;
+    __builtin_memcpy(&v, x.v, 16);
+    if constexpr (VEC) {
+        if (u * 16 < row.bytes) store16(row.p + u * 16, v);
+    } else {
+        store_loose<int(sizeof(typename Unit<DT>::T))>(row.p, u, row.bytes, v);
+    }
+}
+template <int L>
+__device__ __forceinline__ auto shared_row(const void* base, uint64_t row, uint32_t pitch) {
+    if constexpr (L < 64) return NarrowRow{const_cast<char*>(static_cast<const char*>(base)) + row * pitch, pitch};
+    else return row_at(base, row, pitch);
+}
+
+// A unit's values rounded to the type, two to an instruction.
+template <int DT>
+__device__ __forceinline__ Unit<DT> rounded(const float (&v)[Unit<DT>::elems]) {
+    Unit<DT> o;
+    if constexpr (DT == kBF16) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        bf16x2 t[Unit<DT>::elems / 2];
+#pragma unroll
+        for (int e = 0; e < Unit<DT>::elems / 2; e++) t[e] = bf16x2{__bf16(v[2 * e]), __bf16(v[2 * e + 1])};
+        __builtin_memcpy(o.v, t, 16);
+    } else {
+        __builtin_memcpy(o.v, v, 16);
+    }
+    return o;
+}
+
+// Sums over a row's lanes, the same in all of them.
+template <int L>
+__device__ __forceinline__ float row_total(float v, float* cell) {
+    if constexpr (L == 8) {
+        v += dpp<kSwap1>(v);
+        v += dpp<kSwap2>(v);
+        return v + dpp<kHalfMirror>(v);
+    } else if constexpr (L == 16) {
+        return sum16(v);
+    } else {
+        return row_sum<L / 64>(v, cell);
+    }
+}
+template <int L>
+__device__ __forceinline__ void row_totals(float& u, float& v, float (*cells)[Share<L>::waves]) {
+    if constexpr (L <= 64) {
+        u = row_total<L>(u, nullptr);
+        v = row_total<L>(v, nullptr);
+    } else {
+        u = wave_sum(u);
+        v = wave_sum(v);
         if ((threadIdx.x & 63) == 0) {
             cells[0][threadIdx.x >> 6] = u;
             cells[1][threadIdx.x >> 6] = v;
@@ -39,11 +110,16 @@ __device__ __forceinline__ void row_sums(float& u, float& v, float (*cells)[Grou
         __syncthreads();
         u = v = 0.f;
 #pragma unroll
-        for (int k = 0; k < WPR; k++) {
+        for (int k = 0; k < L / 64; k++) {
             u += cells[0][k];
             v += cells[1][k];
         }
     }
+}
+template <int L>
+__device__ __forceinline__ uint32_t first_row() {
+    const uint32_t mine = threadIdx.x / L;   // 0 where the workgroup shares a row
+    return blockIdx.x * Share<L>::rows + (L < 64 ? mine : uint32_t(__builtin_amdgcn_readfirstlane(mine)));
 }
 
 template <int DT, bool VEC, int NV>
@@ -53,40 +129,52 @@ struct Units {
     template <int L, int POL>
     __device__ __forceinline__ void load(bool there, const void* base, uint64_t row, uint32_t pitch, uint32_t lane) {
         if (!there) return;
-        const Row r = row_at(base, row, pitch);
+        const auto r = shared_row<L>(base, row, pitch);
 #pragma unroll
         for (int i = 0; i < NV; i++) v[i] = load_unit<DT, VEC, POL>(r, lane + i * L);
     }
 };
 
 // ---------------------------------------------------------------- forward --
-template <int DT, bool VEC, int NV, int WPR>
-__global__ __launch_bounds__(Group<WPR>::threads) void k_block(BlockArgs a) {
+// More than one unit per lane of a full workgroup leaves no registers for the next
+// row's loads and the weights: those are read again for every row, from the cache.
+template <int DT, bool VEC, int NV, int L>
+__global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
     typedef Unit<DT> U;
-    constexpr int E = U::elems, L = Group<WPR>::lanes;
-    __shared__ float cells[2][4][Group<WPR>::waves];
-    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Group<WPR>::rows;
+    constexpr int E = U::elems;
+    __shared__ float cells[2][4][Share<L>::waves];
+    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Share<L>::rows;
     const uint32_t total = a.rows.start[a.nranks], pitch = a.cols * uint32_t(sizeof(typename U::T));
-    uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
+    uint32_t row = first_row<L>();
     if (row >= total) return;
     int r = rank_of_row(a.rows, a.nranks, row);
     const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = a.post_bias[r] != nullptr, b2 = a.pre_bias[r] != nullptr;
     const bool rms = a.rms, shared_gate = a.gate_kind == kChannelGate, row_gate = a.gate_kind == kRowGate;
+    constexpr bool HELD = NV == 1 || L < 1024;
+    const void *w1_at = a.post_weight[r], *c1_at = a.post_bias[r], *w2_at = a.pre_weight[r], *c2_at = a.pre_bias[r], *gate_at = a.gate[r];
     Units<DT, VEC, NV> w1, c1, w2, c2, gate, z, x;
-    w1.template load<L, 0>(post, a.post_weight[r], 0, pitch, lane);
-    c1.template load<L, 0>(b1, a.post_bias[r], 0, pitch, lane);
-    w2.template load<L, 0>(pre, a.pre_weight[r], 0, pitch, lane);
-    c2.template load<L, 0>(b2, a.pre_bias[r], 0, pitch, lane);
-    gate.template load<L, 0>(shared_gate, a.gate[r], 0, pitch, lane);
+    if constexpr (HELD) {
+        w1.template load<L, 0>(post, w1_at, 0, pitch, lane);
+        c1.template load<L, 0>(b1, c1_at, 0, pitch, lane);
+        w2.template load<L, 0>(pre, w2_at, 0, pitch, lane);
+        c2.template load<L, 0>(b2, c2_at, 0, pitch, lane);
+        gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
+    }
     auto fetch = [&](uint64_t at) {
         z.template load<L, kPolNT>(true, a.z[r], at, pitch, lane);
         x.template load<L, kPolNT>(true, a.x[r], at, pitch, lane);
         gate.template load<L, kPolNT>(row_gate, a.gate[r], at, pitch, lane);
     };
-    fetch(row - a.rows.start[r]);
+    if constexpr (HELD) fetch(row - a.rows.start[r]);
     const float inv = 1.f / float(a.cols), scale = a.scale;
-    auto inside = [&](int i, int e) { return (lane + i * L) * E + e < a.cols; };
+    // whole units are inside a row that is one of them, or outside
+    auto inside = [&](int i, int e) { return (lane + i * L) * E + (VEC ? 0 : e) < a.cols; };
     for (int parity = 0; row < total; parity ^= 1) {
+        if constexpr (!HELD) {
+            while (row >= a.rows.start[r + 1]) r++;
+            fetch(row - a.rows.start[r]);
+            gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
+        }
         float v[NV][E], h[NV][E], f[NV][E];
 #pragma unroll
         for (int i = 0; i < NV; i++)
@@ -99,7 +187,7 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block(BlockArgs a) {
         const int now = r;
         const uint64_t local = row - a.rows.start[now];
         const uint32_t next = row + step;
-        if (next < total) {
+        if (HELD && next < total) {
             while (next >= a.rows.start[r + 1]) r++;
             fetch(next - a.rows.start[r]);
         }
@@ -112,24 +200,28 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block(BlockArgs a) {
 #pragma unroll
                 for (int i = 0; i < NV; i++)
 #pragma unroll
-                    for (int e = 0; e < E; e++) s += inside(i, e) ? t[i][e] : 0.f;
-                mean = row_sum<WPR>(s, cells[parity][cell]) * inv;
+                    for (int e = 0; e < E; e++) s += t[i][e];   // zeros past the row's end
+                mean = row_total<L>(s, cells[parity][cell]) * inv;
             }
             float q = 0.f;
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    t[i][e] -= mean;
-                    q += inside(i, e) ? t[i][e] * t[i][e] : 0.f;
+                    t[i][e] = inside(i, e) ? t[i][e] - mean : 0.f;
+                    q += t[i][e] * t[i][e];
                 }
-            rstd = 1.f / sqrtf(row_sum<WPR>(q, cells[parity][cell + 1]) * inv + a.eps);
+            rstd = 1.f / sqrtf(row_total<L>(q, cells[parity][cell + 1]) * inv + a.eps);
         };
         if (post) {
             float mean, rstd;
             moments(v, 0, mean, rstd);
             stats[0] = mean;
             stats[1] = rstd;
+            if constexpr (!HELD) {
+                w1.template load<L, 0>(true, w1_at, 0, pitch, lane);
+                c1.template load<L, 0>(b1, c1_at, 0, pitch, lane);
+            }
 #pragma unroll
             for (int i = 0; i < NV; i++)
 #pragma unroll
@@ -138,32 +230,32 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block(BlockArgs a) {
                     if (b1) v[i][e] += c1.v[i].get(e);
                 }
         }
-        const Row to = row_at(a.h[now], local, pitch);
+        const auto to = shared_row<L>(a.h[now], local, pitch);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
-            U o;
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                h[i][e] += f[i][e] * v[i][e];
-                o.put(e, h[i][e]);
-            }
-            store_unit<DT, VEC>(to, lane + i * L, o);
+            for (int e = 0; e < E; e++) h[i][e] += f[i][e] * v[i][e];
+            store_unit<DT, VEC>(to, lane + i * L, rounded<DT>(h[i]));
         }
         if (pre) {
             float mean, rstd;
             moments(h, 2, mean, rstd);
             stats[2] = mean;
             stats[3] = rstd;
-            const Row out = row_at(a.y[now], local, pitch);
+            if constexpr (!HELD) {
+                w2.template load<L, 0>(true, w2_at, 0, pitch, lane);
+                c2.template load<L, 0>(b2, c2_at, 0, pitch, lane);
+            }
+            const auto out = shared_row<L>(a.y[now], local, pitch);
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                U o;
+                float y[E];
 #pragma unroll
                 for (int e = 0; e < E; e++) {
-                    const float n = h[i][e] * rstd * w2.v[i].get(e);
-                    o.put(e, b2 ? n + c2.v[i].get(e) : n);
+                    y[e] = h[i][e] * rstd * w2.v[i].get(e);
+                    if (b2) y[e] += c2.v[i].get(e);
                 }
-                store_unit<DT, VEC>(out, lane + i * L, o);
+                store_unit<DT, VEC>(out, lane + i * L, rounded<DT>(y));
             }
         }
         if (lane == 0 && a.stats[now] != nullptr) {
@@ -178,31 +270,43 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block(BlockArgs a) {
 // What a gradient of all rows is summed into, in the strips' order.
 enum { kPostWeight, kPostBias, kPreWeight, kPreBias, kGate, kSums };
 
-template <int DT, bool VEC, int NV, int WPR>
-__global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBackArgs a) {
+// SUM: the sums over the rows too; without, two sums of each row are left for
+// k_block_columns.  BIAS: biases, or sums for them, are among the arguments, and
+// take registers that others then do without.
+template <int DT, bool VEC, int NV, int L, bool SUM, bool BIAS>
+__global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackArgs a) {
     typedef Unit<DT> U;
-    constexpr int E = U::elems, L = Group<WPR>::lanes;
-    __shared__ float cells[2][4][Group<WPR>::waves];
-    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Group<WPR>::rows;
+    constexpr int E = U::elems;
+    __shared__ float cells[2][4][Share<L>::waves];
+    const uint32_t lane = threadIdx.x % L, step = gridDim.x * Share<L>::rows;
     const uint32_t total = a.rows.start[a.nranks], pitch = a.cols * uint32_t(sizeof(typename U::T));
-    uint32_t row = blockIdx.x * Group<WPR>::rows + (WPR == 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : 0);
-    float sums[kSums][NV][E];
+    uint32_t row = first_row<L>();
+    float sums[SUM ? kSums : 1][NV][E];
 #pragma unroll
-    for (int k = 0; k < kSums; k++)
+    for (int k = 0; k < (SUM ? kSums : 1); k++)
 #pragma unroll
         for (int i = 0; i < NV; i++)
 #pragma unroll
             for (int e = 0; e < E; e++) sums[k][i][e] = 0.f;
+    auto add = [&](int k, int i, int e, float v) {
+        if constexpr (SUM) {
+            if (BIAS || (k != kPostBias && k != kPreBias)) sums[k][i][e] += v;
+        }
+    };
     if (row < total) {
         int r = rank_of_row(a.rows, a.nranks, row);
-        const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = a.post_bias[r] != nullptr;
+        const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = BIAS && a.post_bias[r] != nullptr;
         const bool rms = a.rms, shared_gate = a.gate_kind == kChannelGate, row_gate = a.gate_kind == kRowGate, gated = shared_gate || row_gate;
         const bool past = a.dh[r] != nullptr, need_z = a.z[r] != nullptr;
         Units<DT, VEC, NV> w1, c1, w2, gate, z, h, dy, dh;
-        w1.template load<L, 0>(post, a.post_weight[r], 0, pitch, lane);
-        c1.template load<L, 0>(b1, a.post_bias[r], 0, pitch, lane);
-        w2.template load<L, 0>(pre, a.pre_weight[r], 0, pitch, lane);
-        gate.template load<L, 0>(shared_gate, a.gate[r], 0, pitch, lane);
+        constexpr bool HELD = NV == 1 || L < (BIAS ? 512 : 1024);   // as in k_block
+        const void *w1_at = a.post_weight[r], *c1_at = a.post_bias[r], *w2_at = a.pre_weight[r], *gate_at = a.gate[r];
+        if constexpr (HELD) {
+            w1.template load<L, 0>(post, w1_at, 0, pitch, lane);
+            c1.template load<L, 0>(b1, c1_at, 0, pitch, lane);
+            w2.template load<L, 0>(pre, w2_at, 0, pitch, lane);
+            gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
+        }
         float m1, r1, m2, r2;
         auto fetch = [&](uint64_t at) {
             dy.template load<L, kPolNT>(pre, a.dy[r], at, pitch, lane);
@@ -217,9 +321,15 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBac
             r2 = s[3];
         };
         uint64_t local = row - a.rows.start[r];
-        fetch(local);
+        if constexpr (HELD) fetch(local);
         const float inv = 1.f / float(a.cols), scale = a.scale;
         for (int parity = 0; row < total; parity ^= 1) {
+            if constexpr (!HELD) {
+                while (row >= a.rows.start[r + 1]) r++;
+                local = row - a.rows.start[r];
+                fetch(local);
+                w2.template load<L, 0>(pre, w2_at, 0, pitch, lane);
+            }
             float d[NV][E], n[NV][E], g[NV][E];
             // dx
             if (pre) {
@@ -234,11 +344,15 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBac
                         g[i][e] = dye * w2.v[i].get(e);
                         s1 += g[i][e];
                         s2 += g[i][e] * n[i][e];
-                        sums[kPreWeight][i][e] += dye * n[i][e];
-                        sums[kPreBias][i][e] += dye;
+                        add(kPreWeight, i, e, dye * n[i][e]);
+                        add(kPreBias, i, e, dye);
                     }
-                row_sums<WPR>(s1, s2, &cells[parity][0]);
+                row_totals<L>(s1, s2, &cells[parity][0]);
                 const float mean = rms ? 0.f : s1 * inv, along = s2 * inv;
+                if (!SUM && lane == 0) {
+                    a.row_sums[uint64_t(row) * 2] = mean;
+                    a.row_sums[uint64_t(row) * 2 + 1] = along;
+                }
 #pragma unroll
                 for (int i = 0; i < NV; i++)
 #pragma unroll
@@ -249,21 +363,21 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBac
 #pragma unroll
                     for (int e = 0; e < E; e++) d[i][e] = past ? dh.v[i].get(e) : 0.f;
             }
-            const Row to = row_at(a.dx[r], local, pitch);
+            const auto to = shared_row<L>(a.dx[r], local, pitch);
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                U o;
-#pragma unroll
-                for (int e = 0; e < E; e++) o.put(e, d[i][e]);
-                store_unit<DT, VEC>(to, lane + i * L, o);
-            }
+            for (int i = 0; i < NV; i++) store_unit<DT, VEC>(to, lane + i * L, rounded<DT>(d[i]));
             // dz, and the gate's
             const int now = r;
             const uint64_t at = local;
             float t1 = 0.f, t2 = 0.f;
+            if constexpr (!HELD) {
+                w1.template load<L, 0>(post, w1_at, 0, pitch, lane);
+                c1.template load<L, 0>(b1, c1_at, 0, pitch, lane);
+                gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
+            }
 #pragma unroll
             for (int i = 0; i < NV; i++) {
-                U o;
+                float o[E];
 #pragma unroll
                 for (int e = 0; e < E; e++) {
                     n[i][e] = need_z ? z.v[i].get(e) : 0.f;
@@ -272,26 +386,26 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBac
                     if (post) p *= w1.v[i].get(e);
                     if (b1) p += c1.v[i].get(e);
                     const float dg = d[i][e] * p * scale, du = d[i][e] * (gated ? scale * gate.v[i].get(e) : scale);
-                    if (shared_gate) sums[kGate][i][e] += dg;
-                    o.put(e, dg);
+                    if (shared_gate) add(kGate, i, e, dg);
+                    o[e] = dg;
                     g[i][e] = post ? du * w1.v[i].get(e) : du;
-                    sums[kPostWeight][i][e] += du * n[i][e];
-                    sums[kPostBias][i][e] += du;
+                    add(kPostWeight, i, e, du * n[i][e]);
+                    add(kPostBias, i, e, du);
                     t1 += g[i][e];
                     t2 += g[i][e] * n[i][e];
                 }
-                if (row_gate && a.dgate[now] != nullptr) store_unit<DT, VEC>(row_at(a.dgate[now], at, pitch), lane + i * L, o);
+                if (row_gate && a.dgate[now] != nullptr) store_unit<DT, VEC>(shared_row<L>(a.dgate[now], at, pitch), lane + i * L, rounded<DT>(o));
             }
             const float rstd = r1;
             const uint32_t next = row + step;
-            if (next < total) {
+            if (HELD && next < total) {
                 while (next >= a.rows.start[r + 1]) r++;
                 local = next - a.rows.start[r];
                 fetch(local);
             }
-            const Row zto = row_at(a.dz[now], at, pitch);
+            const auto zto = shared_row<L>(a.dz[now], at, pitch);
             if (post) {
-                row_sums<WPR>(t1, t2, &cells[parity][2]);
+                row_totals<L>(t1, t2, &cells[parity][2]);
                 const float mean = rms ? 0.f : t1 * inv, along = t2 * inv;
 #pragma unroll
                 for (int i = 0; i < NV; i++)
@@ -299,48 +413,107 @@ __global__ __launch_bounds__(Group<WPR>::threads) void k_block_backward(BlockBac
                     for (int e = 0; e < E; e++) g[i][e] = rstd * (g[i][e] - mean - n[i][e] * along);
             }
 #pragma unroll
-            for (int i = 0; i < NV; i++) {
-                U o;
-#pragma unroll
-                for (int e = 0; e < E; e++) o.put(e, g[i][e]);
-                store_unit<DT, VEC>(zto, lane + i * L, o);
-            }
+            for (int i = 0; i < NV; i++) store_unit<DT, VEC>(zto, lane + i * L, rounded<DT>(g[i]));
             row = next;
         }
     }
-    // the workgroup's strip of each sum that is wanted
-    float* strip = a.partial + uint64_t(blockIdx.x) * a.wanted * a.cols;
-    uint32_t at = 0;
+    if constexpr (SUM) {
+        // the workgroup's strip of each sum that is wanted
+        float* strip = a.partial + uint64_t(blockIdx.x) * a.wanted * a.cols;
+        uint32_t at = 0;
 #pragma unroll
-    for (int k = 0; k < kSums; k++) {
-        if (!(a.sums >> k & 1)) continue;
-        float* to = strip + uint64_t(at++) * a.cols;
-        if constexpr (WPR == 1) {
-            // the waves' sums one after the other, in a fixed order
-            __shared__ float joined[NV * E * 64];
-            __syncthreads();
-            for (int w = 0; w < Group<WPR>::waves; w++) {
-                if (int(threadIdx.x >> 6) == w) {
+        for (int k = 0; k < kSums; k++) {
+            if (!(a.sums >> k & 1)) continue;
+            float* to = strip + uint64_t(at++) * a.cols;
+            if constexpr (L <= 64) {
+                // the rows that a wave holds side by side, then the waves one after the other
+                __shared__ float joined[NV * E * L];
+                __syncthreads();
+                for (int w = 0; w < Share<L>::waves; w++) {
 #pragma unroll
                     for (int i = 0; i < NV; i++)
 #pragma unroll
                         for (int e = 0; e < E; e++) {
+                            float v = sums[k][i][e];
+#pragma unroll
+                            for (int m = L; m < 64; m <<= 1) v += __shfl_xor(v, m);
                             const uint32_t c = (lane + i * L) * E + e;
-                            joined[c] = w == 0 ? sums[k][i][e] : joined[c] + sums[k][i][e];
+                            if (int(threadIdx.x >> 6) == w && (threadIdx.x & 63) < uint32_t(L)) joined[c] = w == 0 ? v : joined[c] + v;
                         }
+                    __syncthreads();
                 }
-                __syncthreads();
+                for (uint32_t c = threadIdx.x; c < a.cols; c += Share<L>::threads) to[c] = joined[c];
+            } else {
+#pragma unroll
+                for (int i = 0; i < NV; i++)
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const uint32_t c = (lane + i * L) * E + e;
+                        if (c < a.cols) to[c] = sums[k][i][e];
+                    }
             }
-            for (uint32_t c = threadIdx.x; c < a.cols; c += Group<WPR>::threads) to[c] = joined[c];
-        } else {
-#pragma unroll
-            for (int i = 0; i < NV; i++)
-#pragma unroll
-                for (int e = 0; e < E; e++) {
-                    const uint32_t c = (lane + i * L) * E + e;
-                    if (c < a.cols) to[c] = sums[k][i][e];
-                }
         }
+    }
+}
+
+// The sums over the rows from what k_block_backward left of each: strip
+// blockIdx.y of the rows, 16 bytes of columns per thread.
+template <int DT, bool VEC>
+__global__ __launch_bounds__(kBlock) void k_block_columns(BlockBackArgs a) {
+    typedef Unit<DT> U;
+    constexpr int E = U::elems;
+    const uint32_t u = blockIdx.x * kBlock + threadIdx.x, pitch = a.cols * uint32_t(sizeof(typename U::T));
+    if (u * 16 >= pitch) return;
+    const uint64_t total = a.rows.start[a.nranks];
+    const uint32_t lo = uint32_t(total * blockIdx.y / a.strips), hi = uint32_t(total * (blockIdx.y + 1) / a.strips);
+    float sums[kSums][E] = {};
+    int r = rank_of_row(a.rows, a.nranks, lo);
+    const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = a.post_bias[r] != nullptr;
+    const bool shared_gate = a.gate_kind == kChannelGate, row_gate = a.gate_kind == kRowGate, gated = shared_gate || row_gate;
+    const bool past = a.dh[r] != nullptr, need_z = a.z[r] != nullptr;
+    auto some = [&](bool there, const void* base, uint64_t row) {
+        U x = {};
+        if (there) x = load_unit<DT, VEC, kPolNT>(row_at(base, row, pitch), u);
+        return x;
+    };
+    const U w1 = some(post, a.post_weight[r], 0), c1 = some(b1, a.post_bias[r], 0), w2 = some(pre, a.pre_weight[r], 0);
+    U gate = some(shared_gate, a.gate[r], 0);
+    for (uint32_t row = lo; row < hi; row++) {
+        while (row >= a.rows.start[r + 1]) r++;
+        const uint64_t local = row - a.rows.start[r];
+        const U dy = some(pre, a.dy[r], local), h = some(pre, a.h[r], local), dh = some(past, a.dh[r], local), z = some(need_z, a.z[r], local);
+        if (row_gate) gate = some(true, a.gate[r], local);
+        const float* s = a.stats[r] + local * 4;
+        const float m1 = s[0], r1 = s[1], m2 = s[2], r2 = s[3];
+        const float mean = pre ? a.row_sums[uint64_t(row) * 2] : 0.f, along = pre ? a.row_sums[uint64_t(row) * 2 + 1] : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            float d = past ? dh.get(e) : 0.f;
+            if (pre) {
+                const float n = (h.get(e) - m2) * r2;
+                d += r2 * (dy.get(e) * w2.get(e) - mean - n * along);
+                sums[kPreWeight][e] += dy.get(e) * n;
+                sums[kPreBias][e] += dy.get(e);
+            }
+            float n = z.get(e);
+            if (post) n = (n - m1) * r1;
+            float p = n;
+            if (post) p *= w1.get(e);
+            if (b1) p += c1.get(e);
+            const float du = d * (gated ? a.scale * gate.get(e) : a.scale);
+            sums[kPostWeight][e] += du * n;
+            sums[kPostBias][e] += du;
+            sums[kGate][e] += d * p * a.scale;
+        }
+    }
+    uint32_t at = 0;
+#pragma unroll
+    for (int k = 0; k < kSums; k++) {
+        if (!(a.sums >> k & 1)) continue;
+        float* to = a.partial + (uint64_t(blockIdx.y) * a.wanted + at++) * a.cols + u * E;
+#pragma unroll
+        for (int e = 0; e < E; e++)
+            if (u * E + e < a.cols) to[e] = sums[k][e];
     }
 }
 
@@ -490,34 +663,6 @@ __global__ __launch_bounds__(kBlock) void k_block_rows_wide(BlockBackArgs a) {
     }
 }
 
-// Strip blockIdx.y of the rows, one column per thread.
-template <int DT>
-__global__ __launch_bounds__(kBlock) void k_block_columns_wide(BlockBackArgs a) {
-    const uint32_t c = blockIdx.x * kBlock + threadIdx.x;
-    if (c >= a.cols) return;
-    const uint64_t total = a.rows.start[a.nranks];
-    const uint32_t lo = uint32_t(total * blockIdx.y / a.strips), hi = uint32_t(total * (blockIdx.y + 1) / a.strips);
-    float sums[kSums] = {};
-    int r = rank_of_row(a.rows, a.nranks, lo);
-    for (uint32_t row = lo; row < hi; row++) {
-        while (row >= a.rows.start[r + 1]) r++;
-        const WideBack<DT> v(a, r, row - a.rows.start[r]);
-        const float d = v.dx(c, a.row_sums[uint64_t(row) * 2], a.row_sums[uint64_t(row) * 2 + 1]), du = d * v.factor(c);
-        if (a.pre_weight[r] != nullptr) {
-            const float dy = v.dy(c);
-            sums[kPreWeight] += dy * v.n2(c);
-            sums[kPreBias] += dy;
-        }
-        sums[kPostWeight] += du * v.n1(c);
-        sums[kPostBias] += du;
-        sums[kGate] += d * v.p(c) * a.scale;
-    }
-    uint32_t at = 0;
-#pragma unroll
-    for (int k = 0; k < kSums; k++)
-        if (a.sums >> k & 1) a.partial[(uint64_t(blockIdx.y) * a.wanted + at++) * a.cols + c] = sums[k];
-}
-
 // Sum blockIdx.y of those that are wanted, the strips folded in order: 64 columns
 // per workgroup, each of its 16 waves takes every 16th strip, then the waves in
 // order; every rank gets it.
@@ -553,33 +698,47 @@ __global__ __launch_bounds__(1024) void k_block_fold(BlockBackArgs a) {
 }
 
 // -------------------------------------------------------------------- host --
-// How a row is held: WPR waves with NV units per lane each; wpr 0: too wide.
+// How a row is held: L lanes with NV units each; l 0: too wide.  One unit per lane
+// as far as a workgroup goes: more waves hide more of the memory's latency than a
+// second unit does (32768 x 4096 bf16 backward 393 us with two units in 256 lanes).
 struct Hold {
-    int nv, wpr;
+    int nv, l;
 };
-Hold hold(uint32_t units) {
-    if (units <= 64) return {1, 1};
-    if (units <= 128) return {2, 1};
-    if (units <= 256) return {1, 4};
-    if (units <= 512) return {2, 4};
-    if (units <= 1024) return {2, 8};
+Hold hold(uint32_t units, int dtype) {
+    if (units <= 8) return {1, 8};
+    if (units <= 16) return {1, 16};
+    if (units <= 64) return {1, 64};
+    if (units <= 128) return {2, 64};
+    if (units <= 256) return {1, 256};
+    if (units <= 512) return {1, 512};
+    if (units <= 1024) return {2, 512};
+    if (units <= 2048) return {2, 1024};
+    if (units <= 4096 && dtype == kF32) return {4, 1024};
     return {0, 0};
 }
-template <typename F>
+// The backward pass keeps the sums over the rows in registers where one unit per
+// lane is enough; beside more they do not fit.
+bool sums_along(Hold h) { return h.l < 1024 && h.l != 0; }
+template <int DT, typename F>
 void with_hold(Hold h, F&& run) {
-    if (h.wpr == 1 && h.nv == 1) run(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    else if (h.wpr == 1) run(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
-    else if (h.wpr == 4 && h.nv == 1) run(std::integral_constant<int, 1>(), std::integral_constant<int, 4>());
-    else if (h.wpr == 4) run(std::integral_constant<int, 2>(), std::integral_constant<int, 4>());
-    else run(std::integral_constant<int, 2>(), std::integral_constant<int, 8>());
+    typedef std::integral_constant<int, 1> one;
+    if (h.l == 8) run(one(), std::integral_constant<int, 8>());
+    else if (h.l == 16) run(one(), std::integral_constant<int, 16>());
+    else if (h.l == 64 && h.nv == 1) run(one(), std::integral_constant<int, 64>());
+    else if (h.l == 64) run(std::integral_constant<int, 2>(), std::integral_constant<int, 64>());
+    else if (h.l == 256) run(one(), std::integral_constant<int, 256>());
+    else if (h.l == 512 && h.nv == 1) run(one(), std::integral_constant<int, 512>());
+    else if (h.l == 512) run(std::integral_constant<int, 2>(), std::integral_constant<int, 512>());
+    else if (DT == kBF16 || h.nv == 2) run(std::integral_constant<int, 2>(), std::integral_constant<int, 1024>());
+    else if constexpr (DT == kF32) run(std::integral_constant<int, 4>(), std::integral_constant<int, 1024>());
 }
 uint32_t units_of(uint32_t cols, int dtype) { return (cols + (dtype == kBF16 ? 8 : 4) - 1) / (dtype == kBF16 ? 8 : 4); }
 // Workgroups of the backward pass, each of which leaves a strip.
 uint32_t strips_of(uint32_t rows, uint32_t cols, int dtype) {
-    const Hold h = hold(units_of(cols, dtype));
-    if (h.wpr == 0) return rows < 256 ? rows : 256;
-    const uint32_t need = h.wpr == 1 ? (rows + 3) / 4 : rows;
-    uint32_t most = 512;
+    const Hold h = hold(units_of(cols, dtype), dtype);
+    if (!sums_along(h)) return rows < 256 ? rows : 256;
+    const uint32_t per = h.l <= 64 ? 256 / h.l : 1, need = (rows + per - 1) / per;
+    uint32_t most = h.l == 1024 ? 256 : 512;
     if (need < 4 * most) most = (need + 3) / 4;  // at least four rows
     return need < most ? need : most;
 }
@@ -593,15 +752,15 @@ bool rows16(uint32_t cols, int dtype) { return cols * uint64_t(dtype == kBF16 ? 
 template <int DT, bool VEC>
 hipError_t forward(const BlockArgs& a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold(units_of(a.cols, DT));
-    if (h.wpr == 0) {
+    const Hold h = hold(units_of(a.cols, DT), DT);
+    if (h.l == 0) {
         hipLaunchKernelGGL(k_block_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
         return hipGetLastError();
     }
-    with_hold(h, [&](auto nv, auto wpr) {
-        constexpr int W = decltype(wpr)::value;
-        const uint32_t need = (rows + Group<W>::rows - 1) / Group<W>::rows, most = 2048;
-        hipLaunchKernelGGL((k_block<DT, VEC, decltype(nv)::value, W>), dim3(need < most ? need : most), dim3(Group<W>::threads), 0, s, a);
+    with_hold<DT>(h, [&](auto nv, auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        const uint32_t need = (rows + Share<L>::rows - 1) / Share<L>::rows, most = 2048;
+        hipLaunchKernelGGL((k_block<DT, VEC, decltype(nv)::value, L>), dim3(need < most ? need : most), dim3(Share<L>::threads), 0, s, a);
     });
     return hipGetLastError();
 }
@@ -609,15 +768,22 @@ hipError_t forward(const BlockArgs& a, hipStream_t s) {
 template <int DT, bool VEC>
 hipError_t backward(const BlockBackArgs& a, hipStream_t s) {
     const uint32_t rows = a.rows.start[a.nranks];
-    const Hold h = hold(units_of(a.cols, DT));
-    if (rows > 0 && h.wpr == 0) {
-        hipLaunchKernelGGL(k_block_rows_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
-        if (a.wanted > 0) hipLaunchKernelGGL(k_block_columns_wide<DT>, dim3((a.cols + kBlock - 1) / kBlock, a.strips), dim3(kBlock), 0, s, a);
-    } else if (rows > 0) {
-        with_hold(h, [&](auto nv, auto wpr) {
-            constexpr int W = decltype(wpr)::value;
-            hipLaunchKernelGGL((k_block_backward<DT, VEC, decltype(nv)::value, W>), dim3(a.strips), dim3(Group<W>::threads), 0, s, a);
-        });
+    const Hold h = hold(units_of(a.cols, DT), DT);
+    if (rows > 0) {
+        if (h.l == 0) {
+            hipLaunchKernelGGL(k_block_rows_wide<DT>, dim3(rows), dim3(kBlock), 0, s, a);
+        } else {
+            with_hold<DT>(h, [&](auto nv, auto lanes) {
+                constexpr int NV = decltype(nv)::value, L = decltype(lanes)::value;
+                const uint32_t groups = sums_along(h) ? a.strips : rows < 2048 ? rows : 2048;
+                if (a.post_bias[0] != nullptr || (a.sums & (1u << kPostBias | 1u << kPreBias)) != 0)
+                    hipLaunchKernelGGL((k_block_backward<DT, VEC, NV, L, (L < 1024), true>), dim3(groups), dim3(Share<L>::threads), 0, s, a);
+                else
+                    hipLaunchKernelGGL((k_block_backward<DT, VEC, NV, L, (L < 1024), false>), dim3(groups), dim3(Share<L>::threads), 0, s, a);
+            });
+        }
+        if (!sums_along(h) && a.wanted > 0)
+            hipLaunchKernelGGL((k_block_columns<DT, VEC>), dim3((units_of(a.cols, DT) + kBlock - 1) / kBlock, a.strips), dim3(kBlock), 0, s, a);
     }
     if (a.wanted > 0) hipLaunchKernelGGL(k_block_fold<DT>, dim3((a.cols + 63) / 64, a.wanted), dim3(1024), 0, s, a);
     return hipGetLastError();
@@ -635,9 +801,9 @@ hipError_t launch_block(const BlockArgs& a, int dtype, hipStream_t s) {
     return vec ? forward<kF32, true>(a, s) : forward<kF32, false>(a, s);
 }
 
-// The strips, and for rows that no registers hold two sums of each row.
+// The strips, and where they are formed in a launch of their own two sums of each row.
 uint64_t block_workspace(uint32_t rows, uint32_t cols, int dtype) {
-    return up(uint64_t(strips_of(rows, cols, dtype)) * kSums * cols * 4, 256) + (hold(units_of(cols, dtype)).wpr == 0 ? up(uint64_t(rows) * 8, 256) : 0);
+    return up(uint64_t(strips_of(rows, cols, dtype)) * kSums * cols * 4, 256) + (sums_along(hold(units_of(cols, dtype), dtype)) ? 0 : up(uint64_t(rows) * 8, 256));
 }
 
 hipError_t launch_block_backward(BlockBackArgs a, void* workspace, int dtype, hipStream_t s) {

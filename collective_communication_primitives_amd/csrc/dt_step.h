@@ -183,7 +183,7 @@ struct LayerArgs {
     const void* residual[kMaxRanksHost];
     void* out[kMaxRanksHost];
     char* hidden;                           // [slots] rows of hpitch bytes; bf16: a second part hpart bytes behind
-    int32_t* table;                         // header, experts in use [used], their tokens' slots [used][tpad]
+    int32_t* table;                         // header, experts in use and their tokens [used][2], those tokens' slots [used][tpad]
     RowTable rows;
     uint32_t cols, inner, nexperts, per_rank, topk, tokens;
     uint32_t hpitch, used, tpad;            // used: the most experts that can be in use

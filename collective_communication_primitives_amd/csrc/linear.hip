@@ -15,7 +15,7 @@
 // All sums are fp32.  z, y, dx, dW and db are rounded once; dz is rounded to the
 // tensors' type before it enters its two products, as the matrix units take it.
 #include "dt_act.h"
-#include "dt_matrix.h"
+#include "dt_stream.h"
 
 namespace dt {
 namespace {
@@ -404,6 +404,76 @@ __global__ __launch_bounds__(S::threads) void k_linear(LinearArgs a) {
     }
 }
 
+// Few rows to a run: 16 features of one run to a workgroup, whose NW waves share the
+// summed index; weights go past LDS, read once for up to 16 GM rows.
+template <int DT, bool VEC, bool GATED, int NW, int G>
+__device__ __forceinline__ void few_rows(const LinearArgs& a, const Run& r, uint32_t base, f32x4 (*sums)[64]) {
+    typedef typename Elem<DT>::type T;
+    constexpr int W = GATED ? 2 : 1, P = G > 1 ? 1 : 2;
+    const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t pitch = a.cols * uint32_t(sizeof(T)), m0 = blockIdx.x * 16, wide = W * a.outs;
+    // the rows that the lane loads; behind the last one it is repeated
+    const uint32_t m = m0 + (lane >> 2) < a.outs ? m0 + (lane >> 2) : a.outs - 1;
+    const char *w[W], *x[1][G];
+#pragma unroll
+    for (int k = 0; k < W; k++) w[k] = static_cast<const char*>(a.weight[r.rank]) + (uint64_t(r.run) * wide + k * a.outs + m) * pitch;
+#pragma unroll
+    for (int g = 0; g < G; g++) {
+        const uint32_t n = base + g * 16 + (lane >> 2);
+        x[0][g] = static_cast<const char*>(a.x[r.rank]) + (uint64_t(r.lo) + (n < r.count ? n : r.count - 1)) * pitch;
+    }
+    f32x4 acc[W][G];
+#pragma unroll
+    for (int k = 0; k < W; k++)
+#pragma unroll
+        for (int g = 0; g < G; g++) acc[k][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    uint32_t lo, hi;
+    share_steps((pitch + kStepBytes - 1) / kStepBytes, wave, NW, lo, hi);
+    stream_rows<DT, VEC, W, G, 1, P>(w, x, lo, hi, pitch, pitch, acc);
+#pragma unroll
+    for (int k = 0; k < W; k++)
+#pragma unroll
+        for (int g = 0; g < G; g++) sums[(wave * G + g) * W + k][lane] = acc[k][g];
+    __syncthreads();
+    // thread: 16 rows threadIdx.x / 64, the lane's four features of its row
+    const uint32_t g = threadIdx.x >> 6, n = base + g * 16 + (lane & 15), f = m0 + (lane >> 4) * 4;
+    if (g < uint32_t(G) && n < r.count && f < a.outs) {
+        f32x4 z = {0.f, 0.f, 0.f, 0.f}, u = z;
+#pragma unroll
+        for (uint32_t k = 0; k < NW; k++) {
+            z += sums[(k * G + g) * W][lane];
+            if (GATED) u += sums[(k * G + g) * W + W - 1][lane];
+        }
+        const uint32_t left = a.outs - f;
+        const uint64_t row = uint64_t(r.lo) + n;
+        if (a.bias[r.rank] != nullptr) {
+            const T* b = static_cast<const T*>(a.bias[r.rank]) + uint64_t(r.run) * wide + f;
+            z += load_four<DT>(b, a.quads, left);
+            if (GATED) u += load_four<DT>(b + a.outs, a.quads, left);
+        }
+        if (a.pre[r.rank] != nullptr) {
+            T* to = static_cast<T*>(a.pre[r.rank]) + row * wide + f;
+            store_four<DT>(to, z, a.quads, left);
+            if (GATED) store_four<DT>(to + a.outs, u, a.quads, left);
+        }
+        f32x4 y;
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] = act(z[e], a.act) * (GATED ? u[e] : 1.f);
+        if (a.residual[r.rank] != nullptr) y += load_four<DT>(static_cast<const T*>(a.residual[r.rank]) + row * a.outs + f, a.quads, left);
+        store_four<DT>(static_cast<T*>(a.y[r.rank]) + row * a.outs + f, y, a.quads, left);
+    }
+    __syncthreads();  // the next rows' sums
+}
+template <int DT, bool VEC, bool GATED, int NW, int GM>
+__global__ __launch_bounds__(NW * 64) void k_linear_few(LinearArgs a) {
+    __shared__ f32x4 sums[NW * GM * (GATED ? 2 : 1)][64];
+    const Run r = same(run_at(a, blockIdx.y));
+    uint32_t base = 0;
+    if constexpr (GM > 1)
+        for (; base < r.count && r.count - base > 16; base += 16 * GM) few_rows<DT, VEC, GATED, NW, GM>(a, r, base, sums);
+    for (; base < r.count; base += 16) few_rows<DT, VEC, GATED, NW, 1>(a, r, base, sums);
+}
+
 // --------------------------------------------------------------- backward --
 // dz of the runs' rows, kDzRows rows and 1024 columns to a workgroup, and its
 // columns' sums over those rows.  A thread has four neighbouring columns.
@@ -594,20 +664,23 @@ constexpr uint32_t kTileM[] = {256, 128, 64, 64}, kTileN[] = {256, 128, 64, 16};
 constexpr uint32_t kTilesPerCu[] = {1, 2, 4, 6};   // workgroups of a tile's LDS that share a CU
 
 // The tile for products of m features with runs of `mean` rows each.
-Tile pick_tile(int dtype, uint64_t m, uint64_t mean, uint64_t groups, int path) {
-    if (mean <= 16) return kTiny;
+Tile pick_tile(int dtype, uint64_t m, uint64_t mean, uint64_t groups, int path, bool tiny) {
+    if (tiny && mean <= 16) return kTiny;
     auto tiles = [&](uint64_t by) { return ceil_div(m, by) * ceil_div(mean, by) * groups; };
     if (path == kLoose || dtype == kF32) return tiles(128) >= 1024 ? kSquare : kSmall;
     if (mean > 128 && tiles(256) >= 224) return kWide;
-    return mean > 64 && tiles(128) >= 192 ? kSquare : kSmall;
+    return mean > 32 && tiles(128) >= 192 ? kSquare : kSmall;
 }
-template <int DT, int PATH, typename F>
+// launch(Shape) with the shape of `t`; TINY: where pick_tile may say so.
+template <int DT, int PATH, bool TINY, typename F>
 void with_tile(Tile t, F&& launch) {
+    if constexpr (TINY) {
+        if (t == kTiny) return launch(Tiny());
+    }
     if constexpr (DT == kBF16 && PATH != kLoose) {
         if (t == kWide) return launch(Wide());
     }
     if (t == kSquare) launch(Square());
-    else if (t == kTiny) launch(Tiny());
     else launch(Small());
 }
 template <typename F>
@@ -629,18 +702,43 @@ bool on(const void* const* list, int n, uintptr_t boundary) {
 }
 int path_of(uint64_t pitch, bool on4) { return !on4 || pitch % 4 != 0 ? kLoose : pitch % 16 != 0 ? kTail : kWhole; }
 
+// Whether the weights are streamed past LDS: for up to 32 rows of a run on average
+// (64 runs of 4096 x 4096 bf16: 434 us with 32 rows, tiles 491), and for up to 64
+// where the tiles of 128 would leave CUs idle (4 x 4096 x 4096 bf16, 33 rows: 45 us,
+// tiles 51; 8 x 1000 x 1000 fp32, 64 rows: 19, 26; but 64 runs with 64 rows: 553, 427).
+bool few_rows_to_run(int dtype, uint64_t features, uint64_t mean, uint64_t groups) {
+    return mean <= 32 || (mean <= 64 && (dtype == kF32 || ceil_div(features, 128) * groups < 192));
+}
+// 16 waves to a workgroup where there are few of them: a wave's way through the summed index is shorter.
+template <int DT, bool VEC, bool GATED>
+void few(const LinearArgs& a, hipStream_t s) {
+    const dim3 grid((a.outs + 15) / 16, a.runs * a.nranks);
+    const uint64_t rows = a.rows.start[a.nranks];
+    if (rows > 32 * uint64_t(grid.y)) hipLaunchKernelGGL((k_linear_few<DT, VEC, GATED, 4, 4>), grid, dim3(4 * 64), 0, s, a);
+    else if (rows > 16 * uint64_t(grid.y)) hipLaunchKernelGGL((k_linear_few<DT, VEC, GATED, 4, 2>), grid, dim3(4 * 64), 0, s, a);
+    else if (uint64_t(grid.x) * grid.y <= 512) hipLaunchKernelGGL((k_linear_few<DT, VEC, GATED, 16, 1>), grid, dim3(16 * 64), 0, s, a);
+    else hipLaunchKernelGGL((k_linear_few<DT, VEC, GATED, 4, 1>), grid, dim3(4 * 64), 0, s, a);
+}
+
 template <int DT>
 hipError_t forward(LinearArgs a, hipStream_t s) {
     constexpr uint64_t es = sizeof(typename Elem<DT>::type);
     const uint64_t rows = a.rows.start[a.nranks], groups = uint64_t(a.runs) * a.nranks;
     a.vecs = a.outs * es % 16 == 0 && on(a.y, a.nranks, 16) && on(a.pre, a.nranks, 16) && on(a.bias, a.nranks, 16) && on(a.residual, a.nranks, 16);
     const uint64_t features = uint64_t(a.outs) * (a.gated ? 2 : 1);
+    if (few_rows_to_run(DT, features, ceil_div(rows, groups), groups)) {
+        a.quads = a.outs % 4 == 0 && on(a.bias, a.nranks, 4 * es) && on(a.residual, a.nranks, 4 * es) && on(a.y, a.nranks, 4 * es) && on(a.pre, a.nranks, 4 * es);
+        const bool vec = a.cols * es % 16 == 0 && on(a.x, a.nranks, 16) && on(a.weight, a.nranks, 16);
+        if (a.gated) vec ? few<DT, true, true>(a, s) : few<DT, false, true>(a, s);
+        else vec ? few<DT, true, false>(a, s) : few<DT, false, false>(a, s);
+        return hipGetLastError();
+    }
     with_path(path_of(a.cols * es, on(a.x, a.nranks, 4) && on(a.weight, a.nranks, 4)), [&](auto path) {
         constexpr int P = decltype(path)::value;
-        const Tile t = pick_tile(DT, features, ceil_div(rows, groups), groups, P);
+        const Tile t = pick_tile(DT, features, ceil_div(rows, groups), groups, P, false);
         // a run ends inside a tile, so there are up to one tile more than its rows fill
         const uint64_t tiles = ceil_div(features, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
-        with_tile<DT, P>(t, [&](auto shape) {
+        with_tile<DT, P, false>(t, [&](auto shape) {
             typedef decltype(shape) S;
             if (a.gated) hipLaunchKernelGGL((k_linear<DT, S, P, true>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
             else hipLaunchKernelGGL((k_linear<DT, S, P, false>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
@@ -691,9 +789,9 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
         const int zp = path_of(a.zpitch, dz4), wp = path_of(a.cols * es, w4);
         with_path(zp == kLoose || wp == kLoose ? kLoose : zp, [&](auto path) {
             constexpr int P = decltype(path)::value;
-            const Tile t = pick_tile(DT, a.cols, ceil_div(rows, groups), groups, P);
+            const Tile t = pick_tile(DT, a.cols, ceil_div(rows, groups), groups, P, true);
             const uint64_t tiles = ceil_div(a.cols, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
-            with_tile<DT, P>(t, [&](auto shape) {
+            with_tile<DT, P, true>(t, [&](auto shape) {
                 typedef decltype(shape) S;
                 hipLaunchKernelGGL((k_linear_dx<DT, S, P>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
             });
@@ -702,12 +800,10 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
     const bool loose = path_of(a.zpitch, dz4) == kLoose || path_of(a.cols * es, x4) == kLoose;
     auto dweight = [&](auto path) {
         constexpr int P = decltype(path)::value;
-        const Tile t = pick_tile(DT, a.cols, wide < 17 ? 17 : wide, groups, P);
-        with_tile<DT, P>(t, [&](auto shape) {
+        const Tile t = pick_tile(DT, a.cols, wide, groups, P, false);
+        with_tile<DT, P, false>(t, [&](auto shape) {
             typedef decltype(shape) S;
-            if constexpr (!std::is_same<S, Tiny>::value)
-                hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)),
-                                   dim3(S::threads), 0, s, a);
+            hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)), dim3(S::threads), 0, s, a);
         });
     };
     if (loose) dweight(std::integral_constant<int, kLoose>());

@@ -1090,7 +1090,7 @@ def dt_moe_layer(x: Sequence[torch.Tensor], experts: Sequence[torch.Tensor], wei
                  b_in: Optional[Sequence[torch.Tensor]] = None, b_out: Optional[Sequence[torch.Tensor]] = None,
                  residual: Optional[Sequence[torch.Tensor]] = None, act="silu", gated: bool = True,
                  workspace: Optional[torch.Tensor] = None, stream=None, async_op: bool = False, comm_stream=None):
-    """The experts' layer for up to 256 tokens over all ranks, in two launches: out[r] = residual[r] + the sum over a token's
+    """The experts' layer for up to 256 tokens over all ranks, in two or three launches: out[r] = residual[r] + the sum over a token's
     slots of weights * (w_out act(w_in x + b_in) + b_out) of its experts.  x[r], out[r] [tokens, cols]; experts[r], weights[r]
     [tokens, topk] from dt_moe_route; w_in[q] [E / P, inner (gated: 2 * inner), cols], w_out[q] [E / P, cols, inner] of the
     experts that rank q owns."""

@@ -122,6 +122,38 @@ __device__ __forceinline__ uint32_t first_row() {
     return blockIdx.x * Share<L>::rows + (L < 64 ? mine : uint32_t(__builtin_amdgcn_readfirstlane(mine)));
 }
 
+// The rank of a row, which narrow rows' lanes do not share: counted against all
+// ranks' first rows, whose addresses they do.
+template <int L>
+__device__ __forceinline__ int rank_for(const RowTable& t, int nranks, uint32_t row) {
+    if constexpr (L >= 64) return rank_of_row(t, nranks, row);
+    int r = 0;
+    for (int k = 1; k < nranks; k++) r += row >= t.start[k] ? 1 : 0;
+    return r;
+}
+
+// Rank r's pointer of a list in the kernel's arguments.  Narrow rows' lanes may be in
+// several ranks, mostly in one: an index of their own would make the lanes fetch the
+// pointer from the arguments' memory, microseconds away.
+template <int L>
+__device__ __forceinline__ uint32_t start_of(const RowTable& t, int nranks, int r) {
+    if constexpr (L >= 64) return t.start[r];
+    const int r0 = __builtin_amdgcn_readfirstlane(r);
+    uint32_t at = t.start[r0];
+    if (!__all(r == r0))
+        for (int k = 0; k < nranks; k++) at = r == k ? t.start[k] : at;
+    return at;
+}
+template <int L, typename P>
+__device__ __forceinline__ P of_rank(P const (&list)[kMaxRanksHost], int nranks, int r) {
+    if constexpr (L >= 64) return list[r];
+    const int r0 = __builtin_amdgcn_readfirstlane(r);
+    P p = list[r0];
+    if (!__all(r == r0))
+        for (int k = 0; k < nranks; k++) p = r == k ? list[k] : p;
+    return p;
+}
+
 template <int DT, bool VEC, int NV>
 struct Units {
     Unit<DT> v[NV];
@@ -147,11 +179,11 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
     const uint32_t total = a.rows.start[a.nranks], pitch = a.cols * uint32_t(sizeof(typename U::T));
     uint32_t row = first_row<L>();
     if (row >= total) return;
-    int r = rank_of_row(a.rows, a.nranks, row);
-    const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = a.post_bias[r] != nullptr, b2 = a.pre_bias[r] != nullptr;
+    int r = rank_for<L>(a.rows, a.nranks, row);
+    const bool post = of_rank<L>(a.post_weight, a.nranks, r) != nullptr, pre = of_rank<L>(a.pre_weight, a.nranks, r) != nullptr, b1 = of_rank<L>(a.post_bias, a.nranks, r) != nullptr, b2 = of_rank<L>(a.pre_bias, a.nranks, r) != nullptr;
     const bool rms = a.rms, shared_gate = a.gate_kind == kChannelGate, row_gate = a.gate_kind == kRowGate;
     constexpr bool HELD = NV == 1 || L < 1024;
-    const void *w1_at = a.post_weight[r], *c1_at = a.post_bias[r], *w2_at = a.pre_weight[r], *c2_at = a.pre_bias[r], *gate_at = a.gate[r];
+    const void *w1_at = of_rank<L>(a.post_weight, a.nranks, r), *c1_at = of_rank<L>(a.post_bias, a.nranks, r), *w2_at = of_rank<L>(a.pre_weight, a.nranks, r), *c2_at = of_rank<L>(a.pre_bias, a.nranks, r), *gate_at = of_rank<L>(a.gate, a.nranks, r);
     Units<DT, VEC, NV> w1, c1, w2, c2, gate, z, x;
     if constexpr (HELD) {
         w1.template load<L, 0>(post, w1_at, 0, pitch, lane);
@@ -161,18 +193,18 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
         gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
     }
     auto fetch = [&](uint64_t at) {
-        z.template load<L, kPolNT>(true, a.z[r], at, pitch, lane);
-        x.template load<L, kPolNT>(true, a.x[r], at, pitch, lane);
-        gate.template load<L, kPolNT>(row_gate, a.gate[r], at, pitch, lane);
+        z.template load<L, kPolNT>(true, of_rank<L>(a.z, a.nranks, r), at, pitch, lane);
+        x.template load<L, kPolNT>(true, of_rank<L>(a.x, a.nranks, r), at, pitch, lane);
+        gate.template load<L, kPolNT>(row_gate, of_rank<L>(a.gate, a.nranks, r), at, pitch, lane);
     };
-    if constexpr (HELD) fetch(row - a.rows.start[r]);
+    if constexpr (HELD) fetch(row - start_of<L>(a.rows, a.nranks, r));
     const float inv = 1.f / float(a.cols), scale = a.scale;
     // whole units are inside a row that is one of them, or outside
     auto inside = [&](int i, int e) { return (lane + i * L) * E + (VEC ? 0 : e) < a.cols; };
     for (int parity = 0; row < total; parity ^= 1) {
         if constexpr (!HELD) {
             while (row >= a.rows.start[r + 1]) r++;
-            fetch(row - a.rows.start[r]);
+            fetch(row - start_of<L>(a.rows, a.nranks, r));
             gate.template load<L, 0>(shared_gate, gate_at, 0, pitch, lane);
         }
         float v[NV][E], h[NV][E], f[NV][E];
@@ -185,11 +217,12 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
                 f[i][e] = shared_gate || row_gate ? scale * gate.v[i].get(e) : scale;
             }
         const int now = r;
-        const uint64_t local = row - a.rows.start[now];
+        const uint64_t local = row - start_of<L>(a.rows, a.nranks, now);
         const uint32_t next = row + step;
         if (HELD && next < total) {
-            while (next >= a.rows.start[r + 1]) r++;
-            fetch(next - a.rows.start[r]);
+            if constexpr (L < 64) r = rank_for<L>(a.rows, a.nranks, next);
+            else while (next >= a.rows.start[r + 1]) r++;
+            fetch(next - start_of<L>(a.rows, a.nranks, r));
         }
         float stats[4] = {0.f, 0.f, 0.f, 0.f};
         // (v - mean) and 1 / deviation
@@ -230,7 +263,7 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
                     if (b1) v[i][e] += c1.v[i].get(e);
                 }
         }
-        const auto to = shared_row<L>(a.h[now], local, pitch);
+        const auto to = shared_row<L>(of_rank<L>(a.h, a.nranks, now), local, pitch);
 #pragma unroll
         for (int i = 0; i < NV; i++) {
 #pragma unroll
@@ -246,7 +279,7 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
                 w2.template load<L, 0>(true, w2_at, 0, pitch, lane);
                 c2.template load<L, 0>(b2, c2_at, 0, pitch, lane);
             }
-            const auto out = shared_row<L>(a.y[now], local, pitch);
+            const auto out = shared_row<L>(of_rank<L>(a.y, a.nranks, now), local, pitch);
 #pragma unroll
             for (int i = 0; i < NV; i++) {
                 float y[E];
@@ -258,9 +291,9 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block(BlockArgs a) {
                 store_unit<DT, VEC>(out, lane + i * L, rounded<DT>(y));
             }
         }
-        if (lane == 0 && a.stats[now] != nullptr) {
+        if (lane == 0 && of_rank<L>(a.stats, a.nranks, now) != nullptr) {
 #pragma unroll
-            for (int k = 0; k < 4; k++) a.stats[now][local * 4 + k] = stats[k];
+            for (int k = 0; k < 4; k++) of_rank<L>(a.stats, a.nranks, now)[local * 4 + k] = stats[k];
         }
         row = next;
     }
@@ -294,13 +327,13 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackA
         }
     };
     if (row < total) {
-        int r = rank_of_row(a.rows, a.nranks, row);
-        const bool post = a.post_weight[r] != nullptr, pre = a.pre_weight[r] != nullptr, b1 = BIAS && a.post_bias[r] != nullptr;
+        int r = rank_for<L>(a.rows, a.nranks, row);
+        const bool post = of_rank<L>(a.post_weight, a.nranks, r) != nullptr, pre = of_rank<L>(a.pre_weight, a.nranks, r) != nullptr, b1 = BIAS && of_rank<L>(a.post_bias, a.nranks, r) != nullptr;
         const bool rms = a.rms, shared_gate = a.gate_kind == kChannelGate, row_gate = a.gate_kind == kRowGate, gated = shared_gate || row_gate;
-        const bool past = a.dh[r] != nullptr, need_z = a.z[r] != nullptr;
+        const bool past = of_rank<L>(a.dh, a.nranks, r) != nullptr, need_z = of_rank<L>(a.z, a.nranks, r) != nullptr;
         Units<DT, VEC, NV> w1, c1, w2, gate, z, h, dy, dh;
         constexpr bool HELD = NV == 1 || L < (BIAS ? 512 : 1024);   // as in k_block
-        const void *w1_at = a.post_weight[r], *c1_at = a.post_bias[r], *w2_at = a.pre_weight[r], *gate_at = a.gate[r];
+        const void *w1_at = of_rank<L>(a.post_weight, a.nranks, r), *c1_at = of_rank<L>(a.post_bias, a.nranks, r), *w2_at = of_rank<L>(a.pre_weight, a.nranks, r), *gate_at = of_rank<L>(a.gate, a.nranks, r);
         if constexpr (HELD) {
             w1.template load<L, 0>(post, w1_at, 0, pitch, lane);
             c1.template load<L, 0>(b1, c1_at, 0, pitch, lane);
@@ -309,24 +342,24 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackA
         }
         float m1, r1, m2, r2;
         auto fetch = [&](uint64_t at) {
-            dy.template load<L, kPolNT>(pre, a.dy[r], at, pitch, lane);
-            h.template load<L, kPolNT>(pre, a.h[r], at, pitch, lane);
-            dh.template load<L, kPolNT>(past, a.dh[r], at, pitch, lane);
-            z.template load<L, kPolNT>(need_z, a.z[r], at, pitch, lane);
-            gate.template load<L, kPolNT>(row_gate, a.gate[r], at, pitch, lane);
-            const float* s = a.stats[r] + at * 4;
+            dy.template load<L, kPolNT>(pre, of_rank<L>(a.dy, a.nranks, r), at, pitch, lane);
+            h.template load<L, kPolNT>(pre, of_rank<L>(a.h, a.nranks, r), at, pitch, lane);
+            dh.template load<L, kPolNT>(past, of_rank<L>(a.dh, a.nranks, r), at, pitch, lane);
+            z.template load<L, kPolNT>(need_z, of_rank<L>(a.z, a.nranks, r), at, pitch, lane);
+            gate.template load<L, kPolNT>(row_gate, of_rank<L>(a.gate, a.nranks, r), at, pitch, lane);
+            const float* s = of_rank<L>(a.stats, a.nranks, r) + at * 4;
             m1 = s[0];
             r1 = s[1];
             m2 = s[2];
             r2 = s[3];
         };
-        uint64_t local = row - a.rows.start[r];
+        uint64_t local = row - start_of<L>(a.rows, a.nranks, r);
         if constexpr (HELD) fetch(local);
         const float inv = 1.f / float(a.cols), scale = a.scale;
         for (int parity = 0; row < total; parity ^= 1) {
             if constexpr (!HELD) {
                 while (row >= a.rows.start[r + 1]) r++;
-                local = row - a.rows.start[r];
+                local = row - start_of<L>(a.rows, a.nranks, r);
                 fetch(local);
                 w2.template load<L, 0>(pre, w2_at, 0, pitch, lane);
             }
@@ -363,7 +396,7 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackA
 #pragma unroll
                     for (int e = 0; e < E; e++) d[i][e] = past ? dh.v[i].get(e) : 0.f;
             }
-            const auto to = shared_row<L>(a.dx[r], local, pitch);
+            const auto to = shared_row<L>(of_rank<L>(a.dx, a.nranks, r), local, pitch);
 #pragma unroll
             for (int i = 0; i < NV; i++) store_unit<DT, VEC>(to, lane + i * L, rounded<DT>(d[i]));
             // dz, and the gate's
@@ -394,16 +427,17 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackA
                     t1 += g[i][e];
                     t2 += g[i][e] * n[i][e];
                 }
-                if (row_gate && a.dgate[now] != nullptr) store_unit<DT, VEC>(shared_row<L>(a.dgate[now], at, pitch), lane + i * L, rounded<DT>(o));
+                if (row_gate && of_rank<L>(a.dgate, a.nranks, now) != nullptr) store_unit<DT, VEC>(shared_row<L>(of_rank<L>(a.dgate, a.nranks, now), at, pitch), lane + i * L, rounded<DT>(o));
             }
             const float rstd = r1;
             const uint32_t next = row + step;
             if (HELD && next < total) {
-                while (next >= a.rows.start[r + 1]) r++;
-                local = next - a.rows.start[r];
+                if constexpr (L < 64) r = rank_for<L>(a.rows, a.nranks, next);
+                else while (next >= a.rows.start[r + 1]) r++;
+                local = next - start_of<L>(a.rows, a.nranks, r);
                 fetch(local);
             }
-            const auto zto = shared_row<L>(a.dz[now], at, pitch);
+            const auto zto = shared_row<L>(of_rank<L>(a.dz, a.nranks, now), at, pitch);
             if (post) {
                 row_totals<L>(t1, t2, &cells[parity][2]);
                 const float mean = rms ? 0.f : t1 * inv, along = t2 * inv;
@@ -420,30 +454,45 @@ __global__ __launch_bounds__(Share<L>::threads) void k_block_backward(BlockBackA
     if constexpr (SUM) {
         // the workgroup's strip of each sum that is wanted
         float* strip = a.partial + uint64_t(blockIdx.x) * a.wanted * a.cols;
-        uint32_t at = 0;
+        if constexpr (L <= 64) {
+            // the rows that a wave holds side by side, then the waves one after the other
+            __shared__ float joined[kSums][NV * E * L];
 #pragma unroll
-        for (int k = 0; k < kSums; k++) {
-            if (!(a.sums >> k & 1)) continue;
-            float* to = strip + uint64_t(at++) * a.cols;
-            if constexpr (L <= 64) {
-                // the rows that a wave holds side by side, then the waves one after the other
-                __shared__ float joined[NV * E * L];
-                __syncthreads();
-                for (int w = 0; w < Share<L>::waves; w++) {
+            for (int k = 0; k < kSums; k++) {
+                if (!(a.sums >> k & 1)) continue;
 #pragma unroll
-                    for (int i = 0; i < NV; i++)
+                for (int i = 0; i < NV; i++)
 #pragma unroll
-                        for (int e = 0; e < E; e++) {
-                            float v = sums[k][i][e];
+                    for (int e = 0; e < E; e++)
 #pragma unroll
-                            for (int m = L; m < 64; m <<= 1) v += __shfl_xor(v, m);
-                            const uint32_t c = (lane + i * L) * E + e;
-                            if (int(threadIdx.x >> 6) == w && (threadIdx.x & 63) < uint32_t(L)) joined[c] = w == 0 ? v : joined[c] + v;
-                        }
-                    __syncthreads();
+                        for (int m = L; m < 64; m <<= 1) sums[k][i][e] += __shfl_xor(sums[k][i][e], m);
+            }
+            for (int w = 0; w < Share<L>::waves; w++) {
+                if (int(threadIdx.x >> 6) == w && (threadIdx.x & 63) < uint32_t(L)) {
+#pragma unroll
+                    for (int k = 0; k < kSums; k++)
+#pragma unroll
+                        for (int i = 0; i < NV; i++)
+#pragma unroll
+                            for (int e = 0; e < E; e++) {
+                                float* at = &joined[k][(lane + i * L) * E + e];
+                                *at = w == 0 ? sums[k][i][e] : *at + sums[k][i][e];
+                            }
                 }
-                for (uint32_t c = threadIdx.x; c < a.cols; c += Share<L>::threads) to[c] = joined[c];
-            } else {
+                __syncthreads();
+            }
+            uint32_t at = 0;
+            for (int k = 0; k < kSums; k++) {
+                if (!(a.sums >> k & 1)) continue;
+                for (uint32_t c = threadIdx.x; c < a.cols; c += Share<L>::threads) strip[uint64_t(at) * a.cols + c] = joined[k][c];
+                at++;
+            }
+        } else {
+            uint32_t at = 0;
+#pragma unroll
+            for (int k = 0; k < kSums; k++) {
+                if (!(a.sums >> k & 1)) continue;
+                float* to = strip + uint64_t(at++) * a.cols;
 #pragma unroll
                 for (int i = 0; i < NV; i++)
 #pragma unroll
@@ -739,7 +788,7 @@ uint32_t strips_of(uint32_t rows, uint32_t cols, int dtype) {
     if (!sums_along(h)) return rows < 256 ? rows : 256;
     const uint32_t per = h.l <= 64 ? 256 / h.l : 1, need = (rows + per - 1) / per;
     uint32_t most = h.l == 1024 ? 256 : 512;
-    if (need < 4 * most) most = (need + 3) / 4;  // at least four rows
+    if (need > 256 && need < 4 * most) most = (need + 3) / 4;  // at least four rows, but for very few
     return need < most ? need : most;
 }
 bool on16(const void* const* list, int n) {

@@ -349,6 +349,11 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
 #pragma unroll
     for (int j = 0; j < S::NI; j++) fb[0][j] = B.cut(fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j), 0);
     f32x4 acc[S::MI][S::NI];
+    // fp32: a sum runs over kRunSteps steps of 16 terms at most, and these sums are
+    // added up apart, so that its error does not grow with every term of a long one.
+    constexpr bool RUNS = DT == kF32;
+    constexpr uint32_t kRunSteps = 32;
+    f32x4 total[RUNS ? S::MI : 1][RUNS ? S::NI : 1];
     // One step, as in matrix_tile.  settled: the bytes of the following step have
     // been waited for already, behind the tile before, and its stores need not be.
     constexpr int turn_reads = S::MI * (MA == kRows ? 1 : 2) + S::NI * (MB == kRows ? 1 : 2);
@@ -376,8 +381,22 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
 #pragma unroll
         for (int i = 0; i < S::MI; i++)
 #pragma unroll
-            for (int j = 0; j < S::NI; j++) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < S::NI; j++) {
+                acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if constexpr (RUNS) total[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
         for (uint32_t k = 0; k < last; k += 4) {
+            if constexpr (RUNS) {
+                if (k % kRunSteps == 0) {
+#pragma unroll
+                    for (int i = 0; i < S::MI; i++)
+#pragma unroll
+                        for (int j = 0; j < S::NI; j++) {
+                            total[i][j] += acc[i][j];
+                            acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                        }
+                }
+            }
             turn(k + 1, settled, s3, s1, fb[0], fb[1]);
             if (step == end) {   // three steps of this tile are left to be multiplied
                 more = next(ahead);
@@ -396,6 +415,12 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
         constexpr uint32_t room = S::stage / S::waves;
         static_assert(room * 16 >= 16 * S::WM * (DT == kBF16 ? 2 : 4) && room * 16 >= 16 * (S::WM < 64 ? S::WM : 64) * 4,
                       "the wave's room holds 16 rows of its features in the type, or of up to 64 of them in fp32");
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int i = 0; i < S::MI; i++)
+#pragma unroll
+                for (int j = 0; j < S::NI; j++) acc[i][j] += total[i][j];
+        }
         if (active) done(now, acc, s3 + wave * room);
         if (!more) break;
         settled = true;

@@ -159,17 +159,16 @@ struct LinearArgs {
     char* dz;                               // [all ranks' rows] rows of zpitch bytes; unused where dz is dy
     float* partial;                         // [tiles of rows][outs (gated: twice)]
     RowTable rows;
-    uint32_t runs, cols, outs, zpitch;
+    uint32_t runs, cols, outs, zpitch, dz_rows;
     int act, gated, need_dz, nranks;
-    int quads, col_quads;                   // rows of outs, of cols, are whole fours, aligned to them
-    int vecs, col_vecs;                     // the same of 16 bytes, where they are written
+    int vecs, col_vecs;                     // rows of outs, of cols, are whole 16 bytes, aligned to them, where they are written
 };
 uint64_t linear_backward_workspace(const RowTable& rows, int nranks, uint32_t runs, uint64_t outs, int act, int gated, bool dbias, int dtype);
 hipError_t launch_linear(const LinearArgs& a, int dtype, hipStream_t s);
 hipError_t launch_linear_backward(const LinearArgs& a, void* workspace, int dtype, hipStream_t s);
 
 // ------------------------------------------------------ the experts' layer --
-// For few tokens: two launches.  Tokens are numbered over all ranks; a slot is
+// For few tokens: two launches, and one more where few columns are split.  Tokens are numbered over all ranks; a slot is
 // one (token, choice).
 constexpr uint32_t kLayerHeader = 64;       // ints of the table before its rows: [0] experts in use, then nothing
 struct LayerArgs {
@@ -186,7 +185,8 @@ struct LayerArgs {
     int32_t* table;                         // header, experts in use and their tokens [used][2], those tokens' slots [used][tpad]
     RowTable rows;
     uint32_t cols, inner, nexperts, per_rank, topk, tokens;
-    uint32_t hpitch, used, tpad;            // used: the most experts that can be in use
+    float* partial;                         // [splits][tokens][cols], with more than one split
+    uint32_t hpitch, used, tpad, splits;    // used: the most experts that can be in use
     uint64_t hpart;
     int act, gated, nranks;
 };

@@ -105,14 +105,14 @@ __device__ __forceinline__ bool make_plan(const LayerArgs& a, uint32_t i, Plan& 
 }
 
 // ---------------------------------------------------------- first product --
-// Tokens [base, base + 16 G) of the plan.
+// Features [m0, m0 + 16) of tokens [base, base + 16 G) of the plan.
 template <int DT, bool VEC, bool GATED, int NW, int G>
-__device__ __forceinline__ void in_tile(const LayerArgs& a, const Plan& p, uint32_t base, f32x4 (*sums)[64]) {
+__device__ __forceinline__ void in_tile(const LayerArgs& a, const Plan& p, uint32_t m0, uint32_t base, f32x4 (*sums)[64]) {
     typedef typename Elem<DT>::type T;
     constexpr int W = GATED ? 2 : 1, P = G > 1 ? 1 : kPairs;
     const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t e = __builtin_amdgcn_readfirstlane(p.expert), q = e / a.per_rank, local = e % a.per_rank;
-    const uint32_t pitch = a.cols * uint32_t(sizeof(T)), m0 = blockIdx.x * 16;
+    const uint32_t pitch = a.cols * uint32_t(sizeof(T));
     // the rows that the lane loads; behind the last one it is repeated
     const uint32_t m = m0 + (lane >> 2) < a.inner ? m0 + (lane >> 2) : a.inner - 1;
     const char *w[W], *x[1][G];
@@ -182,13 +182,34 @@ __global__ __launch_bounds__(NW * 64) void k_layer_in(LayerArgs a) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.table[0] = int32_t(p.used);
     if (!there) return;
     const uint32_t count = __builtin_amdgcn_readfirstlane(p.count);
-    uint32_t base = 0;
-    if constexpr (GM > 1)
-        for (; base < count && count - base > 16; base += 16 * GM) in_tile<DT, VEC, GATED, NW, GM>(a, p, base, sums);
-    for (; base < count; base += 16) in_tile<DT, VEC, GATED, NW, 1>(a, p, base, sums);
+    for (uint32_t m0 = blockIdx.x * 16; m0 < a.inner; m0 += gridDim.x * 16) {
+        uint32_t base = 0;
+        if constexpr (GM > 1)
+            for (; base < count && count - base > 16; base += 16 * GM) in_tile<DT, VEC, GATED, NW, GM>(a, p, m0, base, sums);
+        for (; base < count; base += 16) in_tile<DT, VEC, GATED, NW, 1>(a, p, m0, base, sums);
+    }
 }
 
 // --------------------------------------------------------- second product --
+// Value c of token t's row of `out`: biases and residual.
+template <int DT>
+__device__ __forceinline__ void finish(const LayerArgs& a, uint32_t t, uint32_t c, float v) {
+    typedef typename Elem<DT>::type T;
+    int r = 0;
+    while (r + 1 < a.nranks && t >= a.rows.start[r + 1]) r++;
+    const uint32_t row = t - a.rows.start[r];
+    if (a.b_out[0] != nullptr)
+        for (uint32_t j = 0; j < a.topk; j++) {
+            const int32_t e = expert_of(a, r, row, j);
+            if (e >= 0)
+                v += a.weights[r][uint64_t(row) * a.topk + j] *
+                     Elem<DT>::get(static_cast<const T*>(a.b_out[uint32_t(e) / a.per_rank])[uint64_t(uint32_t(e) % a.per_rank) * a.cols + c]);
+        }
+    const uint64_t at = uint64_t(row) * a.cols + c;
+    if (a.residual[r] != nullptr) v += Elem<DT>::get(static_cast<const T*>(a.residual[r])[at]);
+    static_cast<T*>(a.out[r])[at] = Elem<DT>::put(v);
+}
+
 // Columns [base, base + 16 G) of an expert's list: their share of `out`, 16 values
 // for each token, is added to the wave's own sums in LDS.
 template <int DT, bool VEC, int G>
@@ -224,11 +245,14 @@ __global__ __launch_bounds__(NW * 64) void k_layer_out(LayerArgs a) {
     for (uint32_t i = threadIdx.x; i < NW * a.tokens * 4; i += NW * 64) sums[i] = f32x4{0.f, 0.f, 0.f, 0.f};
     const uint32_t used = __builtin_amdgcn_readfirstlane(a.table[0]);
     __syncthreads();
-    // A unit: one of an expert's `parts` shares of the summed index.  Fewer experts than waves are shared by them.
-    const uint32_t parts = used >= NW ? 1 : used > 0 ? (NW + used - 1) / used : 1;
+    // A unit: one of an expert's `parts` shares of the summed index.  Fewer experts than waves are shared by them, as
+    // far as a share has four pairs of steps.
+    const uint32_t waves = NW * gridDim.y, most = steps / 8 > 0 ? steps / 8 : 1;
+    uint32_t parts = used >= waves ? 1 : used > 0 ? (waves + used - 1) / used : 1;
+    if (parts > most) parts = most;
     const uint32_t m = m0 + (lane >> 2) < a.cols ? m0 + (lane >> 2) : a.cols - 1;
     f32x4* mine = sums + wave * a.tokens * 4;
-    for (uint32_t unit = wave; unit < used * parts; unit += NW) {
+    for (uint32_t unit = blockIdx.y * NW + wave; unit < used * parts; unit += waves) {
         const uint32_t i = unit / parts;
         const uint32_t e = __builtin_amdgcn_readfirstlane(a.table[kLayerHeader + 2 * i]), count = __builtin_amdgcn_readfirstlane(a.table[kLayerHeader + 2 * i + 1]);
         const uint32_t q = e / a.per_rank, local = e % a.per_rank;
@@ -249,38 +273,52 @@ __global__ __launch_bounds__(NW * 64) void k_layer_out(LayerArgs a) {
         float v = 0.f;
 #pragma unroll
         for (uint32_t k = 0; k < NW; k++) v += all[k * a.tokens * 16 + i];
-        int r = 0;
-        while (r + 1 < a.nranks && t >= a.rows.start[r + 1]) r++;
-        const uint32_t row = t - a.rows.start[r];
-        if (a.b_out[0] != nullptr)
-            for (uint32_t j = 0; j < a.topk; j++) {
-                const int32_t e = expert_of(a, r, row, j);
-                if (e >= 0)
-                    v += a.weights[r][uint64_t(row) * a.topk + j] *
-                         Elem<DT>::get(static_cast<const T*>(a.b_out[uint32_t(e) / a.per_rank])[uint64_t(uint32_t(e) % a.per_rank) * a.cols + c]);
-            }
-        const uint64_t at = uint64_t(row) * a.cols + c;
-        if (a.residual[r] != nullptr) v += Elem<DT>::get(static_cast<const T*>(a.residual[r])[at]);
-        static_cast<T*>(a.out[r])[at] = Elem<DT>::put(v);
+        if (a.splits > 1) a.partial[(uint64_t(blockIdx.y) * a.tokens + t) * a.cols + c] = v;
+        else finish<DT>(a, t, c, v);
     }
+}
+
+// The workgroups' shares of `out` added up in order, where the experts are split among several.
+template <int DT>
+__global__ __launch_bounds__(kBlock) void k_layer_join(LayerArgs a) {
+    const uint32_t c = blockIdx.x * kBlock + threadIdx.x, t = blockIdx.y;
+    if (c >= a.cols) return;
+    float v = 0.f;
+    for (uint32_t k = 0; k < a.splits; k++) v += a.partial[(uint64_t(k) * a.tokens + t) * a.cols + c];
+    finish<DT>(a, t, c, v);
 }
 
 // -------------------------------------------------------------------- host --
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 
+// Waves of the second product's workgroups; their sums take 64 bytes of LDS each for
+// a token: 16 for up to 128 of them.  Many tokens to an expert take the registers of
+// 8 (128 tokens to 4 of 64 experts of 2048 x 4096 bf16: 239 us with 16).
+bool many_tokens(uint64_t slots, uint64_t used) { return slots > 24 * used; }
+uint32_t out_waves(uint64_t tokens, uint64_t slots, uint64_t used) { return tokens > 128 || many_tokens(slots, used) ? 8 : 16; }
+
 struct LayerParts {
-    uint64_t hpitch, hpart, table, bytes;
-    uint32_t used, tpad;
+    uint64_t hpitch, hpart, table, partial, bytes;
+    uint32_t used, tpad, splits;
 };
-LayerParts layer_parts(uint64_t tokens, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype) {
+LayerParts layer_parts(uint64_t tokens, uint64_t cols, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype) {
     LayerParts b;
     const uint64_t slots = tokens * topk;
     b.hpitch = up(inner * (dtype == kBF16 ? 2 : 4), 16);
     b.hpart = slots * b.hpitch;
     b.used = uint32_t(slots < nexperts ? slots : nexperts);
     b.tpad = uint32_t(up(tokens, 16));
+    // Few columns are too few workgroups for the experts' bytes: the experts are split among several then, each wave
+    // with four pairs of steps at least, and a third launch adds up (108 tokens of 192 to 3 of 72 experts of 3840 bf16:
+    // 299 us in 12 workgroups).
+    const uint64_t tiles = (cols + 15) / 16, steps = (b.hpitch + kStepBytes - 1) / kStepBytes;
+    uint64_t splits = 256 / tiles;
+    const uint64_t most = b.used * steps / (out_waves(tokens, slots, b.used) * 8);
+    if (splits > most) splits = most;
+    b.splits = uint32_t(splits < 1 ? 1 : splits > 32 ? 32 : splits);
     b.table = up(b.hpart * (dtype == kBF16 ? 2 : 1), 256);
-    b.bytes = b.table + up((kLayerHeader + 2 * uint64_t(b.used) + uint64_t(b.used) * b.tpad) * 4, 256);
+    b.partial = b.table + up((kLayerHeader + 2 * uint64_t(b.used) + uint64_t(b.used) * b.tpad) * 4, 256);
+    b.bytes = b.partial + (b.splits > 1 ? up(b.splits * tokens * cols * 4, 256) : 0);
     return b;
 }
 bool on16(const void* const* list, int n) {
@@ -293,21 +331,24 @@ bool on16(const void* const* list, int n) {
 // summed index.  Many tokens to an expert: 64 of them at a time.
 template <int DT, bool VEC, bool GATED>
 void first(const LayerArgs& a, hipStream_t s) {
-    const dim3 grid((a.inner + 15) / 16, a.used);
-    const bool many = uint64_t(a.tokens) * a.topk > 24 * uint64_t(a.used);
-    if (many) hipLaunchKernelGGL((k_layer_in<DT, VEC, GATED, 4, 4>), grid, dim3(4 * 64), 0, s, a);
+    // Where the weights' rows are short a workgroup takes several tiles of them: each makes the plan for itself, which
+    // takes as long as 64 KiB of weights (108 tokens of 192 to 3 of 72 experts of 2 x 3840 bf16: 128 us with one tile).
+    const uint64_t tiles = (a.inner + 15) / 16, bytes = uint64_t(GATED ? 32 : 16) * a.cols * sizeof(typename Elem<DT>::type);
+    uint64_t each = bytes < 65536 ? 65536 / bytes : 1;
+    while (each > 1 && tiles / each * a.used < 1024) each /= 2;
+    const dim3 grid(uint32_t((tiles + each - 1) / each), a.used);
+    if (many_tokens(uint64_t(a.tokens) * a.topk, a.used)) hipLaunchKernelGGL((k_layer_in<DT, VEC, GATED, 4, 4>), grid, dim3(4 * 64), 0, s, a);
     else if (uint64_t(grid.x) * grid.y <= 1024) hipLaunchKernelGGL((k_layer_in<DT, VEC, GATED, 16, 1>), grid, dim3(16 * 64), 0, s, a);
     else hipLaunchKernelGGL((k_layer_in<DT, VEC, GATED, 4, 1>), grid, dim3(4 * 64), 0, s, a);
 }
-// The waves' sums take 64 bytes of LDS each for a token: 16 waves for up to 128 of
-// them (128 tokens to 4 of 64 experts of 2048 x 4096 bf16: 289 us with 8, 0 with 16).
 template <int DT, bool VEC>
 void second(const LayerArgs& a, hipStream_t s) {
-    const dim3 grid((a.cols + 15) / 16);
-    const bool many = uint64_t(a.tokens) * a.topk > 24 * uint64_t(a.used);
-    if (many) hipLaunchKernelGGL((k_layer_out<DT, VEC, 8, 4>), grid, dim3(8 * 64), 8 * a.tokens * 64, s, a);
-    else if (a.tokens > 128) hipLaunchKernelGGL((k_layer_out<DT, VEC, 8, 1>), grid, dim3(8 * 64), 8 * a.tokens * 64, s, a);
+    const dim3 grid((a.cols + 15) / 16, a.splits);
+    const uint64_t slots = uint64_t(a.tokens) * a.topk;
+    if (many_tokens(slots, a.used)) hipLaunchKernelGGL((k_layer_out<DT, VEC, 8, 4>), grid, dim3(8 * 64), 8 * a.tokens * 64, s, a);
+    else if (out_waves(a.tokens, slots, a.used) == 8) hipLaunchKernelGGL((k_layer_out<DT, VEC, 8, 1>), grid, dim3(8 * 64), 8 * a.tokens * 64, s, a);
     else hipLaunchKernelGGL((k_layer_out<DT, VEC, 16, 1>), grid, dim3(16 * 64), 16 * a.tokens * 64, s, a);
+    if (a.splits > 1) hipLaunchKernelGGL(k_layer_join<DT>, dim3((a.cols + kBlock - 1) / kBlock, a.tokens), dim3(kBlock), 0, s, a);
 }
 template <int DT>
 hipError_t layer(const LayerArgs& a, hipStream_t s) {
@@ -322,18 +363,20 @@ hipError_t layer(const LayerArgs& a, hipStream_t s) {
 
 }  // namespace
 
-uint64_t layer_workspace(uint64_t tokens, uint64_t, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype) {
-    return tokens == 0 ? 0 : layer_parts(tokens, inner, nexperts, topk, dtype).bytes;
+uint64_t layer_workspace(uint64_t tokens, uint64_t cols, uint64_t inner, uint32_t nexperts, uint32_t topk, int dtype) {
+    return tokens == 0 ? 0 : layer_parts(tokens, cols, inner, nexperts, topk, dtype).bytes;
 }
 
 hipError_t launch_layer(LayerArgs a, void* workspace, int dtype, hipStream_t s) {
-    const LayerParts b = layer_parts(a.tokens, a.inner, a.nexperts, a.topk, dtype);
+    const LayerParts b = layer_parts(a.tokens, a.cols, a.inner, a.nexperts, a.topk, dtype);
     a.hidden = static_cast<char*>(workspace);
     a.hpitch = uint32_t(b.hpitch);
     a.hpart = b.hpart;
     a.table = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + b.table);
     a.used = b.used;
     a.tpad = b.tpad;
+    a.splits = b.splits;
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + b.partial);
     return dtype == kBF16 ? layer<kBF16>(a, s) : layer<kF32>(a, s);
 }
 

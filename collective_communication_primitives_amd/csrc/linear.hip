@@ -228,14 +228,24 @@ __device__ __forceinline__ u32x4* loose_tile(const OA& A, const OB& B, uint32_t 
     return &stage[0][0] + wave * (S::stage / S::waves);
 }
 
-// Four neighbouring values; quads: stored and read as one.
+// Four neighbouring values at any element, `left` of them before the row's end.
 template <int DT>
-__device__ __forceinline__ f32x4 load_four(const typename Elem<DT>::type* p, bool quads, uint32_t left) {
+struct Four;
+template <>
+struct Four<kBF16> {
+    typedef uint32_t type __attribute__((ext_vector_type(2), aligned(2)));
+};
+template <>
+struct Four<kF32> {
+    typedef uint32_t type __attribute__((ext_vector_type(4), aligned(4)));
+};
+template <int DT>
+__device__ __forceinline__ f32x4 load_four(const typename Elem<DT>::type* p, uint32_t left) {
     typedef typename Elem<DT>::type T;
     T t[4];
-    if (quads) {
-        if constexpr (DT == kBF16) *reinterpret_cast<uint2*>(t) = *reinterpret_cast<const uint2*>(p);
-        else *reinterpret_cast<u32x4*>(t) = *reinterpret_cast<const u32x4*>(p);
+    if (left >= 4) {
+        const typename Four<DT>::type v = *reinterpret_cast<const typename Four<DT>::type*>(p);
+        __builtin_memcpy(t, &v, sizeof t);
     } else {
 #pragma unroll
         for (int e = 0; e < 4; e++) t[e] = uint32_t(e) < left ? p[e] : T(0);
@@ -243,13 +253,18 @@ __device__ __forceinline__ f32x4 load_four(const typename Elem<DT>::type* p, boo
     return f32x4{Elem<DT>::get(t[0]), Elem<DT>::get(t[1]), Elem<DT>::get(t[2]), Elem<DT>::get(t[3])};
 }
 template <int DT>
-__device__ __forceinline__ void store_four(typename Elem<DT>::type* p, f32x4 v, bool quads, uint32_t left) {
-    if (quads) {
-        store_quad<DT>(p, v, true);
+__device__ __forceinline__ void store_four(typename Elem<DT>::type* p, f32x4 v, uint32_t left) {
+    typedef typename Elem<DT>::type T;
+    T t[4];
+    store_quad<DT>(t, v, true);
+    if (left >= 4) {
+        typename Four<DT>::type o;
+        __builtin_memcpy(&o, t, sizeof t);
+        *reinterpret_cast<typename Four<DT>::type*>(p) = o;
     } else {
 #pragma unroll
         for (int e = 0; e < 4; e++)
-            if (uint32_t(e) < left) p[e] = Elem<DT>::put(v[e]);
+            if (uint32_t(e) < left) p[e] = t[e];
     }
 }
 
@@ -370,7 +385,7 @@ __device__ __forceinline__ void epilogue(const LinearArgs& a, const LinearTile& 
 enum { kWhole = 0, kTail = 1, kLoose = 2 };
 
 template <int DT, typename S, int PATH, bool GATED>
-__global__ __launch_bounds__(S::threads) void k_linear(LinearArgs a) {
+__global__ __launch_bounds__(S::threads, 2) void k_linear(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t BM = GATED ? S::BM / 2 : S::BM;   // features of a tile
     __shared__ Runs runs;
@@ -448,19 +463,19 @@ __device__ __forceinline__ void few_rows(const LinearArgs& a, const Run& r, uint
         const uint64_t row = uint64_t(r.lo) + n;
         if (a.bias[r.rank] != nullptr) {
             const T* b = static_cast<const T*>(a.bias[r.rank]) + uint64_t(r.run) * wide + f;
-            z += load_four<DT>(b, a.quads, left);
-            if (GATED) u += load_four<DT>(b + a.outs, a.quads, left);
+            z += load_four<DT>(b, left);
+            if (GATED) u += load_four<DT>(b + a.outs, left);
         }
         if (a.pre[r.rank] != nullptr) {
             T* to = static_cast<T*>(a.pre[r.rank]) + row * wide + f;
-            store_four<DT>(to, z, a.quads, left);
-            if (GATED) store_four<DT>(to + a.outs, u, a.quads, left);
+            store_four<DT>(to, z, left);
+            if (GATED) store_four<DT>(to + a.outs, u, left);
         }
         f32x4 y;
 #pragma unroll
         for (int e = 0; e < 4; e++) y[e] = act(z[e], a.act) * (GATED ? u[e] : 1.f);
-        if (a.residual[r.rank] != nullptr) y += load_four<DT>(static_cast<const T*>(a.residual[r.rank]) + row * a.outs + f, a.quads, left);
-        store_four<DT>(static_cast<T*>(a.y[r.rank]) + row * a.outs + f, y, a.quads, left);
+        if (a.residual[r.rank] != nullptr) y += load_four<DT>(static_cast<const T*>(a.residual[r.rank]) + row * a.outs + f, left);
+        store_four<DT>(static_cast<T*>(a.y[r.rank]) + row * a.outs + f, y, left);
     }
     __syncthreads();  // the next rows' sums
 }
@@ -475,59 +490,58 @@ __global__ __launch_bounds__(NW * 64) void k_linear_few(LinearArgs a) {
 }
 
 // --------------------------------------------------------------- backward --
-// dz of the runs' rows, kDzRows rows and 1024 columns to a workgroup, and its
-// columns' sums over those rows.  A thread has four neighbouring columns.
-constexpr uint32_t kDzRows = 64;
-
+// dz of the runs' rows, dz_rows of them and 1024 columns to a workgroup, and its
+// columns' sums over those rows.  A thread has four neighbouring columns, and four
+// rows' loads go out together.  Bound by memory: 52432 rows of 2048 gated, bf16, 236 us, 4.5 TB/s.
 template <int DT, bool GATED>
 __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     __shared__ Runs runs;
-    count_tiles(a, kDzRows, runs);
+    count_tiles(a, a.dz_rows, runs);
     const uint32_t groups = a.runs * a.nranks, tiles = runs.first[groups], m = (blockIdx.x * kThreads + threadIdx.x) * 4;
     const uint32_t wide = GATED ? 2 * a.outs : a.outs;
     const uint64_t ldz = a.zpitch / sizeof(T);
-    const bool quads = a.quads;
     if (m >= a.outs) return;
     const uint32_t left = a.outs - m;
     for (uint32_t t = blockIdx.y; t < tiles; t += gridDim.y) {
         const uint32_t g = run_of_tile(runs.first, groups, t);
         const Run r = run_of(a, runs, g);
-        const uint32_t n0 = (t - runs.first[g]) * kDzRows, rows = r.count - n0 < kDzRows ? r.count - n0 : kDzRows;
+        const uint32_t n0 = (t - runs.first[g]) * a.dz_rows, rows = r.count - n0 < a.dz_rows ? r.count - n0 : a.dz_rows;
         const uint64_t row0 = r.lo + n0;
         const T* dy = static_cast<const T*>(a.dy[r.rank]) + row0 * a.outs + m;
         const T* pre = a.need_dz ? static_cast<const T*>(a.saved[r.rank]) + row0 * wide + m : nullptr;
         T* dz = a.need_dz ? reinterpret_cast<T*>(a.dz) + (a.rows.start[r.rank] + row0) * ldz : nullptr;
         f32x4 sum = {0.f, 0.f, 0.f, 0.f}, sumu = sum;
-        for (uint32_t n = 0; n < rows; n++) {
-            f32x4 d = load_four<DT>(dy + uint64_t(n) * a.outs, quads, left), du = {0.f, 0.f, 0.f, 0.f};
-            if (a.need_dz) {
-                const f32x4 z = load_four<DT>(pre + uint64_t(n) * wide, quads, left);
-                if (GATED) {
-                    const f32x4 u = load_four<DT>(pre + uint64_t(n) * wide + a.outs, quads, left);
+        for (uint32_t n = 0; n < rows; n += 4) {
+            f32x4 d[4], z[4], u[4];
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        float value, slope;
-                        act_and_slope(z[e], a.act, value, slope);
-                        du[e] = d[e] * value;
-                        d[e] = d[e] * u[e] * slope;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        float value, slope;
-                        act_and_slope(z[e], a.act, value, slope);
-                        d[e] *= slope;
-                    }
-                }
-                T* to = dz + n * ldz;
-                store_four<DT>(to + m, d, quads, left);
-                if (GATED) store_four<DT>(to + a.outs + m, du, quads, left);
-                if (left <= 4)  // what lies between the row's end and its pitch
-                    for (uint64_t c = wide; c < ldz; c++) to[c] = T(0);
+            for (int i = 0; i < 4; i++) {
+                const uint32_t row = n + i < rows ? n + i : rows - 1;   // the last row again, and nothing of it is used
+                d[i] = load_four<DT>(dy + uint64_t(row) * a.outs, left);
+                if (a.need_dz) z[i] = load_four<DT>(pre + uint64_t(row) * wide, left);
+                if (GATED) u[i] = load_four<DT>(pre + uint64_t(row) * wide + a.outs, left);
             }
-            sum += d;
-            if (GATED) sumu += du;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (n + i >= rows) break;
+                f32x4 du = {0.f, 0.f, 0.f, 0.f};
+                if (a.need_dz) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        float value, slope;
+                        act_and_slope(z[i][e], a.act, value, slope);
+                        if (GATED) du[e] = d[i][e] * value;
+                        d[i][e] *= GATED ? u[i][e] * slope : slope;
+                    }
+                    T* to = dz + (n + i) * ldz;
+                    store_four<DT>(to + m, d[i], left);
+                    if (GATED) store_four<DT>(to + a.outs + m, du, left);
+                    if (left <= 4)  // what lies between the row's end and its pitch
+                        for (uint64_t c = wide; c < ldz; c++) to[c] = T(0);
+                }
+                sum += d[i];
+                if (GATED) sumu += du;
+            }
         }
         if (a.partial != nullptr) {
             float* to = a.partial + uint64_t(t) * wide + m;
@@ -541,16 +555,31 @@ __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
     }
 }
 
-// db of run blockIdx.y: its tiles' sums in order.
+// db of run blockIdx.y: its tiles' sums in a fixed order, 64 columns to a workgroup,
+// of whose 16 waves each takes every 16th tile.
 template <int DT>
-__global__ __launch_bounds__(kThreads) void k_linear_dbias(LinearArgs a) {
+__global__ __launch_bounds__(1024) void k_linear_dbias(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     __shared__ Runs runs;
-    count_tiles(a, kDzRows, runs);
-    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, c = blockIdx.x * kThreads + threadIdx.x, g = blockIdx.y;
-    if (c >= wide) return;
+    __shared__ float sums[16][64];
+    count_tiles(a, a.dz_rows, runs);
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, g = blockIdx.y;
+    const uint32_t end = runs.first[g + 1];
     float s = 0.f;
-    for (uint32_t t = runs.first[g]; t < runs.first[g + 1]; t++) s += a.partial[uint64_t(t) * wide + c];
+    if (c < wide)
+        for (uint32_t t = runs.first[g] + wave; t < end; t += 16 * 4) {
+            float v[4];  // four tiles' loads go out before the first is added
+#pragma unroll
+            for (int k = 0; k < 4; k++) v[k] = t + 16 * k < end ? a.partial[uint64_t(t + 16 * k) * wide + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; k++) s += v[k];
+        }
+    sums[wave][lane] = s;
+    __syncthreads();
+    if (wave != 0 || c >= wide) return;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; k++) s += sums[k][lane];
     static_cast<T*>(a.dbias[g / a.runs])[uint64_t(g % a.runs) * wide + c] = Elem<DT>::put(s);
 }
 
@@ -585,14 +614,14 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, typename Elem<DT
         for (int i = 0; i < S::MI; i++) {
             const uint32_t m = mw + i * 16 + (lane >> 4) * 4;
             if (m >= cols) continue;
-            store_four<DT>(out + uint64_t(n0 + n) * cols + m, acc[i][j], a.col_quads, cols - m);
+            store_four<DT>(out + uint64_t(n0 + n) * cols + m, acc[i][j], cols - m);
         }
     }
 }
 
 // dx[t][k] = sum over the features of dz[t][m] W[m][k].
 template <int DT, typename S, int PATH>
-__global__ __launch_bounds__(S::threads) void k_linear_dx(LinearArgs a) {
+__global__ __launch_bounds__(S::threads, 2) void k_linear_dx(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t es = sizeof(T);
     __shared__ Runs runs;
@@ -624,7 +653,7 @@ __global__ __launch_bounds__(S::threads) void k_linear_dx(LinearArgs a) {
 
 // dW[m][k] = sum over the run's rows of dz[t][m] x[t][k]; zeros for a run without rows.
 template <int DT, typename S, int PATH>
-__global__ __launch_bounds__(S::threads) void k_linear_dweight(LinearArgs a) {
+__global__ __launch_bounds__(S::threads, 2) void k_linear_dweight(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t es = sizeof(T), KR = kStepBytes / es;
     __shared__ Runs runs;
@@ -661,7 +690,6 @@ typedef Shape<64, 64, 2, 2> Small;
 typedef Shape<64, 16, 1, 1> Tiny;
 enum Tile { kWide, kSquare, kSmall, kTiny };
 constexpr uint32_t kTileM[] = {256, 128, 64, 64}, kTileN[] = {256, 128, 64, 16};
-constexpr uint32_t kTilesPerCu[] = {1, 2, 4, 6};   // workgroups of a tile's LDS that share a CU
 
 // The tile for products of m features with runs of `mean` rows each.
 Tile pick_tile(int dtype, uint64_t m, uint64_t mean, uint64_t groups, int path, bool tiny) {
@@ -683,15 +711,18 @@ void with_tile(Tile t, F&& launch) {
     if (t == kSquare) launch(Square());
     else launch(Small());
 }
-template <typename F>
+// launch(path).  fp32 rows always start on 4-byte boundaries.
+template <int DT, typename F>
 void with_path(int path, F&& launch) {
     if (path == kWhole) launch(std::integral_constant<int, kWhole>());
-    else if (path == kTail) launch(std::integral_constant<int, kTail>());
-    else launch(std::integral_constant<int, kLoose>());
+    else if (DT == kF32 || path == kTail) launch(std::integral_constant<int, kTail>());
+    else if constexpr (DT == kBF16) launch(std::integral_constant<int, kLoose>());
 }
-// Workgroups that walk over at most `tiles` tiles: as many as run at a time.
+// Workgroups that walk over at most `tiles` tiles.  The widest ones: as many as run
+// at a time, one to a CU, whose loads run on from tile to tile.  Of smaller ones
+// several share a CU and fill each other's gaps: one to a tile, as far as that goes.
 uint32_t walkers(uint64_t tiles, Tile t) {
-    const uint64_t most = 256 * kTilesPerCu[t];
+    const uint64_t most = t == kWide ? 256 : 1 << 14;
     return uint32_t(tiles < 1 ? 1 : tiles < most ? tiles : most);
 }
 
@@ -727,13 +758,12 @@ hipError_t forward(LinearArgs a, hipStream_t s) {
     a.vecs = a.outs * es % 16 == 0 && on(a.y, a.nranks, 16) && on(a.pre, a.nranks, 16) && on(a.bias, a.nranks, 16) && on(a.residual, a.nranks, 16);
     const uint64_t features = uint64_t(a.outs) * (a.gated ? 2 : 1);
     if (few_rows_to_run(DT, features, ceil_div(rows, groups), groups)) {
-        a.quads = a.outs % 4 == 0 && on(a.bias, a.nranks, 4 * es) && on(a.residual, a.nranks, 4 * es) && on(a.y, a.nranks, 4 * es) && on(a.pre, a.nranks, 4 * es);
         const bool vec = a.cols * es % 16 == 0 && on(a.x, a.nranks, 16) && on(a.weight, a.nranks, 16);
         if (a.gated) vec ? few<DT, true, true>(a, s) : few<DT, false, true>(a, s);
         else vec ? few<DT, true, false>(a, s) : few<DT, false, false>(a, s);
         return hipGetLastError();
     }
-    with_path(path_of(a.cols * es, on(a.x, a.nranks, 4) && on(a.weight, a.nranks, 4)), [&](auto path) {
+    with_path<DT>(path_of(a.cols * es, on(a.x, a.nranks, 4) && on(a.weight, a.nranks, 4)), [&](auto path) {
         constexpr int P = decltype(path)::value;
         const Tile t = pick_tile(DT, features, ceil_div(rows, groups), groups, P, false);
         // a run ends inside a tile, so there are up to one tile more than its rows fill
@@ -748,9 +778,12 @@ hipError_t forward(LinearArgs a, hipStream_t s) {
 }
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
-uint64_t dz_tiles(const RowTable& rows, int nranks, uint32_t runs) {
+// Rows of a workgroup that forms dz: 32, or 8 where those would be too few
+// workgroups (3762 rows of 509 fp32 with gelu: 41 us with 32).
+uint32_t dz_rows(uint64_t rows, uint64_t wide) { return rows / 32 * ceil_div(wide, 4 * kThreads) >= 1024 ? 32 : 8; }
+uint64_t dz_tiles(const RowTable& rows, int nranks, uint32_t runs, uint64_t wide) {
     const uint64_t n = rows.start[nranks], groups = uint64_t(runs) * nranks;
-    return n / kDzRows + (groups < n ? groups : n);
+    return n / dz_rows(n, wide) + (groups < n ? groups : n);
 }
 struct BackwardParts {
     uint64_t dz, partial, bytes;
@@ -760,7 +793,7 @@ BackwardParts backward_parts(const RowTable& rows, int nranks, uint32_t runs, ui
     BackwardParts b;
     b.dz = 0;
     b.partial = need_dz ? up(rows.start[nranks] * up(wide * es, 16), 256) : 0;
-    b.bytes = b.partial + (dbias ? up(dz_tiles(rows, nranks, runs) * wide * 4, 256) : 0);
+    b.bytes = b.partial + (dbias ? up(dz_tiles(rows, nranks, runs, wide) * wide * 4, 256) : 0);
     return b;
 }
 
@@ -772,22 +805,21 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
     const BackwardParts b = backward_parts(a.rows, a.nranks, a.runs, wide, a.need_dz, dbias, DT);
     a.dz = workspace + b.dz;
     a.zpitch = uint32_t(a.need_dz ? up(wide * es, 16) : wide * es);
+    a.dz_rows = dz_rows(rows, wide);
     a.partial = dbias ? reinterpret_cast<float*>(workspace + b.partial) : nullptr;
-    a.quads = a.outs % 4 == 0 && on(a.dy, a.nranks, 4 * es) && (!a.need_dz || on(a.saved, a.nranks, 4 * es));
     a.col_vecs = a.cols * es % 16 == 0 && on(a.dx, a.nranks, 16) && on(a.dweight, a.nranks, 16);
-    a.col_quads = a.cols % 4 == 0 && on(a.dx, a.nranks, 4 * es) && on(a.dweight, a.nranks, 4 * es);
     if (rows > 0 && (a.need_dz || dbias)) {
-        const uint64_t tiles = dz_tiles(a.rows, a.nranks, a.runs), across = ceil_div(a.outs, 4 * kThreads), most = ceil_div(4096, across);
+        const uint64_t tiles = dz_tiles(a.rows, a.nranks, a.runs, wide), across = ceil_div(a.outs, 4 * kThreads), most = ceil_div(4096, across);
         const dim3 grid(uint32_t(across), uint32_t(tiles < most ? tiles : most));
         if (a.gated) hipLaunchKernelGGL((k_linear_dz<DT, true>), grid, dim3(kThreads), 0, s, a);
         else hipLaunchKernelGGL((k_linear_dz<DT, false>), grid, dim3(kThreads), 0, s, a);
     }
-    if (dbias) hipLaunchKernelGGL(k_linear_dbias<DT>, dim3(uint32_t(ceil_div(wide, kThreads)), uint32_t(groups)), dim3(kThreads), 0, s, a);
+    if (dbias) hipLaunchKernelGGL(k_linear_dbias<DT>, dim3(uint32_t(ceil_div(wide, 64)), uint32_t(groups)), dim3(1024), 0, s, a);
     const bool dz4 = a.need_dz || on(a.dy, a.nranks, 4), x4 = on(a.x, a.nranks, 4), w4 = on(a.weight, a.nranks, 4);
     if (rows > 0) {
         // dx: only dz' rows can end inside 16 bytes that count
         const int zp = path_of(a.zpitch, dz4), wp = path_of(a.cols * es, w4);
-        with_path(zp == kLoose || wp == kLoose ? kLoose : zp, [&](auto path) {
+        with_path<DT>(zp == kLoose || wp == kLoose ? kLoose : zp, [&](auto path) {
             constexpr int P = decltype(path)::value;
             const Tile t = pick_tile(DT, a.cols, ceil_div(rows, groups), groups, P, true);
             const uint64_t tiles = ceil_div(a.cols, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
@@ -806,8 +838,13 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
             hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)), dim3(S::threads), 0, s, a);
         });
     };
-    if (loose) dweight(std::integral_constant<int, kLoose>());
-    else dweight(std::integral_constant<int, kWhole>());
+    if constexpr (DT == kBF16) {
+        if (loose) {
+            dweight(std::integral_constant<int, kLoose>());
+            return hipGetLastError();
+        }
+    }
+    dweight(std::integral_constant<int, kWhole>());
     return hipGetLastError();
 }
 

@@ -80,18 +80,17 @@ class Ranges {
         else if (lo % align != 0) st_ = fail(DT_ERR_ARG, "%s[%d] is not aligned to its elements", name, index);
         else r_[n_++] = Range{lo, lo + n, name, index, write};
     }
+    // Written ranges are put in order and may not meet; each range that is read is
+    // then looked up among them.
     dt_status check(const char* what) {
         if (st_ != DT_OK) return st_;
-        std::sort(r_, r_ + n_, [](const Range& a, const Range& b) { return a.lo < b.lo; });
-        const Range* any = nullptr;      // the range, and the written one, that reach furthest so far
-        const Range* written = nullptr;
-        for (int i = 0; i < n_; i++) {
-            const Range& x = r_[i];
-            const Range* hit = x.write ? any : written;
-            if (hit != nullptr && x.lo < hit->hi)
-                return fail(DT_ERR_ARG, "%s: %s[%d] and %s[%d] overlap", what, hit->name, hit->index, x.name, x.index);
-            if (any == nullptr || x.hi > any->hi) any = &x;
-            if (x.write && (written == nullptr || x.hi > written->hi)) written = &x;
+        Range* const end = std::partition(r_, r_ + n_, [](const Range& a) { return a.write; });
+        std::sort(r_, end, [](const Range& a, const Range& b) { return a.lo < b.lo; });
+        for (const Range* x = r_ + 1; x < end; x++)
+            if (x->lo < x[-1].hi) return overlap(what, x[-1], *x);
+        for (const Range* x = end; x < r_ + n_; x++) {
+            const Range* next = std::lower_bound(r_, end, x->hi, [](const Range& a, uintptr_t at) { return a.lo < at; });
+            if (next != r_ && x->lo < next[-1].hi) return next[-1].lo < x->lo ? overlap(what, next[-1], *x) : overlap(what, *x, next[-1]);
         }
         return DT_OK;
     }
@@ -103,6 +102,9 @@ class Ranges {
         int index;
         bool write;
     };
+    static dt_status overlap(const char* what, const Range& a, const Range& b) {
+        return fail(DT_ERR_ARG, "%s: %s[%d] and %s[%d] overlap", what, a.name, a.index, b.name, b.index);
+    }
     Range r_[17 * DT_MAX_RANKS];
     int n_ = 0;
     dt_status st_ = DT_OK;

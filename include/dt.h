@@ -426,8 +426,8 @@ dt_status dt_linear_backward(const void* const* dy, const void* const* x, const 
                              dt_dtype dtype, void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* The experts' layer for few tokens (at most DT_MAX_LAYER_TOKENS over all ranks),
- * what dt_moe_dispatch, two dt_linear and dt_moe_combine do, in two launches that
- * read each chosen expert's weights once:
+ * what dt_moe_dispatch, two dt_linear and dt_moe_combine do, in two launches (three
+ * where cols is small) that read each chosen expert's weights once:
  *   out[r][t] = residual[r][t] + sum over the slots j of weights[r][t,j] *
  *               (w_out_e act(w_in_e x[r][t] + b_in_e) + b_out_e),   e = experts[r][t,j]
  * with experts and weights as dt_moe_route leaves them (an expert outside [0, E)

@@ -182,14 +182,20 @@ __device__ __forceinline__ u32x4 fragment(const u32x4* tile, uint32_t place, int
     }
 }
 
-// Waits until at most `loads` of this wave's loads and `reads` of its LDS reads
-// (15: as many as the counter holds) are outstanding, then for the workgroup's
-// other waves.
+// Waits until at most `loads` of this wave's loads (63: any number) and `reads`
+// of its LDS reads (15: as many as the counter holds) are outstanding.
 template <int loads, int reads>
-__device__ __forceinline__ void arrive() {
+__device__ __forceinline__ void wait() {
     static_assert(loads < 64 && reads < 16, "the counters hold 6 and 4 bits");
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((loads & 15) | (loads >> 4) << 14 | 7 << 4 | reads << 8);
+    asm volatile("" ::: "memory");
+}
+
+// The same, and then waits for the workgroup's other waves.
+template <int loads, int reads>
+__device__ __forceinline__ void arrive() {
+    wait<loads, reads>();
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -359,11 +365,12 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
     constexpr int turn_reads = S::MI * (MA == kRows ? 1 : 2) + S::NI * (MB == kRows ? 1 : 2);
     bool active = wn < rows(ahead);   // the wave has rows in the tile that is multiplied
     auto turn = [&](uint32_t following_step, bool settled, u32x4* free, const u32x4* following, const u32x4 (&fn)[S::NI], u32x4 (&fnext)[S::NI]) {
-        if (settled) arrive<63, turn_reads < 15 ? turn_reads : 15>();
-        else arrive<S::loads, turn_reads < 15 ? turn_reads : 15>();
+        if (!settled) wait<S::loads, 15>();
+        arrive<63, turn_reads < 15 ? turn_reads : 15>();
         load(free);
         // keeps the compiler from holding every fragment's address of every stage in a register
         asm volatile("" : "+v"(ra), "+v"(rb));
+        wait<63, 0>();   // the last turn's reads, in waves without rows as well: their stage is loaded again in the next turn
         if (!active && following_step != 0) return;
 #pragma unroll
         for (int j = 0; j < S::NI; j++) fnext[j] = B.cut(fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j), following_step);

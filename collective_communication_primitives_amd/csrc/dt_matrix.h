@@ -53,9 +53,9 @@ template <bool TAIL>
 struct RowOperand {
     static constexpr bool tail = TAIL;
     const char* p;     // the tile's first row
-    uint32_t rows, pitch, bytes, valid;
+    uint32_t rows, pitch, bytes, valid, skip;   // skip: bytes of a row before p
     __device__ __forceinline__ rsrc_t at(uint32_t step, bool any) const {
-        return scalar_rsrc(p + step * kStepBytes, any && rows > 0 ? rows * pitch - step * kStepBytes : 0);
+        return scalar_rsrc(p + step * kStepBytes, any && rows > 0 ? rows * pitch - skip - step * kStepBytes : 0);
     }
     __device__ __forceinline__ uint32_t left(uint32_t step) const { return bytes - step * kStepBytes; }
     __device__ __forceinline__ uint32_t group_at(uint32_t group) const { return group * 16 * pitch; }  // 16 rows of the tile

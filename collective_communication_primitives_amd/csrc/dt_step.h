@@ -158,8 +158,10 @@ struct LinearArgs {
     void* dbias[kMaxRanksHost];
     char* dz;                               // [all ranks' rows] rows of zpitch bytes; unused where dz is dy
     float* partial;                         // [tiles of rows][outs (gated: twice)]
+    float* sums;                            // [splits][all ranks' rows][cols], or [splits][all ranks' runs][outs (gated: twice)][cols]
     RowTable rows;
     uint32_t runs, cols, outs, zpitch, dz_rows;
+    uint32_t splits;                        // parts of the summed index, of dx or of dweight
     int act, gated, need_dz, nranks;
     int vecs, col_vecs;                     // rows of outs, of cols, are whole 16 bytes, aligned to them, where they are written
 };

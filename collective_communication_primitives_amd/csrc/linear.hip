@@ -97,11 +97,17 @@ __device__ __forceinline__ uint32_t run_of_tile(const uint32_t* first, uint32_t 
 // A tile of a product: its run, its first feature (or column) m0 and row (or feature) n0.
 struct LinearTile {
     Run r;
-    uint32_t m0, n0;
+    uint32_t m0, n0, split;
 };
+// Of `terms` terms split s has those from part_of(..) * s on, whole steps of KR.
+template <uint32_t KR>
+__device__ __forceinline__ uint32_t part_of(uint32_t terms, uint32_t splits) {
+    return ((terms + KR - 1) / KR + splits - 1) / splits * KR;
+}
 // The workgroup's tiles of products whose rows are the runs': every gridDim.x-th, run
-// by run, so that neighbouring tiles meet the same weights.
-template <uint32_t BM, uint32_t BN>
+// by run, so that neighbouring tiles meet the same weights; SPLIT: all of them for
+// each split of the summed index.
+template <uint32_t BM, uint32_t BN, bool SPLIT>
 struct RowTiles {
     const LinearArgs& a;
     const Runs& runs;
@@ -112,18 +118,19 @@ struct RowTiles {
         all = mts * __builtin_amdgcn_readfirstlane(t.first[a.runs * a.nranks]);
     }
     __device__ __forceinline__ bool operator()(LinearTile& t) {
-        if (id >= all) return false;
-        const uint32_t at = share_of(id, all), g = run_of_tile(runs.first, a.runs * a.nranks, __builtin_amdgcn_readfirstlane(at / mts));
+        if (id >= (SPLIT ? all * a.splits : all)) return false;
+        const uint32_t split = SPLIT ? __builtin_amdgcn_readfirstlane(id / all) : 0;
+        const uint32_t at = share_of(SPLIT ? id - split * all : id, all), g = run_of_tile(runs.first, a.runs * a.nranks, __builtin_amdgcn_readfirstlane(at / mts));
         const uint32_t from = __builtin_amdgcn_readfirstlane(runs.first[g]), to = __builtin_amdgcn_readfirstlane(runs.first[g + 1]);
         uint32_t mt, nt;
         band_tile(at - from * mts, mts, to - from, mt, nt);
         id += gridDim.x;
-        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN};
+        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN, split};
         return true;
     }
 };
 // The same for the runs' weights: run by run, so that a run's rows are read while they are near.
-template <uint32_t BM, uint32_t BN>
+template <uint32_t BM, uint32_t BN, bool SPLIT>
 struct WeightTiles {
     const LinearArgs& a;
     const Runs& runs;
@@ -134,13 +141,17 @@ struct WeightTiles {
         count_tiles(a, BN, t);
     }
     __device__ __forceinline__ bool operator()(LinearTile& t) {
-        const uint32_t each = mts * nts;
-        if (id >= uint64_t(each) * (a.runs * a.nranks)) return false;
-        const uint32_t g = __builtin_amdgcn_readfirstlane(uint32_t(id / each));
+        const uint32_t each = mts * nts, groups = a.runs * a.nranks;
+        if (id >= uint64_t(each) * groups * (SPLIT ? a.splits : 1)) return false;
+        uint32_t g = __builtin_amdgcn_readfirstlane(uint32_t(id / each)), split = 0;
+        if constexpr (SPLIT) {
+            split = g / groups;
+            g -= split * groups;
+        }
         uint32_t mt, nt;
         tile_of(__builtin_amdgcn_readfirstlane(uint32_t(id % each)), mts, nts, mt, nt);
         id += gridDim.x;
-        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN};
+        t = LinearTile{run_of(a, runs, g), mt * BM, nt * BN, split};
         return true;
     }
 };
@@ -389,7 +400,7 @@ __global__ __launch_bounds__(S::threads, 2) void k_linear(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t BM = GATED ? S::BM / 2 : S::BM;   // features of a tile
     __shared__ Runs runs;
-    RowTiles<BM, S::BN> tiles(a, runs, a.outs);
+    RowTiles<BM, S::BN, false> tiles(a, runs, a.outs);
     const uint32_t pitch = a.cols * uint32_t(sizeof(T)), steps = (pitch + kStepBytes - 1) / kStepBytes;
     auto weight_of = [&](const LinearTile& t) {
         return static_cast<const char*>(a.weight[t.r.rank]) + (uint64_t(t.r.run) * (GATED ? 2 : 1) * a.outs + t.m0) * pitch;
@@ -619,65 +630,104 @@ __device__ __forceinline__ void store_tile(const LinearArgs& a, typename Elem<DT
     }
 }
 
-// dx[t][k] = sum over the features of dz[t][m] W[m][k].
-template <int DT, typename S, int PATH>
+// dx[t][k] = sum over the features of dz[t][m] W[m][k].  SPLIT: the sum over one
+// part of the features, left for k_linear_join.
+template <int DT, typename S, int PATH, bool SPLIT>
 __global__ __launch_bounds__(S::threads, 2) void k_linear_dx(LinearArgs a) {
     typedef typename Elem<DT>::type T;
-    constexpr uint32_t es = sizeof(T);
+    constexpr uint32_t es = sizeof(T), KR = kStepBytes / es;
+    static_assert(!SPLIT || PATH != kLoose, "");
     __shared__ Runs runs;
-    RowTiles<S::BM, S::BN> tiles(a, runs, a.cols);
-    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es, steps = (wide * es + kStepBytes - 1) / kStepBytes;
+    RowTiles<S::BM, S::BN, SPLIT> tiles(a, runs, a.cols);
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es, part = SPLIT ? part_of<KR>(wide, a.splits) : wide;
     auto weight_of = [&](const LinearTile& t) {
         return static_cast<const char*>(a.weight[t.r.rank]) + uint64_t(t.r.run) * wide * pitch + t.m0 * es;
     };
     auto rows_of = [&](const LinearTile& t) { return t.r.count - t.n0 < uint32_t(S::BN) ? t.r.count - t.n0 : uint32_t(S::BN); };
     auto done = [&](const LinearTile& t, f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
-        store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dx[t.r.rank]) + uint64_t(t.r.lo) * a.cols, t.m0, t.n0, t.r.count - t.n0, acc, room);
+        if constexpr (SPLIT)
+            store_tile<kF32, S, true>(a, a.sums + ((uint64_t(t.split) * a.rows.start[a.nranks] + a.rows.start[t.r.rank]) + t.r.lo) * a.cols,
+                                      t.m0, t.n0, t.r.count - t.n0, acc, room);
+        else store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dx[t.r.rank]) + uint64_t(t.r.lo) * a.cols, t.m0, t.n0, t.r.count - t.n0, acc, room);
     };
     if constexpr (PATH == kLoose) {
         for (LinearTile t; tiles(t);) {
             f32x4 acc[S::MI][S::NI];
-            loose_tile<DT, S, kCols, kRows>(LooseCols{weight_of(t), wide, pitch, pitch - t.m0 * es}, LooseRows{dz_row<T>(a, t.r, t.n0), rows_of(t), a.zpitch, 0}, steps, acc);
+            loose_tile<DT, S, kCols, kRows>(LooseCols{weight_of(t), wide, pitch, pitch - t.m0 * es}, LooseRows{dz_row<T>(a, t.r, t.n0), rows_of(t), a.zpitch, 0},
+                                            (wide + KR - 1) / KR, acc);
             done(t, acc, nullptr);
         }
     } else {
-        typedef ColOperand<kStepBytes / int(es), 1> OA;
+        typedef ColOperand<KR, 1> OA;
         typedef RowOperand<PATH == kTail> OB;
         matrix_walk<DT, S, kCols, kRows, OA, OB, LinearTile>(tiles, [&](const LinearTile& t, OA& A, OB& B) {
-            A = OA{weight_of(t), wide, pitch, t.m0 * es, 0};
-            B = OB{dz_row<T>(a, t.r, t.n0), rows_of(t), a.zpitch, (a.zpitch + 15) / 16 * 16, wide * es};
-            return steps;
+            const uint32_t from = t.split * part, terms = from >= wide ? 0 : wide - from < part ? wide - from : part;
+            A = OA{weight_of(t) + uint64_t(from) * pitch, terms, pitch, t.m0 * es, 0};
+            B = OB{dz_row<T>(a, t.r, t.n0) + from * es, rows_of(t), a.zpitch, (a.zpitch + 15) / 16 * 16 - from * es, terms * es, from * es};
+            return (terms + KR - 1) / KR;
         }, rows_of, done);
     }
 }
 
-// dW[m][k] = sum over the run's rows of dz[t][m] x[t][k]; zeros for a run without rows.
-template <int DT, typename S, int PATH>
+// dW[m][k] = sum over the run's rows of dz[t][m] x[t][k]; zeros for a run without
+// rows.  SPLIT: the sum over one part of the rows, left for k_linear_join.
+template <int DT, typename S, int PATH, bool SPLIT>
 __global__ __launch_bounds__(S::threads, 2) void k_linear_dweight(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     constexpr uint32_t es = sizeof(T), KR = kStepBytes / es;
+    static_assert(!SPLIT || PATH != kLoose, "");
     __shared__ Runs runs;
     const uint32_t wide = (a.gated ? 2 : 1) * a.outs, pitch = a.cols * es;
-    WeightTiles<S::BM, S::BN> tiles(a, runs, a.cols, wide);
-    auto x_of = [&](const LinearTile& t) { return static_cast<const char*>(a.x[t.r.rank]) + uint64_t(t.r.lo) * pitch + t.m0 * es; };
-    auto dz_of = [&](const LinearTile& t) { return dz_row<T>(a, t.r, 0) + t.n0 * es; };
+    WeightTiles<S::BM, S::BN, SPLIT> tiles(a, runs, a.cols, wide);
+    auto x_of = [&](const LinearTile& t, uint32_t from) { return static_cast<const char*>(a.x[t.r.rank]) + uint64_t(t.r.lo + from) * pitch + t.m0 * es; };
+    auto dz_of = [&](const LinearTile& t, uint32_t from) { return dz_row<T>(a, t.r, from) + t.n0 * es; };
     auto done = [&](const LinearTile& t, f32x4 (&acc)[S::MI][S::NI], u32x4* room) {
-        store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dweight[t.r.rank]) + uint64_t(t.r.run) * wide * a.cols, t.m0, t.n0, wide - t.n0, acc, room);
+        if constexpr (SPLIT)
+            store_tile<kF32, S, true>(a, a.sums + ((uint64_t(t.split) * a.nranks + t.r.rank) * a.runs + t.r.run) * wide * a.cols, t.m0, t.n0, wide - t.n0,
+                                      acc, room);
+        else store_tile<DT, S, PATH != kLoose>(a, static_cast<T*>(a.dweight[t.r.rank]) + uint64_t(t.r.run) * wide * a.cols, t.m0, t.n0, wide - t.n0, acc, room);
     };
     if constexpr (PATH == kLoose) {
         for (LinearTile t; tiles(t);) {
             f32x4 acc[S::MI][S::NI];
-            loose_tile<DT, S, kCols, kCols>(LooseCols{x_of(t), t.r.count, pitch, pitch - t.m0 * es}, LooseCols{dz_of(t), t.r.count, a.zpitch, (wide - t.n0) * es},
-                                            (t.r.count + KR - 1) / KR, acc);
+            loose_tile<DT, S, kCols, kCols>(LooseCols{x_of(t, 0), t.r.count, pitch, pitch - t.m0 * es},
+                                            LooseCols{dz_of(t, 0), t.r.count, a.zpitch, (wide - t.n0) * es}, (t.r.count + KR - 1) / KR, acc);
             done(t, acc, nullptr);
         }
     } else {
         typedef ColOperand<KR, 1> OP;
         matrix_walk<DT, S, kCols, kCols, OP, OP, LinearTile>(tiles, [&](const LinearTile& t, OP& A, OP& B) {
-            A = OP{x_of(t), t.r.count, pitch, t.m0 * es, 0};
-            B = OP{dz_of(t), t.r.count, a.zpitch, t.n0 * es, 0};
-            return (t.r.count + KR - 1) / KR;
+            const uint32_t part = SPLIT ? part_of<KR>(t.r.count, a.splits) : t.r.count, from = SPLIT && t.split * part < t.r.count ? t.split * part : 0;
+            const uint32_t terms = !SPLIT || t.split == 0 || from > 0 ? (t.r.count - from < part ? t.r.count - from : part) : 0;
+            A = OP{x_of(t, from), terms, pitch, t.m0 * es, 0};
+            B = OP{dz_of(t, from), terms, a.zpitch, t.n0 * es, 0};
+            return (terms + KR - 1) / KR;
         }, [&](const LinearTile& t) { return wide - t.n0; }, done);
+    }
+}
+
+// dx's rows, or dweight, from the sums over the parts, in their order: a run's
+// values lie side by side in both.
+template <int DT, bool WEIGHT>
+__global__ __launch_bounds__(kThreads) void k_linear_join(LinearArgs a) {
+    typedef typename Elem<DT>::type T;
+    const Run r = same(run_at(a, blockIdx.y));
+    const uint32_t wide = (a.gated ? 2 : 1) * a.outs;
+    const uint64_t count = uint64_t(WEIGHT ? wide : r.count) * a.cols, apart = uint64_t(WEIGHT ? a.nranks * a.runs * wide : a.rows.start[a.nranks]) * a.cols;
+    const float* from = a.sums + (WEIGHT ? uint64_t(blockIdx.y) * wide : uint64_t(a.rows.start[r.rank]) + r.lo) * a.cols;
+    T* to = WEIGHT ? static_cast<T*>(a.dweight[r.rank]) + uint64_t(r.run) * wide * a.cols : static_cast<T*>(a.dx[r.rank]) + uint64_t(r.lo) * a.cols;
+    for (uint64_t i = uint64_t(blockIdx.x) * kThreads + threadIdx.x; i < count; i += uint64_t(gridDim.x) * kThreads) {
+        float s = 0.f;
+        uint32_t k = 0;
+        for (; k + 8 <= a.splits; k += 8) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) v[j] = from[(k + j) * apart + i];
+#pragma unroll
+            for (int j = 0; j < 8; j++) s += v[j];
+        }
+        for (; k < a.splits; k++) s += from[k * apart + i];
+        to[i] = Elem<DT>::put(s);
     }
 }
 
@@ -785,16 +835,38 @@ uint64_t dz_tiles(const RowTable& rows, int nranks, uint32_t runs, uint64_t wide
     const uint64_t n = rows.start[nranks], groups = uint64_t(runs) * nranks;
     return n / dz_rows(n, wide) + (groups < n ? groups : n);
 }
+// Where a product has too few tiles for the CUs, its sum is split among workgroups:
+// into as many parts as bring the tiles to kSplitTiles of 64 x 64, whose fp32 sums
+// fill kSplitBytes (tiny ones: as many bytes), of 16 steps or more each.  The sums'
+// way through memory and one launch more are worth it from four parts on (dx and
+// dweight in us, split and not: 17 rows of 33 fp32 from 2 x 7808 gated 42, 384; 8192
+// rows of 2048 fp32 from 128 107, 238; 128 rows of 4096 bf16 from 4096 37, 45; but in
+// two parts 1024 rows of 1024 bf16 from 1024 37, 24, and fp32 66, 58).
+constexpr uint64_t kSplitTiles = 512, kSplitBytes = kSplitTiles * 64 * 64 * 4, kFewestParts = 4;
+uint64_t part_terms(int dtype) { return 16 * kStepBytes / (dtype == kBF16 ? 2 : 4); }
+uint32_t splits_of(uint64_t tiles, bool tiny, uint64_t terms, int dtype) {
+    const uint64_t by_tiles = kSplitTiles * (tiny ? 4 : 1) / tiles, by_terms = terms / part_terms(dtype);
+    const uint64_t n = by_tiles < by_terms ? by_tiles : by_terms;
+    return n < kFewestParts ? 1 : uint32_t(n);
+}
 struct BackwardParts {
-    uint64_t dz, partial, bytes;
+    uint64_t dz, partial, sums, bytes;
 };
 BackwardParts backward_parts(const RowTable& rows, int nranks, uint32_t runs, uint64_t wide, bool need_dz, bool dbias, int dtype) {
-    const uint64_t es = dtype == kBF16 ? 2 : 4;
+    const uint64_t es = dtype == kBF16 ? 2 : 4, n = rows.start[nranks], groups = uint64_t(runs) * nranks;
     BackwardParts b;
     b.dz = 0;
-    b.partial = need_dz ? up(rows.start[nranks] * up(wide * es, 16), 256) : 0;
-    b.bytes = b.partial + (dbias ? up(dz_tiles(rows, nranks, runs, wide) * wide * 4, 256) : 0);
+    b.partial = need_dz ? up(n * up(wide * es, 16), 256) : 0;
+    b.sums = b.partial + (dbias ? up(dz_tiles(rows, nranks, runs, wide) * wide * 4, 256) : 0);
+    const bool may_split = wide >= kFewestParts * part_terms(dtype) || ceil_div(n, groups) >= kFewestParts * part_terms(dtype);
+    b.bytes = b.sums + (may_split ? kSplitBytes : 0);
     return b;
+}
+
+template <int DT, bool WEIGHT>
+void join(const LinearArgs& a, uint64_t each, hipStream_t s) {
+    const uint64_t need = ceil_div(each, kThreads);
+    hipLaunchKernelGGL((k_linear_join<DT, WEIGHT>), dim3(uint32_t(need < 1024 ? need : 1024), a.runs * a.nranks), dim3(kThreads), 0, s, a);
 }
 
 template <int DT>
@@ -807,6 +879,7 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
     a.zpitch = uint32_t(a.need_dz ? up(wide * es, 16) : wide * es);
     a.dz_rows = dz_rows(rows, wide);
     a.partial = dbias ? reinterpret_cast<float*>(workspace + b.partial) : nullptr;
+    a.sums = reinterpret_cast<float*>(workspace + b.sums);
     a.col_vecs = a.cols * es % 16 == 0 && on(a.dx, a.nranks, 16) && on(a.dweight, a.nranks, 16);
     if (rows > 0 && (a.need_dz || dbias)) {
         const uint64_t tiles = dz_tiles(a.rows, a.nranks, a.runs, wide), across = ceil_div(a.outs, 4 * kThreads), most = ceil_div(4096, across);
@@ -821,21 +894,43 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
         const int zp = path_of(a.zpitch, dz4), wp = path_of(a.cols * es, w4);
         with_path<DT>(zp == kLoose || wp == kLoose ? kLoose : zp, [&](auto path) {
             constexpr int P = decltype(path)::value;
-            const Tile t = pick_tile(DT, a.cols, ceil_div(rows, groups), groups, P, true);
+            const uint64_t mean = ceil_div(rows, groups);
+            if constexpr (P != kLoose) {
+                const bool tiny = mean <= kTileN[kTiny];
+                const uint64_t filled = ceil_div(a.cols, kTileM[kTiny]) * ceil_div(mean, kTileN[tiny ? kTiny : kSmall]) * groups;
+                a.splits = splits_of(filled, tiny, wide, DT);
+                if (a.splits > 1) {
+                    const uint64_t tiles = ceil_div(a.cols, kTileM[kTiny]) * (rows / kTileN[tiny ? kTiny : kSmall] + (groups < rows ? groups : rows)) * a.splits;
+                    if (tiny) hipLaunchKernelGGL((k_linear_dx<DT, Tiny, P, true>), dim3(walkers(tiles, kTiny)), dim3(Tiny::threads), 0, s, a);
+                    else hipLaunchKernelGGL((k_linear_dx<DT, Small, P, true>), dim3(walkers(tiles, kSmall)), dim3(Small::threads), 0, s, a);
+                    join<DT, false>(a, mean * a.cols, s);
+                    return;
+                }
+            }
+            const Tile t = pick_tile(DT, a.cols, mean, groups, P, true);
             const uint64_t tiles = ceil_div(a.cols, kTileM[t]) * (rows / kTileN[t] + (groups < rows ? groups : rows));
             with_tile<DT, P, true>(t, [&](auto shape) {
                 typedef decltype(shape) S;
-                hipLaunchKernelGGL((k_linear_dx<DT, S, P>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
+                hipLaunchKernelGGL((k_linear_dx<DT, S, P, false>), dim3(walkers(tiles, t)), dim3(S::threads), 0, s, a);
             });
         });
     }
     const bool loose = path_of(a.zpitch, dz4) == kLoose || path_of(a.cols * es, x4) == kLoose;
     auto dweight = [&](auto path) {
         constexpr int P = decltype(path)::value;
+        if constexpr (P != kLoose) {
+            const uint64_t filled = ceil_div(a.cols, kTileM[kSmall]) * ceil_div(wide, kTileN[kSmall]) * groups;
+            a.splits = splits_of(filled, false, ceil_div(rows, groups), DT);
+            if (a.splits > 1) {
+                hipLaunchKernelGGL((k_linear_dweight<DT, Small, P, true>), dim3(walkers(filled * a.splits, kSmall)), dim3(Small::threads), 0, s, a);
+                join<DT, true>(a, wide * a.cols, s);
+                return;
+            }
+        }
         const Tile t = pick_tile(DT, a.cols, wide, groups, P, false);
         with_tile<DT, P, false>(t, [&](auto shape) {
             typedef decltype(shape) S;
-            hipLaunchKernelGGL((k_linear_dweight<DT, S, P>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)), dim3(S::threads), 0, s, a);
+            hipLaunchKernelGGL((k_linear_dweight<DT, S, P, false>), dim3(walkers(ceil_div(a.cols, S::BM) * ceil_div(wide, S::BN) * groups, t)), dim3(S::threads), 0, s, a);
         });
     };
     if constexpr (DT == kBF16) {

@@ -417,7 +417,8 @@ dt_status dt_linear(const void* const* x, const void* const* weight, const void*
  * (NULL: not formed), zeros for a run without rows.  residual's is dy itself.  pre:
  * the forward pass's z, read unless act is DT_ACT_NONE and the product is not
  * gated (may be NULL then).  For bf16 tensors z's gradient is rounded to bf16 before
- * it enters the two products. */
+ * it enters the two products.  The workspace holds z's gradient and, where few tiles
+ * meet a long sum, up to 8 MiB of the sum's parts. */
 size_t dt_linear_backward_workspace(int nranks, const size_t* rows, int runs, size_t outs, dt_act act, int gated, int with_dbias,
                                     dt_dtype dtype);
 dt_status dt_linear_backward(const void* const* dy, const void* const* x, const void* const* weight, const void* const* pre,

@@ -73,6 +73,53 @@ def test_buffers_larger_than_their_runs(dt, dtype):
         check_backward(dt, c, "silu", True)
 
 
+# -------------------------------------------- few tiles and a long summed index --
+LONG = {
+    # runs' rows of each rank (None: one run without offsets), cols, outs
+    "a router": (None, [2000, 1500], 200, 48),
+    "a router of whole lines": (None, [4100], 512, 64),
+    "few columns": ([[40, 0, 33]], None, 24, 1500),
+    "few rows": ([[1, 3], [0, 2]], None, 136, 2200),
+    "odd rows": ([[777]], None, 99, 1033),
+    "rows that end inside 16 bytes": ([[300, 411]], None, 66, 1034),
+    "few rows that end inside 16 bytes": ([[30, 41]], None, 66, 2070),
+    "one long run": ([[2500, 0, 3, 5]], None, 64, 40),
+    "a row of many features": (None, [1], 40, 9001),
+}
+
+
+@DTYPES
+@pytest.mark.parametrize("which", LONG, ids=lambda k: k.replace(" ", "_"))
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+def test_gradients_with_long_sums(dt, which, gated, dtype):
+    """Sums that are formed in parts: over the features for dx, over the rows for dweight."""
+    note(f"long sums: {which} gated={gated} {dtype}")
+    counts, rows, cols, outs = LONG[which]
+    c = Case(rows or [sum(n) + 3 for n in counts], counts and [ends_of(n) for n in counts], cols, outs, gated, dtype, seed=40)
+    check_backward(dt, c, "silu", True)
+    check_backward(dt, c, "none", False)
+
+
+@DTYPES
+def test_long_sums_meet_only_their_rows(dt, dtype):
+    """Rows outside the runs and the weights of a run without rows hold NaN, and an infinity stays in its row of dx."""
+    note(f"long sums and NaN {dtype}")
+    for cols, outs in ((64, 1200), (66, 1202), (40, 2100)):
+        c = Case([3000], [[20, 1500, 1500, 2900]], cols, outs, False, dtype, seed=41)
+        dy, nan = c.new(3000, outs), float("nan")
+        for t in (c.x[0], dy):
+            t[:20], t[2900:] = nan, nan
+        c.weight[0][1] = nan
+        dy[100, outs - 1] = float("inf")
+        dx, dw = torch.zeros_like(c.x[0]), torch.zeros_like(c.weight[0])
+        dt.dt_linear_backward([dy], c.x, c.weight, [dx], [dw], offsets=c.offsets)
+        torch.cuda.synchronize()
+        finite = dx[20:2900].isfinite().all(1)
+        assert not bool(finite[80]) and int((~finite).sum()) == 1 and bool((dw[1] == 0).all())
+        assert bool(dw[0, :-1].isfinite().all()) and not bool(dw[0, -1].isfinite().any()) and bool(dw[2].isfinite().all())
+        assert bool((dx[:20] == 0).all()) and bool((dx[2900:] == 0).all())
+
+
 # ------------------------------------------------------- elements past 32 bits --
 def test_products_of_rows_past_32_bits(dt):
     """Runs at the end of 2^25 rows of 72 and 136 elements: their elements' numbers and bytes pass 2^32."""

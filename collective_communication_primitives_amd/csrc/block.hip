@@ -782,13 +782,21 @@ void with_hold(Hold h, F&& run) {
     else if constexpr (DT == kF32) run(std::integral_constant<int, 4>(), std::integral_constant<int, 1024>());
 }
 uint32_t units_of(uint32_t cols, int dtype) { return (cols + (dtype == kBF16 ? 8 : 4) - 1) / (dtype == kBF16 ? 8 : 4); }
-// Workgroups of the backward pass, each of which leaves a strip.
+bool rows16(uint32_t cols, int dtype) { return cols * uint64_t(dtype == kBF16 ? 2 : 4) % 16 == 0; }
+// Workgroups of the backward pass, each of which leaves a strip: two to a CU, with
+// four rows or more each.  Rows that are not whole 16 bytes wait longer for their
+// loads and get as many workgroups as the registers let run, where a lane holds one
+// unit (fp32: 8 x 4001 rows of 1001 274 us with 512 workgroups, 213 with 768, 185 with
+// 1024; bf16: 8 x 8192 of 1999 861, 666, 899, as 768 run at a time; whole 16 bytes,
+// fp32: 8 x 8192 of 1024 293, 305, 320).
 uint32_t strips_of(uint32_t rows, uint32_t cols, int dtype) {
     const Hold h = hold(units_of(cols, dtype), dtype);
     if (!sums_along(h)) return rows < 256 ? rows : 256;
     const uint32_t per = h.l <= 64 ? 256 / h.l : 1, need = (rows + per - 1) / per;
-    uint32_t most = h.l == 1024 ? 256 : 512;
-    if (need > 256 && need < 4 * most) most = (need + 3) / 4;  // at least four rows, but for very few
+    const bool more = h.l <= 256 && h.nv == 1 && !rows16(cols, dtype);
+    uint32_t most = h.l == 1024 ? 256 : !more ? 512 : dtype == kBF16 ? 768 : 1024;
+    const uint32_t least = more ? 3 : 4;  // rows, but for very few in all
+    if (need > 256 && need < least * most) most = (need + least - 1) / least;
     return need < most ? need : most;
 }
 bool on16(const void* const* list, int n) {
@@ -796,7 +804,6 @@ bool on16(const void* const* list, int n) {
         if (reinterpret_cast<uintptr_t>(list[r]) % 16 != 0) return false;
     return true;
 }
-bool rows16(uint32_t cols, int dtype) { return cols * uint64_t(dtype == kBF16 ? 2 : 4) % 16 == 0; }
 
 template <int DT, bool VEC>
 hipError_t forward(const BlockArgs& a, hipStream_t s) {

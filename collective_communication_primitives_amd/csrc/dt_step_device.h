@@ -70,12 +70,22 @@ __device__ __forceinline__ void store_loose(char* row, uint32_t u, uint32_t byte
         const typename Loose<ES>::type v = x;
         __builtin_nontemporal_store(v, reinterpret_cast<typename Loose<ES>::type*>(row + at));
     } else if (at < bytes) {
-        typedef typename std::conditional<ES == 2, uint16_t, uint32_t>::type T;
-        T t[16 / ES];
-        __builtin_memcpy(t, &x, 16);
-#pragma unroll
-        for (int e = 0; e < 16 / ES; e++)
-            if (at + e * ES < bytes) *reinterpret_cast<T*>(row + at + e * ES) = t[e];
+        // eight, four and two bytes of what is left of the row
+        typedef uint32_t Two __attribute__((ext_vector_type(2), aligned(2)));
+        typedef uint32_t One __attribute__((aligned(2)));
+        char* to = row + at;
+        if ((bytes - at) & 8) {
+            *reinterpret_cast<Two*>(to) = Two{x[0], x[1]};
+            x[0] = x[2];
+            x[1] = x[3];
+            to += 8;
+        }
+        if ((bytes - at) & 4) {
+            *reinterpret_cast<One*>(to) = x[0];
+            x[0] = x[1];
+            to += 4;
+        }
+        if (ES == 2 && ((bytes - at) & 2)) *reinterpret_cast<uint16_t*>(to) = uint16_t(x[0]);
     }
 }
 

@@ -173,6 +173,28 @@ def test_norms_of_rows_past_32_bits(dt):
         assert torch.equal(t[:-n].view(torch.int16), t[:1].expand(rows - n, -1).contiguous().view(torch.int16)), name
 
 
+@DTYPES
+@pytest.mark.parametrize("cols", [1, 3, 9, 61, 301, 1001, 1999, 4001])
+def test_rows_that_follow_do_not_matter(dt, cols, dtype):
+    """Rows that end inside 16 bytes: every other row is NaN, and nothing of it reaches the rows between."""
+    note(f"block between rows of NaN, cols={cols} {dtype}")
+    b = Block([41, 2, 1], cols, dtype, gate="row", seed=cols)
+    other = Block([41, 2, 1], cols, dtype, gate="row", seed=cols)
+    for kind in ("z", "x", "gate", "dy", "dh", "h"):
+        for t in getattr(other, kind):
+            t[1::2] = float("nan")
+    stats = [torch.rand(n, 4, device="cuda") + 0.5 for n in b.rows]
+    got = []
+    for c in (b, other):
+        h, y, dz, dx, dg = ([torch.zeros_like(t) for t in c.z] for _ in range(5))
+        dt.dt_block_norm(c.z, c.x, h, y, gate=c.gate, post_weight=b.w1, post_bias=b.b1, pre_weight=b.w2, pre_bias=b.b2)
+        dt.dt_block_norm_backward(c.dy, c.dh, c.z, c.h, stats, dz, dx, gate=c.gate, post_weight=b.w1, post_bias=b.b1, pre_weight=b.w2, dgate=dg)
+        torch.cuda.synchronize()
+        got.append(h + y + dz + dx + dg)
+    for one, two in zip(*got):
+        assert torch.equal(one[::2], two[::2]) and bool(one.isfinite().all()) and bool(two[1::2].isnan().all())
+
+
 # -------------------------------------------------------------------- together --
 def test_a_training_step(dt):
     """Block norm, router, routing, dispatch, the experts' two products, combine, block norm; and the way back: every gradient

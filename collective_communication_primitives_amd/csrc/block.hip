@@ -11,6 +11,10 @@
 //   dw2 = sum dy n2, db2 = sum dy, dw1 = sum du n1, db1 = sum du over all ranks' rows,
 //   dgate = scale dx p, summed over all ranks' rows for a gate that they share
 //
+// Bound by memory: 8 x 4096 rows of 8192 bf16 forward 367 us (5.8 TB/s), 8 x 4096 of
+// 4096 backward 331 us (5.0 TB/s, 10 us of it the strips' fold), 2831 ragged rows of
+// 1001 fp32 backward 29 + 6 us, few rows by the launch (one row per rank 5 us).
+//
 // A row lives in the registers of its waves through both norms, so each tensor is
 // read and written once; the variance is that of the centred values, and y is
 // taken from h before it is rounded.  All sums are fp32; results are rounded once.

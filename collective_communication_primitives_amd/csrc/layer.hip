@@ -11,6 +11,11 @@
 // summed index.  An expert's tokens stand side by side as the columns of the matrix
 // instructions, so that each weight meets no more of them than it has.
 //
+// 128 bf16 tokens of 4096 to 4 of 64 experts of 2 x 2048: 389 us for the first
+// product's 2.1 GB (5.5 TB/s), 238 for the second's 1.1 GB (4.5 TB/s: fewer columns,
+// each workgroup with all experts).  One token of 2048 to 2 of 64 of 2 x 1024: 11.5 +
+// 7.5 us, most of it the way from the choice to the weights' first bytes.
+//
 // All sums are fp32, in a fixed order.  Between the products h is kept in fp32, for
 // bf16 in two parts, its rounding and the rest's: the second matrix instruction is
 // free beside the weight's bytes.  A slot's weight is multiplied into h, so that the

@@ -14,6 +14,14 @@
 //
 // All sums are fp32.  z, y, dx, dW and db are rounded once; dz is rounded to the
 // tensors' type before it enters its two products, as the matrix units take it.
+//
+// Many rows are bound by the matrix units: 52432 bf16 rows of 4096 in 64 runs to 2 x
+// 2048 gated, pre kept, 1.87 ms (0.94 PFLOP/s; 8192 rows of 4096 to 11008 with gelu
+// 0.74 ms, 1.0), dz 0.25 ms (memory), dx 1.65 (1.07), dweight 1.80 (0.98).  Tiles that
+// runs end in are 15% of the work, weights that no neighbour has fetched yet cost 9%,
+// pre's stores 7%.  Few rows are bound by the weights' bytes: 16 rows of 4096 in four
+// runs to 4096 24 us, 5.6 TB/s.  fp32: 5444 ragged rows of 1001 from 509 backward 17 us
+// for dz, 5 for the bias, 67 for dx and 69 for dweight, 80 TFLOP/s in tiles of 64 x 64.
 #include "dt_act.h"
 #include "dt_stream.h"
 
@@ -829,7 +837,7 @@ hipError_t forward(LinearArgs a, hipStream_t s) {
 
 uint64_t up(uint64_t n, uint64_t to) { return (n + to - 1) / to * to; }
 // Rows of a workgroup that forms dz: 32, or 8 where those would be too few
-// workgroups (3762 rows of 509 fp32 with gelu: 41 us with 32).
+// workgroups (6048 rows of 509 fp32 with gelu: 41 us with 32).
 uint32_t dz_rows(uint64_t rows, uint64_t wide) { return rows / 32 * ceil_div(wide, 4 * kThreads) >= 1024 ? 32 : 8; }
 uint64_t dz_tiles(const RowTable& rows, int nranks, uint32_t runs, uint64_t wide) {
     const uint64_t n = rows.start[nranks], groups = uint64_t(runs) * nranks;

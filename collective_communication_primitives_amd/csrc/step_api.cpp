@@ -1,6 +1,7 @@
 // step_api.cpp -- the C ABI of the model-step operators of include/dt.h:
 // argument checks, row tables and workspace sizes.  The arithmetic is in
-// norm.hip, moe.hip, loss.hip, linear.hip, layer.hip and block.hip; nothing here allocates or throws.
+// norm.hip, moe.hip, loss.hip, linear.hip, layer.hip and block.hip; nothing here
+// allocates or throws.
 #include <stdarg.h>
 #include <stdio.h>
 

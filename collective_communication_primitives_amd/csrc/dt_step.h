@@ -161,6 +161,7 @@ struct LinearArgs {
     float* sums;                            // [splits][all ranks' rows][cols], or [splits][all ranks' runs][outs (gated: twice)][cols]
     RowTable rows;
     uint32_t runs, cols, outs, zpitch, dz_rows;
+    uint32_t dz_tiles;                      // of dz_rows rows, that partial has room for
     uint32_t splits;                        // parts of the summed index, of dx or of dweight
     int act, gated, need_dz, nranks;
     int vecs, col_vecs;                     // rows of outs, of cols, are whole 16 bytes, aligned to them, where they are written

@@ -517,7 +517,9 @@ __global__ __launch_bounds__(kThreads) void k_linear_dz(LinearArgs a) {
     typedef typename Elem<DT>::type T;
     __shared__ Runs runs;
     count_tiles(a, a.dz_rows, runs);
-    const uint32_t groups = a.runs * a.nranks, tiles = runs.first[groups], m = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    const uint32_t groups = a.runs * a.nranks, m = (blockIdx.x * kThreads + threadIdx.x) * 4;
+    // offsets that decrease, which are not allowed, could make the runs longer than all rows
+    const uint32_t tiles = runs.first[groups] < a.dz_tiles ? runs.first[groups] : a.dz_tiles;
     const uint32_t wide = GATED ? 2 * a.outs : a.outs;
     const uint64_t ldz = a.zpitch / sizeof(T);
     if (m >= a.outs) return;
@@ -583,7 +585,7 @@ __global__ __launch_bounds__(1024) void k_linear_dbias(LinearArgs a) {
     __shared__ float sums[16][64];
     count_tiles(a, a.dz_rows, runs);
     const uint32_t wide = (a.gated ? 2 : 1) * a.outs, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane, g = blockIdx.y;
-    const uint32_t end = runs.first[g + 1];
+    const uint32_t end = runs.first[g + 1] < a.dz_tiles ? runs.first[g + 1] : a.dz_tiles;
     float s = 0.f;
     if (c < wide)
         for (uint32_t t = runs.first[g] + wave; t < end; t += 16 * 4) {
@@ -886,6 +888,7 @@ hipError_t backward(LinearArgs a, char* workspace, hipStream_t s) {
     a.dz = workspace + b.dz;
     a.zpitch = uint32_t(a.need_dz ? up(wide * es, 16) : wide * es);
     a.dz_rows = dz_rows(rows, wide);
+    a.dz_tiles = uint32_t(dz_tiles(a.rows, a.nranks, a.runs, wide));
     a.partial = dbias ? reinterpret_cast<float*>(workspace + b.partial) : nullptr;
     a.sums = reinterpret_cast<float*>(workspace + b.sums);
     a.col_vecs = a.cols * es % 16 == 0 && on(a.dx, a.nranks, 16) && on(a.dweight, a.nranks, 16);

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import block_reference as ref
-from gpu_util import note
+from gpu_util import Guarded, note
 from test_gpu_block import Block
 from test_gpu_layer import Layer
 from test_gpu_linear import DTYPES, Case, check_backward, check_forward, normal
@@ -71,6 +71,24 @@ def test_buffers_larger_than_their_runs(dt, dtype):
         c = Case([40000], [ends], 72, 40, True, dtype, seed=23)
         check_forward(dt, c, "silu", True, True, True)
         check_backward(dt, c, "silu", True)
+
+
+@DTYPES
+def test_decreasing_offsets_stay_inside_the_buffers(dt, dtype):
+    """They are not allowed, and their rows' values are anyone's: but nothing outside the buffers and the workspace is written."""
+    note(f"decreasing offsets {dtype}")
+    rows, runs, cols, outs = 200, 8, 64, 48
+    g = torch.Generator(device="cuda").manual_seed(39)
+    x, dy, w = (normal(g, dtype, *s) for s in ((rows, cols), (rows, outs), (runs, outs, cols)))
+    off = [torch.tensor([0, 200, 0, 200, -5, 900, 0, 150, 20], dtype=torch.int32, device="cuda")]
+    y, pre, dx, dw, db = (Guarded(n, dtype).poison() for n in (rows * outs, rows * outs, rows * cols, runs * outs * cols, runs * outs))
+    need = dt.dt_linear_backward_workspace([rows], runs, outs, "gelu", False, True, dtype)
+    space = Guarded((need + 3) // 4, torch.float32).poison()
+    dt.dt_linear([x], [w], [y.t], pre=[pre.t], offsets=off, act="gelu")
+    dt.dt_linear_backward([dy], [x], [w], [dx.t], [dw.t], pre=[pre.t], dbias=[db.t], offsets=off, act="gelu", workspace=space.t)
+    torch.cuda.synchronize()
+    for t in (y, pre, dx, dw, db, space):
+        t.check()
 
 
 # -------------------------------------------- few tiles and a long summed index --

@@ -864,6 +864,12 @@ bool on16(const void* const* list, int n) {
         if (reinterpret_cast<uintptr_t>(list[r]) % 16 != 0) return false;
     return true;
 }
+// Whether a list that is read is there: a rank without rows may list NULL.
+bool given(const void* const* list, int n) {
+    for (int r = 0; r < n; r++)
+        if (list[r] != nullptr) return true;
+    return false;
+}
 
 template <int DT, bool VEC>
 hipError_t forward(const BlockArgs& a, hipStream_t s) {
@@ -892,7 +898,7 @@ hipError_t backward(const BlockBackArgs& a, hipStream_t s) {
             with_hold<DT>(h, [&](auto nv, auto lanes) {
                 constexpr int NV = decltype(nv)::value, L = decltype(lanes)::value;
                 const uint32_t groups = sums_along(h) ? a.strips : rows < 2048 ? rows : 2048;
-                if (a.post_bias[0] != nullptr || (a.sums & (1u << kPostBias | 1u << kPreBias)) != 0)
+                if (given(a.post_bias, a.nranks) || (a.sums & (1u << kPostBias | 1u << kPreBias)) != 0)
                     hipLaunchKernelGGL((k_block_backward<DT, VEC, NV, L, (L < 1024), true>), dim3(groups), dim3(Share<L>::threads), 0, s, a);
                 else
                     hipLaunchKernelGGL((k_block_backward<DT, VEC, NV, L, (L < 1024), false>), dim3(groups), dim3(Share<L>::threads), 0, s, a);

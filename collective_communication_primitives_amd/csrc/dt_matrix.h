@@ -315,7 +315,7 @@ __device__ __forceinline__ uint32_t fresh_lane() {
 // the registers.
 //   next(t)               the workgroup's next tile; false: there is none
 //   operands(t, A, B)     sets its operands and returns its steps of the summed
-//                         index; a row's end and pitch are the same in all tiles
+//                         index; a row's pitch is the same in all tiles
 //   rows(t)               its rows of B that are there: waves with none of them leave
 //                         the matrix units to the others
 //   done(t, acc, room)    what becomes of its sums, acc as matrix_tile leaves it; room:
@@ -328,8 +328,8 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Tile now, ahead;     // multiplied, loaded
     if (!next(ahead)) return;
-    OA A;
-    OB B;
+    OA A, now_a;         // loaded; a row's end in the tile that is multiplied
+    OB B, now_b;
     auto rounds = [](uint32_t n) { return n == 0 ? 4 : (n + 3) / 4 * 4; };
     uint32_t steps = operands(ahead, A, B), end = rounds(steps), step = 0;   // of the loads
     bool more = true;
@@ -372,18 +372,23 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
         asm volatile("" : "+v"(ra), "+v"(rb));
         wait<63, 0>();   // the last turn's reads, in waves without rows as well: their stage is loaded again in the next turn
         if (!active && following_step != 0) return;
+        // the loads may be in the next tile already, whose rows may end elsewhere
+        const OA& end_a = following_step == 0 ? A : now_a;
+        const OB& end_b = following_step == 0 ? B : now_b;
 #pragma unroll
-        for (int j = 0; j < S::NI; j++) fnext[j] = B.cut(fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j), following_step);
+        for (int j = 0; j < S::NI; j++) fnext[j] = end_b.cut(fragment<DT, MB, S::BN>(following + S::BM * kChunks, rb, j), following_step);
 #pragma unroll
         for (int i = 0; i < S::MI; i++) {
 #pragma unroll
             for (int j = 0; j < S::NI; j++) acc[i][j] = multiply<DT>(fa[i], fn[j], acc[i][j]);
-            fa[i] = A.cut(fragment<DT, MA, S::BM>(following, ra, i), following_step);
+            fa[i] = end_a.cut(fragment<DT, MA, S::BM>(following, ra, i), following_step);
         }
     };
     bool settled = false;
     while (true) {
         now = ahead;
+        now_a = A;
+        now_b = B;
         const uint32_t last = end;
 #pragma unroll
         for (int i = 0; i < S::MI; i++)

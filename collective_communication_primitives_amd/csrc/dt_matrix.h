@@ -17,6 +17,9 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kChunks = 4;             // 16-byte chunks of the summed index per step
 constexpr int kStepBytes = kChunks * 16;
+// fp32: a sum runs over so many steps of 16 terms at most, and these sums are added
+// up apart, so that its error does not grow with every term of a long one.
+constexpr uint32_t kRunSteps = 32;
 enum { kRows = 0, kCols = 1 };
 
 // A workgroup's tile of `out`: BM rows of A by BN rows of B, cut among GM x GN
@@ -355,10 +358,7 @@ __device__ __forceinline__ void matrix_walk(Next&& next, Operands&& operands, Ro
 #pragma unroll
     for (int j = 0; j < S::NI; j++) fb[0][j] = B.cut(fragment<DT, MB, S::BN>(s0 + S::BM * kChunks, rb, j), 0);
     f32x4 acc[S::MI][S::NI];
-    // fp32: a sum runs over kRunSteps steps of 16 terms at most, and these sums are
-    // added up apart, so that its error does not grow with every term of a long one.
     constexpr bool RUNS = DT == kF32;
-    constexpr uint32_t kRunSteps = 32;
     f32x4 total[RUNS ? S::MI : 1][RUNS ? S::NI : 1];
     // One step, as in matrix_tile.  settled: the bytes of the following step have
     // been waited for already, behind the tile before, and its stores need not be.

@@ -51,6 +51,10 @@ __device__ __forceinline__ u32x4 to_rows(u32x4 v) {
 // they are multiplied.  Single steps bring each line to the CU twice (the same
 // products 415 and 278 us with four steps on their way, 389 and 239 with two pairs;
 // three pairs 414 and 262: fewer waves fit).
+//
+// fp32: a sum runs over kRunSteps steps of 16 terms at most, as in matrix_walk, and
+// these sums are added up apart (8 runs of 48 rows of 4096 to 2048 97 us either way,
+// gated 173 instead of 165; one run of 40 rows of 8192 to 4096 82 instead of 90).
 template <int DT, bool VEC, int W, int G, int PARTS, int P>
 __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const char* const (&x)[PARTS][G], uint32_t lo, uint32_t hi, uint32_t bytes,
                                             uint32_t xbytes, f32x4 (&acc)[W][G]) {
@@ -87,18 +91,40 @@ __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const cha
         multiply_step(a[i][0], b[i][0]);
         multiply_step(a[i][1], b[i][1]);
     };
+    constexpr bool RUNS = DT == kF32;
+    f32x4 total[RUNS ? W : 1][RUNS ? G : 1];
+    if constexpr (RUNS) {
+#pragma unroll
+        for (int k = 0; k < W; k++)
+#pragma unroll
+            for (int g = 0; g < G; g++) total[k][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    auto run_ends = [&] {
+        if constexpr (RUNS) {
+#pragma unroll
+            for (int k = 0; k < W; k++)
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    total[k][g] += acc[k][g];
+                    acc[k][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+                }
+        }
+    };
     constexpr uint32_t U = 2 * P;
+    static_assert(kRunSteps % U == 0, "a run is whole turns of the loop");
     uint32_t s = lo;
     if (s + U <= end) {
 #pragma unroll
         for (int i = 0; i < P; i++) load(i, s + 2 * i);
         for (; s + 2 * U <= end; s += U) {
+            if ((s - lo) % kRunSteps == 0) run_ends();
 #pragma unroll
             for (int i = 0; i < P; i++) {
                 multiply_pair(i);
                 load(i, s + U + 2 * i);
             }
         }
+        run_ends();   // fewer than 2 U steps are left, and at most one that the row ends in
 #pragma unroll
         for (int i = 0; i < P; i++) {
             multiply_pair(i);
@@ -122,6 +148,12 @@ __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const cha
 #pragma unroll
         for (int k = 0; k < W; k++) fa[k] = end_at<DT, VEC>(w[k], at, bytes);
         multiply_step(fa, fb);
+    }
+    if constexpr (RUNS) {
+#pragma unroll
+        for (int k = 0; k < W; k++)
+#pragma unroll
+            for (int g = 0; g < G; g++) acc[k][g] += total[k][g];
     }
 }
 // Steps of share `i` of `n`, whole pairs of them (a pair is a line of the weights).

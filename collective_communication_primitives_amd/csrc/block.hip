@@ -826,8 +826,9 @@ Hold hold(uint32_t units, int dtype) {
     if (units <= 4096 && dtype == kF32) return {4, 1024};
     return {0, 0};
 }
-// The backward pass keeps the sums over the rows in registers where one unit per
-// lane is enough; beside more they do not fit.
+// The backward pass keeps the sums over the rows in registers where a row is shared
+// by fewer than 1024 lanes, up to two units in each; 1024 lanes have 128 registers
+// each, where the sums do not fit.
 bool sums_along(Hold h) { return h.l < 1024 && h.l != 0; }
 template <int DT, typename F>
 void with_hold(Hold h, F&& run) {
@@ -855,7 +856,7 @@ uint32_t strips_of(uint32_t rows, uint32_t cols, int dtype) {
     if (!sums_along(h)) return rows < 256 ? rows : 256;
     const uint32_t per = h.l <= 64 ? 256 / h.l : 1, need = (rows + per - 1) / per;
     const bool more = h.l <= 256 && h.nv == 1 && !rows16(cols, dtype);
-    uint32_t most = h.l == 1024 ? 256 : !more ? 512 : dtype == kBF16 ? 768 : 1024;
+    uint32_t most = !more ? 512 : dtype == kBF16 ? 768 : 1024;
     if (need > 256 && need < 4 * most) most = (need + 3) / 4;  // at least four rows, but for very few
     return need < most ? need : most;
 }

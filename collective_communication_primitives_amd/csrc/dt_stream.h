@@ -9,16 +9,11 @@
 namespace dt {
 namespace {
 
-// A lane's 16 bytes of a weight row, which no other workgroup reads.  Not past the
-// cache for all that: an instruction takes half of each 128-byte line, the next one
-// the rest (past it: 544 us instead of 474).
+// A lane's 16 bytes of a row.  Those of a weight row are read by no other workgroup,
+// but not past the cache for all that: an instruction takes half of each 128-byte
+// line, the next one the rest (past it: 544 us instead of 474).
 template <int DT, bool VEC>
-__device__ __forceinline__ u32x4 weight_at(const char* row, uint32_t at) {
-    if constexpr (VEC) return *reinterpret_cast<const u32x4*>(row + at);
-    else return *reinterpret_cast<const typename Loose<DT == kBF16 ? 2 : 4>::type*>(row + at);
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ u32x4 near_at(const char* row, uint32_t at) {
+__device__ __forceinline__ u32x4 lane_at(const char* row, uint32_t at) {
     if constexpr (VEC) return *reinterpret_cast<const u32x4*>(row + at);
     else return *reinterpret_cast<const typename Loose<DT == kBF16 ? 2 : 4>::type*>(row + at);
 }
@@ -64,13 +59,13 @@ __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const cha
 #pragma unroll
         for (int h = 0; h < 2; h++)
 #pragma unroll
-            for (int k = 0; k < W; k++) a[i][h][k] = weight_at<DT, VEC>(w[k], (s + h) * kStepBytes + from);
+            for (int k = 0; k < W; k++) a[i][h][k] = lane_at<DT, VEC>(w[k], (s + h) * kStepBytes + from);
 #pragma unroll
         for (int p = 0; p < PARTS; p++)
 #pragma unroll
             for (int g = 0; g < G; g++)
 #pragma unroll
-                for (int h = 0; h < 2; h++) b[i][h][p][g] = near_at<DT, VEC || PARTS == 2>(x[p][g], (s + h) * kStepBytes + from);
+                for (int h = 0; h < 2; h++) b[i][h][p][g] = lane_at<DT, VEC || PARTS == 2>(x[p][g], (s + h) * kStepBytes + from);
     };
     auto multiply_step = [&](const u32x4 (&fa)[W], const u32x4 (&fb)[PARTS][G]) {
         u32x4 t[PARTS][G];

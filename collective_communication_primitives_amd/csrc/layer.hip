@@ -14,7 +14,9 @@
 // 128 bf16 tokens of 4096 to 4 of 64 experts of 2 x 2048: 389 us for the first
 // product's 2.1 GB (5.5 TB/s), 238 for the second's 1.1 GB (4.5 TB/s: fewer columns,
 // each workgroup with all experts).  One token of 2048 to 2 of 64 of 2 x 1024: 11.5 +
-// 7.5 us, most of it the way from the choice to the weights' first bytes.
+// 7.5 us, latency, where the bytes take 4 in all: two launches of 128 workgroups, on
+// half of the CUs, and the first one's make their plan, five barriers and two
+// dependent reads of the choice, before they ask for the first weight.
 //
 // All sums are fp32, in a fixed order.  Between the products h is kept in fp32, for
 // bf16 in two parts, its rounding and the rest's: the second matrix instruction is

@@ -10,7 +10,11 @@
 //
 // The runs' ends are known on the device only (dt_moe_dispatch leaves them
 // there), so a workgroup counts the tiles of all runs itself and walks over its
-// share of them; nothing depends on the capacity of the rows' buffers.
+// share of them.  The host knows the buffers' rows only and takes them as the rows in
+// use, evenly among the runs, when it picks a kernel: the results do not depend on
+// that, the time does a little (64 runs of 4 to 30 bf16 rows of 4096 to 2 x 1024
+// gated, 185 to 227 us in tight buffers, 185 to 212 in buffers 2 to 16 times as long),
+// and more where the runs' lengths differ much.
 //
 // All sums are fp32.  z, y, dx, dW and db are rounded once; dz is rounded to the
 // tensors' type before it enters its two products, as the matrix units take it.

@@ -50,11 +50,23 @@ __device__ __forceinline__ u32x4 to_rows(u32x4 v) {
 // fp32: a sum runs over kRunSteps steps of 16 terms at most, as in matrix_walk, and
 // these sums are added up apart (8 runs of 48 rows of 4096 to 2048 97 us either way,
 // gated 173 instead of 165; one run of 40 rows of 8192 to 4096 82 instead of 90).
+//
+// A second part, what rounding left of the first, has sums of its own, added where
+// the first part's sum is finite: it is zero or of the other sign as it happens, and
+// an infinite weight would make NaN of it where the whole value makes an infinity.
 template <int DT, bool VEC, int W, int G, int PARTS, int P>
 __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const char* const (&x)[PARTS][G], uint32_t lo, uint32_t hi, uint32_t bytes,
                                             uint32_t xbytes, f32x4 (&acc)[W][G]) {
     const uint32_t from = (threadIdx.x & 3) * 16, whole = bytes / kStepBytes, end = hi < whole ? hi : whole;
+    static_assert(PARTS == 1 || (PARTS == 2 && DT == kBF16), "fp32 is whole");
     u32x4 a[P][2][W], b[P][2][PARTS][G];
+    f32x4 rest[PARTS == 2 ? W : 1][PARTS == 2 ? G : 1];
+    if constexpr (PARTS == 2) {
+#pragma unroll
+        for (int k = 0; k < W; k++)
+#pragma unroll
+            for (int g = 0; g < G; g++) rest[k][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
     auto load = [&](int i, uint32_t s) {
 #pragma unroll
         for (int h = 0; h < 2; h++)
@@ -77,9 +89,10 @@ __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const cha
         for (int k = 0; k < W; k++) {
             const u32x4 f = to_rows(fa[k]);
 #pragma unroll
-            for (int g = 0; g < G; g++)
-#pragma unroll
-                for (int p = 0; p < PARTS; p++) acc[k][g] = multiply<DT>(f, t[p][g], acc[k][g]);
+            for (int g = 0; g < G; g++) {
+                acc[k][g] = multiply<DT>(f, t[0][g], acc[k][g]);
+                if constexpr (PARTS == 2) rest[k][g] = multiply<DT>(f, t[1][g], rest[k][g]);
+            }
         }
     };
     auto multiply_pair = [&](int i) {
@@ -149,6 +162,14 @@ __device__ __forceinline__ void stream_rows(const char* const (&w)[W], const cha
         for (int k = 0; k < W; k++)
 #pragma unroll
             for (int g = 0; g < G; g++) acc[k][g] += total[k][g];
+    }
+    if constexpr (PARTS == 2) {
+#pragma unroll
+        for (int k = 0; k < W; k++)
+#pragma unroll
+            for (int g = 0; g < G; g++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) acc[k][g][e] += fabsf(acc[k][g][e]) < INFINITY ? rest[k][g][e] : 0.f;
     }
 }
 // Steps of share `i` of `n`, whole pairs of them (a pair is a line of the weights).

@@ -20,8 +20,9 @@
 //
 // All sums are fp32, in a fixed order.  Between the products h is kept in fp32, for
 // bf16 in two parts, its rounding and the rest's: the second matrix instruction, and
-// the sums of its own that it has, are free beside the weight's bytes.  A slot's weight is multiplied into h, so that the
-// second product runs on over the experts without a sum for each of them.
+// the sums of its own that it has, are free beside the weight's bytes.  A slot's
+// weight is multiplied into h, so that the second product runs on over the experts
+// without a sum for each of them.
 #include "dt_act.h"
 #include "dt_stream.h"
 

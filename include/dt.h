@@ -438,7 +438,7 @@ dt_status dt_linear_backward(const void* const* dy, const void* const* x, const 
  * w_out[q] [E/P, cols, inner], b_out[q] [E/P, cols] (biases and residual NULL:
  * none).  out[r], residual[r], x[r] [tokens[r], cols].  What lies between the two
  * products is kept in fp32, or for bf16 tensors in two bf16 parts.  An expert's
- * w_in and w_out are below 2 GiB each. */
+ * w_out is below 2 GiB, its gated w_in, twice as large, below 4. */
 size_t dt_moe_layer_workspace(int nranks, const size_t* tokens, size_t cols, size_t inner, int nexperts, int topk,
                               dt_dtype dtype);
 dt_status dt_moe_layer(const void* const* x, const int32_t* const* experts, const float* const* weights,

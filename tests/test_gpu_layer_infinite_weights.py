@@ -25,8 +25,8 @@ def test_an_infinite_weight_gives_an_infinity(dt, tokens, cols, inner, experts, 
     note(f"layer with infinite weights, {tokens} tokens of {cols}, {topk} of {experts} experts of {inner} {dtype}")
     g = torch.Generator(device="cuda").manual_seed(70 + tokens)
     new = lambda *s: torch.randn(*s, generator=g, device="cuda")
-    # the first product is one of integers below 2^7, so what lies between the products is exact: whole bf16 values with no
-    # second part in even features, in odd ones values that have one of the opposite sign (7.99 rounds to 8)
+    # the first product gives whole numbers of up to 24, of which the second bf16 part is zero; the first choice's weight takes
+    # a little off them, and the second part has the other sign (7.99 rounds to 8)
     x = torch.zeros(tokens, cols, device="cuda")
     x[:, 0] = torch.randint(1, 4, (tokens,), generator=g, device="cuda") * torch.where(new(tokens) > 0, 1.0, -1.0)
     w_in, b_in = torch.zeros(experts, inner, cols, device="cuda"), torch.zeros(experts, inner, device="cuda")
